@@ -95,6 +95,8 @@ typedef enum {
                                 outside [0, num_pages)                            */
 #define DS_DEVERR_ROWREQ 4   /* prefill: row_req[t] outside [0, num_requests)     */
 #define DS_DEVERR_TIMEOUT 8  /* an internal pipeline wait gave up (library bug)   */
+#define DS_DEVERR_NOPAGE 16  /* pages: the pool has too few free pages            */
+#define DS_DEVERR_LEN 32     /* a length that the operation cannot take           */
 
 /*
  * Message of the last error on the calling host thread ("" if none). The
@@ -375,6 +377,217 @@ int ds_indexer_logits(const void* q, const float* weights, const void* k_pages,
  */
 int ds_kv_cache_write(const void* latent, int64_t num_rows, const int64_t* slots, int kv_dtype,
                       void* kv_pages, int64_t num_pages, int32_t* err_flag, void* stream);
+
+/*
+ * Block-scaled 8-bit cache ("kv8"): the paged cache of layers that keep keys
+ * and values per head (draft layers and the dense layers beside the sparse
+ * ones), held as OCP FP8 E4M3 codes with one float32 scale for each page of
+ * 64 positions, side (key or value) and head:
+ *
+ *  kv_pages     uint8 [num_pages, 2, num_kv_heads, 64, head_dim], 16-byte
+ *               aligned; index 0 of the second axis holds keys, 1 values.
+ *  kv_scales    float32 [num_pages, 2, num_kv_heads].
+ *               value = code * scale of its page, side and head. Scales are
+ *               positive and finite; ds_kv8_append writes powers of two.
+ *
+ * It uses the block tables and the page size of the latent cache: position s
+ * of a request lies in slot s % 64 of page block_table[request, s / 64]. What
+ * a page holds behind the request's last position is never used, whatever it
+ * is (NaN codes included).
+ *
+ * head_dim is 64 or 128; num_heads is a multiple of num_kv_heads (query head
+ * h reads key/value head h / (num_heads / num_kv_heads)), both at most 1024,
+ * and the product num_pages * 2 * num_kv_heads * 64 is at most 2^31 - 64.
+ *
+ * Ragged calls give each request's tokens by token_starts, int32
+ * [num_requests + 1] in device memory, never decreasing: request r owns rows
+ * token_starts[r] .. token_starts[r + 1] - 1 of the token-indexed arrays (the
+ * values are clamped to [0, num_tokens]). lens[r] counts the positions of
+ * request r INCLUDING these n tokens, which are its last n positions.
+ *
+ *
+ * ds_kv8_append: the keys and values of new tokens into the cache.
+ *
+ *  k, v         bfloat16, row t at k + t * k_stride (v + t * v_stride)
+ *               elements, each row [num_kv_heads, head_dim] contiguous;
+ *               16-byte aligned, strides multiples of 8 and at least
+ *               num_kv_heads * head_dim (slices of a fused projection).
+ *  block_table  int32 [num_requests, bt_stride].
+ *  err_flag     optional: DS_DEVERR_LEN for a request with lens[r] < n (it
+ *               writes nothing), DS_DEVERR_PAGE for a page beyond bt_stride
+ *               or outside the pool (its tokens are not written).
+ *
+ * Scale of a touched (page, side, head): a = max |x| of the new tokens in the
+ * page; need = the smallest power of two with a <= 448 * need, its exponent
+ * limited to [-60, 120] (0 if a = 0); old = the present scale if the page
+ * holds earlier positions of the request, else 0; scale = max(old, need), or
+ * 2^-60 if both are 0. Earlier codes become E4M3(code * (old / scale)) when
+ * the scale grew, new ones are E4M3(x / scale), rounded to nearest with ties
+ * to even, saturating at +-448. A NaN becomes the NaN code and does not enter
+ * a. With power-of-two scales a growing scale changes earlier values only
+ * where their codes leave E4M3's normal range.
+ *
+ * A page that is written belongs to one request of the call (pages shared
+ * after ds_pages_fork are full ones, which are never written again). Calls
+ * that repeat a page give unspecified bytes in it.
+ */
+int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                  int64_t num_tokens, const int32_t* token_starts, int64_t num_requests,
+                  const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                  int num_kv_heads, int head_dim, void* kv_pages, float* kv_scales,
+                  int64_t num_pages, int32_t* err_flag, void* stream);
+
+/*
+ * ds_kv8_decode: attention of next_n new tokens per request (1, or target and
+ * draft tokens under multi-token prediction) over the kv8 cache. Token j of
+ * request r sees the first clamp(lens[r] - next_n + 1 + j, 0, 64 * bt_stride)
+ * positions: s_i = scale * q . k_i, out = sum_i softmax(s)_i v_i, lse =
+ * ln sum_i exp(s_i); a token that sees nothing gives out = 0, lse = -inf.
+ *
+ *  q            bfloat16, token (r, j) at q + (r * next_n + j) * q_stride
+ *               elements, [num_heads, head_dim] contiguous; 16-byte aligned,
+ *               q_stride a multiple of 8 and at least num_heads * head_dim.
+ *               A non-finite value makes its head's outputs NaN.
+ *  next_n       1 .. 64.
+ *  out          bfloat16 [num_requests, next_n, num_heads, head_dim], 16-byte
+ *               aligned; lse float32 [num_requests, next_n, num_heads].
+ *  workspace    >= ds_kv8_decode_workspace_size() bytes, 256-byte aligned;
+ *               contents need no initialisation.
+ *  err_flag     optional: DS_DEVERR_PAGE for a page outside the pool (its
+ *               positions are left out of the softmax).
+ *
+ * A request's outputs depend on its own q, length and cache alone, bit for
+ * bit: contexts are cut at fixed positions, whatever else the batch holds.
+ */
+int ds_kv8_decode(const void* q, int64_t q_stride, const void* kv_pages, const float* kv_scales,
+                  int64_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                  const int32_t* lens, int64_t num_requests, int next_n, int num_heads,
+                  int num_kv_heads, int head_dim, float scale, void* out, float* lse,
+                  void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* Workspace bytes of ds_kv8_decode (0 for an unsupported shape). */
+size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_heads,
+                                    int num_kv_heads, int head_dim, int64_t bt_stride);
+
+/*
+ * ds_kv8_prefill: the same attention for ragged prompts (or prompt chunks):
+ * token i of a request with n tokens sees the first
+ * clamp(lens[r] - n + 1 + i, 0, 64 * bt_stride) positions (causal). Rows of
+ * out and lse that belong to no request are left as they are. Arguments as
+ * for ds_kv8_decode; q, out and lse are indexed by token. The workspace may
+ * be NULL where ds_kv8_prefill_workspace_size() is 0.
+ *
+ * A token's outputs depend on its own request alone, bit for bit, and not on
+ * how the request's tokens are spread over calls.
+ */
+int ds_kv8_prefill(const void* q, int64_t q_stride, int64_t num_tokens,
+                   const int32_t* token_starts, int64_t num_requests, const void* kv_pages,
+                   const float* kv_scales, int64_t num_pages, const int32_t* block_table,
+                   int64_t bt_stride, const int32_t* lens, int num_heads, int num_kv_heads,
+                   int head_dim, float scale, void* out, float* lse, void* workspace,
+                   size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* Workspace bytes of ds_kv8_prefill. */
+size_t ds_kv8_prefill_workspace_size(int64_t num_tokens, int64_t num_requests, int num_heads,
+                                     int num_kv_heads, int head_dim);
+
+/*
+ * Pages of a paged cache: who holds them, and moving them.
+ *
+ * The state is three device arrays of the caller:
+ *  refcounts    int32 [num_pages]: how many block-table entries hold the
+ *               page; a page is free when its count is not positive.
+ *  block_table  int32 [num_rows, bt_stride]: row r holds its first
+ *               ceil(lens[r] / 64) entries (lens clamped to
+ *               [0, 64 * bt_stride]); the rest holds nothing.
+ *  lens         int32 [num_rows].
+ * Pages are handed out lowest number first, in the order of the call's list,
+ * so the state after a call follows from the state before it.
+ *
+ * The caches that the pages index (any number of layers, codes, scales,
+ * latent rows, indexer keys) are given as pools, an array in HOST memory that
+ * is read during the call: pool i holds num_pages pages of page_bytes bytes
+ * each, back to back, from data (4-byte aligned; page_bytes a multiple of 4).
+ * At most DS_MAX_POOLS pools, 2^22 pages and 2^24 rows; lists of at most 65535
+ * entries; the pools' page_bytes sum to at most 2^28.
+ *
+ * Common to these calls: a negative list entry is padding; a row outside
+ * [0, num_rows) is skipped and sets DS_DEVERR_ROWREQ; workspaces have
+ * ds_pages_workspace_size() bytes, 256-byte aligned, and need no
+ * initialisation. Concurrent calls need separate workspaces, and calls on the
+ * same state need an order between them.
+ */
+#define DS_MAX_POOLS 128
+typedef struct {
+  void* data;
+  int64_t page_bytes;
+} ds_page_pool;
+
+/* Workspace bytes of the page calls for a pool and a list of n entries. */
+size_t ds_pages_workspace_size(int64_t num_pages, int64_t n);
+
+/*
+ * Page src[i] to page dst[i] in every pool, i < n (int32 lists). An i with a
+ * negative src or dst is padding; a page at or past num_pages sets
+ * DS_DEVERR_PAGE and copies nothing. No dst may repeat or be a src of the
+ * same call (the copies run at once).
+ */
+int ds_pages_copy(const ds_page_pool* pools, int num_pools, int64_t num_pages, const int32_t* src,
+                  const int32_t* dst, int64_t n, int32_t* err_flag, void* stream);
+
+/*
+ * Gives up everything the listed rows hold: each held page loses one count,
+ * the entries become -1 and the length 0. A row that is listed twice is freed
+ * once. A held entry of -1 counts for nothing; one outside the pool, or of a
+ * page whose count is not positive, sets DS_DEVERR_PAGE and changes no count.
+ */
+int ds_pages_free(int32_t* refcounts, int64_t num_pages, int32_t* block_table, int64_t bt_stride,
+                  int32_t* lens, int64_t num_rows, const int32_t* rows, int64_t n,
+                  int32_t* err_flag, void* stream);
+
+/*
+ * Makes row children[i] a copy of row parents[i]: full pages are shared (one
+ * count more each), a partly filled last page is copied in every pool to a
+ * free page of its own (so both rows may append), the length is taken over.
+ * Parents are read as they were before the call. A child has to be empty
+ * (length <= 0) and listed once: otherwise the later entry is skipped and
+ * DS_DEVERR_ROWREQ set. The i-th copied page takes the i-th free page; a
+ * child for which none is left stays empty and sets DS_DEVERR_NOPAGE. A page
+ * outside the pool is taken over as it is and sets DS_DEVERR_PAGE.
+ */
+int ds_pages_fork(const ds_page_pool* pools, int num_pools, int32_t* refcounts, int64_t num_pages,
+                  int32_t* block_table, int64_t bt_stride, int32_t* lens, int64_t num_rows,
+                  const int32_t* parents, const int32_t* children, int64_t n, void* workspace,
+                  size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/*
+ * Grows row rows[i] to new_lens[i] positions: the entries it holds more get
+ * free pages (count 1). A new length below the present one or above
+ * 64 * bt_stride sets DS_DEVERR_LEN, a row listed before sets
+ * DS_DEVERR_ROWREQ; both are skipped. Entry i takes the free pages after
+ * those that the entries before it ask for; where that passes the last free
+ * page the row stays as it is and DS_DEVERR_NOPAGE is set.
+ */
+int ds_pages_extend(int32_t* refcounts, int64_t num_pages, int32_t* block_table,
+                    int64_t bt_stride, int32_t* lens, int64_t num_rows, const int32_t* rows,
+                    const int32_t* new_lens, int64_t n, void* workspace, size_t workspace_bytes,
+                    int32_t* err_flag, void* stream);
+
+/*
+ * Moves the live pages to the front of the pool: with num_live pages live,
+ * the i-th live page at or past num_live goes to the i-th free page below it,
+ * in every pool, and the tables follow. Results go to block_table_out
+ * (entries that no row holds are copied as they are), refcounts_out and
+ * num_live_out (int32); block_table_out may be block_table and refcounts_out
+ * may be refcounts. The pools change in place; pages at and past num_live
+ * keep their bytes. A held entry outside the pool or of a free page stays and
+ * sets DS_DEVERR_PAGE. Workspace: ds_pages_workspace_size(num_pages, 0).
+ */
+int ds_pages_compact(const ds_page_pool* pools, int num_pools, const int32_t* refcounts,
+                     int64_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                     const int32_t* lens, int64_t num_rows, int32_t* refcounts_out,
+                     int32_t* block_table_out, int32_t* num_live_out, void* workspace,
+                     size_t workspace_bytes, int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,8 @@ tensors and the current stream into those calls.
 from ._native import (  # noqa: F401
     DSError,
     DEVERR_IDX,
+    DEVERR_LEN,
+    DEVERR_NOPAGE,
     DEVERR_PAGE,
     DEVERR_ROWREQ,
     DEVERR_TIMEOUT,
@@ -25,4 +27,19 @@ from ._native import (  # noqa: F401
     swa_workspace_size,
     topk_per_row,
     topk_workspace_size,
+)
+from .kv8 import (  # noqa: F401
+    kv8_append,
+    kv8_decode,
+    kv8_decode_workspace_size,
+    kv8_prefill,
+    kv8_prefill_workspace_size,
+)
+from .pages import (  # noqa: F401
+    pages_compact,
+    pages_copy,
+    pages_extend,
+    pages_fork,
+    pages_free,
+    pages_workspace_size,
 )

@@ -17,6 +17,7 @@ from . import build as _build
 DS_OK = 0
 KV_DTYPES = {"bf16": 0, "fp8": 1, 0: 0, 1: 1}
 DEVERR_IDX, DEVERR_PAGE, DEVERR_ROWREQ, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_NOPAGE, DEVERR_LEN = 16, 32
 
 _lib = None
 _lock = threading.Lock()
@@ -78,6 +79,33 @@ def lib():
         L.ds_indexer_logits.restype = i32
         L.ds_indexer_logits.argtypes = [vp, vp, vp, i64, vp, i64, i64, vp, vp, i64, i32, i32, vp,
                                         i64, vp, vp]
+        L.ds_kv8_append.restype = i32
+        L.ds_kv8_append.argtypes = [vp, vp, i64, i64, i64, vp, i64, vp, i64, vp, i32, i32, vp, vp,
+                                    i64, vp, vp]
+        L.ds_kv8_decode.restype = i32
+        L.ds_kv8_decode.argtypes = [vp, i64, vp, vp, i64, vp, i64, vp, i64, i32, i32, i32, i32,
+                                    f32, vp, vp, vp, sz, vp, vp]
+        L.ds_kv8_decode_workspace_size.restype = sz
+        L.ds_kv8_decode_workspace_size.argtypes = [i64, i32, i32, i32, i32, i64]
+        L.ds_kv8_prefill.restype = i32
+        L.ds_kv8_prefill.argtypes = [vp, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp, i32, i32,
+                                     i32, f32, vp, vp, vp, sz, vp, vp]
+        L.ds_kv8_prefill_workspace_size.restype = sz
+        L.ds_kv8_prefill_workspace_size.argtypes = [i64, i64, i32, i32, i32]
+        L.ds_pages_workspace_size.restype = sz
+        L.ds_pages_workspace_size.argtypes = [i64, i64]
+        L.ds_pages_copy.restype = i32
+        L.ds_pages_copy.argtypes = [vp, i32, i64, vp, vp, i64, vp, vp]
+        L.ds_pages_free.restype = i32
+        L.ds_pages_free.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp]
+        L.ds_pages_fork.restype = i32
+        L.ds_pages_fork.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, sz, vp,
+                                    vp]
+        L.ds_pages_extend.restype = i32
+        L.ds_pages_extend.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, sz, vp, vp]
+        L.ds_pages_compact.restype = i32
+        L.ds_pages_compact.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp,
+                                       vp]
         _lib = L
         return _lib
 
@@ -85,7 +113,10 @@ def lib():
 EXPORTED = ("ds_last_error", "ds_supported_config", "ds_topk_workspace_size",
             "ds_sparse_mla_workspace_size", "ds_topk_per_row", "ds_sparse_mla_decode",
             "ds_sparse_mla_prefill", "ds_sparse_mla_decode_noalloc", "ds_kv_cache_write",
-            "ds_sparse_mla_decode_swa", "ds_sparse_mla_swa_workspace_size", "ds_indexer_logits")
+            "ds_sparse_mla_decode_swa", "ds_sparse_mla_swa_workspace_size", "ds_indexer_logits",
+            "ds_kv8_append", "ds_kv8_decode", "ds_kv8_decode_workspace_size", "ds_kv8_prefill",
+            "ds_kv8_prefill_workspace_size", "ds_pages_workspace_size", "ds_pages_copy",
+            "ds_pages_free", "ds_pages_fork", "ds_pages_extend", "ds_pages_compact")
 
 
 def last_error():

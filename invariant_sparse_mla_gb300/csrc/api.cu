@@ -196,6 +196,8 @@ int report_error(int status, const char* fmt, ...) {
   return status;
 }
 
+int report_ok() { return ok(); }
+
 }  // namespace dsmla
 
 extern "C" {

@@ -176,6 +176,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // returns `status`.
 int report_error(int status, const char* fmt, ...);
 
+// Clears this host thread's message and returns DS_OK.
+int report_ok();
+
 // The device a launch on `stream` runs on. The runtime launches only into a
 // stream of the current device (a stream of another device is refused), so
 // this is the current device; the stream is not queried, since querying a

@@ -47,3 +47,12 @@ from .attention import (  # noqa: F401
     sparse_mla_rows_sink,
     sparse_mla_decode_swa,
 )
+from .kv8 import (  # noqa: F401
+    kv8_append,
+    kv8_attention,
+    kv8_bounds,
+    kv8_need_scale,
+    kv8_visible,
+)
+from . import pages  # noqa: F401
+from .pages import pages_compact, pages_extend, pages_fork, pages_free  # noqa: F401
