@@ -23,7 +23,6 @@ struct Params {
   int64_t q_stride;
   int64_t tokens;
   const int32_t* starts;
-  int next_n;
   int heads, group;
   float scale;
   __nv_bfloat16* out;
@@ -59,10 +58,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_attention_kernel(const Params
   const int64_t t = w / p.heads;
   const int h = (int)(w % p.heads), g = h / p.group;
   int64_t r, seen;
-  if (p.starts == nullptr) {
-    r = t / p.next_n;
-    seen = (int64_t)p.c.lens[r] - p.next_n + 1 + t % p.next_n;
-  } else {
+  {
     auto start_of = [&](int64_t i) {
       const int64_t s = p.starts[i];
       return s < 0 ? 0 : (s > p.tokens ? p.tokens : s);
@@ -143,7 +139,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_attention_kernel(const Params
 }
 
 cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t stream) {
-  Params p{reinterpret_cast<const __nv_bfloat16*>(a.q), a.q_stride, a.tokens, a.starts, a.next_n,
+  Params p{reinterpret_cast<const __nv_bfloat16*>(a.q), a.q_stride, a.tokens, a.starts,
            a.heads, a.heads / a.c.kv_heads, a.scale, reinterpret_cast<__nv_bfloat16*>(a.out),
            a.lse, a.c};
   const dim3 grid((unsigned)((a.tokens * a.heads + kWarps - 1) / kWarps));
@@ -154,15 +150,10 @@ cudaError_t launch(const Kv8AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream) {
-  return launch(a, stream);
-}
-
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream) {
   return launch(a, stream);
 }
 
-size_t kv8_decode_workspace_bytes(int64_t, int, int, int, int, int64_t) { return 256; }
 size_t kv8_prefill_workspace_bytes(int64_t, int64_t, int, int, int) { return 0; }
 
 }  // namespace dsmla

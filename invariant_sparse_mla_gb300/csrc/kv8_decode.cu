@@ -1,0 +1,959 @@
+// Decode attention over the block-scaled 8-bit cache, on the 8-bit tensor
+// cores: keys and values are multiplied as they lie in the cache.
+//
+// Mathematics. With codes K, V (E4M3) and page scales a, b, token i of a page
+// gives s_i = scale * a * (q . K_i) and out = sum_i 2^(s_i - M) b V_i / L. The
+// tensor core takes 8-bit operands on both sides, so the side that is ours is
+// written as a sum of E4M3 pieces, each piece a column of its own so that it
+// has its own power-of-two weight:
+//   q = 2^-k (q0 + q1 / 32): |q| 2^k is at most 256, q0 = E4M3(q 2^k), q1 the
+//     rounded remainder times 32. A bf16 number has 8 significant bits and
+//     two pieces hold 2 x 4, so this is exact down to 2^-14 of the largest |q|
+//     of the row and off by 2^-23 of that below;
+//   p b = 2^-6 (p0 + p1 / 32 + p2 / 1024) with p <= 4 relative to the running
+//     maximum: at least 12 significant bits down to p = 2^-12, 8 down to
+//     2^-18, off by 2^-26 below (three pieces because a long tail of small
+//     weights counts: 2^17 positions of weight 2^-17 weigh as much as one
+//     of weight 1).
+// So S^T = K [q0 q1] and O^T = V^T [p0 p1 p2], both with the cache's bytes as
+// the A operand straight from TMA: no byte of the cache is converted.
+//
+// The running maximum m of a row covers s_i + log2 b_i (then p b <= 4 whatever
+// the page scales are) and moves only when a tile passes it by more than 2^2;
+// l = sum 2^(s_i - m) is kept in fp32 of the unrounded weights.
+//
+// Work split. A row's context is cut into spans of 256 to 4096 positions, the
+// power of two that gives at most 32 spans up to 131072 positions: a
+// function of the request's length alone, so a request's bits do not depend
+// on the batch. A persistent grid (two CTAs per SM) takes the (request, kv
+// head, row group, span) items in order, each CTA an equal share of the
+// 128-position tiles; a second kernel joins the spans in order. Rows with one
+// span are finished by the first kernel.
+//
+// Per CTA: warps 0-3 softmax (TMEM lane = position), warp 4 TMA producer over
+// a ring of tile halves (K or V of 128 positions), warp 5 MMA issuer. Ring,
+// S, P and O barriers run on across items, so the next item's pages stream in
+// while the last one is finished. The bound is HBM: 2 * dim bytes a position.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kv8.h"
+#include "ptx.cuh"
+
+namespace dsmla {
+
+namespace {
+
+constexpr int kTile = 128;                 // positions per tile (two pages)
+constexpr int kThreads = 192;
+constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kMaxRows = 40;               // query rows of one row group
+constexpr int kMetaSlots = 8;
+constexpr float kTau = 2.0f;               // log2: p b may reach 2^kTau
+constexpr float kPScale = 64.0f;           // 2^(8 - kTau): stored weights stay <= 256
+constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
+constexpr int kMinSpan = 256, kMaxSpan = 4096;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__host__ __device__ inline int span_of(int64_t len) {
+  int s = kMinSpan;
+  while (s < kMaxSpan && (int64_t)s * 32 < len) s *= 2;
+  return s;
+}
+
+// Most spans a row of at most `len` positions can have.
+int64_t max_spans(int64_t len) {
+  const int64_t a = (len + kMinSpan - 1) / kMinSpan, b = (len + kMaxSpan - 1) / kMaxSpan;
+  return a < 32 ? a : (b > 32 ? b : 32);
+}
+
+struct Shape {
+  int rows;     // per row group
+  int groups;   // row groups of a kv head
+};
+
+Shape shape_of(int next_n, int group) {
+  const int total = next_n * group;
+  Shape s;
+  s.groups = (total + kMaxRows - 1) / kMaxRows;
+  s.rows = (total + s.groups - 1) / s.groups;
+  return s;
+}
+
+template <int R8, int DIM>
+struct Layout {
+  static constexpr int kNP = (3 * R8 + 15) / 16 * 16;       // columns of P and O
+  static constexpr int kUnit = kTile * DIM;                 // K or V of one tile
+  static constexpr int kQBytes = 2 * R8 * DIM;
+  static constexpr int kPBytes = kNP * kTile;
+  static constexpr int kRest = kQBytes + 2 * kPBytes + 2048 + 1024;
+  static constexpr int kFit = (113 * 1024 - kRest) / kUnit;
+  static constexpr int kUnits = kFit > 8 ? 8 : kFit;
+  static_assert(kUnits >= 4, "two tiles fit");
+  static constexpr int kRing = 0;
+  static constexpr int kP = kRing + kUnits * kUnit;         // 2 buffers
+  static constexpr int kQ = kP + 2 * kPBytes;
+  static constexpr int kBars = kQ + (kQBytes + 1023) / 1024 * 1024;
+  static constexpr int kMeta = kBars + 32 * 8;              // kMetaSlots x 2 float4
+  static constexpr int kF = kMeta + kMetaSlots * 32;        // per row: factor, m, alpha
+  static constexpr int kM = kF + R8 * 4;
+  static constexpr int kAlpha = kM + R8 * 4;
+  static constexpr int kWarpMax = kAlpha + R8 * 4;          // 4 x R8 floats
+  static constexpr int kVis = kWarpMax + 4 * R8 * 4;        // positions each row sees
+  static constexpr int kMisc = kVis + R8 * 4;               // tmem slot, abort, start of work
+  static constexpr int kEnd = kMisc + 64;
+  static constexpr int kSmem = kEnd + 1024;
+  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+  static constexpr uint32_t kCols = 2 * R8 + kNP <= 64 ? 64u : (2 * R8 + kNP <= 128 ? 128u : 256u);
+  static_assert(2 * R8 + kNP <= 256, "two CTAs per SM share TMEM");
+};
+
+enum Bar {
+  kFull = 0,        // <= 8: unit landed
+  kEmpty = 8,       // <= 8: unit's MMAs done
+  kSFull = 16,      // S ready
+  kSFree = 17,      // S read by the 128 softmax threads
+  kPFull = 18,      // 2: P written
+  kPvDone = 20,     // 2: PV done (P buffer free, O holds the tile)
+  kQReady = 22,     // Q pieces written
+  kDrain = 23,
+  kNumBars = 24
+};
+
+struct Params {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int next_n, heads, group, rows, row_groups;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;
+  float2* part_ml;
+  int64_t spans;         // slots per (request, kv head, row group)
+  Kv8Cache c;
+};
+
+// The items of one CTA, in order. Every role walks the same sequence.
+struct Walk {
+  int64_t at, end;       // tile numbers: start of the present item, end of the CTA's share
+  int64_t r;             // request
+  int64_t len;           // its positions
+  int tiles, span_tiles, spans;
+  int hg, s;             // kv head * row_groups + row group; span
+};
+
+__device__ __forceinline__ int64_t row_len(const Params& p, int64_t r) {
+  int64_t len = p.c.lens[r];
+  const int64_t most = p.c.bt_stride * kPage;
+  return len < 0 ? 0 : (len > most ? most : len);
+}
+
+__device__ __forceinline__ void walk_load(const Params& p, Walk& w) {
+  w.len = row_len(p, w.r);
+  w.tiles = (int)((w.len + kTile - 1) / kTile);
+  const int span = span_of(w.len);
+  w.span_tiles = span / kTile;
+  w.spans = (int)((w.len + span - 1) / span);
+}
+
+// Moves to the first item at or behind tile offset x of request w.r (whose
+// first tile is number `base`), then to later requests while empty.
+__device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
+  const int hgs = p.c.kv_heads * p.row_groups;
+  while (true) {
+    if (w.s >= w.spans) {   // also a request without positions
+      w.s = 0;
+      ++w.hg;
+    }
+    if (w.spans == 0 || w.hg >= hgs) {
+      w.hg = 0;
+      w.s = 0;
+      if (++w.r >= p.c.requests) return false;
+      walk_load(p, w);
+      if (w.spans == 0) {
+        w.s = 0;
+        continue;
+      }
+    }
+    return w.at < w.end;
+  }
+}
+
+__device__ __forceinline__ int item_tiles(const Walk& w) {
+  const int left = w.tiles - w.s * w.span_tiles;
+  return left < w.span_tiles ? left : w.span_tiles;
+}
+
+__device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
+  w.at += item_tiles(w);
+  ++w.s;
+  if (w.at >= w.end) return false;
+  return walk_settle(p, w);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t b) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)b, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Byte offset of (row, byte) in a K-major tile of DIM-byte rows in the swizzle
+// the copies use (128 bytes for dim 128, 64 for dim 64).
+template <int DIM>
+__device__ __forceinline__ uint32_t swz(int row, int byte) {
+  const int c = byte >> 4;
+  if constexpr (DIM == 128)
+    return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4) + (byte & 15));
+  else
+    return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4) + (byte & 15));
+}
+
+template <int DIM>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+  if constexpr (DIM == 128)
+    return make_sw128_desc(addr, 16, 1024);
+  else
+    return make_sw64_desc(addr, 16, 512);
+}
+
+// Order-preserving int of a float (for integer warp maxima).
+__device__ __forceinline__ int float_key(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float key_float(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
+}
+
+template <int R8, int DIM>
+__global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
+    const __grid_constant__ CUtensorMap map, const Params p) {
+  using LY = Layout<R8, DIM>;
+  constexpr int NP = LY::kNP, NU = LY::kUnits;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LY::kBars);
+  float4* meta = reinterpret_cast<float4*>(smem + LY::kMeta);
+  float* f_s = reinterpret_cast<float*>(smem + LY::kF);
+  float* m_s = reinterpret_cast<float*>(smem + LY::kM);
+  float* alpha_s = reinterpret_cast<float*>(smem + LY::kAlpha);
+  float* wmax_s = reinterpret_cast<float*>(smem + LY::kWarpMax);
+  int* vis_s = reinterpret_cast<int*>(smem + LY::kVis);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 4);
+  int64_t* start_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 8);   // request, its first tile
+  int64_t* scan_s = reinterpret_cast<int64_t*>(smem + LY::kWarpMax);     // before the loop only
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool all = i == kSFree || i == kPFull || i == kPFull + 1 || i == kQReady;
+      mbar_init(&bars[i], all ? 128u : 1u);
+    }
+    mbar_fence_init();
+    *abort_s = 0;
+    start_s[0] = -1;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, LY::kCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's share: tiles of all requests in a row, an equal part each.
+  // Thread t sums a run of requests; a scan over the block finds the run that
+  // holds the first tile of the share.
+  const int hgs = p.c.kv_heads * p.row_groups;
+  const int64_t per = (p.c.requests + kThreads - 1) / kThreads;
+  int64_t sum = 0;
+  for (int64_t r = tid * per; r < p.c.requests && r < (tid + 1) * per; ++r)
+    sum += (row_len(p, r) + kTile - 1) / kTile * hgs;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) scan_s[warp] = inc;
+  __syncthreads();
+  int64_t total = 0, before = inc - sum;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan_s[w];
+    total += scan_s[w];
+  }
+  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  if (lo < hi && lo >= before && lo < before + sum) {
+    int64_t base = before;
+    for (int64_t r = tid * per; r < p.c.requests; ++r) {
+      const int64_t n = (row_len(p, r) + kTile - 1) / kTile * hgs;
+      if (lo < base + n) {
+        start_s[0] = r;
+        start_s[1] = base;
+        break;
+      }
+      base += n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk w;
+  w.r = start_s[0];
+  w.end = hi;
+  bool some = w.r >= 0;
+  if (some) {
+    walk_load(p, w);
+    const int64_t x = lo - start_s[1];
+    w.hg = (int)(x / w.tiles);
+    const int tt = (int)(x % w.tiles);
+    w.s = (tt + w.span_tiles - 1) / w.span_tiles;
+    // The item's first tile (also where s is one past the last span).
+    const int st = w.s * w.span_tiles < w.tiles ? w.s * w.span_tiles : w.tiles;
+    w.at = lo + (st - tt);
+    some = w.at < w.end && walk_settle(p, w);
+  }
+
+  bool failed = false;
+  if (warp == kProducerWarp) {
+    // ---------------------------------------------------------- producer
+    int64_t u = 0;          // units issued
+    int64_t g = 0;          // tiles issued
+    int err_bits = 0;
+    const int none = (int)(p.c.num_pages * 2 * p.c.kv_heads * kPage);   // a row past the pool: zeros
+    while (some && !failed) {
+      const int kvh = w.hg / p.row_groups;
+      const int nt = item_tiles(w);
+      const int64_t block0 = (int64_t)w.s * w.span_tiles * 2;
+      const int64_t blocks = (w.len + kPage - 1) / kPage;
+      // Lane l looks up pages l and l + 32 of the span, all at once.
+      int y[2];
+      float ks[2], vs[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t b = block0 + lane + 32 * i;
+        y[i] = none;
+        ks[i] = vs[i] = 0.0f;
+        if (lane + 32 * i < 2 * nt && b < blocks) {
+          const int64_t page = p.c.block_table[w.r * p.c.bt_stride + b];
+          if (page >= 0 && page < p.c.num_pages) {
+            const int64_t part = page * 2 * p.c.kv_heads + kvh;
+            y[i] = (int)(part * kPage);
+            ks[i] = p.c.scales[part];
+            vs[i] = p.c.scales[part + p.c.kv_heads];
+          } else {
+            err_bits |= kErrPage;
+          }
+        }
+      }
+      for (int t = 0; t < nt; ++t, ++g) {
+        int yy[2];
+        float kk[2], vv[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int src = (2 * t + h) & 31, hi2 = (2 * t + h) >> 5;
+          yy[h] = __shfl_sync(0xffffffffu, hi2 ? y[1] : y[0], src);
+          kk[h] = __shfl_sync(0xffffffffu, hi2 ? ks[1] : ks[0], src);
+          vv[h] = __shfl_sync(0xffffffffu, hi2 ? vs[1] : vs[0], src);
+        }
+        bool ok = true;
+        if (lane == 0) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side, ++u) {
+            const int st = (int)(u % NU);
+            if (u >= NU && !mbar_wait(&bars[kEmpty + st], (uint32_t)((u / NU - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            if (side == 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                meta[(g & (kMetaSlots - 1)) * 2 + h] =
+                    make_float4(kk[h], vv[h], log2f(vv[h]), yy[h] == none ? 0.0f : 1.0f);
+            }
+            mbar_arrive_expect_tx(&bars[kFull + st], LY::kUnit);
+            const uint32_t dst = sbase + LY::kRing + st * LY::kUnit;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = yy[h] == none ? none : yy[h] + side * p.c.kv_heads * kPage;
+              tma_load_box(dst + h * (kPage * DIM), &map, 0, row, &bars[kFull + st]);
+            }
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+      }
+      if (!failed) some = walk_next(p, w);
+    }
+    if (lane == 0) {
+      // Every copy has landed before the CTA can exit.
+      for (int64_t i = u > NU ? u - NU : 0; i < u; ++i)
+        if (!mbar_wait(&bars[kFull + i % NU], (uint32_t)((i / NU) & 1))) failed = true;
+    }
+    if (err_bits && p.c.err != nullptr) atomicOr(p.c.err, err_bits);
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = make_idesc_e4m3(kTile, 2 * R8, 0, 0);
+      constexpr uint32_t idesc_o = make_idesc_e4m3(DIM, NP, 1, 0);
+      const uint64_t q_desc = tile_desc<DIM>(sbase + LY::kQ);
+      const uint64_t ring_desc = tile_desc<DIM>(sbase + LY::kRing);
+      const uint64_t p_desc = make_sw128_desc(sbase + LY::kP, 16, 1024);
+      int64_t g = 0;          // tiles whose S was issued
+      int64_t pv = 0;         // tiles whose PV was issued
+      bool first_of_pv = true;
+      auto issue_pv = [&](bool first) {
+        // O^T (+)= V^T P^T of tile pv.
+        const int64_t u = 2 * pv + 1;
+        const int st = (int)(u % NU), pb = (int)(pv & 1);
+        if (!mbar_wait(&bars[kPFull + pb], (uint32_t)((pv >> 1) & 1)) ||
+            !mbar_wait(&bars[kFull + st], (uint32_t)((u / NU) & 1)))
+          return false;
+        tc_fence_after();
+        const uint64_t a = ring_desc + (uint64_t)((st * LY::kUnit) >> 4);
+        const uint64_t b = p_desc + (uint64_t)((pb * LY::kPBytes) >> 4);
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          mma_f8_ss(tmem + 2 * R8, a + ((k * 32 * DIM) >> 4), b + ((k * 32) >> 4), idesc_o,
+                    (!first || k > 0) ? 1u : 0u);
+        mma_commit(&bars[kEmpty + st]);
+        mma_commit(&bars[kPvDone + pb]);
+        ++pv;
+        return true;
+      };
+      int64_t items = 0;
+      while (some && !failed) {
+        const int nt = item_tiles(w);
+        for (int t = 0; t < nt && !failed; ++t) {
+          const int64_t u = 2 * g;
+          const int st = (int)(u % NU);
+          // The item's Q pieces (written after the last item's S was read);
+          // S is free again once tile g - 1 was read.
+          if (t == 0 && !mbar_wait(&bars[kQReady], (uint32_t)(items & 1))) failed = true;
+          if (!failed && g > 0 && !mbar_wait(&bars[kSFree], (uint32_t)((g - 1) & 1)))
+            failed = true;
+          if (!failed && !mbar_wait(&bars[kFull + st], (uint32_t)((u / NU) & 1))) failed = true;
+          if (failed) break;
+          tc_fence_after();
+          const uint64_t a = ring_desc + (uint64_t)((st * LY::kUnit) >> 4);
+#pragma unroll
+          for (int k = 0; k < DIM / 32; ++k)
+            mma_f8_ss(tmem, a + ((k * 32) >> 4), q_desc + ((k * 32) >> 4), idesc_s,
+                      k > 0 ? 1u : 0u);
+          mma_commit(&bars[kEmpty + st]);
+          mma_commit(&bars[kSFull]);
+          ++g;
+          if (t > 0) {
+            if (!issue_pv(first_of_pv)) failed = true;
+            first_of_pv = false;
+          }
+        }
+        if (failed) break;
+        if (!issue_pv(first_of_pv)) failed = true;
+        first_of_pv = true;
+        ++items;
+        if (!failed) some = walk_next(p, w);
+      }
+      mma_commit(&bars[kDrain]);
+      if (!mbar_wait(&bars[kDrain], 0)) failed = true;
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- softmax
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int dim0 = DIM == 128 ? warp * 32 + lane : warp * 16 + lane;   // this lane's O row
+    const bool has_dim = DIM == 128 || lane < 16;
+    float l[R8];
+    int64_t g = 0;
+    int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
+    while (some && !failed) {
+      const int nt = item_tiles(w);
+      const int kvh = w.hg / p.row_groups, rg = w.hg % p.row_groups;
+      const int row0 = rg * p.rows;
+      const int rows = min(p.rows, p.next_n * p.group - row0);
+      const int64_t qid = w.r * hgs + w.hg;
+      // The Q pieces: warp w takes rows w, w + 4, ...; a row's largest |q| sets
+      // its power of two. (All S that read the last Q are complete: their
+      // results were read.)
+      if (qid != last_q) {
+        last_q = qid;
+        for (int r = warp; r < R8; r += 4) {
+          constexpr int E = DIM / 32;
+          float x[E], a = 0.0f;
+          bool nan = false;
+#pragma unroll
+          for (int i = 0; i < E; ++i) x[i] = 0.0f;
+          if (r < rows) {
+            const int j = (row0 + r) / p.group, gh = (row0 + r) % p.group;
+            const __nv_bfloat16* src = p.q + (w.r * p.next_n + j) * p.q_stride +
+                                       ((int64_t)kvh * p.group + gh) * DIM + lane * E;
+            if constexpr (E == 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              x[0] = __uint_as_float(v.x << 16);
+              x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+              x[2] = __uint_as_float(v.y << 16);
+              x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+            } else {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(src);
+              x[0] = __uint_as_float(v << 16);
+              x[1] = __uint_as_float(v & 0xFFFF0000u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            a = fmaxf(a, fabsf(x[i]));
+            nan |= x[i] != x[i];
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          nan = __any_sync(0xffffffffu, nan) || a == INFINITY;
+          // a 2^k in [128, 256); 2^k stays a normal float.
+          int k = a > 0.0f ? 7 - ((int)(__float_as_uint(a) >> 23) - 127) : 0;
+          k = k > 120 ? 120 : (k < -120 ? -120 : k);
+          const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+          uint32_t b0[E / 2], b1[E / 2];
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const float u0 = x[2 * i] * up, u1 = x[2 * i + 1] * up;
+            b0[i] = to_e4m3x2(u0, u1);
+            const float2 h = from_e4m3x2(b0[i]);
+            b1[i] = to_e4m3x2((u0 - h.x) * 32.0f, (u1 - h.y) * 32.0f);
+          }
+          const uint32_t at0 = sbase + LY::kQ + swz<DIM>(r, lane * E);
+          const uint32_t at1 = sbase + LY::kQ + swz<DIM>(R8 + r, lane * E);
+          if constexpr (E == 4) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0), "r"(b0[0] | (b0[1] << 16)) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1), "r"(b1[0] | (b1[1] << 16)) : "memory");
+          } else {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at0), "h"((uint16_t)b0[0]) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at1), "h"((uint16_t)b1[0]) : "memory");
+          }
+          if (lane == 0)
+            f_s[r] = nan ? NAN : __uint_as_float((uint32_t)(127 - k) << 23) * p.scale_log2;
+        }
+        fence_proxy_async_smem();
+      }
+      // Row r's token j sees len - next_n + 1 + j positions (clamped).
+      const int64_t raw_len = p.c.lens[w.r];
+      auto visible = [&](int r) {
+        const int64_t v = raw_len - p.next_n + 1 + (row0 + r) / p.group;
+        return (int)(v < 0 ? 0 : (v > w.len ? w.len : v));
+      };
+      if (tid < R8) {
+        m_s[tid] = -INFINITY;
+        vis_s[tid] = visible(tid);
+      }
+#pragma unroll
+      for (int r = 0; r < R8; ++r) l[r] = 0.0f;
+      uint64_t nan_rows = 0;    // rows that see a NaN value in this lane's dim
+      named_bar_sync(1, 128);   // f_s, m_s, vis_s
+      mbar_arrive(&bars[kQReady]);
+
+      const int min_vis = vis_s[0];
+      for (int t = 0; t < nt; ++t, ++g) {
+        const int64_t pos0 = ((int64_t)w.s * w.span_tiles + t) * kTile;
+        const int64_t pos = pos0 + tid;
+        const int pb = (int)(g & 1);
+        if (!mbar_wait(&bars[kSFull], (uint32_t)(g & 1))) *abort_s = 1;
+        tc_fence_after();
+        const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tid >> 6)];   // ks, vs, log2 vs, valid
+        float s[R8];
+#pragma unroll
+        for (int c = 0; c < R8 / 8; ++c) {
+          float lo8[8];
+          tmem_ld8x2_sync(tmem + lane_base + c * 8, tmem + lane_base + R8 + c * 8, s + 8 * c, lo8);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s[8 * c + i] = __fmaf_rn(lo8[i], 0.03125f, s[8 * c + i]);
+        }
+        tc_fence_before();
+        mbar_arrive(&bars[kSFree]);
+        bool above = false;
+        const bool here = mt.w != 0.0f && pos < w.len;
+        if (pos0 + kTile <= min_vis) {
+#pragma unroll
+          for (int r = 0; r < R8; ++r) {
+            const float x = s[r] * (f_s[r] * mt.x);
+            s[r] = here ? x : -INFINITY;
+            above |= s[r] + mt.z > m_s[r] + kTau;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < R8; ++r) {
+            const float x = s[r] * (f_s[r] * mt.x);
+            s[r] = here && pos < vis_s[r] ? x : -INFINITY;
+            above |= s[r] + mt.z > m_s[r] + kTau;
+          }
+        }
+        const bool move = named_bar_or(2, 128, above);
+        if (*abort_s) {
+          failed = true;
+          break;
+        }
+        if (move) {
+          // Some row's maximum grows by more than 2^kTau: new maxima for the
+          // rows that do (by their own values alone), and their sums and
+          // outputs so far rescaled.
+#pragma unroll
+          for (int r = 0; r < R8; ++r) {
+            const int k = __reduce_max_sync(0xffffffffu, float_key(s[r] + mt.z));
+            if (lane == 0) wmax_s[warp * R8 + r] = key_float(k);
+          }
+          named_bar_sync(1, 128);
+          if (tid < R8) {
+            float top = wmax_s[tid];
+#pragma unroll
+            for (int v = 1; v < 4; ++v) top = fmaxf(top, wmax_s[v * R8 + tid]);
+            const float old = m_s[tid];
+            float al = 1.0f;
+            if (top > old + kTau) {
+              al = ex2(old - top);   // 0 for the first
+              m_s[tid] = top;
+            }
+            alpha_s[tid] = al;
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int r = 0; r < R8; ++r) l[r] *= alpha_s[r];
+          if (t > 0) {
+            if (!mbar_wait(&bars[kPvDone + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1)))
+              *abort_s = 1;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < R8 / 8; ++c) {
+              float al[8];
+              bool change = false;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                al[i] = alpha_s[8 * c + i];
+                change |= al[i] != 1.0f;
+              }
+              if (change) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                  const uint32_t at = tmem + lane_base + 2 * R8 + k * R8 + 8 * c;
+                  float o[8];
+                  tmem_ld8_sync(at, o);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) o[i] *= al[i];
+                  tmem_st8(at, o);
+                }
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // The weights, their sum, and their pieces into P (once PV of tile
+        // g - 2 has read that buffer).
+        if (g >= 2 && !mbar_wait(&bars[kPvDone + pb], (uint32_t)(((g >> 1) - 1) & 1)))
+          *abort_s = 1;
+        const uint32_t pbase = sbase + LY::kP + pb * LY::kPBytes;
+        const float vscale = mt.y * kPScale;
+#pragma unroll
+        for (int r = 0; r < R8; r += 2) {
+          float e[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float m = m_s[r + i];
+            e[i] = ex2(s[r + i] - (m == -INFINITY ? 0.0f : m));
+            l[r + i] += e[i];
+            e[i] = here ? e[i] * vscale : 0.0f;
+          }
+          uint32_t b[3];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            b[k] = to_e4m3x2(e[0], e[1]);
+            if (k < 2) {
+              const float2 h = from_e4m3x2(b[k]);
+              e[0] = (e[0] - h.x) * 32.0f;
+              e[1] = (e[1] - h.y) * 32.0f;
+            }
+            const int n = k * R8 + r;
+            st_u8(pbase + swz<128>(n, tid), b[k]);
+            st_u8(pbase + swz<128>(n + 1, tid), b[k] >> 8);
+          }
+        }
+        // Value rows behind the context hold anything: a weight of 0 times a
+        // NaN code is NaN, so they become 0. Where the rows of the group see
+        // different lengths, a NaN value that only some of them see becomes 0
+        // as well and is remembered for those.
+        if (pos0 + kTile > min_vis) {
+          const int64_t u = 2 * g + 1;
+          const int st = (int)(u % NU);
+          if (!mbar_wait(&bars[kFull + st], (uint32_t)((u / NU) & 1))) *abort_s = 1;
+          uint8_t* vt = smem + LY::kRing + st * LY::kUnit;
+          uint4* row = reinterpret_cast<uint4*>(vt + tid * DIM);
+          bool nan = false;
+          if (pos >= w.len) {
+#pragma unroll
+            for (int i = 0; i < DIM / 16; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+          } else if (pos >= min_vis) {
+#pragma unroll
+            for (int i = 0; i < DIM / 16; ++i) {
+              const uint4 v = row[i];
+              nan |= (__vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                      __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                      __vcmpeq4(v.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                      __vcmpeq4(v.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
+            }
+          }
+          if (named_bar_or(2, 128, nan)) {
+            if (has_dim) {
+              for (int i = 0; i < kTile; ++i) {
+                const int64_t ps = pos0 + i;
+                if (ps < min_vis || ps >= w.len) continue;
+                uint8_t* at = vt + swz<DIM>(i, dim0);
+                if ((*at & 0x7Fu) != 0x7Fu) continue;
+                *at = 0;
+                for (int r = 0; r < rows; ++r)
+                  if (ps < vis_s[r]) nan_rows |= 1ull << r;
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bars[kPFull + pb]);
+      }
+      if (failed) break;
+
+      // ------------------------------------------------ end of the item
+      if (!mbar_wait(&bars[kPvDone + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) *abort_s = 1;
+      tc_fence_after();
+#pragma unroll
+      for (int r = 0; r < R8; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) wmax_s[warp * R8 + r] = v;
+      }
+      named_bar_sync(1, 128);
+      if (*abort_s) {
+        failed = true;
+        break;
+      }
+      const int64_t slot = (qid * p.spans + w.s) * p.rows;
+#pragma unroll
+      for (int c = 0; c < R8 / 8; ++c) {
+        if (c * 8 >= rows) break;
+        float o0[8], o1[8], o2[8];
+        const uint32_t at = tmem + lane_base + 2 * R8 + 8 * c;
+        tmem_ld8x2_sync(at, at + R8, o0, o1);
+        tmem_ld8_sync(at + 2 * R8, o2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 8 * c + i;
+          if (r >= rows) break;
+          const float ls = (wmax_s[r] + wmax_s[R8 + r]) + (wmax_s[2 * R8 + r] + wmax_s[3 * R8 + r]);
+          float o = __fmaf_rn(o2[i], 0.0009765625f, __fmaf_rn(o1[i], 0.03125f, o0[i])) *
+                    (1.0f / kPScale);
+          if ((nan_rows >> r) & 1) o = NAN;
+          if (w.spans == 1) {
+            const int64_t token = w.r * p.next_n + (row0 + r) / p.group;
+            const int64_t h = token * p.heads + kvh * p.group + (row0 + r) % p.group;
+            if (has_dim)
+              p.out[h * DIM + dim0] = __float2bfloat16(ls == 0.0f ? 0.0f : __fdiv_rn(o, ls));
+            if (tid == 0) p.lse[h] = ls == 0.0f ? -INFINITY : (m_s[r] + log2f(ls)) * kLn2;
+          } else {
+            if (has_dim) p.part_o[(slot + r) * DIM + dim0] = o;
+            if (tid == 0) p.part_ml[slot + r] = make_float2(m_s[r], ls);
+          }
+        }
+      }
+      named_bar_sync(1, 128);   // m_s and wmax_s are read before the next item writes them
+      some = walk_next(p, w);
+    }
+  }
+  if (failed && p.c.err != nullptr) atomicOr(p.c.err, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, LY::kCols);
+}
+
+// Joins the spans of a row, in order: one warp per (request, token, head).
+// Requests without positions get their zeros here; those with one span are
+// complete already.
+template <int DIM>
+__global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
+  constexpr int E = DIM / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+  if (w >= p.c.requests * p.next_n * p.heads) return;
+  const int64_t token = w / p.heads;
+  const int h = (int)(w % p.heads);
+  const int64_t r = token / p.next_n;
+  const int64_t len = row_len(p, r);
+  const int span = span_of(len);
+  const int64_t spans = (len + span - 1) / span;
+  if (spans == 1) return;
+  const int kvh = h / p.group;
+  const int row = (int)(token % p.next_n) * p.group + h % p.group;
+  const int rg = row / p.rows, rr = row % p.rows;
+  const int64_t slot0 =
+      ((r * p.c.kv_heads + kvh) * p.row_groups + rg) * p.spans * p.rows + rr;
+  float M = -INFINITY;
+  for (int64_t s = lane; s < spans; s += 32) M = fmaxf(M, p.part_ml[slot0 + s * p.rows].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float m0 = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f, acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+  for (int64_t s = 0; s < spans; ++s) {
+    const float2 ml = p.part_ml[slot0 + s * p.rows];
+    const float wt = ex2(ml.x - m0);
+    L = __fmaf_rn(wt, ml.y, L);
+    const float* o = p.part_o + (slot0 + s * p.rows) * DIM + lane * E;
+    if constexpr (E == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(o);
+      acc[0] = __fmaf_rn(wt, v.x, acc[0]);
+      acc[1] = __fmaf_rn(wt, v.y, acc[1]);
+      acc[2] = __fmaf_rn(wt, v.z, acc[2]);
+      acc[3] = __fmaf_rn(wt, v.w, acc[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(o);
+      acc[0] = __fmaf_rn(wt, v.x, acc[0]);
+      acc[1] = __fmaf_rn(wt, v.y, acc[1]);
+    }
+  }
+  const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
+  uint32_t b[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    b[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  __nv_bfloat16* out = p.out + w * DIM + lane * E;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(b[0], b[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = b[0];
+  if (lane == 0) p.lse[w] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+int sm_count(int dev) {
+  static std::atomic<int> cached[PerDeviceOnce::kMaxDevices];
+  const bool tracked = dev >= 0 && dev < PerDeviceOnce::kMaxDevices;
+  int n = tracked ? cached[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      return 152;
+    }
+    if (tracked) cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int R8, int DIM>
+cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, unsigned grid,
+                        cudaStream_t stream) {
+  using LY = Layout<R8, DIM>;
+  static PerDeviceOnce once;
+  auto kern = kv8_decode_kernel<R8, DIM>;
+  const cudaError_t e = set_max_dynamic_smem(once, dev, kern, LY::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), LY::kSmem, stream, 1u, map, p);
+}
+
+template <int DIM>
+cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStream_t stream) {
+  // At most one CTA per item, two per SM.
+  const int64_t items = p.c.requests * p.c.kv_heads * p.row_groups * p.spans;
+  const int64_t most = 2 * (int64_t)sm_count(dev);
+  const unsigned grid = (unsigned)(items < most ? items : most);
+  cudaError_t e;
+  switch ((p.rows + 7) / 8) {
+    case 1: e = launch_main<8, DIM>(map, p, dev, grid, stream); break;
+    case 2: e = launch_main<16, DIM>(map, p, dev, grid, stream); break;
+    case 3: e = launch_main<24, DIM>(map, p, dev, grid, stream); break;
+    case 4: e = launch_main<32, DIM>(map, p, dev, grid, stream); break;
+    default: e = launch_main<40, DIM>(map, p, dev, grid, stream); break;
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t rows = p.c.requests * p.next_n * p.heads;
+  return launch_pdl(kv8_decode_join_kernel<DIM>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0,
+                    stream, 1u, p);
+}
+
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
+                                  int64_t bt_stride) {
+  const Shape s = shape_of(next_n, heads / kv_heads);
+  const int64_t rows = requests * kv_heads * s.groups * max_spans(bt_stride * kPage) * s.rows;
+  return 256 + pad256((size_t)rows * dim * 4) + (size_t)rows * 8;
+}
+
+cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const int dim = a.c.dim;
+  CUtensorMap map;
+  const cuuint64_t gdim[2] = {(cuuint64_t)dim,
+                              (cuuint64_t)(a.c.num_pages * 2 * a.c.kv_heads * kPage)};
+  const cuuint64_t gstride[1] = {(cuuint64_t)dim};
+  const cuuint32_t box[2] = {(cuuint32_t)dim, (cuuint32_t)kPage};
+  const cuuint32_t estride[2] = {1, 1};
+  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.c.pages, gdim, gstride, box, estride,
+          CU_TENSOR_MAP_INTERLEAVE_NONE,
+          dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  int dev = 0;
+  cudaError_t e = stream_device(stream, &dev);
+  if (e != cudaSuccess) return e;
+  Params p;
+  const Shape s = shape_of(a.next_n, a.heads / a.c.kv_heads);
+  p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  p.q_stride = a.q_stride;
+  p.next_n = a.next_n;
+  p.heads = a.heads;
+  p.group = a.heads / a.c.kv_heads;
+  p.rows = s.rows;
+  p.row_groups = s.groups;
+  p.scale_log2 = a.scale * kLog2e;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.spans = max_spans(a.c.bt_stride * kPage);
+  const int64_t slots = a.c.requests * a.c.kv_heads * s.groups * p.spans * s.rows;
+  p.part_o = reinterpret_cast<float*>(a.workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) +
+                                        pad256((size_t)slots * dim * 4));
+  p.c = a.c;
+  return dim == 128 ? launch_dim<128>(map, p, dev, stream) : launch_dim<64>(map, p, dev, stream);
+}
+
+}  // namespace dsmla
