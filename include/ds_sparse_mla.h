@@ -397,7 +397,8 @@ int ds_kv_cache_write(const void* latent, int64_t num_rows, const int64_t* slots
  *
  * head_dim is 64 or 128; num_heads is a multiple of num_kv_heads (query head
  * h reads key/value head h / (num_heads / num_kv_heads)), both at most 1024,
- * and the product num_pages * 2 * num_kv_heads * 64 is at most 2^31 - 64.
+ * bt_stride is at most 2^24, num_requests at most 2^20, and the product
+ * num_pages * 2 * num_kv_heads * 64 below 2^31.
  *
  * Ragged calls give each request's tokens by token_starts, int32
  * [num_requests + 1] in device memory, never decreasing: request r owns rows

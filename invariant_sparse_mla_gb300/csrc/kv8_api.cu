@@ -57,8 +57,8 @@ int check_cache(const char* fn, const dsmla::Kv8Cache& c) {
   if (c.bt_stride < 1)
     return report_error(DS_ERR_SHAPE, "%s: bt_stride=%lld must be >= 1", fn,
                         (long long)c.bt_stride);
-  if (c.bt_stride > (int64_t)INT32_MAX / dsmla::kPage)
-    return report_error(DS_ERR_UNSUPPORTED, "%s: bt_stride=%lld is too large", fn,
+  if (c.bt_stride > (1 << 24))
+    return report_error(DS_ERR_UNSUPPORTED, "%s: bt_stride=%lld exceeds 2^24", fn,
                         (long long)c.bt_stride);
   if (c.requests < 0)
     return report_error(DS_ERR_SHAPE, "%s: num_requests=%lld is negative", fn,

@@ -1,25 +1,27 @@
 // Decode attention over the block-scaled 8-bit cache, on the 8-bit tensor
 // cores: keys and values are multiplied as they lie in the cache.
 //
-// Mathematics. With codes K, V (E4M3) and page scales a, b, token i of a page
-// gives s_i = scale * a * (q . K_i) and out = sum_i 2^(s_i - M) b V_i / L. The
-// tensor core takes 8-bit operands on both sides, so the side that is ours is
-// written as a sum of E4M3 pieces, each piece a column of its own so that it
-// has its own power-of-two weight:
-//   q = 2^-k (q0 + q1 / 32): |q| 2^k is at most 256, q0 = E4M3(q 2^k), q1 the
-//     rounded remainder times 32. A bf16 number has 8 significant bits and
-//     two pieces hold 2 x 4, so this is exact down to 2^-14 of the largest |q|
-//     of the row and off by 2^-23 of that below;
-//   p b = 2^-6 (p0 + p1 / 32 + p2 / 1024) with p <= 4 relative to the running
-//     maximum: at least 12 significant bits down to p = 2^-12, 8 down to
-//     2^-18, off by 2^-26 below (three pieces because a long tail of small
-//     weights counts: 2^17 positions of weight 2^-17 weigh as much as one
-//     of weight 1).
-// So S^T = K [q0 q1] and O^T = V^T [p0 p1 p2], both with the cache's bytes as
-// the A operand straight from TMA: no byte of the cache is converted.
+// Mathematics. With codes K, V (E4M3) and page scales a, b, position i of a
+// page gives s_i = scale * a * (q . K_i) and out = sum_i 2^(s_i - M) b V_i / L.
 //
-// The running maximum m of a row covers s_i + log2 b_i (then p b <= 4 whatever
-// the page scales are) and moves only when a tile passes it by more than 2^2;
+// S^T = K Q^T runs on the 8-bit tensor cores with the cache's key bytes as
+// they lie there. They take 8-bit operands on both sides, so q is written as
+// two E4M3 pieces, each a column of its own with its own power of two:
+//   q = 2^-k (q0 + q1 / 32): |q| 2^k is at most 256, q0 = E4M3(q 2^k), q1 the
+//   rounded remainder times 32. A bf16 number has 8 significant bits and two
+//   pieces hold 2 x 4, so this is exact down to 2^-14 of the row's largest
+//   |q| and off by 2^-23 of that below.
+//
+// O^T = V^T P^T runs in f16: E4M3 to f16 is exact and one instruction for two
+// values, and a weight p b, kept as 2^7 p b <= 2^15 in f16, has 11 significant
+// bits down to 2^-21 and at least 8 down to 2^-24 of the running maximum.
+// (Weights as three E4M3 pieces, with V as it lies, were built first: the
+// pieces cost more instructions per row than converting V costs per tile, and
+// allow a factor of 4 between a weight and the maximum instead of 2^8, so that
+// most tiles rescaled: 32 x 5 tokens of 64/8 heads took 1462 us.)
+//
+// The running maximum m of a row covers s_i + log2 b_i (p b <= 2^8 whatever
+// the page scales are) and moves only when a tile passes it by more than 2^8;
 // l = sum 2^(s_i - m) is kept in fp32 of the unrounded weights.
 //
 // Work split. A row's context is cut into spans of 256 to 4096 positions, the
@@ -30,10 +32,11 @@
 // 128-position tiles; a second kernel joins the spans in order. Rows with one
 // span are finished by the first kernel.
 //
-// Per CTA: warps 0-3 softmax (TMEM lane = position), warp 4 TMA producer over
-// a ring of tile halves (K or V of 128 positions), warp 5 MMA issuer. Ring,
-// S, P and O barriers run on across items, so the next item's pages stream in
-// while the last one is finished. The bound is HBM: 2 * dim bytes a position.
+// Per CTA: warps 0-7 softmax (TMEM lane = position; warps w and w + 4 take one
+// half of the rows each; they also convert V), warp 8 TMA producer over a ring
+// of K and a ring of V tiles (128 positions), warp 9 MMA issuer. The rings
+// and barriers run on across items, so the next item's pages stream in while
+// the last one is finished. The bound is HBM: 2 * dim bytes a position.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -52,12 +55,14 @@ namespace dsmla {
 namespace {
 
 constexpr int kTile = 128;                 // positions per tile (two pages)
-constexpr int kThreads = 192;
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmax = 32 * kSoftmaxWarps;
+constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
+constexpr int kThreads = kSoftmax + 64;
 constexpr int kMaxRows = 40;               // query rows of one row group
 constexpr int kMetaSlots = 8;
-constexpr float kTau = 2.0f;               // log2: p b may reach 2^kTau
-constexpr float kPScale = 64.0f;           // 2^(8 - kTau): stored weights stay <= 256
+constexpr float kTau = 8.0f;               // log2: p b may reach 2^kTau
+constexpr float kPScale = 128.0f;          // 2^(15 - kTau): stored weights stay <= 2^15
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMinSpan = 256, kMaxSpan = 4096;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -90,42 +95,49 @@ Shape shape_of(int next_n, int group) {
 
 template <int R8, int DIM>
 struct Layout {
-  static constexpr int kNP = (3 * R8 + 15) / 16 * 16;       // columns of P and O
-  static constexpr int kUnit = kTile * DIM;                 // K or V of one tile
-  static constexpr int kQBytes = 2 * R8 * DIM;
-  static constexpr int kPBytes = kNP * kTile;
-  static constexpr int kRest = kQBytes + 2 * kPBytes + 2048 + 1024;
+  static constexpr int kNP = (R8 + 15) / 16 * 16;           // columns of P and O
+  static constexpr int kUnit = kTile * DIM;                 // K or V codes of one tile
+  static constexpr int kQBytes = (2 * R8 * DIM + 1023) / 1024 * 1024;
+  static constexpr int kPBlock = kNP * 128;                 // P of 64 positions
+  static constexpr int kRest = 2 * kUnit + kQBytes + 2 * kPBlock + 2048 + 1024;
   static constexpr int kFit = (113 * 1024 - kRest) / kUnit;
   static constexpr int kUnits = kFit > 8 ? 8 : kFit;
-  static_assert(kUnits >= 4, "two tiles fit");
-  static constexpr int kRing = 0;
-  static constexpr int kP = kRing + kUnits * kUnit;         // 2 buffers
-  static constexpr int kQ = kP + 2 * kPBytes;
-  static constexpr int kBars = kQ + (kQBytes + 1023) / 1024 * 1024;
+  static constexpr int kNK = (kUnits + 1) / 2, kNV = kUnits / 2;   // stages of the two rings
+  static_assert(kNK >= 2 && kNV >= 1, "the next tile's K lands behind the present one's");
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + kNK * kUnit;
+  static constexpr int kV16 = kV + kNV * kUnit;             // V of the present tile in f16
+  static constexpr int kP = kV16 + 2 * kUnit;
+  static constexpr int kQ = kP + 2 * kPBlock;
+  static constexpr int kBars = kQ + kQBytes;
   static constexpr int kMeta = kBars + 32 * 8;              // kMetaSlots x 2 float4
-  static constexpr int kF = kMeta + kMetaSlots * 32;        // per row: factor, m, alpha
+  static constexpr int kF = kMeta + kMetaSlots * 32;        // per row: factor, reference, alpha
   static constexpr int kM = kF + R8 * 4;
   static constexpr int kAlpha = kM + R8 * 4;
   static constexpr int kWarpMax = kAlpha + R8 * 4;          // 4 x R8 floats
   static constexpr int kVis = kWarpMax + 4 * R8 * 4;        // positions each row sees
-  static constexpr int kMisc = kVis + R8 * 4;               // tmem slot, abort, start of work
+  static constexpr int kBy = kVis + R8 * 4;                 // by how much a reference moved
+  static constexpr int kSet = kBy + R8 * 4;                 // whether the row has one
+  static constexpr int kMisc = kSet + R8 * 4;               // tmem slot, abort, start of work
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
-  static constexpr uint32_t kCols = 2 * R8 + kNP <= 64 ? 64u : (2 * R8 + kNP <= 128 ? 128u : 256u);
-  static_assert(2 * R8 + kNP <= 256, "two CTAs per SM share TMEM");
+  static constexpr uint32_t kCols = 2 * R8 + kNP <= 32 ? 32u : (2 * R8 + kNP <= 64 ? 64u : 128u);
+  static_assert(2 * R8 + kNP <= 128, "TMEM columns");
 };
 
 enum Bar {
-  kFull = 0,        // <= 8: unit landed
-  kEmpty = 8,       // <= 8: unit's MMAs done
+  kKFull = 0,       // <= 4: K landed
+  kKEmpty = 4,      // <= 4: its MMAs done
+  kVFull = 8,       // <= 4: V landed
+  kVEmpty = 12,     // <= 4: V read by the softmax threads
   kSFull = 16,      // S ready
-  kSFree = 17,      // S read by the 128 softmax threads
-  kPFull = 18,      // 2: P written
-  kPvDone = 20,     // 2: PV done (P buffer free, O holds the tile)
-  kQReady = 22,     // Q pieces written
-  kDrain = 23,
-  kNumBars = 24
+  kSFree = 17,      // S read by the softmax threads
+  kPFull = 18,      // P and the f16 V written
+  kPvDone = 19,     // PV done (P and f16 V free, O holds the tile)
+  kQReady = 20,     // Q pieces written
+  kDrain = 21,
+  kNumBars = 22
 };
 
 struct Params {
@@ -144,15 +156,14 @@ struct Params {
 // The items of one CTA, in order. Every role walks the same sequence.
 struct Walk {
   int64_t at, end;       // tile numbers: start of the present item, end of the CTA's share
-  int64_t r;             // request
-  int64_t len;           // its positions
+  int r;                 // request
+  int len;               // its positions (at most 2^30)
   int tiles, span_tiles, spans;
   int hg, s;             // kv head * row_groups + row group; span
 };
 
-__device__ __forceinline__ int64_t row_len(const Params& p, int64_t r) {
-  int64_t len = p.c.lens[r];
-  const int64_t most = p.c.bt_stride * kPage;
+__device__ __forceinline__ int row_len(const Params& p, int64_t r) {
+  const int len = p.c.lens[r], most = (int)(p.c.bt_stride * kPage);
   return len < 0 ? 0 : (len > most ? most : len);
 }
 
@@ -213,8 +224,63 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t b) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-__device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Four E4M3 codes as two f16 pairs (exact).
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+
+// Sums over the warp of four values a lane: lane l returns the sum of value
+// 2 * bit4(l) + bit3(l).
+__device__ __forceinline__ float warp_sum4(const float* v, int lane) {
+  float a[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[2 + i] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[2 + i], 16);
+  }
+  const bool up = lane & 8;
+  float c = (up ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  return c;
+}
+
+// N (a multiple of 4) TMEM columns of the warp's lanes; tmem_fence(v) comes
+// between the loads and the first use.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+#pragma unroll
+  for (int c = 0; c < N; c += 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3])
+                 : "r"(taddr + c)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_fence(float* v) {
+  tmem_wait_ld();
+  // Uses of v depend on these (volatile statements keep their order), so none
+  // is scheduled before the wait.
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i])::"memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
+}
+
+__device__ __forceinline__ bool has_nan_code(uint4 v) {
+  const uint32_t k = 0x7F7F7F7Fu;
+  return (__vcmpeq4(v.x & k, k) | __vcmpeq4(v.y & k, k) | __vcmpeq4(v.z & k, k) |
+          __vcmpeq4(v.w & k, k)) != 0u;
 }
 
 // Byte offset of (row, byte) in a K-major tile of DIM-byte rows in the swizzle
@@ -249,7 +315,7 @@ template <int R8, int DIM>
 __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     const __grid_constant__ CUtensorMap map, const Params p) {
   using LY = Layout<R8, DIM>;
-  constexpr int NP = LY::kNP, NU = LY::kUnits;
+  constexpr int NP = LY::kNP, NK = LY::kNK, NV = LY::kNV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -260,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
   float* alpha_s = reinterpret_cast<float*>(smem + LY::kAlpha);
   float* wmax_s = reinterpret_cast<float*>(smem + LY::kWarpMax);
   int* vis_s = reinterpret_cast<int*>(smem + LY::kVis);
+  float* by_s = reinterpret_cast<float*>(smem + LY::kBy);
+  int* set_s = reinterpret_cast<int*>(smem + LY::kSet);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 4);
   int64_t* start_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 8);   // request, its first tile
@@ -268,11 +336,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool all = i == kSFree || i == kPFull || i == kPFull + 1 || i == kQReady;
-      mbar_init(&bars[i], all ? 128u : 1u);
+      const bool all = i == kSFree || i == kPFull || i == kQReady ||
+                       (i >= kVEmpty && i < kVEmpty + NV);
+      mbar_init(&bars[i], all ? (uint32_t)kSoftmax : 1u);
     }
     mbar_fence_init();
     *abort_s = 0;
+    for (int r = 0; r < R8; ++r) set_s[r] = 0;
     start_s[0] = -1;
   }
   if (warp == kMmaWarp) {
@@ -322,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk w;
-  w.r = start_s[0];
+  w.r = (int)start_s[0];
   w.end = hi;
   bool some = w.r >= 0;
   if (some) {
@@ -340,25 +410,25 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
   bool failed = false;
   if (warp == kProducerWarp) {
     // ---------------------------------------------------------- producer
-    int64_t u = 0;          // units issued
-    int64_t g = 0;          // tiles issued
+    uint32_t g = 0;         // tiles issued
+    uint32_t k_issued = 0, v_issued = 0;
     int err_bits = 0;
     const int none = (int)(p.c.num_pages * 2 * p.c.kv_heads * kPage);   // a row past the pool: zeros
     while (some && !failed) {
       const int kvh = w.hg / p.row_groups;
       const int nt = item_tiles(w);
-      const int64_t block0 = (int64_t)w.s * w.span_tiles * 2;
-      const int64_t blocks = (w.len + kPage - 1) / kPage;
+      const int block0 = w.s * w.span_tiles * 2;
+      const int blocks = (w.len + kPage - 1) / kPage;
       // Lane l looks up pages l and l + 32 of the span, all at once.
       int y[2];
       float ks[2], vs[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t b = block0 + lane + 32 * i;
+        const int b = block0 + lane + 32 * i;
         y[i] = none;
         ks[i] = vs[i] = 0.0f;
         if (lane + 32 * i < 2 * nt && b < blocks) {
-          const int64_t page = p.c.block_table[w.r * p.c.bt_stride + b];
+          const int64_t page = p.c.block_table[(int64_t)w.r * p.c.bt_stride + b];
           if (page >= 0 && page < p.c.num_pages) {
             const int64_t part = page * 2 * p.c.kv_heads + kvh;
             y[i] = (int)(part * kPage);
@@ -382,9 +452,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         bool ok = true;
         if (lane == 0) {
 #pragma unroll
-          for (int side = 0; side < 2; ++side, ++u) {
-            const int st = (int)(u % NU);
-            if (u >= NU && !mbar_wait(&bars[kEmpty + st], (uint32_t)((u / NU - 1) & 1))) {
+          for (int side = 0; side < 2; ++side) {
+            const int n = side ? NV : NK;
+            const int st = (int)(g % n);
+            uint64_t* full = &bars[(side ? kVFull : kKFull) + st];
+            if (g >= n && !mbar_wait(&bars[(side ? kVEmpty : kKEmpty) + st],
+                                     (uint32_t)((g / n - 1) & 1))) {
               ok = false;
               break;
             }
@@ -394,13 +467,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
                 meta[(g & (kMetaSlots - 1)) * 2 + h] =
                     make_float4(kk[h], vv[h], log2f(vv[h]), yy[h] == none ? 0.0f : 1.0f);
             }
-            mbar_arrive_expect_tx(&bars[kFull + st], LY::kUnit);
-            const uint32_t dst = sbase + LY::kRing + st * LY::kUnit;
+            mbar_arrive_expect_tx(full, LY::kUnit);
+            const uint32_t dst = sbase + (side ? LY::kV : LY::kK) + st * LY::kUnit;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int row = yy[h] == none ? none : yy[h] + side * p.c.kv_heads * kPage;
-              tma_load_box(dst + h * (kPage * DIM), &map, 0, row, &bars[kFull + st]);
+              tma_load_box(dst + h * (kPage * DIM), &map, 0, row, full);
             }
+            if (side == 0)
+              k_issued = g + 1;
+            else
+              v_issued = g + 1;
           }
         }
         if (!__all_sync(0xffffffffu, ok)) {
@@ -412,8 +489,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     }
     if (lane == 0) {
       // Every copy has landed before the CTA can exit.
-      for (int64_t i = u > NU ? u - NU : 0; i < u; ++i)
-        if (!mbar_wait(&bars[kFull + i % NU], (uint32_t)((i / NU) & 1))) failed = true;
+      for (uint32_t i = k_issued > NK ? k_issued - NK : 0; i < k_issued; ++i)
+        if (!mbar_wait(&bars[kKFull + i % NK], (uint32_t)((i / NK) & 1))) failed = true;
+      for (uint32_t i = v_issued > NV ? v_issued - NV : 0; i < v_issued; ++i)
+        if (!mbar_wait(&bars[kVFull + i % NV], (uint32_t)((i / NV) & 1))) failed = true;
     }
     if (err_bits && p.c.err != nullptr) atomicOr(p.c.err, err_bits);
     __syncwarp();
@@ -421,52 +500,47 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     // -------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_s = make_idesc_e4m3(kTile, 2 * R8, 0, 0);
-      constexpr uint32_t idesc_o = make_idesc_e4m3(DIM, NP, 1, 0);
+      constexpr uint32_t idesc_o = make_idesc_f16(DIM, NP, 1, 0);
       const uint64_t q_desc = tile_desc<DIM>(sbase + LY::kQ);
-      const uint64_t ring_desc = tile_desc<DIM>(sbase + LY::kRing);
+      const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
+      // f16 V: 64-dim column blocks of 128 rows x 128 bytes.
+      const uint64_t v_desc = make_sw128_desc(sbase + LY::kV16, kTile * 128, 1024);
       const uint64_t p_desc = make_sw128_desc(sbase + LY::kP, 16, 1024);
-      int64_t g = 0;          // tiles whose S was issued
-      int64_t pv = 0;         // tiles whose PV was issued
+      uint32_t g = 0;         // tiles whose S was issued
+      uint32_t pv = 0;         // tiles whose PV was issued
       bool first_of_pv = true;
       auto issue_pv = [&](bool first) {
         // O^T (+)= V^T P^T of tile pv.
-        const int64_t u = 2 * pv + 1;
-        const int st = (int)(u % NU), pb = (int)(pv & 1);
-        if (!mbar_wait(&bars[kPFull + pb], (uint32_t)((pv >> 1) & 1)) ||
-            !mbar_wait(&bars[kFull + st], (uint32_t)((u / NU) & 1)))
-          return false;
+        if (!mbar_wait(&bars[kPFull], (uint32_t)(pv & 1))) return false;
         tc_fence_after();
-        const uint64_t a = ring_desc + (uint64_t)((st * LY::kUnit) >> 4);
-        const uint64_t b = p_desc + (uint64_t)((pb * LY::kPBytes) >> 4);
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k)
-          mma_f8_ss(tmem + 2 * R8, a + ((k * 32 * DIM) >> 4), b + ((k * 32) >> 4), idesc_o,
-                    (!first || k > 0) ? 1u : 0u);
-        mma_commit(&bars[kEmpty + st]);
-        mma_commit(&bars[kPvDone + pb]);
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_bf16_ss(tmem + 2 * R8, v_desc + ((k * 16 * 128) >> 4),
+                      p_desc + (((k >> 2) * LY::kPBlock + (k & 3) * 32) >> 4), idesc_o,
+                      (!first || k > 0) ? 1u : 0u);
+        mma_commit(&bars[kPvDone]);
         ++pv;
         return true;
       };
-      int64_t items = 0;
+      uint32_t items = 0;
       while (some && !failed) {
         const int nt = item_tiles(w);
         for (int t = 0; t < nt && !failed; ++t) {
-          const int64_t u = 2 * g;
-          const int st = (int)(u % NU);
+          const int st = (int)(g % NK);
           // The item's Q pieces (written after the last item's S was read);
           // S is free again once tile g - 1 was read.
           if (t == 0 && !mbar_wait(&bars[kQReady], (uint32_t)(items & 1))) failed = true;
           if (!failed && g > 0 && !mbar_wait(&bars[kSFree], (uint32_t)((g - 1) & 1)))
             failed = true;
-          if (!failed && !mbar_wait(&bars[kFull + st], (uint32_t)((u / NU) & 1))) failed = true;
+          if (!failed && !mbar_wait(&bars[kKFull + st], (uint32_t)((g / NK) & 1))) failed = true;
           if (failed) break;
           tc_fence_after();
-          const uint64_t a = ring_desc + (uint64_t)((st * LY::kUnit) >> 4);
+          const uint64_t a = k_desc + (uint64_t)((st * LY::kUnit) >> 4);
 #pragma unroll
           for (int k = 0; k < DIM / 32; ++k)
             mma_f8_ss(tmem, a + ((k * 32) >> 4), q_desc + ((k * 32) >> 4), idesc_s,
                       k > 0 ? 1u : 0u);
-          mma_commit(&bars[kEmpty + st]);
+          mma_commit(&bars[kKEmpty + st]);
           mma_commit(&bars[kSFull]);
           ++g;
           if (t > 0) {
@@ -486,73 +560,76 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int dim0 = DIM == 128 ? warp * 32 + lane : warp * 16 + lane;   // this lane's O row
+    constexpr int RH = R8 / 2;             // rows of this warp: half * RH ...
+    const int quad = warp & 3, half = warp >> 2;
+    const int tok = quad * 32 + lane;      // position of the tile (TMEM lane)
+    const int rh = half * RH;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + rh, t_o = tmem + lane_base + 2 * R8 + rh;
+    const int dim0 = DIM == 128 ? tok : quad * 16 + lane;   // this lane's O row
     const bool has_dim = DIM == 128 || lane < 16;
-    float l[R8];
-    int64_t g = 0;
+    // P[row][position] in f16, two blocks of 64 positions; byte of this thread's
+    // position in row 0 of its rows, without the swizzle's row bits.
+    uint8_t* const p_at = smem + LY::kP + (tok >> 6) * LY::kPBlock;
+    const int pc = (tok & 63) >> 3, pb = (tok & 7) * 2;
+    float l[RH];
+    uint32_t g = 0;
     int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
     while (some && !failed) {
       const int nt = item_tiles(w);
       const int kvh = w.hg / p.row_groups, rg = w.hg % p.row_groups;
       const int row0 = rg * p.rows;
       const int rows = min(p.rows, p.next_n * p.group - row0);
-      const int64_t qid = w.r * hgs + w.hg;
-      // The Q pieces: warp w takes rows w, w + 4, ...; a row's largest |q| sets
+      const int64_t qid = (int64_t)w.r * hgs + w.hg;
+      // The Q pieces: warp w takes rows w, w + 8, ...; a row's largest |q| sets
       // its power of two. (All S that read the last Q are complete: their
       // results were read.)
       if (qid != last_q) {
         last_q = qid;
-        for (int r = warp; r < R8; r += 4) {
-          constexpr int E = DIM / 32;
-          float x[E], a = 0.0f;
-          bool nan = false;
+        constexpr int E = DIM / 32, NR = R8 / 8;
+        float x[NR][E];
 #pragma unroll
-          for (int i = 0; i < E; ++i) x[i] = 0.0f;
+        for (int i = 0; i < NR; ++i) {
+          const int r = warp + 8 * i;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[i][e] = 0.0f;
           if (r < rows) {
             const int j = (row0 + r) / p.group, gh = (row0 + r) % p.group;
-            const __nv_bfloat16* src = p.q + (w.r * p.next_n + j) * p.q_stride +
+            const __nv_bfloat16* src = p.q + ((int64_t)w.r * p.next_n + j) * p.q_stride +
                                        ((int64_t)kvh * p.group + gh) * DIM + lane * E;
-            if constexpr (E == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              x[0] = __uint_as_float(v.x << 16);
-              x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-              x[2] = __uint_as_float(v.y << 16);
-              x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-            } else {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(src);
-              x[0] = __uint_as_float(v << 16);
-              x[1] = __uint_as_float(v & 0xFFFF0000u);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const uint32_t v = reinterpret_cast<const uint32_t*>(src)[e / 2];
+              x[i][e] = __uint_as_float(v << 16);
+              x[i][e + 1] = __uint_as_float(v & 0xFFFF0000u);
             }
           }
+        }
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            a = fmaxf(a, fabsf(x[i]));
-            nan |= x[i] != x[i];
+        for (int i = 0; i < NR; ++i) {
+          const int r = warp + 8 * i;
+          float a = 0.0f;
+          bool nan = false;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            a = fmaxf(a, fabsf(x[i][e]));
+            nan |= x[i][e] != x[i][e];
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
           nan = __any_sync(0xffffffffu, nan) || a == INFINITY;
           // a 2^k in [128, 256); 2^k stays a normal float.
           int k = a > 0.0f ? 7 - ((int)(__float_as_uint(a) >> 23) - 127) : 0;
           k = k > 120 ? 120 : (k < -120 ? -120 : k);
           const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-          uint32_t b0[E / 2], b1[E / 2];
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            const float u0 = x[2 * i] * up, u1 = x[2 * i + 1] * up;
-            b0[i] = to_e4m3x2(u0, u1);
-            const float2 h = from_e4m3x2(b0[i]);
-            b1[i] = to_e4m3x2((u0 - h.x) * 32.0f, (u1 - h.y) * 32.0f);
-          }
-          const uint32_t at0 = sbase + LY::kQ + swz<DIM>(r, lane * E);
-          const uint32_t at1 = sbase + LY::kQ + swz<DIM>(R8 + r, lane * E);
-          if constexpr (E == 4) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0), "r"(b0[0] | (b0[1] << 16)) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1), "r"(b1[0] | (b1[1] << 16)) : "memory");
-          } else {
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at0), "h"((uint16_t)b0[0]) : "memory");
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at1), "h"((uint16_t)b1[0]) : "memory");
+          for (int e = 0; e < E; e += 2) {
+            const float u0 = x[i][e] * up, u1 = x[i][e + 1] * up;
+            const uint32_t b0 = to_e4m3x2(u0, u1);
+            const float2 h = from_e4m3x2(b0);
+            const uint32_t b1 = to_e4m3x2((u0 - h.x) * 32.0f, (u1 - h.y) * 32.0f);
+            uint8_t* q0 = smem + LY::kQ;
+            *reinterpret_cast<uint16_t*>(q0 + swz<DIM>(r, lane * E + e)) = (uint16_t)b0;
+            *reinterpret_cast<uint16_t*>(q0 + swz<DIM>(R8 + r, lane * E + e)) = (uint16_t)b1;
           }
           if (lane == 0)
             f_s[r] = nan ? NAN : __uint_as_float((uint32_t)(127 - k) << 23) * p.scale_log2;
@@ -560,233 +637,248 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         fence_proxy_async_smem();
       }
       // Row r's token j sees len - next_n + 1 + j positions (clamped).
-      const int64_t raw_len = p.c.lens[w.r];
-      auto visible = [&](int r) {
-        const int64_t v = raw_len - p.next_n + 1 + (row0 + r) / p.group;
-        return (int)(v < 0 ? 0 : (v > w.len ? w.len : v));
-      };
       if (tid < R8) {
-        m_s[tid] = -INFINITY;
-        vis_s[tid] = visible(tid);
+        const int64_t v = (int64_t)p.c.lens[w.r] - p.next_n + 1 + (row0 + tid) / p.group;
+        m_s[tid] = 0.0f;
+        vis_s[tid] = (int)(v < 0 ? 0 : (v > w.len ? w.len : v));
       }
 #pragma unroll
-      for (int r = 0; r < R8; ++r) l[r] = 0.0f;
-      uint64_t nan_rows = 0;    // rows that see a NaN value in this lane's dim
-      named_bar_sync(1, 128);   // f_s, m_s, vis_s
+      for (int i = 0; i < RH; ++i) l[i] = 0.0f;
+      uint32_t nan_rows = 0;    // rows that see a NaN value in this lane's dim
+      named_bar_sync(1, kSoftmax);   // f_s, m_s, vis_s
       mbar_arrive(&bars[kQReady]);
-
       const int min_vis = vis_s[0];
+      bool unset = true;        // some row has no reference yet
+
       for (int t = 0; t < nt; ++t, ++g) {
-        const int64_t pos0 = ((int64_t)w.s * w.span_tiles + t) * kTile;
-        const int64_t pos = pos0 + tid;
-        const int pb = (int)(g & 1);
+        const int pos0 = (w.s * w.span_tiles + t) * kTile;
+        const int pos = pos0 + tok;
         if (!mbar_wait(&bars[kSFull], (uint32_t)(g & 1))) *abort_s = 1;
         tc_fence_after();
-        const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tid >> 6)];   // ks, vs, log2 vs, valid
-        float s[R8];
+        const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tok >> 6)];   // ks, vs, log2 vs, valid
+        float s[RH];
+        {
+          float lo[RH];
+          tmem_ld<RH>(t_s, s);
+          tmem_ld<RH>(t_s + R8, lo);
+          tmem_fence<RH>(s);
+          tmem_fence<RH>(lo);
 #pragma unroll
-        for (int c = 0; c < R8 / 8; ++c) {
-          float lo8[8];
-          tmem_ld8x2_sync(tmem + lane_base + c * 8, tmem + lane_base + R8 + c * 8, s + 8 * c, lo8);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s[8 * c + i] = __fmaf_rn(lo8[i], 0.03125f, s[8 * c + i]);
+          for (int i = 0; i < RH; ++i) s[i] = __fmaf_rn(lo[i], 0.03125f, s[i]);
         }
         tc_fence_before();
         mbar_arrive(&bars[kSFree]);
-        bool above = false;
         const bool here = mt.w != 0.0f && pos < w.len;
-        if (pos0 + kTile <= min_vis) {
+        const bool edge = pos0 + kTile > min_vis;   // some row's context ends in the tile
+        // s becomes the exponent relative to the row's reference.
 #pragma unroll
-          for (int r = 0; r < R8; ++r) {
-            const float x = s[r] * (f_s[r] * mt.x);
-            s[r] = here ? x : -INFINITY;
-            above |= s[r] + mt.z > m_s[r] + kTau;
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < R8; ++r) {
-            const float x = s[r] * (f_s[r] * mt.x);
-            s[r] = here && pos < vis_s[r] ? x : -INFINITY;
-            above |= s[r] + mt.z > m_s[r] + kTau;
-          }
+        for (int i = 0; i < RH; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(f_s + rh + i);
+          const float4 m = *reinterpret_cast<const float4*>(m_s + rh + i);
+          s[i] = __fmaf_rn(s[i], f.x * mt.x, -m.x);
+          s[i + 1] = __fmaf_rn(s[i + 1], f.y * mt.x, -m.y);
+          s[i + 2] = __fmaf_rn(s[i + 2], f.z * mt.x, -m.z);
+          s[i + 3] = __fmaf_rn(s[i + 3], f.w * mt.x, -m.w);
         }
-        const bool move = named_bar_or(2, 128, above);
+        if (!here) {
+#pragma unroll
+          for (int i = 0; i < RH; ++i) s[i] = -INFINITY;
+        } else if (edge) {
+#pragma unroll
+          for (int i = 0; i < RH; ++i)
+            if (pos >= vis_s[rh + i]) s[i] = -INFINITY;
+        }
+        bool above = unset;
+        const float slack = kTau - mt.z;
+#pragma unroll
+        for (int i = 0; i < RH; ++i) above |= s[i] > slack;
+        const bool move = named_bar_or(2, kSoftmax, above);
         if (*abort_s) {
           failed = true;
           break;
         }
         if (move) {
-          // Some row's maximum grows by more than 2^kTau: new maxima for the
-          // rows that do (by their own values alone), and their sums and
-          // outputs so far rescaled.
+          // Rows without a reference take the largest s + log2 b of the tile;
+          // rows that pass theirs by more than 2^kTau move it there, and
+          // their sums and outputs so far are rescaled. Each row by its own
+          // values alone.
 #pragma unroll
-          for (int r = 0; r < R8; ++r) {
-            const int k = __reduce_max_sync(0xffffffffu, float_key(s[r] + mt.z));
-            if (lane == 0) wmax_s[warp * R8 + r] = key_float(k);
+          for (int i = 0; i < RH; ++i) {
+            const int k = __reduce_max_sync(0xffffffffu, float_key(s[i] + mt.z));
+            if (lane == (i & 31)) wmax_s[quad * R8 + rh + i] = key_float(k);
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1, kSoftmax);
+          bool open = false;
           if (tid < R8) {
             float top = wmax_s[tid];
 #pragma unroll
             for (int v = 1; v < 4; ++v) top = fmaxf(top, wmax_s[v * R8 + tid]);
-            const float old = m_s[tid];
-            float al = 1.0f;
-            if (top > old + kTau) {
-              al = ex2(old - top);   // 0 for the first
-              m_s[tid] = top;
+            const int vis = vis_s[tid];
+            const bool first = set_s[tid] == 0;
+            float by = 0.0f, al = 1.0f;
+            if (first ? top > -INFINITY : top > kTau) {
+              by = top;
+              al = first ? 0.0f : ex2(-top);
+              m_s[tid] += top;
+              set_s[tid] = 1;
+            } else if (first) {
+              open = vis > pos0 + kTile;   // it may see something later
             }
             alpha_s[tid] = al;
+            by_s[tid] = by;
           }
-          named_bar_sync(1, 128);
+          unset = named_bar_or(1, kSoftmax, open);
 #pragma unroll
-          for (int r = 0; r < R8; ++r) l[r] *= alpha_s[r];
+          for (int i = 0; i < RH; ++i) {
+            l[i] *= alpha_s[rh + i];
+            s[i] -= by_s[rh + i];
+          }
           if (t > 0) {
-            if (!mbar_wait(&bars[kPvDone + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1)))
-              *abort_s = 1;
+            if (!mbar_wait(&bars[kPvDone], (uint32_t)((g - 1) & 1))) *abort_s = 1;
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < R8 / 8; ++c) {
-              float al[8];
-              bool change = false;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                al[i] = alpha_s[8 * c + i];
-                change |= al[i] != 1.0f;
-              }
-              if (change) {
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                  const uint32_t at = tmem + lane_base + 2 * R8 + k * R8 + 8 * c;
-                  float o[8];
-                  tmem_ld8_sync(at, o);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) o[i] *= al[i];
-                  tmem_st8(at, o);
-                }
+            for (int i = 0; i < RH; i += 4) {
+              const float4 al = *reinterpret_cast<const float4*>(alpha_s + rh + i);
+              if (al.x != 1.0f || al.y != 1.0f || al.z != 1.0f || al.w != 1.0f) {
+                float o[4];
+                tmem_ld<4>(t_o + i, o);
+                tmem_fence<4>(o);
+                o[0] *= al.x;
+                o[1] *= al.y;
+                o[2] *= al.z;
+                o[3] *= al.w;
+                tmem_st4(t_o + i, o);
               }
             }
             tmem_wait_st();
           }
         }
-        // The weights, their sum, and their pieces into P (once PV of tile
-        // g - 2 has read that buffer).
-        if (g >= 2 && !mbar_wait(&bars[kPvDone + pb], (uint32_t)(((g >> 1) - 1) & 1)))
-          *abort_s = 1;
-        const uint32_t pbase = sbase + LY::kP + pb * LY::kPBytes;
-        const float vscale = mt.y * kPScale;
+        // The weights, their sum, and P (free once PV of the last tile is done).
+        const float vscale = here ? mt.y * kPScale : 0.0f;
 #pragma unroll
-        for (int r = 0; r < R8; r += 2) {
-          float e[2];
+        for (int i = 0; i < RH; ++i) {
+          s[i] = ex2(s[i]);
+          l[i] += s[i];
+        }
+        if (g > 0 && !mbar_wait(&bars[kPvDone], (uint32_t)((g - 1) & 1))) *abort_s = 1;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float m = m_s[r + i];
-            e[i] = ex2(s[r + i] - (m == -INFINITY ? 0.0f : m));
-            l[r + i] += e[i];
-            e[i] = here ? e[i] * vscale : 0.0f;
-          }
-          uint32_t b[3];
+        for (int i = 0; i < RH; i += 2) {
+          const __half2 h = __floats2half2_rn(s[i] * vscale, s[i + 1] * vscale);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            b[k] = to_e4m3x2(e[0], e[1]);
-            if (k < 2) {
-              const float2 h = from_e4m3x2(b[k]);
-              e[0] = (e[0] - h.x) * 32.0f;
-              e[1] = (e[1] - h.y) * 32.0f;
-            }
-            const int n = k * R8 + r;
-            st_u8(pbase + swz<128>(n, tid), b[k]);
-            st_u8(pbase + swz<128>(n + 1, tid), b[k] >> 8);
+          for (int e = 0; e < 2; ++e) {
+            const int r = rh + i + e;
+            *reinterpret_cast<__half*>(p_at + r * 128 + ((pc ^ (r & 7)) << 4) + pb) =
+                e ? __high2half(h) : __low2half(h);
           }
         }
-        // Value rows behind the context hold anything: a weight of 0 times a
-        // NaN code is NaN, so they become 0. Where the rows of the group see
-        // different lengths, a NaN value that only some of them see becomes 0
-        // as well and is remembered for those.
-        if (pos0 + kTile > min_vis) {
-          const int64_t u = 2 * g + 1;
-          const int st = (int)(u % NU);
-          if (!mbar_wait(&bars[kFull + st], (uint32_t)((u / NU) & 1))) *abort_s = 1;
-          uint8_t* vt = smem + LY::kRing + st * LY::kUnit;
-          uint4* row = reinterpret_cast<uint4*>(vt + tid * DIM);
+        // V to f16: half a position's dims per thread. What lies behind the
+        // context is anything, and a weight of 0 times NaN is NaN: it becomes 0.
+        {
+          const int st = (int)(g % NV);
+          if (!mbar_wait(&bars[kVFull + st], (uint32_t)((g / NV) & 1))) *abort_s = 1;
+          const uint8_t* src = smem + LY::kV + st * LY::kUnit;
+          uint8_t* dst = smem + LY::kV16 + tok * 128;
+          constexpr int NC = DIM / 32;         // 16-code chunks of this thread
+          uint4 v[NC];
           bool nan = false;
-          if (pos >= w.len) {
 #pragma unroll
-            for (int i = 0; i < DIM / 16; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
-          } else if (pos >= min_vis) {
-#pragma unroll
-            for (int i = 0; i < DIM / 16; ++i) {
-              const uint4 v = row[i];
-              nan |= (__vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                      __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                      __vcmpeq4(v.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                      __vcmpeq4(v.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
-            }
+          for (int c = 0; c < NC; ++c) {
+            v[c] = *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, (half * NC + c) * 16));
+            if (pos >= w.len) v[c] = make_uint4(0u, 0u, 0u, 0u);
           }
-          if (named_bar_or(2, 128, nan)) {
-            if (has_dim) {
-              for (int i = 0; i < kTile; ++i) {
-                const int64_t ps = pos0 + i;
-                if (ps < min_vis || ps >= w.len) continue;
-                uint8_t* at = vt + swz<DIM>(i, dim0);
-                if ((*at & 0x7Fu) != 0x7Fu) continue;
-                *at = 0;
-                for (int r = 0; r < rows; ++r)
-                  if (ps < vis_s[r]) nan_rows |= 1ull << r;
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) nan |= has_nan_code(v[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const uint2 a = codes_to_f16(v[c].x), b = codes_to_f16(v[c].y),
+                        d = codes_to_f16(v[c].z), e = codes_to_f16(v[c].w);
+            const int cc = half * NC + c;
+            uint8_t* at = dst + (cc >> 2) * (kTile * 128);
+            const int ch = (cc & 3) * 2;
+            *reinterpret_cast<uint4*>(at + ((ch ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (tok & 7)) << 4)) =
+                make_uint4(d.x, d.y, e.x, e.y);
+          }
+          mbar_arrive(&bars[kVEmpty + st]);
+          // Where the rows of the group see different lengths, a NaN value that
+          // only some of them see becomes 0 and is remembered for those (each
+          // warp for its own rows; warps of the first half clear it).
+          if (edge && named_bar_or(2, kSoftmax, nan && pos >= min_vis)) {
+            for (int pass = 0; pass < 2; ++pass) {
+              if (has_dim && (pass == 0 || half == 0)) {
+                for (int i = 0; i < kTile; ++i) {
+                  const int ps = pos0 + i;
+                  if (ps < min_vis || ps >= w.len) continue;
+                  uint16_t* at = reinterpret_cast<uint16_t*>(
+                      smem + LY::kV16 + (dim0 >> 6) * (kTile * 128) + swz<128>(i, (dim0 & 63) * 2));
+                  if ((*at & 0x7FFFu) <= 0x7C00u) continue;
+                  if (pass == 1) *at = 0;
+                  for (int r = 0; r < RH; ++r)
+                    if (ps < vis_s[rh + r]) nan_rows |= 1u << r;
+                }
               }
+              named_bar_sync(1, kSoftmax);
             }
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&bars[kPFull + pb]);
+        mbar_arrive(&bars[kPFull]);
       }
       if (failed) break;
 
       // ------------------------------------------------ end of the item
-      if (!mbar_wait(&bars[kPvDone + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) *abort_s = 1;
-      tc_fence_after();
 #pragma unroll
-      for (int r = 0; r < R8; ++r) {
-        float v = l[r];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) wmax_s[warp * R8 + r] = v;
+      for (int i = 0; i < RH; i += 4) {
+        const float v = warp_sum4(l + i, lane);
+        const int r = ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
+        if ((lane & 7) == 0) wmax_s[quad * R8 + rh + i + r] = v;
       }
-      named_bar_sync(1, 128);
+      if (!mbar_wait(&bars[kPvDone], (uint32_t)((g - 1) & 1))) *abort_s = 1;
+      tc_fence_after();
+      float o[RH];
+      tmem_ld<RH>(t_o, o);
+      tmem_fence<RH>(o);
+      named_bar_sync(1, kSoftmax);
       if (*abort_s) {
         failed = true;
         break;
       }
-      const int64_t slot = (qid * p.spans + w.s) * p.rows;
+      if (nan_rows != 0) {
 #pragma unroll
-      for (int c = 0; c < R8 / 8; ++c) {
-        if (c * 8 >= rows) break;
-        float o0[8], o1[8], o2[8];
-        const uint32_t at = tmem + lane_base + 2 * R8 + 8 * c;
-        tmem_ld8x2_sync(at, at + R8, o0, o1);
-        tmem_ld8_sync(at + 2 * R8, o2);
+        for (int i = 0; i < RH; ++i)
+          if ((nan_rows >> i) & 1) o[i] = NAN;
+      }
+      auto sum_of = [&](int r) {
+        return (wmax_s[r] + wmax_s[R8 + r]) + (wmax_s[2 * R8 + r] + wmax_s[3 * R8 + r]);
+      };
+      if (w.spans == 1) {
+        // The row is complete.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 8 * c + i;
-          if (r >= rows) break;
-          const float ls = (wmax_s[r] + wmax_s[R8 + r]) + (wmax_s[2 * R8 + r] + wmax_s[3 * R8 + r]);
-          float o = __fmaf_rn(o2[i], 0.0009765625f, __fmaf_rn(o1[i], 0.03125f, o0[i])) *
-                    (1.0f / kPScale);
-          if ((nan_rows >> r) & 1) o = NAN;
-          if (w.spans == 1) {
-            const int64_t token = w.r * p.next_n + (row0 + r) / p.group;
+        for (int i = 0; i < RH; ++i) {
+          const int r = rh + i;
+          if (r < rows) {
+            const int64_t token = (int64_t)w.r * p.next_n + (row0 + r) / p.group;
             const int64_t h = token * p.heads + kvh * p.group + (row0 + r) % p.group;
-            if (has_dim)
-              p.out[h * DIM + dim0] = __float2bfloat16(ls == 0.0f ? 0.0f : __fdiv_rn(o, ls));
-            if (tid == 0) p.lse[h] = ls == 0.0f ? -INFINITY : (m_s[r] + log2f(ls)) * kLn2;
-          } else {
-            if (has_dim) p.part_o[(slot + r) * DIM + dim0] = o;
-            if (tid == 0) p.part_ml[slot + r] = make_float2(m_s[r], ls);
+            const float ls = sum_of(r);
+            const float x = ls == 0.0f ? 0.0f : __fdiv_rn(o[i] * (1.0f / kPScale), ls);
+            if (has_dim) p.out[h * DIM + dim0] = __float2bfloat16(x);
+            if (tok == 0) p.lse[h] = ls == 0.0f ? -INFINITY : (m_s[r] + log2f(ls)) * kLn2;
           }
         }
+      } else {
+        const int64_t slot = (qid * p.spans + w.s) * p.rows;
+        float* at = p.part_o + (slot + rh) * DIM + dim0;
+#pragma unroll
+        for (int i = 0; i < RH; ++i)
+          if (has_dim && rh + i < rows) at[i * DIM] = o[i] * (1.0f / kPScale);
+        if (tid < rows)
+          p.part_ml[slot + tid] = make_float2(set_s[tid] ? m_s[tid] : -INFINITY, sum_of(tid));
       }
-      named_bar_sync(1, 128);   // m_s and wmax_s are read before the next item writes them
+      if (tid < R8) set_s[tid] = 0;
+      named_bar_sync(1, kSoftmax);   // m_s and wmax_s are read before the next item writes them
       some = walk_next(p, w);
     }
   }
@@ -811,9 +903,9 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
   const int64_t token = w / p.heads;
   const int h = (int)(w % p.heads);
   const int64_t r = token / p.next_n;
-  const int64_t len = row_len(p, r);
+  const int len = row_len(p, r);
   const int span = span_of(len);
-  const int64_t spans = (len + span - 1) / span;
+  const int spans = (len + span - 1) / span;
   if (spans == 1) return;
   const int kvh = h / p.group;
   const int row = (int)(token % p.next_n) * p.group + h % p.group;
@@ -821,7 +913,7 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
   const int64_t slot0 =
       ((r * p.c.kv_heads + kvh) * p.row_groups + rg) * p.spans * p.rows + rr;
   float M = -INFINITY;
-  for (int64_t s = lane; s < spans; s += 32) M = fmaxf(M, p.part_ml[slot0 + s * p.rows].x);
+  for (int s = lane; s < spans; s += 32) M = fmaxf(M, p.part_ml[slot0 + s * p.rows].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float m0 = M == -INFINITY ? 0.0f : M;
@@ -829,7 +921,7 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.0f;
 #pragma unroll 4
-  for (int64_t s = 0; s < spans; ++s) {
+  for (int s = 0; s < spans; ++s) {
     const float2 ml = p.part_ml[slot0 + s * p.rows];
     const float wt = ex2(ml.x - m0);
     L = __fmaf_rn(wt, ml.y, L);

@@ -163,7 +163,8 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16 inputs, fp32 accumulation.
+// D[tmem] (+)= A[smem] * B[smem]^T, bf16 inputs (or f16 ones, as the
+// instruction descriptor says), fp32 accumulation.
 __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -395,6 +396,12 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, int a_mn_ma
          | ((uint32_t)b_mn_major << 16)    // B major-ness
          | ((uint32_t)(N >> 3) << 17)      // N / 8
          | ((uint32_t)(M >> 4) << 24);     // M / 16
+}
+
+// Instruction descriptor for kind::f16 with f16 A/B and fp32 D.
+__host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, int a_mn_major,
+                                                      int b_mn_major) {
+  return make_idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
 }  // namespace dsmla
