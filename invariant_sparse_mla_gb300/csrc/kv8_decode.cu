@@ -13,18 +13,19 @@
 //   |q| and off by 2^-23 of that below.
 //
 // O^T = V^T P^T runs in f16: E4M3 to f16 is exact and one instruction for two
-// values, and a weight p b, kept as 2^7 p b <= 2^15 in f16, has 11 significant
-// bits down to 2^-21 and at least 8 down to 2^-24 of the running maximum.
+// values, and a weight p b, kept as 2^3 p b <= 2^15 in f16, has 11 significant
+// bits down to p b = 2^-17 and at least 8 down to 2^-20.
 // (Weights as three E4M3 pieces, with V as it lies, were built first: the
 // pieces cost more instructions per row than converting V costs per tile, and
 // allow a factor of 4 between a weight and the maximum instead of 2^8, so that
 // most tiles rescaled: 32 x 5 tokens of 64/8 heads took 1462 us.)
 //
-// The running maximum m of a row covers s_i + log2 b_i (p b <= 2^8 whatever
-// the page scales are) and moves only when a tile passes it by more than 2^8;
-// l = sum 2^(s_i - m) is kept in fp32 of the unrounded weights.
+// The reference m of a row is the largest s_i + log2 b_i of its first tile and
+// moves only when a tile passes it by more than 2^12 (so p b <= 2^12 whatever
+// the page scales are); l = sum 2^(s_i - m) is kept in fp32 of the unrounded
+// weights.
 //
-// Work split. A row's context is cut into spans of 256 to 4096 positions, the
+// Work split. A row's context is cut into spans of 512 to 4096 positions, the
 // power of two that gives at most 32 spans up to 131072 positions: a
 // function of the request's length alone, so a request's bits do not depend
 // on the batch. A persistent grid (two CTAs per SM) takes the (request, kv
@@ -61,10 +62,10 @@ constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
 constexpr int kThreads = kSoftmax + 64;
 constexpr int kMaxRows = 40;               // query rows of one row group
 constexpr int kMetaSlots = 8;
-constexpr float kTau = 8.0f;               // log2: p b may reach 2^kTau
-constexpr float kPScale = 128.0f;          // 2^(15 - kTau): stored weights stay <= 2^15
+constexpr float kTau = 12.0f;              // log2: p b may reach 2^kTau
+constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay <= 2^15
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-constexpr int kMinSpan = 256, kMaxSpan = 4096;
+constexpr int kMinSpan = 512, kMaxSpan = 4096;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -98,8 +99,10 @@ struct Layout {
   static constexpr int kNP = (R8 + 15) / 16 * 16;           // columns of P and O
   static constexpr int kUnit = kTile * DIM;                 // K or V codes of one tile
   static constexpr int kQBytes = (2 * R8 * DIM + 1023) / 1024 * 1024;
-  static constexpr int kPBlock = kNP * 128;                 // P of 64 positions
-  static constexpr int kRest = 2 * kUnit + kQBytes + 2 * kPBlock + 2048 + 1024;
+  // P^T [position][row] in f16: rows of 32, 64 or 128 bytes, swizzled to match.
+  static constexpr int kPRow = kNP <= 16 ? 32 : (kNP <= 32 ? 64 : 128);
+  static constexpr int kPBytes = kTile * kPRow;
+  static constexpr int kRest = 2 * kUnit + kQBytes + kPBytes + 2048 + 1024;
   static constexpr int kFit = (113 * 1024 - kRest) / kUnit;
   static constexpr int kUnits = kFit > 8 ? 8 : kFit;
   static constexpr int kNK = (kUnits + 1) / 2, kNV = kUnits / 2;   // stages of the two rings
@@ -108,7 +111,7 @@ struct Layout {
   static constexpr int kV = kK + kNK * kUnit;
   static constexpr int kV16 = kV + kNV * kUnit;             // V of the present tile in f16
   static constexpr int kP = kV16 + 2 * kUnit;
-  static constexpr int kQ = kP + 2 * kPBlock;
+  static constexpr int kQ = kP + kPBytes;
   static constexpr int kBars = kQ + kQBytes;
   static constexpr int kMeta = kBars + 32 * 8;              // kMetaSlots x 2 float4
   static constexpr int kF = kMeta + kMetaSlots * 32;        // per row: factor, reference, alpha
@@ -136,8 +139,9 @@ enum Bar {
   kPFull = 18,      // P and the f16 V written
   kPvDone = 19,     // PV done (P and f16 V free, O holds the tile)
   kQReady = 20,     // Q pieces written
-  kDrain = 21,
-  kNumBars = 22
+  kVote = 21,       // every softmax warp has said whether a reference moves
+  kDrain = 22,
+  kNumBars = 23
 };
 
 struct Params {
@@ -158,17 +162,22 @@ struct Walk {
   int64_t at, end;       // tile numbers: start of the present item, end of the CTA's share
   int r;                 // request
   int len;               // its positions (at most 2^30)
+  int raw;               // lens[r] as it is
   int tiles, span_tiles, spans;
   int hg, s;             // kv head * row_groups + row group; span
 };
 
-__device__ __forceinline__ int row_len(const Params& p, int64_t r) {
-  const int len = p.c.lens[r], most = (int)(p.c.bt_stride * kPage);
+__device__ __forceinline__ int clamp_len(const Params& p, int len) {
+  const int most = (int)(p.c.bt_stride * kPage);
   return len < 0 ? 0 : (len > most ? most : len);
+}
+__device__ __forceinline__ int row_len(const Params& p, int64_t r) {
+  return clamp_len(p, p.c.lens[r]);
 }
 
 __device__ __forceinline__ void walk_load(const Params& p, Walk& w) {
-  w.len = row_len(p, w.r);
+  w.raw = p.c.lens[w.r];
+  w.len = clamp_len(p, w.raw);
   w.tiles = (int)((w.len + kTile - 1) / kTile);
   const int span = span_of(w.len);
   w.span_tiles = span / kTile;
@@ -252,6 +261,22 @@ __device__ __forceinline__ float warp_sum4(const float* v, int lane) {
   return c;
 }
 
+// Maxima the same way (a REDUX per row instead is several times slower: 7 us
+// a move of 40 rows, measured).
+__device__ __forceinline__ float warp_max4(const float* v, float add, int lane) {
+  float a[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 16;
+    a[i] = fmaxf(up ? v[2 + i] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[2 + i], 16));
+  }
+  const bool up = lane & 8;
+  float c = fmaxf(up ? a[1] : a[0], __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 8)) + add;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+  return c;
+}
+
 // N (a multiple of 4) TMEM columns of the warp's lanes; tmem_fence(v) comes
 // between the loads and the first use.
 template <int N>
@@ -302,15 +327,6 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
     return make_sw64_desc(addr, 16, 512);
 }
 
-// Order-preserving int of a float (for integer warp maxima).
-__device__ __forceinline__ int float_key(float x) {
-  const int b = __float_as_int(x);
-  return b ^ ((b >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float key_float(int k) {
-  return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
-}
-
 template <int R8, int DIM>
 __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     const __grid_constant__ CUtensorMap map, const Params p) {
@@ -328,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
   int* vis_s = reinterpret_cast<int*>(smem + LY::kVis);
   float* by_s = reinterpret_cast<float*>(smem + LY::kBy);
   int* set_s = reinterpret_cast<int*>(smem + LY::kSet);
+  volatile int* move_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
-  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 4);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 40);
   int64_t* start_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 8);   // request, its first tile
   int64_t* scan_s = reinterpret_cast<int64_t*>(smem + LY::kWarpMax);     // before the loop only
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -338,10 +355,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     for (int i = 0; i < kNumBars; ++i) {
       const bool all = i == kSFree || i == kPFull || i == kQReady ||
                        (i >= kVEmpty && i < kVEmpty + NV);
-      mbar_init(&bars[i], all ? (uint32_t)kSoftmax : 1u);
+      mbar_init(&bars[i], all ? (uint32_t)kSoftmax : (i == kVote ? (uint32_t)kSoftmaxWarps : 1u));
     }
     mbar_fence_init();
-    *abort_s = 0;
+    abort_s[0] = abort_s[1] = 0;
+    move_s[0] = move_s[1] = 0;
     for (int r = 0; r < R8; ++r) set_s[r] = 0;
     start_s[0] = -1;
   }
@@ -414,31 +432,46 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     uint32_t k_issued = 0, v_issued = 0;
     int err_bits = 0;
     const int none = (int)(p.c.num_pages * 2 * p.c.kv_heads * kPage);   // a row past the pool: zeros
-    while (some && !failed) {
-      const int kvh = w.hg / p.row_groups;
-      const int nt = item_tiles(w);
-      const int block0 = w.s * w.span_tiles * 2;
-      const int blocks = (w.len + kPage - 1) / kPage;
-      // Lane l looks up pages l and l + 32 of the span, all at once.
+    // Lane l looks up pages l and l + 32 of a span (and their scales), all at
+    // once; the next item's while this item's tiles are issued, since a lookup
+    // takes two trips to memory and the rings hold less than that.
+    struct Lookup {
       int y[2];
       float ks[2], vs[2];
+    };
+    auto look = [&](const Walk& i) {
+      Lookup k;
+      const int kvh = i.hg / p.row_groups, n = 2 * item_tiles(i);
+      const int block0 = i.s * i.span_tiles * 2;
+      const int blocks = (i.len + kPage - 1) / kPage;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int b = block0 + lane + 32 * i;
-        y[i] = none;
-        ks[i] = vs[i] = 0.0f;
-        if (lane + 32 * i < 2 * nt && b < blocks) {
-          const int64_t page = p.c.block_table[(int64_t)w.r * p.c.bt_stride + b];
+      for (int e = 0; e < 2; ++e) {
+        const int b = block0 + lane + 32 * e;
+        k.y[e] = none;
+        k.ks[e] = k.vs[e] = 0.0f;
+        if (lane + 32 * e < n && b < blocks) {
+          const int64_t page = p.c.block_table[(int64_t)i.r * p.c.bt_stride + b];
           if (page >= 0 && page < p.c.num_pages) {
             const int64_t part = page * 2 * p.c.kv_heads + kvh;
-            y[i] = (int)(part * kPage);
-            ks[i] = p.c.scales[part];
-            vs[i] = p.c.scales[part + p.c.kv_heads];
+            k.y[e] = (int)(part * kPage);
+            k.ks[e] = p.c.scales[part];
+            k.vs[e] = p.c.scales[part + p.c.kv_heads];
           } else {
             err_bits |= kErrPage;
           }
         }
       }
+      return k;
+    };
+    Lookup next;
+    if (some) next = look(w);
+    while (some && !failed) {
+      const int nt = item_tiles(w);
+      const Lookup now = next;
+      const int* y = now.y;
+      const float *ks = now.ks, *vs = now.vs;
+      some = walk_next(p, w);
+      if (some) next = look(w);
       for (int t = 0; t < nt; ++t, ++g) {
         int yy[2];
         float kk[2], vv[2];
@@ -456,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
             const int n = side ? NV : NK;
             const int st = (int)(g % n);
             uint64_t* full = &bars[(side ? kVFull : kKFull) + st];
-            if (g >= n && !mbar_wait(&bars[(side ? kVEmpty : kKEmpty) + st],
+            if (g >= n && !mbar_wait_long(&bars[(side ? kVEmpty : kKEmpty) + st],
                                      (uint32_t)((g / n - 1) & 1))) {
               ok = false;
               break;
@@ -485,14 +518,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
           break;
         }
       }
-      if (!failed) some = walk_next(p, w);
     }
     if (lane == 0) {
       // Every copy has landed before the CTA can exit.
       for (uint32_t i = k_issued > NK ? k_issued - NK : 0; i < k_issued; ++i)
-        if (!mbar_wait(&bars[kKFull + i % NK], (uint32_t)((i / NK) & 1))) failed = true;
+        if (!mbar_wait_long(&bars[kKFull + i % NK], (uint32_t)((i / NK) & 1))) failed = true;
       for (uint32_t i = v_issued > NV ? v_issued - NV : 0; i < v_issued; ++i)
-        if (!mbar_wait(&bars[kVFull + i % NV], (uint32_t)((i / NV) & 1))) failed = true;
+        if (!mbar_wait_long(&bars[kVFull + i % NV], (uint32_t)((i / NV) & 1))) failed = true;
     }
     if (err_bits && p.c.err != nullptr) atomicOr(p.c.err, err_bits);
     __syncwarp();
@@ -500,39 +532,48 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     // -------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_s = make_idesc_e4m3(kTile, 2 * R8, 0, 0);
-      constexpr uint32_t idesc_o = make_idesc_f16(DIM, NP, 1, 0);
+      constexpr uint32_t idesc_o = make_idesc_f16(DIM, NP, 1, 1);
       const uint64_t q_desc = tile_desc<DIM>(sbase + LY::kQ);
       const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
       // f16 V: 64-dim column blocks of 128 rows x 128 bytes.
       const uint64_t v_desc = make_sw128_desc(sbase + LY::kV16, kTile * 128, 1024);
-      const uint64_t p_desc = make_sw128_desc(sbase + LY::kP, 16, 1024);
+      // P^T: 8 positions x kPRow bytes an atom.
+      const uint64_t p_desc = LY::kPRow == 128 ? make_sw128_desc(sbase + LY::kP, 16, 1024)
+                              : LY::kPRow == 64 ? make_sw64_desc(sbase + LY::kP, 16, 512)
+                                                : make_sw32_desc(sbase + LY::kP, 16, 256);
       uint32_t g = 0;         // tiles whose S was issued
       uint32_t pv = 0;         // tiles whose PV was issued
       bool first_of_pv = true;
       auto issue_pv = [&](bool first) {
         // O^T (+)= V^T P^T of tile pv.
-        if (!mbar_wait(&bars[kPFull], (uint32_t)(pv & 1))) return false;
+        if (!mbar_wait_long(&bars[kPFull], (uint32_t)(pv & 1))) return false;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_bf16_ss(tmem + 2 * R8, v_desc + ((k * 16 * 128) >> 4),
-                      p_desc + (((k >> 2) * LY::kPBlock + (k & 3) * 32) >> 4), idesc_o,
+                      p_desc + ((k * 16 * LY::kPRow) >> 4), idesc_o,
                       (!first || k > 0) ? 1u : 0u);
         mma_commit(&bars[kPvDone]);
         ++pv;
         return true;
       };
-      uint32_t items = 0;
+      uint32_t queries = 0;
+      int64_t last_q = -1;
       while (some && !failed) {
         const int nt = item_tiles(w);
+        const int64_t qid = (int64_t)w.r * hgs + w.hg;
         for (int t = 0; t < nt && !failed; ++t) {
           const int st = (int)(g % NK);
-          // The item's Q pieces (written after the last item's S was read);
+          // New Q pieces (written after the last S of the old ones was read);
           // S is free again once tile g - 1 was read.
-          if (t == 0 && !mbar_wait(&bars[kQReady], (uint32_t)(items & 1))) failed = true;
-          if (!failed && g > 0 && !mbar_wait(&bars[kSFree], (uint32_t)((g - 1) & 1)))
+          if (qid != last_q) {
+            last_q = qid;
+            if (!mbar_wait_long(&bars[kQReady], queries & 1u)) failed = true;
+            ++queries;
+          }
+          if (!failed && g > 0 && !mbar_wait_long(&bars[kSFree], (uint32_t)((g - 1) & 1)))
             failed = true;
-          if (!failed && !mbar_wait(&bars[kKFull + st], (uint32_t)((g / NK) & 1))) failed = true;
+          if (!failed && !mbar_wait_long(&bars[kKFull + st], (uint32_t)((g / NK) & 1))) failed = true;
           if (failed) break;
           tc_fence_after();
           const uint64_t a = k_desc + (uint64_t)((st * LY::kUnit) >> 4);
@@ -551,11 +592,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         if (failed) break;
         if (!issue_pv(first_of_pv)) failed = true;
         first_of_pv = true;
-        ++items;
         if (!failed) some = walk_next(p, w);
       }
       mma_commit(&bars[kDrain]);
-      if (!mbar_wait(&bars[kDrain], 0)) failed = true;
+      if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
     }
     __syncwarp();
   } else {
@@ -565,15 +605,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     const int tok = quad * 32 + lane;      // position of the tile (TMEM lane)
     const int rh = half * RH;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + rh, t_o = tmem + lane_base + 2 * R8 + rh;
+    constexpr int PH = NP / 2;             // P and O columns of a half: rows, then padding
+    const uint32_t t_s = tmem + lane_base + rh, t_o = tmem + lane_base + 2 * R8 + half * PH;
     const int dim0 = DIM == 128 ? tok : quad * 16 + lane;   // this lane's O row
     const bool has_dim = DIM == 128 || lane < 16;
-    // P[row][position] in f16, two blocks of 64 positions; byte of this thread's
-    // position in row 0 of its rows, without the swizzle's row bits.
-    uint8_t* const p_at = smem + LY::kP + (tok >> 6) * LY::kPBlock;
-    const int pc = (tok & 63) >> 3, pb = (tok & 7) * 2;
+    // 16-byte chunk c (eight columns) of this thread's position in P^T.
+    auto p_chunk = [&](int c) {
+      constexpr int W = LY::kPRow;
+      const int x = W == 128 ? (tok & 7) : (W == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1);
+      return reinterpret_cast<uint4*>(smem + LY::kP + tok * W + ((c ^ x) << 4));
+    };
     float l[RH];
     uint32_t g = 0;
+    // A wait that gave up ends the loop at the next vote, for every warp alike:
+    // it is noted under that vote's tile, before this warp votes there.
+    auto give_up = [&] { abort_s[(g + 1) & 1] = (int)(g + 2); };
     int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
     while (some && !failed) {
       const int nt = item_tiles(w);
@@ -615,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
             a = fmaxf(a, fabsf(x[i][e]));
             nan |= x[i][e] != x[i][e];
           }
-          a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
           nan = __any_sync(0xffffffffu, nan) || a == INFINITY;
           // a 2^k in [128, 256); 2^k stays a normal float.
           int k = a > 0.0f ? 7 - ((int)(__float_as_uint(a) >> 23) - 127) : 0;
@@ -635,10 +682,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
             f_s[r] = nan ? NAN : __uint_as_float((uint32_t)(127 - k) << 23) * p.scale_log2;
         }
         fence_proxy_async_smem();
+        mbar_arrive(&bars[kQReady]);   // (f_s is read behind the barrier below)
       }
       // Row r's token j sees len - next_n + 1 + j positions (clamped).
       if (tid < R8) {
-        const int64_t v = (int64_t)p.c.lens[w.r] - p.next_n + 1 + (row0 + tid) / p.group;
+        const int64_t v = (int64_t)w.raw - p.next_n + 1 + (row0 + tid) / p.group;
         m_s[tid] = 0.0f;
         vis_s[tid] = (int)(v < 0 ? 0 : (v > w.len ? w.len : v));
       }
@@ -646,14 +694,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
       for (int i = 0; i < RH; ++i) l[i] = 0.0f;
       uint32_t nan_rows = 0;    // rows that see a NaN value in this lane's dim
       named_bar_sync(1, kSoftmax);   // f_s, m_s, vis_s
-      mbar_arrive(&bars[kQReady]);
       const int min_vis = vis_s[0];
       bool unset = true;        // some row has no reference yet
 
       for (int t = 0; t < nt; ++t, ++g) {
         const int pos0 = (w.s * w.span_tiles + t) * kTile;
         const int pos = pos0 + tok;
-        if (!mbar_wait(&bars[kSFull], (uint32_t)(g & 1))) *abort_s = 1;
+        if (!mbar_wait_long(&bars[kSFull], (uint32_t)(g & 1))) abort_s[g & 1] = (int)(g + 1);
         tc_fence_after();
         const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tok >> 6)];   // ks, vs, log2 vs, valid
         float s[RH];
@@ -692,114 +739,44 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         const float slack = kTau - mt.z;
 #pragma unroll
         for (int i = 0; i < RH; ++i) above |= s[i] > slack;
-        const bool move = named_bar_or(2, kSoftmax, above);
-        if (*abort_s) {
-          failed = true;
-          break;
-        }
-        if (move) {
-          // Rows without a reference take the largest s + log2 b of the tile;
-          // rows that pass theirs by more than 2^kTau move it there, and
-          // their sums and outputs so far are rescaled. Each row by its own
-          // values alone.
-#pragma unroll
-          for (int i = 0; i < RH; ++i) {
-            const int k = __reduce_max_sync(0xffffffffu, float_key(s[i] + mt.z));
-            if (lane == (i & 31)) wmax_s[quad * R8 + rh + i] = key_float(k);
-          }
-          named_bar_sync(1, kSoftmax);
-          bool open = false;
-          if (tid < R8) {
-            float top = wmax_s[tid];
-#pragma unroll
-            for (int v = 1; v < 4; ++v) top = fmaxf(top, wmax_s[v * R8 + tid]);
-            const int vis = vis_s[tid];
-            const bool first = set_s[tid] == 0;
-            float by = 0.0f, al = 1.0f;
-            if (first ? top > -INFINITY : top > kTau) {
-              by = top;
-              al = first ? 0.0f : ex2(-top);
-              m_s[tid] += top;
-              set_s[tid] = 1;
-            } else if (first) {
-              open = vis > pos0 + kTile;   // it may see something later
-            }
-            alpha_s[tid] = al;
-            by_s[tid] = by;
-          }
-          unset = named_bar_or(1, kSoftmax, open);
-#pragma unroll
-          for (int i = 0; i < RH; ++i) {
-            l[i] *= alpha_s[rh + i];
-            s[i] -= by_s[rh + i];
-          }
-          if (t > 0) {
-            if (!mbar_wait(&bars[kPvDone], (uint32_t)((g - 1) & 1))) *abort_s = 1;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < RH; i += 4) {
-              const float4 al = *reinterpret_cast<const float4*>(alpha_s + rh + i);
-              if (al.x != 1.0f || al.y != 1.0f || al.z != 1.0f || al.w != 1.0f) {
-                float o[4];
-                tmem_ld<4>(t_o + i, o);
-                tmem_fence<4>(o);
-                o[0] *= al.x;
-                o[1] *= al.y;
-                o[2] *= al.z;
-                o[3] *= al.w;
-                tmem_st4(t_o + i, o);
-              }
-            }
-            tmem_wait_st();
-          }
-        }
-        // The weights, their sum, and P (free once PV of the last tile is done).
-        const float vscale = here ? mt.y * kPScale : 0.0f;
-#pragma unroll
-        for (int i = 0; i < RH; ++i) {
-          s[i] = ex2(s[i]);
-          l[i] += s[i];
-        }
-        if (g > 0 && !mbar_wait(&bars[kPvDone], (uint32_t)((g - 1) & 1))) *abort_s = 1;
-#pragma unroll
-        for (int i = 0; i < RH; i += 2) {
-          const __half2 h = __floats2half2_rn(s[i] * vscale, s[i + 1] * vscale);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = rh + i + e;
-            *reinterpret_cast<__half*>(p_at + r * 128 + ((pc ^ (r & 7)) << 4) + pb) =
-                e ? __high2half(h) : __low2half(h);
-          }
-        }
+        // Does some row's reference move? Each warp says so and goes on to V; the
+        // answer is there when it is needed. (Slot g & 1 holds the last tile,
+        // plus 1, that moved one; a warp is at most one tile ahead.)
+        if (__any_sync(0xffffffffu, above) && lane == 0) move_s[g & 1] = (int)(g + 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kVote]);
+        // P and the f16 V are free once PV of the last tile is done.
+        if (g > 0 && !mbar_wait_long(&bars[kPvDone], (uint32_t)((g - 1) & 1))) give_up();
         // V to f16: half a position's dims per thread. What lies behind the
         // context is anything, and a weight of 0 times NaN is NaN: it becomes 0.
         {
           const int st = (int)(g % NV);
-          if (!mbar_wait(&bars[kVFull + st], (uint32_t)((g / NV) & 1))) *abort_s = 1;
+          if (!mbar_wait_long(&bars[kVFull + st], (uint32_t)((g / NV) & 1))) give_up();
           const uint8_t* src = smem + LY::kV + st * LY::kUnit;
           uint8_t* dst = smem + LY::kV16 + tok * 128;
           constexpr int NC = DIM / 32;         // 16-code chunks of this thread
-          uint4 v[NC];
           bool nan = false;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            v[c] = *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, (half * NC + c) * 16));
-            if (pos >= w.len) v[c] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          if (edge) {
+          for (int c0 = 0; c0 < NC; c0 += 2) {
+            uint4 v[2];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) nan |= has_nan_code(v[c]);
-          }
+            for (int c = 0; c < 2; ++c) {
+              v[c] = *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, (half * NC + c0 + c) * 16));
+              if (pos >= w.len) v[c] = make_uint4(0u, 0u, 0u, 0u);
+              if (edge) nan |= has_nan_code(v[c]);
+            }
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const uint2 a = codes_to_f16(v[c].x), b = codes_to_f16(v[c].y),
-                        d = codes_to_f16(v[c].z), e = codes_to_f16(v[c].w);
-            const int cc = half * NC + c;
-            uint8_t* at = dst + (cc >> 2) * (kTile * 128);
-            const int ch = (cc & 3) * 2;
-            *reinterpret_cast<uint4*>(at + ((ch ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (tok & 7)) << 4)) =
-                make_uint4(d.x, d.y, e.x, e.y);
+            for (int c = 0; c < 2; ++c) {
+              const uint2 a = codes_to_f16(v[c].x), b = codes_to_f16(v[c].y),
+                          d = codes_to_f16(v[c].z), e = codes_to_f16(v[c].w);
+              const int cc = half * NC + c0 + c;
+              uint8_t* at = dst + (cc >> 2) * (kTile * 128);
+              const int ch = (cc & 3) * 2;
+              *reinterpret_cast<uint4*>(at + ((ch ^ (tok & 7)) << 4)) =
+                  make_uint4(a.x, a.y, b.x, b.y);
+              *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (tok & 7)) << 4)) =
+                  make_uint4(d.x, d.y, e.x, e.y);
+            }
           }
           mbar_arrive(&bars[kVEmpty + st]);
           // Where the rows of the group see different lengths, a NaN value that
@@ -823,11 +800,100 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
             }
           }
         }
+        if (!mbar_wait_long(&bars[kVote], g & 1u)) give_up();
+        if (abort_s[g & 1] == (int)(g + 1)) {
+          failed = true;
+          break;
+        }
+        if (move_s[g & 1] == (int)(g + 1)) {
+          // Rows without a reference take the largest s + log2 b of the tile;
+          // rows that pass theirs by more than 2^kTau move it there, and
+          // their sums and outputs so far are rescaled. Each row by its own
+          // values alone.
+#pragma unroll
+          for (int i = 0; i < RH; i += 4) {
+            // (A warp's 32 positions lie in one page: one log2 b.)
+            const float top = warp_max4(s + i, mt.z, lane);
+            const int r = ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
+            if ((lane & 7) == 0) wmax_s[quad * R8 + rh + i + r] = top;
+          }
+          named_bar_sync(1, kSoftmax);
+          bool open = false;
+          if (tid < R8) {
+            float top = wmax_s[tid];
+#pragma unroll
+            for (int v = 1; v < 4; ++v) top = fmaxf(top, wmax_s[v * R8 + tid]);
+            const int vis = vis_s[tid];
+            const bool first = set_s[tid] == 0;
+            float by = 0.0f, al = 1.0f;
+            if (first ? top > -INFINITY : top > kTau) {
+              by = top;
+              al = first ? 0.0f : ex2(-top);
+              m_s[tid] += top;
+              set_s[tid] = 1;
+            } else if (first) {
+              open = vis > pos0 + kTile;   // it may see something later
+            }
+            alpha_s[tid] = al;
+            by_s[tid] = by;
+          }
+          unset = named_bar_or(1, kSoftmax, open);
+#pragma unroll
+          for (int i = 0; i < RH; i += 4) {
+            const float4 al = *reinterpret_cast<const float4*>(alpha_s + rh + i);
+            const float4 by = *reinterpret_cast<const float4*>(by_s + rh + i);
+            l[i] *= al.x;
+            l[i + 1] *= al.y;
+            l[i + 2] *= al.z;
+            l[i + 3] *= al.w;
+            s[i] -= by.x;
+            s[i + 1] -= by.y;
+            s[i + 2] -= by.z;
+            s[i + 3] -= by.w;
+          }
+          if (t > 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < RH; i += 4) {
+              const float4 al = *reinterpret_cast<const float4*>(alpha_s + rh + i);
+              if (al.x != 1.0f || al.y != 1.0f || al.z != 1.0f || al.w != 1.0f) {
+                float o[4];
+                tmem_ld<4>(t_o + i, o);
+                tmem_fence<4>(o);
+                o[0] *= al.x;
+                o[1] *= al.y;
+                o[2] *= al.z;
+                o[3] *= al.w;
+                tmem_st4(t_o + i, o);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // The weights, their sum, and P.
+        const float vscale = here ? mt.y * kPScale : 0.0f;
+#pragma unroll
+        for (int i = 0; i < RH; ++i) {
+          s[i] = ex2(s[i]);
+          l[i] += s[i];
+        }
+#pragma unroll
+        for (int c = 0; c < (RH + 7) / 8; ++c) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 8 * c + 2 * e;
+            const __half2 h = i < RH ? __floats2half2_rn(s[i < RH ? i : 0] * vscale,
+                                                         s[i < RH ? i + 1 : 0] * vscale)
+                                     : __floats2half2_rn(0.0f, 0.0f);
+            b[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *p_chunk(half * (PH / 8) + c) = make_uint4(b[0], b[1], b[2], b[3]);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bars[kPFull]);
       }
-      if (failed) break;
 
       // ------------------------------------------------ end of the item
 #pragma unroll
@@ -836,16 +902,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         const int r = ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
         if ((lane & 7) == 0) wmax_s[quad * R8 + rh + i + r] = v;
       }
-      if (!mbar_wait(&bars[kPvDone], (uint32_t)((g - 1) & 1))) *abort_s = 1;
+      if (!mbar_wait_long(&bars[kPvDone], (uint32_t)((g - 1) & 1))) abort_s[g & 1] = (int)(g + 1);
       tc_fence_after();
       float o[RH];
       tmem_ld<RH>(t_o, o);
       tmem_fence<RH>(o);
       named_bar_sync(1, kSoftmax);
-      if (*abort_s) {
-        failed = true;
-        break;
-      }
       if (nan_rows != 0) {
 #pragma unroll
         for (int i = 0; i < RH; ++i)
@@ -881,6 +943,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
       named_bar_sync(1, kSoftmax);   // m_s and wmax_s are read before the next item writes them
       some = walk_next(p, w);
     }
+    failed |= (abort_s[0] | abort_s[1]) != 0;
   }
   if (failed && p.c.err != nullptr) atomicOr(p.c.err, kErrTimeout);
   tc_fence_before();

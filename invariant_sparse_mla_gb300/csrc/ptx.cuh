@@ -71,6 +71,26 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The same for waits of a tile's length and more: the thread is suspended up
+// to about 20 us a try (woken by the phase's completion), so that a waiting
+// warp leaves the issue slots to the others.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity,
+                                               uint64_t limit_cycles = 1ull << 32) {
+  const uint64_t t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if ((uint64_t)(clock64() - t0) > limit_cycles) return false;
+  }
+}
+
 // Arrives once on `bar` and adds `tx` bytes to the transfer count its
 // current phase waits for (the bytes asynchronous copies will deliver).
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t tx) {
@@ -376,6 +396,13 @@ __device__ __forceinline__ uint64_t make_sw64_desc(uint32_t smem_addr, uint32_t 
   uint64_t d = make_sw128_desc(smem_addr, lbo_bytes, sbo_bytes);
   d &= ~((uint64_t)7 << 61);
   return d | ((uint64_t)4 << 61);
+}
+
+// And with a 32-byte swizzle (layout type 6): rows of 32 bytes, atoms of 8
+// rows = 256 bytes.
+__device__ __forceinline__ uint64_t make_sw32_desc(uint32_t smem_addr, uint32_t lbo_bytes,
+                                                   uint32_t sbo_bytes) {
+  return make_sw128_desc(smem_addr, lbo_bytes, sbo_bytes) | ((uint64_t)4 << 61);
 }
 
 // Instruction descriptor for kind::f8f6f4 with E4M3 A/B (format 0) and fp32 D.
