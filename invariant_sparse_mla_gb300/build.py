@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "libds_sparse_mla.so"
 SOURCES = ["api.cu", "topk.cu", "attention.cu", "cache_write.cu", "noalloc.cu", "indexer.cu",
-           "kv8_api.cu", "kv8_append.cu", "kv8_attention.cu", "kv8_decode.cu", "pages.cu"]
+           "kv8_api.cu", "kv8_append.cu", "kv8_decode.cu", "kv8_prefill.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -57,6 +57,9 @@ size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int k
 size_t kv8_prefill_workspace_bytes(int64_t tokens, int64_t requests, int heads, int kv_heads,
                                    int dim);
 
+// CTAs of a prefill call per kv head.
+int64_t kv8_prefill_units(int64_t tokens, int64_t requests, int group);
+
 // ---- pages
 struct PageState {
   int32_t* refs;

@@ -40,16 +40,12 @@
 // the last one is finished. The bound is HBM: 2 * dim bytes a position.
 
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
 
-#include "kv8.h"
-#include "ptx.cuh"
+#include "kv8_common.cuh"
 
 namespace dsmla {
 
@@ -66,8 +62,6 @@ constexpr float kTau = 12.0f;              // log2: p b may reach 2^kTau
 constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay <= 2^15
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMinSpan = 512, kMaxSpan = 4096;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 __host__ __device__ inline int span_of(int64_t len) {
   int s = kMinSpan;
@@ -219,30 +213,12 @@ __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
   return walk_settle(p, w);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t b) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)b, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
-// Four E4M3 codes as two f16 pairs (exact).
-__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
-  uint2 r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "mov.b32 {lo, hi}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(r.x), "=r"(r.y)
-      : "r"(w));
-  return r;
 }
 
 // Sums over the warp of four values a lane: lane l returns the sum of value
@@ -275,48 +251,6 @@ __device__ __forceinline__ float warp_max4(const float* v, float add, int lane) 
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
   return c;
-}
-
-// N (a multiple of 4) TMEM columns of the warp's lanes; tmem_fence(v) comes
-// between the loads and the first use.
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
-#pragma unroll
-  for (int c = 0; c < N; c += 4)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3])
-                 : "r"(taddr + c)
-                 : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_fence(float* v) {
-  tmem_wait_ld();
-  // Uses of v depend on these (volatile statements keep their order), so none
-  // is scheduled before the wait.
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i])::"memory");
-}
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
-               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
-               : "memory");
-}
-
-__device__ __forceinline__ bool has_nan_code(uint4 v) {
-  const uint32_t k = 0x7F7F7F7Fu;
-  return (__vcmpeq4(v.x & k, k) | __vcmpeq4(v.y & k, k) | __vcmpeq4(v.z & k, k) |
-          __vcmpeq4(v.w & k, k)) != 0u;
-}
-
-// Byte offset of (row, byte) in a K-major tile of DIM-byte rows in the swizzle
-// the copies use (128 bytes for dim 128, 64 for dim 64).
-template <int DIM>
-__device__ __forceinline__ uint32_t swz(int row, int byte) {
-  const int c = byte >> 4;
-  if constexpr (DIM == 128)
-    return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4) + (byte & 15));
-  else
-    return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4) + (byte & 15));
 }
 
 template <int DIM>
