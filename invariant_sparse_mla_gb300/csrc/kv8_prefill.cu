@@ -44,9 +44,9 @@ constexpr int kRows = 256;               // query rows per CTA
 constexpr int kThreads = 512;
 constexpr int kLoaderWarp = 8, kMmaWarp = 12;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-// Registers: 512 threads launch with 128 each; 256 * 192 + 128 * 104 +
-// 128 * 24 = 65536 = 512 * 128.
-constexpr int kRegsSoftmax = 192, kRegsLoader = 104, kRegsMma = 24;
+// Registers: 512 threads launch with 128 each; 256 * 176 + 128 * 112 +
+// 128 * 48 = 65536 = 512 * 128.
+constexpr int kRegsSoftmax = 176, kRegsLoader = 112, kRegsMma = 48;
 
 template <int DIM>
 struct Layout {
@@ -482,62 +482,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     if (err_bits && lt == 0 && p.c.err != nullptr) atomicOr(p.c.err, err_bits);
   } else {
     regs_dec<kRegsMma>();
-    if (warp == kMmaWarp && lane == 0 && nt > 0) {
+    if (warp == kMmaWarp && nt > 0) {
       // -------------------------------------------------------- MMA issuer
+      // (the whole warp; one lane issues)
       constexpr uint32_t idesc_s = make_idesc_f16(128, kTile, 0, 0);
       constexpr uint32_t idesc_o = make_idesc_f16(128, DIM, 0, 1);
       const uint64_t q_desc = make_sw128_desc(sbase + LY::kQ, 16, 1024);
       const uint64_t k_desc = make_sw128_desc(sbase + LY::kK, 16, 1024);
       const uint64_t v_desc = make_sw128_desc(sbase + LY::kV, LY::kBlock, 1024);
-      auto issue_s = [&](int m, int st) {
+      const bool leader = elect_one();
+      auto issue_s = [&](int m, uint64_t kd, uint64_t* k_empty) {
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < DIM / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * LY::kBlock + (k & 3) * 32);
-          mma_bf16_ss(tmem + LY::kS + m * kTile, q_desc + ((m * LY::kTileBytes + off) >> 4),
-                      k_desc + ((st * LY::kTileBytes + off) >> 4), idesc_s, k > 0 ? 1u : 0u);
-        }
-        mma_commit(&bars[kSFull + m]);
-      };
-      failed = !mbar_wait_long(&bars[kQFull], 0) || !mbar_wait_long(&bars[kKFull], 0);
-      if (!failed) {
-        tc_fence_after();
-        for (int m = 0; m < mts; ++m) issue_s(m, 0);
-        mma_commit(&bars[kKEmpty]);
-      }
-      for (int j = 0; j < nt && !failed; ++j) {
-        const int st = j & 1, sn = (j + 1) & 1;
-        if (!mbar_wait_long(&bars[kVFull + st], (j >> 1) & 1)) {
-          failed = true;
-          break;
-        }
-#pragma unroll 1
-        for (int m = 0; m < mts; ++m) {
-          if (!mbar_wait_long(&bars[kPFull + m], j & 1)) {
-            failed = true;
-            break;
+          for (int k = 0; k < DIM / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * LY::kBlock + (k & 3) * 32);
+            mma_bf16_ss(tmem + LY::kS + m * kTile, q_desc + ((m * LY::kTileBytes + off) >> 4),
+                        kd + (off >> 4), idesc_s, k > 0 ? 1u : 0u);
           }
-          tc_fence_after();
+          mma_commit(&bars[kSFull + m]);
+          if (m == mts - 1) mma_commit(k_empty);
+        }
+        __syncwarp();
+      };
+      auto issue_o = [&](int m, uint64_t vd, uint64_t* v_empty, bool first) {
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kS + m * kTile + k * 8,
-                       v_desc + ((st * LY::kTileBytes + k * 16 * 128) >> 4), idesc_o,
-                       (j > 0 || k > 0) ? 1u : 0u);
+                       vd + ((k * 16 * 128) >> 4), idesc_o, k > 0 ? 1u : (first ? 0u : 1u));
           mma_commit(&bars[kPvDone + m]);
-          if (m == mts - 1) mma_commit(&bars[kVEmpty + st]);
+          if (m == mts - 1) mma_commit(v_empty);
+        }
+        __syncwarp();
+      };
+      failed = !mbar_wait_long(&bars[kQFull], 0) || !mbar_wait_long(&bars[kKFull], 0);
+      failed = __any_sync(0xffffffffu, failed);
+      if (!failed) {
+        tc_fence_after();
+        issue_s(0, k_desc, &bars[kKEmpty]);
+        if (mts == 2) issue_s(1, k_desc, &bars[kKEmpty]);
+      }
+      for (int j = 0; j < nt && !failed; ++j) {
+        const int st = j & 1, sn = st ^ 1;
+        const uint64_t vd = v_desc + (uint64_t)((st * LY::kTileBytes) >> 4);
+        const uint64_t kd = k_desc + (uint64_t)((sn * LY::kTileBytes) >> 4);
+        bool ok = mbar_wait_long(&bars[kVFull + st], (j >> 1) & 1);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m >= mts) break;
+          ok = ok && mbar_wait_long(&bars[kPFull + m], j & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          issue_o(m, vd, &bars[kVEmpty + st], j == 0);
           if (j + 1 < nt) {
             // The next S overwrites this P: only once PV has ended.
-            if ((m == 0 && !mbar_wait_long(&bars[kKFull + sn], ((j + 1) >> 1) & 1)) ||
-                !mbar_wait_long(&bars[kPvDone + m], j & 1)) {
-              failed = true;
-              break;
-            }
+            if (m == 0) ok = mbar_wait_long(&bars[kKFull + sn], ((j + 1) >> 1) & 1);
+            ok = ok && mbar_wait_long(&bars[kPvDone + m], j & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            issue_s(m, sn);
-            if (m == mts - 1) mma_commit(&bars[kKEmpty + sn]);
+            issue_s(m, kd, &bars[kKEmpty + sn]);
           }
         }
+        failed = !__all_sync(0xffffffffu, ok);
       }
-      mma_commit(&bars[kDrain]);
+      if (leader) mma_commit(&bars[kDrain]);
+      __syncwarp();
       if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
     }
     __syncwarp();
