@@ -464,52 +464,59 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc_e4m3(kTile, 2 * R8, 0, 0);
-      constexpr uint32_t idesc_o = make_idesc_f16(DIM, NP, 1, 1);
-      const uint64_t q_desc = tile_desc<DIM>(sbase + LY::kQ);
-      const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
-      // f16 V: 64-dim column blocks of 128 rows x 128 bytes.
-      const uint64_t v_desc = make_sw128_desc(sbase + LY::kV16, kTile * 128, 1024);
-      // P^T: 8 positions x kPRow bytes an atom.
-      const uint64_t p_desc = LY::kPRow == 128 ? make_sw128_desc(sbase + LY::kP, 16, 1024)
-                              : LY::kPRow == 64 ? make_sw64_desc(sbase + LY::kP, 16, 512)
-                                                : make_sw32_desc(sbase + LY::kP, 16, 256);
-      uint32_t g = 0;         // tiles whose S was issued
-      uint32_t pv = 0;         // tiles whose PV was issued
-      bool first_of_pv = true;
-      auto issue_pv = [&](bool first) {
-        // O^T (+)= V^T P^T of tile pv.
-        if (!mbar_wait_long(&bars[kPFull], (uint32_t)(pv & 1))) return false;
-        tc_fence_after();
+    // (the whole warp; one lane issues)
+    constexpr uint32_t idesc_s = make_idesc_e4m3(kTile, 2 * R8, 0, 0);
+    constexpr uint32_t idesc_o = make_idesc_f16(DIM, NP, 1, 1);
+    const uint64_t q_desc = tile_desc<DIM>(sbase + LY::kQ);
+    const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
+    // f16 V: 64-dim column blocks of 128 rows x 128 bytes.
+    const uint64_t v_desc = make_sw128_desc(sbase + LY::kV16, kTile * 128, 1024);
+    // P^T: 8 positions x kPRow bytes an atom.
+    const uint64_t p_desc = LY::kPRow == 128 ? make_sw128_desc(sbase + LY::kP, 16, 1024)
+                            : LY::kPRow == 64 ? make_sw64_desc(sbase + LY::kP, 16, 512)
+                                              : make_sw32_desc(sbase + LY::kP, 16, 256);
+    const bool leader = elect_one();
+    uint32_t g = 0;         // tiles whose S was issued
+    uint32_t pv = 0;        // tiles whose PV was issued
+    uint32_t queries = 0;
+    int64_t last_q = -1;
+    auto issue_pv = [&](bool first) {
+      // O^T (+)= V^T P^T of tile pv.
+      if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kPFull], pv & 1u))) return false;
+      tc_fence_after();
+      if (leader) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_bf16_ss(tmem + 2 * R8, v_desc + ((k * 16 * 128) >> 4),
                       p_desc + ((k * 16 * LY::kPRow) >> 4), idesc_o,
-                      (!first || k > 0) ? 1u : 0u);
+                      k > 0 ? 1u : (first ? 0u : 1u));
         mma_commit(&bars[kPvDone]);
-        ++pv;
-        return true;
-      };
-      uint32_t queries = 0;
-      int64_t last_q = -1;
-      while (some && !failed) {
-        const int nt = item_tiles(w);
-        const int64_t qid = (int64_t)w.r * hgs + w.hg;
-        for (int t = 0; t < nt && !failed; ++t) {
-          const int st = (int)(g % NK);
-          // New Q pieces (written after the last S of the old ones was read);
-          // S is free again once tile g - 1 was read.
-          if (qid != last_q) {
-            last_q = qid;
-            if (!mbar_wait_long(&bars[kQReady], queries & 1u)) failed = true;
-            ++queries;
-          }
-          if (!failed && g > 0 && !mbar_wait_long(&bars[kSFree], (uint32_t)((g - 1) & 1)))
-            failed = true;
-          if (!failed && !mbar_wait_long(&bars[kKFull + st], (uint32_t)((g / NK) & 1))) failed = true;
-          if (failed) break;
-          tc_fence_after();
+      }
+      __syncwarp();
+      ++pv;
+      return true;
+    };
+    while (some && !failed) {
+      const int nt = item_tiles(w);
+      const int64_t qid = (int64_t)w.r * hgs + w.hg;
+      for (int t = 0; t < nt && !failed; ++t) {
+        const int st = (int)(g % NK);
+        // New Q pieces (written after the last S of the old ones was read); S is
+        // free again once tile g - 1 was read.
+        bool ok = true;
+        if (qid != last_q) {
+          last_q = qid;
+          ok = mbar_wait_long(&bars[kQReady], queries & 1u);
+          ++queries;
+        }
+        ok = ok && (g == 0 || mbar_wait_long(&bars[kSFree], (g - 1) & 1u)) &&
+             mbar_wait_long(&bars[kKFull + st], (g / NK) & 1u);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        if (leader) {
           const uint64_t a = k_desc + (uint64_t)((st * LY::kUnit) >> 4);
 #pragma unroll
           for (int k = 0; k < DIM / 32; ++k)
@@ -517,20 +524,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
                       k > 0 ? 1u : 0u);
           mma_commit(&bars[kKEmpty + st]);
           mma_commit(&bars[kSFull]);
-          ++g;
-          if (t > 0) {
-            if (!issue_pv(first_of_pv)) failed = true;
-            first_of_pv = false;
-          }
         }
-        if (failed) break;
-        if (!issue_pv(first_of_pv)) failed = true;
-        first_of_pv = true;
-        if (!failed) some = walk_next(p, w);
+        __syncwarp();
+        ++g;
+        if (t > 0 && !issue_pv(t == 1)) failed = true;
       }
-      mma_commit(&bars[kDrain]);
-      if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
+      if (failed) break;
+      if (!issue_pv(nt == 1)) failed = true;
+      if (!failed) some = walk_next(p, w);
     }
+    if (leader) mma_commit(&bars[kDrain]);
+    __syncwarp();
+    if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
