@@ -124,6 +124,9 @@ int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stri
                         "num_kv_heads * head_dim = %lld",
                         fn, (long long)k_stride, (long long)v_stride, (long long)row);
   if (num_tokens == 0 || num_requests == 0) return report_ok();
+  if (num_tokens / dsmla::kPage + 2 * num_requests > (int64_t)INT32_MAX / (2 * num_kv_heads))
+    return report_error(DS_ERR_UNSUPPORTED, "%s: num_tokens=%lld and num_requests=%lld are too "
+                        "large for one launch", fn, (long long)num_tokens, (long long)num_requests);
   st = check_ptrs(fn, {{k, "k", 16},
                        {v, "v", 16},
                        {token_starts, "token_starts", 4},

@@ -9,15 +9,17 @@
 // written token by token keeps its earlier values exactly, but for codes that
 // fall below the normal range.
 //
-// One CTA of 128 threads owns one (page of a request, side, head): nothing
-// is shared between CTAs, so there is no atomic and no second pass. The
-// tokens stay in registers between the maximum and the rounding: thread i
-// holds 16-byte chunks i, i + 128, ... of the page's [64, dim] block. The
-// bound is HBM: 2 bytes read and 1 written per element.
+// One CTA of 128 threads (or one warp, where requests bring few tokens) owns
+// one (page of a request, side, head): nothing is shared between them, so
+// there is no atomic and no second pass. The tokens stay in registers between
+// the maximum and the rounding: thread i holds 16-byte chunks i, i + 128, ...
+// of the page's [64, dim] block. The bound is HBM, 2 bytes read and 1 written
+// per element, and for few tokens the chain of lookups (request, length,
+// page, scale).
 //
 // The grid covers an upper bound of the touched pages: n consecutive
 // positions touch at most floor(n / 64) + 2 pages, so request r's pages are
-// numbered from floor(starts[r] / 64) + 2 r and a binary search finds r.
+// numbered from floor(starts[r] / 64) + 2 r and a search by 32 finds r.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,112 +58,90 @@ struct Params {
   Kv8Cache c;
 };
 
-template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Params p) {
-  constexpr int kRowChunks = DIM / 8;                     // 16-byte chunks of a token's head
-  constexpr int kSteps = kPage * kRowChunks / kThreads;   // chunks per thread
-  __shared__ float warp_max[kThreads / 32];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x;
-  const int head = blockIdx.y >> 1, side = blockIdx.y & 1;
-  const int64_t unit = blockIdx.x;
-  // The last request whose first unit is not past this one.
-  int64_t lo = 0, hi = p.c.requests - 1;
+// One touched page: where its new tokens come from and go to.
+struct Unit {
+  int64_t token0;     // token at slot 0 of the page (may be before the first)
+  int64_t page;
+  int had, upto;      // earlier positions; new ones are slots [had, upto)
+};
+
+// The page that unit number `unit` stands for; false if none. Called by whole
+// warps: the request is found by probing 32 of them at a time.
+__device__ __forceinline__ bool find_unit(const Params& p, int64_t unit, bool report, Unit* u) {
+  const int lane = threadIdx.x & 31;
   auto start_of = [&](int64_t r) {
     const int64_t s = p.starts[r];
     return s < 0 ? 0 : (s > p.tokens ? p.tokens : s);
   };
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if ((start_of(mid) >> 6) + 2 * mid <= unit)
-      lo = mid;
-    else
-      hi = mid - 1;
+  // The last request whose first unit is not past this one lies in
+  // [lo, lo + size).
+  int64_t lo = 0, size = p.c.requests;
+  while (size > 1) {
+    const int64_t step = (size + 31) / 32;
+    const int64_t r = lo + lane * step;
+    const bool at = r < lo + size && (start_of(r) >> 6) + 2 * r <= unit;
+    const int n = __popc(__ballot_sync(0xffffffffu, at));   // monotone: the first n lanes
+    const int64_t end = lo + size;
+    lo += (n > 0 ? n - 1 : 0) * step;
+    size = end - lo < step ? end - lo : step;
   }
-  const int64_t r = lo;
-  const int64_t t0 = start_of(r), n = start_of(r + 1) - t0;
-  if (n <= 0) return;
-  const int64_t len = p.c.lens[r], first = len - n;
-  const int64_t j = unit - ((t0 >> 6) + 2 * r);   // page of this request's touched ones
+  const int64_t t0 = start_of(lo), n = start_of(lo + 1) - t0;
+  if (n <= 0) return false;
+  const int64_t len = p.c.lens[lo], first = len - n;
+  const int64_t j = unit - ((t0 >> 6) + 2 * lo);   // page of this request's touched ones
   if (first < 0) {
-    if (j == 0 && blockIdx.y == 0 && tid == 0 && p.c.err != nullptr)
-      atomicOr(p.c.err, kErrLen);
-    return;
+    if (j == 0 && report && p.c.err != nullptr) atomicOr(p.c.err, kErrLen);
+    return false;
   }
   const int64_t block = (first >> 6) + j;
-  if (j < 0 || (block << 6) >= len) return;
-  int64_t page = -1;
-  if (block < p.c.bt_stride) page = p.c.block_table[r * p.c.bt_stride + block];
-  if (page < 0 || page >= p.c.num_pages) {
-    if (blockIdx.y == 0 && tid == 0 && p.c.err != nullptr) atomicOr(p.c.err, kErrPage);
-    return;
+  if (j < 0 || (block << 6) >= len) return false;
+  u->page = -1;
+  if (block < p.c.bt_stride) u->page = p.c.block_table[lo * p.c.bt_stride + block];
+  if (u->page < 0 || u->page >= p.c.num_pages) {
+    if (report && p.c.err != nullptr) atomicOr(p.c.err, kErrPage);
+    return false;
   }
   const int64_t pos0 = block << 6;
-  const int had = first > pos0 ? (int)(first - pos0) : 0;             // earlier positions
-  const int upto = len - pos0 < kPage ? (int)(len - pos0) : kPage;    // new: [had, upto)
-  const int64_t part = (page * 2 + side) * p.c.kv_heads + head;
-  float* scale_at = p.c.scales + part;
-  const float old = had > 0 ? *scale_at : 0.0f;
+  u->token0 = t0 + (pos0 - first);
+  u->had = first > pos0 ? (int)(first - pos0) : 0;
+  u->upto = len - pos0 < kPage ? (int)(len - pos0) : kPage;
+  return true;
+}
 
-  const __nv_bfloat16* src = side ? p.v : p.k;
-  const int64_t stride = side ? p.v_stride : p.k_stride;
-  uint4 x[kSteps];
+__device__ __forceinline__ float amax8(uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int c = tid + i * kThreads, slot = c / kRowChunks, ch = c % kRowChunks;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= had && slot < upto) {
-      const int64_t t = t0 + (pos0 + slot - first);
-      x[i] = *reinterpret_cast<const uint4*>(src + t * stride + head * DIM + ch * 8);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      a = fmaxf(a, fmaxf(fabsf(__uint_as_float(w[u] << 16)),
-                         fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
-  }
+  for (int u = 0; u < 4; ++u)
+    a = fmaxf(a, fmaxf(fabsf(__uint_as_float(w[u] << 16)),
+                       fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
+  return a;
+}
+
+__device__ __forceinline__ float warp_max(float a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  if ((tid & 31) == 0) warp_max[tid >> 5] = a;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, warp_max[w]);
-  float s = fmaxf(old, need_scale(a));
-  if (!(s > 0.0f)) s = __uint_as_float((uint32_t)(127 - 60) << 23);
+  return a;
+}
 
-  uint8_t* dst = p.c.pages + part * (int64_t)(kPage * DIM);
-  if (had > 0 && s != old) {
-    // Earlier codes at the grown scale.
-    const float f = __fdiv_rn(old, s);
-    for (int c = tid; c < had * DIM / 4; c += kThreads) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(dst) + c;
-      const uint32_t w = *at;
-      uint32_t r2 = 0u;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const __half2_raw h =
-            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w >> (16 * u)) & 0xFFFFu), __NV_E4M3);
-        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        r2 |= e4m3x2(g.x * f, g.y * f) << (16 * u);
-      }
-      *at = r2;
-    }
+__device__ __forceinline__ float new_scale(float old, float a) {
+  const float s = fmaxf(old, need_scale(a));
+  return s > 0.0f ? s : __uint_as_float((uint32_t)(127 - 60) << 23);
+}
+
+// Eight values over the scale. Dividing by a power of two is multiplying by
+// its reciprocal, exactly; a scale that a caller set to something else takes
+// the division.
+struct Quantizer {
+  float s, inv;
+  bool pow2;
+  __device__ __forceinline__ explicit Quantizer(float scale) : s(scale) {
+    const uint32_t b = __float_as_uint(scale);
+    pow2 = (b & 0x7FFFFFu) == 0u && b >= (67u << 23) && b <= (247u << 23);
+    inv = pow2 ? __uint_as_float((254u << 23) - b) : 0.0f;
   }
-  // Dividing by a power of two is multiplying by its reciprocal, exactly; a
-  // scale that a caller set to something else takes the division.
-  const uint32_t sb = __float_as_uint(s);
-  const bool pow2 = (sb & 0x7FFFFFu) == 0u && sb >= (67u << 23) && sb <= (247u << 23);
-  const float inv = pow2 ? __uint_as_float((254u << 23) - sb) : 0.0f;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int c = tid + i * kThreads, slot = c / kRowChunks;
-    if (slot < had || slot >= upto) continue;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+  __device__ __forceinline__ uint2 operator()(uint4 x) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[2] = {0u, 0u};
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -170,9 +150,128 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Params p) {
                               : e4m3x2(__fdiv_rn(f0, s), __fdiv_rn(f1, s));
       o[u >> 1] |= b << (16 * (u & 1));
     }
-    reinterpret_cast<uint2*>(dst)[c] = make_uint2(o[0], o[1]);
+    return make_uint2(o[0], o[1]);
+  }
+};
+
+// Four earlier codes at a grown scale, f = old / new.
+__device__ __forceinline__ uint32_t again(uint32_t w, float f) {
+  uint32_t r = 0u;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w >> (16 * u)) & 0xFFFFu), __NV_E4M3);
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    r |= e4m3x2(g.x * f, g.y * f) << (16 * u);
+  }
+  return r;
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kThreads) kv8_append_page_kernel(const Params p) {
+  constexpr int kRowChunks = DIM / 8;                     // 16-byte chunks of a token's head
+  constexpr int kSteps = kPage * kRowChunks / kThreads;   // chunks per thread
+  __shared__ float warp_top[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int side = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % p.c.kv_heads;
+  const int64_t unit = (blockIdx.x >> 1) / p.c.kv_heads;
+  Unit u;
+  if (!find_unit(p, unit, tid == 0 && side == 0 && head == 0, &u)) return;
+  const int64_t part = (u.page * 2 + side) * p.c.kv_heads + head;
+  float* scale_at = p.c.scales + part;
+  const float old = u.had > 0 ? *scale_at : 0.0f;
+  const int64_t stride = side ? p.v_stride : p.k_stride;
+  const __nv_bfloat16* src = (side ? p.v : p.k) + u.token0 * stride + head * DIM;
+  uint4 x[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int c = tid + i * kThreads, slot = c / kRowChunks, ch = c % kRowChunks;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (slot >= u.had && slot < u.upto)
+      x[i] = __ldcs(reinterpret_cast<const uint4*>(src + slot * stride + ch * 8));
+  }
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) a = fmaxf(a, amax8(x[i]));
+  a = warp_max(a);
+  if ((tid & 31) == 0) warp_top[tid >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, warp_top[w]);
+  const float s = new_scale(old, a);
+  uint8_t* dst = p.c.pages + part * (int64_t)(kPage * DIM);
+  if (u.had > 0 && s != old) {
+    const float f = __fdiv_rn(old, s);
+    for (int c = tid; c < u.had * DIM / 4; c += kThreads) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(dst) + c;
+      *at = again(*at, f);
+    }
+  }
+  const Quantizer quant(s);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int c = tid + i * kThreads, slot = c / kRowChunks;
+    if (slot >= u.had && slot < u.upto) reinterpret_cast<uint2*>(dst)[c] = quant(x[i]);
   }
   if (tid == 0) *scale_at = s;
+}
+
+// The same with one warp per (page, side, head), for calls with few tokens a
+// request: a CTA then finds its page once for eight of them, and there are an
+// eighth of the CTAs.
+template <int DIM>
+__global__ void __launch_bounds__(256) kv8_append_few_kernel(const Params p) {
+  constexpr int kRowChunks = DIM / 8;
+  constexpr int kHeld = 4;            // chunks a lane keeps in registers
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int parts = 2 * p.c.kv_heads, per_unit = (parts + 7) / 8;
+  const int64_t unit = blockIdx.x / per_unit;
+  const int ph = (int)(blockIdx.x % per_unit) * 8 + (threadIdx.x >> 5);   // side, head
+  if (ph >= parts) return;
+  Unit u;
+  if (!find_unit(p, unit, lane == 0 && ph == 0, &u)) return;
+  const int side = ph / p.c.kv_heads, head = ph % p.c.kv_heads;
+  const int64_t part = (u.page * 2 + side) * p.c.kv_heads + head;
+  float* scale_at = p.c.scales + part;
+  const float old = u.had > 0 ? *scale_at : 0.0f;
+  const int64_t stride = side ? p.v_stride : p.k_stride;
+  const __nv_bfloat16* src = (side ? p.v : p.k) + u.token0 * stride + head * DIM;
+  const int c0 = u.had * kRowChunks, c1 = u.upto * kRowChunks;
+  auto at = [&](int c) {
+    return *reinterpret_cast<const uint4*>(src + (c / kRowChunks) * stride + (c % kRowChunks) * 8);
+  };
+  uint4 x[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = c0 + lane + 32 * i;
+    x[i] = c < c1 ? at(c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) a = fmaxf(a, amax8(x[i]));
+  for (int c = c0 + lane + 32 * kHeld; c < c1; c += 32) a = fmaxf(a, amax8(at(c)));
+  const float s = new_scale(old, warp_max(a));
+  uint8_t* dst = p.c.pages + part * (int64_t)(kPage * DIM);
+  if (u.had > 0 && s != old) {
+    const float f = __fdiv_rn(old, s);
+    for (int c = lane; c < u.had * DIM / 4; c += 32) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(dst) + c;
+      *w = again(*w, f);
+    }
+  }
+  const Quantizer quant(s);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = c0 + lane + 32 * i;
+    if (c < c1) reinterpret_cast<uint2*>(dst)[c] = quant(x[i]);
+  }
+  for (int c = c0 + lane + 32 * kHeld; c < c1; c += 32) reinterpret_cast<uint2*>(dst)[c] = quant(at(c));
+  __syncwarp();   // every lane has read the old scale
+  if (lane == 0) *scale_at = s;
 }
 
 }  // namespace
@@ -180,10 +279,18 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Params p) {
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream) {
   Params p{reinterpret_cast<const __nv_bfloat16*>(a.k), reinterpret_cast<const __nv_bfloat16*>(a.v),
            a.k_stride, a.v_stride, a.tokens, a.starts, a.c};
-  const dim3 grid((unsigned)(a.tokens / kPage + 2 * a.c.requests), (unsigned)(2 * a.c.kv_heads));
+  // At most 16 tokens a request on average: the kernel for few.
+  const int64_t units = a.tokens / kPage + 2 * a.c.requests;
+  if (a.tokens <= 16 * a.c.requests) {
+    const dim3 grid((unsigned)(units * ((2 * a.c.kv_heads + 7) / 8)));
+    if (a.c.dim == 128)
+      return launch_pdl(kv8_append_few_kernel<128>, grid, dim3(256), 0, stream, 1u, p);
+    return launch_pdl(kv8_append_few_kernel<64>, grid, dim3(256), 0, stream, 1u, p);
+  }
+  const dim3 grid((unsigned)(units * 2 * a.c.kv_heads));
   if (a.c.dim == 128)
-    return launch_pdl(kv8_append_kernel<128>, grid, dim3(kThreads), 0, stream, 1u, p);
-  return launch_pdl(kv8_append_kernel<64>, grid, dim3(kThreads), 0, stream, 1u, p);
+    return launch_pdl(kv8_append_page_kernel<128>, grid, dim3(kThreads), 0, stream, 1u, p);
+  return launch_pdl(kv8_append_page_kernel<64>, grid, dim3(kThreads), 0, stream, 1u, p);
 }
 
 }  // namespace dsmla

@@ -34,16 +34,21 @@ constexpr int kPiece = 16384;         // payload bytes per CTA
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrRow = DS_DEVERR_ROWREQ,
               kErrNoPage = DS_DEVERR_NOPAGE, kErrLen = DS_DEVERR_LEN;
 
+// Passed by value: a call with few pools (up to 16) launches with a tenth of
+// the parameter bytes of one with many.
+constexpr int kFewPools = 16;
+template <int MAX>
 struct Pools {
   int n;
   int pieces;                         // over all pools, for one page
-  uint8_t* data[DS_MAX_POOLS];
-  int64_t bytes[DS_MAX_POOLS];        // of a page
-  int first[DS_MAX_POOLS + 1];        // first piece of each pool
+  uint8_t* data[MAX];
+  int64_t bytes[MAX];                 // of a page
+  int first[MAX + 1];                 // first piece of each pool
 };
 
-Pools make_pools(const ds_page_pool* pools, int n) {
-  Pools r;
+template <int MAX>
+Pools<MAX> make_pools(const ds_page_pool* pools, int n) {
+  Pools<MAX> r;
   r.n = n;
   r.first[0] = 0;
   for (int i = 0; i < n; ++i) {
@@ -116,7 +121,8 @@ __device__ __forceinline__ T block_sum(T v, T* sh) {
 
 // Piece `piece` of one page's payload, from page src to page dst. 16-byte
 // vectors where the pool's base and page size allow it, else 4-byte words.
-__device__ __forceinline__ void copy_piece(const Pools& pools, int piece, int64_t src,
+template <int MAX>
+__device__ __forceinline__ void copy_piece(const Pools<MAX>& pools, int piece, int64_t src,
                                            int64_t dst) {
   int lo = 0, hi = pools.n - 1;
   while (lo < hi) {
@@ -151,8 +157,9 @@ __device__ __forceinline__ void copy_piece(const Pools& pools, int piece, int64_
 }
 
 // ------------------------------------------------------------------- copy
+template <int MAX>
 __global__ void __launch_bounds__(kThreads) pages_copy_kernel(
-    const __grid_constant__ Pools pools, int64_t num_pages, const int32_t* __restrict__ src,
+    const __grid_constant__ Pools<MAX> pools, int64_t num_pages, const int32_t* __restrict__ src,
     const int32_t* __restrict__ dst, int32_t* err) {
   pdl_wait();
   pdl_trigger();
@@ -332,8 +339,9 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(
   w.aux[i] = (int32_t)aux;
 }
 
+template <int MAX>
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(
-    const __grid_constant__ Pools pools, const PageState s, const Workspace w, int segs,
+    const __grid_constant__ Pools<MAX> pools, const PageState s, const Workspace w, int segs,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ children) {
   extern __shared__ int seg_at[];
   __shared__ int tmp[kThreads / 32];
@@ -494,8 +502,9 @@ __device__ __forceinline__ int new_page_of(const Workspace& w, int page, int num
 }
 
 // Block ranges: reference counts, block-table rows, payload.
+template <int MAX>
 __global__ void __launch_bounds__(kThreads) pages_apply_kernel(
-    const __grid_constant__ Pools pools, const PageState s, const Workspace w, int ref_blocks,
+    const __grid_constant__ Pools<MAX> pools, const PageState s, const Workspace w, int ref_blocks,
     int64_t row_blocks, int32_t* refs_out, int32_t* table_out) {
   pdl_wait();
   pdl_trigger();
@@ -536,6 +545,37 @@ __global__ void __launch_bounds__(kThreads) pages_apply_kernel(
                w.holes[i / pools.pieces]);
 }
 
+template <int MAX>
+cudaError_t run_copy(const ds_page_pool* pools, int num_pools, int64_t num_pages,
+                     const int32_t* src, const int32_t* dst, int64_t n, int32_t* err,
+                     cudaStream_t stream) {
+  const Pools<MAX> p = make_pools<MAX>(pools, num_pools);
+  return launch_pdl(pages_copy_kernel<MAX>, dim3((unsigned)(n * p.pieces)), dim3(kThreads), 0,
+                    stream, 1u, p, num_pages, src, dst, err);
+}
+
+template <int MAX>
+cudaError_t run_fork(const ds_page_pool* pools, int num_pools, const PageState& s,
+                     const Workspace& w, int segs, const int32_t* parents,
+                     const int32_t* children, int64_t n, cudaStream_t stream) {
+  const Pools<MAX> p = make_pools<MAX>(pools, num_pools);
+  const int64_t per = p.pieces > 0 ? p.pieces : 1;
+  return launch_pdl(pages_fork_kernel<MAX>, dim3((unsigned)(n * per)), dim3(kThreads), segs * 4,
+                    stream, 1u, p, s, w, segs, parents, children);
+}
+
+template <int MAX>
+cudaError_t run_apply(const ds_page_pool* pools, int num_pools, const PageState& s,
+                      const Workspace& w, int32_t* refs_out, int32_t* table_out,
+                      cudaStream_t stream) {
+  const Pools<MAX> p = make_pools<MAX>(pools, num_pools);
+  const int ref_blocks = (int)((s.num_pages + kThreads - 1) / kThreads);
+  const int64_t copy_blocks = p.pieces > 0 ? 152 * 8 : 0;
+  return launch_pdl(pages_apply_kernel<MAX>,
+                    dim3((unsigned)(ref_blocks + s.num_rows + copy_blocks)), dim3(kThreads), 0,
+                    stream, 1u, p, s, w, ref_blocks, s.num_rows, refs_out, table_out);
+}
+
 }  // namespace
 
 size_t pages_workspace_bytes(int64_t num_pages, int64_t n) {
@@ -545,9 +585,9 @@ size_t pages_workspace_bytes(int64_t num_pages, int64_t n) {
 cudaError_t launch_pages_copy(const ds_page_pool* pools, int num_pools, int64_t num_pages,
                               const int32_t* src, const int32_t* dst, int64_t n, int32_t* err,
                               cudaStream_t stream) {
-  const Pools p = make_pools(pools, num_pools);
-  return launch_pdl(pages_copy_kernel, dim3((unsigned)(n * p.pieces)), dim3(kThreads), 0, stream,
-                    1u, p, num_pages, src, dst, err);
+  return num_pools <= kFewPools
+             ? run_copy<kFewPools>(pools, num_pools, num_pages, src, dst, n, err, stream)
+             : run_copy<DS_MAX_POOLS>(pools, num_pools, num_pages, src, dst, n, err, stream);
 }
 
 cudaError_t launch_pages_free(const PageState& s, const int32_t* rows, int64_t n,
@@ -560,15 +600,14 @@ cudaError_t launch_pages_fork(const ds_page_pool* pools, int num_pools, const Pa
                               void* workspace, cudaStream_t stream) {
   Workspace w;
   carve(&w, workspace, s.num_pages, n);
-  const Pools p = make_pools(pools, num_pools);
   const int segs = num_segs(s.num_pages);
-  cudaError_t e = launch_pdl(pages_plan_kernel<true>,
-                             dim3((unsigned)(segs + (n + kThreads - 1) / kThreads)),
-                             dim3(kThreads), 0, stream, 1u, s, w, segs, parents, children, n);
+  const cudaError_t e = launch_pdl(pages_plan_kernel<true>,
+                                   dim3((unsigned)(segs + (n + kThreads - 1) / kThreads)),
+                                   dim3(kThreads), 0, stream, 1u, s, w, segs, parents, children, n);
   if (e != cudaSuccess) return e;
-  const int64_t per = p.pieces > 0 ? p.pieces : 1;
-  return launch_pdl(pages_fork_kernel, dim3((unsigned)(n * per)), dim3(kThreads), segs * 4, stream,
-                    1u, p, s, w, segs, parents, children);
+  return num_pools <= kFewPools
+             ? run_fork<kFewPools>(pools, num_pools, s, w, segs, parents, children, n, stream)
+             : run_fork<DS_MAX_POOLS>(pools, num_pools, s, w, segs, parents, children, n, stream);
 }
 
 cudaError_t launch_pages_extend(const PageState& s, const int32_t* rows, const int32_t* new_lens,
@@ -589,7 +628,6 @@ cudaError_t launch_pages_compact(const ds_page_pool* pools, int num_pools, const
                                  void* workspace, cudaStream_t stream) {
   Workspace w;
   carve(&w, workspace, s.num_pages, 0);
-  const Pools p = make_pools(pools, num_pools);
   const int segs = num_segs(s.num_pages);
   cudaError_t e = launch_pdl(pages_snapshot_kernel, dim3((unsigned)segs), dim3(kThreads), 0, stream,
                              1u, s, w);
@@ -597,11 +635,9 @@ cudaError_t launch_pages_compact(const ds_page_pool* pools, int num_pools, const
   e = launch_pdl(pages_lists_kernel, dim3((unsigned)segs), dim3(kThreads), 0, stream, 1u, s, w,
                  segs, num_live_out);
   if (e != cudaSuccess) return e;
-  const int ref_blocks = (int)((s.num_pages + kThreads - 1) / kThreads);
-  const int64_t copy_blocks = p.pieces > 0 ? 152 * 8 : 0;
-  return launch_pdl(pages_apply_kernel, dim3((unsigned)(ref_blocks + s.num_rows + copy_blocks)),
-                    dim3(kThreads), 0, stream, 1u, p, s, w, ref_blocks, s.num_rows, refs_out,
-                    table_out);
+  return num_pools <= kFewPools
+             ? run_apply<kFewPools>(pools, num_pools, s, w, refs_out, table_out, stream)
+             : run_apply<DS_MAX_POOLS>(pools, num_pools, s, w, refs_out, table_out, stream);
 }
 
 static_assert(kMaxSegs * 4 <= 48 * 1024 - 256, "segment counts fit the default shared memory");
