@@ -475,8 +475,9 @@ size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_he
  * token i of a request with n tokens sees the first
  * clamp(lens[r] - n + 1 + i, 0, 64 * bt_stride) positions (causal). Rows of
  * out and lse that belong to no request are left as they are. Arguments as
- * for ds_kv8_decode; q, out and lse are indexed by token. The workspace may
- * be NULL where ds_kv8_prefill_workspace_size() is 0.
+ * for ds_kv8_decode; q, out and lse are indexed by token. The workspace has
+ * ds_kv8_prefill_workspace_size() bytes, 256-byte aligned; its contents need
+ * no initialisation.
  *
  * A token's outputs depend on its own request alone, bit for bit, and not on
  * how the request's tokens are spread over calls.

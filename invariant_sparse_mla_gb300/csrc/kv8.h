@@ -57,7 +57,9 @@ size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int k
 size_t kv8_prefill_workspace_bytes(int64_t tokens, int64_t requests, int heads, int kv_heads,
                                    int dim);
 
-// CTAs of a prefill call per kv head.
+// SMs of a device (looked up once).
+int kv8_sm_count(int dev);
+// Items (256 query rows) of a prefill call per kv head, an upper bound.
 int64_t kv8_prefill_units(int64_t tokens, int64_t requests, int group);
 
 // ---- pages

@@ -955,20 +955,6 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
   if (lane == 0) p.lse[w] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-int sm_count(int dev) {
-  static std::atomic<int> cached[PerDeviceOnce::kMaxDevices];
-  const bool tracked = dev >= 0 && dev < PerDeviceOnce::kMaxDevices;
-  int n = tracked ? cached[dev].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-      (void)cudaGetLastError();
-      return 152;
-    }
-    if (tracked) cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 template <int R8, int DIM>
 cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, unsigned grid,
                         cudaStream_t stream) {
@@ -984,7 +970,7 @@ template <int DIM>
 cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStream_t stream) {
   // At most one CTA per item, two per SM.
   const int64_t items = p.c.requests * p.c.kv_heads * p.row_groups * p.spans;
-  const int64_t most = 2 * (int64_t)sm_count(dev);
+  const int64_t most = 2 * (int64_t)kv8_sm_count(dev);
   const unsigned grid = (unsigned)(items < most ? items : most);
   cudaError_t e;
   switch ((p.rows + 7) / 8) {
@@ -1003,6 +989,20 @@ cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStr
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
+
+int kv8_sm_count(int dev) {
+  static std::atomic<int> cached[PerDeviceOnce::kMaxDevices];
+  const bool tracked = dev >= 0 && dev < PerDeviceOnce::kMaxDevices;
+  int n = tracked ? cached[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      return 152;
+    }
+    if (tracked) cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
                                   int64_t bt_stride) {

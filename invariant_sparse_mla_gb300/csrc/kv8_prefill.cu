@@ -17,8 +17,15 @@
 // request's cache and its own q alone.
 //
 // Work split: query rows are (token, head of the group) pairs of one kv head,
-// in order, so that a K/V tile serves the whole group; a CTA owns 256 rows in
-// two row tiles of 128, one kv head, and all positions they see.
+// in order, so that a K/V tile serves the whole group; an item is 256 rows (two
+// row tiles of 128), one kv head, and all positions they see. A small kernel
+// first numbers the tiles of all items; one CTA per SM then takes an equal run
+// of them. A run that ends inside an item hands the rows' state (reference,
+// sum and fp32 outputs) to the next CTA, which continues where it stopped: the
+// same operations in the same order, so that where runs are cut changes no
+// bit. A CTA does the piece that it hands over first and the piece that it
+// takes over last, so nobody waits in practice (512 equal items on 152 SMs
+// would otherwise take 4 rounds for 3.4 rounds of work).
 //   warps 0-3, 4-7   softmax of row tile 0 and 1 (thread = row = TMEM lane);
 //   warps 8-11       codes from global memory, through registers, to f16 tiles
 //                    of K and V in shared memory (two buffers each): the copy
@@ -26,7 +33,9 @@
 //                    memory first would cost 64 KB of its bandwidth a tile;
 //   warp 12          MMA issuer: S = Q K^T (M 128, N 128), O += P V with P from
 //                    TMEM, where it lies over S. The two row tiles alternate,
-//                    so that one's products run under the other's softmax.
+//                    so that one's products run under the other's softmax,
+//                    and PV begins when half of a P is there;
+//   warp 13          looks the pieces up ahead of the others.
 // The bound is the tensor pipe and shared-memory bandwidth behind it: an M 128
 // x N 128 x K 16 product reads 8 KB in the 64 cycles it takes.
 
@@ -44,9 +53,29 @@ constexpr int kRows = 256;               // query rows per CTA
 constexpr int kThreads = 512;
 constexpr int kLoaderWarp = 8, kMmaWarp = 12;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-// Registers: 512 threads launch with 128 each; 256 * 176 + 128 * 112 +
-// 128 * 48 = 65536 = 512 * 128.
-constexpr int kRegsSoftmax = 176, kRegsLoader = 112, kRegsMma = 48;
+// Registers: 512 threads launch with 128 each; 256 * 152 + 128 * 128 +
+// 128 * 80 = 65536 = 512 * 128.
+constexpr int kRegsSoftmax = 152, kRegsMma = 80;
+
+constexpr int kMaxCtas = 192;
+
+// What the first kernel writes: item (unit u of one kv head) has weight
+// first[u + 1] - first[u] tiles (1 for rows that see nothing, 0 for none).
+struct alignas(32) UnitInfo {
+  int64_t row0;          // first row of the request's rows
+  int32_t r, t0, n;      // request, its first token, its tokens
+  int32_t raw_len;
+};
+struct Plan {
+  int64_t* first;        // [units + 1]
+  UnitInfo* info;        // [units]
+  int32_t* flags;        // [kMaxCtas]
+  uint8_t* state;        // [kMaxCtas] x state_bytes
+};
+// O [dim / 4][256 rows] float4, then (reference or unset, sum) and the NaN bits.
+__host__ __device__ constexpr int64_t state_bytes(int dim) {
+  return (int64_t)kRows * (dim * 4 + 16 + dim / 8);
+}
 
 template <int DIM>
 struct Layout {
@@ -57,29 +86,42 @@ struct Layout {
   static constexpr int kV = kK + 2 * kTileBytes;          // two buffers
   static constexpr int kBars = kV + 2 * kTileBytes;
   static constexpr int kMeta = kBars + 32 * 8;            // 4 tiles x 2 pages x float4
-  static constexpr int kNanMap = kMeta + 4 * 32;          // 2 x [128][DIM / 16] u16
+  static constexpr int kPiece = kMeta + 4 * 32;           // 2 x 64 bytes
+  static constexpr int kNanMap = kPiece + 128;            // 2 x [128][DIM / 16] u16
   static constexpr int kNanMapBytes = kTile * (DIM / 16) * 2;
   static constexpr int kRowNan = kNanMap + 2 * kNanMapBytes;   // [256][DIM / 16] u16
   static constexpr int kMisc = kRowNan + kRows * (DIM / 16) * 2;
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // TMEM: S (P over its first half) and O of both row tiles.
+  // TMEM: S (P over its upper half) and O of both row tiles.
   static constexpr uint32_t kS = 0, kO = 2 * kTile;
   static constexpr uint32_t kCols = 2 * kTile + 2 * DIM <= 256 ? 256u : 512u;
 };
 
 enum Bar {
-  kQFull = 0,       // the softmax threads of the row tiles
-  kKFull = 1,       // 2: the 128 loader threads
-  kKEmpty = 3,      // 2: commit
-  kVFull = 5,       // 2: the 128 loader threads
-  kVEmpty = 7,      // 2: commit
-  kSFull = 9,       // 2 (row tile): commit
-  kPFull = 11,      // 2: the row tile's 128 softmax threads
-  kPvDone = 13,     // 2: commit
-  kDrain = 15,
-  kNumBars = 16
+  kQFull = 0,       // 2 (row tile): its 128 softmax threads
+  kKFull = 2,       // 2: the 128 loader threads
+  kKEmpty = 4,      // 2: commit
+  kVFull = 6,       // 2: the 128 loader threads
+  kVEmpty = 8,      // 2: commit
+  kSFull = 10,      // 2 (row tile): commit
+  kPHalf = 12,      // 2: the row tile's softmax threads (positions 64-127 of P)
+  kPFull = 14,      // 2: the same (all of P)
+  kPvDone = 16,     // 2: commit
+  kPieceFull = 18,  // 2: the scheduling lane
+  kPieceEmpty = 20, // 2: every thread that reads pieces
+  kDrain = 22,
+  kNumBars = 23
+};
+constexpr int kPieceReaders = 256 + 128 + 32;
+
+// One run of tiles [j0, j1) of an item. r < 0 ends the list.
+struct alignas(64) Piece {
+  int64_t row0;
+  int32_t r, t0, n, raw_len;
+  int32_t kvh, nt, j0, j1;
+  int32_t take, give;    // state slots to continue from / to hand over to, or -1
 };
 
 struct Params {
@@ -88,12 +130,204 @@ struct Params {
   int64_t tokens;
   const int32_t* starts;
   int heads, group;
-  int64_t units;         // row tiles pairs of one kv head, an upper bound
+  int64_t units;         // items of one kv head, an upper bound
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
+  Plan plan;
   Kv8Cache c;
 };
+
+__device__ __forceinline__ int clamp_pos(const Params& p, int64_t v) {
+  const int64_t most = p.c.bt_stride * kPage;
+  return (int)(v < 0 ? 0 : (v > most ? most : v));
+}
+// Positions that a row of the request sees.
+__device__ __forceinline__ int visible(const Params& p, int raw_len, int n, int64_t row) {
+  return clamp_pos(p, raw_len - n + 1 + row / p.group);
+}
+__device__ __forceinline__ int64_t last_row_of(const Params& p, int64_t row0, int n) {
+  const int64_t rows = (int64_t)n * p.group;
+  return row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
+}
+// Tiles of an item.
+__device__ __forceinline__ int item_tiles(const Params& p, int raw_len, int n, int64_t row0) {
+  return (visible(p, raw_len, n, last_row_of(p, row0, n)) + kTile - 1) / kTile;
+}
+
+// Units of request r are numbered from floor(starts[r] * group / 256) + r (at
+// least as many as it has); one CTA finds each unit's request and numbers the
+// tiles.
+__global__ void __launch_bounds__(1024) kv8_prefill_plan_kernel(const Params p) {
+  __shared__ int64_t part[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < kMaxCtas) p.plan.flags[tid] = 0;
+  auto start_of = [&](int64_t r) {
+    const int64_t s = p.starts[r];
+    return s < 0 ? 0 : (s > p.tokens ? p.tokens : s);
+  };
+  const int64_t per = (p.units + 1023) / 1024;
+  const int64_t u0 = tid * per, u1 = u0 + per < p.units ? u0 + per : p.units;
+  int64_t sum = 0;
+  if (u0 < u1) {
+    // The request of the first unit; the others follow.
+    int64_t lo = 0, hi = p.c.requests - 1;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      if (start_of(mid) * p.group / kRows + mid <= u0)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    int64_t r = lo, t0 = start_of(r), t1 = start_of(r + 1);
+    int raw = p.c.lens[r];
+    for (int64_t u = u0; u < u1; ++u) {
+      while (r + 1 < p.c.requests && t1 * p.group / kRows + r + 1 <= u) {
+        ++r;
+        t0 = t1;
+        t1 = start_of(r + 1);
+        raw = p.c.lens[r];
+      }
+      UnitInfo i;
+      i.r = (int)r;
+      i.t0 = (int)t0;
+      i.n = (int)(t1 > t0 ? t1 - t0 : 0);
+      i.raw_len = raw;
+      i.row0 = (u - (t0 * p.group / kRows + r)) * kRows;
+      int w = 0;
+      if (i.row0 >= 0 && i.row0 < (int64_t)i.n * p.group) {
+        w = item_tiles(p, raw, i.n, i.row0);
+        if (w == 0) w = 1;
+      }
+      p.plan.info[u] = i;
+      p.plan.first[u] = sum;     // within the thread's run; completed below
+      sum += w;
+    }
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int64_t before = inc - sum, total = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  if (before != 0)
+    for (int64_t u = u0; u < u1; ++u) p.plan.first[u] += before;
+  if (tid == 0) p.plan.first[p.units] = total;
+}
+
+// The pieces of CTA `blockIdx.x`, one after the other.
+struct Scheduler {
+  const Params& p;
+  int64_t per_head, lo, hi;       // tiles of a kv head; the CTA's run
+  int64_t i0, i1, at;             // items kvh * units + u of its ends; the next one
+  bool first_cut, last_cut;
+  int phase;
+
+  __device__ int64_t start_of(int64_t i) const {
+    return i / p.units * per_head + p.plan.first[i % p.units];
+  }
+  __device__ int64_t weight_of(int64_t i) const {
+    return p.plan.first[i % p.units + 1] - p.plan.first[i % p.units];
+  }
+  // The item that holds tile x.
+  __device__ int64_t find(int64_t x) const {
+    const int64_t head = x / per_head;
+    x -= head * per_head;
+    int64_t a = 0, b = p.units - 1;   // last unit with first[u] <= x
+    while (a < b) {
+      const int64_t mid = (a + b + 1) >> 1;
+      if (p.plan.first[mid] <= x)
+        a = mid;
+      else
+        b = mid - 1;
+    }
+    return head * p.units + a;        // (its weight is not 0)
+  }
+  __device__ explicit Scheduler(const Params& params) : p(params) {
+    per_head = p.plan.first[p.units];
+    const int64_t total = per_head * p.c.kv_heads;
+    lo = total * blockIdx.x / gridDim.x;
+    hi = total * (blockIdx.x + 1) / gridDim.x;
+    phase = 3;
+    if (lo >= hi) return;
+    i0 = find(lo);
+    i1 = find(hi - 1);
+    first_cut = start_of(i0) < lo;
+    last_cut = start_of(i1) + weight_of(i1) > hi;
+    at = i0;
+    phase = i0 != i1 && last_cut ? 0 : 1;
+  }
+  __device__ Piece piece(int64_t i) const {
+    const UnitInfo u = p.plan.info[i % p.units];
+    const int64_t s = start_of(i), e = s + weight_of(i);
+    Piece x;
+    x.row0 = u.row0;
+    x.r = u.r;
+    x.t0 = u.t0;
+    x.n = u.n;
+    x.raw_len = u.raw_len;
+    x.kvh = (int)(i / p.units);
+    x.nt = item_tiles(p, u.raw_len, u.n, u.row0);
+    x.j0 = (int)(lo > s ? lo - s : 0);
+    x.j1 = (int)((hi < e ? hi : e) - s);
+    if (x.j1 > x.nt) x.j1 = x.nt;     // rows that see nothing: weight 1, no tile
+    x.take = lo > s ? (int)blockIdx.x - 1 : -1;
+    x.give = hi < e ? (int)blockIdx.x : -1;
+    return x;
+  }
+  __device__ Piece next() {
+    if (phase == 0) {                 // what the next CTA waits for
+      phase = 1;
+      return piece(i1);
+    }
+    if (phase == 1) {
+      while (at <= i1) {
+        const int64_t i = at++;
+        if (weight_of(i) == 0) continue;
+        if (i0 != i1 && ((i == i0 && first_cut) || (i == i1 && last_cut))) continue;
+        return piece(i);
+      }
+      phase = 2;
+    }
+    if (phase == 2) {                 // what the CTA before has begun
+      phase = 3;
+      if (i0 != i1 && first_cut) return piece(i0);
+    }
+    Piece x;
+    x.r = -1;
+    return x;
+  }
+};
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p) {
@@ -103,50 +337,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LY::kBars);
   float4* meta = reinterpret_cast<float4*>(smem + LY::kMeta);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + LY::kPiece);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
-  volatile int* nan_tag = reinterpret_cast<volatile int*>(smem + LY::kMisc + 8);   // 2
+  volatile uint32_t* nan_tag = reinterpret_cast<volatile uint32_t*>(smem + LY::kMisc + 8);   // 2
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
-
-  // ---- which rows: n tokens of request r are n * group rows, and the row
-  // tile pairs of request r are numbered from floor(starts[r] * group / 256) +
-  // r (at least as many as it has). The last ones, which see most, go first.
-  const int64_t unit = p.units - 1 - blockIdx.x % p.units;
-  const int kvh = (int)(blockIdx.x / p.units);
-  auto start_of = [&](int64_t r) {
-    const int64_t s = p.starts[r];
-    return s < 0 ? 0 : (s > p.tokens ? p.tokens : s);
-  };
-  int64_t lo = 0, hi = p.c.requests - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (start_of(mid) * p.group / kRows + mid <= unit)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int64_t r = lo, t0 = start_of(r);
-  const int64_t n = start_of(r + 1) - t0;
-  const int64_t row0 = (unit - (t0 * p.group / kRows + r)) * kRows;
-  if (n <= 0 || row0 < 0 || row0 >= n * p.group) return;   // the whole CTA
-  const int raw_len = p.c.lens[r];
-  const int most = (int)(p.c.bt_stride * kPage);
-  auto clamp_pos = [&](int64_t v) { return (int)(v < 0 ? 0 : (v > most ? most : v)); };
-  const int len = clamp_pos(raw_len);
-  auto visible = [&](int64_t row) { return clamp_pos(raw_len - n + 1 + row / p.group); };
-  const int64_t last_row = row0 + kRows <= n * p.group ? row0 + kRows - 1 : n * p.group - 1;
-  const int mts = last_row - row0 >= kTile ? 2 : 1;         // row tiles with rows
-  const int min_vis = visible(row0);
-  const int nt = (visible(last_row) + kTile - 1) / kTile;   // tiles
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i == kQFull) count = 128u * mts;
-      if ((i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) ||
-          (i >= kPFull && i < kPFull + 2))
+      if (i < kKEmpty || (i >= kVFull && i < kVEmpty) || (i >= kPHalf && i < kPvDone))
         count = 128u;
+      if (i >= kPieceEmpty && i < kDrain) count = kPieceReaders;
       mbar_init(&bars[i], count);
     }
     mbar_fence_init();
@@ -156,182 +357,301 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     tmem_alloc(tmem_slot, LY::kCols);
     tmem_relinquish();
   }
+  pdl_wait();
+  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // The next piece, in shared memory until piece_done() (every reader calls both
+  // in step; r < 0: no more).
+  uint32_t np = 0;
   bool failed = false;
+  auto next_piece = [&]() {
+    const bool ok = mbar_wait_long(&bars[kPieceFull + (np & 1)], (np >> 1) & 1);
+    if (!__all_sync(0xffffffffu, ok)) failed = true;
+    return const_cast<const volatile Piece*>(&pieces[np & 1]);
+  };
+  auto piece_done = [&]() {
+    mbar_arrive(&bars[kPieceEmpty + (np & 1)]);
+    ++np;
+  };
+
   if (warp < kLoaderWarp) {
     // ----------------------------------------------------------- softmax
     regs_inc<kRegsSoftmax>();
     const int m = warp >> 2;                         // row tile
-    const int tiles = m < mts ? nt : 0;
     const int row = (warp & 3) * 32 + lane;          // TMEM lane
-    const int64_t grow = row0 + m * kTile + row;     // row of the request
-    const bool active = grow < n * p.group;
-    const int64_t token = t0 + grow / p.group;
-    const int head = kvh * p.group + (int)(grow % p.group);
-    const int vis = active ? visible(grow) : 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + LY::kS + m * kTile;
     const uint32_t t_o = tmem + lane_base + LY::kO + m * DIM;
-    float f;
-    {
-      // The row's q times a power of two, in f16.
-      uint4 x[DIM / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + head * DIM);
+    uint16_t* const row_bits =
+        reinterpret_cast<uint16_t*>(smem + LY::kRowNan) + (m * kTile + row) * (DIM / 16);
+    uint32_t tiles = 0;        // tiles of this row tile so far
+    uint32_t kv = 0;           // tiles of the CTA so far
+    while (true) {
+      const volatile Piece& x = *next_piece();
+      if (failed || x.r < 0) break;
+      // Row of the request, whether it and its row tile exist, and its q and out.
+      auto grow = [&]() { return x.row0 + m * kTile + row; };
+      auto exists = [&]() { return grow() < (int64_t)x.n * p.group; };
+      auto token = [&]() { return x.t0 + grow() / p.group; };
+      auto head = [&]() { return x.kvh * p.group + (int)(grow() % p.group); };
+      const bool any = x.row0 + m * kTile < (int64_t)x.n * p.group;
+      const int vis = exists() ? visible(p, x.raw_len, x.n, grow()) : 0;
+      const int min_vis = visible(p, x.raw_len, x.n, x.row0);
+      float f = 0.0f;
+      if (any && x.j1 > x.j0) {
+        const bool active = exists();
+        // The row's q times a power of two, in f16.
+        uint4 v[DIM / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + token() * p.q_stride + head() * DIM);
 #pragma unroll
-      for (int i = 0; i < DIM / 8; ++i) x[i] = active ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t top = 0u;   // largest magnitude bits (NaN above infinity)
+        for (int i = 0; i < DIM / 8; ++i) v[i] = active ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t top = 0u;   // largest magnitude bits (NaN above infinity)
 #pragma unroll
-      for (int i = 0; i < DIM / 8; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < DIM / 8; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          top = max(top, max((w[u] << 16) & 0x7FFFFFFFu, w[u] & 0x7FFF0000u));
-      }
-      // Largest |q| 2^k in [2^14, 2^15); 2^k stays a normal float.
-      int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
-      k = k > 120 ? 120 : (k < -120 ? -120 : k);
-      const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-      f = top >= 0x7F800000u ? NAN
-                             : __uint_as_float((uint32_t)(127 - k) << 23) * p.scale_log2;
-      uint8_t* dst = smem + LY::kQ + m * LY::kTileBytes;
-#pragma unroll
-      for (int i = 0; i < DIM / 8; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const __half2 v = __floats2half2_rn(__uint_as_float(w[u] << 16) * up,
-                                              __uint_as_float(w[u] & 0xFFFF0000u) * up);
-          h[u] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int u = 0; u < 4; ++u)
+            top = max(top, max((w[u] << 16) & 0x7FFFFFFFu, w[u] & 0x7FFF0000u));
         }
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * LY::kBlock + swz<128>(row, (i & 7) * 16)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
+        // Largest |q| 2^k in [2^14, 2^15); 2^k stays a normal float.
+        int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
+        k = k > 120 ? 120 : (k < -120 ? -120 : k);
+        const float up = copysignf(__uint_as_float((uint32_t)(k + 127) << 23), p.scale_log2);
+        f = top >= 0x7F800000u ? NAN
+                               : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
+        uint8_t* dst = smem + LY::kQ + m * LY::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < DIM / 8; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __half2 y = __floats2half2_rn(__uint_as_float(w[u] << 16) * up,
+                                                __uint_as_float(w[u] & 0xFFFF0000u) * up);
+            h[u] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * LY::kBlock + swz<128>(row, (i & 7) * 16)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kQFull + m]);
       }
-      fence_proxy_async_smem();
-      if (m < mts) mbar_arrive(&bars[kQFull]);
-    }
-    float ref = 0.0f, l = 0.0f;
-    bool unset = true, row_nan = false;
-    for (int j = 0; j < tiles; ++j) {
-      const int pos0 = j * kTile;
-      if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kSFull + m], j & 1))) {
+      float ref = 0.0f, l = 0.0f;
+      bool unset = true, row_nan = false;
+      if (x.take >= 0) {
+        // Continue from the CTA before: it does this piece first.
+        const uint8_t* st = p.plan.state + x.take * state_bytes(DIM);
+        const uint64_t began = clock64();
+        bool there = true;
+        while (true) {
+          int flag;
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
+                       : "=r"(flag)
+                       : "l"(p.plan.flags + x.take)
+                       : "memory");
+          if (flag == 256) break;   // 256 threads have written theirs
+          if ((uint64_t)(clock64() - began) > (1ull << 32)) {
+            there = false;
+            break;
+          }
+          __nanosleep(200);
+        }
+        if (!__all_sync(0xffffffffu, there)) {
+          failed = true;
+          break;
+        }
+        const int rr = m * kTile + row;
+        const float4* so = reinterpret_cast<const float4*>(st);
+#pragma unroll 4
+        for (int d = 0; d < DIM; d += 4) {
+          const float4 o = so[(d / 4) * kRows + rr];
+          const float v[4] = {o.x, o.y, o.z, o.w};
+          tmem_st4(t_o + d, v);
+        }
+        tmem_wait_st();
+        const float4 ml = reinterpret_cast<const float4*>(st + kRows * DIM * 4)[rr];
+        ref = ml.x;
+        l = ml.y;
+        unset = ml.z != 0.0f;
+        row_nan = ml.w != 0.0f;
+        const uint16_t* sn = reinterpret_cast<const uint16_t*>(st + kRows * (DIM * 4 + 16));
+        if (row_nan)
+          for (int c = 0; c < DIM / 16; ++c) row_bits[c] = sn[c * kRows + rr];
+      }
+      uint32_t g = kv;         // tile of the CTA
+      for (int j = any ? x.j0 : x.j1; j < x.j1; ++j, ++g) {
+        const int pos0 = j * kTile;
+        if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kSFull + m], tiles & 1))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        // The row's largest score of each page, 64 columns at a time (a page has
+        // one scale, so the scores themselves compare), then the weights:
+        // positions 64-127 from the registers that hold them, 0-63 read again.
+        // P goes over the upper half of S, which is in registers by then.
+        float2 s[32];
+        float* const s1 = reinterpret_cast<float*>(s);
+        const float4 mt0 = meta[(g & 3) * 2], mt1 = meta[(g & 3) * 2 + 1];
+        // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
+        const int end0 = mt0.w != 0.0f ? vis - pos0 : 0, end1 = mt1.w != 0.0f ? vis - pos0 - 64 : 0;
+        auto load = [&](int half) {
+          tmem_ld32(t_s + 64 * half, s1);
+          tmem_ld32(t_s + 64 * half + 32, s1 + 32);
+          tmem_fence<64>(s1);
+        };
+        auto hide = [&](int end) {
+          if (end < 64) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s1[i] = i < end ? s1[i] : -INFINITY;
+          }
+        };
+        auto largest = [&]() {
+          float top[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) top[u] = fmaxf(s1[u], s1[4 + u]);
+#pragma unroll
+          for (int i = 8; i < 64; i += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top[u] = fmaxf(fmaxf(top[u], s1[i + u]), s1[i + 4 + u]);
+          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        };
+        const float g0 = f * mt0.x, g1 = f * mt1.x;
+        load(0);
+        hide(end0);
+        const float top0 = largest();
+        load(1);
+        hide(end1);
+        const float top1 = largest();
+        // (-inf times a product of scales that is 0 would be NaN.)
+        float ymax = top0 > -INFINITY ? __fmaf_rn(top0, g0, mt0.y - ref) : -INFINITY;
+        if (top1 > -INFINITY) ymax = fmaxf(ymax, __fmaf_rn(top1, g1, mt1.y - ref));
+        const bool move = unset ? ymax > -INFINITY : ymax > 15.0f;
+        if (__any_sync(0xffffffffu, move)) {
+          const float by = move ? ymax - 3.0f : 0.0f;
+          const float al = move ? (unset ? 0.0f : ex2(-by)) : 1.0f;
+          if (move) {
+            ref += by;
+            l *= al;
+            unset = false;
+          }
+          // (S of tile j was issued behind the end of PV of tile j - 1.)
+          if (j > 0 && __any_sync(0xffffffffu, al != 1.0f)) {
+#pragma unroll 1
+            for (int c = 0; c < DIM; c += 16) {
+              float o[16];
+              tmem_ld<16>(t_o + c, o);
+              tmem_fence<16>(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= al;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) tmem_st4(t_o + c + i, o + i);
+            }
+          }
+        }
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+          if (half == 0) load(0);
+          const int end = half ? end1 : end0;
+          const float gg = half ? g1 : g0, cc = (half ? mt1.y : mt0.y) - ref;
+          const float2 g2 = make_float2(gg, gg), c2 = make_float2(cc, cc);
+          float2 sum = make_float2(0.0f, 0.0f);
+          // (Hidden scores of half 1 are -inf already; hide() follows the product
+          // with the scales, which may be 0.)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = fma2(s[i], g2, c2);
+          hide(end);
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) {
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = make_float2(ex2(s[c + i].x), ex2(s[c + i].y));
+              sum = add2(sum, e);
+              const __half2 w = __floats2half2_rn(e.x, e.y);
+              h[i] = *reinterpret_cast<const uint32_t*>(&w);
+            }
+            tmem_st16u(t_s + 64 + 32 * half + c, h);
+          }
+          l = __fmaf_rn(sum.x + sum.y, half ? mt1.z : mt0.z, l);
+          if (half == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars[kPHalf + m]);
+          }
+        }
+        // Where rows see different lengths, NaN values were taken out of the tile
+        // and listed: the rows that see one get a NaN in that dim.
+        if (pos0 + kTile > min_vis) {
+          if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kVFull + (g & 1)], (g >> 1) & 1))) {
+            failed = true;
+            break;
+          }
+          if (nan_tag[g & 1] == g + 1) {
+            const uint16_t* map =
+                reinterpret_cast<const uint16_t*>(smem + LY::kNanMap + (g & 1) * LY::kNanMapBytes);
+            if (!row_nan)
+              for (int c = 0; c < DIM / 16; ++c) row_bits[c] = 0;
+            row_nan = true;
+            for (int i = 0; i < kTile && pos0 + i < vis; ++i)
+              for (int c = 0; c < DIM / 16; ++c) row_bits[c] |= map[i * (DIM / 16) + c];
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars[kPFull + m]);
+        ++tiles;
+      }
+      if (failed) break;
+      kv += (uint32_t)(x.j1 - x.j0);
+      if (any && x.j1 > x.j0 &&
+          !__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1))) {
         failed = true;
         break;
       }
       tc_fence_after();
-      float s[kTile];
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld32(t_s + c, s + c);
-      const float4 mt0 = meta[(j & 3) * 2], mt1 = meta[(j & 3) * 2 + 1];
-      tmem_fence<kTile>(s);
-      // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
-      const float g0 = f * mt0.x, g1 = f * mt1.x;
-      const float c0 = mt0.y - ref, c1 = mt1.y - ref;
-#pragma unroll
-      for (int i = 0; i < 64; ++i) s[i] = __fmaf_rn(s[i], g0, c0);
-#pragma unroll
-      for (int i = 64; i < 128; ++i) s[i] = __fmaf_rn(s[i], g1, c1);
-      if (pos0 + kTile > vis || mt0.w == 0.0f || mt1.w == 0.0f) {
-        const int end0 = mt0.w != 0.0f ? vis - pos0 : 0, end1 = mt1.w != 0.0f ? vis - pos0 : 0;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) s[i] = i < end0 ? s[i] : -INFINITY;
-#pragma unroll
-        for (int i = 64; i < 128; ++i) s[i] = i < end1 ? s[i] : -INFINITY;
-      }
-      float top[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) top[u] = fmaxf(s[u], s[4 + u]);
-#pragma unroll
-      for (int i = 8; i < kTile; i += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], fmaxf(s[i + u], s[i + 4 + u]));
-      const float ymax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      const bool move = unset ? ymax > -INFINITY : ymax > 15.0f;
-      if (__any_sync(0xffffffffu, move)) {
-        const float by = move ? ymax - 3.0f : 0.0f;
-        const float al = move ? (unset ? 0.0f : ex2(-by)) : 1.0f;
-        if (move) {
-          ref += by;
-          l *= al;
-          unset = false;
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] -= by;
-        }
-        // (S of tile j was issued behind the end of PV of tile j - 1.)
-        if (j > 0 && __any_sync(0xffffffffu, al != 1.0f)) {
+      if (x.give >= 0) {
+        uint8_t* st = p.plan.state + x.give * state_bytes(DIM);
+        const int rr = m * kTile + row;
+        float4* so = reinterpret_cast<float4*>(st);
+        if (any) {
 #pragma unroll 1
-          for (int c = 0; c < DIM; c += 16) {
+          for (int d = 0; d < DIM; d += 16) {
             float o[16];
-            tmem_ld<16>(t_o + c, o);
+            tmem_ld<16>(t_o + d, o);
             tmem_fence<16>(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= al;
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) tmem_st4(t_o + c + i, o + i);
+            for (int i = 0; i < 16; i += 4)
+              so[(d + i) / 4 * kRows + rr] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
+        reinterpret_cast<float4*>(st + kRows * DIM * 4)[rr] =
+            make_float4(ref, l, unset ? 1.0f : 0.0f, row_nan ? 1.0f : 0.0f);
+        uint16_t* sn = reinterpret_cast<uint16_t*>(st + kRows * (DIM * 4 + 16));
+        if (row_nan)
+          for (int c = 0; c < DIM / 16; ++c) sn[c * kRows + rr] = row_bits[c];
+        __threadfence();
+        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.plan.flags + x.give)
+                     : "memory");
+        piece_done();
+        continue;
       }
-      float sum0[2] = {0.0f, 0.0f}, sum1[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t h[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = ex2(s[c + 2 * i]), b = ex2(s[c + 2 * i + 1]);
-          if (c < 64) {
-            sum0[0] += a;
-            sum0[1] += b;
-          } else {
-            sum1[0] += a;
-            sum1[1] += b;
-          }
-          const __half2 v = __floats2half2_rn(a, b);
-          h[i] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-        tmem_st16u(t_s + c / 2, h);
+      if (!any) {
+        piece_done();
+        continue;
       }
-      l = __fmaf_rn(sum0[0] + sum0[1], mt0.z, l);
-      l = __fmaf_rn(sum1[0] + sum1[1], mt1.z, l);
-      // Where rows see different lengths, NaN values were taken out of the tile
-      // and listed: the rows that see one get a NaN in that dim.
-      if (pos0 + kTile > min_vis) {
-        if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kVFull + (j & 1)], (j >> 1) & 1))) {
-          failed = true;
-          break;
-        }
-        if (nan_tag[j & 1] == j + 1) {
-          const uint16_t* map =
-              reinterpret_cast<const uint16_t*>(smem + LY::kNanMap + (j & 1) * LY::kNanMapBytes);
-          uint16_t* mine =
-              reinterpret_cast<uint16_t*>(smem + LY::kRowNan) + (m * kTile + row) * (DIM / 16);
-          if (!row_nan)
-            for (int c = 0; c < DIM / 16; ++c) mine[c] = 0;
-          row_nan = true;
-          for (int i = 0; i < kTile && pos0 + i < vis; ++i)
-            for (int c = 0; c < DIM / 16; ++c) mine[c] |= map[i * (DIM / 16) + c];
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars[kPFull + m]);
-    }
-    if (!failed && tiles > 0 &&
-        !__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1)))
-      failed = true;
-    tc_fence_after();
-    if (!failed) {
+      const bool active = exists();
+      const int64_t at = token() * p.heads + head();
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(0.125f, l);
-      __nv_bfloat16* dst = p.out + (token * p.heads + head) * DIM;
-      const uint16_t* mine =
-          reinterpret_cast<const uint16_t*>(smem + LY::kRowNan) + (m * kTile + row) * (DIM / 16);
+      __nv_bfloat16* dst = p.out + at * DIM;
 #pragma unroll
       for (int c = 0; c < DIM; c += 32) {
         float o[32];
-        if (tiles > 0) {
+        if (x.nt > 0) {
           tmem_ld32(t_o + c, o);
           tmem_fence<32>(o);
         }
@@ -341,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           float a = l == 0.0f ? 0.0f : o[2 * i] * inv, b = l == 0.0f ? 0.0f : o[2 * i + 1] * inv;
           if (row_nan) {
             const int d = c + 2 * i;
-            if ((mine[d >> 4] >> (d & 15)) & 1) a = NAN;
-            if ((mine[d >> 4] >> ((d & 15) + 1)) & 1) b = NAN;
+            if ((row_bits[d >> 4] >> (d & 15)) & 1) a = NAN;
+            if ((row_bits[d >> 4] >> ((d & 15) + 1)) & 1) b = NAN;
           }
-          const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-          h[i] = *reinterpret_cast<const uint32_t*>(&v);
+          const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
+          h[i] = *reinterpret_cast<const uint32_t*>(&y);
         }
         if (active) {
 #pragma unroll
@@ -354,135 +674,145 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
                 make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
         }
       }
-      if (active)
-        p.lse[token * p.heads + head] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
+      if (active) p.lse[at] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
+      piece_done();
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ loader
-    regs_dec<kRegsLoader>();
     constexpr int NC = kTile * DIM / 16 / 128;     // 16-code chunks per thread and tile
     constexpr int RC = DIM / 16;                   // chunks per position
     const int lt = tid - kLoaderWarp * 32;
-    const int32_t* table = p.c.block_table + r * p.c.bt_stride;
     const int64_t side = (int64_t)p.c.kv_heads * kPage * DIM;
     int err_bits = 0;
-    // The pages of tile j (-1: none, or outside the pool).
-    auto pages_of = [&](int j, int64_t* pg) {
+    uint32_t g = 0;                                // tiles so far
+    while (true) {
+      const volatile Piece& x = *next_piece();
+      if (failed || x.r < 0) break;
+      const int j0 = x.j0, j1 = x.j1, kvh = x.kvh;
+      const int32_t* table = p.c.block_table + x.r * p.c.bt_stride;
+      const int len = clamp_pos(p, x.raw_len);
+      const int min_vis = visible(p, x.raw_len, x.n, x.row0);
+      // The pages of tile j (-1: none, or outside the pool).
+      auto pages_of = [&](int j, int* pg) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        pg[h] = -1;
-        const int b = j * 2 + h;
-        if (j < nt && b * kPage < len) {
-          const int64_t v = table[b];
-          if (v >= 0 && v < p.c.num_pages)
-            pg[h] = v;
-          else
-            err_bits |= kErrPage;
+        for (int h = 0; h < 2; ++h) {
+          pg[h] = -1;
+          const int b = j * 2 + h;
+          if (j < j1 && b * kPage < len) {
+            const int v = table[b];
+            if (v >= 0 && v < p.c.num_pages)
+              pg[h] = v;
+            else
+              err_bits |= kErrPage;
+          }
         }
-      }
-    };
-    // Chunk e of this thread: position lt / RC + e * 128 / RC of the tile.
-    auto load = [&](const int64_t* pg, int64_t off, uint4* x) {
-#pragma unroll
-      for (int e = 0; e < NC; ++e) {
-        const int64_t page = pg[e / (NC / 2)];
-        x[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (page >= 0)
-          x[e] = __ldg(reinterpret_cast<const uint4*>(
-                           p.c.pages + ((page * 2) * p.c.kv_heads + kvh) * (int64_t)(kPage * DIM) +
-                           off) +
-                       lt + (e % (NC / 2)) * 128);
-      }
-    };
-    auto store = [&](uint8_t* dst, const uint4* x) {
-#pragma unroll
-      for (int e = 0; e < NC; ++e) {
-        const int row = lt / RC + e * (128 / RC), c = lt % RC;
-        const uint2 a = codes_to_f16(x[e].x), b = codes_to_f16(x[e].y),
-                    d = codes_to_f16(x[e].z), g = codes_to_f16(x[e].w);
-        uint8_t* at = dst + (c >> 2) * LY::kBlock;
-        const int ch = (c & 3) * 2;
-        *reinterpret_cast<uint4*>(at + row * 128 + ((ch ^ (row & 7)) << 4)) =
-            make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(at + row * 128 + (((ch + 1) ^ (row & 7)) << 4)) =
-            make_uint4(d.x, d.y, g.x, g.y);
-      }
-    };
-    uint4 kx[NC], vx[NC];
-    int64_t now[2], next[2];
-    float ks = 0.0f, vs = 1.0f;      // scales of page lt of the tile (threads 0 and 1)
-    auto scales_of = [&](const int64_t* pg) {
-      ks = 0.0f;
-      vs = 1.0f;
-      const int64_t page = lt == 0 ? pg[0] : pg[1];
-      if (lt < 2 && page >= 0) {
-        const int64_t part = page * 2 * p.c.kv_heads + kvh;
-        ks = p.c.scales[part];
-        vs = p.c.scales[part + p.c.kv_heads];
-      }
-    };
-    pages_of(0, now);
-    pages_of(1, next);
-    load(now, 0, kx);
-    load(now, side, vx);
-    scales_of(now);
-    for (int j = 0; j < nt; ++j) {
-      const int st = j & 1;
-      if (!__all_sync(0xffffffffu,
-                      j < 2 || mbar_wait_long(&bars[kKEmpty + st], ((j >> 1) - 1) & 1))) {
-        failed = true;
-        break;
-      }
-      store(smem + LY::kK + st * LY::kTileBytes, kx);
-      if (lt < 2)
-        meta[(j & 3) * 2 + lt] =
-            make_float4(ks, log2f(vs) + 3.0f, __fdiv_rn(0.125f, vs),
-                        (lt == 0 ? now[0] : now[1]) >= 0 ? 1.0f : 0.0f);
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kKFull + st]);
-      load(next, 0, kx);
-      scales_of(next);
-      if (!__all_sync(0xffffffffu,
-                      j < 2 || mbar_wait_long(&bars[kVEmpty + st], ((j >> 1) - 1) & 1))) {
-        failed = true;
-        break;
-      }
-      // Positions behind the context hold anything: zeros in their place (a
-      // weight of 0 times NaN is NaN). Where the CTA's rows see different
-      // lengths, NaN codes become 0 too, and are listed.
-      if ((j + 1) * kTile > min_vis) {
+      };
+      // Chunk e of this thread: position lt / RC + e * 128 / RC of the tile.
+      auto load = [&](const int* pg, int64_t off, uint4* v) {
 #pragma unroll
         for (int e = 0; e < NC; ++e) {
-          const int row = lt / RC + e * (128 / RC), pos = j * kTile + row;
-          uint32_t bits = 0u;
-          if (pos >= len) {
-            vx[e] = make_uint4(0u, 0u, 0u, 0u);
-          } else if (pos >= min_vis && has_nan_code(vx[e])) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&vx[e]);
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-              if (((w[u >> 2] >> (8 * (u & 3))) & 0x7Fu) == 0x7Fu) {
-                bits |= 1u << u;
-                w[u >> 2] &= ~(0xFFu << (8 * (u & 3)));
-              }
-            nan_tag[st] = j + 1;
-          }
-          reinterpret_cast<uint16_t*>(smem + LY::kNanMap + st * LY::kNanMapBytes)[row * RC + lt % RC] =
-              (uint16_t)bits;
+          const int64_t page = pg[e / (NC / 2)];
+          v[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (page >= 0)
+            v[e] = __ldg(reinterpret_cast<const uint4*>(
+                             p.c.pages +
+                             ((page * 2) * p.c.kv_heads + kvh) * (int64_t)(kPage * DIM) + off) +
+                         lt + (e % (NC / 2)) * 128);
         }
+      };
+      auto store = [&](uint8_t* dst, const uint4* v) {
+#pragma unroll
+        for (int e = 0; e < NC; ++e) {
+          const int row = lt / RC + e * (128 / RC), c = lt % RC;
+          const uint2 a = codes_to_f16(v[e].x), b = codes_to_f16(v[e].y),
+                      d = codes_to_f16(v[e].z), h = codes_to_f16(v[e].w);
+          uint8_t* at = dst + (c >> 2) * LY::kBlock;
+          const int ch = (c & 3) * 2;
+          *reinterpret_cast<uint4*>(at + row * 128 + ((ch ^ (row & 7)) << 4)) =
+              make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4*>(at + row * 128 + (((ch + 1) ^ (row & 7)) << 4)) =
+              make_uint4(d.x, d.y, h.x, h.y);
+        }
+      };
+      uint4 kx[NC], vx[NC];
+      int now[2], next[2];
+      float ks = 0.0f, vs = 1.0f;      // scales of page lt of the tile (threads 0 and 1)
+      auto scales_of = [&](const int* pg) {
+        ks = 0.0f;
+        vs = 1.0f;
+        const int64_t page = lt == 0 ? pg[0] : pg[1];
+        if (lt < 2 && page >= 0) {
+          const int64_t part = page * 2 * p.c.kv_heads + kvh;
+          ks = p.c.scales[part];
+          vs = p.c.scales[part + p.c.kv_heads];
+        }
+      };
+      pages_of(j0, now);
+      pages_of(j0 + 1, next);
+      load(now, 0, kx);
+      load(now, side, vx);
+      scales_of(now);
+      for (int j = j0; j < j1; ++j, ++g) {
+        const int st = (int)(g & 1);
+        if (!__all_sync(0xffffffffu,
+                        g < 2 || mbar_wait_long(&bars[kKEmpty + st], ((g >> 1) - 1) & 1))) {
+          failed = true;
+          break;
+        }
+        store(smem + LY::kK + st * LY::kTileBytes, kx);
+        if (lt < 2)
+          meta[(g & 3) * 2 + lt] =
+              make_float4(ks, log2f(vs) + 3.0f, __fdiv_rn(0.125f, vs),
+                          (lt == 0 ? now[0] : now[1]) >= 0 ? 1.0f : 0.0f);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kKFull + st]);
+        load(next, 0, kx);
+        scales_of(next);
+        if (!__all_sync(0xffffffffu,
+                        g < 2 || mbar_wait_long(&bars[kVEmpty + st], ((g >> 1) - 1) & 1))) {
+          failed = true;
+          break;
+        }
+        // Positions behind the context hold anything: zeros in their place (a
+        // weight of 0 times NaN is NaN). Where the item's rows see different
+        // lengths, NaN codes become 0 too, and are listed.
+        if ((j + 1) * kTile > min_vis) {
+#pragma unroll
+          for (int e = 0; e < NC; ++e) {
+            const int row = lt / RC + e * (128 / RC), pos = j * kTile + row;
+            uint32_t bits = 0u;
+            if (pos >= len) {
+              vx[e] = make_uint4(0u, 0u, 0u, 0u);
+            } else if (pos >= min_vis && has_nan_code(vx[e])) {
+              uint32_t w[4] = {vx[e].x, vx[e].y, vx[e].z, vx[e].w};
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if (((w[u >> 2] >> (8 * (u & 3))) & 0x7Fu) == 0x7Fu) {
+                  bits |= 1u << u;
+                  w[u >> 2] &= ~(0xFFu << (8 * (u & 3)));
+                }
+              vx[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              nan_tag[st] = g + 1;
+            }
+            reinterpret_cast<uint16_t*>(smem + LY::kNanMap +
+                                        st * LY::kNanMapBytes)[row * RC + lt % RC] = (uint16_t)bits;
+          }
+        }
+        store(smem + LY::kV + st * LY::kTileBytes, vx);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kVFull + st]);
+        load(next, side, vx);
+        now[0] = next[0];
+        now[1] = next[1];
+        pages_of(j + 2, next);
       }
-      store(smem + LY::kV + st * LY::kTileBytes, vx);
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kVFull + st]);
-      load(next, side, vx);
-      now[0] = next[0];
-      now[1] = next[1];
-      pages_of(j + 2, next);
+      if (failed) break;
+      piece_done();
     }
     if (err_bits && lt == 0 && p.c.err != nullptr) atomicOr(p.c.err, err_bits);
   } else {
     regs_dec<kRegsMma>();
-    if (warp == kMmaWarp && nt > 0) {
+    if (warp == kMmaWarp) {
       // -------------------------------------------------------- MMA issuer
       // (the whole warp; one lane issues)
       constexpr uint32_t idesc_s = make_idesc_f16(128, kTile, 0, 0);
@@ -491,63 +821,102 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
       const uint64_t k_desc = make_sw128_desc(sbase + LY::kK, 16, 1024);
       const uint64_t v_desc = make_sw128_desc(sbase + LY::kV, LY::kBlock, 1024);
       const bool leader = elect_one();
-      auto issue_s = [&](int m, uint64_t kd, uint64_t* k_empty) {
-        if (leader) {
+      uint32_t g = 0;                    // tiles of the CTA so far
+      uint32_t done[2] = {0u, 0u};       // tiles of each row tile
+      uint32_t items[2] = {0u, 0u};      // Q of each row tile
+      while (true) {
+        const volatile Piece& x = *next_piece();
+        if (failed || x.r < 0) break;
+        const int nt = x.j1 - x.j0;
+        const bool begins = x.j0 == 0;
+        const int mts = last_row_of(p, x.row0, x.n) - x.row0 >= kTile ? 2 : 1;
+        piece_done();
+        if (nt <= 0) continue;
+        auto issue_s = [&](int m, uint32_t t) {
+          const uint64_t kd = k_desc + (uint64_t)(((t & 1) * LY::kTileBytes) >> 4);
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < DIM / 16; ++k) {
-            const uint32_t off = (uint32_t)((k >> 2) * LY::kBlock + (k & 3) * 32);
-            mma_bf16_ss(tmem + LY::kS + m * kTile, q_desc + ((m * LY::kTileBytes + off) >> 4),
-                        kd + (off >> 4), idesc_s, k > 0 ? 1u : 0u);
+            for (int k = 0; k < DIM / 16; ++k) {
+              const uint32_t off = (uint32_t)((k >> 2) * LY::kBlock + (k & 3) * 32);
+              mma_bf16_ss(tmem + LY::kS + m * kTile, q_desc + ((m * LY::kTileBytes + off) >> 4),
+                          kd + (off >> 4), idesc_s, k > 0 ? 1u : 0u);
+            }
+            mma_commit(&bars[kSFull + m]);
+            if (m == mts - 1) mma_commit(&bars[kKEmpty + (t & 1)]);
           }
-          mma_commit(&bars[kSFull + m]);
-          if (m == mts - 1) mma_commit(k_empty);
-        }
-        __syncwarp();
-      };
-      auto issue_o = [&](int m, uint64_t vd, uint64_t* v_empty, bool first) {
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kS + m * kTile + k * 8,
-                       vd + ((k * 16 * 128) >> 4), idesc_o, k > 0 ? 1u : (first ? 0u : 1u));
-          mma_commit(&bars[kPvDone + m]);
-          if (m == mts - 1) mma_commit(v_empty);
-        }
-        __syncwarp();
-      };
-      failed = !mbar_wait_long(&bars[kQFull], 0) || !mbar_wait_long(&bars[kKFull], 0);
-      failed = __any_sync(0xffffffffu, failed);
-      if (!failed) {
-        tc_fence_after();
-        issue_s(0, k_desc, &bars[kKEmpty]);
-        if (mts == 2) issue_s(1, k_desc, &bars[kKEmpty]);
-      }
-      for (int j = 0; j < nt && !failed; ++j) {
-        const int st = j & 1, sn = st ^ 1;
-        const uint64_t vd = v_desc + (uint64_t)((st * LY::kTileBytes) >> 4);
-        const uint64_t kd = k_desc + (uint64_t)((sn * LY::kTileBytes) >> 4);
-        bool ok = mbar_wait_long(&bars[kVFull + st], (j >> 1) & 1);
+          __syncwarp();
+        };
+        // Waits are the warp's: one lane's failure is everyone's.
+        auto wait = [&](int bar, uint32_t phase) {
+          if (!failed && !__all_sync(0xffffffffu, mbar_wait_long(&bars[bar], phase & 1)))
+            failed = true;
+        };
+        // The first S of the piece, behind the last PV of the piece before.
+        wait(kKFull + (g & 1), g >> 1);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (m >= mts) break;
-          ok = ok && mbar_wait_long(&bars[kPFull + m], j & 1);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          wait(kQFull + m, items[m]);
+          if (done[m] != 0) wait(kPvDone + m, done[m] - 1);
+          ++items[m];
+          if (failed) break;
           tc_fence_after();
-          issue_o(m, vd, &bars[kVEmpty + st], j == 0);
-          if (j + 1 < nt) {
-            // The next S overwrites this P: only once PV has ended.
-            if (m == 0) ok = mbar_wait_long(&bars[kKFull + sn], ((j + 1) >> 1) & 1);
-            ok = ok && mbar_wait_long(&bars[kPvDone + m], j & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            issue_s(m, kd, &bars[kKEmpty + sn]);
+          issue_s(m, g);
+        }
+        for (int j = 0; j < nt && !failed; ++j, ++g) {
+          const uint64_t vd = v_desc + (uint64_t)(((g & 1) * LY::kTileBytes) >> 4);
+          const bool fresh = j == 0 && begins;
+          wait(kVFull + (g & 1), g >> 1);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (m >= mts) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              wait((half ? kPFull : kPHalf) + m, done[m]);
+              if (failed) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int k = 4 * (1 - half); k < 4 * (1 - half) + 4; ++k)
+                  mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kS + m * kTile + 64 + k * 8,
+                             vd + ((k * 16 * 128) >> 4), idesc_o,
+                             k != 4 || half ? 1u : (fresh ? 0u : 1u));
+                if (half) {
+                  mma_commit(&bars[kPvDone + m]);
+                  if (m == mts - 1) mma_commit(&bars[kVEmpty + (g & 1)]);
+                }
+              }
+              __syncwarp();
+            }
+            ++done[m];
+            if (j + 1 < nt && !failed) {
+              // The next S overwrites this P: only once PV has ended.
+              if (m == 0) wait(kKFull + ((g + 1) & 1), (g + 1) >> 1);
+              wait(kPvDone + m, done[m] - 1);
+              if (failed) break;
+              tc_fence_after();
+              issue_s(m, g + 1);
+            }
           }
         }
-        failed = !__all_sync(0xffffffffu, ok);
+        if (failed) break;
       }
       if (leader) mma_commit(&bars[kDrain]);
       __syncwarp();
       if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
+    } else if (warp == kMmaWarp + 1 && lane == 0) {
+      // ----------------------------------------------------- piece lookups
+      Scheduler sched(p);
+      for (uint32_t i = 0;; ++i) {
+        const Piece x = sched.next();
+        if (i >= 2 && !mbar_wait_long(&bars[kPieceEmpty + (i & 1)], ((i >> 1) - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        pieces[i & 1] = x;
+        mbar_arrive(&bars[kPieceFull + (i & 1)]);
+        if (x.r < 0) break;
+      }
     }
     __syncwarp();
   }
@@ -562,10 +931,33 @@ template <int DIM>
 cudaError_t launch(const Params& p, int dev, cudaStream_t stream) {
   static PerDeviceOnce once;
   auto kern = kv8_prefill_kernel<DIM>;
-  const cudaError_t e = set_max_dynamic_smem(once, dev, kern, Layout<DIM>::kSmem);
+  cudaError_t e = set_max_dynamic_smem(once, dev, kern, Layout<DIM>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)(p.units * p.c.kv_heads)), dim3(kThreads),
-                    Layout<DIM>::kSmem, stream, 1u, p);
+  e = launch_pdl(kv8_prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, 1u, p);
+  if (e != cudaSuccess) return e;
+  const int64_t items = p.units * p.c.kv_heads;
+  int64_t ctas = kv8_sm_count(dev);
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  if (ctas > items) ctas = items;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Layout<DIM>::kSmem, stream, 1u, p);
+}
+
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t carve(Plan* plan, void* base, int64_t units, int dim) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* x = base ? static_cast<uint8_t*>(base) + at : nullptr;
+    at += pad256(bytes);
+    return x;
+  };
+  Plan r;
+  r.first = reinterpret_cast<int64_t*>(take((size_t)(units + 1) * 8));
+  r.info = reinterpret_cast<UnitInfo*>(take((size_t)units * sizeof(UnitInfo)));
+  r.flags = reinterpret_cast<int32_t*>(take(kMaxCtas * 4));
+  r.state = take((size_t)kMaxCtas * state_bytes(dim));
+  if (plan) *plan = r;
+  return at;
 }
 
 }  // namespace
@@ -574,7 +966,11 @@ int64_t kv8_prefill_units(int64_t tokens, int64_t requests, int group) {
   return tokens * group / kRows + requests;
 }
 
-size_t kv8_prefill_workspace_bytes(int64_t, int64_t, int, int, int) { return 0; }
+size_t kv8_prefill_workspace_bytes(int64_t tokens, int64_t requests, int heads, int kv_heads,
+                                   int dim) {
+  if (tokens == 0 || requests == 0) return 0;
+  return carve(nullptr, nullptr, kv8_prefill_units(tokens, requests, heads / kv_heads), dim);
+}
 
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream) {
   int dev = 0;
@@ -592,6 +988,7 @@ cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream) {
   p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   p.c = a.c;
+  carve(&p.plan, a.workspace, p.units, a.c.dim);
   return a.c.dim == 128 ? launch<128>(p, dev, stream) : launch<64>(p, dev, stream);
 }
 

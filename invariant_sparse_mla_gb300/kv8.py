@@ -141,7 +141,7 @@ def _outputs(q, d, dev, out, lse):
     if q.shape[-1] != d:
         raise ValueError(f"q must have head dim {d}, got {q.shape[-1]}")
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _arg(out, "out", torch.bfloat16, dev)
         if out.shape != q.shape:
@@ -170,8 +170,8 @@ def kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=N
     out, lse = _outputs(q, d, dev, out, lse)
     L = lib()
     if workspace is None:
-        workspace = kv_pages.new_empty(
-            (r and L.ds_kv8_decode_workspace_size(r, nn, h, hk, d, width) or 256,))
+        need = r and L.ds_kv8_decode_workspace_size(r, nn, h, hk, d, width)
+        workspace = torch.empty(need or 256, dtype=torch.uint8, device=dev)
     else:
         _arg(workspace, "workspace", torch.uint8, dev)
     _run(dev, L.ds_kv8_decode, q.data_ptr(), qs, kv_pages.data_ptr(), kv_scales.data_ptr(), pages,
@@ -198,7 +198,7 @@ def kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, 
     L = lib()
     if workspace is None:
         need = t and L.ds_kv8_prefill_workspace_size(t, n, h, hk, d)
-        workspace = kv_pages.new_empty((need,)) if need else None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _arg(workspace, "workspace", torch.uint8, dev)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())

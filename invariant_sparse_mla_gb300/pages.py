@@ -54,8 +54,8 @@ def _list(t, name, dev, n=None):
 def _workspace(workspace, refcounts, n):
     if workspace is None:
         need = lib().ds_pages_workspace_size(refcounts.shape[0], n)
-        workspace = refcounts.new_empty((need // 4 or 64,))
-        return workspace, workspace.data_ptr(), 4 * workspace.shape[0]
+        workspace = torch.empty(need or 256, dtype=torch.uint8, device=refcounts.device)
+        return workspace, workspace.data_ptr(), need
     _arg(workspace, "workspace", torch.uint8, refcounts.device)
     return workspace, workspace.data_ptr(), workspace.numel()
 
@@ -110,17 +110,17 @@ def pages_compact(pools, refcounts, block_table, lens, block_table_out=None, ref
     dev, state = _state(refcounts, block_table, lens)
     num_pages = refcounts.shape[0]
     if block_table_out is None:
-        block_table_out = block_table.new_empty(block_table.shape)
+        block_table_out = torch.empty_like(block_table)
     else:
         _arg(block_table_out, "block_table_out", torch.int32, dev, 2)
         if block_table_out.shape != block_table.shape:
             raise ValueError(f"block_table_out must be {tuple(block_table.shape)}")
     if refcounts_out is None:
-        refcounts_out = refcounts.new_empty((num_pages,))
+        refcounts_out = torch.empty_like(refcounts)
     else:
         _list(refcounts_out, "refcounts_out", dev, num_pages)
     if num_live is None:
-        num_live = refcounts.new_empty((1,))
+        num_live = torch.empty(1, dtype=torch.int32, device=dev)
     else:
         _list(num_live, "num_live", dev, 1)
     workspace, ws, ws_bytes = _workspace(workspace, refcounts, 0)
