@@ -239,10 +239,10 @@ int ds_kv8_prefill(const void* q, int64_t q_stride, int64_t num_tokens,
   if (st == DS_OK) st = check_tokens(fn, num_tokens);
   if (st != DS_OK) return st;
   if (num_tokens == 0 || num_requests == 0) return report_ok();
-  if (dsmla::kv8_prefill_units(num_tokens, num_requests, num_heads / num_kv_heads) >
-      (int64_t)INT32_MAX / num_kv_heads)
-    return report_error(DS_ERR_UNSUPPORTED, "%s: num_tokens=%lld is too large for one launch", fn,
-                        (long long)num_tokens);
+  if (num_tokens > (int64_t)INT32_MAX / (num_heads / num_kv_heads) - 256)
+    return report_error(DS_ERR_UNSUPPORTED, "%s: num_tokens=%lld is too large with %d query heads "
+                        "a kv head (below 2^31 rows)", fn, (long long)num_tokens,
+                        num_heads / num_kv_heads);
   const size_t need = dsmla::kv8_prefill_workspace_bytes(num_tokens, num_requests, num_heads,
                                                          num_kv_heads, head_dim);
   st = check_ptrs(fn, {{q, "q", 16},

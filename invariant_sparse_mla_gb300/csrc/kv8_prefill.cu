@@ -53,17 +53,20 @@ constexpr int kRows = 256;               // query rows per CTA
 constexpr int kThreads = 512;
 constexpr int kLoaderWarp = 8, kMmaWarp = 12;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-// Registers: 512 threads launch with 128 each; 256 * 152 + 128 * 128 +
-// 128 * 80 = 65536 = 512 * 128.
-constexpr int kRegsSoftmax = 152, kRegsMma = 80;
+// Registers: 512 threads launch with 128 each; 256 * 160 + 128 * 120 +
+// 128 * 72 = 65536 = 512 * 128.
+constexpr int kRegsSoftmax = 160, kRegsLoader = 120, kRegsMma = 72;
 
 constexpr int kMaxCtas = 192;
 
 // What the first kernel writes: item (unit u of one kv head) has weight
-// first[u + 1] - first[u] tiles (1 for rows that see nothing, 0 for none).
+// first[u + 1] - first[u]: its tiles and kItemCost for its queries and outputs
+// (about that many tiles' time), 0 for a unit without rows.
+constexpr int kItemCost = 5;
+// (Rows of a request are counted in 31 bits: num_tokens * group < 2^31.)
 struct alignas(32) UnitInfo {
-  int64_t row0;          // first row of the request's rows
   int32_t r, t0, n;      // request, its first token, its tokens
+  int32_t row0;          // first row of the request's rows; < 0: none
   int32_t raw_len;
 };
 struct Plan {
@@ -94,9 +97,13 @@ struct Layout {
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // TMEM: S (P over its upper half) and O of both row tiles.
+  // TMEM columns: S and O of both row tiles and, where there is room, P; else P
+  // lies over the upper half of S.
+  static constexpr bool kApart = DIM == 64;
   static constexpr uint32_t kS = 0, kO = 2 * kTile;
-  static constexpr uint32_t kCols = 2 * kTile + 2 * DIM <= 256 ? 256u : 512u;
+  static constexpr uint32_t kP = kApart ? kO + 2 * DIM : kS + 64, kPStep = kApart ? 64 : kTile;
+  static constexpr uint32_t kCols = 512u;
+  static_assert(kApart ? kP + 2 * kPStep <= kCols : kO + 2 * DIM <= kCols, "TMEM columns");
 };
 
 enum Bar {
@@ -109,17 +116,18 @@ enum Bar {
   kPHalf = 12,      // 2: the row tile's softmax threads (positions 64-127 of P)
   kPFull = 14,      // 2: the same (all of P)
   kPvDone = 16,     // 2: commit
-  kPieceFull = 18,  // 2: the scheduling lane
-  kPieceEmpty = 20, // 2: every thread that reads pieces
-  kDrain = 22,
-  kNumBars = 23
+  kPvHalf = 18,     // 2: commit, PV of positions 64-127
+  kPieceFull = 20,  // 2: the scheduling lane
+  kPieceEmpty = 22, // 2: every thread that reads pieces
+  kSFree = 24,      // 2: the row tile's softmax threads have read S (P apart)
+  kDrain = 26,
+  kNumBars = 27
 };
 constexpr int kPieceReaders = 256 + 128 + 32;
 
 // One run of tiles [j0, j1) of an item. r < 0 ends the list.
 struct alignas(64) Piece {
-  int64_t row0;
-  int32_t r, t0, n, raw_len;
+  int32_t r, t0, n, row0, raw_len;
   int32_t kvh, nt, j0, j1;
   int32_t take, give;    // state slots to continue from / to hand over to, or -1
 };
@@ -143,15 +151,15 @@ __device__ __forceinline__ int clamp_pos(const Params& p, int64_t v) {
   return (int)(v < 0 ? 0 : (v > most ? most : v));
 }
 // Positions that a row of the request sees.
-__device__ __forceinline__ int visible(const Params& p, int raw_len, int n, int64_t row) {
-  return clamp_pos(p, raw_len - n + 1 + row / p.group);
+__device__ __forceinline__ int visible(const Params& p, int raw_len, int n, int row) {
+  return clamp_pos(p, (int64_t)raw_len - n + 1 + row / p.group);
 }
-__device__ __forceinline__ int64_t last_row_of(const Params& p, int64_t row0, int n) {
-  const int64_t rows = (int64_t)n * p.group;
-  return row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
+__device__ __forceinline__ int last_row_of(const Params& p, int row0, int n) {
+  const int left = n * p.group - row0;
+  return row0 + (left < kRows ? left : kRows) - 1;
 }
 // Tiles of an item.
-__device__ __forceinline__ int item_tiles(const Params& p, int raw_len, int n, int64_t row0) {
+__device__ __forceinline__ int item_tiles(const Params& p, int raw_len, int n, int row0) {
   return (visible(p, raw_len, n, last_row_of(p, row0, n)) + kTile - 1) / kTile;
 }
 
@@ -195,11 +203,12 @@ __global__ void __launch_bounds__(1024) kv8_prefill_plan_kernel(const Params p) 
       i.t0 = (int)t0;
       i.n = (int)(t1 > t0 ? t1 - t0 : 0);
       i.raw_len = raw;
-      i.row0 = (u - (t0 * p.group / kRows + r)) * kRows;
+      const int64_t row0 = (u - (t0 * p.group / kRows + r)) * kRows;
+      i.row0 = -1;
       int w = 0;
-      if (i.row0 >= 0 && i.row0 < (int64_t)i.n * p.group) {
-        w = item_tiles(p, raw, i.n, i.row0);
-        if (w == 0) w = 1;
+      if (row0 >= 0 && row0 < (int64_t)i.n * p.group) {
+        i.row0 = (int)row0;
+        w = item_tiles(p, raw, i.n, i.row0) + kItemCost;
       }
       p.plan.info[u] = i;
       p.plan.first[u] = sum;     // within the thread's run; completed below
@@ -227,18 +236,11 @@ __global__ void __launch_bounds__(1024) kv8_prefill_plan_kernel(const Params p) 
 // The pieces of CTA `blockIdx.x`, one after the other.
 struct Scheduler {
   const Params& p;
-  int64_t per_head, lo, hi;       // tiles of a kv head; the CTA's run
+  int64_t per_head, lo, hi;       // weight of a kv head; the CTA's run
   int64_t i0, i1, at;             // items kvh * units + u of its ends; the next one
-  bool first_cut, last_cut;
   int phase;
 
-  __device__ int64_t start_of(int64_t i) const {
-    return i / p.units * per_head + p.plan.first[i % p.units];
-  }
-  __device__ int64_t weight_of(int64_t i) const {
-    return p.plan.first[i % p.units + 1] - p.plan.first[i % p.units];
-  }
-  // The item that holds tile x.
+  // The item that holds weight x.
   __device__ int64_t find(int64_t x) const {
     const int64_t head = x / per_head;
     x -= head * per_head;
@@ -261,48 +263,63 @@ struct Scheduler {
     if (lo >= hi) return;
     i0 = find(lo);
     i1 = find(hi - 1);
-    first_cut = start_of(i0) < lo;
-    last_cut = start_of(i1) + weight_of(i1) > hi;
     at = i0;
-    phase = i0 != i1 && last_cut ? 0 : 1;
+    phase = 0;
   }
+  // The CTA's tiles of item i: from its own start where the run begins in the
+  // item's cost, none where it ends there. r < 0: no piece.
   __device__ Piece piece(int64_t i) const {
-    const UnitInfo u = p.plan.info[i % p.units];
-    const int64_t s = start_of(i), e = s + weight_of(i);
     Piece x;
-    x.row0 = u.row0;
-    x.r = u.r;
-    x.t0 = u.t0;
-    x.n = u.n;
-    x.raw_len = u.raw_len;
+    x.r = -1;
+    const int64_t u = i % p.units;
+    const int64_t s = i / p.units * per_head + p.plan.first[u];
+    const int nt = (int)(p.plan.first[u + 1] - p.plan.first[u]) - kItemCost;
+    if (nt < 0) return x;
+    auto tile_of = [&](int64_t w) {
+      const int64_t t = w - s - kItemCost;
+      return (int)(t < 0 ? 0 : (t > nt ? nt : t));
+    };
+    x.j0 = tile_of(lo);
+    x.j1 = tile_of(hi);
+    if (nt > 0 ? x.j0 >= x.j1 : (s < lo || s >= hi)) return x;
+    const UnitInfo info = p.plan.info[u];
+    x.r = info.r;
+    x.row0 = info.row0;
+    x.t0 = info.t0;
+    x.n = info.n;
+    x.raw_len = info.raw_len;
     x.kvh = (int)(i / p.units);
-    x.nt = item_tiles(p, u.raw_len, u.n, u.row0);
-    x.j0 = (int)(lo > s ? lo - s : 0);
-    x.j1 = (int)((hi < e ? hi : e) - s);
-    if (x.j1 > x.nt) x.j1 = x.nt;     // rows that see nothing: weight 1, no tile
-    x.take = lo > s ? (int)blockIdx.x - 1 : -1;
-    x.give = hi < e ? (int)blockIdx.x : -1;
+    x.nt = nt;
+    x.take = x.j0 > 0 ? (int)blockIdx.x - 1 : -1;
+    x.give = x.j1 < nt ? (int)blockIdx.x : -1;
     return x;
   }
+  // First what the next CTA waits for, last what the CTA before has begun.
   __device__ Piece next() {
-    if (phase == 0) {                 // what the next CTA waits for
-      phase = 1;
-      return piece(i1);
-    }
-    if (phase == 1) {
-      while (at <= i1) {
-        const int64_t i = at++;
-        if (weight_of(i) == 0) continue;
-        if (i0 != i1 && ((i == i0 && first_cut) || (i == i1 && last_cut))) continue;
-        return piece(i);
-      }
-      phase = 2;
-    }
-    if (phase == 2) {                 // what the CTA before has begun
-      phase = 3;
-      if (i0 != i1 && first_cut) return piece(i0);
-    }
     Piece x;
+    if (phase == 0) {
+      phase = 1;
+      if (i1 != i0) {
+        x = piece(i1);
+        if (x.r >= 0 && x.give >= 0) return x;
+      }
+    }
+    while (phase == 1) {
+      if (at > i1) {
+        phase = 2;
+        break;
+      }
+      x = piece(at++);
+      if (x.r < 0 || (i0 != i1 && (x.take >= 0 || x.give >= 0))) continue;
+      return x;
+    }
+    if (phase == 2) {
+      phase = 3;
+      if (i0 != i1) {
+        x = piece(i0);
+        if (x.r >= 0 && x.take >= 0) return x;
+      }
+    }
     x.r = -1;
     return x;
   }
@@ -345,9 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i < kKEmpty || (i >= kVFull && i < kVEmpty) || (i >= kPHalf && i < kPvDone))
+      if (i < kKEmpty || (i >= kVFull && i < kVEmpty) || (i >= kPHalf && i < kPvDone) ||
+          (i >= kSFree && i < kDrain))
         count = 128u;
-      if (i >= kPieceEmpty && i < kDrain) count = kPieceReaders;
+      if (i >= kPieceEmpty && i < kSFree) count = kPieceReaders;
       mbar_init(&bars[i], count);
     }
     mbar_fence_init();
@@ -386,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + LY::kS + m * kTile;
     const uint32_t t_o = tmem + lane_base + LY::kO + m * DIM;
+    const uint32_t t_p = tmem + lane_base + LY::kP + m * LY::kPStep;
     uint16_t* const row_bits =
         reinterpret_cast<uint16_t*>(smem + LY::kRowNan) + (m * kTile + row) * (DIM / 16);
     uint32_t tiles = 0;        // tiles of this row tile so far
@@ -393,40 +412,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     while (true) {
       const volatile Piece& x = *next_piece();
       if (failed || x.r < 0) break;
-      // Row of the request, whether it and its row tile exist, and its q and out.
-      auto grow = [&]() { return x.row0 + m * kTile + row; };
-      auto exists = [&]() { return grow() < (int64_t)x.n * p.group; };
-      auto token = [&]() { return x.t0 + grow() / p.group; };
-      auto head = [&]() { return x.kvh * p.group + (int)(grow() % p.group); };
-      const bool any = x.row0 + m * kTile < (int64_t)x.n * p.group;
-      const int vis = exists() ? visible(p, x.raw_len, x.n, grow()) : 0;
+      const int first = x.row0 + m * kTile;            // rows of the row tile
+      const int rows = x.n * p.group - first;          // at most 128 of them exist
+      const bool any = rows > 0;
+      const int vis = row < rows ? visible(p, x.raw_len, x.n, first + row) : 0;
       const int min_vis = visible(p, x.raw_len, x.n, x.row0);
+      // Element offset of a row of this warp in q (stride q_stride) or out.
+      auto offset = [&](int i, int64_t stride) {
+        const int rr = first + (warp & 3) * 32 + i;
+        return (x.t0 + rr / p.group) * stride + (x.kvh * p.group + rr % p.group) * DIM;
+      };
+      constexpr int RL = DIM / 8, RI = 32 / RL;        // lanes of a row; rows of a step
+      const int sub = lane / RL, ch = lane % RL;       // row of the step, 16-byte chunk
+      const int left = rows - (warp & 3) * 32;         // rows of this warp that exist
       float f = 0.0f;
       if (any && x.j1 > x.j0) {
-        const bool active = exists();
-        // The row's q times a power of two, in f16.
-        uint4 v[DIM / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + token() * p.q_stride + head() * DIM);
+        // The rows' q, each times a power of two of its own, in f16. A warp does
+        // its 32 rows, RI at a time; lane i then keeps row i's factor.
+        uint4 v[RL];
 #pragma unroll
-        for (int i = 0; i < DIM / 8; ++i) v[i] = active ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        uint32_t top = 0u;   // largest magnitude bits (NaN above infinity)
+        for (int i = 0; i < RL; ++i) {
+          const int rr = i * RI + sub;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < left)
+            v[i] = *reinterpret_cast<const uint4*>(p.q + offset(rr, p.q_stride) + ch * 8);
+        }
+        uint8_t* dst = smem + LY::kQ + m * LY::kTileBytes + (ch >> 3) * LY::kBlock;
 #pragma unroll
-        for (int i = 0; i < DIM / 8; ++i) {
+        for (int i = 0; i < RL; ++i) {
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t top = 0u;   // largest magnitude bits (NaN above infinity)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             top = max(top, max((w[u] << 16) & 0x7FFFFFFFu, w[u] & 0x7FFF0000u));
-        }
-        // Largest |q| 2^k in [2^14, 2^15); 2^k stays a normal float.
-        int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
-        k = k > 120 ? 120 : (k < -120 ? -120 : k);
-        const float up = copysignf(__uint_as_float((uint32_t)(k + 127) << 23), p.scale_log2);
-        f = top >= 0x7F800000u ? NAN
-                               : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
-        uint8_t* dst = smem + LY::kQ + m * LY::kTileBytes;
 #pragma unroll
-        for (int i = 0; i < DIM / 8; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int o = RL / 2; o > 0; o >>= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // Largest |q| 2^k in [2^14, 2^15); 2^k stays a normal float.
+          int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
+          k = k > 120 ? 120 : (k < -120 ? -120 : k);
+          const float up = copysignf(__uint_as_float((uint32_t)(k + 127) << 23), p.scale_log2);
+          const float fr = top >= 0x7F800000u
+                               ? NAN
+                               : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
+          const float mine = __shfl_sync(0xffffffffu, fr, (lane % RI) * RL);
+          if (lane / RI == i) f = mine;
           uint32_t h[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -434,14 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
                                                 __uint_as_float(w[u] & 0xFFFF0000u) * up);
             h[u] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * LY::kBlock + swz<128>(row, (i & 7) * 16)) =
+          *reinterpret_cast<uint4*>(
+              dst + swz<128>((warp & 3) * 32 + i * RI + sub, (ch & 7) * 16)) =
               make_uint4(h[0], h[1], h[2], h[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars[kQFull + m]);
       }
       float ref = 0.0f, l = 0.0f;
-      bool unset = true, row_nan = false;
+      bool unset = vis > 0, row_nan = false;   // (a row that sees nothing needs none)
       if (x.take >= 0) {
         // Continue from the CTA before: it does this piece first.
         const uint8_t* st = p.plan.state + x.take * state_bytes(DIM);
@@ -490,27 +521,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           break;
         }
         tc_fence_after();
-        // The row's largest score of each page, 64 columns at a time (a page has
-        // one scale, so the scores themselves compare), then the weights:
-        // positions 64-127 from the registers that hold them, 0-63 read again.
-        // P goes over the upper half of S, which is in registers by then.
+        // 64 columns (one page, one scale) at a time, positions 64-127 first: P
+        // may go over the upper half of S, which is in registers by then.
         float2 s[32];
         float* const s1 = reinterpret_cast<float*>(s);
         const float4 mt0 = meta[(g & 3) * 2], mt1 = meta[(g & 3) * 2 + 1];
         // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
         const int end0 = mt0.w != 0.0f ? vis - pos0 : 0, end1 = mt1.w != 0.0f ? vis - pos0 - 64 : 0;
-        auto load = [&](int half) {
+        const float g0 = f * mt0.x, g1 = f * mt1.x;
+        // s = exponents relative to the reference; returns the largest.
+        auto exponents = [&](int half) {
           tmem_ld32(t_s + 64 * half, s1);
           tmem_ld32(t_s + 64 * half + 32, s1 + 32);
+          const float gg = half ? g1 : g0, cc = (half ? mt1.y : mt0.y) - ref;
+          const float2 g2 = make_float2(gg, gg), c2 = make_float2(cc, cc);
+          const int end = half ? end1 : end0;
           tmem_fence<64>(s1);
-        };
-        auto hide = [&](int end) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = fma2(s[i], g2, c2);
           if (end < 64) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) s1[i] = i < end ? s1[i] : -INFINITY;
           }
-        };
-        auto largest = [&]() {
           float top[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) top[u] = fmaxf(s1[u], s1[4 + u]);
@@ -520,27 +552,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             for (int u = 0; u < 4; ++u) top[u] = fmaxf(fmaxf(top[u], s1[i + u]), s1[i + 4 + u]);
           return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         };
-        const float g0 = f * mt0.x, g1 = f * mt1.x;
-        load(0);
-        hide(end0);
-        const float top0 = largest();
-        load(1);
-        hide(end1);
-        const float top1 = largest();
-        // (-inf times a product of scales that is 0 would be NaN.)
-        float ymax = top0 > -INFINITY ? __fmaf_rn(top0, g0, mt0.y - ref) : -INFINITY;
-        if (top1 > -INFINITY) ymax = fmaxf(ymax, __fmaf_rn(top1, g1, mt1.y - ref));
-        const bool move = unset ? ymax > -INFINITY : ymax > 15.0f;
-        if (__any_sync(0xffffffffu, move)) {
-          const float by = move ? ymax - 3.0f : 0.0f;
+        // Moves the reference of rows with `move` to their largest, y, and the sums
+        // and outputs so far with it. O holds the tiles before (PV of the last
+        // may still run) and, at half 0, this tile's half 1.
+        auto rebase = [&](bool move, float y, bool half1_in) {
+          const float by = move ? y - 3.0f : 0.0f;
           const float al = move ? (unset ? 0.0f : ex2(-by)) : 1.0f;
           if (move) {
             ref += by;
             l *= al;
             unset = false;
           }
-          // (S of tile j was issued behind the end of PV of tile j - 1.)
-          if (j > 0 && __any_sync(0xffffffffu, al != 1.0f)) {
+          if ((j > 0 || half1_in) && __any_sync(0xffffffffu, al != 1.0f)) {
+            bool ok = true;
+            if (half1_in)
+              ok = mbar_wait_long(&bars[kPvHalf + m], tiles & 1);
+            else if (j > x.j0)
+              ok = mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) failed = true;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < DIM; c += 16) {
               float o[16];
@@ -551,32 +581,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
               for (int i = 0; i < 16; i += 4) tmem_st4(t_o + c + i, o + i);
             }
+            tmem_wait_st();
           }
+        };
+        if (__any_sync(0xffffffffu, unset)) {
+          const float y = fmaxf(exponents(0), exponents(1));
+          rebase(unset ? y > -INFINITY : y > 15.0f, y, false);
         }
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
-          if (half == 0) load(0);
-          const int end = half ? end1 : end0;
-          const float gg = half ? g1 : g0, cc = (half ? mt1.y : mt0.y) - ref;
-          const float2 g2 = make_float2(gg, gg), c2 = make_float2(cc, cc);
-          float2 sum = make_float2(0.0f, 0.0f);
-          // (Hidden scores of half 1 are -inf already; hide() follows the product
-          // with the scales, which may be 0.)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = fma2(s[i], g2, c2);
-          hide(end);
-#pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t h[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = make_float2(ex2(s[c + i].x), ex2(s[c + i].y));
-              sum = add2(sum, e);
-              const __half2 w = __floats2half2_rn(e.x, e.y);
-              h[i] = *reinterpret_cast<const uint32_t*>(&w);
-            }
-            tmem_st16u(t_s + 64 + 32 * half + c, h);
+          // Rarely a weight would pass 2^15: the exponents again, with a new
+          // reference.
+          while (true) {
+            const float y = exponents(half);
+            const bool move = y > 15.0f;
+            if (!__any_sync(0xffffffffu, move)) break;
+            rebase(move, y, half == 0);
           }
+          if (LY::kApart && half == 0) {
+            tc_fence_before();
+            mbar_arrive(&bars[kSFree + m]);
+          }
+          uint32_t h[32];
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 e = make_float2(ex2(s[i].x), ex2(s[i].y));
+            sum = add2(sum, e);
+            const __half2 w = __floats2half2_rn(e.x, e.y);
+            h[i] = *reinterpret_cast<const uint32_t*>(&w);
+          }
+          // (The columns of P apart are free once PV of the last tile has ended; S
+          // over P was issued behind that.)
+          if (LY::kApart && half == 1 && tiles > 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1)))
+              failed = true;
+            tc_fence_after();
+          }
+          tmem_st16u(t_p + 32 * half, h);
+          tmem_st16u(t_p + 16 + 32 * half, h + 16);
           l = __fmaf_rn(sum.x + sum.y, half ? mt1.z : mt0.z, l);
           if (half == 1) {
             tmem_wait_st();
@@ -644,41 +687,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         piece_done();
         continue;
       }
-      const bool active = exists();
-      const int64_t at = token() * p.heads + head();
+      // Outputs by way of the row tile's Q buffer (its last S is long done), so
+      // that rows are written whole.
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(0.125f, l);
-      __nv_bfloat16* dst = p.out + at * DIM;
-#pragma unroll
+      uint8_t* stage = smem + LY::kQ + m * LY::kTileBytes;
+#pragma unroll 1
       for (int c = 0; c < DIM; c += 32) {
         float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
         if (x.nt > 0) {
           tmem_ld32(t_o + c, o);
           tmem_fence<32>(o);
         }
-        uint32_t h[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a = l == 0.0f ? 0.0f : o[2 * i] * inv, b = l == 0.0f ? 0.0f : o[2 * i + 1] * inv;
-          if (row_nan) {
-            const int d = c + 2 * i;
-            if ((row_bits[d >> 4] >> (d & 15)) & 1) a = NAN;
-            if ((row_bits[d >> 4] >> ((d & 15) + 1)) & 1) b = NAN;
-          }
-          const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
-          h[i] = *reinterpret_cast<const uint32_t*>(&y);
+        for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0.0f : o[i] * inv;
+        if (row_nan) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if ((row_bits[(c + i) >> 4] >> (i & 15)) & 1) o[i] = NAN;
         }
-        if (active) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(dst + c)[i] =
-                make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * i + 2 * u], o[8 * i + 2 * u + 1]);
+            h[u] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          *reinterpret_cast<uint4*>(stage + (c >> 6) * LY::kBlock +
+                                    swz<128>(row, ((c >> 3) & 7) * 16 + i * 16)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
-      if (active) p.lse[at] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < RL; ++i) {
+        const int rr = i * RI + sub;
+        const uint4 y = *reinterpret_cast<const uint4*>(
+            stage + (ch >> 3) * LY::kBlock + swz<128>((warp & 3) * 32 + rr, (ch & 7) * 16));
+        if (rr < left)
+          *reinterpret_cast<uint4*>(p.out + offset(rr, (int64_t)p.heads * DIM) + ch * 8) = y;
+      }
+      __syncwarp();
+      if (lane < left)
+        p.lse[offset(lane, (int64_t)p.heads * DIM) / DIM] =
+            l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
       piece_done();
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ loader
+    regs_dec<kRegsLoader>();
     constexpr int NC = kTile * DIM / 16 / 128;     // 16-code chunks per thread and tile
     constexpr int RC = DIM / 16;                   // chunks per position
     const int lt = tid - kLoaderWarp * 32;
@@ -726,12 +785,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           const int row = lt / RC + e * (128 / RC), c = lt % RC;
           const uint2 a = codes_to_f16(v[e].x), b = codes_to_f16(v[e].y),
                       d = codes_to_f16(v[e].z), h = codes_to_f16(v[e].w);
-          uint8_t* at = dst + (c >> 2) * LY::kBlock;
-          const int ch = (c & 3) * 2;
-          *reinterpret_cast<uint4*>(at + row * 128 + ((ch ^ (row & 7)) << 4)) =
-              make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(at + row * 128 + (((ch + 1) ^ (row & 7)) << 4)) =
-              make_uint4(d.x, d.y, h.x, h.y);
+          // Lanes of the second column block store their upper 16 bytes first:
+          // eight lanes then write eight different bank groups.
+          uint8_t* at = dst + (c >> 2) * LY::kBlock + row * 128;
+          const int o = (c >> 2) & 1, ch = (c & 3) * 2;
+          const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, h.x, h.y);
+          *reinterpret_cast<uint4*>(at + (((ch + o) ^ (row & 7)) << 4)) = o ? hi : lo;
+          *reinterpret_cast<uint4*>(at + (((ch + 1 - o) ^ (row & 7)) << 4)) = o ? lo : hi;
         }
       };
       uint4 kx[NC], vx[NC];
@@ -829,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         if (failed || x.r < 0) break;
         const int nt = x.j1 - x.j0;
         const bool begins = x.j0 == 0;
-        const int mts = last_row_of(p, x.row0, x.n) - x.row0 >= kTile ? 2 : 1;
+        const int mts = x.n * p.group - x.row0 > kTile ? 2 : 1;
         piece_done();
         if (nt <= 0) continue;
         auto issue_s = [&](int m, uint32_t t) {
@@ -857,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         for (int m = 0; m < 2; ++m) {
           if (m >= mts) break;
           wait(kQFull + m, items[m]);
-          if (done[m] != 0) wait(kPvDone + m, done[m] - 1);
+          if (!LY::kApart && done[m] != 0) wait(kPvDone + m, done[m] - 1);
           ++items[m];
           if (failed) break;
           tc_fence_after();
@@ -872,16 +932,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             if (m >= mts) break;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+              if (LY::kApart && half == 1 && j + 1 < nt) {
+                // The next S as soon as this one is read. (Not ahead of PV's first
+                // half: softmax may wait for that before it has read all of S.)
+                if (m == 0) wait(kKFull + ((g + 1) & 1), (g + 1) >> 1);
+                wait(kSFree + m, done[m]);
+                if (failed) break;
+                tc_fence_after();
+                issue_s(m, g + 1);
+              }
               wait((half ? kPFull : kPHalf) + m, done[m]);
               if (failed) break;
               tc_fence_after();
               if (leader) {
 #pragma unroll
                 for (int k = 4 * (1 - half); k < 4 * (1 - half) + 4; ++k)
-                  mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kS + m * kTile + 64 + k * 8,
+                  mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kP + m * LY::kPStep + k * 8,
                              vd + ((k * 16 * 128) >> 4), idesc_o,
                              k != 4 || half ? 1u : (fresh ? 0u : 1u));
-                if (half) {
+                if (!half) {
+                  mma_commit(&bars[kPvHalf + m]);
+                } else {
                   mma_commit(&bars[kPvDone + m]);
                   if (m == mts - 1) mma_commit(&bars[kVEmpty + (g & 1)]);
                 }
@@ -889,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
               __syncwarp();
             }
             ++done[m];
-            if (j + 1 < nt && !failed) {
+            if (!LY::kApart && j + 1 < nt && !failed) {
               // The next S overwrites this P: only once PV has ended.
               if (m == 0) wait(kKFull + ((g + 1) & 1), (g + 1) >> 1);
               wait(kPvDone + m, done[m] - 1);

@@ -76,6 +76,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // warp leaves the issue slots to the others.
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity,
                                                uint64_t limit_cycles = 1ull << 32) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = clock64();
   while (true) {
     uint32_t ok;
