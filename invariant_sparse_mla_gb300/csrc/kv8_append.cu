@@ -9,13 +9,12 @@
 // written token by token keeps its earlier values exactly, but for codes that
 // fall below the normal range.
 //
-// One CTA of 128 threads (or one warp, where requests bring few tokens) owns
-// one (page of a request, side, head): nothing is shared between them, so
-// there is no atomic and no second pass. The tokens stay in registers between
-// the maximum and the rounding: thread i holds 16-byte chunks i, i + 128, ...
-// of the page's [64, dim] block. The bound is HBM, 2 bytes read and 1 written
-// per element, and for few tokens the chain of lookups (request, length,
-// page, scale).
+// A CTA takes a (page of a request, side) and some heads, one after the other,
+// or, where requests bring few tokens, a warp takes a (page, side, head):
+// nothing is shared between them, so there is no atomic and no second pass. The
+// tokens stay in registers between the maximum and the rounding. The bound is
+// HBM, 2 bytes read and 1 written per element, and for few tokens the chain of
+// lookups (request, length, page, scale).
 //
 // The grid covers an upper bound of the touched pages: n consecutive
 // positions touch at most floor(n / 64) + 2 pages, so request r's pages are
@@ -28,12 +27,13 @@
 #include <stdint.h>
 
 #include "kv8.h"
+#include "ptx.cuh"
 
 namespace dsmla {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrLen = DS_DEVERR_LEN;
 
 // Smallest power of two s with a <= 448 s, exponent limited to [-60, 120].
@@ -167,55 +167,84 @@ __device__ __forceinline__ uint32_t again(uint32_t w, float f) {
   return r;
 }
 
+// One CTA per touched page, side and run of heads. A thread's 16-byte copies
+// land in shared memory (two heads ahead, without holding registers) and are
+// read back by the same thread, so only the maximum crosses threads. (A CTA
+// per head with the loads in registers spent most of its time on the lookups:
+// 30 us for 16k tokens of 8 heads x 128.)
 template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv8_append_page_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads) kv8_append_page_kernel(const Params p,
+                                                                  const int heads_per_cta) {
   constexpr int kRowChunks = DIM / 8;                     // 16-byte chunks of a token's head
   constexpr int kSteps = kPage * kRowChunks / kThreads;   // chunks per thread
-  __shared__ float warp_top[kThreads / 32];
+  constexpr int kStages = 3;
+  extern __shared__ uint4 staged[];                       // [kStages][kSteps][kThreads]
+  __shared__ float warp_top[2][kThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int side = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % p.c.kv_heads;
-  const int64_t unit = (blockIdx.x >> 1) / p.c.kv_heads;
+  const int runs = (p.c.kv_heads + heads_per_cta - 1) / heads_per_cta;
+  const int side = blockIdx.x & 1, run = (int)(blockIdx.x >> 1) % runs;
+  const int64_t unit = (blockIdx.x >> 1) / runs;
   Unit u;
-  if (!find_unit(p, unit, tid == 0 && side == 0 && head == 0, &u)) return;
-  const int64_t part = (u.page * 2 + side) * p.c.kv_heads + head;
-  float* scale_at = p.c.scales + part;
-  const float old = u.had > 0 ? *scale_at : 0.0f;
+  if (!find_unit(p, unit, tid == 0 && side == 0 && run == 0, &u)) return;
+  const int h0 = run * heads_per_cta, h1 = min(h0 + heads_per_cta, p.c.kv_heads);
+  const int64_t part0 = (u.page * 2 + side) * p.c.kv_heads;
   const int64_t stride = side ? p.v_stride : p.k_stride;
-  const __nv_bfloat16* src = (side ? p.v : p.k) + u.token0 * stride + head * DIM;
-  uint4 x[kSteps];
+  const __nv_bfloat16* src = (side ? p.v : p.k) + u.token0 * stride;
+  auto fetch = [&](int h) {
+    if (h < h1) {
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int c = tid + i * kThreads, slot = c / kRowChunks, ch = c % kRowChunks;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= u.had && slot < u.upto)
-      x[i] = __ldcs(reinterpret_cast<const uint4*>(src + slot * stride + ch * 8));
-  }
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) a = fmaxf(a, amax8(x[i]));
-  a = warp_max(a);
-  if ((tid & 31) == 0) warp_top[tid >> 5] = a;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, warp_top[w]);
-  const float s = new_scale(old, a);
-  uint8_t* dst = p.c.pages + part * (int64_t)(kPage * DIM);
-  if (u.had > 0 && s != old) {
-    const float f = __fdiv_rn(old, s);
-    for (int c = tid; c < u.had * DIM / 4; c += kThreads) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(dst) + c;
-      *at = again(*at, f);
+      for (int i = 0; i < kSteps; ++i) {
+        const int c = tid + i * kThreads, slot = c / kRowChunks, ch = c % kRowChunks;
+        if (slot >= u.had && slot < u.upto)
+          cp_async_16(smem_u32(&staged[((h - h0) % kStages * kSteps + i) * kThreads + tid]),
+                      src + slot * stride + h * DIM + ch * 8, 16);
+      }
     }
-  }
-  const Quantizer quant(s);
+    cp_async_commit();
+  };
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int c = tid + i * kThreads, slot = c / kRowChunks;
-    if (slot >= u.had && slot < u.upto) reinterpret_cast<uint2*>(dst)[c] = quant(x[i]);
+  for (int s = 0; s < kStages - 1; ++s) fetch(h0 + s);
+  for (int h = h0; h < h1; ++h) {
+    float* scale_at = p.c.scales + part0 + h;
+    const float old = u.had > 0 ? *scale_at : 0.0f;
+    fetch(h + kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    uint4 x[kSteps];
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int slot = (tid + i * kThreads) / kRowChunks;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (slot >= u.had && slot < u.upto)
+        x[i] = staged[((h - h0) % kStages * kSteps + i) * kThreads + tid];
+      a = fmaxf(a, amax8(x[i]));
+    }
+    a = warp_max(a);
+    float* top = warp_top[h & 1];   // the last head's is still read by others
+    if ((tid & 31) == 0) top[tid >> 5] = a;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, top[w]);
+    const float s = new_scale(old, a);
+    uint8_t* dst = p.c.pages + (part0 + h) * (int64_t)(kPage * DIM);
+    if (u.had > 0 && s != old) {
+      const float f = __fdiv_rn(old, s);
+      for (int c = tid; c < u.had * DIM / 4; c += kThreads) {
+        uint32_t* at = reinterpret_cast<uint32_t*>(dst) + c;
+        *at = again(*at, f);
+      }
+    }
+    const Quantizer quant(s);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int c = tid + i * kThreads, slot = c / kRowChunks;
+      if (slot >= u.had && slot < u.upto) reinterpret_cast<uint2*>(dst)[c] = quant(x[i]);
+    }
+    if (tid == 0) *scale_at = s;
   }
-  if (tid == 0) *scale_at = s;
+  cp_async_wait_all();
 }
 
 // The same with one warp per (page, side, head), for calls with few tokens a
@@ -274,6 +303,18 @@ __global__ void __launch_bounds__(256) kv8_append_few_kernel(const Params p) {
   if (lane == 0) *scale_at = s;
 }
 
+template <int DIM>
+cudaError_t launch_pages(const Params& p, dim3 grid, int heads_per_cta, cudaStream_t stream) {
+  constexpr int kSmem = 3 * kPage * DIM * 2;
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = stream_device(stream, &dev);
+  if (e == cudaSuccess) e = set_max_dynamic_smem(once, dev, kv8_append_page_kernel<DIM>, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_append_page_kernel<DIM>, grid, dim3(kThreads), kSmem, stream, 1u, p,
+                    heads_per_cta);
+}
+
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream) {
@@ -287,10 +328,15 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream) {
       return launch_pdl(kv8_append_few_kernel<128>, grid, dim3(256), 0, stream, 1u, p);
     return launch_pdl(kv8_append_few_kernel<64>, grid, dim3(256), 0, stream, 1u, p);
   }
-  const dim3 grid((unsigned)(units * 2 * a.c.kv_heads));
-  if (a.c.dim == 128)
-    return launch_pdl(kv8_append_page_kernel<128>, grid, dim3(kThreads), 0, stream, 1u, p);
-  return launch_pdl(kv8_append_page_kernel<64>, grid, dim3(kThreads), 0, stream, 1u, p);
+  // Heads per CTA: all CTAs resident at once, four per SM, where that is less
+  // than all heads.
+  const int64_t items = units * 2 * a.c.kv_heads;
+  int64_t per = (items + 152 * 4 - 1) / (152 * 4);
+  if (per > a.c.kv_heads) per = a.c.kv_heads;
+  const int64_t runs = (a.c.kv_heads + per - 1) / per;
+  const dim3 grid((unsigned)(units * 2 * runs));
+  return a.c.dim == 128 ? launch_pages<128>(p, grid, (int)per, stream)
+                        : launch_pages<64>(p, grid, (int)per, stream);
 }
 
 }  // namespace dsmla

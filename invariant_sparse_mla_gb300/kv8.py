@@ -4,7 +4,8 @@ Argument marshalling for ds_kv8_append / ds_kv8_decode / ds_kv8_prefill (see
 include/ds_sparse_mla.h). The cache of one layer is ``kv_pages`` uint8
 [num_pages, 2, kv_heads, 64, dim] (E4M3 codes, keys then values) with
 ``kv_scales`` float32 [num_pages, 2, kv_heads]; block tables are those of the
-latent cache.
+latent cache. A ``stream`` argument runs the call, and what it allocates, on
+that stream instead of the current one.
 """
 
 import torch
@@ -12,21 +13,38 @@ import torch
 from ._native import _check, _need, lib
 
 
-def _stream_of(stream, dev):
-    """The raw handle of ``stream``, or of the device's current stream."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return stream.cuda_stream
+# Workspaces kept for the streams they were allocated on, by (device, raw
+# stream): calls on one stream run in order, so they share one. (An allocation
+# between launches costs about 4 us on the host, half of a small call.) Larger
+# ones than this, and those of calls that are being captured into a graph, are
+# allocated anew.
+_KEEP_BYTES = 64 << 20
+_kept = {}
+
+
+def _scratch(need, dev, raw):
+    """A workspace of at least ``need`` bytes for a call on ``raw``, the current
+    stream."""
+    if (need > _KEEP_BYTES or torch.cuda.current_device() != dev.index
+            or torch.cuda.is_current_stream_capturing()):
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    key = (dev.index, raw)
+    kept = _kept.get(key)
+    if kept is None or kept.numel() < need:
+        # (Dropping the smaller one is safe: its memory goes back to this stream.)
+        kept = _kept[key] = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=dev)
+    return kept
 
 
 def _run(dev, fn, *args):
-    """Calls fn(*args) with ``dev`` current (the runtime launches only into
-    streams of the current device)."""
+    """Calls fn(*args, the device's current stream) with ``dev`` current (the
+    runtime launches only into streams of the current device)."""
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        status = fn(*args)
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args)
+            status = fn(*args, raw)
     if status:
         _check(status)
 
@@ -113,6 +131,9 @@ def kv8_append(k, v, token_starts, block_table, lens, kv_pages, kv_scales, err_f
     be strided) at the ends of their requests, quantised in place; request r
     owns tokens ``token_starts[r]:token_starts[r + 1]`` and ``lens`` includes
     them. Returns ``kv_pages``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_append(k, v, token_starts, block_table, lens, kv_pages, kv_scales, err_flag)
     dev = _device(kv_pages, "kv_pages", torch.uint8)
     pages, hk, d = _cache(kv_pages, kv_scales, dev)
     ks = _tokens(k, "k", torch.bfloat16, dev, 1)
@@ -123,7 +144,7 @@ def kv8_append(k, v, token_starts, block_table, lens, kv_pages, kv_scales, err_f
     _starts(token_starts, n, dev)
     _run(dev, lib().ds_kv8_append, k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0],
          token_starts.data_ptr(), n, block_table.data_ptr(), width, lens.data_ptr(), hk, d,
-         kv_pages.data_ptr(), kv_scales.data_ptr(), pages, flag, _stream_of(stream, dev))
+         kv_pages.data_ptr(), kv_scales.data_ptr(), pages, flag)
     return kv_pages
 
 
@@ -160,6 +181,10 @@ def kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=N
     """Attention of the last ``next_n`` tokens of every request over the
     block-scaled cache: q bf16 [R, next_n, H, dim] (tokens may be evenly
     strided); returns (out bf16 like q, lse fp32 [R, next_n, H])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out, lse,
+                              workspace, err_flag)
     dev = _device(kv_pages, "kv_pages", torch.uint8)
     pages, hk, d = _cache(kv_pages, kv_scales, dev)
     qs = _tokens(q, "q", torch.bfloat16, dev, 2)
@@ -171,13 +196,12 @@ def kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=N
     L = lib()
     if workspace is None:
         need = r and L.ds_kv8_decode_workspace_size(r, nn, h, hk, d, width)
-        workspace = torch.empty(need or 256, dtype=torch.uint8, device=dev)
+        workspace = _scratch(need or 256, dev, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         _arg(workspace, "workspace", torch.uint8, dev)
     _run(dev, L.ds_kv8_decode, q.data_ptr(), qs, kv_pages.data_ptr(), kv_scales.data_ptr(), pages,
          block_table.data_ptr(), width, lens.data_ptr(), r, nn, h, hk, d, float(scale),
-         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), flag,
-         _stream_of(stream, dev))
+         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), flag)
     return out, lse
 
 
@@ -188,6 +212,10 @@ def kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, 
     ``token_starts[r]:token_starts[r + 1]``, the last of its ``lens[r]``
     positions; returns (out bf16 [T, H, dim], lse fp32 [T, H]). Rows of no
     request are left as they are (unset in outputs allocated here)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, out,
+                               lse, workspace, err_flag)
     dev = _device(kv_pages, "kv_pages", torch.uint8)
     pages, hk, d = _cache(kv_pages, kv_scales, dev)
     qs = _tokens(q, "q", torch.bfloat16, dev, 1)
@@ -198,12 +226,12 @@ def kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, 
     L = lib()
     if workspace is None:
         need = t and L.ds_kv8_prefill_workspace_size(t, n, h, hk, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        workspace = need and _scratch(need, dev, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         _arg(workspace, "workspace", torch.uint8, dev)
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    ws, ws_bytes = (None, 0) if not t else (workspace.data_ptr(), workspace.numel())
     _run(dev, L.ds_kv8_prefill, q.data_ptr(), qs, t, token_starts.data_ptr(), n,
          kv_pages.data_ptr(), kv_scales.data_ptr(), pages, block_table.data_ptr(), width,
          lens.data_ptr(), h, hk, d, float(scale), out.data_ptr(), lse.data_ptr(), ws, ws_bytes,
-         flag, _stream_of(stream, dev))
+         flag)
     return out, lse

@@ -444,3 +444,31 @@ def test_prefill_strided_queries(ds):
     b = ds.kv8_prefill(q.contiguous(), starts, codes, scales, table, lens, 0.1)
     torch.cuda.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_kept_workspaces_of_streams_and_graphs(ds):
+    """Calls of several sizes in turn on two streams and in a captured graph,
+    replayed between them: each with its own workspace."""
+    cases = [Cache([900, 130], 2, 128, seed=50), Cache([2000, 700, 65, 1500], 4, 64, seed=51)]
+    args, want = [], []
+    for c in cases:
+        q = c.q(len(c.lens), 16).to(DEV).view(len(c.lens), 1, 16, c.dim)
+        args.append((q, *c.device(), 0.09))
+        ws = torch.empty(ds.kv8_decode_workspace_size(len(c.lens), 1, 16, c.kv_heads, c.dim,
+                                                      c.table.shape[1]),
+                         dtype=torch.uint8, device=DEV)
+        want.append(ds.kv8_decode(*args[-1], workspace=ws)[0].clone())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        inside = ds.kv8_decode(*args[1])[0]
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        for i in (0, 1):
+            got.append((i, ds.kv8_decode(*args[i])[0]))
+            got.append((i, ds.kv8_decode(*args[i], stream=side)[0]))
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(inside, want[1])
+    assert all(torch.equal(o, want[i]) for i, o in got)
