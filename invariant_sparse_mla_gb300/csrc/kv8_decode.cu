@@ -25,7 +25,7 @@
 // the page scales are); l = sum 2^(s_i - m) is kept in fp32 of the unrounded
 // weights.
 //
-// Work split. A row's context is cut into spans of 512 to 4096 positions, the
+// Work split. A row's context is cut into spans of 1024 to 4096 positions, the
 // power of two that gives at most 32 spans up to 131072 positions: a
 // function of the request's length alone, so a request's bits do not depend
 // on the batch. A persistent grid (two CTAs per SM) takes the (request, kv
@@ -61,7 +61,7 @@ constexpr int kMetaSlots = 8;
 constexpr float kTau = 12.0f;              // log2: p b may reach 2^kTau
 constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay <= 2^15
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-constexpr int kMinSpan = 512, kMaxSpan = 4096;
+constexpr int kMinSpan = 1024, kMaxSpan = 4096;
 
 __host__ __device__ inline int span_of(int64_t len) {
   int s = kMinSpan;
@@ -97,10 +97,13 @@ struct Layout {
   static constexpr int kPRow = kNP <= 16 ? 32 : (kNP <= 32 ? 64 : 128);
   static constexpr int kPBytes = kTile * kPRow;
   static constexpr int kRest = 2 * kUnit + kQBytes + kPBytes + 2048 + 1024;
-  static constexpr int kFit = (113 * 1024 - kRest) / kUnit;
+  // CTAs per SM: three where their registers and shared memory allow it.
+  static constexpr int kCtas = DIM == 64 && R8 <= 16 ? 3 : 2;
+  static constexpr int kBudget = 228 * 1024 / kCtas - 1024;   // (1 KB a CTA is the system's)
+  static constexpr int kFit = (kBudget - kRest) / kUnit;
   static constexpr int kUnits = kFit > 8 ? 8 : kFit;
   static constexpr int kNK = (kUnits + 1) / 2, kNV = kUnits / 2;   // stages of the two rings
-  static_assert(kNK >= 2 && kNV >= 1, "the next tile's K lands behind the present one's");
+  static_assert(kNK >= 1 && kNV >= 1, "a tile fits");
   static constexpr int kK = 0;
   static constexpr int kV = kK + kNK * kUnit;
   static constexpr int kV16 = kV + kNV * kUnit;             // V of the present tile in f16
@@ -108,7 +111,7 @@ struct Layout {
   static constexpr int kQ = kP + kPBytes;
   static constexpr int kBars = kQ + kQBytes;
   static constexpr int kMeta = kBars + 32 * 8;              // kMetaSlots x 2 float4
-  static constexpr int kF = kMeta + kMetaSlots * 32;        // per row: factor, reference, alpha
+  static constexpr int kF = kMeta + kMetaSlots * 32;        // per row: factor, minus the reference, alpha
   static constexpr int kM = kF + R8 * 4;
   static constexpr int kAlpha = kM + R8 * 4;
   static constexpr int kWarpMax = kAlpha + R8 * 4;          // 4 x R8 floats
@@ -118,9 +121,9 @@ struct Layout {
   static constexpr int kMisc = kSet + R8 * 4;               // tmem slot, abort, start of work
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
-  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+  static_assert(kSmem <= kBudget, "shared memory of an SM");
   static constexpr uint32_t kCols = 2 * R8 + kNP <= 32 ? 32u : (2 * R8 + kNP <= 64 ? 64u : 128u);
-  static_assert(2 * R8 + kNP <= 128, "TMEM columns");
+  static_assert(2 * R8 + kNP <= 128 && kCtas * kCols <= 512, "TMEM columns");
 };
 
 enum Bar {
@@ -262,7 +265,7 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
 }
 
 template <int R8, int DIM>
-__global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
+__global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_kernel(
     const __grid_constant__ CUtensorMap map, const Params p) {
   using LY = Layout<R8, DIM>;
   constexpr int NP = LY::kNP, NK = LY::kNK, NV = LY::kNV;
@@ -560,6 +563,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
     // it is noted under that vote's tile, before this warp votes there.
     auto give_up = [&] { abort_s[(g + 1) & 1] = (int)(g + 2); };
     int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
+    // Requests without positions are no items: their outputs here.
+    for (int64_t r = blockIdx.x; r < p.c.requests; r += gridDim.x) {
+      if (row_len(p, r) > 0) continue;
+      const int64_t n = (int64_t)p.next_n * p.heads;
+      uint4* out = reinterpret_cast<uint4*>(p.out + r * n * DIM);
+      for (int64_t i = tid; i < n * DIM / 8; i += kSoftmax) out[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int64_t i = tid; i < n; i += kSoftmax) p.lse[r * n + i] = -INFINITY;
+    }
     while (some && !failed) {
       const int nt = item_tiles(w);
       const int kvh = w.hg / p.row_groups, rg = w.hg % p.row_groups;
@@ -649,30 +660,36 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
           tmem_ld<RH>(t_s + R8, lo);
           tmem_fence<RH>(s);
           tmem_fence<RH>(lo);
+          const float2 w = make_float2(0.03125f, 0.03125f);
 #pragma unroll
-          for (int i = 0; i < RH; ++i) s[i] = __fmaf_rn(lo[i], 0.03125f, s[i]);
+          for (int i = 0; i < RH; i += 2) {
+            const float2 x = fma2(make_float2(lo[i], lo[i + 1]), w, make_float2(s[i], s[i + 1]));
+            s[i] = x.x;
+            s[i + 1] = x.y;
+          }
         }
         tc_fence_before();
         mbar_arrive(&bars[kSFree]);
-        const bool here = mt.w != 0.0f && pos < w.len;
         const bool edge = pos0 + kTile > min_vis;   // some row's context ends in the tile
         // s becomes the exponent relative to the row's reference.
+        const float2 ks = make_float2(mt.x, mt.x);
 #pragma unroll
         for (int i = 0; i < RH; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(f_s + rh + i);
-          const float4 m = *reinterpret_cast<const float4*>(m_s + rh + i);
-          s[i] = __fmaf_rn(s[i], f.x * mt.x, -m.x);
-          s[i + 1] = __fmaf_rn(s[i + 1], f.y * mt.x, -m.y);
-          s[i + 2] = __fmaf_rn(s[i + 2], f.z * mt.x, -m.z);
-          s[i + 3] = __fmaf_rn(s[i + 3], f.w * mt.x, -m.w);
+          const float4 m = *reinterpret_cast<const float4*>(m_s + rh + i);   // minus the reference
+          const float2 g0 = mul2(make_float2(f.x, f.y), ks), g1 = mul2(make_float2(f.z, f.w), ks);
+          const float2 x = fma2(make_float2(s[i], s[i + 1]), g0, make_float2(m.x, m.y));
+          const float2 y = fma2(make_float2(s[i + 2], s[i + 3]), g1, make_float2(m.z, m.w));
+          s[i] = x.x;
+          s[i + 1] = x.y;
+          s[i + 2] = y.x;
+          s[i + 3] = y.y;
         }
-        if (!here) {
-#pragma unroll
-          for (int i = 0; i < RH; ++i) s[i] = -INFINITY;
-        } else if (edge) {
+        if (edge || mt.w == 0.0f) {
+          const bool here = mt.w != 0.0f && pos < w.len;
 #pragma unroll
           for (int i = 0; i < RH; ++i)
-            if (pos >= vis_s[rh + i]) s[i] = -INFINITY;
+            if (!here || pos >= vis_s[rh + i]) s[i] = -INFINITY;
         }
         bool above = unset;
         const float slack = kTau - mt.z;
@@ -686,8 +703,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         if (lane == 0) mbar_arrive(&bars[kVote]);
         // P and the f16 V are free once PV of the last tile is done.
         if (g > 0 && !mbar_wait_long(&bars[kPvDone], (uint32_t)((g - 1) & 1))) give_up();
-        // V to f16: half a position's dims per thread. What lies behind the
-        // context is anything, and a weight of 0 times NaN is NaN: it becomes 0.
+        // V to f16: half a position's dims per thread.
         {
           const int st = (int)(g % NV);
           if (!mbar_wait_long(&bars[kVFull + st], (uint32_t)((g / NV) & 1))) give_up();
@@ -695,26 +711,35 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
           uint8_t* dst = smem + LY::kV16 + tok * 128;
           constexpr int NC = DIM / 32;         // 16-code chunks of this thread
           bool nan = false;
+          auto convert = [&](int c, uint4 v) {
+            const uint2 a = codes_to_f16(v.x), b = codes_to_f16(v.y), d = codes_to_f16(v.z),
+                        e = codes_to_f16(v.w);
+            const int cc = half * NC + c;
+            uint8_t* at = dst + (cc >> 2) * (kTile * 128);
+            const int ch = (cc & 3) * 2;
+            *reinterpret_cast<uint4*>(at + ((ch ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (tok & 7)) << 4)) =
+                make_uint4(d.x, d.y, e.x, e.y);
+          };
+          auto codes = [&](int c) {
+            return *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, (half * NC + c) * 16));
+          };
+          if (!edge) {
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 2) {
-            uint4 v[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              v[c] = *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, (half * NC + c0 + c) * 16));
-              if (pos >= w.len) v[c] = make_uint4(0u, 0u, 0u, 0u);
-              if (edge) nan |= has_nan_code(v[c]);
+            for (int c0 = 0; c0 < NC; c0 += 2) {
+              const uint4 v0 = codes(c0), v1 = codes(c0 + 1);
+              convert(c0, v0);
+              convert(c0 + 1, v1);
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint2 a = codes_to_f16(v[c].x), b = codes_to_f16(v[c].y),
-                          d = codes_to_f16(v[c].z), e = codes_to_f16(v[c].w);
-              const int cc = half * NC + c0 + c;
-              uint8_t* at = dst + (cc >> 2) * (kTile * 128);
-              const int ch = (cc & 3) * 2;
-              *reinterpret_cast<uint4*>(at + ((ch ^ (tok & 7)) << 4)) =
-                  make_uint4(a.x, a.y, b.x, b.y);
-              *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (tok & 7)) << 4)) =
-                  make_uint4(d.x, d.y, e.x, e.y);
+          } else {
+            // What lies behind the context is anything, and a weight of 0 times NaN
+            // is NaN: it becomes 0.
+#pragma unroll 1
+            for (int c = 0; c < NC; ++c) {
+              uint4 v = codes(c);
+              if (pos >= w.len) v = make_uint4(0u, 0u, 0u, 0u);
+              nan |= has_nan_code(v);
+              convert(c, v);
             }
           }
           mbar_arrive(&bars[kVEmpty + st]);
@@ -768,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
             if (first ? top > -INFINITY : top > kTau) {
               by = top;
               al = first ? 0.0f : ex2(-top);
-              m_s[tid] += top;
+              m_s[tid] -= top;
               set_s[tid] = 1;
             } else if (first) {
               open = vis > pos0 + kTile;   // it may see something later
@@ -810,11 +835,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
           }
         }
         // The weights, their sum, and P.
-        const float vscale = here ? mt.y * kPScale : 0.0f;
+        // (A page left out has a value scale of 0, hidden positions a weight of 0.)
+        const float2 vscale = make_float2(mt.y * kPScale, mt.y * kPScale);
 #pragma unroll
-        for (int i = 0; i < RH; ++i) {
-          s[i] = ex2(s[i]);
-          l[i] += s[i];
+        for (int i = 0; i < RH; i += 2) {
+          float2 e = make_float2(ex2(s[i]), ex2(s[i + 1]));
+          const float2 sum = add2(make_float2(l[i], l[i + 1]), e);
+          l[i] = sum.x;
+          l[i + 1] = sum.y;
+          e = mul2(e, vscale);
+          s[i] = e.x;
+          s[i + 1] = e.y;
         }
 #pragma unroll
         for (int c = 0; c < (RH + 7) / 8; ++c) {
@@ -822,8 +853,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 8 * c + 2 * e;
-            const __half2 h = i < RH ? __floats2half2_rn(s[i < RH ? i : 0] * vscale,
-                                                         s[i < RH ? i + 1 : 0] * vscale)
+            const __half2 h = i < RH ? __floats2half2_rn(s[i < RH ? i : 0], s[i < RH ? i + 1 : 0])
                                      : __floats2half2_rn(0.0f, 0.0f);
             b[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
@@ -866,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
             const float ls = sum_of(r);
             const float x = ls == 0.0f ? 0.0f : __fdiv_rn(o[i] * (1.0f / kPScale), ls);
             if (has_dim) p.out[h * DIM + dim0] = __float2bfloat16(x);
-            if (tok == 0) p.lse[h] = ls == 0.0f ? -INFINITY : (m_s[r] + log2f(ls)) * kLn2;
+            if (tok == 0) p.lse[h] = ls == 0.0f ? -INFINITY : (log2f(ls) - m_s[r]) * kLn2;
           }
         }
       } else {
@@ -876,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
         for (int i = 0; i < RH; ++i)
           if (has_dim && rh + i < rows) at[i * DIM] = o[i] * (1.0f / kPScale);
         if (tid < rows)
-          p.part_ml[slot + tid] = make_float2(set_s[tid] ? m_s[tid] : -INFINITY, sum_of(tid));
+          p.part_ml[slot + tid] = make_float2(set_s[tid] ? -m_s[tid] : -INFINITY, sum_of(tid));
       }
       if (tid < R8) set_s[tid] = 0;
       named_bar_sync(1, kSoftmax);   // m_s and wmax_s are read before the next item writes them
@@ -892,8 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_decode_kernel(
 }
 
 // Joins the spans of a row, in order: one warp per (request, token, head).
-// Requests without positions get their zeros here; those with one span are
-// complete already.
+// Requests with one span (or none) are complete already.
 template <int DIM>
 __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
   constexpr int E = DIM / 32;
@@ -908,7 +937,7 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
   const int len = row_len(p, r);
   const int span = span_of(len);
   const int spans = (len + span - 1) / span;
-  if (spans == 1) return;
+  if (spans <= 1) return;
   const int kvh = h / p.group;
   const int row = (int)(token % p.next_n) * p.group + h % p.group;
   const int rg = row / p.rows, rr = row % p.rows;
@@ -956,31 +985,31 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
 }
 
 template <int R8, int DIM>
-cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, unsigned grid,
+cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, int64_t items,
                         cudaStream_t stream) {
   using LY = Layout<R8, DIM>;
   static PerDeviceOnce once;
   auto kern = kv8_decode_kernel<R8, DIM>;
   const cudaError_t e = set_max_dynamic_smem(once, dev, kern, LY::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), LY::kSmem, stream, 1u, map, p);
+  // At most one CTA per item.
+  const int64_t most = LY::kCtas * (int64_t)kv8_sm_count(dev);
+  return launch_pdl(kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), LY::kSmem,
+                    stream, 1u, map, p);
 }
 
 template <int DIM>
 cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStream_t stream) {
-  // At most one CTA per item, two per SM.
   const int64_t items = p.c.requests * p.c.kv_heads * p.row_groups * p.spans;
-  const int64_t most = 2 * (int64_t)kv8_sm_count(dev);
-  const unsigned grid = (unsigned)(items < most ? items : most);
   cudaError_t e;
   switch ((p.rows + 7) / 8) {
-    case 1: e = launch_main<8, DIM>(map, p, dev, grid, stream); break;
-    case 2: e = launch_main<16, DIM>(map, p, dev, grid, stream); break;
-    case 3: e = launch_main<24, DIM>(map, p, dev, grid, stream); break;
-    case 4: e = launch_main<32, DIM>(map, p, dev, grid, stream); break;
-    default: e = launch_main<40, DIM>(map, p, dev, grid, stream); break;
+    case 1: e = launch_main<8, DIM>(map, p, dev, items, stream); break;
+    case 2: e = launch_main<16, DIM>(map, p, dev, items, stream); break;
+    case 3: e = launch_main<24, DIM>(map, p, dev, items, stream); break;
+    case 4: e = launch_main<32, DIM>(map, p, dev, items, stream); break;
+    default: e = launch_main<40, DIM>(map, p, dev, items, stream); break;
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.spans == 1) return e;   // no table holds a row of two spans
   const int64_t rows = p.c.requests * p.next_n * p.heads;
   return launch_pdl(kv8_decode_join_kernel<DIM>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0,
                     stream, 1u, p);
