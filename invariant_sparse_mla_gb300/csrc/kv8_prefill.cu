@@ -32,9 +32,10 @@
 //                    engine cannot widen them, and staging the codes in shared
 //                    memory first would cost 64 KB of its bandwidth a tile;
 //   warp 12          MMA issuer: S = Q K^T (M 128, N 128), O += P V with P from
-//                    TMEM, where it lies over S. The two row tiles alternate,
-//                    so that one's products run under the other's softmax,
-//                    and PV begins when half of a P is there;
+//                    TMEM. One row tile's products run under the other's
+//                    softmax. With dim 128 P lies over S; with dim 64 there is
+//                    room for P apart, and the next S is computed under this
+//                    one's softmax;
 //   warp 13          looks the pieces up ahead of the others.
 // The bound is the tensor pipe and shared-memory bandwidth behind it: an M 128
 // x N 128 x K 16 product reads 8 KB in the 64 cycles it takes.
@@ -113,15 +114,13 @@ enum Bar {
   kVFull = 6,       // 2: the 128 loader threads
   kVEmpty = 8,      // 2: commit
   kSFull = 10,      // 2 (row tile): commit
-  kPHalf = 12,      // 2: the row tile's softmax threads (positions 64-127 of P)
-  kPFull = 14,      // 2: the same (all of P)
-  kPvDone = 16,     // 2: commit
-  kPvHalf = 18,     // 2: commit, PV of positions 64-127
-  kPieceFull = 20,  // 2: the scheduling lane
-  kPieceEmpty = 22, // 2: every thread that reads pieces
-  kSFree = 24,      // 2: the row tile's softmax threads have read S (P apart)
-  kDrain = 26,
-  kNumBars = 27
+  kPFull = 12,      // 2: the row tile's softmax threads
+  kPvDone = 14,     // 2: commit
+  kPieceFull = 16,  // 2: the scheduling lane
+  kPieceEmpty = 18, // 2: every thread that reads pieces
+  kSFree = 20,      // 2: the row tile's softmax threads have read S (P apart)
+  kDrain = 22,
+  kNumBars = 23
 };
 constexpr int kPieceReaders = 256 + 128 + 32;
 
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i < kKEmpty || (i >= kVFull && i < kVEmpty) || (i >= kPHalf && i < kPvDone) ||
+      if (i < kKEmpty || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kPvDone) ||
           (i >= kSFree && i < kDrain))
         count = 128u;
       if (i >= kPieceEmpty && i < kSFree) count = kPieceReaders;
@@ -531,24 +530,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             for (int u = 0; u < 4; ++u) top[u] = fmaxf(fmaxf(top[u], s1[i + u]), s1[i + 4 + u]);
           return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         };
-        // Moves the reference of rows with `move` to their largest, y, and the sums
-        // and outputs so far with it. O holds the tiles before (PV of the last
-        // may still run) and, at half 0, this tile's half 1.
+        // Moves the reference of rows with `move` by a whole number of powers of
+        // two, to about their largest, y, and the sums and outputs so far with it:
+        // O of the tiles before (PV of the last may still run) and, at half 0,
+        // P of this tile's half 1, which nobody has read yet.
         auto rebase = [&](bool move, float y, bool half1_in) {
-          const float by = move ? y - 3.0f : 0.0f;
-          const float al = move ? (unset ? 0.0f : ex2(-by)) : 1.0f;
+          const int by = move ? (int)fminf(ceilf(y) - 3.0f, 1000.0f) : 0;
+          const float al =
+              by == 0 ? 1.0f : (unset || by > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - by) << 23));
           if (move) {
-            ref += by;
+            ref += (float)by;
             l *= al;
             unset = false;
           }
-          if ((j > 0 || half1_in) && __any_sync(0xffffffffu, al != 1.0f)) {
-            bool ok = true;
-            if (half1_in)
-              ok = mbar_wait_long(&bars[kPvHalf + m], tiles & 1);
-            else if (j > x.j0)
-              ok = mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) failed = true;
+          if (!__any_sync(0xffffffffu, al != 1.0f)) return;
+          if (j > 0) {
+            if (j > x.j0 &&
+                !__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1)))
+              failed = true;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < DIM; c += 16) {
@@ -560,8 +559,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
               for (int i = 0; i < 16; i += 4) tmem_st4(t_o + c + i, o + i);
             }
-            tmem_wait_st();
           }
+          if (half1_in) {
+            const __half2 h = __float2half2_rn(al);
+#pragma unroll 1
+            for (int c = 32; c < 64; c += 16) {
+              float o[16];
+              tmem_ld<16>(t_p + c, o);
+              tmem_fence<16>(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), h);
+                o[i] = *reinterpret_cast<const float*>(&w);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) tmem_st4(t_p + c + i, o + i);
+            }
+          }
+          tmem_wait_st();
         };
         if (__any_sync(0xffffffffu, unset)) {
           const float y = fmaxf(exponents(0), exponents(1));
@@ -600,11 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           tmem_st16u(t_p + 32 * half, h);
           tmem_st16u(t_p + 16 + 32 * half, h + 16);
           l = __fmaf_rn(sum.x + sum.y, half ? mt1.z : mt0.z, l);
-          if (half == 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars[kPHalf + m]);
-          }
+          if (half == 1) tmem_wait_st();   // (half 0 may read it back)
         }
         // Where rows see different lengths, NaN values were taken out of the tile
         // and listed: the rows that see one get a NaN in that dim.
@@ -909,37 +920,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (m >= mts) break;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (LY::kApart && half == 1 && j + 1 < nt) {
-                // The next S as soon as this one is read. (Not ahead of PV's first
-                // half: softmax may wait for that before it has read all of S.)
-                if (m == 0) wait(kKFull + ((g + 1) & 1), (g + 1) >> 1);
-                wait(kSFree + m, done[m]);
-                if (failed) break;
-                tc_fence_after();
-                issue_s(m, g + 1);
-              }
-              wait((half ? kPFull : kPHalf) + m, done[m]);
+            if (LY::kApart && j + 1 < nt) {
+              // The next S as soon as this one is read.
+              if (m == 0) wait(kKFull + ((g + 1) & 1), (g + 1) >> 1);
+              wait(kSFree + m, done[m]);
               if (failed) break;
               tc_fence_after();
-              if (leader) {
-#pragma unroll
-                for (int k = 4 * (1 - half); k < 4 * (1 - half) + 4; ++k)
-                  mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kP + m * LY::kPStep + k * 8,
-                             vd + ((k * 16 * 128) >> 4), idesc_o,
-                             k != 4 || half ? 1u : (fresh ? 0u : 1u));
-                if (!half) {
-                  mma_commit(&bars[kPvHalf + m]);
-                } else {
-                  mma_commit(&bars[kPvDone + m]);
-                  if (m == mts - 1) mma_commit(&bars[kVEmpty + (g & 1)]);
-                }
-              }
-              __syncwarp();
+              issue_s(m, g + 1);
             }
+            wait(kPFull + m, done[m]);
+            if (failed) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kP + m * LY::kPStep + k * 8,
+                           vd + ((k * 16 * 128) >> 4), idesc_o, k > 0 ? 1u : (fresh ? 0u : 1u));
+              mma_commit(&bars[kPvDone + m]);
+              if (m == mts - 1) mma_commit(&bars[kVEmpty + (g & 1)]);
+            }
+            __syncwarp();
             ++done[m];
-            if (!LY::kApart && j + 1 < nt && !failed) {
+            if (!LY::kApart && j + 1 < nt) {
               // The next S overwrites this P: only once PV has ended.
               if (m == 0) wait(kKFull + ((g + 1) & 1), (g + 1) >> 1);
               wait(kPvDone + m, done[m] - 1);
