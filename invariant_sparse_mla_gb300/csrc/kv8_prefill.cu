@@ -24,8 +24,9 @@
 // sum and fp32 outputs) to the next CTA, which continues where it stopped: the
 // same operations in the same order, so that where runs are cut changes no
 // bit. A CTA does the piece that it hands over first and the piece that it
-// takes over last, so nobody waits in practice (512 equal items on 152 SMs
-// would otherwise take 4 rounds for 3.4 rounds of work).
+// takes over last, so nobody waits in practice, and the launch is cooperative
+// (every CTA resident), so that a wait always ends. (512 equal items on 152 SMs
+// would otherwise take 4 rounds for 3.4 rounds of work.)
 //   warps 0-3, 4-7   softmax of row tile 0 and 1 (thread = row = TMEM lane);
 //   warps 8-11       codes from global memory, through registers, to f16 tiles
 //                    of K and V in shared memory (two buffers each): the copy
@@ -991,7 +992,19 @@ cudaError_t launch(const Params& p, int dev, cudaStream_t stream) {
   int64_t ctas = kv8_sm_count(dev);
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   if (ctas > items) ctas = items;
-  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Layout<DIM>::kSmem, stream, 1u, p);
+  // CTAs wait for the state of the one before: a cooperative launch keeps all of
+  // them resident.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<DIM>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
