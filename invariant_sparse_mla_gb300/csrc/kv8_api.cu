@@ -177,6 +177,10 @@ int ds_kv8_decode(const void* q, int64_t q_stride, const void* kv_pages, const f
   if (next_n < 1 || next_n > 64)
     return report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64",
                         fn, next_n);
+  if (num_requests * next_n > (int64_t)INT32_MAX / num_heads)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: num_requests=%lld is too large with next_n=%d and num_heads=%d "
+                        "(below 2^31 rows)", fn, (long long)num_requests, next_n, num_heads);
   if (num_requests == 0) return report_ok();
   st = check_ptrs(fn, {{q, "q", 16},
                        {kv_pages, "kv_pages", 16},

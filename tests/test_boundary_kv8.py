@@ -63,6 +63,7 @@ def test_cache_calls_reject_bad_arguments(L, name, base):
         bad(DS_ERR_SHAPE, "v_stride=128", vs=128)
         bad(DS_ERR_SHAPE, "num_tokens=-3", T=-3)
         bad(DS_ERR_NULL, "token_starts", starts=None)
+        bad(DS_ERR_UNSUPPORTED, "num_tokens", T=1 << 24, N=1 << 20, hk=1024, ks=131072, vs=131072)
         bad(DS_ERR_ALIGN, "k must be 16-byte", k=A + 4)
         assert _call(L, name, base, T=0, k=None, v=None) == DS_OK
         return
@@ -76,11 +77,13 @@ def test_cache_calls_reject_bad_arguments(L, name, base):
     if name == "ds_kv8_decode":
         bad(DS_ERR_UNSUPPORTED, "next_n=0", nn=0)
         bad(DS_ERR_UNSUPPORTED, "next_n=65", nn=65)
+        bad(DS_ERR_UNSUPPORTED, "num_requests=1048576", N=1 << 20, nn=64, h=64, qs=8192)
         need = L.ds_kv8_decode_workspace_size(2, 1, 8, 2, 128, 4)
         bad(DS_ERR_WORKSPACE, str(need), wsb=need - 1)
         assert _call(L, name, base, N=0, q=None) == DS_OK
     else:
         bad(DS_ERR_SHAPE, "num_tokens=-1", T=-1)
+        bad(DS_ERR_UNSUPPORTED, "num_tokens", T=1 << 24, h=1024, qs=131072)
         bad(DS_ERR_NULL, "token_starts", starts=None)
         assert _call(L, name, base, T=0, q=None) == DS_OK
 

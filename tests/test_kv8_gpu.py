@@ -472,3 +472,92 @@ def test_kept_workspaces_of_streams_and_graphs(ds):
     torch.cuda.synchronize()
     assert torch.equal(inside, want[1])
     assert all(torch.equal(o, want[i]) for i, o in got)
+
+
+def _poisoned(c, r, pos, side, head, dim_at):
+    """The cache with a NaN code at one position, and with a 0 there."""
+    p = c.table[r, pos // 64]
+    out = []
+    for code in (0x7F, 0x00):
+        codes = c.codes.copy()
+        codes[p, side, head, pos % 64, dim_at] = code
+        out.append(torch.as_tensor(codes).to(DEV))
+    return out
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length", [130, 1100])
+def test_decode_nan_of_a_later_token_stays_with_those_that_see_it(ds, dim, length):
+    """A NaN value at the third of five tokens: earlier tokens' bits are those
+    of a cache without it, later ones are NaN in that dim alone; a NaN key
+    makes later tokens' outputs NaN and leaves earlier ones."""
+    c = Cache([length, 70], 2, dim, seed=60)
+    q = c.q(10, 6).to(DEV).view(2, 5, 6, dim)
+    _, scales, table, lens = c.device()
+    for side in (1, 0):
+        nan, zero = _poisoned(c, 0, length - 3, side, 1, 37)
+        got = ds.kv8_decode(q, nan, scales, table, lens, 0.1)
+        want = ds.kv8_decode(q, zero, scales, table, lens, 0.1)
+        torch.cuda.synchronize()
+        clean = torch.ones(2, 5, 6, dim, dtype=torch.bool, device=DEV)
+        clean[0, 2:, 3:] = False
+        if side == 1:
+            clean[0, 2:, 3:] = torch.arange(dim, device=DEV) != 37
+            assert torch.equal(got[1], want[1])
+        assert torch.equal(got[0][clean], want[0][clean])
+        assert torch.isnan(got[0][~clean]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_nan_of_a_later_token_stays_with_those_that_see_it(ds, dim):
+    c = Cache([400, 90], 2, dim, seed=61)
+    q = c.q(300, 6).to(DEV)
+    _, scales, table, lens = c.device()
+    starts = torch.tensor([0, 250, 300], dtype=torch.int32, device=DEV)
+    for side in (1, 0):
+        for pos in (399, 300, 151):                 # first seen by token pos - 150
+            nan, zero = _poisoned(c, 0, pos, side, 1, 37)
+            got = ds.kv8_prefill(q, starts, nan, scales, table, lens, 0.1)
+            want = ds.kv8_prefill(q, starts, zero, scales, table, lens, 0.1)
+            torch.cuda.synchronize()
+            clean = torch.ones(300, 6, dim, dtype=torch.bool, device=DEV)
+            clean[pos - 150:250, 3:] = False
+            if side == 1:
+                clean[pos - 150:250, 3:] = torch.arange(dim, device=DEV) != 37
+                assert torch.equal(got[1], want[1])
+            assert torch.equal(got[0][clean], want[0][clean])
+            assert torch.isnan(got[0][~clean]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_runs_cut_inside_items(ds, dim):
+    """Items of very different lengths, so that the CTAs' runs end inside them:
+    the bits are those of calls of one request each."""
+    lens = [3000, 40, 2900, 129, 1500, 2, 2222]
+    counts = [700, 40, 1, 129, 300, 2, 60]
+    c = Cache(lens, 3, dim, seed=62)
+    q = c.q(sum(counts), 12).to(DEV)
+    codes, scales, table, lens_d = c.device()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    starts = np.concatenate([[0], np.cumsum(counts)])
+    out, lse = ds.kv8_prefill(q, torch.as_tensor(starts, **i32), codes, scales, table, lens_d, 0.09)
+    for r, n in enumerate(counts):
+        lo, hi = int(starts[r]), int(starts[r + 1])
+        o, l = ds.kv8_prefill(q[lo:hi], torch.tensor([0, n], **i32), codes, scales,
+                              table[r:r + 1].contiguous(), lens_d[r:r + 1].contiguous(), 0.09)
+        assert torch.equal(o, out[lo:hi]) and torch.equal(l, lse[lo:hi])
+    for r in (2, 5):                                # and against the oracle
+        lo, hi = int(starts[r]), int(starts[r + 1])
+        rows = [(r, v) for _, v in oracle.kv8_visible([lens[r]], [counts[r]], c.table.shape[1])]
+        ref = oracle.kv8_attention(bits(q[lo:hi]), rows, c.codes, c.scales, c.table, 0.09)
+        _close(out[lo:hi], lse[lo:hi], ref, dim, lens[r])
+
+
+def test_prefill_growing_scores_move_the_reference(ds):
+    """Keys that grow along the context: the running reference has to move
+    again and again, in either half of a tile."""
+    c = Cache([900], 1, 64, seed=63, spread=1)
+    for b in range(15):
+        c.scales[c.table[0, b], 0] = 2.0 ** (b - 9)
+    _prefill(ds, c, [400], 4)
+    _decode(ds, c, 3, 4)
