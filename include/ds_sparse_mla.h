@@ -389,6 +389,11 @@ int ds_kv_cache_write(const void* latent, int64_t num_rows, const int64_t* slots
  *  kv_scales    float32 [num_pages, 2, num_kv_heads].
  *               value = code * scale of its page, side and head. Scales are
  *               positive and finite; ds_kv8_append writes powers of two.
+ *               (A row whose largest score passes 2^22 in magnitude, where
+ *               float32 cannot tell weights apart any more, can give NaN.
+ *               Where value scales of one request differ by a
+ *               factor of 2^100 or more, a page of the small ones can drop
+ *               out of a row's softmax.)
  *
  * It uses the block tables and the page size of the latent cache: position s
  * of a request lies in slot s % 64 of page block_table[request, s / 64]. What
@@ -457,8 +462,9 @@ int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stri
  *  err_flag     optional: DS_DEVERR_PAGE for a page outside the pool (its
  *               positions are left out of the softmax).
  *
- * A request's outputs depend on its own q, length and cache alone, bit for
- * bit: contexts are cut at fixed positions, whatever else the batch holds.
+ * num_requests * next_n * num_heads is below 2^31. A request's outputs depend
+ * on its own q, length and cache alone, bit for bit: contexts are cut at fixed
+ * positions, whatever else the batch holds.
  */
 int ds_kv8_decode(const void* q, int64_t q_stride, const void* kv_pages, const float* kv_scales,
                   int64_t num_pages, const int32_t* block_table, int64_t bt_stride,
@@ -477,7 +483,9 @@ size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_he
  * out and lse that belong to no request are left as they are. Arguments as
  * for ds_kv8_decode; q, out and lse are indexed by token. The workspace has
  * ds_kv8_prefill_workspace_size() bytes, 256-byte aligned; its contents need
- * no initialisation.
+ * no initialisation. num_tokens * num_heads / num_kv_heads is below 2^31 - 256
+ * and bt_stride at most 2^20 (a request's context is walked in order, and waits
+ * have a limit).
  *
  * A token's outputs depend on its own request alone, bit for bit, and not on
  * how the request's tokens are spread over calls.

@@ -242,6 +242,9 @@ int ds_kv8_prefill(const void* q, int64_t q_stride, int64_t num_tokens,
   if (st == DS_OK) st = check_heads(fn, num_heads, num_kv_heads, q_stride, head_dim, scale);
   if (st == DS_OK) st = check_tokens(fn, num_tokens);
   if (st != DS_OK) return st;
+  if (bt_stride > (1 << 20))
+    return report_error(DS_ERR_UNSUPPORTED, "%s: bt_stride=%lld exceeds 2^20", fn,
+                        (long long)bt_stride);
   if (num_tokens == 0 || num_requests == 0) return report_ok();
   if (num_tokens > (int64_t)INT32_MAX / (num_heads / num_kv_heads) - 256)
     return report_error(DS_ERR_UNSUPPORTED, "%s: num_tokens=%lld is too large with %d query heads "

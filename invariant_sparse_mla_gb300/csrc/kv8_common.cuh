@@ -23,6 +23,14 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Two fp32 operations in one instruction.
+// By how much a row's reference m goes up for a tile whose largest exponent
+// relative to it is y (both in powers of two): to 3 above y, as a weight is
+// stored as 2^3 p b. From 2^23 on m and y are rounded by too much for that, and
+// the reference, and with it the row, becomes NaN.
+__device__ __forceinline__ float reference_step(float m, float y) {
+  return fmaxf(fabsf(m), fabsf(y)) <= 0x1p23f ? y - 3.0f : NAN;
+}
+
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, c, d;\n\t"

@@ -22,8 +22,9 @@
 //
 // The reference m of a row is the largest s_i + log2 b_i of its first tile and
 // moves only when a tile passes it by more than 2^12 (so p b <= 2^12 whatever
-// the page scales are); l = sum 2^(s_i - m) is kept in fp32 of the unrounded
-// weights.
+// the page scales are). 8 p b is one exponential, of S g + (log2 8b - m), so
+// that no large b meets a p below the smallest float; l = sum 2^(s_i - m) is
+// kept in fp32 of the unrounded weights, each times 1 / 8b.
 //
 // Work split. A row's context is cut into spans of 1024 to 4096 positions, the
 // power of two that gives at most 32 spans up to 131072 positions: a
@@ -60,6 +61,7 @@ constexpr int kMaxRows = 40;               // query rows of one row group
 constexpr int kMetaSlots = 8;
 constexpr float kTau = 12.0f;              // log2: p b may reach 2^kTau
 constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay <= 2^15
+constexpr float kLog2PScale = 3.0f;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMinSpan = 1024, kMaxSpan = 4096;
 
@@ -242,7 +244,7 @@ __device__ __forceinline__ float warp_sum4(const float* v, int lane) {
 
 // Maxima the same way (a REDUX per row instead is several times slower: 7 us
 // a move of 40 rows, measured).
-__device__ __forceinline__ float warp_max4(const float* v, float add, int lane) {
+__device__ __forceinline__ float warp_max4(const float* v, int lane) {
   float a[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -250,7 +252,7 @@ __device__ __forceinline__ float warp_max4(const float* v, float add, int lane) 
     a[i] = fmaxf(up ? v[2 + i] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[2 + i], 16));
   }
   const bool up = lane & 8;
-  float c = fmaxf(up ? a[1] : a[0], __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 8)) + add;
+  float c = fmaxf(up ? a[1] : a[0], __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 8));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
   return c;
@@ -385,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
       for (int e = 0; e < 2; ++e) {
         const int b = block0 + lane + 32 * e;
         k.y[e] = none;
-        k.ks[e] = k.vs[e] = 0.0f;
+        k.ks[e] = 0.0f;
+        k.vs[e] = 1.0f;
         if (lane + 32 * e < n && b < blocks) {
           const int64_t page = p.c.block_table[(int64_t)i.r * p.c.bt_stride + b];
           if (page >= 0 && page < p.c.num_pages) {
@@ -435,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
 #pragma unroll
               for (int h = 0; h < 2; ++h)
                 meta[(g & (kMetaSlots - 1)) * 2 + h] =
-                    make_float4(kk[h], vv[h], log2f(vv[h]), yy[h] == none ? 0.0f : 1.0f);
+                    make_float4(kk[h], log2f(vv[h]) + kLog2PScale,
+                                __fdiv_rn(1.0f / kPScale, vv[h]), yy[h] == none ? 0.0f : 1.0f);
             }
             mbar_arrive_expect_tx(full, LY::kUnit);
             const uint32_t dst = sbase + (side ? LY::kV : LY::kK) + st * LY::kUnit;
@@ -652,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
         const int pos = pos0 + tok;
         if (!mbar_wait_long(&bars[kSFull], (uint32_t)(g & 1))) abort_s[g & 1] = (int)(g + 1);
         tc_fence_after();
-        const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tok >> 6)];   // ks, vs, log2 vs, valid
+        // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
+        const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tok >> 6)];
         float s[RH];
         {
           float lo[RH];
@@ -671,15 +676,17 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
         tc_fence_before();
         mbar_arrive(&bars[kSFree]);
         const bool edge = pos0 + kTile > min_vis;   // some row's context ends in the tile
-        // s becomes the exponent relative to the row's reference.
-        const float2 ks = make_float2(mt.x, mt.x);
+        // s becomes log2 of the stored weight: the exponent relative to the row's
+        // reference, and 8 b.
+        const float2 ks = make_float2(mt.x, mt.x), vs = make_float2(mt.y, mt.y);
 #pragma unroll
         for (int i = 0; i < RH; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(f_s + rh + i);
           const float4 m = *reinterpret_cast<const float4*>(m_s + rh + i);   // minus the reference
           const float2 g0 = mul2(make_float2(f.x, f.y), ks), g1 = mul2(make_float2(f.z, f.w), ks);
-          const float2 x = fma2(make_float2(s[i], s[i + 1]), g0, make_float2(m.x, m.y));
-          const float2 y = fma2(make_float2(s[i + 2], s[i + 3]), g1, make_float2(m.z, m.w));
+          const float2 c0 = add2(make_float2(m.x, m.y), vs), c1 = add2(make_float2(m.z, m.w), vs);
+          const float2 x = fma2(make_float2(s[i], s[i + 1]), g0, c0);
+          const float2 y = fma2(make_float2(s[i + 2], s[i + 3]), g1, c1);
           s[i] = x.x;
           s[i + 1] = x.y;
           s[i + 2] = y.x;
@@ -692,9 +699,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
             if (!here || pos >= vis_s[rh + i]) s[i] = -INFINITY;
         }
         bool above = unset;
-        const float slack = kTau - mt.z;
 #pragma unroll
-        for (int i = 0; i < RH; ++i) above |= s[i] > slack;
+        for (int i = 0; i < RH; ++i) above |= s[i] > kTau + kLog2PScale;
         // Does some row's reference move? Each warp says so and goes on to V; the
         // answer is there when it is needed. (Slot g & 1 holds the last tile,
         // plus 1, that moved one; a warp is at most one tile ahead.)
@@ -776,8 +782,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
           // values alone.
 #pragma unroll
           for (int i = 0; i < RH; i += 4) {
-            // (A warp's 32 positions lie in one page: one log2 b.)
-            const float top = warp_max4(s + i, mt.z, lane);
+            const float top = warp_max4(s + i, lane);
             const int r = ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
             if ((lane & 7) == 0) wmax_s[quad * R8 + rh + i + r] = top;
           }
@@ -790,10 +795,12 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
             const int vis = vis_s[tid];
             const bool first = set_s[tid] == 0;
             float by = 0.0f, al = 1.0f;
-            if (first ? top > -INFINITY : top > kTau) {
-              by = top;
-              al = first ? 0.0f : ex2(-top);
-              m_s[tid] -= top;
+            if (first ? top > -INFINITY : top > kTau + kLog2PScale) {
+              // (By what the reference moves once rounded.)
+              const float m = m_s[tid] - reference_step(m_s[tid], top);
+              by = m_s[tid] - m;
+              al = first ? 0.0f : ex2(-by);
+              m_s[tid] = m;
               set_s[tid] = 1;
             } else if (first) {
               open = vis > pos0 + kTile;   // it may see something later
@@ -835,15 +842,13 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
           }
         }
         // The weights, their sum, and P.
-        // (A page left out has a value scale of 0, hidden positions a weight of 0.)
-        const float2 vscale = make_float2(mt.y * kPScale, mt.y * kPScale);
+        const float2 rv = make_float2(mt.z, mt.z);
 #pragma unroll
         for (int i = 0; i < RH; i += 2) {
-          float2 e = make_float2(ex2(s[i]), ex2(s[i + 1]));
-          const float2 sum = add2(make_float2(l[i], l[i + 1]), e);
+          const float2 e = make_float2(ex2(s[i]), ex2(s[i + 1]));
+          const float2 sum = fma2(e, rv, make_float2(l[i], l[i + 1]));
           l[i] = sum.x;
           l[i + 1] = sum.y;
-          e = mul2(e, vscale);
           s[i] = e.x;
           s[i + 1] = e.y;
         }

@@ -536,11 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         // O of the tiles before (PV of the last may still run) and, at half 0,
         // P of this tile's half 1, which nobody has read yet.
         auto rebase = [&](bool move, float y, bool half1_in) {
-          const int by = move ? (int)fminf(ceilf(y) - 3.0f, 1000.0f) : 0;
-          const float al =
-              by == 0 ? 1.0f : (unset || by > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - by) << 23));
+          const float by = move ? reference_step(ref, ceilf(y)) : 0.0f;
+          const float al = by == 0.0f ? 1.0f
+                           : unset || by > 126.0f
+                               ? 0.0f
+                               : __uint_as_float((uint32_t)(127 - (int)by) << 23);
           if (move) {
-            ref += (float)by;
+            ref += by;
             l *= al;
             unset = false;
           }
@@ -581,12 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         };
         if (__any_sync(0xffffffffu, unset)) {
           const float y = fmaxf(exponents(0), exponents(1));
-          rebase(unset ? y > -INFINITY : y > 15.0f, y, false);
+          rebase(unset && y > -INFINITY, y, false);
         }
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
           // Rarely a weight would pass 2^15: the exponents again, with a new
-          // reference.
+          // reference (3 above the largest, or NaN: the loop ends).
           while (true) {
             const float y = exponents(half);
             const bool move = y > 15.0f;

@@ -84,6 +84,7 @@ def test_cache_calls_reject_bad_arguments(L, name, base):
     else:
         bad(DS_ERR_SHAPE, "num_tokens=-1", T=-1)
         bad(DS_ERR_UNSUPPORTED, "num_tokens", T=1 << 24, h=1024, qs=131072)
+        bad(DS_ERR_UNSUPPORTED, "bt_stride", bts=(1 << 20) + 1)
         bad(DS_ERR_NULL, "token_starts", starts=None)
         assert _call(L, name, base, T=0, q=None) == DS_OK
 

@@ -561,3 +561,105 @@ def test_prefill_growing_scores_move_the_reference(ds):
         c.scales[c.table[0, b], 0] = 2.0 ** (b - 9)
     _prefill(ds, c, [400], 4)
     _decode(ds, c, 3, 4)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_nan_query_leaves_its_neighbours(ds, dim):
+    """A NaN in one head of one token: that row is NaN, the others' bits stay,
+    also where references move."""
+    c = Cache([900], 1, dim, seed=64, spread=1)
+    for b in range(15):
+        c.scales[c.table[0, b], 0] = 2.0 ** (b - 9)
+    q = c.q(300, 3).to(DEV)
+    codes, scales, table, lens = c.device()
+    starts = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    out, lse = ds.kv8_prefill(q, starts, codes, scales, table, lens, 0.1)
+    bad = q.clone()
+    bad[17, 1, 5] = float("nan")
+    bad[200, 2, 0] = float("inf")
+    got, glse = ds.kv8_prefill(bad, starts, codes, scales, table, lens, 0.1)
+    torch.cuda.synchronize()
+    clean = torch.ones(300, 3, dtype=torch.bool, device=DEV)
+    clean[17, 1] = clean[200, 2] = False
+    assert torch.equal(got[clean], out[clean]) and torch.equal(glse[clean], lse[clean])
+    assert torch.isnan(got[~clean]).all() and torch.isnan(glse[~clean]).all()
+
+
+def _staircase(dim, length, seed):
+    """Keys whose first dim climbs through the positive codes along the context
+    (the others are 0), with several positions on each."""
+    c = Cache([length], 1, dim, seed=seed, spread=1)
+    codes = (np.arange(length) * 126 // length + 1).astype(np.uint8)
+    for i in range(length):
+        c.codes[c.table[0, i // 64], 0, 0, i % 64] = 0
+        c.codes[c.table[0, i // 64], 0, 0, i % 64, 0] = codes[i]
+    c.scales[c.table[0, :-(-length // 64)], 0] = 1.0
+    return c, oracle.e4m3_to_float64(codes)
+
+
+def _both(ds, c, q, n):
+    """(out, lse) of the last n tokens by decode and by prefill."""
+    codes, scales, table, lens = c.device()
+    starts = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    o, l = ds.kv8_decode(q[None], codes, scales, table, lens, 1.0)
+    yield o[0], l[0]
+    yield ds.kv8_prefill(q, starts, codes, scales, table, lens, 1.0)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lift", [6, 10, 13])
+def test_large_scores(ds, dim, lift):
+    """Scores of up to 2^21.8: equal ones share, smaller ones get nothing.
+
+    q . k is exact here (one dim, a power of two); times log2 e and less the
+    reference it is rounded twice to 2^-24 of x = |score| log2 e at most, which
+    moves a weight, and the sum that divides it, by a factor of 2^(2^-23 x) each
+    (equal scores of the reference's own tile and of a later one are rounded
+    apart, so that it shows). Steps differ by 2^-4 of a score.
+    out: that, half a step of bf16 (2^-8) and of the f16 weights (2^-11), and
+    2^-16 for weights too small for 11 bits; lse: fewer than 16 roundings of
+    2^-24 of it."""
+    n = 60
+    c, keys = _staircase(dim, 700, seed=65)
+    q = torch.zeros((n, 2, dim), dtype=torch.bfloat16)
+    q[:, :, 0] = 2.0 ** lift
+    rows = [(0, 700 - n + 1 + j) for j in range(n)]
+    out, lse, weight = oracle.kv8_attention(bits(q), rows, c.codes, c.scales, c.table, 1.0)[:3]
+    x = keys.max() * 2.0 ** lift * math.log2(math.e)
+    tol = 2.0 ** -8 + 2.0 ** -10 + 2 * math.expm1(math.log(2) * 2.0 ** -23 * x)
+    for o, l in _both(ds, c, q.to(DEV), n):
+        o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+        assert (np.abs(o - out) <= tol * weight).all()
+        assert (np.abs(l - lse) <= 2.0 ** -20 * (np.abs(lse) + 1)).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lift", [20, 40, 100, 125])
+@pytest.mark.parametrize("length", [90, 400])
+def test_scores_beyond_the_grain_of_a_float_are_nan(ds, length, lift, dim):
+    """2^lift log2(e) times the largest visible key is far above 2^23 in the
+    last tokens, in the first tile or a later one: they are NaN, and tokens
+    whose largest is below 2^22 are not."""
+    n = 60
+    c, keys = _staircase(dim, length, seed=66)
+    q = torch.zeros((n, 2, dim), dtype=torch.bfloat16)
+    q[:, 0, 0] = 2.0 ** lift
+    q[:, 1, 0] = 2.0 ** 4
+    top = np.array([keys[:length - n + 1 + j].max() for j in range(n)]) * 2.0 ** lift
+    over = torch.as_tensor(top * math.log2(math.e) >= 2.0 ** 24)
+    under = torch.as_tensor(top < 2.0 ** 22)
+    assert over.any()
+    for o, l in _both(ds, c, q.to(DEV), n):
+        o, l = o.cpu(), l.cpu()
+        assert torch.isnan(l[over, 0]).all() and torch.isnan(o[over, 0]).all()
+        assert torch.isfinite(l[under, 0]).all() and torch.isfinite(o[under, 0]).all()
+        assert torch.isfinite(l[:, 1]).all() and torch.isfinite(o[:, 1]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("exponent", [117, -60])
+def test_value_scales_at_their_limits(ds, dim, exponent):
+    c = Cache([700, 90], 1, dim, seed=67)
+    c.scales[:, 1] *= np.float32(2.0 ** (exponent + 6))
+    _decode(ds, c, 3, 4)
+    _prefill(ds, c, [300, 70], 4)
