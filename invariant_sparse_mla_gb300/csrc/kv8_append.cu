@@ -320,9 +320,13 @@ cudaError_t launch_pages(const Params& p, dim3 grid, int heads_per_cta, cudaStre
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream) {
   Params p{reinterpret_cast<const __nv_bfloat16*>(a.k), reinterpret_cast<const __nv_bfloat16*>(a.v),
            a.k_stride, a.v_stride, a.tokens, a.starts, a.c};
-  // At most 16 tokens a request on average: the kernel for few.
+  // Few tokens a request (on average): a warp per (page, side, head). With 8
+  // heads x 128, us of this kernel against the other one:
+  //   requests x tokens   128 x 5   128 x 32   128 x 64   16 x 8   16 x 24
+  //                       4.4 13.4  11.8 15.9  19.9 18.4  3.1 4.0  5.6 4.2
+  // so up to 40 tokens, or 16 where few CTAs of the other one wait for a place.
   const int64_t units = a.tokens / kPage + 2 * a.c.requests;
-  if (a.tokens <= 16 * a.c.requests) {
+  if (a.tokens <= (a.c.requests * a.c.kv_heads >= 512 ? 40 : 16) * a.c.requests) {
     const dim3 grid((unsigned)(units * ((2 * a.c.kv_heads + 7) / 8)));
     if (a.c.dim == 128)
       return launch_pdl(kv8_append_few_kernel<128>, grid, dim3(256), 0, stream, 1u, p);

@@ -35,7 +35,8 @@ constexpr int kErrPage = DS_DEVERR_PAGE, kErrRow = DS_DEVERR_ROWREQ,
               kErrNoPage = DS_DEVERR_NOPAGE, kErrLen = DS_DEVERR_LEN;
 
 // Passed by value: a call with few pools (up to 16) launches with a tenth of
-// the parameter bytes of one with many.
+// the parameter bytes of one with many (a fork and a free, 2 pools: 19.4 us on
+// the host, 20.2 with the many's parameters).
 constexpr int kFewPools = 16;
 template <int MAX>
 struct Pools {

@@ -8,18 +8,28 @@ latent cache. A ``stream`` argument runs the call, and what it allocates, on
 that stream instead of the current one.
 """
 
+import threading
+
 import torch
 
 from ._native import _check, _need, lib
 
 
 # Workspaces kept for the streams they were allocated on, by (device, raw
-# stream): calls on one stream run in order, so they share one. (An allocation
-# between launches costs about 4 us on the host, half of a small call.) Larger
-# ones than this, and those of calls that are being captured into a graph, are
-# allocated anew.
+# stream): calls of one thread on one stream run in order, so they share one.
+# (Each thread has its own: the launches of two calls could come in turn. An
+# allocation between launches costs about 4 us on the host, half of a small
+# call.) Larger ones than this, and those of calls that are being captured into
+# a graph, are allocated anew.
 _KEEP_BYTES = 64 << 20
-_kept = {}
+
+
+class _Kept(threading.local):
+    def __init__(self):
+        self.by_stream = {}
+
+
+_kept = _Kept()
 
 
 def _scratch(need, dev, raw):
@@ -29,10 +39,11 @@ def _scratch(need, dev, raw):
             or torch.cuda.is_current_stream_capturing()):
         return torch.empty(need, dtype=torch.uint8, device=dev)
     key = (dev.index, raw)
-    kept = _kept.get(key)
+    by_stream = _kept.by_stream
+    kept = by_stream.get(key)
     if kept is None or kept.numel() < need:
         # (Dropping the smaller one is safe: its memory goes back to this stream.)
-        kept = _kept[key] = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=dev)
+        kept = by_stream[key] = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=dev)
     return kept
 
 
@@ -226,12 +237,11 @@ def kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, 
     L = lib()
     if workspace is None:
         need = t and L.ds_kv8_prefill_workspace_size(t, n, h, hk, d)
-        workspace = need and _scratch(need, dev, torch._C._cuda_getCurrentRawStream(dev.index))
+        workspace = _scratch(need or 256, dev, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         _arg(workspace, "workspace", torch.uint8, dev)
-    ws, ws_bytes = (None, 0) if not t else (workspace.data_ptr(), workspace.numel())
     _run(dev, L.ds_kv8_prefill, q.data_ptr(), qs, t, token_starts.data_ptr(), n,
          kv_pages.data_ptr(), kv_scales.data_ptr(), pages, block_table.data_ptr(), width,
-         lens.data_ptr(), h, hk, d, float(scale), out.data_ptr(), lse.data_ptr(), ws, ws_bytes,
-         flag)
+         lens.data_ptr(), h, hk, d, float(scale), out.data_ptr(), lse.data_ptr(),
+         workspace.data_ptr(), workspace.numel(), flag)
     return out, lse

@@ -22,6 +22,8 @@ def pages_workspace_size(num_pages, n):
 
 def _pools(pools, num_pages, dev):
     """The pools as the C array {pointer, bytes of a page}, packed."""
+    if num_pages < 1:
+        raise ValueError("the pools have no pages")
     words = []
     index = dev.index
     for t in pools:
@@ -74,7 +76,10 @@ def pages_copy(pools, src, dst, err_flag=None, stream=None):
     flag = _flag(err_flag, dev)
     if not pools:
         return
-    num_pages = pools[0].shape[0]
+    first = pools[0]
+    if not isinstance(first, torch.Tensor) or first.dim() < 1:
+        raise TypeError("every pool must be a torch.Tensor of pages")
+    num_pages = first.shape[0]
     _run(dev, lib().ds_pages_copy, _pools(pools, num_pages, dev), len(pools), num_pages,
          src.data_ptr(), dst.data_ptr(), n, flag)
 

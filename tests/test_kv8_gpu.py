@@ -8,6 +8,7 @@ them shows.
 """
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -663,3 +664,64 @@ def test_value_scales_at_their_limits(ds, dim, exponent):
     c.scales[:, 1] *= np.float32(2.0 ** (exponent + 6))
     _decode(ds, c, 3, 4)
     _prefill(ds, c, [300, 70], 4)
+
+
+def test_refusals_of_the_bindings(ds):
+    """Shapes that no kernel serves are the library's errors, calls without
+    requests or tokens do nothing."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    lens, table = torch.tensor([5], **i32), torch.zeros((1, 1), **i32)
+    starts = torch.tensor([0, 5], **i32)
+    for dim, heads, what in ((32, 4, "head_dim"), (64, 3, "num_heads")):
+        codes = torch.zeros((1, 2, 2, 64, dim), dtype=torch.uint8, device=DEV)
+        scales = torch.ones((1, 2, 2), device=DEV)
+        q = torch.zeros((5, heads, dim), dtype=torch.bfloat16, device=DEV)
+        with pytest.raises(Exception, match=what):
+            ds.kv8_prefill(q, starts, codes, scales, table, lens, 0.1)
+        with pytest.raises(Exception, match=what):
+            ds.kv8_decode(q[None], codes, scales, table, lens, 0.1)
+    codes = torch.zeros((1, 2, 2, 64, 64), dtype=torch.uint8, device=DEV)
+    q = torch.zeros((5, 2, 64), dtype=torch.bfloat16, device=DEV)
+    none = torch.zeros((0, 1), **i32), torch.zeros(0, **i32)
+    out = torch.full_like(q, 7.0)
+    ds.kv8_prefill(q, torch.zeros(1, **i32), codes, scales, *none, 0.1, out=out)
+    assert (out == 7).all()                       # rows of no request stay
+    assert ds.kv8_prefill(q[:0], starts * 0, codes, scales, table, lens, 0.1)[0].shape == (0, 2, 64)
+    assert ds.kv8_decode(q[:0, None], codes, scales, *none, 0.1)[0].shape == (0, 1, 2, 64)
+    ds.kv8_append(q[:0], q[:0], starts * 0, table, lens, codes, scales)
+    torch.cuda.synchronize()
+    assert (scales == 1).all()
+
+
+def test_threads_have_workspaces_of_their_own(ds):
+    """Two threads on one stream: the launches of their calls come in any order."""
+    c = Cache([900, 1300], 2, 128, seed=68)
+    codes, scales, table, lens = c.device()
+    starts = torch.tensor([0, 200, 500], dtype=torch.int32, device=DEV)
+    q = c.q(500, 4).to(DEV)
+    want = [ds.kv8_prefill(q * s, starts, codes, scales, table, lens, 0.1)[0] for s in (1, -1)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        x = q * (1, -1)[i]
+        for _ in range(50):
+            o, _ = ds.kv8_prefill(x, starts, codes, scales, table, lens, 0.1)
+            if not torch.equal(o, want[i]):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_append_dozens_of_tokens_to_many_requests(ds, dim):
+    """Up to 40 tokens a request, more than a lane holds in registers."""
+    counts = [(37 * i) % 79 for i in range(66)]
+    assert sum(counts) <= 40 * len(counts)
+    _append_case(ds, [n + (53 * i) % 130 for i, n in enumerate(counts)], counts, 8, dim, seed=69)

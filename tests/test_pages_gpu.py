@@ -304,3 +304,16 @@ def test_a_server_run(ds):
     grow([3, 0], [60, 10])
     look()
     assert before is not None
+
+
+def test_refusals_of_pools(ds):
+    i32 = dict(dtype=torch.int32, device=DEV)
+    one = torch.zeros(1, **i32)
+    with pytest.raises(ValueError, match="no pages"):
+        ds.pages_copy([torch.zeros((0, 64), device=DEV)], one, one)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        ds.pages_copy([None], one, one)
+    with pytest.raises(ValueError, match="contiguous"):
+        ds.pages_copy([torch.zeros((4, 64), device=DEV), torch.zeros((5, 64), device=DEV)], one, one)
+    with pytest.raises(Exception, match="page_bytes"):
+        ds.pages_copy([torch.zeros((4, 6), dtype=torch.uint8, device=DEV)], one, one)
