@@ -27,19 +27,31 @@
 // takes over last, so nobody waits in practice, and the launch is cooperative
 // (every CTA resident), so that a wait always ends. (512 equal items on 152 SMs
 // would otherwise take 4 rounds for 3.4 rounds of work.)
-//   warps 0-3, 4-7   softmax of row tile 0 and 1 (thread = row = TMEM lane);
-//   warps 8-11       codes from global memory, through registers, to f16 tiles
+//   softmax warps    thread = row = TMEM lane; with dim 64 two threads share a
+//                    row, a page of the tile each. With dim 128, P over S, the
+//                    tensor pipe and the memory of S and O bound the loop, and
+//                    reading S twice for want of registers costs more than the
+//                    shorter way to P gives: ragged prompts of dim 64 take 293 us
+//                    so and 332 with one thread a row, a chunk of dim 128 takes
+//                    1773 us with one thread and 1965 with two;
+//   4 loader warps   codes from global memory, through registers, to f16 tiles
 //                    of K and V in shared memory (two buffers each): the copy
 //                    engine cannot widen them, and staging the codes in shared
 //                    memory first would cost 64 KB of its bandwidth a tile;
-//   warp 12          MMA issuer: S = Q K^T (M 128, N 128), O += P V with P from
+//   MMA issuer       (a warp) S = Q K^T (M 128, N 128), O += P V with P from
 //                    TMEM. One row tile's products run under the other's
 //                    softmax. With dim 128 P lies over S; with dim 64 there is
 //                    room for P apart, and the next S is computed under this
-//                    one's softmax;
-//   warp 13          looks the pieces up ahead of the others.
-// The bound is the tensor pipe and shared-memory bandwidth behind it: an M 128
-// x N 128 x K 16 product reads 8 KB in the 64 cycles it takes.
+//                    one's softmax. (An M 128 product takes 64 cycles a K of 16
+//                    from N 64 to N 128, so that S by pages of 64 positions, two
+//                    in flight, took 2073 us.)
+//   a last warp      looks the pieces up ahead of the others.
+//
+// The bound is the way S -> softmax -> P -> O of a row tile: two of them in turn
+// keep the tensor pipe busy half the time (dim 128; the last 2048 of 32768
+// positions, 64 / 8 heads: 1773 us, 1202 TFLOP/s). Shared memory is near: an
+// M 128 x N 128 x K 16 product reads 8 KB in its 64 cycles, and without the
+// loader's stores the same takes 1486 us, without the softmax 1410.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -52,13 +64,7 @@ namespace {
 
 constexpr int kTile = 128;               // positions per K/V tile (two pages)
 constexpr int kRows = 256;               // query rows per CTA
-constexpr int kThreads = 512;
-constexpr int kLoaderWarp = 8, kMmaWarp = 12;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-// Registers: 512 threads launch with 128 each; 256 * 160 + 128 * 120 +
-// 128 * 72 = 65536 = 512 * 128.
-constexpr int kRegsSoftmax = 160, kRegsLoader = 120, kRegsMma = 72;
-
 constexpr int kMaxCtas = 192;
 
 // What the first kernel writes: item (unit u of one kv head) has weight
@@ -77,9 +83,10 @@ struct Plan {
   int32_t* flags;        // [kMaxCtas]
   uint8_t* state;        // [kMaxCtas] x state_bytes
 };
-// O [dim / 4][256 rows] float4, then (reference or unset, sum) and the NaN bits.
+// O [dim / 4][256 rows] float4, then (reference, sum, unset, NaN) for either
+// half and the NaN bits.
 __host__ __device__ constexpr int64_t state_bytes(int dim) {
-  return (int64_t)kRows * (dim * 4 + 16 + dim / 8);
+  return (int64_t)kRows * (dim * 4 + 32 + dim / 8);
 }
 
 template <int DIM>
@@ -95,17 +102,31 @@ struct Layout {
   static constexpr int kNanMap = kPiece + 128;            // 2 x [128][DIM / 16] u16
   static constexpr int kNanMapBytes = kTile * (DIM / 16) * 2;
   static constexpr int kRowNan = kNanMap + 2 * kNanMapBytes;   // [256][DIM / 16] u16
-  static constexpr int kMisc = kRowNan + kRows * (DIM / 16) * 2;
+  static constexpr int kFactor = kRowNan + kRows * (DIM / 16) * 2;   // [256] floats
+  static constexpr int kSwap = kFactor + kRows * 4;              // [256][2] floats
+  static constexpr int kMisc = kSwap + kRows * 8;
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  // Warps: kShare threads share a row (warps of 32 rows: 4 * kShare a row tile),
+  // then 4 loader warps and the MMA issuer's four.
+  static constexpr int kShare = DIM == 64 ? 2 : 1;
+  static constexpr int kLoaderWarp = 8 * kShare, kMmaWarp = kLoaderWarp + 4;
+  static constexpr int kRowThreads = 128 * kShare;          // of a row tile
+  static constexpr int kThreads = 32 * (kMmaWarp + 4);
+  static constexpr int kPieceReaders = 2 * kRowThreads + 128 + 32;
+  // Registers: 512 threads launch with 128 each, 768 with 80.
+  static constexpr int kRegsSoftmax = kShare == 2 ? 80 : 160;
+  static constexpr int kRegsLoader = 120, kRegsMma = kShare == 2 ? 40 : 72;
+  static_assert(2 * kRowThreads * kRegsSoftmax + 128 * (kRegsLoader + kRegsMma) <=
+                kThreads * (65536 / kThreads / 8 * 8), "registers of the launch");
   // TMEM columns: S and O of both row tiles and, where there is room, P; else P
   // lies over the upper half of S.
   static constexpr bool kApart = DIM == 64;
   static constexpr uint32_t kS = 0, kO = 2 * kTile;
   static constexpr uint32_t kP = kApart ? kO + 2 * DIM : kS + 64, kPStep = kApart ? 64 : kTile;
   static constexpr uint32_t kCols = 512u;
-  static_assert(kApart ? kP + 2 * kPStep <= kCols : kO + 2 * DIM <= kCols, "TMEM columns");
+  static_assert((kApart ? kP + 2 * kPStep : kO + 2 * DIM) <= kCols, "TMEM columns");
 };
 
 enum Bar {
@@ -123,7 +144,6 @@ enum Bar {
   kDrain = 22,
   kNumBars = 23
 };
-constexpr int kPieceReaders = 256 + 128 + 32;
 
 // One run of tiles [j0, j1) of an item. r < 0 ends the list.
 struct alignas(64) Piece {
@@ -326,8 +346,9 @@ struct Scheduler {
 };
 
 template <int DIM>
-__global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p) {
+__global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(const Params p) {
   using LY = Layout<DIM>;
+  constexpr int kMmaWarp = LY::kMmaWarp, kLoaderWarp = LY::kLoaderWarp, H = LY::kShare;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -341,10 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i < kKEmpty || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kPvDone) ||
-          (i >= kSFree && i < kDrain))
-        count = 128u;
-      if (i >= kPieceEmpty && i < kSFree) count = kPieceReaders;
+      if ((i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty)) count = 128u;
+      if (i < kKFull || (i >= kPFull && i < kPvDone) || (i >= kSFree && i < kDrain)) count = LY::kRowThreads;
+      if (i >= kPieceEmpty && i < kSFree) count = LY::kPieceReaders;
       mbar_init(&bars[i], count);
     }
     mbar_fence_init();
@@ -377,19 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
 
   if (warp < kLoaderWarp) {
     // ----------------------------------------------------------- softmax
-    regs_inc<kRegsSoftmax>();
-    const int m = warp >> 2;                         // row tile
+    if constexpr (LY::kRegsSoftmax > 80) regs_inc<LY::kRegsSoftmax>();
+    // Row tile; with two threads a row, which page of a tile and half of the dims
+    // is this one's (else both).
+    const int m = warp / (4 * H), half = H == 2 ? (warp >> 2) & 1 : 0;
     const int row = (warp & 3) * 32 + lane;          // TMEM lane
+    const int pair = 1 + m * 4 + (warp & 3);         // named barrier of the rows' two warps
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + LY::kS + m * kTile;
-    const uint32_t t_o = tmem + lane_base + LY::kO + m * DIM;
-    const uint32_t t_p = tmem + lane_base + LY::kP + m * LY::kPStep;
-    uint16_t* const row_bits =
-        reinterpret_cast<uint16_t*>(smem + LY::kRowNan) + (m * kTile + row) * (DIM / 16);
+    const uint32_t t_s = tmem + lane_base + LY::kS + m * kTile + half * kPage;
+    const uint32_t t_o = tmem + lane_base + LY::kO + m * DIM + half * (DIM / H);
+    const uint32_t t_p = tmem + lane_base + LY::kP + m * LY::kPStep + half * (kPage / 2);
+    constexpr int NB = DIM / 16 / H;                 // words of NaN bits of this thread's dims
+    uint16_t* const row_bits = reinterpret_cast<uint16_t*>(smem + LY::kRowNan) +
+                               (m * kTile + row) * (DIM / 16) + half * NB;
+    float* const factor = reinterpret_cast<float*>(smem + LY::kFactor) + m * kTile;
+    float* const swap = reinterpret_cast<float*>(smem + LY::kSwap) + (m * kTile + row) * 2;
+    // Waits are the warp's, and none follows one that gave up: the piece runs to
+    // its end without meaning.
+    auto wait = [&](int bar, uint32_t phase) {
+      if (!failed && !__all_sync(0xffffffffu, mbar_wait_long(&bars[bar], phase & 1)))
+        failed = true;
+    };
     uint32_t tiles = 0;        // tiles of this row tile so far
     uint32_t kv = 0;           // tiles of the CTA so far
     while (true) {
       const volatile Piece& x = *next_piece();
+      // (Two warps of the same rows give up together: neither waits for one that left.)
+      if constexpr (H == 2) failed = named_bar_or(pair, 64, failed);
       if (failed || x.r < 0) break;
       const int first = x.row0 + m * kTile;            // rows of the row tile
       const int rows = x.n * p.group - first;          // at most 128 of them exist
@@ -401,24 +435,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         const int rr = first + (warp & 3) * 32 + i;
         return (x.t0 + rr / p.group) * stride + (x.kvh * p.group + rr % p.group) * DIM;
       };
-      constexpr int RL = DIM / 8, RI = 32 / RL;        // lanes of a row; rows of a step
-      const int sub = lane / RL, ch = lane % RL;       // row of the step, 16-byte chunk
       const int left = rows - (warp & 3) * 32;         // rows of this warp that exist
       float f = 0.0f;
       if (any && x.j1 > x.j0) {
         // The rows' q, each times a power of two of its own, in f16. A warp does
-        // its 32 rows, RI at a time; lane i then keeps row i's factor.
-        uint4 v[RL];
+        // its 32 rows, or 16 of them, RI at a time.
+        constexpr int RL = DIM / 8, RI = 32 / RL;      // lanes of a row; rows of a step
+        const int sub = lane / RL, ch = lane % RL;     // row of the step, 16-byte chunk
+        uint4 v[RL / H];
 #pragma unroll
-        for (int i = 0; i < RL; ++i) {
-          const int rr = i * RI + sub;
+        for (int i = 0; i < RL / H; ++i) {
+          const int rr = half * 16 + i * RI + sub;
           v[i] = make_uint4(0u, 0u, 0u, 0u);
           if (rr < left)
             v[i] = *reinterpret_cast<const uint4*>(p.q + offset(rr, p.q_stride) + ch * 8);
         }
         uint8_t* dst = smem + LY::kQ + m * LY::kTileBytes + (ch >> 3) * LY::kBlock;
 #pragma unroll
-        for (int i = 0; i < RL; ++i) {
+        for (int i = 0; i < RL / H; ++i) {
+          const int rr = (warp & 3) * 32 + half * 16 + i * RI + sub;
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t top = 0u;   // largest magnitude bits (NaN above infinity)
 #pragma unroll
@@ -431,11 +466,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
           int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
           k = k > 120 ? 120 : (k < -120 ? -120 : k);
           const float up = copysignf(__uint_as_float((uint32_t)(k + 127) << 23), p.scale_log2);
-          const float fr = top >= 0x7F800000u
-                               ? NAN
-                               : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
-          const float mine = __shfl_sync(0xffffffffu, fr, (lane % RI) * RL);
-          if (lane / RI == i) f = mine;
+          const float mine =
+              top >= 0x7F800000u
+                  ? NAN
+                  : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
+          if constexpr (H == 2) {
+            if (ch == 0) factor[rr] = mine;
+          } else {
+            const float its = __shfl_sync(0xffffffffu, mine, (lane % RI) * RL);
+            if (lane / RI == i) f = its;
+          }
           uint32_t h[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -443,15 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
                                                 __uint_as_float(w[u] & 0xFFFF0000u) * up);
             h[u] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          *reinterpret_cast<uint4*>(
-              dst + swz<128>((warp & 3) * 32 + i * RI + sub, (ch & 7) * 16)) =
+          *reinterpret_cast<uint4*>(dst + swz<128>(rr, (ch & 7) * 16)) =
               make_uint4(h[0], h[1], h[2], h[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars[kQFull + m]);
+        if constexpr (H == 2) {
+          named_bar_sync(pair, 64);
+          f = factor[row];
+        }
       }
-      float ref = 0.0f, l = 0.0f;
-      bool unset = vis > 0, row_nan = false;   // (a row that sees nothing needs none)
+      float ref = 0.0f, l = 0.0f;              // l: of this half's page
+      bool unset = vis > 0, row_nan = false;   // (a row that sees nothing needs no reference)
       if (x.take >= 0) {
         // Continue from the CTA before: it does this piece first.
         const uint8_t* st = p.plan.state + x.take * state_bytes(DIM);
@@ -463,178 +506,239 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
                        : "=r"(flag)
                        : "l"(p.plan.flags + x.take)
                        : "memory");
-          if (flag == 256) break;   // 256 threads have written theirs
+          if (flag == 2 * LY::kRowThreads) break;   // all softmax threads have written theirs
           if ((uint64_t)(clock64() - began) > (1ull << 32)) {
             there = false;
             break;
           }
           __nanosleep(200);
         }
-        if (!__all_sync(0xffffffffu, there)) {
-          failed = true;
-          break;
-        }
+        if (!__all_sync(0xffffffffu, there)) failed = true;
         const int rr = m * kTile + row;
-        const float4* so = reinterpret_cast<const float4*>(st);
+        const float4* so = reinterpret_cast<const float4*>(st) + half * (DIM / 4 / H) * kRows;
 #pragma unroll 4
-        for (int d = 0; d < DIM; d += 4) {
+        for (int d = 0; d < DIM / H; d += 4) {
           const float4 o = so[(d / 4) * kRows + rr];
           const float v[4] = {o.x, o.y, o.z, o.w};
           tmem_st4(t_o + d, v);
         }
         tmem_wait_st();
-        const float4 ml = reinterpret_cast<const float4*>(st + kRows * DIM * 4)[rr];
+        const float4 ml =
+            reinterpret_cast<const float4*>(st + kRows * DIM * 4)[half * kRows + rr];
         ref = ml.x;
         l = ml.y;
         unset = ml.z != 0.0f;
         row_nan = ml.w != 0.0f;
-        const uint16_t* sn = reinterpret_cast<const uint16_t*>(st + kRows * (DIM * 4 + 16));
+        const uint16_t* sn =
+            reinterpret_cast<const uint16_t*>(st + kRows * (DIM * 4 + 32)) + half * NB * kRows;
         if (row_nan)
-          for (int c = 0; c < DIM / 16; ++c) row_bits[c] = sn[c * kRows + rr];
+          for (int c = 0; c < NB; ++c) row_bits[c] = sn[c * kRows + rr];
       }
+      // Moves the reference by a whole number of powers of two to 3 above the row's
+      // largest exponent y, and the sum and the outputs of the tiles before with it
+      // (PV of the last one may still run). Returns the outputs' factor.
+      auto move_reference = [&](bool move, float y, int j) {
+        const float by = move ? reference_step(ref, ceilf(y)) : 0.0f;
+        const float al = by == 0.0f ? 1.0f
+                         : unset || by > 126.0f
+                             ? 0.0f
+                             : __uint_as_float((uint32_t)(127 - (int)by) << 23);
+        if (move) {
+          ref += by;
+          l *= al;
+          unset = false;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, al != 1.0f)) {
+          if (j > x.j0) wait(kPvDone + m, tiles - 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < DIM / H; c += 16) {
+            float o[16];
+            tmem_ld<16>(t_o + c, o);
+            tmem_fence<16>(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= al;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) tmem_st4(t_o + c + i, o + i);
+          }
+          tmem_wait_st();
+        }
+        return al;
+      };
       uint32_t g = kv;         // tile of the CTA
       for (int j = any ? x.j0 : x.j1; j < x.j1; ++j, ++g) {
         const int pos0 = j * kTile;
         if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kSFull + m], tiles & 1))) {
           failed = true;
-          break;
+          if constexpr (H == 1) break;
         }
         tc_fence_after();
-        // 64 columns (one page, one scale) at a time, positions 64-127 first: P
-        // may go over the upper half of S, which is in registers by then.
-        float2 s[32];
-        float* const s1 = reinterpret_cast<float*>(s);
-        const float4 mt0 = meta[(g & 3) * 2], mt1 = meta[(g & 3) * 2 + 1];
-        // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
-        const int end0 = mt0.w != 0.0f ? vis - pos0 : 0, end1 = mt1.w != 0.0f ? vis - pos0 - 64 : 0;
-        const float g0 = f * mt0.x, g1 = f * mt1.x;
-        // s = exponents relative to the reference; returns the largest.
-        auto exponents = [&](int half) {
-          tmem_ld32(t_s + 64 * half, s1);
-          tmem_ld32(t_s + 64 * half + 32, s1 + 32);
-          const float gg = half ? g1 : g0, cc = (half ? mt1.y : mt0.y) - ref;
-          const float2 g2 = make_float2(gg, gg), c2 = make_float2(cc, cc);
-          const int end = half ? end1 : end0;
-          tmem_fence<64>(s1);
+        if constexpr (H == 2) {
+          // This thread's page: (key scale, log2 of 8 times the value scale, its
+          // reciprocal, valid). Its S is read twice, for the largest and for the
+          // weights: 64 values do not fit in the registers of 24 warps.
+          const float4 mt = meta[(g & 3) * 2 + half];
+          const int end = mt.w != 0.0f ? vis - pos0 - half * kPage : 0;
+          const float gg = f * mt.x;
+          float s[32];
+          // 32 columns of S, what the row does not see at -infinity.
+          auto load = [&](int q) {
+            tmem_ld32(t_s + 32 * q, s);
+            tmem_fence<32>(s);
+          };
+          auto mask = [&](int q) {
+            if (end < kPage) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = fma2(s[i], g2, c2);
-          if (end < 64) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s1[i] = i < end ? s1[i] : -INFINITY;
-          }
-          float top[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) top[u] = fmaxf(s1[u], s1[4 + u]);
-#pragma unroll
-          for (int i = 8; i < 64; i += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) top[u] = fmaxf(fmaxf(top[u], s1[i + u]), s1[i + 4 + u]);
-          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        };
-        // Moves the reference of rows with `move` by a whole number of powers of
-        // two, to about their largest, y, and the sums and outputs so far with it:
-        // O of the tiles before (PV of the last may still run) and, at half 0,
-        // P of this tile's half 1, which nobody has read yet.
-        auto rebase = [&](bool move, float y, bool half1_in) {
-          const float by = move ? reference_step(ref, ceilf(y)) : 0.0f;
-          const float al = by == 0.0f ? 1.0f
-                           : unset || by > 126.0f
-                               ? 0.0f
-                               : __uint_as_float((uint32_t)(127 - (int)by) << 23);
-          if (move) {
-            ref += by;
-            l *= al;
-            unset = false;
-          }
-          if (!__any_sync(0xffffffffu, al != 1.0f)) return;
-          if (j > 0) {
-            if (j > x.j0 &&
-                !__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1)))
-              failed = true;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < DIM; c += 16) {
-              float o[16];
-              tmem_ld<16>(t_o + c, o);
-              tmem_fence<16>(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= al;
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) tmem_st4(t_o + c + i, o + i);
+              for (int i = 0; i < 32; ++i) s[i] = 32 * q + i < end ? s[i] : -INFINITY;
             }
-          }
-          if (half1_in) {
-            const __half2 h = __float2half2_rn(al);
-#pragma unroll 1
-            for (int c = 32; c < 64; c += 16) {
-              float o[16];
-              tmem_ld<16>(t_p + c, o);
-              tmem_fence<16>(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), h);
-                o[i] = *reinterpret_cast<const float*>(&w);
-              }
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) tmem_st4(t_p + c + i, o + i);
-            }
-          }
-          tmem_wait_st();
-        };
-        if (__any_sync(0xffffffffu, unset)) {
-          const float y = fmaxf(exponents(0), exponents(1));
-          rebase(unset && y > -INFINITY, y, false);
-        }
-#pragma unroll
-        for (int half = 1; half >= 0; --half) {
-          // Rarely a weight would pass 2^15: the exponents again, with a new
-          // reference (3 above the largest, or NaN: the loop ends).
+          };
+          // Rarely a weight would pass 2^15 (or the row has no reference yet): again,
+          // with a new one (3 above the largest, or NaN: the loop ends).
           while (true) {
-            const float y = exponents(half);
-            const bool move = y > 15.0f;
-            if (!__any_sync(0xffffffffu, move)) break;
-            rebase(move, y, half == 0);
+            // (gg is not negative: the largest exponent is that of the largest S.)
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              load(q);
+              mask(q);
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], s[i + k]), s[i + 4 + k]);
+            }
+            float y =
+                __fmaf_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), gg, mt.y - ref);
+            const float most = unset ? -INFINITY : 15.0f;
+            if (!named_bar_or(pair, 64, y > most)) break;
+            swap[half] = y;
+            named_bar_sync(pair, 64);
+            y = fmaxf(swap[0], swap[1]);
+            move_reference(y > most, y, j);
           }
-          if (LY::kApart && half == 0) {
-            tc_fence_before();
-            mbar_arrive(&bars[kSFree + m]);
-          }
-          uint32_t h[32];
+          // The weights; P's columns are free once PV of the last tile has ended.
+          if (tiles > 0) wait(kPvDone + m, tiles - 1);
+          tc_fence_after();
+          const float cc = mt.y - ref;
+          const float2 g2 = make_float2(gg, gg), c2 = make_float2(cc, cc);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 e = make_float2(ex2(s[i].x), ex2(s[i].y));
-            sum = add2(sum, e);
-            const __half2 w = __floats2half2_rn(e.x, e.y);
-            h[i] = *reinterpret_cast<const uint32_t*>(&w);
+          for (int q = 0; q < 2; ++q) {
+            load(q);
+            if (q == 1) {
+              tc_fence_before();
+              mbar_arrive(&bars[kSFree + m]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 e = fma2(make_float2(s[i], s[i + 1]), g2, c2);
+              s[i] = e.x;
+              s[i + 1] = e.y;
+            }
+            mask(q);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 e = make_float2(ex2(s[i]), ex2(s[i + 1]));
+              sum = add2(sum, e);
+              const __half2 z = __floats2half2_rn(e.x, e.y);
+              w[i / 2] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+            tmem_st16u(t_p + 16 * q, w);
           }
-          // (The columns of P apart are free once PV of the last tile has ended; S
-          // over P was issued behind that.)
-          if (LY::kApart && half == 1 && tiles > 0) {
-            if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1)))
-              failed = true;
-            tc_fence_after();
+          l = __fmaf_rn(sum.x + sum.y, mt.z, l);
+        } else {
+          // 64 columns (one page, one scale) at a time, positions 64-127 first: P
+          // may go over the upper half of S, which is in registers by then.
+          float2 s[32];
+          float* const s1 = reinterpret_cast<float*>(s);
+          const float4 mt0 = meta[(g & 3) * 2], mt1 = meta[(g & 3) * 2 + 1];
+          // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
+          const int end0 = mt0.w != 0.0f ? vis - pos0 : 0, end1 = mt1.w != 0.0f ? vis - pos0 - 64 : 0;
+          const float g0 = f * mt0.x, g1 = f * mt1.x;
+          // s = exponents relative to the reference; returns the largest.
+          auto exponents = [&](int page) {
+            tmem_ld32(t_s + 64 * page, s1);
+            tmem_ld32(t_s + 64 * page + 32, s1 + 32);
+            const float gg = page ? g1 : g0, cc = (page ? mt1.y : mt0.y) - ref;
+            const float2 g2 = make_float2(gg, gg), c2 = make_float2(cc, cc);
+            const int end = page ? end1 : end0;
+            tmem_fence<64>(s1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = fma2(s[i], g2, c2);
+            if (end < 64) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) s1[i] = i < end ? s1[i] : -INFINITY;
+            }
+            float top[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top[u] = fmaxf(s1[u], s1[4 + u]);
+#pragma unroll
+            for (int i = 8; i < 64; i += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) top[u] = fmaxf(fmaxf(top[u], s1[i + u]), s1[i + 4 + u]);
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          };
+          // P of this tile's page 1, which nobody has read yet, moves with a reference
+          // that page 0 moves.
+          auto rebase = [&](bool move, float y, bool upper_in) {
+            const float al = move_reference(move, y, j);
+            if (upper_in && __any_sync(0xffffffffu, al != 1.0f)) {
+              const __half2 h = __float2half2_rn(al);
+#pragma unroll 1
+              for (int c = 32; c < 64; c += 16) {
+                float o[16];
+                tmem_ld<16>(t_p + c, o);
+                tmem_fence<16>(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), h);
+                  o[i] = *reinterpret_cast<const float*>(&w);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) tmem_st4(t_p + c + i, o + i);
+              }
+              tmem_wait_st();
+            }
+          };
+#pragma unroll
+          for (int page = 1; page >= 0; --page) {
+            // Rarely a weight would pass 2^15 (or the row has no reference yet): the
+            // exponents again, with a new one (3 above the largest, or NaN: the loop
+            // ends).
+            while (true) {
+              const float y = exponents(page);
+              const bool move = y > (unset ? -INFINITY : 15.0f);
+              if (!__any_sync(0xffffffffu, move)) break;
+              rebase(move, y, page == 0);
+            }
+            uint32_t h[32];
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float2 e = make_float2(ex2(s[i].x), ex2(s[i].y));
+              sum = add2(sum, e);
+              const __half2 w = __floats2half2_rn(e.x, e.y);
+              h[i] = *reinterpret_cast<const uint32_t*>(&w);
+            }
+            tmem_st16u(t_p + 32 * page, h);
+            tmem_st16u(t_p + 16 + 32 * page, h + 16);
+            l = __fmaf_rn(sum.x + sum.y, page ? mt1.z : mt0.z, l);
+            if (page == 1) tmem_wait_st();   // (page 0 may read it back)
           }
-          tmem_st16u(t_p + 32 * half, h);
-          tmem_st16u(t_p + 16 + 32 * half, h + 16);
-          l = __fmaf_rn(sum.x + sum.y, half ? mt1.z : mt0.z, l);
-          if (half == 1) tmem_wait_st();   // (half 0 may read it back)
         }
         // Where rows see different lengths, NaN values were taken out of the tile
         // and listed: the rows that see one get a NaN in that dim.
         if (pos0 + kTile > min_vis) {
-          if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kVFull + (g & 1)], (g >> 1) & 1))) {
-            failed = true;
-            break;
-          }
+          wait(kVFull + (g & 1), g >> 1);
           if (nan_tag[g & 1] == g + 1) {
             const uint16_t* map =
-                reinterpret_cast<const uint16_t*>(smem + LY::kNanMap + (g & 1) * LY::kNanMapBytes);
+                reinterpret_cast<const uint16_t*>(smem + LY::kNanMap + (g & 1) * LY::kNanMapBytes) +
+                half * NB;
             if (!row_nan)
-              for (int c = 0; c < DIM / 16; ++c) row_bits[c] = 0;
+              for (int c = 0; c < NB; ++c) row_bits[c] = 0;
             row_nan = true;
             for (int i = 0; i < kTile && pos0 + i < vis; ++i)
-              for (int c = 0; c < DIM / 16; ++c) row_bits[c] |= map[i * (DIM / 16) + c];
+              for (int c = 0; c < NB; ++c) row_bits[c] |= map[i * (DIM / 16) + c];
           }
         }
         tmem_wait_st();
@@ -642,21 +746,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         mbar_arrive(&bars[kPFull + m]);
         ++tiles;
       }
-      if (failed) break;
       kv += (uint32_t)(x.j1 - x.j0);
-      if (any && x.j1 > x.j0 &&
-          !__all_sync(0xffffffffu, mbar_wait_long(&bars[kPvDone + m], (tiles - 1) & 1))) {
-        failed = true;
-        break;
-      }
+      if (any && x.j1 > x.j0) wait(kPvDone + m, tiles - 1);
+      if constexpr (H == 2) failed = named_bar_or(pair, 64, failed);
+      if (failed) break;
       tc_fence_after();
       if (x.give >= 0) {
         uint8_t* st = p.plan.state + x.give * state_bytes(DIM);
         const int rr = m * kTile + row;
-        float4* so = reinterpret_cast<float4*>(st);
+        float4* so = reinterpret_cast<float4*>(st) + half * (DIM / 4 / H) * kRows;
         if (any) {
 #pragma unroll 1
-          for (int d = 0; d < DIM; d += 16) {
+          for (int d = 0; d < DIM / H; d += 16) {
             float o[16];
             tmem_ld<16>(t_o + d, o);
             tmem_fence<16>(o);
@@ -665,11 +766,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
               so[(d + i) / 4 * kRows + rr] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        reinterpret_cast<float4*>(st + kRows * DIM * 4)[rr] =
+        reinterpret_cast<float4*>(st + kRows * DIM * 4)[half * kRows + rr] =
             make_float4(ref, l, unset ? 1.0f : 0.0f, row_nan ? 1.0f : 0.0f);
-        uint16_t* sn = reinterpret_cast<uint16_t*>(st + kRows * (DIM * 4 + 16));
+        uint16_t* sn = reinterpret_cast<uint16_t*>(st + kRows * (DIM * 4 + 32)) + half * NB * kRows;
         if (row_nan)
-          for (int c = 0; c < DIM / 16; ++c) sn[c * kRows + rr] = row_bits[c];
+          for (int c = 0; c < NB; ++c) sn[c * kRows + rr] = row_bits[c];
         __threadfence();
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.plan.flags + x.give)
                      : "memory");
@@ -680,57 +781,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
         piece_done();
         continue;
       }
+      if constexpr (H == 2) {
+        swap[half] = l;
+        named_bar_sync(pair, 64);
+        l = swap[0] + swap[1];
+      }
       // Outputs by way of the row tile's Q buffer (its last S is long done), so
-      // that rows are written whole.
+      // that rows are written in long pieces. A warp does its half of the dims.
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(0.125f, l);
       uint8_t* stage = smem + LY::kQ + m * LY::kTileBytes;
 #pragma unroll 1
-      for (int c = 0; c < DIM; c += 32) {
-        float o[32];
+      for (int c = 0; c < DIM / H; c += 16) {
+        const int d0 = half * (DIM / H) + c;
+        float o[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) o[i] = 0.0f;
         if (x.nt > 0) {
-          tmem_ld32(t_o + c, o);
-          tmem_fence<32>(o);
+          tmem_ld<16>(t_o + c, o);
+          tmem_fence<16>(o);
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0.0f : o[i] * inv;
+        for (int i = 0; i < 16; ++i) o[i] = l == 0.0f ? 0.0f : o[i] * inv;
         if (row_nan) {
+          const uint32_t bits = row_bits[c >> 4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if ((row_bits[(c + i) >> 4] >> (i & 15)) & 1) o[i] = NAN;
+          for (int i = 0; i < 16; ++i)
+            if ((bits >> i) & 1) o[i] = NAN;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           uint32_t h[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * i + 2 * u], o[8 * i + 2 * u + 1]);
             h[u] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          *reinterpret_cast<uint4*>(stage + (c >> 6) * LY::kBlock +
-                                    swz<128>(row, ((c >> 3) & 7) * 16 + i * 16)) =
+          *reinterpret_cast<uint4*>(stage + (d0 >> 6) * LY::kBlock +
+                                    swz<128>(row, ((d0 >> 3) & 7) * 16 + i * 16)) =
               make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
       __syncwarp();
+      constexpr int OL = DIM / 8 / H, OI = 32 / OL;    // lanes of the row's part; rows of a step
 #pragma unroll
-      for (int i = 0; i < RL; ++i) {
-        const int rr = i * RI + sub;
+      for (int i = 0; i < OL; ++i) {
+        const int rr = i * OI + lane / OL, ch = half * OL + lane % OL;
         const uint4 y = *reinterpret_cast<const uint4*>(
             stage + (ch >> 3) * LY::kBlock + swz<128>((warp & 3) * 32 + rr, (ch & 7) * 16));
         if (rr < left)
           *reinterpret_cast<uint4*>(p.out + offset(rr, (int64_t)p.heads * DIM) + ch * 8) = y;
       }
-      __syncwarp();
-      if (lane < left)
+      if (half == 0 && lane < left)
         p.lse[offset(lane, (int64_t)p.heads * DIM) / DIM] =
             l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
+      // The next Q goes over what the other warp may still read.
+      if constexpr (H == 2)
+        named_bar_sync(pair, 64);
+      else
+        __syncwarp();
       piece_done();
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ loader
-    regs_dec<kRegsLoader>();
+    if constexpr (LY::kRegsLoader > 65536 / LY::kThreads)
+      regs_inc<LY::kRegsLoader>();
+    else
+      regs_dec<LY::kRegsLoader>();
     constexpr int NC = kTile * DIM / 16 / 128;     // 16-code chunks per thread and tile
     constexpr int RC = DIM / 16;                   // chunks per position
     const int lt = tid - kLoaderWarp * 32;
@@ -864,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
     }
     if (err_bits && lt == 0 && p.c.err != nullptr) atomicOr(p.c.err, err_bits);
   } else {
-    regs_dec<kRegsMma>();
+    regs_dec<LY::kRegsMma>();
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- MMA issuer
       // (the whole warp; one lane issues)
@@ -937,7 +1053,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const Params p
             if (leader) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_f16_ts(tmem + LY::kO + m * DIM, tmem + LY::kP + m * LY::kPStep + k * 8,
+                mma_f16_ts(tmem + LY::kO + m * DIM,
+                           tmem + LY::kP + m * LY::kPStep + k * 8,
                            vd + ((k * 16 * 128) >> 4), idesc_o, k > 0 ? 1u : (fresh ? 0u : 1u));
               mma_commit(&bars[kPvDone + m]);
               if (m == mts - 1) mma_commit(&bars[kVEmpty + (g & 1)]);
@@ -998,7 +1115,7 @@ cudaError_t launch(const Params& p, int dev, cudaStream_t stream) {
   // them resident.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Layout<DIM>::kThreads);
   cfg.dynamicSmemBytes = Layout<DIM>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
