@@ -15,7 +15,9 @@
 // The table work is a few thousand integers, bound by launches and memory
 // latency; page payloads are bound by HBM (each byte read and written once)
 // and are cut into 16 KB pieces so that every SM takes part however few pages
-// move.
+// move. Copying 366 MB takes 55.9 us and compacting a pool by moving 3 GB 475
+// us (6.5 and 6.4 TB/s counting reads and writes); a fork with its extend and
+// free takes 38 us of host time for 30 us on the GPU.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
