@@ -725,3 +725,61 @@ def test_append_dozens_of_tokens_to_many_requests(ds, dim):
     counts = [(37 * i) % 79 for i in range(66)]
     assert sum(counts) <= 40 * len(counts)
     _append_case(ds, [n + (53 * i) % 130 for i, n in enumerate(counts)], counts, 8, dim, seed=69)
+
+
+def test_offsets_beyond_32_bits(ds):
+    """The same request in a small cache and in the last pages of one of more
+    than 4 GB: append, decode and prefill give the same bits."""
+    hk, dim, length = 8, 128, 300
+    pages = (9 << 29) // (2 * hk * 64 * dim)               # 4.8 GB
+    i32 = dict(dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(70)
+    kv = torch.randn((length, 2, hk, dim), device=DEV, generator=g).to(torch.bfloat16)
+    q = torch.randn((40, 16, dim), device=DEV, generator=g).to(torch.bfloat16)
+    starts, lens = torch.tensor([0, length], **i32), torch.tensor([length], **i32)
+    qs = torch.tensor([0, 40], **i32)
+    got = []
+    for n in (8, pages):
+        codes = torch.empty((n, 2, hk, 64, dim), dtype=torch.uint8, device=DEV)
+        scales = torch.empty((n, 2, hk), device=DEV)
+        ids = torch.arange(n - 1, n - 6, -1, device=DEV)
+        table = ids.int()[None].contiguous()
+        ds.kv8_append(kv[:, 0], kv[:, 1], starts, table, lens, codes, scales)
+        got.append((ds.kv8_decode(q[None], codes, scales, table, lens, 0.09)[0][0],
+                    ds.kv8_prefill(q, qs, codes, scales, table, lens, 0.09)[0],
+                    codes[ids].clone()))
+        ds.pages_copy([codes, scales], ids[:1].int(), torch.tensor([0], **i32))
+        torch.cuda.synchronize()
+        assert torch.equal(codes[0], codes[ids[0]]) and torch.equal(scales[0], scales[ids[0]])
+        del codes
+    a, b = got
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    held = torch.arange(320, device=DEV).view(5, 1, 1, 64, 1) < length
+    assert torch.equal(torch.where(held, a[2], 0), torch.where(held, b[2], 0))
+
+
+def test_prefill_on_two_streams_at_once(ds):
+    c = Cache([2500, 1300, 3000], 2, 64, seed=71)
+    codes, scales, table, lens = c.device()
+    starts = torch.tensor([0, 700, 1500, 2300], dtype=torch.int32, device=DEV)
+    q = c.q(2300, 8).to(DEV)
+    qs = [q, -q]
+    want = [ds.kv8_prefill(x, starts, codes, scales, table, lens, 0.1)[0] for x in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got.append((i, ds.kv8_prefill(qs[i], starts, codes, scales, table, lens, 0.1,
+                                          stream=s)[0]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in got)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_of_one_long_request(ds, dim):
+    """One token on a long context, and a group whose rows fill one row tile and
+    a little of the next."""
+    c = Cache([20000], 1, dim, seed=72)
+    _prefill(ds, c, [1], 3)
+    _prefill(ds, c, [43], 3)

@@ -317,3 +317,30 @@ def test_refusals_of_pools(ds):
         ds.pages_copy([torch.zeros((4, 64), device=DEV), torch.zeros((5, 64), device=DEV)], one, one)
     with pytest.raises(Exception, match="page_bytes"):
         ds.pages_copy([torch.zeros((4, 6), dtype=torch.uint8, device=DEV)], one, one)
+
+
+@pytest.mark.parametrize("count", [16, 17, 128])
+def test_many_pools_on_another_stream(ds, count):
+    s = State(90, 12, [700, 64, 130, 0, 0], seed=12, share=[(0, 2, 2)])
+    g = torch.Generator(device=DEV).manual_seed(13)
+    s.pools = [torch.randint(-9, 9, (90, 4 * (i % 5 + 1)), generator=g, device=DEV,
+                             dtype=torch.int32) for i in range(count)]
+    refs, table, lens = s.device()
+    parents, kids = _i32([0, 2]), _i32([3, 4])
+    moves = [(50, 80), (3, 85)]
+    want = _copied(s.pools, moves)
+    r, t, l, flags, m = oracle.pages_fork(s.refs, s.table, s.lens, [0, 2], [3, 4])
+    want = _copied(want, m)
+    side, err = torch.cuda.Stream(), _err()
+    src, dst = _i32([50, 3]), _i32([80, 85])
+    torch.cuda.synchronize()
+    ds.pages_copy(s.pools, src, dst, err_flag=err, stream=side)
+    ds.pages_fork(s.pools, refs, table, lens, parents, kids, err_flag=err, stream=side)
+    s.check(r, t, l, flags, err)
+    assert all(torch.equal(a, b) for a, b in zip(s.pools, want))
+    r2, t2, f2, n, m = oracle.pages_compact(r, t, l)
+    want = _copied(want, m)
+    out = ds.pages_compact(s.pools, refs, table, lens, err_flag=err, stream=side)
+    torch.cuda.synchronize()
+    assert int(out[2]) == n and out[0].tolist() == t2 and out[1].tolist() == r2
+    assert all(torch.equal(a, b) for a, b in zip(s.pools, want))
