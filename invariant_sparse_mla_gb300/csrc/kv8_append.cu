@@ -108,15 +108,22 @@ __device__ __forceinline__ bool find_unit(const Params& p, int64_t unit, bool re
   return true;
 }
 
-__device__ __forceinline__ float amax8(uint4 x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float a = 0.0f;
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    a = fmaxf(a, fmaxf(fabsf(__uint_as_float(w[u] << 16)),
-                       fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
-  return a;
+__device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
+
+// Largest magnitudes, two at a time (a NaN loses against any number).
+struct Amax {
+  __nv_bfloat162 m = pair(0u);
+  __device__ __forceinline__ void add(uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = __hmax2(m, __habs2(pair(w[u])));
+  }
+  __device__ __forceinline__ float value() const {
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
 
 __device__ __forceinline__ float warp_max(float a) {
 #pragma unroll
@@ -130,27 +137,33 @@ __device__ __forceinline__ float new_scale(float old, float a) {
 }
 
 // Eight values over the scale. Dividing by a power of two is multiplying by
-// its reciprocal, exactly; a scale that a caller set to something else takes
-// the division.
+// its reciprocal, exactly, also in bf16 (what falls below bf16's normal range
+// rounds to a code of 0); a scale that a caller set to something else takes the
+// division.
 struct Quantizer {
-  float s, inv;
+  float s;
+  __nv_bfloat162 inv;
   bool pow2;
   __device__ __forceinline__ explicit Quantizer(float scale) : s(scale) {
     const uint32_t b = __float_as_uint(scale);
     pow2 = (b & 0x7FFFFFu) == 0u && b >= (67u << 23) && b <= (247u << 23);
-    inv = pow2 ? __uint_as_float((254u << 23) - b) : 0.0f;
+    const uint32_t h = ((254u << 23) - b) >> 16;
+    inv = pair(pow2 ? h | (h << 16) : 0u);
   }
   __device__ __forceinline__ uint2 operator()(uint4 x) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o[2] = {0u, 0u};
+    uint32_t b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float f0 = __uint_as_float(w[u] << 16), f1 = __uint_as_float(w[u] & 0xFFFF0000u);
-      const uint32_t b = pow2 ? e4m3x2(f0 * inv, f1 * inv)
-                              : e4m3x2(__fdiv_rn(f0, s), __fdiv_rn(f1, s));
-      o[u >> 1] |= b << (16 * (u & 1));
+      if (pow2) {
+        const __nv_bfloat162 y = __hmul2(pair(w[u]), inv);
+        b[u] = e4m3x2(__low2float(y), __high2float(y));
+      } else {
+        b[u] = e4m3x2(__fdiv_rn(__uint_as_float(w[u] << 16), s),
+                      __fdiv_rn(__uint_as_float(w[u] & 0xFFFF0000u), s));
+      }
     }
-    return make_uint2(o[0], o[1]);
+    return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
   }
 };
 
@@ -213,16 +226,16 @@ __global__ void __launch_bounds__(kThreads) kv8_append_page_kernel(const Params 
     fetch(h + kStages - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     uint4 x[kSteps];
-    float a = 0.0f;
+    Amax amax;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int slot = (tid + i * kThreads) / kRowChunks;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (slot >= u.had && slot < u.upto)
         x[i] = staged[((h - h0) % kStages * kSteps + i) * kThreads + tid];
-      a = fmaxf(a, amax8(x[i]));
+      amax.add(x[i]);
     }
-    a = warp_max(a);
+    float a = warp_max(amax.value());
     float* top = warp_top[h & 1];   // the last head's is still read by others
     if ((tid & 31) == 0) top[tid >> 5] = a;
     __syncthreads();
@@ -280,11 +293,11 @@ __global__ void __launch_bounds__(256) kv8_append_few_kernel(const Params p) {
     const int c = c0 + lane + 32 * i;
     x[i] = c < c1 ? at(c) : make_uint4(0u, 0u, 0u, 0u);
   }
-  float a = 0.0f;
+  Amax amax;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) a = fmaxf(a, amax8(x[i]));
-  for (int c = c0 + lane + 32 * kHeld; c < c1; c += 32) a = fmaxf(a, amax8(at(c)));
-  const float s = new_scale(old, warp_max(a));
+  for (int i = 0; i < kHeld; ++i) amax.add(x[i]);
+  for (int c = c0 + lane + 32 * kHeld; c < c1; c += 32) amax.add(at(c));
+  const float s = new_scale(old, warp_max(amax.value()));
   uint8_t* dst = p.c.pages + part * (int64_t)(kPage * DIM);
   if (u.had > 0 && s != old) {
     const float f = __fdiv_rn(old, s);
@@ -324,7 +337,7 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream) {
   // Few tokens a request (on average): a warp per (page, side, head). With 8
   // heads x 128, us of this kernel against the other one:
   //   requests x tokens   128 x 5   128 x 32   128 x 64   16 x 8   16 x 24
-  //                       4.4 13.4  11.8 15.9  19.9 18.4  3.1 4.0  5.6 4.2
+  //                       4.4 13.4  10.8 15.9  19.9 18.4  3.1 4.0  5.6 4.2
   // so up to 40 tokens, or 16 where few CTAs of the other one wait for a place.
   const int64_t units = a.tokens / kPage + 2 * a.c.requests;
   if (a.tokens <= (a.c.requests * a.c.kv_heads >= 512 ? 40 : 16) * a.c.requests) {
