@@ -1076,18 +1076,31 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       if (leader) mma_commit(&bars[kDrain]);
       __syncwarp();
       if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
-    } else if (warp == kMmaWarp + 1 && lane == 0) {
+    } else if (warp == kMmaWarp + 1) {
       // ----------------------------------------------------- piece lookups
+      // (every lane alike; the lanes then ask for the piece's q, which is read when
+      // the one before has ended)
       Scheduler sched(p);
       for (uint32_t i = 0;; ++i) {
         const Piece x = sched.next();
-        if (i >= 2 && !mbar_wait_long(&bars[kPieceEmpty + (i & 1)], ((i >> 1) - 1) & 1)) {
+        if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait_long(&bars[kPieceEmpty + (i & 1)],
+                                                              ((i >> 1) - 1) & 1))) {
           failed = true;
           break;
         }
-        pieces[i & 1] = x;
-        mbar_arrive(&bars[kPieceFull + (i & 1)]);
+        if (lane == 0) {
+          pieces[i & 1] = x;
+          mbar_arrive(&bars[kPieceFull + (i & 1)]);
+        }
         if (x.r < 0) break;
+        const int last = last_row_of(p, x.row0, x.n);
+        for (int rr = x.row0 + lane; rr <= last; rr += 32) {
+          const __nv_bfloat16* at = p.q + (x.t0 + rr / p.group) * p.q_stride +
+                                    (x.kvh * p.group + rr % p.group) * DIM;
+#pragma unroll
+          for (int d = 0; d < DIM; d += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + d));
+        }
       }
     }
     __syncwarp();
