@@ -568,9 +568,11 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       uint32_t g = kv;         // tile of the CTA
       for (int j = any ? x.j0 : x.j1; j < x.j1; ++j, ++g) {
         const int pos0 = j * kTile;
-        if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kSFull + m], tiles & 1))) {
+        if constexpr (H == 2) {
+          wait(kSFull + m, tiles);
+        } else if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kSFull + m], tiles & 1))) {
           failed = true;
-          if constexpr (H == 1) break;
+          break;
         }
         tc_fence_after();
         if constexpr (H == 2) {
