@@ -173,6 +173,7 @@ struct Walk {
   int raw;               // lens[r] as it is
   int tiles, span_tiles, spans;
   int hg, s;             // kv head * row_groups + row group; span
+  int kvh, rg;           // the two parts of hg
 };
 
 __device__ __forceinline__ int clamp_len(const Params& p, int len) {
@@ -200,9 +201,13 @@ __device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
     if (w.s >= w.spans) {   // also a request without positions
       w.s = 0;
       ++w.hg;
+      if (++w.rg == p.row_groups) {
+        w.rg = 0;
+        ++w.kvh;
+      }
     }
     if (w.spans == 0 || w.hg >= hgs) {
-      w.hg = 0;
+      w.hg = w.kvh = w.rg = 0;
       w.s = 0;
       if (++w.r >= p.c.requests) return false;
       walk_load(p, w);
@@ -365,6 +370,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     walk_load(p, w);
     const int64_t x = lo - start_s[1];
     w.hg = (int)(x / w.tiles);
+    w.kvh = w.hg / p.row_groups;
+    w.rg = w.hg % p.row_groups;
     const int tt = (int)(x % w.tiles);
     w.s = (tt + w.span_tiles - 1) / w.span_tiles;
     // The item's first tile (also where s is one past the last span).
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     };
     auto look = [&](const Walk& i) {
       Lookup k;
-      const int kvh = i.hg / p.row_groups, n = 2 * item_tiles(i);
+      const int kvh = i.kvh, n = 2 * item_tiles(i);
       const int block0 = i.s * i.span_tiles * 2;
       const int blocks = (i.len + kPage - 1) / kPage;
 #pragma unroll
@@ -576,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     // it is noted under that vote's tile, before this warp votes there.
     auto give_up = [&] { abort_s[(g + 1) & 1] = (int)(g + 2); };
     int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
+    int token = 0;             // of row tid
     // Requests without positions are no items: their outputs here.
     for (int64_t r = blockIdx.x; r < p.c.requests; r += gridDim.x) {
       if (row_len(p, r) > 0) continue;
@@ -586,8 +594,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     }
     while (some && !failed) {
       const int nt = item_tiles(w);
-      const int kvh = w.hg / p.row_groups, rg = w.hg % p.row_groups;
-      const int row0 = rg * p.rows;
+      const int kvh = w.kvh, row0 = w.rg * p.rows;
       const int rows = min(p.rows, p.next_n * p.group - row0);
       const int64_t qid = (int64_t)w.r * hgs + w.hg;
       // The Q pieces: warp w takes rows w, w + 8, ...; a row's largest |q| sets
@@ -595,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
       // results were read.)
       if (qid != last_q) {
         last_q = qid;
+        token = (row0 + tid) / p.group;
         constexpr int E = DIM / 32, NR = R8 / 8;
         float x[NR][E];
 #pragma unroll
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
       }
       // Row r's token j sees len - next_n + 1 + j positions (clamped).
       if (tid < R8) {
-        const int64_t v = (int64_t)w.raw - p.next_n + 1 + (row0 + tid) / p.group;
+        const int64_t v = (int64_t)w.raw - p.next_n + 1 + token;
         m_s[tid] = 0.0f;
         vis_s[tid] = (int)(v < 0 ? 0 : (v > w.len ? w.len : v));
       }
