@@ -33,7 +33,7 @@
 //                    reading S twice for want of registers costs more than the
 //                    shorter way to P gives: ragged prompts of dim 64 take 293 us
 //                    so and 332 with one thread a row, a chunk of dim 128 takes
-//                    1773 us with one thread and 1965 with two;
+//                    1767 us with one thread and 1965 with two;
 //   4 loader warps   codes from global memory, through registers, to f16 tiles
 //                    of K and V in shared memory (two buffers each): the copy
 //                    engine cannot widen them, and staging the codes in shared
@@ -49,7 +49,7 @@
 //
 // The bound is the way S -> softmax -> P -> O of a row tile: two of them in turn
 // keep the tensor pipe busy half the time (dim 128; the last 2048 of 32768
-// positions, 64 / 8 heads: 1773 us, 1202 TFLOP/s). Shared memory is near: an
+// positions, 64 / 8 heads: 1767 us, 1205 TFLOP/s). Shared memory is near: an
 // M 128 x N 128 x K 16 product reads 8 KB in its 64 cycles, and without the
 // loader's stores the same takes 1486 us, without the softmax 1410.
 
