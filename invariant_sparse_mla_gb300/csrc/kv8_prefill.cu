@@ -130,7 +130,7 @@ struct Layout {
 };
 
 enum Bar {
-  kQFull = 0,       // 2 (row tile): its 128 softmax threads
+  kQFull = 0,       // 2 (row tile): its softmax threads
   kKFull = 2,       // 2: the 128 loader threads
   kKEmpty = 4,      // 2: commit
   kVFull = 6,       // 2: the 128 loader threads
