@@ -449,6 +449,9 @@ int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stri
  * request r sees the first clamp(lens[r] - next_n + 1 + j, 0, 64 * bt_stride)
  * positions: s_i = scale * q . k_i, out = sum_i softmax(s)_i v_i, lse =
  * ln sum_i exp(s_i); a token that sees nothing gives out = 0, lse = -inf.
+ * (A weight times its page's value scale is held in 11 bits down to 2^-17 of
+ * the row's largest and in fewer below; under 2^-27 of it, it adds nothing to
+ * out. lse and the weights' sum are fp32.)
  *
  *  q            bfloat16, token (r, j) at q + (r * next_n + j) * q_stride
  *               elements, [num_heads, head_dim] contiguous; 16-byte aligned,
