@@ -16,8 +16,9 @@
 // latency; page payloads are bound by HBM (each byte read and written once)
 // and are cut into 16 KB pieces so that every SM takes part however few pages
 // move. Copying 366 MB takes 55.9 us and compacting a pool by moving 3 GB 475
-// us (6.5 and 6.4 TB/s counting reads and writes); a fork with its extend and
-// free takes 38 us of host time for 30 us on the GPU.
+// us (6.5 and 6.4 TB/s counting reads and writes); freeing, forking and
+// extending 96 of 256 rows, 98 MB copied, takes 44 us (the forking kernel 21 of
+// them, five launches most of the rest).
 
 #include <cuda_runtime.h>
 #include <stdint.h>
