@@ -451,7 +451,8 @@ int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stri
  * ln sum_i exp(s_i); a token that sees nothing gives out = 0, lse = -inf.
  * (A weight times its page's value scale is held in 11 bits down to 2^-17 of
  * the row's largest and in fewer below; under 2^-27 of it, it adds nothing to
- * out. lse and the weights' sum are fp32.)
+ * out. lse and the weights' sum are fp32. The form in which q is multiplied
+ * moves a score by at most 2^-18, whatever q holds.)
  *
  *  q            bfloat16, token (r, j) at q + (r * next_n + j) * q_stride
  *               elements, [num_heads, head_dim] contiguous; 16-byte aligned,
@@ -488,7 +489,8 @@ size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_he
  * ds_kv8_prefill_workspace_size() bytes, 256-byte aligned; its contents need
  * no initialisation. num_tokens * num_heads / num_kv_heads is below 2^31 - 256
  * and bt_stride at most 2^20 (a request's context is walked in order, and waits
- * have a limit).
+ * have a limit). An element of q below 2^-28 of its head's largest is taken
+ * with an error of up to 2^-39 of that one.
  *
  * A token's outputs depend on its own request alone, bit for bit, and not on
  * how the request's tokens are spread over calls.

@@ -10,7 +10,11 @@
 //   q = 2^-k (q0 + q1 / 32): |q| 2^k is at most 256, q0 = E4M3(q 2^k), q1 the
 //   rounded remainder times 32. A bf16 number has 8 significant bits and two
 //   pieces hold 2 x 4, so this is exact down to 2^-14 of the row's largest
-//   |q| and off by 2^-23 of that below.
+//   |q| and off by up to 2^-22 of that below, which moves a score by at most
+//   scale * a * 448 * the sum of what is lost. Where that passes 2^-18 (an
+//   element of q far above the others; its keys may well be 0) the softmax
+//   threads add the lost part's product with the keys in fp32: a decision of
+//   the row and the page, so that bits depend on nothing else.
 //
 // O^T = V^T P^T runs in f16: E4M3 to f16 is exact and one instruction for two
 // values, and a weight p b, kept as 2^3 p b <= 2^15 in f16, has 11 significant
@@ -71,6 +75,7 @@ constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay
 constexpr float kLog2PScale = 3.0f;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMinSpan = 1024, kMaxSpan = 4096;
+constexpr float kLostMax = 0x1p-18f;       // log2: what two pieces of q may lose of a score
 
 __host__ __device__ inline int span_of(int64_t len) {
   int s = kMinSpan;
@@ -129,7 +134,8 @@ struct Layout {
   static constexpr int kVis = kWarpMax + 4 * R8 * 4;        // positions each row sees
   static constexpr int kBy = kVis + R8 * 4;                 // by how much a reference moved
   static constexpr int kSet = kBy + R8 * 4;                 // whether the row has one
-  static constexpr int kMisc = kSet + R8 * 4;               // tmem slot, abort, start of work
+  static constexpr int kLost = kSet + R8 * 4;               // what a score may lose at key scale 1
+  static constexpr int kMisc = kLost + R8 * 4;              // tmem slot, abort, start of work
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= kBudget, "shared memory of an SM");
@@ -240,6 +246,94 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t b) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The power of two that brings a row's largest |q|, a, to [128, 256); it stays a
+// normal float.
+__device__ __forceinline__ int q_exponent(float a) {
+  const int k = a > 0.0f ? 7 - ((int)(__float_as_uint(a) >> 23) - 127) : 0;
+  return k > 120 ? 120 : (k < -120 ? -120 : k);
+}
+__device__ __forceinline__ float pow2f(int k) {
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+// Two values as two pieces each, and (exactly) what they leave out.
+struct Pieces {
+  uint32_t b0, b1;
+  float lost0, lost1;
+};
+__device__ __forceinline__ Pieces q_pieces(float u0, float u1) {
+  Pieces x;
+  x.b0 = to_e4m3x2(u0, u1);
+  const float2 h = from_e4m3x2(x.b0);
+  const float r0 = (u0 - h.x) * 32.0f, r1 = (u1 - h.y) * 32.0f;
+  x.b1 = to_e4m3x2(r0, r1);
+  const float2 t = from_e4m3x2(x.b1);
+  x.lost0 = (r0 - t.x) * 0.03125f;
+  x.lost1 = (r1 - t.y) * 0.03125f;
+  return x;
+}
+
+__device__ __forceinline__ float warp_top(float a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
+}
+
+// Adds to one TMEM column of the warp's lanes.
+__device__ __forceinline__ void tmem_add(uint32_t taddr, float x) {
+  float v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+               : "=f"(v)
+               : "r"(taddr)
+               : "memory");
+  tmem_fence<1>(&v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(v + x)
+               : "memory");
+  tmem_wait_st();
+}
+
+// Lane l's dims (DIM / 32 from l * DIM / 32 on) of a query row.
+template <int DIM>
+__device__ __forceinline__ void load_q(const __nv_bfloat16* row, int lane, float* x) {
+  constexpr int E = DIM / 32;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const uint32_t v = reinterpret_cast<const uint32_t*>(row + lane * E)[e / 2];
+    x[e] = __uint_as_float(v << 16);
+    x[e + 1] = __uint_as_float(v & 0xFFFF0000u);
+  }
+}
+
+// The part of a query row that its two pieces lose, times 2^k, times the codes
+// of this lane's key (of a lane that has none: nullptr).
+template <int DIM>
+__device__ __noinline__ float lost_product(const __nv_bfloat16* row, const uint8_t* key) {
+  constexpr int E = DIM / 32;
+  const int lane = threadIdx.x & 31;
+  float x[E], a = 0.0f;
+  load_q<DIM>(row, lane, x);
+#pragma unroll
+  for (int e = 0; e < E; ++e) a = fmaxf(a, fabsf(x[e]));
+  const float up = pow2f(q_exponent(warp_top(a)));
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const Pieces z = q_pieces(x[e] * up, x[e + 1] * up);
+    x[e] = z.lost0;
+    x[e + 1] = z.lost1;
+  }
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int d = 0; d < DIM; d += 4) {
+    const uint2 h = codes_to_f16(key ? *reinterpret_cast<const uint32_t*>(key + d) : 0u);
+    const float2 k0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+    const float2 k1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+    const float k[4] = {k0.x, k0.y, k1.x, k1.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sum = __fmaf_rn(__shfl_sync(0xffffffffu, x[e % E], (d + e) / E), k[e], sum);
+  }
+  return sum;
+}
+
 // Sums over the warp of four values a lane: lane l returns the sum of value
 // 2 * bit4(l) + bit3(l).
 __device__ __forceinline__ float warp_sum4(const float* v, int lane) {
@@ -297,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
   int* vis_s = reinterpret_cast<int*>(smem + LY::kVis);
   float* by_s = reinterpret_cast<float*>(smem + LY::kBy);
   int* set_s = reinterpret_cast<int*>(smem + LY::kSet);
+  float* lost_s = reinterpret_cast<float*>(smem + LY::kLost);
+  volatile int* lossy_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 48);   // a Q's number
   volatile int* move_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 40);
@@ -312,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     }
     mbar_fence_init();
     abort_s[0] = abort_s[1] = 0;
-    move_s[0] = move_s[1] = 0;
+    move_s[0] = move_s[1] = *lossy_s = 0;
     for (int r = 0; r < R8; ++r) set_s[r] = 0;
     start_s[0] = -1;
   }
@@ -584,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     auto give_up = [&] { abort_s[(g + 1) & 1] = (int)(g + 2); };
     int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
     int token = 0;             // of row tid
+    int queries = 0;           // Qs so far
     // Requests without positions are no items: their outputs here.
     for (int64_t r = blockIdx.x; r < p.c.requests; r += gridDim.x) {
       if (row_len(p, r) > 0) continue;
@@ -597,12 +694,17 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
       const int kvh = w.kvh, row0 = w.rg * p.rows;
       const int rows = min(p.rows, p.next_n * p.group - row0);
       const int64_t qid = (int64_t)w.r * hgs + w.hg;
+      auto q_row = [&](int row) {
+        return p.q + ((int64_t)w.r * p.next_n + row / p.group) * p.q_stride +
+               ((int64_t)kvh * p.group + row % p.group) * DIM;
+      };
       // The Q pieces: warp w takes rows w, w + 8, ...; a row's largest |q| sets
       // its power of two. (All S that read the last Q are complete: their
       // results were read.)
       if (qid != last_q) {
         last_q = qid;
         token = (row0 + tid) / p.group;
+        ++queries;
         constexpr int E = DIM / 32, NR = R8 / 8;
         float x[NR][E];
 #pragma unroll
@@ -610,17 +712,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
           const int r = warp + 8 * i;
 #pragma unroll
           for (int e = 0; e < E; ++e) x[i][e] = 0.0f;
-          if (r < rows) {
-            const int j = (row0 + r) / p.group, gh = (row0 + r) % p.group;
-            const __nv_bfloat16* src = p.q + ((int64_t)w.r * p.next_n + j) * p.q_stride +
-                                       ((int64_t)kvh * p.group + gh) * DIM + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const uint32_t v = reinterpret_cast<const uint32_t*>(src)[e / 2];
-              x[i][e] = __uint_as_float(v << 16);
-              x[i][e + 1] = __uint_as_float(v & 0xFFFF0000u);
-            }
-          }
+          if (r < rows) load_q<DIM>(q_row(row0 + r), lane, x[i]);
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
@@ -632,25 +724,36 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
             a = fmaxf(a, fabsf(x[i][e]));
             nan |= x[i][e] != x[i][e];
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          a = warp_top(a);
           nan = __any_sync(0xffffffffu, nan) || a == INFINITY;
-          // a 2^k in [128, 256); 2^k stays a normal float.
-          int k = a > 0.0f ? 7 - ((int)(__float_as_uint(a) >> 23) - 127) : 0;
-          k = k > 120 ? 120 : (k < -120 ? -120 : k);
-          const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+          const int k = q_exponent(a);
+          const float up = pow2f(k);
+          bool tiny = false;     // some element is too small for two pieces
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
             const float u0 = x[i][e] * up, u1 = x[i][e + 1] * up;
-            const uint32_t b0 = to_e4m3x2(u0, u1);
-            const float2 h = from_e4m3x2(b0);
-            const uint32_t b1 = to_e4m3x2((u0 - h.x) * 32.0f, (u1 - h.y) * 32.0f);
+            const Pieces z = q_pieces(u0, u1);
+            tiny |= (fabsf(u0) < 0x1p-7f && u0 != 0.0f) || (fabsf(u1) < 0x1p-7f && u1 != 0.0f);
             uint8_t* q0 = smem + LY::kQ;
-            *reinterpret_cast<uint16_t*>(q0 + swz<DIM>(r, lane * E + e)) = (uint16_t)b0;
-            *reinterpret_cast<uint16_t*>(q0 + swz<DIM>(R8 + r, lane * E + e)) = (uint16_t)b1;
+            *reinterpret_cast<uint16_t*>(q0 + swz<DIM>(r, lane * E + e)) = (uint16_t)z.b0;
+            *reinterpret_cast<uint16_t*>(q0 + swz<DIM>(R8 + r, lane * E + e)) = (uint16_t)z.b1;
           }
-          if (lane == 0)
-            f_s[r] = nan ? NAN : __uint_as_float((uint32_t)(127 - k) << 23) * p.scale_log2;
+          float lost = 0.0f;     // (a NaN row's scores are NaN whatever it loses)
+          if (!nan && __any_sync(0xffffffffu, tiny)) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const Pieces z = q_pieces(x[i][e] * up, x[i][e + 1] * up);
+              lost += fabsf(z.lost0) + fabsf(z.lost1);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lost += __shfl_xor_sync(0xffffffffu, lost, o);
+            if (lane == 0) *lossy_s = queries;
+          }
+          const float f = pow2f(-k) * p.scale_log2;
+          if (lane == 0) {
+            f_s[r] = nan ? NAN : f;
+            lost_s[r] = 448.0f * lost * fabsf(f);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars[kQReady]);   // (f_s is read behind the barrier below)
@@ -664,7 +767,10 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
 #pragma unroll
       for (int i = 0; i < RH; ++i) l[i] = 0.0f;
       uint32_t nan_rows = 0;    // rows that see a NaN value in this lane's dim
-      named_bar_sync(1, kSoftmax);   // f_s, m_s, vis_s
+      named_bar_sync(1, kSoftmax);   // f_s, m_s, vis_s, lost_s, lossy_s
+      float lost_top = 0.0f;    // most that a row of this warp may lose at key scale 1
+      if (*lossy_s == queries)
+        for (int i = 0; i < RH; ++i) lost_top = fmaxf(lost_top, lost_s[rh + i]);
       const int min_vis = vis_s[0];
       bool unset = true;        // some row has no reference yet
 
@@ -675,6 +781,18 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
         tc_fence_after();
         // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
         const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tok >> 6)];
+        if (lost_top * mt.x > kLostMax) {
+          // What q's pieces lose goes to S where it lies. (The page is there, and
+          // the warp's positions share it; behind the context nothing is read.)
+          const int64_t page = p.c.block_table[(int64_t)w.r * p.c.bt_stride + pos / kPage];
+          const uint8_t* key =
+              pos < w.len ? p.c.pages + ((page * 2 * p.c.kv_heads + kvh) * kPage + pos % kPage) * DIM
+                          : nullptr;
+#pragma unroll 1
+          for (int r = 0; r < RH; ++r)
+            if (lost_s[rh + r] * mt.x > kLostMax)
+              tmem_add(t_s + r, lost_product<DIM>(q_row(row0 + rh + r), key));
+        }
         float s[RH];
         {
           float lo[RH];

@@ -1,0 +1,101 @@
+"""GPU tests of the block-scaled 8-bit cache where its numbers leave the usual
+range: queries with one element far above the others, scores far below those
+that matter, long contexts, key scales and tables at their limits.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from harness import ensure_built
+from kv8_cases import DEV, Cache, bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ds():
+    return ensure_built()
+
+
+def _both(ds, c, q, counts, scale, **kw):
+    """(kernel, out, lse) of the last counts[r] (all equal) tokens by decode and
+    by prefill."""
+    codes, scales, table, lens = c.device()
+    n, h = counts[0], q.shape[1]
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+    q = q.to(DEV)
+    o, l = ds.kv8_decode(q.view(len(counts), n, h, c.dim), codes, scales, table, lens, scale, **kw)
+    yield "decode", o.flatten(0, 1), l.flatten(0, 1)
+    yield "prefill", *ds.kv8_prefill(q, starts, codes, scales, table, lens, scale, **kw)
+
+
+def _ref(c, q, counts, scale):
+    rows = oracle.kv8_visible(c.lens, counts, c.table.shape[1])
+    return oracle.kv8_attention(bits(q), rows, c.codes, c.scales, c.table, scale)
+
+
+def _close(out, lse, ref, dim, length, score=0.0):
+    """Within oracle.kv8_bounds, for scores that are off by `score` [T, heads]
+    more: that moves a weight, and the sum that divides it, by that factor."""
+    ref_out, ref_lse, weight, reach, _ = ref
+    tol, tol_lse = oracle.kv8_bounds(ref_out, ref_lse, weight, reach, dim, length)
+    score = np.broadcast_to(score, ref_lse.shape)
+    tol = tol + 1.01 * 2 * np.expm1(score)[..., None] * weight
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(o - ref_out) <= tol).all(), np.nanmax(np.abs(o - ref_out) / tol)
+    fin = np.isfinite(ref_lse)
+    assert np.array_equal(np.isneginf(l), ~fin)
+    tol_lse = tol_lse + score
+    assert (np.abs(l - ref_lse)[fin] <= tol_lse[fin]).all(), \
+        np.nanmax(np.abs(l - ref_lse)[fin] / tol_lse[fin])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lift", [9, 14, 17, 20, 22])
+@pytest.mark.parametrize("group,n", [(1, 1), (4, 3), (13, 3)])
+def test_one_element_of_q_far_above_the_others(ds, group, n, lift, dim):
+    """2^lift in one dim whose key codes are 0, in every other head: the other
+    dims alone make the score.
+
+    Decode may lose 2^-18 of a score (base 2) to its form of q. Prefill holds q
+    times a power of two, its largest at least 2^14, in f16, exact down to 2^-14
+    and with half steps of 2^-25 below: 2^-39 of the row's largest for each."""
+    c = Cache([700, 90, 1100], 2, dim, seed=80 + group)
+    c.codes[:, 0, :, :, 5] = 0
+    c.table[0, 2] = -1
+    counts, heads, scale = [n] * 3, 2 * group, 1 / math.sqrt(dim)
+    q = c.q(3 * n, heads)
+    q[:, ::2, 5] = 2.0 ** lift
+    q[0, 0, 5] *= -1.0
+    ref = _ref(c, q, counts, scale)
+    k = oracle.e4m3_to_float64(c.codes[:, 0]) * c.scales[:, 0, :, None, None].astype(np.float64)
+    keys = np.nanmax(np.abs(k).sum(-1))
+    top = q.abs().amax(-1).double().numpy()
+    for name, out, lse in _both(ds, c, q, counts, scale):
+        _close(out, lse, ref, dim, 1100,
+               2.0 ** -18 if name == "decode" else 2.0 ** -39 * top * keys * scale)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_such_a_row_changes_no_other(ds, dim):
+    """Neither its neighbours' bits, nor its own where it stands alone."""
+    c = Cache([700, 1500], 1, dim, seed=84)
+    c.codes[:, 0, :, :, 5] = 0
+    q = c.q(10, 7).to(DEV).view(2, 5, 7, dim)
+    codes, scales, table, lens = c.device()
+    want = ds.kv8_decode(q, codes, scales, table, lens, 0.1)
+    far = q.clone()
+    far[0, 3, 2, 5] = far[1, 0, 6, 5] = 2.0 ** 21
+    got = ds.kv8_decode(far, codes, scales, table, lens, 0.1)
+    torch.cuda.synchronize()
+    same = torch.ones(2, 5, 7, dtype=torch.bool, device=DEV)
+    same[0, 3, 2] = same[1, 0, 6] = False
+    assert torch.equal(got[0][same], want[0][same]) and torch.equal(got[1][same], want[1][same])
+    for r, j in ((0, 3), (1, 0)):
+        one = ds.kv8_decode(far[r:r + 1, j:j + 1].contiguous(), codes, scales,
+                            table[r:r + 1].contiguous(), lens[r:r + 1] - 4 + j, 0.1)
+        assert torch.equal(one[0][0, 0], got[0][r, j]) and torch.equal(one[1][0, 0], got[1][r, j])
