@@ -390,7 +390,8 @@ int ds_kv_cache_write(const void* latent, int64_t num_rows, const int64_t* slots
  *               value = code * scale of its page, side and head. Scales are
  *               positive and finite; ds_kv8_append writes powers of two.
  *               (A row whose largest score passes 2^22 in magnitude, where
- *               float32 cannot tell weights apart any more, can give NaN.
+ *               float32 cannot tell weights apart any more, can give NaN;
+ *               a score below float32's range counts as not seen.
  *               Where value scales of one request differ by a
  *               factor of 2^100 or more, a page of the small ones can drop
  *               out of a row's softmax.)

@@ -22,7 +22,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Two fp32 operations in one instruction.
 // By how much a row's reference m goes up for a tile whose largest exponent
 // relative to it is y (both in powers of two): to 3 above y, as a weight is
 // stored as 2^3 p b. From 2^23 on m and y are rounded by too much for that, and
@@ -30,7 +29,12 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float reference_step(float m, float y) {
   return fmaxf(fabsf(m), fabsf(y)) <= 0x1p23f ? y - 3.0f : NAN;
 }
+// A row's first reference comes from exponents above this. Below, a weight is 0
+// beside any score that can be a reference, and the row waits for one; if none
+// comes it is NaN.
+constexpr float kLowest = -0x1p23f;
 
+// Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, c, d;\n\t"

@@ -75,6 +75,7 @@ constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay
 constexpr float kLog2PScale = 3.0f;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMinSpan = 1024, kMaxSpan = 4096;
+constexpr float kOnlyLow = -0x1p30f;        // reference of a span's row that only has lower scores
 constexpr float kLostMax = 0x1p-18f;       // log2: what two pieces of q may lose of a score
 
 __host__ __device__ inline int span_of(int64_t len) {
@@ -133,7 +134,7 @@ struct Layout {
   static constexpr int kWarpMax = kAlpha + R8 * 4;          // 4 x R8 floats
   static constexpr int kVis = kWarpMax + 4 * R8 * 4;        // positions each row sees
   static constexpr int kBy = kVis + R8 * 4;                 // by how much a reference moved
-  static constexpr int kSet = kBy + R8 * 4;                 // whether the row has one
+  static constexpr int kSet = kBy + R8 * 4;                 // 1: the row has one; 2: only scores too low
   static constexpr int kLost = kSet + R8 * 4;               // what a score may lose at key scale 1
   static constexpr int kMisc = kLost + R8 * 4;              // tmem slot, abort, start of work
   static constexpr int kEnd = kMisc + 64;
@@ -928,9 +929,9 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
 #pragma unroll
             for (int v = 1; v < 4; ++v) top = fmaxf(top, wmax_s[v * R8 + tid]);
             const int vis = vis_s[tid];
-            const bool first = set_s[tid] == 0;
+            const bool first = set_s[tid] != 1;
             float by = 0.0f, al = 1.0f;
-            if (first ? top > -INFINITY : top > kTau + kLog2PScale) {
+            if (top > (first ? kLowest : kTau + kLog2PScale)) {
               // (By what the reference moves once rounded.)
               const float m = m_s[tid] - reference_step(m_s[tid], top);
               by = m_s[tid] - m;
@@ -938,7 +939,10 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
               m_s[tid] = m;
               set_s[tid] = 1;
             } else if (first) {
+              if (top > -INFINITY) set_s[tid] = 2;
               open = vis > pos0 + kTile;   // it may see something later
+              // (Where no join follows, the row's last tile makes its sum NaN.)
+              if (!open && w.spans == 1 && set_s[tid] == 2) by = NAN;
             }
             alpha_s[tid] = al;
             by_s[tid] = by;
@@ -1046,7 +1050,8 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
         for (int i = 0; i < RH; ++i)
           if (has_dim && rh + i < rows) at[i * DIM] = o[i] * (1.0f / kPScale);
         if (tid < rows)
-          p.part_ml[slot + tid] = make_float2(set_s[tid] ? -m_s[tid] : -INFINITY, sum_of(tid));
+          p.part_ml[slot + tid] = make_float2(
+              set_s[tid] == 1 ? -m_s[tid] : (set_s[tid] == 2 ? kOnlyLow : -INFINITY), sum_of(tid));
       }
       if (tid < R8) set_s[tid] = 0;
       named_bar_sync(1, kSoftmax);   // m_s and wmax_s are read before the next item writes them
@@ -1109,6 +1114,7 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
       acc[1] = __fmaf_rn(wt, v.y, acc[1]);
     }
   }
+  if (M == kOnlyLow) L = NAN;
   const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
   uint32_t b[E / 2];
 #pragma unroll

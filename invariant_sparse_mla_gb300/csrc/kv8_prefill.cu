@@ -84,7 +84,8 @@ struct Plan {
   uint8_t* state;        // [kMaxCtas] x state_bytes
 };
 // O [dim / 4][256 rows] float4, then (reference, sum, unset, NaN) for either
-// half and the NaN bits.
+// half (unset 2: the row has seen scores too low for a reference) and the NaN
+// bits.
 __host__ __device__ constexpr int64_t state_bytes(int dim) {
   return (int64_t)kRows * (dim * 4 + 32 + dim / 8);
 }
@@ -495,6 +496,7 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       }
       float ref = 0.0f, l = 0.0f;              // l: of this half's page
       bool unset = vis > 0, row_nan = false;   // (a row that sees nothing needs no reference)
+      bool low = false;                        // without one, the row saw scores too low for it
       if (x.take >= 0) {
         // Continue from the CTA before: it does this piece first.
         const uint8_t* st = p.plan.state + x.take * state_bytes(DIM);
@@ -528,6 +530,7 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         ref = ml.x;
         l = ml.y;
         unset = ml.z != 0.0f;
+        low = ml.z == 2.0f;
         row_nan = ml.w != 0.0f;
         const uint16_t* sn =
             reinterpret_cast<const uint16_t*>(st + kRows * (DIM * 4 + 32)) + half * NB * kRows;
@@ -610,7 +613,8 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
             }
             float y =
                 __fmaf_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), gg, mt.y - ref);
-            const float most = unset ? -INFINITY : 15.0f;
+            const float most = unset ? kLowest : 15.0f;
+            low |= unset && y > -INFINITY;
             if (!named_bar_or(pair, 64, y > most)) break;
             swap[half] = y;
             named_bar_sync(pair, 64);
@@ -709,7 +713,8 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
             // ends).
             while (true) {
               const float y = exponents(page);
-              const bool move = y > (unset ? -INFINITY : 15.0f);
+              const bool move = y > (unset ? kLowest : 15.0f);
+              low |= unset && y > -INFINITY;
               if (!__any_sync(0xffffffffu, move)) break;
               rebase(move, y, page == 0);
             }
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
           }
         }
         reinterpret_cast<float4*>(st + kRows * DIM * 4)[half * kRows + rr] =
-            make_float4(ref, l, unset ? 1.0f : 0.0f, row_nan ? 1.0f : 0.0f);
+            make_float4(ref, l, unset ? (low ? 2.0f : 1.0f) : 0.0f, row_nan ? 1.0f : 0.0f);
         uint16_t* sn = reinterpret_cast<uint16_t*>(st + kRows * (DIM * 4 + 32)) + half * NB * kRows;
         if (row_nan)
           for (int c = 0; c < NB; ++c) sn[c * kRows + rr] = row_bits[c];
@@ -783,6 +788,7 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         piece_done();
         continue;
       }
+      if (unset && low) l = NAN;
       if constexpr (H == 2) {
         swap[half] = l;
         named_bar_sync(pair, 64);

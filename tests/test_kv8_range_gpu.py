@@ -99,3 +99,81 @@ def test_such_a_row_changes_no_other(ds, dim):
         one = ds.kv8_decode(far[r:r + 1, j:j + 1].contiguous(), codes, scales,
                             table[r:r + 1].contiguous(), lens[r:r + 1] - 4 + j, 0.1)
         assert torch.equal(one[0][0, 0], got[0][r, j]) and torch.equal(one[1][0, 0], got[1][r, j])
+
+
+def _low_pages(c, low):
+    """The pages that `low` lists, of every request, get one key: -448 in dim 0
+    at a scale of 2^8, 0 elsewhere."""
+    for r in range(len(c.lens)):
+        for b in low:
+            if b < c.table.shape[1] and c.table[r, b] >= 0:
+                c.codes[c.table[r, b], 0] = 0
+                c.codes[c.table[r, b], 0, :, :, 0] = 0xFE
+                c.scales[c.table[r, b], 0] = 2.0 ** 8
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length,low", [
+    (400, [0, 1]), (400, [0]), (400, [1]), (400, [0, 1, 2, 3, 4]), (400, [2, 3]), (150, [0, 1]),
+    (2500, range(16)), (2500, range(16, 32)), (2500, range(39)), (2500, [0, 1, 16, 17, 32, 33]),
+    (2500, range(20)),
+])
+def test_scores_far_below_add_nothing(ds, length, low, dim):
+    """Pages whose scores are below -2^25, before, between and behind ordinary
+    ones: weights of 0 beside them, as if the pages were not there. A row that
+    sees no other score is NaN."""
+    low = list(low)
+    c = Cache([length, 77], 1, dim, seed=90)
+    counts, heads = [60] * 2, 3
+    c.lens[1] = 67                                    # (of the two pages it has)
+    _low_pages(c, low)
+    q = torch.as_tensor(c.rng.uniform(0.5, 2.0, (120, heads, dim)).astype(np.float32))
+    q *= torch.as_tensor(c.rng.choice([-1.0, 1.0], (120, heads, dim)).astype(np.float32))
+    q[..., 0] = 2.0 ** 12                             # (q in two pieces is exact: 2^-1 is left of it)
+    q = q.to(torch.bfloat16)
+    # Ordinary pages hold 0 in dim 0.
+    for p in range(c.pages):
+        if not (c.codes[p, 0, :, :, 0] == 0xFE).all():
+            c.codes[p, 0, :, :, 0] = 0
+    scale = 0.125
+    assert 448 * 2.0 ** 8 * 2.0 ** 12 * scale > 2.0 ** 25
+    rows = oracle.kv8_visible(c.lens, counts, c.table.shape[1])
+    there = c.table.copy()
+    there[:, [b for b in low if b < there.shape[1]]] = -1
+    ref = oracle.kv8_attention(bits(q), rows, c.codes, c.scales, there, scale)
+    only_low = np.array([v > 0 and all(b in low for b in range(-(-v // 64))) for _, v in rows])
+    assert np.array_equal(only_low, np.isneginf(ref[1]).all(1))
+    for _, out, lse in _both(ds, c, q, counts, scale):
+        o, l = out.cpu(), lse.cpu()
+        assert torch.isnan(o[only_low]).all() and torch.isnan(l[only_low]).all()
+        _close(o[~only_low], l[~only_low], tuple(x[~only_low] for x in ref[:4]) + (False,), dim,
+               length)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_low_scores_in_chunks_and_cut_runs(ds, dim):
+    """Items of very different lengths whose first 17 pages are low, so that
+    rows are handed over before they have a reference: the bits are those of
+    calls of one request each."""
+    lens, counts = [3000, 40, 2900, 1129, 1500], [700, 40, 1, 129, 300]
+    c = Cache(lens, 3, dim, seed=91)
+    c.codes[:, 0, :, :, 0] = 0
+    _low_pages(c, range(17))
+    q = c.q(sum(counts), 12)
+    q[..., 0] = 2.0 ** 12
+    q = q.to(DEV)
+    codes, scales, table, lens_d = c.device()
+    starts = np.concatenate([[0], np.cumsum(counts)])
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out, lse = ds.kv8_prefill(q, torch.as_tensor(starts, **i32), codes, scales, table, lens_d, 0.125)
+    torch.cuda.synchronize()
+    seen = torch.zeros(len(q), dtype=torch.bool, device=DEV)
+    for r, n in enumerate(counts):
+        lo, hi = int(starts[r]), int(starts[r + 1])
+        seen[lo:hi] = torch.arange(lens[r] - n + 1, lens[r] + 1, device=DEV) > 17 * 64
+        o, l = ds.kv8_prefill(q[lo:hi], torch.tensor([0, n], **i32), codes, scales,
+                              table[r:r + 1].contiguous(), lens_d[r:r + 1].contiguous(), 0.125)
+        assert torch.equal(o.nan_to_num(7.0), out[lo:hi].nan_to_num(7.0))
+        assert torch.equal(l.nan_to_num(7.0), lse[lo:hi].nan_to_num(7.0))
+    assert torch.isfinite(lse[seen]).all() and torch.isfinite(out[seen].float()).all()
+    assert torch.isnan(lse[~seen]).all() and torch.isnan(out[~seen].float()).all()
