@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
   const int64_t per = (p.c.requests + kThreads - 1) / kThreads;
   int64_t sum = 0;
   for (int64_t r = tid * per; r < p.c.requests && r < (tid + 1) * per; ++r)
-    sum += (row_len(p, r) + kTile - 1) / kTile * hgs;
+    sum += (row_len(p, r) + kTile - 1) / kTile * (int64_t)hgs;
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
   if (lo < hi && lo >= before && lo < before + sum) {
     int64_t base = before;
     for (int64_t r = tid * per; r < p.c.requests; ++r) {
-      const int64_t n = (row_len(p, r) + kTile - 1) / kTile * hgs;
+      const int64_t n = (row_len(p, r) + kTile - 1) / kTile * (int64_t)hgs;
       if (lo < base + n) {
         start_s[0] = r;
         start_s[1] = base;

@@ -177,3 +177,35 @@ def test_low_scores_in_chunks_and_cut_runs(ds, dim):
         assert torch.equal(l.nan_to_num(7.0), lse[lo:hi].nan_to_num(7.0))
     assert torch.isfinite(lse[seen]).all() and torch.isfinite(out[seen].float()).all()
     assert torch.isnan(lse[~seen]).all() and torch.isnan(out[~seen].float()).all()
+
+
+@pytest.mark.slow
+def test_decode_of_more_than_2_31_tiles(ds):
+    """2^28 positions (one page, 2^22 times) and 1024 heads: 2^31 tiles of 128
+    positions. Every page adds the same, so the outputs are those of one page and
+    lse is ln 2^22 above its.
+
+    65536 spans are joined one after the other in fp32: their sum, and the
+    outputs', are off by 2^16 2^-24 of it each; a span's own 4096 positions and
+    its weights (11 bits) add less than 2^-10, bf16 2^-8."""
+    hk, dim, blocks = 1024, 64, 1 << 22
+    c = Cache([64], hk, dim, seed=92, extra_pages=0, extra_width=0)
+    q = c.q(1, hk)
+    ref_out, ref_lse, weight, reach, _ = _ref(c, q, [1], 0.125)
+    codes, scales, _, _ = c.device()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table, lens = torch.zeros((1, blocks), **i32), torch.tensor([64 * blocks], **i32)
+    out = torch.full((1, 1, hk, dim), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((1, 1, hk), 7.0, device=DEV)
+    need = ds.kv8_decode_workspace_size(1, 1, hk, hk, dim, blocks)
+    free, _ = torch.cuda.mem_get_info()
+    if need + (1 << 30) > free:
+        pytest.skip(f"needs {need >> 30} GiB of workspace")
+    ds.kv8_decode(q.to(DEV)[None], codes, scales, table, lens, 0.125, out=out, lse=lse)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    o, l = out[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
+    assert (np.abs(o - ref_out) <= 2.0 ** -8 * np.abs(ref_out) +
+            (2 * 2.0 ** -8 + 2.0 ** -10) * 1.01 * weight).all()
+    want = ref_lse + math.log(blocks)
+    assert (np.abs(l - want) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -20 * np.abs(want)).all()
