@@ -569,7 +569,8 @@ int ds_pages_free(int32_t* refcounts, int64_t num_pages, int32_t* block_table, i
  * (length <= 0) and listed once: otherwise the later entry is skipped and
  * DS_DEVERR_ROWREQ set. The i-th copied page takes the i-th free page; a
  * child for which none is left stays empty and sets DS_DEVERR_NOPAGE. A page
- * outside the pool is taken over as it is and sets DS_DEVERR_PAGE.
+ * outside the pool is taken over as it is, also where it is a partly filled
+ * last one, and sets DS_DEVERR_PAGE.
  */
 int ds_pages_fork(const ds_page_pool* pools, int num_pools, int32_t* refcounts, int64_t num_pages,
                   int32_t* block_table, int64_t bt_stride, int32_t* lens, int64_t num_rows,

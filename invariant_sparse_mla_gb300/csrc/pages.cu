@@ -293,8 +293,8 @@ __device__ __forceinline__ int64_t need_before(const Workspace& w, int64_t i) {
   return block_sum(v, tmp);
 }
 
-// Fork: need = 1 where a partly filled page is copied, aux = the parent's
-// length, -1 for an entry that is skipped. Extend: need = pages to add, aux =
+// Fork: need = 1 where a partly filled page is copied (one outside the pool is
+// not), aux = the parent's length, -1 for an entry that is skipped. Extend: need = pages to add, aux =
 // the present length or -1. Everything is read before anything is written.
 template <bool FORK>
 __global__ void __launch_bounds__(kThreads) pages_plan_kernel(
@@ -328,7 +328,10 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(
   }
   if (ok && FORK) {
     aux = clamp_len(s.lens[a[i]], s.bt_stride);
-    need = aux % kPage != 0;
+    if (aux % kPage != 0) {
+      const int64_t page = s.table[a[i] * s.bt_stride + aux / kPage];
+      need = page >= 0 && page < s.num_pages;
+    }
   }
   if (ok && !FORK) {
     const int64_t len = clamp_len(s.lens[row], s.bt_stride), want = b[i];
@@ -370,16 +373,17 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(
     }
     if (threadIdx.x == 0) new_page = select_free(w, s.num_pages, segs, seg_at, (int)rank);
     __syncthreads();
-    const int64_t old = from[full];
-    const bool good = old >= 0 && old < s.num_pages;
     if (piece == 0 && threadIdx.x == 0) {
       to[full] = new_page;
       s.refs[new_page] = 1;
-      if (!good) raise(s.err, kErrPage);
     }
-    if (good && pools.pieces > 0) copy_piece(pools, piece, old, new_page);
+    if (pools.pieces > 0) copy_piece(pools, piece, (int64_t)from[full], (int64_t)new_page);
   }
   if (piece != 0) return;
+  if (!w.need[i] && len % kPage != 0 && threadIdx.x == 0) {
+    to[full] = from[full];
+    raise(s.err, kErrPage);
+  }
   for (int64_t j = threadIdx.x; j < full; j += kThreads) {
     const int page = from[j];
     to[j] = page;

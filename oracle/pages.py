@@ -62,16 +62,17 @@ def pages_fork(refs, table, lens, parents, children):
         length = min(max(before[2][a], 0), PAGE * width)
         full = length // PAGE
         if length % PAGE:
-            mine, rank = rank, rank + 1
-            if mine >= len(free):
-                flags.add("nopage")
-                continue
             src = before[1][a][full]
-            table[c][full] = free[mine]
-            refs[free[mine]] = 1
             if 0 <= src < len(refs):
+                mine, rank = rank, rank + 1
+                if mine >= len(free):
+                    flags.add("nopage")
+                    continue
+                table[c][full] = free[mine]
+                refs[free[mine]] = 1
                 copies.append((src, free[mine]))
             else:
+                table[c][full] = src
                 flags.add("page")
         for j in range(full):
             p = before[1][a][j]

@@ -344,3 +344,24 @@ def test_many_pools_on_another_stream(ds, count):
     torch.cuda.synchronize()
     assert int(out[2]) == n and out[0].tolist() == t2 and out[1].tolist() == r2
     assert all(torch.equal(a, b) for a, b in zip(s.pools, want))
+
+
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+def test_fork_takes_a_last_page_outside_the_pool_over(ds, bad):
+    """No page is taken for it, the child's entry is the parent's, and both rows'
+    attention leaves its positions out."""
+    s = State(40, 14, [700, 130, 100, 0, 0, 0], seed=14)
+    s.table[1][2] = bad
+    parents, children = [0, 1, 2], [3, 4, 5]
+    refs, table, lens = s.device()
+    r, t, l, flags, moves = oracle.pages_fork(s.refs, s.table, s.lens, parents, children)
+    assert flags == {"page"} and len(moves) == 2 and t[4][2] == bad
+    want = _copied(s.pools, moves)
+    err = _err()
+    ds.pages_fork(s.pools, refs, table, lens, _i32(parents), _i32(children), err_flag=err)
+    s.check(r, t, l, flags, err)
+    assert all(torch.equal(a, b) for a, b in zip(s.pools, want))
+    codes = torch.randint(0, 0x7F, (40, 2, 1, 64, 64), dtype=torch.uint8, device=DEV)
+    q = torch.randn((1, 1, 2, 64), device=DEV).to(torch.bfloat16).expand(6, 1, 2, 64).contiguous()
+    out, lse = ds.kv8_decode(q, codes, torch.full((40, 2, 1), 0.01, device=DEV), table, lens, 0.1)
+    assert torch.equal(out[4], out[1]) and torch.equal(lse[4], lse[1])
