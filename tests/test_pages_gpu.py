@@ -365,3 +365,37 @@ def test_fork_takes_a_last_page_outside_the_pool_over(ds, bad):
     q = torch.randn((1, 1, 2, 64), device=DEV).to(torch.bfloat16).expand(6, 1, 2, 64).contiguous()
     out, lse = ds.kv8_decode(q, codes, torch.full((40, 2, 1), 0.01, device=DEV), table, lens, 0.1)
     assert torch.equal(out[4], out[1]) and torch.equal(lse[4], lse[1])
+
+
+def test_a_fork_leaves_its_parents_outputs(ds):
+    """Attention of every row before a fork, after it, and after the children
+    have appended: the parents' is unchanged, the children's starts as theirs."""
+    hk, d, rows, pages = 2, 64, 4, 30
+    g = torch.Generator(device=DEV).manual_seed(15)
+    refs = torch.zeros(pages, dtype=torch.int32, device=DEV)
+    table = torch.full((rows, 4), -1, dtype=torch.int32, device=DEV)
+    lens = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    codes = torch.full((pages, 2, hk, 64, d), 0x7F, dtype=torch.uint8, device=DEV)
+    scales = torch.full((pages, 2, hk), float("nan"), device=DEV)
+    err = _err()
+
+    def grow(which, counts, new_lens):
+        ds.pages_extend(refs, table, lens, _i32(which), _i32(new_lens), err_flag=err)
+        x = torch.randn((sum(counts), 2, hk, d), generator=g, device=DEV).to(torch.bfloat16)
+        ds.kv8_append(x[:, 0], x[:, 1], _i32(np.concatenate([[0], np.cumsum(counts)])), table, lens,
+                      codes, scales, err_flag=err)
+
+    q = torch.randn((1, 1, 8, d), generator=g, device=DEV).to(torch.bfloat16)
+    q = q.expand(rows, 1, 8, d).contiguous()
+    look = lambda: ds.kv8_decode(q, codes, scales, table, lens, 0.125, err_flag=err)  # noqa: E731
+    grow([0, 1], [150, 64, 0, 0], [150, 64])
+    before = look()
+    ds.pages_fork([codes, scales], refs, table, lens, _i32([0, 1]), _i32([2, 3]), err_flag=err)
+    after = look()
+    grow([2, 3], [0, 0, 30, 7], [180, 71])
+    later = look()
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    for b, a, x in zip(before, after, later):
+        assert torch.equal(a[:2], b[:2]) and torch.equal(a[2:], b[:2])
+        assert torch.equal(x[:2], b[:2]) and not (x[2:] == b[:2]).flatten(1).all(1).any()
