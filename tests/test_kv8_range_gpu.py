@@ -209,3 +209,57 @@ def test_decode_of_more_than_2_31_tiles(ds):
             (2 * 2.0 ** -8 + 2.0 ** -10) * 1.01 * weight).all()
     want = ref_lse + math.log(blocks)
     assert (np.abs(l - want) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -20 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length", [32768, 32769, 45000, 65537, 131072, 131073, 140000])
+def test_decode_of_long_contexts(ds, length, dim):
+    """Spans of 1024, 2048 and 4096 positions (32 and 64 pages, a lane looks up
+    two of the latter), up to 32 and more of them; a page of the last span is
+    outside the pool."""
+    c = Cache([length, 300], 1, dim, seed=100, extra_width=0)
+    c.table[0, -(-length // 64) - 2] = -1
+    counts, heads, scale = [2, 2], 3, 1 / math.sqrt(dim)
+    q = c.q(4, heads)
+    codes, scales, table, lens = c.device()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = ds.kv8_decode(q.to(DEV).view(2, 2, heads, dim), codes, scales, table, lens, scale,
+                             err_flag=err)
+    _close(out.flatten(0, 1), lse.flatten(0, 1), _ref(c, q, counts, scale), dim, length)
+    assert int(err) == ds.DEVERR_PAGE
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("exponent", [-12, -9, -7, -5])
+def test_append_to_scales_that_are_no_powers_of_two(ds, exponent, few, dim):
+    """Partly filled pages whose scale is 1.2345 2^exponent: kept where it covers
+    the new tokens, grown (to a power of two) where it does not; a few tokens a
+    request (a warp each) or many (a CTA a page)."""
+    counts = [1, 5, 0, 12, 3] if few else [40, 100, 0, 64, 130]
+    lens = [n + had for n, had in zip(counts, [7, 60, 30, 64 + 33, 1])]
+    c = Cache([max(x, 0) for x in lens], 3, dim, seed=110 + exponent)
+    c.scales[...] = np.float32(1.2345) * 2.0 ** exponent
+    before = [x - n for x, n in zip(lens, counts)]
+    for r, x in enumerate(before):
+        for b in range(c.table.shape[1]):
+            if c.table[r, b] >= 0 and 64 * b + 64 > x:
+                at = c.codes[c.table[r, b], :, :, max(0, x - 64 * b):]
+                at[...] = c.rng.integers(0, 256, at.shape)
+    x = torch.as_tensor(c.rng.standard_normal((sum(counts), 2, 3, dim)).astype(np.float32))
+    x = (x * torch.exp2(torch.as_tensor(c.rng.integers(-3, 4, (sum(counts), 2, 3, 1))).float())) \
+        .to(torch.bfloat16)
+    starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    want = oracle.kv8_append(bits(x[:, 0]), bits(x[:, 1]), starts, lens, c.table, c.codes, c.scales)
+    codes, scales, table, lens_d = c.device()
+    kv = x.to(DEV)
+    ds.kv8_append(kv[:, 0], kv[:, 1], torch.as_tensor(starts).to(DEV), table, lens_d, codes, scales)
+    torch.cuda.synchronize()
+    assert np.array_equal(scales.cpu().numpy(), want[1])
+    got, ref = (oracle.e4m3_to_float64(a) for a in (codes.cpu().numpy(), want[0]))
+    assert np.array_equal(got, ref, equal_nan=True)
+    # (Both kinds are there, in one of the exponents at least.)
+    firsts = [c.table[r, x // 64] for r, x in enumerate(before) if counts[r] and x % 64]
+    grown = want[1][firsts] != c.scales[firsts]
+    assert exponent > -12 or grown.all()
+    assert exponent < -5 or not grown.all()
