@@ -453,7 +453,7 @@ int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stri
  * (A weight times its page's value scale is held in 11 bits down to 2^-17 of
  * the row's largest and in fewer below; under 2^-27 of it, it adds nothing to
  * out. lse and the weights' sum are fp32. The form in which q is multiplied
- * moves a score by at most 2^-18, whatever q holds.)
+ * moves a score by at most 2^-14, whatever q holds.)
  *
  *  q            bfloat16, token (r, j) at q + (r * next_n + j) * q_stride
  *               elements, [num_heads, head_dim] contiguous; 16-byte aligned,

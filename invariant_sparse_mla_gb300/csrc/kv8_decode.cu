@@ -11,9 +11,9 @@
 //   rounded remainder times 32. A bf16 number has 8 significant bits and two
 //   pieces hold 2 x 4, so this is exact down to 2^-14 of the row's largest
 //   |q| and off by up to 2^-22 of that below, which moves a score by at most
-//   scale * a * 448 * the sum of what is lost. Where that passes 2^-18 (an
-//   element of q far above the others; its keys may well be 0) the softmax
-//   threads add the lost part's product with the keys in fp32: a decision of
+//   scale * a * 448 * the sum of what is lost. Where that passes 2^-14 (an
+//   element of q hundreds of times the others; its keys may well be 0) the
+//   softmax threads add the lost part's product with the keys: a decision of
 //   the row and the page, so that bits depend on nothing else.
 //
 // O^T = V^T P^T runs in f16: E4M3 to f16 is exact and one instruction for two
@@ -76,7 +76,7 @@ constexpr float kLog2PScale = 3.0f;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMinSpan = 1024, kMaxSpan = 4096;
 constexpr float kOnlyLow = -0x1p30f;        // reference of a span's row that only has lower scores
-constexpr float kLostMax = 0x1p-18f;       // log2: what two pieces of q may lose of a score
+constexpr float kLostMax = 0x1p-14f;       // log2: what two pieces of q may lose of a score
 
 __host__ __device__ inline int span_of(int64_t len) {
   int s = kMinSpan;
@@ -279,17 +279,17 @@ __device__ __forceinline__ float warp_top(float a) {
   return a;
 }
 
-// Adds to one TMEM column of the warp's lanes.
-__device__ __forceinline__ void tmem_add(uint32_t taddr, float x) {
-  float v;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-               : "=f"(v)
+// Adds to two TMEM columns of the warp's lanes.
+__device__ __forceinline__ void tmem_add2(uint32_t taddr, float a, float b) {
+  float v[2];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];"
+               : "=f"(v[0]), "=f"(v[1])
                : "r"(taddr)
                : "memory");
-  tmem_fence<1>(&v);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(v + x)
+  tmem_fence<2>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr),
+               "f"(v[0] + a), "f"(v[1] + b)
                : "memory");
-  tmem_wait_st();
 }
 
 // Lane l's dims (DIM / 32 from l * DIM / 32 on) of a query row.
@@ -304,35 +304,79 @@ __device__ __forceinline__ void load_q(const __nv_bfloat16* row, int lane, float
   }
 }
 
-// The part of a query row that its two pieces lose, times 2^k, times the codes
-// of this lane's key (of a lane that has none: nullptr).
+// Adds what the pieces of up to eight query rows lose to S of the warp's 32
+// positions: the lost part times 2^29 (at most 2^14, 8 significant bits) and the
+// codes are exact in f16, and the product is summed in fp32. `row` is query row
+// lane / 4 of them or nullptr, `keys` the first position's codes, `there` how
+// many of them are in the context, `taddr` S of the first row. By mma.sync from
+// global memory, as there is no room in shared memory for two more pieces of q.
+// 32 x 5 tokens of 64 / 8 heads x 128 on 16384 positions: 268 us, 2055 us where
+// every row needs this.
 template <int DIM>
-__device__ __noinline__ float lost_product(const __nv_bfloat16* row, const uint8_t* key) {
-  constexpr int E = DIM / 32;
-  const int lane = threadIdx.x & 31;
-  float x[E], a = 0.0f;
-  load_q<DIM>(row, lane, x);
-#pragma unroll
-  for (int e = 0; e < E; ++e) a = fmaxf(a, fabsf(x[e]));
-  const float up = pow2f(q_exponent(warp_top(a)));
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const Pieces z = q_pieces(x[e] * up, x[e + 1] * up);
-    x[e] = z.lost0;
-    x[e + 1] = z.lost1;
-  }
-  float sum = 0.0f;
+__device__ __noinline__ void add_lost(const __nv_bfloat16* row, const uint8_t* keys, int there,
+                                      uint32_t taddr, int rows) {
+  // Lane 4 g + c holds dims [c, c + 1) * DIM / 4 of row g, and of positions g + 8 i;
+  // four of the dims a step. (Kept small: its registers are taken from those of
+  // the tiles that need none of this.)
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  auto q4 = [&](int s) {
+    return row ? reinterpret_cast<const uint2*>(row + c * (DIM / 4))[s] : make_uint2(0u, 0u);
+  };
+  float up = 0.0f;
 #pragma unroll 1
-  for (int d = 0; d < DIM; d += 4) {
-    const uint2 h = codes_to_f16(key ? *reinterpret_cast<const uint32_t*>(key + d) : 0u);
-    const float2 k0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
-    const float2 k1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
-    const float k[4] = {k0.x, k0.y, k1.x, k1.y};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      sum = __fmaf_rn(__shfl_sync(0xffffffffu, x[e % E], (d + e) / E), k[e], sum);
+  for (int s = 0; s < DIM / 16; ++s) {
+    const uint2 w = q4(s);
+    up = fmaxf(fmaxf(up, fabsf(__uint_as_float(w.x << 16))),
+               fmaxf(fabsf(__uint_as_float(w.x & 0xFFFF0000u)),
+                     fmaxf(fabsf(__uint_as_float(w.y << 16)),
+                           fabsf(__uint_as_float(w.y & 0xFFFF0000u)))));
   }
-  return sum;
+  up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+  up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+  up = pow2f(q_exponent(up));
+  auto lost = [&](uint32_t w) {
+    const Pieces z =
+        q_pieces(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+    const __half2 h = __floats2half2_rn(z.lost0 * 0x1p29f, z.lost1 * 0x1p29f);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  };
+  float d[2][4] = {};
+  keys += g * DIM + c * (DIM / 4);
+#pragma unroll 1
+  for (int s = 0; s < DIM / 16; ++s) {
+    const uint2 w = q4(s);
+    const uint32_t b0 = lost(w.x), b1 = lost(w.y);
+    auto codes = [&](int i) {
+      const uint32_t k =
+          8 * i + g < there ? reinterpret_cast<const uint32_t*>(keys + 8 * i * DIM)[s] : 0u;
+      return codes_to_f16(k);
+    };
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint2 lo = codes(2 * m), hi = codes(2 * m + 1);
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+          "{%8,%9}, {%0,%1,%2,%3};"
+          : "+f"(d[m][0]), "+f"(d[m][1]), "+f"(d[m][2]), "+f"(d[m][3])
+          : "r"(lo.x), "r"(hi.x), "r"(lo.y), "r"(hi.y), "r"(b0), "r"(b1));
+    }
+  }
+  // Position `lane` of row j lies in d[lane / 16][2 (lane / 8 % 2) + j % 2] of
+  // lane 4 (lane % 8) + j / 2.
+#pragma unroll 1
+  for (int j = 0; j < 8; j += 2) {
+    float x[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = __shfl_sync(0xffffffffu, d[i / 2][2 * (i % 2) + u], (lane & 7) * 4 + j / 2);
+        if (lane / 8 == i) x[u] = v;
+      }
+    }
+    if (j < rows) tmem_add2(taddr + j, x[0] * 0x1p-29f, x[1] * 0x1p-29f);
+  }
+  tmem_wait_st();
 }
 
 // Sums over the warp of four values a lane: lane l returns the sum of value
@@ -784,15 +828,19 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
         const float4 mt = meta[(g & (kMetaSlots - 1)) * 2 + (tok >> 6)];
         if (lost_top * mt.x > kLostMax) {
           // What q's pieces lose goes to S where it lies. (The page is there, and
-          // the warp's positions share it; behind the context nothing is read.)
-          const int64_t page = p.c.block_table[(int64_t)w.r * p.c.bt_stride + pos / kPage];
-          const uint8_t* key =
-              pos < w.len ? p.c.pages + ((page * 2 * p.c.kv_heads + kvh) * kPage + pos % kPage) * DIM
-                          : nullptr;
+          // the warp's positions share it.)
+          const int first = pos0 + quad * 32;
+          const int64_t page = p.c.block_table[(int64_t)w.r * p.c.bt_stride + first / kPage];
+          const uint8_t* keys =
+              p.c.pages + ((page * 2 * p.c.kv_heads + kvh) * kPage + first % kPage) * DIM;
 #pragma unroll 1
-          for (int r = 0; r < RH; ++r)
-            if (lost_s[rh + r] * mt.x > kLostMax)
-              tmem_add(t_s + r, lost_product<DIM>(q_row(row0 + rh + r), key));
+          for (int i = 0; i < RH; i += 8) {
+            const int r = i + lane / 4;
+            const bool lossy = r < RH && lost_s[rh + r] * mt.x > kLostMax;
+            if (__any_sync(0xffffffffu, lossy))
+              add_lost<DIM>(lossy ? q_row(row0 + rh + r) : nullptr, keys, w.len - first, t_s + i,
+                            RH - i);
+          }
         }
         float s[RH];
         {

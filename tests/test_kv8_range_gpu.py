@@ -61,8 +61,8 @@ def test_one_element_of_q_far_above_the_others(ds, group, n, lift, dim):
     """2^lift in one dim whose key codes are 0, in every other head: the other
     dims alone make the score.
 
-    Decode may lose 2^-18 of a score (base 2) to its form of q. Prefill holds q
-    times a power of two, its largest at least 2^14, in f16, exact down to 2^-14
+    Decode's form of q may move a score by 2^-14 (of a power of two). Prefill holds
+    q times a power of two, its largest at least 2^14, in f16, exact down to 2^-14
     and with half steps of 2^-25 below: 2^-39 of the row's largest for each."""
     c = Cache([700, 90, 1100], 2, dim, seed=80 + group)
     c.codes[:, 0, :, :, 5] = 0
@@ -77,7 +77,7 @@ def test_one_element_of_q_far_above_the_others(ds, group, n, lift, dim):
     top = q.abs().amax(-1).double().numpy()
     for name, out, lse in _both(ds, c, q, counts, scale):
         _close(out, lse, ref, dim, 1100,
-               2.0 ** -18 if name == "decode" else 2.0 ** -39 * top * keys * scale)
+               2.0 ** -14 if name == "decode" else 2.0 ** -39 * top * keys * scale)
 
 
 @pytest.mark.parametrize("dim", [64, 128])
