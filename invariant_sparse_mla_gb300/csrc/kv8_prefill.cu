@@ -689,7 +689,6 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
           auto rebase = [&](bool move, float y, bool upper_in) {
             const float al = move_reference(move, y, j);
             if (upper_in && __any_sync(0xffffffffu, al != 1.0f)) {
-              const __half2 h = __float2half2_rn(al);
 #pragma unroll 1
               for (int c = 32; c < 64; c += 16) {
                 float o[16];
@@ -697,7 +696,9 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
                 tmem_fence<16>(o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), h);
+                  // (In fp32: al may be below f16's range where a weight times it is not.)
+                  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
+                  const __half2 w = __floats2half2_rn(x.x * al, x.y * al);
                   o[i] = *reinterpret_cast<const float*>(&w);
                 }
 #pragma unroll

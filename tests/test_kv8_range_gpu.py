@@ -263,3 +263,27 @@ def test_append_to_scales_that_are_no_powers_of_two(ds, exponent, few, dim):
     grown = want[1][firsts] != c.scales[firsts]
     assert exponent > -12 or grown.all()
     assert exponent < -5 or not grown.all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("first", [0, 1])
+@pytest.mark.parametrize("mid,top", [(11, 26), (11, 24), (9, 22), (8, 26), (11, 28), (0, 14)])
+def test_a_reference_that_moves_far_keeps_the_weights_beside_it(ds, mid, top, first, dim):
+    """One page of a tile 2^mid above the tile before, and one position of the
+    other page 2^top above it, whose value is 0: the output is the page's, whose
+    weights are 2^(mid - top) of the largest."""
+    c = Cache([400], 1, dim, seed=120)
+    c.scales[:] = 1.0
+    for p in c.table[0][c.table[0] >= 0]:
+        c.codes[p] = 0
+    code = {0: 0, 8: 0x50, 9: 0x51, 11: 0x53, 14: 0x56, 22: 0x5B, 24: 0x5C, 26: 0x5D, 28: 0x5E}
+    assert all(oracle.e4m3_to_float64(np.uint8(v)) == k for k, v in code.items())
+    a, b = c.table[0, 2 + first], c.table[0, 3 - first]      # pages of the second tile
+    c.codes[a, 0, 0, :, 0], c.codes[a, 1] = code[mid], 0x38
+    c.codes[b, 0, 0, 17, 0] = code[top]
+    q = torch.zeros((3, 2, dim), dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    ref = _ref(c, q, [3], math.log(2))
+    assert (ref[0] > 2.0 ** (mid - top)).all()
+    for _, out, lse in _both(ds, c, q, [3], math.log(2)):
+        _close(out, lse, ref, dim, 400)
