@@ -403,8 +403,9 @@ int ds_kv_cache_write(const void* latent, int64_t num_rows, const int64_t* slots
  *
  * head_dim is 64 or 128; num_heads is a multiple of num_kv_heads (query head
  * h reads key/value head h / (num_heads / num_kv_heads)), both at most 1024,
- * bt_stride is at most 2^24, num_requests at most 2^20, and the product
- * num_pages * 2 * num_kv_heads * 64 below 2^31.
+ * bt_stride is at most 2^24, num_requests at most 2^20, num_tokens (of append
+ * and prefill) at most 2^24, and the product num_pages * 2 * num_kv_heads * 64
+ * below 2^31.
  *
  * Ragged calls give each request's tokens by token_starts, int32
  * [num_requests + 1] in device memory, never decreasing: request r owns rows
@@ -430,7 +431,9 @@ int ds_kv_cache_write(const void* latent, int64_t num_rows, const int64_t* slots
  * holds earlier positions of the request, else 0; scale = max(old, need), or
  * 2^-60 if both are 0. Earlier codes become E4M3(code * (old / scale)) when
  * the scale grew, new ones are E4M3(x / scale), rounded to nearest with ties
- * to even, saturating at +-448. A NaN becomes the NaN code and does not enter
+ * to even, saturating at +-448; a quotient or product that float32 does not
+ * hold (the scale before the call was no power of two) is rounded to float32
+ * first. A NaN becomes the NaN code and does not enter
  * a. With power-of-two scales a growing scale changes earlier values only
  * where their codes leave E4M3's normal range.
  *
@@ -477,7 +480,11 @@ int ds_kv8_decode(const void* q, int64_t q_stride, const void* kv_pages, const f
                   int num_kv_heads, int head_dim, float scale, void* out, float* lse,
                   void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
 
-/* Workspace bytes of ds_kv8_decode (0 for an unsupported shape). */
+/*
+ * Workspace bytes of ds_kv8_decode (0 for an unsupported shape). They follow
+ * the table's width, not the lengths: up to 32 spans for each row of q to
+ * 131072 positions, one for each 4096 above.
+ */
 size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_heads,
                                     int num_kv_heads, int head_dim, int64_t bt_stride);
 

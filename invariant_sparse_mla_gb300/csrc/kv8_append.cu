@@ -334,11 +334,17 @@ cudaError_t launch_pages(const Params& p, dim3 grid, int heads_per_cta, cudaStre
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream) {
   Params p{reinterpret_cast<const __nv_bfloat16*>(a.k), reinterpret_cast<const __nv_bfloat16*>(a.v),
            a.k_stride, a.v_stride, a.tokens, a.starts, a.c};
-  // Few tokens a request (on average): a warp per (page, side, head). With 8
-  // heads x 128, us of this kernel against the other one:
+  // Few tokens a request (on average): a warp per (page, side, head). us of this
+  // kernel against the other one:
   //   requests x tokens   128 x 5   128 x 32   128 x 64   16 x 8   16 x 24
-  //                       4.4 13.4  10.8 15.9  19.9 18.4  3.1 4.0  5.6 4.2
-  // so up to 40 tokens, or 16 where few CTAs of the other one wait for a place.
+  //   8 heads x 128       4.5 12.5  10.8 15.2  18.2 17.9  3.1 3.9  5.2 4.1
+  //   8 heads x 64        4.2 11.3  6.8 14.6   11.1 15.9  2.8 4.4  3.8 4.4
+  //   4 heads x 128       3.4 7.7   9.1 9.4    15.9 10.9  3.0 2.8  5.6 3.0
+  //   1 head x 128        3.1 4.2   6.6 4.9    10.1 5.9   2.8 2.7  4.7 2.8
+  // so up to 40 tokens, or 16 where few CTAs of the other one wait for a place. (At
+  // the limits the slower side may be taken: 128 x 40 of 4 heads x 128 11.3 for
+  // 9.8, 16 x 16 of 1 head 3.8 for 2.8. One long prompt among many short ones goes
+  // with them, since the lengths are on the device.)
   const int64_t units = a.tokens / kPage + 2 * a.c.requests;
   if (a.tokens <= (a.c.requests * a.c.kv_heads >= 512 ? 40 : 16) * a.c.requests) {
     const dim3 grid((unsigned)(units * ((2 * a.c.kv_heads + 7) / 8)));

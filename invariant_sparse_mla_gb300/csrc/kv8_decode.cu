@@ -1,5 +1,5 @@
-// Decode attention over the block-scaled 8-bit cache, on the 8-bit tensor
-// cores: keys and values are multiplied as they lie in the cache.
+// Decode attention over the block-scaled 8-bit cache: keys are multiplied on the
+// 8-bit tensor cores as they lie in the cache, values in f16.
 //
 // Mathematics. With codes K, V (E4M3) and page scales a, b, position i of a
 // page gives s_i = scale * a * (q . K_i) and out = sum_i 2^(s_i - M) b V_i / L.

@@ -24,9 +24,13 @@
 // sum and fp32 outputs) to the next CTA, which continues where it stopped: the
 // same operations in the same order, so that where runs are cut changes no
 // bit. A CTA does the piece that it hands over first and the piece that it
-// takes over last, so nobody waits in practice, and the launch is cooperative
-// (every CTA resident), so that a wait always ends. (512 equal items on 152 SMs
-// would otherwise take 4 rounds for 3.4 rounds of work.)
+// takes over last, so that nobody waits where runs are longer than items, and
+// the launch is cooperative (every CTA resident), so that a wait always ends.
+// (512 equal items on 152 SMs would otherwise take 4 rounds for 3.4 rounds of
+// work.) What this does not do is walk one item's positions in parallel: the
+// grid has at most as many CTAs as there are items, and the CTAs of an item
+// longer than a run follow one another. 16 tokens on 32768 positions, 64 / 8 heads
+// x 128, are 8 items: 443 us (decode, which cuts contexts, takes 76).
 //   softmax warps    thread = row = TMEM lane; with dim 64 two threads share a
 //                    row, a page of the tile each. With dim 128, P over S, the
 //                    tensor pipe and the memory of S and O bound the loop, and

@@ -56,7 +56,7 @@ def _close(out, lse, ref, dim, length, score=0.0):
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("lift", [9, 14, 17, 20, 22])
-@pytest.mark.parametrize("group,n", [(1, 1), (4, 3), (13, 3)])
+@pytest.mark.parametrize("group,n", [(1, 1), (4, 3), (7, 3), (10, 3), (13, 3)])
 def test_one_element_of_q_far_above_the_others(ds, group, n, lift, dim):
     """2^lift in one dim whose key codes are 0, in every other head: the other
     dims alone make the score.
