@@ -282,10 +282,14 @@ struct Scheduler {
   __device__ explicit Scheduler(const Params& params) : p(params) {
     per_head = p.plan.first[p.units];
     const int64_t total = per_head * p.c.kv_heads;
-    lo = total * blockIdx.x / gridDim.x;
-    hi = total * (blockIdx.x + 1) / gridDim.x;
+    // Every run holds something, so that the CTA before is the one that hands over:
+    // where the call's requests have less than a weight a CTA (most of them
+    // without tokens), the last CTAs have no run.
+    const int64_t n = total < gridDim.x ? total : gridDim.x;
     phase = 3;
-    if (lo >= hi) return;
+    if (blockIdx.x >= n) return;
+    lo = total * blockIdx.x / n;
+    hi = total * (blockIdx.x + 1) / n;
     i0 = find(lo);
     i1 = find(hi - 1);
     at = i0;

@@ -287,3 +287,28 @@ def test_a_reference_that_moves_far_keeps_the_weights_beside_it(ds, mid, top, fi
     assert (ref[0] > 2.0 ** (mid - top)).all()
     for _, out, lse in _both(ds, c, q, [3], math.log(2)):
         _close(out, lse, ref, dim, 400)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("requests,kv_heads", [(24, 8), (64, 4), (200, 1), (1000, 2)])
+@pytest.mark.parametrize("length,n", [(300, 1), (700, 3), (2000, 40), (129, 129)])
+def test_prefill_of_one_request_among_many_without_tokens(ds, length, n, requests, kv_heads, dim):
+    """A padded batch in which one request brings tokens, fewer tiles than there
+    are CTAs: its bits are those of a call of its own."""
+    c = Cache([length], kv_heads, dim, seed=140)
+    codes, scales, one, _ = c.device()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    q = c.q(n, 3 * kv_heads).to(DEV)
+    alone = ds.kv8_prefill(q, torch.tensor([0, n], **i32), codes, scales, one,
+                           torch.tensor([length], **i32), 0.1)
+    err = torch.zeros(1, **i32)
+    for at in (0, requests // 3, requests - 1):
+        table = torch.full((requests, one.shape[1]), -1, **i32)
+        table[at] = one[0]
+        lens = torch.zeros(requests, **i32)
+        lens[at] = length
+        starts = torch.where(torch.arange(requests + 1, device=DEV) > at, n, 0).int()
+        got = ds.kv8_prefill(q, starts, codes, scales, table, lens, 0.1, err_flag=err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        assert torch.equal(got[0], alone[0]) and torch.equal(got[1], alone[1])
