@@ -279,6 +279,11 @@ struct Scheduler {
     }
     return head * p.units + a;        // (its weight is not 0)
   }
+  // The first item with a weight behind item i, which has none (requests without
+  // tokens are such units, any number of them in a row). The one at i1 has.
+  __device__ int64_t skip(int64_t i) const {
+    return find(i / p.units * per_head + p.plan.first[i % p.units]);
+  }
   __device__ explicit Scheduler(const Params& params) : p(params) {
     per_head = p.plan.first[p.units];
     const int64_t total = per_head * p.c.kv_heads;
@@ -296,13 +301,14 @@ struct Scheduler {
     phase = 0;
   }
   // The CTA's tiles of item i: from its own start where the run begins in the
-  // item's cost, none where it ends there. r < 0: no piece.
+  // item's cost, none where it ends there. r < 0: no piece; nt < 0: no such item.
   __device__ Piece piece(int64_t i) const {
     Piece x;
     x.r = -1;
     const int64_t u = i % p.units;
     const int64_t s = i / p.units * per_head + p.plan.first[u];
     const int nt = (int)(p.plan.first[u + 1] - p.plan.first[u]) - kItemCost;
+    x.nt = nt;
     if (nt < 0) return x;
     auto tile_of = [&](int64_t w) {
       const int64_t t = w - s - kItemCost;
@@ -318,7 +324,6 @@ struct Scheduler {
     x.n = info.n;
     x.raw_len = info.raw_len;
     x.kvh = (int)(i / p.units);
-    x.nt = nt;
     x.take = x.j0 > 0 ? (int)blockIdx.x - 1 : -1;
     x.give = x.j1 < nt ? (int)blockIdx.x : -1;
     return x;
@@ -338,7 +343,8 @@ struct Scheduler {
         phase = 2;
         break;
       }
-      x = piece(at++);
+      x = piece(at);
+      at = x.nt < 0 ? skip(at) : at + 1;
       if (x.r < 0 || (i0 != i1 && (x.take >= 0 || x.give >= 0))) continue;
       return x;
     }

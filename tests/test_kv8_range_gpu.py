@@ -312,3 +312,32 @@ def test_prefill_of_one_request_among_many_without_tokens(ds, length, n, request
         torch.cuda.synchronize()
         assert int(err) == 0
         assert torch.equal(got[0], alone[0]) and torch.equal(got[1], alone[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_million_requests_most_without_tokens(ds, dim):
+    """2^20 requests (the most there may be), few of them with positions and
+    tokens: the same outputs as alone, in time that the empty ones do not fill."""
+    n, hk = 1 << 20, 2
+    c = Cache([300], hk, dim, seed=130)
+    codes, scales, one, _ = c.device()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = one.expand(n, -1).contiguous()
+    err = torch.zeros(1, **i32)
+    q = c.q(1, 6).to(DEV)
+    want = ds.kv8_decode(q[None], codes, scales, one, torch.tensor([300], **i32), 0.1)
+    alone = ds.kv8_prefill(q, torch.tensor([0, 1], **i32), codes, scales, one,
+                           torch.tensor([300], **i32), 0.1)
+    for where in ([0, n - 1], [n - 1], [0], [5, 77777, 77778, n // 2, n - 9]):
+        full = torch.zeros(n, dtype=torch.bool, device=DEV)
+        full[where] = True
+        starts = torch.cat([torch.zeros(1, **i32), torch.cumsum(full, 0).int()])
+        lens = torch.where(full, 300, 0).int()
+        out, lse = ds.kv8_prefill(q.expand(len(where), -1, -1).contiguous(), starts, codes, scales,
+                                  table, lens, 0.1, err_flag=err)
+        assert (out == alone[0]).all() and (lse == alone[1]).all() and int(err) == 0
+        out, lse = ds.kv8_decode(q.expand(n, -1, -1)[:, None].contiguous(), codes, scales, table,
+                                 lens, 0.1, err_flag=err)
+        assert (out[full] == want[0][0]).all() and (lse[full] == want[1][0]).all()
+        assert (out[~full] == 0).all() and torch.isneginf(lse[~full]).all() and int(err) == 0
+        del out, lse
