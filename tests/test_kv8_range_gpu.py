@@ -341,3 +341,46 @@ def test_a_million_requests_most_without_tokens(ds, dim):
         assert (out[full] == want[0][0]).all() and (lse[full] == want[1][0]).all()
         assert (out[~full] == 0).all() and torch.isneginf(lse[~full]).all() and int(err) == 0
         del out, lse
+
+
+def test_a_captured_serving_step(ds):
+    """extend, append, decode and prefill of a step in one graph, replayed with
+    new tokens: the states and outputs of the same steps run one by one."""
+    hk, d, heads, rows, pages = 2, 128, 8, 5, 40
+    i32 = dict(dtype=torch.int32, device=DEV)
+    counts = torch.tensor([5, 0, 1, 17, 40], **i32)
+    starts = torch.cat([torch.zeros(1, **i32), torch.cumsum(counts, 0).int()])
+    which, t = torch.arange(rows, **i32), int(counts.sum())
+    x = torch.empty((t, 2, hk, d), dtype=torch.bfloat16, device=DEV)
+    q = torch.empty((t, heads, d), dtype=torch.bfloat16, device=DEV)
+
+    def state():
+        return (torch.zeros(pages, **i32), torch.full((rows, 6), -1, **i32), torch.zeros(rows, **i32),
+                torch.full((pages, 2, hk, 64, d), 0x7F, dtype=torch.uint8, device=DEV),
+                torch.full((pages, 2, hk), float("nan"), device=DEV), torch.zeros(1, **i32))
+
+    def step(refs, table, lens, codes, scales, err):
+        ds.pages_extend(refs, table, lens, which, lens + counts, err_flag=err)
+        ds.kv8_append(x[:, 0], x[:, 1], starts, table, lens, codes, scales, err_flag=err)
+        out = ds.kv8_prefill(q, starts, codes, scales, table, lens, 0.09, err_flag=err)
+        return out + ds.kv8_decode(q[:rows, None], codes, scales, table, lens, 0.09, err_flag=err)
+
+    fill = lambda k: [y.normal_(generator=torch.Generator(device=DEV).manual_seed(k))  # noqa: E731
+                      for y in (x, q)]
+    eager, kept = state(), state()
+    fill(0)
+    step(*state())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(*kept)
+    for k in range(7):
+        fill(k)
+        want = step(*eager)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for a, b in zip(kept[:3] + kept[5:], eager[:3] + eager[5:]):
+            assert torch.equal(a, b)
+        assert torch.equal(kept[3], eager[3]) and torch.equal(kept[4].nan_to_num(9),
+                                                              eager[4].nan_to_num(9))
+    assert int(kept[5]) == 0 and kept[2].tolist() == [35, 0, 7, 119, 280]
