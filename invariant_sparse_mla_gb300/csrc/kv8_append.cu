@@ -184,7 +184,7 @@ __device__ __forceinline__ uint32_t again(uint32_t w, float f) {
 // land in shared memory (two heads ahead, without holding registers) and are
 // read back by the same thread, so only the maximum crosses threads. 8 prompts
 // of 700 to 4001 tokens, 8 heads x 128: 23 us, 4.6 TB/s of 105 MB, issue slots
-// 61 % busy. (A CTA per head with the loads in registers spent most of its time
+// 62 % busy. (A CTA per head with the loads in registers spent most of its time
 // on the lookups: 30 us.)
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv8_append_page_kernel(const Params p,

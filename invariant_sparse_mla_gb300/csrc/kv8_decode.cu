@@ -35,8 +35,8 @@
 // function of the request's length alone, so a request's bits do not depend
 // on the batch. (64 / 8 heads x 128, one token of one request on 4096 / 16384
 // positions: 14 / 16 us; with spans of 2048 at least 21 / 21 us, of 4096 31 / 34
-// us. Large batches pay for it: 32 x 5 tokens on 4096 to 32768 positions 318 us
-// instead of 298, as the spans' partial outputs are written and read once more.)
+// us. Large batches pay for it: 32 x 5 tokens on 4096 to 32768 positions 20 us of
+// 318, as the spans' partial outputs are written and read once more.)
 // A persistent grid takes the (request, kv head, row group, span) items in
 // order, each CTA an equal share of the 128-position tiles; a second kernel
 // joins the spans in order. Rows with one span are finished by the first kernel.
@@ -47,9 +47,9 @@
 // and barriers run on across items, so the next item's pages stream in while
 // the last one is finished. The bound is HBM, 2 * dim bytes a position, with
 // one token a request (16 requests on 8192 to 131072 positions, 128 / 8 heads:
-// 349 us, 5.65 TB/s), and the softmax threads' work with many rows a kv head (32
-// x 5 tokens, 64 / 8 heads: 40 rows a tile, 318 us, 3.70 TB/s, issue slots 47 %
-// busy, DRAM 57 %).
+// 344 us, 5.74 TB/s), and the softmax threads' work with many rows a kv head (32
+// x 5 tokens, 64 / 8 heads: 40 rows a tile, 314 us, 3.74 TB/s, issue slots 46 %
+// busy, DRAM 56 %).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -134,7 +134,7 @@ struct Layout {
   static constexpr int kWarpMax = kAlpha + R8 * 4;          // 4 x R8 floats
   static constexpr int kVis = kWarpMax + 4 * R8 * 4;        // positions each row sees
   static constexpr int kBy = kVis + R8 * 4;                 // by how much a reference moved
-  static constexpr int kSet = kBy + R8 * 4;                 // 1: the row has one; 2: only scores too low
+  static constexpr int kSet = kBy + R8 * 4;                 // 1: row has one; 2: only low scores
   static constexpr int kLost = kSet + R8 * 4;               // what a score may lose at key scale 1
   static constexpr int kMisc = kLost + R8 * 4;              // tmem slot, abort, start of work
   static constexpr int kEnd = kMisc + 64;

@@ -30,13 +30,13 @@
 // work.) What this does not do is walk one item's positions in parallel: the
 // grid has at most as many CTAs as there are items, and the CTAs of an item
 // longer than a run follow one another. 16 tokens on 32768 positions, 64 / 8 heads
-// x 128, are 8 items: 443 us (decode, which cuts contexts, takes 76).
+// x 128, are 8 items: 450 us (decode, which cuts contexts, takes 75).
 //   softmax warps    thread = row = TMEM lane; with dim 64 two threads share a
 //                    row, a page of the tile each. With dim 128, P over S, the
 //                    tensor pipe and the memory of S and O bound the loop, and
 //                    reading S twice for want of registers costs more than the
-//                    shorter way to P gives: ragged prompts of dim 64 take 293 us
-//                    so and 332 with one thread a row, a chunk of dim 128 takes
+//                    shorter way to P gives: ragged prompts of dim 64 took 293 us
+//                    so and 332 with one thread a row, a chunk of dim 128 took
 //                    1767 us with one thread and 1965 with two;
 //   4 loader warps   codes from global memory, through registers, to f16 tiles
 //                    of K and V in shared memory (two buffers each): the copy
@@ -53,9 +53,10 @@
 //
 // The bound is the way S -> softmax -> P -> O of a row tile: two of them in turn
 // keep the tensor pipe busy half the time (dim 128; the last 2048 of 32768
-// positions, 64 / 8 heads: 1767 us, 1205 TFLOP/s). Shared memory is near: an
-// M 128 x N 128 x K 16 product reads 8 KB in its 64 cycles, and without the
-// loader's stores the same takes 1486 us, without the softmax 1410.
+// positions, 64 / 8 heads: 1769 us, 1204 TFLOP/s; 12 ragged prompts of dim 64, 28 /
+// 4 heads: 292 us). Shared memory is near: an M 128 x N 128 x K 16 product reads
+// 8 KB in its 64 cycles, and without the loader's stores the chunk took 1486 us,
+// without the softmax 1410.
 
 #include <cuda_runtime.h>
 #include <stdint.h>

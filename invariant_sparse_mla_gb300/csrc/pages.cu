@@ -15,10 +15,13 @@
 // The table work is a few thousand integers, bound by launches and memory
 // latency; page payloads are bound by HBM (each byte read and written once)
 // and are cut into 16 KB pieces so that every SM takes part however few pages
-// move. Copying 366 MB takes 55.9 us and compacting a pool by moving 3 GB 475
+// move. Copying 366 MB takes 56.0 us and compacting a pool by moving 3 GB 473
 // us (6.5 and 6.4 TB/s counting reads and writes); freeing, forking and
-// extending 96 of 256 rows, 98 MB copied, takes 44 us (the forking kernel 21 of
-// them, five launches most of the rest).
+// extending 96 of 256 rows, 98 MB copied, takes 40 us (the forking kernel 21 of
+// them, five launches most of the rest). Fork and extend look for an entry's
+// rank and page in every CTA and for repeats in every entry: made for lists of
+// dozens or hundreds, right for 65535 (extending as many rows takes 1.7 ms,
+// forking them 2.6).
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -294,8 +297,9 @@ __device__ __forceinline__ int64_t need_before(const Workspace& w, int64_t i) {
 }
 
 // Fork: need = 1 where a partly filled page is copied (one outside the pool is
-// not), aux = the parent's length, -1 for an entry that is skipped. Extend: need = pages to add, aux =
-// the present length or -1. Everything is read before anything is written.
+// not), aux = the parent's length, -1 for an entry that is skipped. Extend: need
+// = pages to add, aux = the present length or -1. Everything is read before
+// anything is written.
 template <bool FORK>
 __global__ void __launch_bounds__(kThreads) pages_plan_kernel(
     const PageState s, const Workspace w, int segs, const int32_t* __restrict__ a,
