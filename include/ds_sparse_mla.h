@@ -524,6 +524,10 @@ size_t ds_kv8_prefill_workspace_size(int64_t num_tokens, int64_t num_requests, i
  *               ceil(lens[r] / 64) entries (lens clamped to
  *               [0, 64 * bt_stride]); the rest holds nothing.
  *  lens         int32 [num_rows].
+ * A caller that lowers a length itself (rejected tokens) stays within the row's
+ * last page: entries behind ceil(lens[r] / 64) count as empty, so that their
+ * pages would be lost, and a page that ds_pages_fork shares must not become one
+ * that is appended to.
  * Pages are handed out lowest number first, in the order of the call's list,
  * so the state after a call follows from the state before it.
  *
