@@ -97,6 +97,7 @@ typedef enum {
 #define DS_DEVERR_TIMEOUT 8  /* an internal pipeline wait gave up (library bug)   */
 #define DS_DEVERR_NOPAGE 16  /* pages: the pool has too few free pages            */
 #define DS_DEVERR_LEN 32     /* a length that the operation cannot take           */
+#define DS_DEVERR_SHARED 64  /* a page to be rewritten that other rows hold too   */
 
 /*
  * Message of the last error on the calling host thread ("" if none). The
@@ -515,6 +516,124 @@ size_t ds_kv8_prefill_workspace_size(int64_t num_tokens, int64_t num_requests, i
                                      int num_kv_heads, int head_dim);
 
 /*
+ * ds_qk_norm_rope: norms of queries and keys per head and the rotation by
+ * position, in one pass, in front of ds_kv8_append and the attention (and, with
+ * 576 dims, of ds_kv_cache_write and the sparse attention).
+ *
+ * A head's row x of head_dim values becomes
+ *   y_d = x_d * w_d / sqrt(mean over d < norm_dim of x_d^2 + eps), d < norm_dim,
+ *   y_d = x_d behind (and everywhere on a side without weights),
+ * and then the rot_dim values from rot_start on are turned in pairs (u, v) by
+ * a_i = position * inv_freq_i: (u cos a_i - v sin a_i, v cos a_i + u sin a_i).
+ * Pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved != 0. All
+ * in float32 (squares of values above 2^63 overflow there), rounded to bfloat16
+ * once; the angle is exact to about 2^-22 turns at any position.
+ *
+ *  q, k         bfloat16, row t at q + t * q_stride (k + t * k_stride)
+ *               elements, [heads, head_dim] contiguous; 16-byte aligned, strides
+ *               multiples of 8 and at least heads * head_dim. k may be NULL with
+ *               num_k_heads = 0.
+ *  q_weight,    bfloat16 [norm_dim], 16-byte aligned, or NULL: no norm on that
+ *  k_weight     side.
+ *  positions    int32 [num_tokens], any value (a negative one turns the other
+ *               way); inv_freq float32 [rot_dim / 2]. Both unused with rot_dim 0.
+ *  q_out,       as q and k, with strides of their own. Either may be its input
+ *  k_out        with the same stride; other overlaps give unspecified results.
+ *
+ * head_dim is a multiple of 16 up to 1024, norm_dim one of 8 in [0, head_dim],
+ * rot_dim one of 16, rot_start one of 8; at most 1024 heads a side and 2^24
+ * tokens. A row's result depends on that row alone, bit for bit.
+ */
+int ds_qk_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const void* q_weight,
+                    const void* k, int64_t k_stride, int num_k_heads, const void* k_weight,
+                    int64_t num_tokens, int head_dim, int norm_dim, float eps,
+                    const int32_t* positions, const float* inv_freq, int rot_start, int rot_dim,
+                    int interleaved, void* q_out, int64_t q_out_stride, void* k_out,
+                    int64_t k_out_stride, void* stream);
+
+/*
+ * ds_kv8_accept: after the drafts of a tree were verified, the accepted ones
+ * move to the places behind the positions that were there before them, in all
+ * layers by one launch.
+ *
+ *  layers       array in HOST memory, read during the call: the caches that the
+ *               block table indexes, all of num_pages pages, num_kv_heads and
+ *               head_dim. At most DS_MAX_KV8_LAYERS, each listed once.
+ *  lens         int32 [num_requests], the next_n drafts of each request included
+ *               (draft i lies at position lens[r] - next_n + i). Not changed.
+ *  accepted     int32 [num_requests, width], width <= next_n <= 64: the accepted
+ *               drafts' numbers, ascending, -1 behind them. Drafts that are not
+ *               listed are dropped.
+ *  new_lens     int32 [num_requests]: lens[r] - next_n + the number accepted. Not
+ *               lens itself: hand it to ds_pages_shrink, which gives the pages
+ *               behind back and sets the length.
+ *  err_flag     optional: DS_DEVERR_IDX for a list that is not ascending, holds a
+ *               number past next_n or one behind a -1; DS_DEVERR_LEN for a
+ *               length in (0, next_n) or above 64 * bt_stride; DS_DEVERR_PAGE
+ *               for a page outside the pool. Such a request stays as it is, its
+ *               new length is its length. So does one of length <= 0, without
+ *               an error.
+ *
+ * Scales: a page that gets positions has the largest scale of the pages that its
+ * positions come from (itself among them where it keeps any); a code whose page
+ * had a smaller one becomes E4M3(code * (old / scale)) as in ds_kv8_append, and
+ * all others are copied as they are. Slots behind the new length keep their bytes.
+ * The pages that hold the drafts belong to one request each (as ds_kv8_append
+ * asks); others are not written.
+ */
+#define DS_MAX_KV8_LAYERS 128
+typedef struct {
+  void* kv_pages;
+  float* kv_scales;
+} ds_kv8_layer;
+
+int ds_kv8_accept(const ds_kv8_layer* layers, int num_layers, int64_t num_pages,
+                  const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                  int64_t num_requests, int num_kv_heads, int head_dim, int next_n,
+                  const int32_t* accepted, int width, int32_t* new_lens, int32_t* err_flag,
+                  void* stream);
+
+/*
+ * ds_kv8_evict: holds every request of one layer's cache to `budget` positions.
+ * Each kv head of a request with more keeps its first `first` positions, its
+ * last `recent` ones, and of those between the budget - first - recent with the
+ * most mass (equal mass: the lower position; NaN below everything), in their
+ * order: they move to positions 0 .. budget - 1, codes, scales and mass alike.
+ * Heads keep positions of their own; what a head's position stands for is the
+ * caller's affair (keys hold their rotation already).
+ *
+ *  mass         float32 [num_requests, num_kv_heads, mass_stride], 16-byte
+ *               aligned, mass_stride a multiple of 4 up to 2^28: the attention
+ *               weight that each position got (ds_kv8_mass). Entries from budget
+ *               on keep their values.
+ *  budget       >= first + recent; budget - first - recent at most 16384.
+ *  refcounts    optional int32 [num_pages]: a request whose first
+ *               ceil(budget / 64) pages, which are rewritten, include one with a
+ *               count above 1 stays as it is and sets DS_DEVERR_SHARED. Without
+ *               it the caller answers for that.
+ *  new_lens     int32 [num_requests]: the length afterwards. lens is not changed:
+ *               it is the same for all layers, and ds_pages_shrink sets it once
+ *               they are done.
+ *  workspace    >= ds_kv8_evict_workspace_size() bytes, 256-byte aligned, no
+ *               initialisation. Concurrent calls need separate ones.
+ *  err_flag     optional: DS_DEVERR_LEN for a length above 64 * bt_stride or
+ *               mass_stride, DS_DEVERR_PAGE for a page outside the pool; such a
+ *               request stays as it is.
+ *
+ * Scales as for ds_kv8_accept. num_requests * num_kv_heads is at most 2^26. A
+ * request's result depends on that request alone, bit for bit.
+ */
+int ds_kv8_evict(float* mass, int64_t mass_stride, int budget, int first, int recent,
+                 void* kv_pages, float* kv_scales, int64_t num_pages, const int32_t* refcounts,
+                 const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                 int64_t num_requests, int num_kv_heads, int head_dim, int32_t* new_lens,
+                 void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* Workspace bytes of ds_kv8_evict (0 for an unsupported shape). */
+size_t ds_kv8_evict_workspace_size(int64_t num_requests, int num_kv_heads, int64_t mass_stride,
+                                   int budget, int first, int recent);
+
+/*
  * Pages of a paged cache: who holds them, and moving them.
  *
  * The state is three device arrays of the caller:
@@ -524,10 +643,10 @@ size_t ds_kv8_prefill_workspace_size(int64_t num_tokens, int64_t num_requests, i
  *               ceil(lens[r] / 64) entries (lens clamped to
  *               [0, 64 * bt_stride]); the rest holds nothing.
  *  lens         int32 [num_rows].
- * A caller that lowers a length itself (rejected tokens) stays within the row's
- * last page: entries behind ceil(lens[r] / 64) count as empty, so that their
- * pages would be lost, and a page that ds_pages_fork shares must not become one
- * that is appended to.
+ * Lengths are lowered by ds_pages_shrink. A caller that lowers one itself stays
+ * within the row's last page: entries behind ceil(lens[r] / 64) count as empty,
+ * so that their pages would be lost. Either way a page that ds_pages_fork shares
+ * must not become one that is appended to.
  * Pages are handed out lowest number first, in the order of the call's list,
  * so the state after a call follows from the state before it.
  *
@@ -600,6 +719,17 @@ int ds_pages_extend(int32_t* refcounts, int64_t num_pages, int32_t* block_table,
                     int64_t bt_stride, int32_t* lens, int64_t num_rows, const int32_t* rows,
                     const int32_t* new_lens, int64_t n, void* workspace, size_t workspace_bytes,
                     int32_t* err_flag, void* stream);
+
+/*
+ * Lowers row rows[i] to new_lens[i] positions: the pages that it no longer needs
+ * lose one count and their entries become -1. A new length above the present
+ * one or below 0 sets DS_DEVERR_LEN and a row listed before DS_DEVERR_ROWREQ;
+ * both are skipped. A new length equal to lens[r] changes nothing, whatever it
+ * is. Entries that are no pages of the row's count as for ds_pages_free.
+ */
+int ds_pages_shrink(int32_t* refcounts, int64_t num_pages, int32_t* block_table,
+                    int64_t bt_stride, int32_t* lens, int64_t num_rows, const int32_t* rows,
+                    const int32_t* new_lens, int64_t n, int32_t* err_flag, void* stream);
 
 /*
  * Moves the live pages to the front of the pool: with num_live pages live,

@@ -13,6 +13,7 @@ from ._native import (  # noqa: F401
     DEVERR_NOPAGE,
     DEVERR_PAGE,
     DEVERR_ROWREQ,
+    DEVERR_SHARED,
     DEVERR_TIMEOUT,
     EXPORTED,
     attention_workspace_size,
@@ -29,17 +30,22 @@ from ._native import (  # noqa: F401
     topk_workspace_size,
 )
 from .kv8 import (  # noqa: F401
+    kv8_accept,
     kv8_append,
     kv8_decode,
     kv8_decode_workspace_size,
+    kv8_evict,
+    kv8_evict_workspace_size,
     kv8_prefill,
     kv8_prefill_workspace_size,
 )
+from .norm_rope import qk_norm_rope  # noqa: F401
 from .pages import (  # noqa: F401
     pages_compact,
     pages_copy,
     pages_extend,
     pages_fork,
     pages_free,
+    pages_shrink,
     pages_workspace_size,
 )

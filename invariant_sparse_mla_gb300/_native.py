@@ -17,7 +17,7 @@ from . import build as _build
 DS_OK = 0
 KV_DTYPES = {"bf16": 0, "fp8": 1, 0: 0, 1: 1}
 DEVERR_IDX, DEVERR_PAGE, DEVERR_ROWREQ, DEVERR_TIMEOUT = 1, 2, 4, 8
-DEVERR_NOPAGE, DEVERR_LEN = 16, 32
+DEVERR_NOPAGE, DEVERR_LEN, DEVERR_SHARED = 16, 32, 64
 
 _lib = None
 _lock = threading.Lock()
@@ -106,6 +106,19 @@ def lib():
         L.ds_pages_compact.restype = i32
         L.ds_pages_compact.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp,
                                        vp]
+        L.ds_pages_shrink.restype = i32
+        L.ds_pages_shrink.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, vp]
+        L.ds_qk_norm_rope.restype = i32
+        L.ds_qk_norm_rope.argtypes = [vp, i64, i32, vp, vp, i64, i32, vp, i64, i32, i32, f32, vp,
+                                      vp, i32, i32, i32, vp, i64, vp, i64, vp]
+        L.ds_kv8_accept.restype = i32
+        L.ds_kv8_accept.argtypes = [vp, i32, i64, vp, i64, vp, i64, i32, i32, i32, vp, i32, vp, vp,
+                                    vp]
+        L.ds_kv8_evict.restype = i32
+        L.ds_kv8_evict.argtypes = [vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, i64, i32,
+                                   i32, vp, vp, sz, vp, vp]
+        L.ds_kv8_evict_workspace_size.restype = sz
+        L.ds_kv8_evict_workspace_size.argtypes = [i64, i32, i64, i32, i32, i32]
         _lib = L
         return _lib
 
@@ -116,7 +129,9 @@ EXPORTED = ("ds_last_error", "ds_supported_config", "ds_topk_workspace_size",
             "ds_sparse_mla_decode_swa", "ds_sparse_mla_swa_workspace_size", "ds_indexer_logits",
             "ds_kv8_append", "ds_kv8_decode", "ds_kv8_decode_workspace_size", "ds_kv8_prefill",
             "ds_kv8_prefill_workspace_size", "ds_pages_workspace_size", "ds_pages_copy",
-            "ds_pages_free", "ds_pages_fork", "ds_pages_extend", "ds_pages_compact")
+            "ds_pages_free", "ds_pages_fork", "ds_pages_extend", "ds_pages_compact",
+            "ds_pages_shrink", "ds_qk_norm_rope", "ds_kv8_accept", "ds_kv8_evict",
+            "ds_kv8_evict_workspace_size")
 
 
 def last_error():

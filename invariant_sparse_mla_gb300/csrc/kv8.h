@@ -49,9 +49,32 @@ struct Kv8AttnArgs {
   void* workspace;
 };
 
+// Accepted drafts (layers give the pages and scales; c.pages is not used).
+struct Kv8AcceptArgs {
+  Kv8Cache c;
+  const int32_t* accepted;     // [requests, width]
+  int width;
+  int next_n;
+  int32_t* new_lens;           // [requests]
+};
+
+struct Kv8EvictArgs {
+  Kv8Cache c;
+  float* mass;                 // [requests, kv_heads, mass_stride]
+  int64_t mass_stride;
+  int budget, first, recent;
+  const int32_t* refcounts;    // [num_pages] or nullptr
+  int32_t* new_lens;           // [requests]
+  int32_t *starts, *ends, *top;   // workspace: [requests * kv_heads], and [.., ranked]
+};
+
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int num_layers, const Kv8AcceptArgs& a,
+                              cudaStream_t stream);
+cudaError_t launch_kv8_evict(Kv8EvictArgs a, void* workspace, cudaStream_t stream);
+size_t kv8_evict_workspace_bytes(int64_t requests, int kv_heads, int ranked, int64_t mass_stride);
 size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
                                   int64_t bt_stride);
 size_t kv8_prefill_workspace_bytes(int64_t tokens, int64_t requests, int heads, int kv_heads,
@@ -83,6 +106,8 @@ cudaError_t launch_pages_fork(const ds_page_pool* pools, int num_pools, const Pa
                               void* workspace, cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageState& s, const int32_t* rows, const int32_t* new_lens,
                                 int64_t n, void* workspace, cudaStream_t stream);
+cudaError_t launch_pages_shrink(const PageState& s, const int32_t* rows, const int32_t* new_lens,
+                                int64_t n, cudaStream_t stream);
 cudaError_t launch_pages_compact(const ds_page_pool* pools, int num_pools, const PageState& s,
                                  int32_t* refs_out, int32_t* table_out, int32_t* num_live_out,
                                  void* workspace, cudaStream_t stream);

@@ -1,4 +1,5 @@
-// Host side of the block-scaled 8-bit cache and of the page operations:
+// Host side of the block-scaled 8-bit cache, of the norm with rotation in front
+// of it and of the page operations:
 // argument validation before any launch, with messages that name the
 // parameter, and the workspace sizes.
 
@@ -10,6 +11,7 @@
 #include "ds_sparse_mla.h"
 #include "internal.h"
 #include "kv8.h"
+#include "norm_rope.h"
 
 namespace {
 
@@ -90,6 +92,23 @@ int check_tokens(const char* fn, int64_t tokens) {
   if (tokens > (1 << 24))
     return report_error(DS_ERR_UNSUPPORTED, "%s: num_tokens=%lld exceeds 2^24", fn,
                         (long long)tokens);
+  return DS_OK;
+}
+
+int check_budget(const char* fn, int budget, int first, int recent, int64_t mass_stride) {
+  if (mass_stride < 4 || mass_stride % 4 != 0 || mass_stride > ((int64_t)1 << 28))
+    return report_error(DS_ERR_SHAPE,
+                        "%s: mass_stride=%lld must be a positive multiple of 4 up to 2^28", fn,
+                        (long long)mass_stride);
+  if (budget < 1 || first < 0 || recent < 0 || first > budget || recent > budget - first)
+    return report_error(DS_ERR_SHAPE,
+                        "%s: budget=%d must be positive and at least first=%d + recent=%d, neither "
+                        "of them negative",
+                        fn, budget, first, recent);
+  if (budget - first - recent > 16384)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: budget - first - recent = %d is not supported; available: up to 16384",
+                        fn, budget - first - recent);
   return DS_OK;
 }
 
@@ -279,6 +298,194 @@ int ds_kv8_prefill(const void* q, int64_t q_stride, int64_t num_tokens,
   return launched(fn, dsmla::launch_kv8_prefill(a, as_stream(stream)));
 }
 
+size_t ds_kv8_evict_workspace_size(int64_t num_requests, int num_kv_heads, int64_t mass_stride,
+                                   int budget, int first, int recent) {
+  const char* fn = "ds_kv8_evict_workspace_size";
+  dsmla::Kv8Cache c{};
+  c.num_pages = 1;
+  c.bt_stride = 1;
+  c.requests = num_requests;
+  c.kv_heads = num_kv_heads;
+  c.dim = 64;
+  if (check_cache(fn, c) != DS_OK || check_budget(fn, budget, first, recent, mass_stride) != DS_OK)
+    return 0;
+  return dsmla::kv8_evict_workspace_bytes(num_requests, num_kv_heads, budget - first - recent,
+                                          mass_stride);
+}
+
+int ds_kv8_evict(float* mass, int64_t mass_stride, int budget, int first, int recent,
+                 void* kv_pages, float* kv_scales, int64_t num_pages, const int32_t* refcounts,
+                 const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                 int64_t num_requests, int num_kv_heads, int head_dim, int32_t* new_lens,
+                 void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  const char* fn = "ds_kv8_evict";
+  dsmla::Kv8EvictArgs a{};
+  a.c = {static_cast<uint8_t*>(kv_pages), kv_scales, num_pages, block_table, bt_stride, lens,
+         num_requests, num_kv_heads, head_dim, err_flag};
+  int st = check_cache(fn, a.c);
+  if (st == DS_OK) st = check_budget(fn, budget, first, recent, mass_stride);
+  if (st != DS_OK) return st;
+  if (num_requests * num_kv_heads > (int64_t)1 << 26)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: num_requests=%lld with %d kv heads is too large (2^26 rows)", fn,
+                        (long long)num_requests, num_kv_heads);
+  if (num_requests == 0) return report_ok();
+  st = check_ptrs(fn, {{mass, "mass", 16},
+                       {kv_pages, "kv_pages", 16},
+                       {kv_scales, "kv_scales", 4},
+                       {refcounts, "refcounts", 4, true},
+                       {block_table, "block_table", 4},
+                       {lens, "lens", 4},
+                       {new_lens, "new_lens", 4},
+                       {workspace, "workspace", 256},
+                       {err_flag, "err_flag", 4, true}});
+  if (st != DS_OK) return st;
+  if (new_lens == lens)
+    return report_error(DS_ERR_SHAPE, "%s: new_lens must not be lens", fn);
+  const size_t need = dsmla::kv8_evict_workspace_bytes(num_requests, num_kv_heads,
+                                                       budget - first - recent, mass_stride);
+  if (workspace_bytes < need)
+    return report_error(DS_ERR_WORKSPACE,
+                        "%s: workspace_bytes=%zu is smaller than the %zu bytes needed", fn,
+                        workspace_bytes, need);
+  a.mass = mass;
+  a.mass_stride = mass_stride;
+  a.budget = budget;
+  a.first = first;
+  a.recent = recent;
+  a.refcounts = refcounts;
+  a.new_lens = new_lens;
+  return launched(fn, dsmla::launch_kv8_evict(a, workspace, as_stream(stream)));
+}
+
+int ds_kv8_accept(const ds_kv8_layer* layers, int num_layers, int64_t num_pages,
+                  const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                  int64_t num_requests, int num_kv_heads, int head_dim, int next_n,
+                  const int32_t* accepted, int width, int32_t* new_lens, int32_t* err_flag,
+                  void* stream) {
+  const char* fn = "ds_kv8_accept";
+  dsmla::Kv8AcceptArgs a{};
+  a.c = {nullptr, nullptr, num_pages, block_table, bt_stride, lens, num_requests, num_kv_heads,
+         head_dim, err_flag};
+  int st = check_cache(fn, a.c);
+  if (st != DS_OK) return st;
+  if (num_layers < 1 || num_layers > DS_MAX_KV8_LAYERS)
+    return report_error(DS_ERR_UNSUPPORTED, "%s: num_layers=%d must be in [1, %d]", fn, num_layers,
+                        DS_MAX_KV8_LAYERS);
+  if (next_n < 1 || next_n > 64)
+    return report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64",
+                        fn, next_n);
+  if (width < 1 || width > next_n)
+    return report_error(DS_ERR_SHAPE, "%s: width=%d must be in [1, next_n=%d]", fn, width, next_n);
+  if (num_requests > (int64_t)INT32_MAX / (2 * num_layers * (int64_t)num_kv_heads))
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: num_requests=%lld is too large with num_layers=%d and %d kv heads", fn,
+                        (long long)num_requests, num_layers, num_kv_heads);
+  if (num_requests == 0) return report_ok();
+  if (layers == nullptr) return report_error(DS_ERR_NULL, "%s: layers is NULL", fn);
+  for (int i = 0; i < num_layers; ++i) {
+    if (layers[i].kv_pages == nullptr || layers[i].kv_scales == nullptr)
+      return report_error(DS_ERR_NULL, "%s: layers[%d].%s is NULL", fn, i,
+                          layers[i].kv_pages == nullptr ? "kv_pages" : "kv_scales");
+    if (!aligned(layers[i].kv_pages, 16) || !aligned(layers[i].kv_scales, 4))
+      return report_error(DS_ERR_ALIGN,
+                          "%s: layers[%d]: kv_pages must be 16-byte and kv_scales 4-byte aligned",
+                          fn, i);
+    for (int j = 0; j < i; ++j)
+      if (layers[j].kv_pages == layers[i].kv_pages || layers[j].kv_scales == layers[i].kv_scales)
+        return report_error(DS_ERR_SHAPE, "%s: layers[%d] and layers[%d] are the same cache", fn, j,
+                            i);
+  }
+  st = check_ptrs(fn, {{block_table, "block_table", 4},
+                       {lens, "lens", 4},
+                       {accepted, "accepted", 4},
+                       {new_lens, "new_lens", 4},
+                       {err_flag, "err_flag", 4, true}});
+  if (st != DS_OK) return st;
+  if (new_lens == lens)
+    return report_error(DS_ERR_SHAPE, "%s: new_lens must not be lens", fn);
+  a.accepted = accepted;
+  a.width = width;
+  a.next_n = next_n;
+  a.new_lens = new_lens;
+  return launched(fn, dsmla::launch_kv8_accept(layers, num_layers, a, as_stream(stream)));
+}
+
+// ------------------------------------------------------ norm with rotation
+int ds_qk_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const void* q_weight,
+                    const void* k, int64_t k_stride, int num_k_heads, const void* k_weight,
+                    int64_t num_tokens, int head_dim, int norm_dim, float eps,
+                    const int32_t* positions, const float* inv_freq, int rot_start, int rot_dim,
+                    int interleaved, void* q_out, int64_t q_out_stride, void* k_out,
+                    int64_t k_out_stride, void* stream) {
+  const char* fn = "ds_qk_norm_rope";
+  if (head_dim < 16 || head_dim > 1024 || head_dim % 16 != 0)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: head_dim=%d is not supported; available: multiples of 16 up to 1024",
+                        fn, head_dim);
+  if (num_q_heads < 1 || num_q_heads > 1024)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: num_q_heads=%d is not supported; available: 1 .. 1024", fn,
+                        num_q_heads);
+  if (num_k_heads < 0 || num_k_heads > 1024)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: num_k_heads=%d is not supported; available: 0 .. 1024", fn,
+                        num_k_heads);
+  int st = check_tokens(fn, num_tokens);
+  if (st != DS_OK) return st;
+  if (norm_dim < 0 || norm_dim > head_dim || norm_dim % 8 != 0)
+    return report_error(DS_ERR_SHAPE,
+                        "%s: norm_dim=%d must be a multiple of 8 in [0, head_dim=%d]", fn, norm_dim,
+                        head_dim);
+  if (norm_dim == 0 && (q_weight != nullptr || k_weight != nullptr))
+    return report_error(DS_ERR_SHAPE, "%s: norm_dim=0 takes no q_weight or k_weight", fn);
+  if (rot_dim < 0 || rot_dim % 16 != 0 || rot_start < 0 || rot_start % 8 != 0 ||
+      rot_dim > head_dim || rot_start > head_dim - rot_dim)
+    return report_error(DS_ERR_SHAPE,
+                        "%s: rot_dim=%d must be a multiple of 16 and rot_start=%d one of 8, inside "
+                        "head_dim=%d",
+                        fn, rot_dim, rot_start, head_dim);
+  if (!(eps >= 0.0f) || !std::isfinite(eps))
+    return report_error(DS_ERR_SHAPE, "%s: eps must be finite and not negative", fn);
+  const struct {
+    const char* name;
+    int64_t stride;
+    int heads;
+  } strides[] = {{"q_stride", q_stride, num_q_heads},
+                 {"k_stride", k_stride, num_k_heads},
+                 {"q_out_stride", q_out_stride, num_q_heads},
+                 {"k_out_stride", k_out_stride, num_k_heads}};
+  for (const auto& s : strides)
+    if (s.heads > 0 && (s.stride < (int64_t)s.heads * head_dim || s.stride % 8 != 0))
+      return report_error(DS_ERR_SHAPE,
+                          "%s: %s=%lld must be a multiple of 8 and at least heads * head_dim = %lld",
+                          fn, s.name, (long long)s.stride, (long long)s.heads * head_dim);
+  if (num_tokens == 0) return report_ok();
+  const bool no_k = num_k_heads == 0;
+  st = check_ptrs(fn, {{q, "q", 16},
+                       {k, "k", 16, no_k},
+                       {q_weight, "q_weight", 16, true},
+                       {k_weight, "k_weight", 16, true},
+                       {positions, "positions", 4, rot_dim == 0},
+                       {inv_freq, "inv_freq", 4, rot_dim == 0},
+                       {q_out, "q_out", 16},
+                       {k_out, "k_out", 16, no_k}});
+  if (st != DS_OK) return st;
+  dsmla::NormRopeArgs a{};
+  a.q = {q, q_stride, q_out, q_out_stride, q_weight, num_q_heads};
+  a.k = {k, k_stride, k_out, k_out_stride, k_weight, num_k_heads};
+  a.tokens = num_tokens;
+  a.dim = head_dim;
+  a.norm_dim = norm_dim;
+  a.rot_start = rot_start;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.eps = eps;
+  return launched(fn, dsmla::launch_norm_rope(a, as_stream(stream)));
+}
+
 }  // extern "C"
 
 // ------------------------------------------------------------------- pages
@@ -427,6 +634,20 @@ int ds_pages_extend(int32_t* refcounts, int64_t num_pages, int32_t* block_table,
   if (st != DS_OK) return st;
   return launched(fn, dsmla::launch_pages_extend(s, rows, new_lens, n, workspace,
                                                  as_stream(stream)));
+}
+
+int ds_pages_shrink(int32_t* refcounts, int64_t num_pages, int32_t* block_table,
+                    int64_t bt_stride, int32_t* lens, int64_t num_rows, const int32_t* rows,
+                    const int32_t* new_lens, int64_t n, int32_t* err_flag, void* stream) {
+  const char* fn = "ds_pages_shrink";
+  const dsmla::PageState s{refcounts, num_pages, block_table, bt_stride, lens, num_rows, err_flag};
+  int st = check_state(fn, s);
+  if (st == DS_OK) st = check_list(fn, n);
+  if (st != DS_OK) return st;
+  if (n == 0) return report_ok();
+  st = check_ptrs(fn, {{rows, "rows", 4}, {new_lens, "new_lens", 4}});
+  if (st != DS_OK) return st;
+  return launched(fn, dsmla::launch_pages_shrink(s, rows, new_lens, n, as_stream(stream)));
 }
 
 int ds_pages_compact(const ds_page_pool* pools, int num_pools, const int32_t* refcounts,

@@ -1,4 +1,4 @@
-// Pages of a paged cache: copying, forking, freeing, extending, compacting.
+// Pages of a paged cache: copying, forking, freeing, extending, shrinking, compacting.
 //
 // A page is free when its reference count is not positive, and free pages are
 // handed out lowest number first: what a call does follows from the state
@@ -428,6 +428,46 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(
   if (threadIdx.x == 0) s.lens[row] = new_lens[i];
 }
 
+// ----------------------------------------------------------------- shrink
+// One CTA per entry: what lies behind the new length is given back, as by free.
+__global__ void __launch_bounds__(kThreads) pages_shrink_kernel(
+    const PageState s, const int32_t* __restrict__ rows, const int32_t* __restrict__ new_lens) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = blockIdx.x, r = rows[i];
+  if (r < 0) return;
+  bool again = false;
+  for (int64_t j = threadIdx.x; j < i; j += kThreads) again |= rows[j] == (int32_t)r;
+  again = __syncthreads_or(again);
+  if (r >= s.num_rows || again) {
+    if (threadIdx.x == 0) raise(s.err, kErrRow);
+    return;
+  }
+  const int64_t raw = s.lens[r], len = clamp_len(raw, s.bt_stride), want = new_lens[i];
+  if (want == raw) return;
+  if (want < 0 || want > len) {
+    if (threadIdx.x == 0) raise(s.err, kErrLen);
+    return;
+  }
+  __syncthreads();   // every thread has read the length
+  const int64_t held = (len + kPage - 1) / kPage;
+  for (int64_t j = (want + kPage - 1) / kPage + threadIdx.x; j < held; j += kThreads) {
+    int32_t* at = &s.table[r * s.bt_stride + j];
+    const int page = *at;
+    *at = -1;
+    if (page == -1) continue;
+    if (page < 0 || page >= s.num_pages) {
+      raise(s.err, kErrPage);
+      continue;
+    }
+    if (atomicSub(&s.refs[page], 1) <= 0) {
+      atomicAdd(&s.refs[page], 1);
+      raise(s.err, kErrPage);
+    }
+  }
+  if (threadIdx.x == 0) s.lens[r] = (int32_t)want;
+}
+
 // ---------------------------------------------------------------- compact
 __global__ void __launch_bounds__(kThreads) pages_snapshot_kernel(const PageState s,
                                                                  const Workspace w) {
@@ -633,6 +673,12 @@ cudaError_t launch_pages_extend(const PageState& s, const int32_t* rows, const i
   if (e != cudaSuccess) return e;
   return launch_pdl(pages_extend_kernel, dim3((unsigned)n), dim3(kThreads), segs * 4, stream, 1u, s,
                     w, segs, rows, new_lens);
+}
+
+cudaError_t launch_pages_shrink(const PageState& s, const int32_t* rows, const int32_t* new_lens,
+                                int64_t n, cudaStream_t stream) {
+  return launch_pdl(pages_shrink_kernel, dim3((unsigned)n), dim3(kThreads), 0, stream, 1u, s, rows,
+                    new_lens);
 }
 
 cudaError_t launch_pages_compact(const ds_page_pool* pools, int num_pools, const PageState& s,

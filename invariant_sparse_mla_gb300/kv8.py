@@ -1,13 +1,14 @@
-"""The block-scaled 8-bit KV cache: append, decode and prefill attention.
+"""The block-scaled 8-bit KV cache: append, decode and prefill attention, and
+what moves its positions (accepted drafts, eviction).
 
-Argument marshalling for ds_kv8_append / ds_kv8_decode / ds_kv8_prefill (see
-include/ds_sparse_mla.h). The cache of one layer is ``kv_pages`` uint8
+Argument marshalling for the ds_kv8_* calls (see include/ds_sparse_mla.h). The cache of one layer is ``kv_pages`` uint8
 [num_pages, 2, kv_heads, 64, dim] (E4M3 codes, keys then values) with
 ``kv_scales`` float32 [num_pages, 2, kv_heads]; block tables are those of the
 latent cache. A ``stream`` argument runs the call, and what it allocates, on
 that stream instead of the current one.
 """
 
+import struct
 import threading
 
 import torch
@@ -245,3 +246,86 @@ def kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, 
          lens.data_ptr(), h, hk, d, float(scale), out.data_ptr(), lse.data_ptr(),
          workspace.data_ptr(), workspace.numel(), flag)
     return out, lse
+
+
+def _new_lens(new_lens, n, dev):
+    if new_lens is None:
+        return torch.empty(n, dtype=torch.int32, device=dev)
+    _arg(new_lens, "new_lens", torch.int32, dev, 1)
+    if new_lens.shape[0] != n:
+        raise ValueError(f"new_lens must have {n} entries")
+    return new_lens
+
+
+def kv8_accept(layers, block_table, lens, next_n, accepted, new_lens=None, err_flag=None,
+               stream=None):
+    """Move the accepted drafts of every request behind what was there before
+    them, in all ``layers`` (a list of (kv_pages, kv_scales), in place): draft
+    i of ``next_n`` lies at position ``lens[r] - next_n + i``, ``accepted``
+    int32 [R, width] holds the accepted numbers, ascending, -1 behind them.
+    Returns the new lengths (int32 [R]); ``lens`` stays (see pages_shrink)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_accept(layers, block_table, lens, next_n, accepted, new_lens, err_flag)
+    dev = _device(block_table, "block_table", torch.int32)
+    n, width, flag = _requests(block_table, lens, dev, err_flag)
+    _arg(accepted, "accepted", torch.int32, dev, 2)
+    if accepted.shape[0] != n:
+        raise ValueError("accepted must have one row per block_table row")
+    if not layers:
+        raise ValueError("layers must hold a cache")
+    words, shape = [], None
+    for pages, scales in layers:
+        here = _cache(pages, scales, dev)
+        if shape is not None and here != shape:
+            raise ValueError("every layer must have the same pages, heads and dim")
+        shape = here
+        words += (pages.data_ptr(), scales.data_ptr())
+    new_lens = _new_lens(new_lens, n, dev)
+    pages, hk, d = shape
+    _run(dev, lib().ds_kv8_accept, struct.pack(f"{len(words)}q", *words), len(layers), pages,
+         block_table.data_ptr(), width, lens.data_ptr(), n, hk, d, next_n, accepted.data_ptr(),
+         accepted.shape[1], new_lens.data_ptr(), flag)
+    return new_lens
+
+
+def kv8_evict_workspace_size(num_requests, num_kv_heads, mass_stride, budget, first, recent):
+    return int(lib().ds_kv8_evict_workspace_size(num_requests, num_kv_heads, mass_stride, budget,
+                                                 first, recent))
+
+
+def kv8_evict(mass, budget, first, recent, kv_pages, kv_scales, block_table, lens, refcounts=None,
+              new_lens=None, workspace=None, err_flag=None, stream=None):
+    """Hold every request to ``budget`` positions: each kv head keeps its first
+    ``first``, its last ``recent`` and the ones with the most ``mass`` (fp32
+    [R, kv_heads, positions]) between them, moved to the front (cache and mass in
+    place). Returns the new lengths (int32 [R]); ``lens`` stays (see
+    pages_shrink)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_evict(mass, budget, first, recent, kv_pages, kv_scales, block_table, lens,
+                             refcounts, new_lens, workspace, err_flag)
+    dev = _device(kv_pages, "kv_pages", torch.uint8)
+    pages, hk, d = _cache(kv_pages, kv_scales, dev)
+    n, width, flag = _requests(block_table, lens, dev, err_flag)
+    _arg(mass, "mass", torch.float32, dev, 3)
+    if mass.shape[:2] != (n, hk):
+        raise ValueError(f"mass must be [{n}, {hk}, positions], got {tuple(mass.shape)}")
+    counts = None
+    if refcounts is not None:
+        _arg(refcounts, "refcounts", torch.int32, dev, 1)
+        if refcounts.shape[0] != pages:
+            raise ValueError(f"refcounts must have {pages} entries")
+        counts = refcounts.data_ptr()
+    new_lens = _new_lens(new_lens, n, dev)
+    L = lib()
+    if workspace is None:
+        need = n and L.ds_kv8_evict_workspace_size(n, hk, mass.shape[2], budget, first, recent)
+        workspace = _scratch(need or 256, dev, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        _arg(workspace, "workspace", torch.uint8, dev)
+    _run(dev, L.ds_kv8_evict, mass.data_ptr(), mass.shape[2], budget, first, recent,
+         kv_pages.data_ptr(), kv_scales.data_ptr(), pages, counts, block_table.data_ptr(), width,
+         lens.data_ptr(), n, hk, d, new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(),
+         flag)
+    return new_lens

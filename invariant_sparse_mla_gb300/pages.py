@@ -1,4 +1,4 @@
-"""Pages of a paged cache: copy, free, fork, extend, compact.
+"""Pages of a paged cache: copy, free, fork, extend, shrink, compact.
 
 Argument marshalling for the ds_pages_* calls (see include/ds_sparse_mla.h).
 The state is ``refcounts`` int32 [num_pages], ``block_table`` int32
@@ -120,6 +120,18 @@ def pages_extend(refcounts, block_table, lens, rows, new_lens, workspace=None, e
     n = _list(new_lens, "new_lens", dev, _list(rows, "rows", dev))
     workspace, ws, ws_bytes = _workspace(workspace, refcounts, n)
     _run(dev, lib().ds_pages_extend, *state, rows.data_ptr(), new_lens.data_ptr(), n, ws, ws_bytes,
+         _flag(err_flag, dev))
+
+
+def pages_shrink(refcounts, block_table, lens, rows, new_lens, err_flag=None, stream=None):
+    """Lower row ``rows[i]`` to ``new_lens[i]`` positions and give back the pages
+    behind them (in place)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pages_shrink(refcounts, block_table, lens, rows, new_lens, err_flag)
+    dev, state = _state(refcounts, block_table, lens)
+    n = _list(new_lens, "new_lens", dev, _list(rows, "rows", dev))
+    _run(dev, lib().ds_pages_shrink, *state, rows.data_ptr(), new_lens.data_ptr(), n,
          _flag(err_flag, dev))
 
 

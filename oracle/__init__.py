@@ -55,4 +55,18 @@ from .kv8 import (  # noqa: F401
     kv8_visible,
 )
 from . import pages  # noqa: F401
-from .pages import pages_compact, pages_extend, pages_fork, pages_free  # noqa: F401
+from .pages import (  # noqa: F401
+    pages_compact,
+    pages_extend,
+    pages_fork,
+    pages_free,
+    pages_shrink,
+)
+from .kv8_step import (  # noqa: F401
+    kv8_accept,
+    kv8_evict,
+    kv8_mass,
+    kv8_tree,
+    qk_norm_rope,
+    tree_sees,
+)

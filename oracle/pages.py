@@ -138,3 +138,34 @@ def pages_compact(refs, table, lens):
                 flags.add("page")
         new_table.append(row)
     return new_refs, new_table, flags, n, moves
+
+
+def pages_shrink(refs, table, lens, rows, new_lens):
+    refs, table, lens = _copy(refs, table, lens)
+    before = list(lens)
+    flags, seen = set(), set()
+    for r, want in zip(rows, new_lens):
+        if r < 0:
+            continue
+        again = r in seen
+        seen.add(r)
+        if r >= len(table) or again:
+            flags.add("row")
+            continue
+        width = len(table[r])
+        if want == before[r]:
+            continue
+        if want < 0 or want > min(max(before[r], 0), PAGE * width):
+            flags.add("len")
+            continue
+        for j in range(held(want, width), held(before[r], width)):
+            p = table[r][j]
+            table[r][j] = -1
+            if p == -1:
+                continue
+            if not 0 <= p < len(refs) or refs[p] <= 0:
+                flags.add("page")
+                continue
+            refs[p] -= 1
+        lens[r] = want
+    return refs, table, lens, flags
