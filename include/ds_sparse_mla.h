@@ -594,6 +594,40 @@ int ds_kv8_accept(const ds_kv8_layer* layers, int num_layers, int64_t num_pages,
                   void* stream);
 
 /*
+ * ds_kv8_mass: adds up the attention weight that cached positions get from new
+ * tokens, for ds_kv8_evict. With the lse that ds_kv8_prefill, ds_kv8_decode or
+ * ds_kv8_tree_decode gave for the same q and cache,
+ *   mass[r, g, p] += sum over request r's tokens that see p (as in
+ *   ds_kv8_prefill) and the heads h of kv head g of exp(scale * q . k_p - lse).
+ * The positions of the call's own tokens, the last n of each request, start at
+ * 0: they are set, whatever mass held there, and a fresh page needs no clearing.
+ *
+ *  q, token_starts, kv_pages, kv_scales, block_table, lens, scale   as for
+ *               ds_kv8_prefill (decode: one token a request).
+ *  lse          float32 [num_tokens, num_heads]; -inf: the row adds nothing.
+ *  mass         float32 [num_requests, num_kv_heads, mass_stride], mass_stride at
+ *               least 64 * bt_stride. Rows of requests without tokens and
+ *               entries at and past lens[r] keep their values. A fork's row is a
+ *               copy that the caller makes.
+ *  err_flag     optional: DS_DEVERR_PAGE for a page outside the pool: its
+ *               positions get nothing (0 where they are the call's own).
+ *
+ * Scores are products of bfloat16 q and the codes with fp32 sums (about 2^-20 of
+ * the largest partial sum), exponentials and sums are fp32. A NaN key makes its
+ * own position NaN, a non-finite q or a NaN lse the positions that the row sees.
+ * num_tokens * num_heads / num_kv_heads is below 2^31 - 256 and bt_stride at most
+ * 2^20. A request's mass depends on that request alone, bit for bit; it does
+ * depend, in the last bits, on how its tokens are spread over calls. Needs no
+ * workspace.
+ */
+int ds_kv8_mass(const void* q, int64_t q_stride, const float* lse, int64_t num_tokens,
+                const int32_t* token_starts, int64_t num_requests, const void* kv_pages,
+                const float* kv_scales, int64_t num_pages, const int32_t* block_table,
+                int64_t bt_stride, const int32_t* lens, int num_heads, int num_kv_heads,
+                int head_dim, float scale, float* mass, int64_t mass_stride, int32_t* err_flag,
+                void* stream);
+
+/*
  * ds_kv8_evict: holds every request of one layer's cache to `budget` positions.
  * Each kv head of a request with more keeps its first `first` positions, its
  * last `recent` ones, and of those between the budget - first - recent with the

@@ -36,6 +36,7 @@ from .kv8 import (  # noqa: F401
     kv8_decode_workspace_size,
     kv8_evict,
     kv8_evict_workspace_size,
+    kv8_mass,
     kv8_prefill,
     kv8_prefill_workspace_size,
 )

@@ -68,9 +68,23 @@ struct Kv8EvictArgs {
   int32_t *starts, *ends, *top;   // workspace: [requests * kv_heads], and [.., ranked]
 };
 
+struct Kv8MassArgs {
+  Kv8Cache c;
+  const void* q;
+  int64_t q_stride;            // elements between tokens
+  const float* lse;            // [tokens, heads]
+  int64_t tokens;
+  const int32_t* starts;       // [requests + 1]
+  int heads;
+  float scale;
+  float* mass;                 // [requests, kv_heads, mass_stride]
+  int64_t mass_stride;
+};
+
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int num_layers, const Kv8AcceptArgs& a,
                               cudaStream_t stream);
 cudaError_t launch_kv8_evict(Kv8EvictArgs a, void* workspace, cudaStream_t stream);

@@ -298,6 +298,55 @@ int ds_kv8_prefill(const void* q, int64_t q_stride, int64_t num_tokens,
   return launched(fn, dsmla::launch_kv8_prefill(a, as_stream(stream)));
 }
 
+int ds_kv8_mass(const void* q, int64_t q_stride, const float* lse, int64_t num_tokens,
+                const int32_t* token_starts, int64_t num_requests, const void* kv_pages,
+                const float* kv_scales, int64_t num_pages, const int32_t* block_table,
+                int64_t bt_stride, const int32_t* lens, int num_heads, int num_kv_heads,
+                int head_dim, float scale, float* mass, int64_t mass_stride, int32_t* err_flag,
+                void* stream) {
+  const char* fn = "ds_kv8_mass";
+  dsmla::Kv8MassArgs a{};
+  a.c = {const_cast<uint8_t*>(static_cast<const uint8_t*>(kv_pages)),
+         const_cast<float*>(kv_scales), num_pages, block_table, bt_stride, lens, num_requests,
+         num_kv_heads, head_dim, err_flag};
+  int st = check_cache(fn, a.c);
+  if (st == DS_OK) st = check_heads(fn, num_heads, num_kv_heads, q_stride, head_dim, scale);
+  if (st == DS_OK) st = check_tokens(fn, num_tokens);
+  if (st != DS_OK) return st;
+  if (bt_stride > (1 << 20))
+    return report_error(DS_ERR_UNSUPPORTED, "%s: bt_stride=%lld exceeds 2^20", fn,
+                        (long long)bt_stride);
+  if (mass_stride < bt_stride * dsmla::kPage)
+    return report_error(DS_ERR_SHAPE,
+                        "%s: mass_stride=%lld must be at least 64 * bt_stride = %lld", fn,
+                        (long long)mass_stride, (long long)bt_stride * dsmla::kPage);
+  if (num_tokens == 0 || num_requests == 0) return report_ok();
+  if (num_tokens > (int64_t)INT32_MAX / (num_heads / num_kv_heads) - 256)
+    return report_error(DS_ERR_UNSUPPORTED, "%s: num_tokens=%lld is too large with %d query heads "
+                        "a kv head (below 2^31 rows)", fn, (long long)num_tokens,
+                        num_heads / num_kv_heads);
+  st = check_ptrs(fn, {{q, "q", 16},
+                       {lse, "lse", 4},
+                       {token_starts, "token_starts", 4},
+                       {kv_pages, "kv_pages", 16},
+                       {kv_scales, "kv_scales", 4},
+                       {block_table, "block_table", 4},
+                       {lens, "lens", 4},
+                       {mass, "mass", 4},
+                       {err_flag, "err_flag", 4, true}});
+  if (st != DS_OK) return st;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.lse = lse;
+  a.tokens = num_tokens;
+  a.starts = token_starts;
+  a.heads = num_heads;
+  a.scale = scale;
+  a.mass = mass;
+  a.mass_stride = mass_stride;
+  return launched(fn, dsmla::launch_kv8_mass(a, as_stream(stream)));
+}
+
 size_t ds_kv8_evict_workspace_size(int64_t num_requests, int num_kv_heads, int64_t mass_stride,
                                    int budget, int first, int recent) {
   const char* fn = "ds_kv8_evict_workspace_size";

@@ -248,6 +248,37 @@ def kv8_prefill(q, token_starts, kv_pages, kv_scales, block_table, lens, scale, 
     return out, lse
 
 
+def kv8_mass(q, lse, token_starts, kv_pages, kv_scales, block_table, lens, scale, mass,
+             err_flag=None, stream=None):
+    """Add to ``mass`` (fp32 [R, kv_heads, positions], at least 64 per table
+    entry) the attention weight that every position gets from the new tokens: q
+    bf16 [T, H, dim] and ``token_starts`` as for kv8_prefill, ``lse`` fp32 [T, H]
+    as attention gave it. The tokens' own positions are set instead. Returns
+    ``mass``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_mass(q, lse, token_starts, kv_pages, kv_scales, block_table, lens, scale,
+                            mass, err_flag)
+    dev = _device(kv_pages, "kv_pages", torch.uint8)
+    pages, hk, d = _cache(kv_pages, kv_scales, dev)
+    qs = _tokens(q, "q", torch.bfloat16, dev, 1)
+    n, width, flag = _requests(block_table, lens, dev, err_flag)
+    _starts(token_starts, n, dev)
+    t, h, qd = q.shape
+    if qd != d:
+        raise ValueError(f"q must have head dim {d}, got {qd}")
+    _arg(lse, "lse", torch.float32, dev, 2)
+    if lse.shape != (t, h):
+        raise ValueError(f"lse must be [{t}, {h}], got {tuple(lse.shape)}")
+    _arg(mass, "mass", torch.float32, dev, 3)
+    if mass.shape[:2] != (n, hk):
+        raise ValueError(f"mass must be [{n}, {hk}, positions], got {tuple(mass.shape)}")
+    _run(dev, lib().ds_kv8_mass, q.data_ptr(), qs, lse.data_ptr(), t, token_starts.data_ptr(), n,
+         kv_pages.data_ptr(), kv_scales.data_ptr(), pages, block_table.data_ptr(), width,
+         lens.data_ptr(), h, hk, d, float(scale), mass.data_ptr(), mass.shape[2], flag)
+    return mass
+
+
 def _new_lens(new_lens, n, dev):
     if new_lens is None:
         return torch.empty(n, dtype=torch.int32, device=dev)

@@ -1,0 +1,258 @@
+"""GPU tests of the attention mass against float64, and of a run of mass and
+eviction as a server would use them."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from harness import ensure_built
+from kv8_cases import Cache, bits
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def ds():
+    return ensure_built()
+
+
+def _starts(counts, lead=0):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32) + lead
+
+
+def _lse_of(q, starts, c, scale):
+    """float32 lse of causal attention, as the attention calls give it."""
+    counts = np.diff(starts)
+    rows = oracle.kv8_visible(c.lens, counts, c.table.shape[1])
+    lse = np.full(q.shape[:2], np.nan, np.float32)
+    got = oracle.kv8_attention(bits(q)[starts[0]:starts[-1]], rows, c.codes, c.scales, c.table, scale)
+    lse[starts[0]:starts[-1]] = got[1]
+    return lse
+
+
+def _check(got, want, old, reach, dim, steps, starts, lens, width):
+    """A score is a dim-term fp32 sum, its exponent two more roundings of it and of
+    the lse; a weight is off by that and by 2^-21 of the exponential, a sum of
+    columns and steps by a half step each."""
+    for r, raw in enumerate(lens):
+        n, length = int(starts[r + 1] - starts[r]), min(max(raw, 0), 64 * width)
+        for g in range(got.shape[1]):
+            base = np.where(np.arange(got.shape[2]) < raw - n, old[r, g], 0.0)
+            added = np.maximum(want[r, g] - base, 0.0)
+            rel = np.expm1((dim + 16) * 2.0 ** -24 * reach[r, g]) + (80 + steps) * 2.0 ** -24 + 2.0 ** -20
+            tol = rel * added + 2.0 ** -23 * np.abs(want[r, g]) + 1e-37
+            bad = ~(np.abs(got[r, g] - want[r, g]) <= tol)
+            bad &= ~(np.isnan(got[r, g]) & np.isnan(want[r, g]))
+            assert not bad[:length].any(), (r, g, np.nonzero(bad)[0][:5])
+            # nothing behind the last position, nothing of requests without tokens
+            keep = slice(length if n else 0, None)
+            assert np.array_equal(got[r, g, keep], old[r, g, keep], equal_nan=True)
+
+
+def _case(ds, lens, counts, heads, hk, dim, seed, gain=2.5, lead=0, tail=0, pad=0, bad=(), extra=0,
+          edit=None, spread=3, err_want=0):
+    c = Cache(lens, hk, dim, seed, spread=spread)
+    for r, b, p in bad:
+        c.table[r, b] = p
+    starts = _starts(counts, lead)
+    t = int(starts[-1]) + tail
+    q = c.q(t, heads + pad, gain)
+    scale = dim ** -0.5
+    if edit is not None:
+        edit(q, c)
+    lse = _lse_of(q[:, :heads], starts, c, scale)
+    mass = np.abs(c.rng.standard_normal((len(lens), hk, 64 * c.table.shape[1] + extra))) \
+        .astype(np.float32)
+    codes, scales, table, lens_d = c.device()
+    md = torch.as_tensor(mass).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = ds.kv8_mass(q.to(DEV)[:, :heads], torch.as_tensor(lse).to(DEV),
+                      torch.as_tensor(starts).to(DEV), codes, scales, table, lens_d, scale, md,
+                      err_flag=err)
+    torch.cuda.synchronize()
+    assert got is md and int(err) == err_want
+    want, reach = oracle.kv8_mass(bits(q[:, :heads]), lse, starts, c.codes, c.scales, c.table,
+                                  c.lens, scale, mass)
+    _check(md.cpu().numpy(), want, mass, reach, dim, max(counts) * heads // hk // 128 + 1, starts,
+           c.lens, c.table.shape[1])
+    return md
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,hk", [(1, 1), (8, 1), (6, 2), (16, 2), (28, 4), (130, 1)])
+def test_one_token(ds, heads, hk, dim):
+    _case(ds, [1, 64, 65, 128, 129, 700, 0, 300], [1, 1, 1, 1, 1, 1, 1, 1], heads, hk, dim, seed=heads)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,counts,heads,hk", [
+    ([1], [1], 3, 1), ([200], [200], 4, 2), ([500, 130, 64, 7], [3, 130, 0, 7], 14, 2),
+    ([900, 257], [33, 256], 8, 1), ([128, 128, 129], [128, 127, 1], 2, 2), ([640], [129], 1, 1),
+    ([300, 40, 0, -3, 77], [17, 1, 0, 0, 16], 40, 8)])
+def test_ragged(ds, lens, counts, heads, hk, dim):
+    _case(ds, lens, counts, heads, hk, dim, seed=len(lens) + dim, lead=3, tail=2, pad=heads % 3)
+
+
+def test_many_items_per_cta(ds):
+    """More items than the GPU has SMs, of several requests: rings wrap."""
+    rng = np.random.default_rng(1)
+    lens = rng.integers(100, 1500, 24)
+    _case(ds, lens, rng.integers(0, 4, 24), 16, 8, 128, seed=1)
+    _case(ds, lens, rng.integers(0, 30, 24), 16, 8, 64, seed=2)
+
+
+def test_a_request_shorter_than_its_tokens(ds):
+    _case(ds, [5, 100], [9, 130], 4, 2, 64, seed=3)
+
+
+def test_pages_outside_the_pool(ds):
+    _case(ds, [300, 200], [4, 70], 4, 2, 128, seed=4, bad=[(0, 1, -1), (0, 4, 10 ** 6), (1, 2, -7)],
+          err_want=2)
+
+
+def test_every_code_and_magnitude(ds):
+    """All E4M3 codes (subnormal ones too) and q far from 1, exactly."""
+    def edit(q, c):
+        flat = c.codes[c.table[0, 0], 0, 0]
+        flat[:] = np.arange(flat.size, dtype=np.int64).reshape(flat.shape) % 0x7F
+        flat[1::2] |= 0x80
+        q[:] = 0
+        q[:, :, 0] = 1.0
+        q[:, :, 7] = 2.0 ** -9
+        q[:, 0, 9] = 3e-5
+    _case(ds, [64], [3], 2, 1, 64, seed=5, edit=edit, spread=1)
+    _case(ds, [64, 200], [3, 9], 2, 1, 128, seed=6, gain=1e-30)
+    _case(ds, [64, 200], [3, 9], 2, 1, 128, seed=6, gain=40.0)
+
+
+def test_non_finite_inputs(ds):
+    c = Cache([200, 150], 2, 64, 7)
+    scale = 0.125
+    q = c.q(5, 4)
+    starts = _starts([3, 2])
+    lse = _lse_of(q, starts, c, scale)
+    codes, scales, table, lens = c.device()
+
+    def run(q, lse, codes=codes):
+        mass = torch.ones((2, 2, 64 * table.shape[1]), device=DEV)
+        ds.kv8_mass(q.to(DEV), torch.as_tensor(lse).to(DEV), torch.as_tensor(starts).to(DEV), codes,
+                    scales, table, lens, scale, mass)
+        torch.cuda.synchronize()
+        return mass.cpu()
+    want = run(q, lse)
+    # a NaN key: its position alone, in its head alone
+    bad = codes.clone()
+    bad[table[0, 1].item(), 0, 1, 5, 40] = 0xFF
+    got = run(q, lse, bad)
+    assert got[0, 1, 69].isnan() and got.isnan().sum() == 1
+    got[0, 1, 69] = want[0, 1, 69]
+    assert torch.equal(got, want)
+    # a row whose lse is -inf adds nothing, one of +inf neither; NaN shows where it sees
+    l2 = lse.copy()
+    l2[0, 0], l2[4, 3] = -np.inf, np.nan
+    got = run(q, l2)
+    # (token 0 sees 198 positions and its weights sum to 1; one below 2^-25 is lost beside 1)
+    assert not got[0].isnan().any() and (got[0, 0] <= want[0, 0]).all()
+    less = (want[0, 0].double() - got[0, 0].double()).sum().item()
+    assert abs(less - 1.0) <= 200 * 2.0 ** -22 and torch.equal(got[0, 1], want[0, 1])
+    assert got[1, 1, :150].isnan().all() and not got[1, 0].isnan().any()
+    q2 = q.clone()
+    q2[1, 2, 3] = float("nan")     # token 1 of request 0 sees 199 positions
+    got = run(q2, lse)
+    assert got[0, 1, :199].isnan().all() and not got[0, 1, 199:].isnan().any()
+    assert not got[0, 0].isnan().any() and torch.equal(got[1], want[1])
+
+
+def test_bits_do_not_depend_on_the_batch(ds):
+    rng = np.random.default_rng(8)
+    lens, counts = [1500, 300, 2000, 64, 900, 1100], [1, 40, 5, 64, 700, 0]
+    c = Cache(lens, 4, 128, 8)
+    starts, scale = _starts(counts), 128 ** -0.5
+    q = c.q(int(starts[-1]), 12)
+    lse = torch.as_tensor(rng.standard_normal((len(q), 12)).astype(np.float32) + 8).to(DEV)
+    codes, scales, table, ln = c.device()
+    qd, sd = q.to(DEV), torch.as_tensor(starts).to(DEV)
+    whole = torch.zeros((6, 4, 64 * table.shape[1]), device=DEV)
+    ds.kv8_mass(qd, lse, sd, codes, scales, table, ln, scale, whole)
+    for r in range(6):
+        a, b = starts[r], starts[r + 1]
+        one = torch.zeros((1, 4, 64 * table.shape[1]), device=DEV)
+        ds.kv8_mass(qd[a:b], lse[a:b], sd[r:r + 2] - int(a), codes, scales, table[r:r + 1].contiguous(),
+                    ln[r:r + 1], scale, one)
+        assert torch.equal(one[0], whole[r])
+
+
+def test_weights_of_a_row_sum_to_one(ds):
+    """With the lse of the cache's own attention the mass of a step is one per
+    query row, and repeated calls add up."""
+    lens = [3000, 128, 777]
+    c = Cache(lens, 2, 128, 9)
+    codes, scales, table, ln = c.device()
+    q = c.q(3, 16).to(DEV)
+    out, lse = ds.kv8_decode(q[:, None], codes, scales, table, ln, 0.09)
+    starts = torch.arange(4, dtype=torch.int32, device=DEV)
+    mass = torch.zeros((3, 2, 64 * table.shape[1]), device=DEV)
+    for i in range(1, 4):
+        ds.kv8_mass(q, lse[:, 0].contiguous(), starts, codes, scales, table, ln, 0.09, mass)
+        # (the last position is the call's own: it is set, not added to)
+        last = torch.stack([mass[r, :, n - 1] for r, n in enumerate(lens)])
+        total = mass.double().sum(-1) - last
+        rest = (total / i + last).cpu()
+        # decode's scores are off by up to 2^-14 and more roundings
+        assert (rest - 8).abs().max() <= 8 * 2.0 ** -13
+
+
+def test_capture_streams_and_two_at_once(ds):
+    c = Cache([1500, 800], 2, 64, 10)
+    codes, scales, table, ln = c.device()
+    starts = torch.as_tensor(_starts([40, 8])).to(DEV)
+    q, lse = c.q(48, 4).to(DEV), torch.full((48, 4), 6.0, device=DEV)
+    z = torch.zeros((2, 2, 64 * table.shape[1]), device=DEV)
+
+    def run(mass, **kw):
+        return ds.kv8_mass(q, lse, starts, codes, scales, table, ln, 0.125, mass, **kw)
+    want = run(z.clone())
+    a, b, m = z.clone(), z.clone(), z.clone()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        a.zero_()
+        b.zero_()
+        torch.cuda.synchronize()
+        run(a, stream=s1)
+        run(b, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(m)
+    for _ in range(2):
+        m.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(m, want)
+
+
+def test_refusals(ds):
+    c = Cache([100], 2, 64, 11)
+    codes, scales, table, ln = c.device()
+    starts = torch.as_tensor(_starts([2])).to(DEV)
+    q, lse = c.q(2, 4).to(DEV), torch.zeros((2, 4), device=DEV)
+    mass = torch.zeros((1, 2, 64 * table.shape[1]), device=DEV)
+    with pytest.raises(ValueError):
+        ds.kv8_mass(q, lse[:1], starts, codes, scales, table, ln, 0.1, mass)
+    with pytest.raises(ValueError):
+        ds.kv8_mass(q, lse, starts[:1], codes, scales, table, ln, 0.1, mass)
+    with pytest.raises(ValueError):
+        ds.kv8_mass(q, lse, starts, codes, scales, table, ln, 0.1, mass[:, :1].contiguous())
+    with pytest.raises(ds.DSError, match="mass_stride"):
+        ds.kv8_mass(q, lse, starts, codes, scales, table, ln, 0.1, mass[..., :64].contiguous())
+    with pytest.raises(TypeError):
+        ds.kv8_mass(q, lse.double(), starts, codes, scales, table, ln, 0.1, mass)
+    with pytest.raises(ds.DSError, match="num_heads=3"):
+        ds.kv8_mass(q[:, :3].contiguous(), lse[:, :3].contiguous(), starts, codes, scales, table, ln,
+                    0.1, mass)
+    ds.kv8_mass(q[:0], lse[:0], starts * 0, codes, scales, table, ln, 0.1, mass)
+    assert (mass == 0).all()
