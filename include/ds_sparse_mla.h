@@ -490,6 +490,26 @@ size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_he
                                     int num_kv_heads, int head_dim, int64_t bt_stride);
 
 /*
+ * ds_kv8_tree_decode: the same for a tree of drafts: the next_n tokens of request
+ * r are nodes, node i at position lens[r] - next_n + i of the cache. Node j sees
+ * every position before lens[r] - next_n, and node i where bit i of masks[r, j]
+ * is set (its ancestors and itself, in a tree; any set is taken, also one with no
+ * bit). Positions below 0 do not exist, those past the table are not seen; bits
+ * from next_n on are ignored.
+ *
+ *  masks        uint64 [num_requests, next_n], 8-byte aligned.
+ *
+ * All else as for ds_kv8_decode, its workspace size included. With masks of a
+ * chain (bit i set for i <= j) the results are those of ds_kv8_decode, bit for bit.
+ */
+int ds_kv8_tree_decode(const void* q, int64_t q_stride, const uint64_t* masks,
+                       const void* kv_pages, const float* kv_scales, int64_t num_pages,
+                       const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                       int64_t num_requests, int next_n, int num_heads, int num_kv_heads,
+                       int head_dim, float scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/*
  * ds_kv8_prefill: the same attention for ragged prompts (or prompt chunks):
  * token i of a request with n tokens sees the first
  * clamp(lens[r] - n + 1 + i, 0, 64 * bt_stride) positions (causal). Rows of

@@ -39,6 +39,7 @@ from .kv8 import (  # noqa: F401
     kv8_mass,
     kv8_prefill,
     kv8_prefill_workspace_size,
+    kv8_tree_decode,
 )
 from .norm_rope import qk_norm_rope  # noqa: F401
 from .pages import (  # noqa: F401

@@ -111,6 +111,9 @@ def lib():
         L.ds_qk_norm_rope.restype = i32
         L.ds_qk_norm_rope.argtypes = [vp, i64, i32, vp, vp, i64, i32, vp, i64, i32, i32, f32, vp,
                                       vp, i32, i32, i32, vp, i64, vp, i64, vp]
+        L.ds_kv8_tree_decode.restype = i32
+        L.ds_kv8_tree_decode.argtypes = [vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, i32, i32, i32,
+                                         i32, f32, vp, vp, vp, sz, vp, vp]
         L.ds_kv8_mass.restype = i32
         L.ds_kv8_mass.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i32, i32,
                                   i32, f32, vp, i64, vp, vp]
@@ -133,7 +136,7 @@ EXPORTED = ("ds_last_error", "ds_supported_config", "ds_topk_workspace_size",
             "ds_kv8_append", "ds_kv8_decode", "ds_kv8_decode_workspace_size", "ds_kv8_prefill",
             "ds_kv8_prefill_workspace_size", "ds_pages_workspace_size", "ds_pages_copy",
             "ds_pages_free", "ds_pages_fork", "ds_pages_extend", "ds_pages_compact",
-            "ds_pages_shrink", "ds_qk_norm_rope", "ds_kv8_mass", "ds_kv8_accept",
+            "ds_pages_shrink", "ds_qk_norm_rope", "ds_kv8_tree_decode", "ds_kv8_mass", "ds_kv8_accept",
             "ds_kv8_evict", "ds_kv8_evict_workspace_size")
 
 

@@ -42,6 +42,7 @@ struct Kv8AttnArgs {
   int64_t tokens;              // rows of q: requests * next_n, or num_tokens
   const int32_t* starts;       // prefill: [requests + 1]; decode: nullptr
   int next_n;                  // decode; 0 for prefill
+  const uint64_t* masks;       // decode of a tree: [requests, next_n]; nullptr: causal
   int heads;
   float scale;
   void* out;

@@ -120,6 +120,58 @@ int launched(const char* fn, cudaError_t e) {
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// Decode attention, causal or (tree) by masks.
+int decode(const char* fn, const void* q, int64_t q_stride, bool tree, const uint64_t* masks,
+           const void* kv_pages, const float* kv_scales, int64_t num_pages,
+           const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+           int64_t num_requests, int next_n, int num_heads, int num_kv_heads, int head_dim,
+           float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+           int32_t* err_flag, void* stream) {
+  dsmla::Kv8AttnArgs a{};
+  a.c = {const_cast<uint8_t*>(static_cast<const uint8_t*>(kv_pages)),
+         const_cast<float*>(kv_scales), num_pages, block_table, bt_stride, lens, num_requests,
+         num_kv_heads, head_dim, err_flag};
+  int st = check_cache(fn, a.c);
+  if (st == DS_OK) st = check_heads(fn, num_heads, num_kv_heads, q_stride, head_dim, scale);
+  if (st != DS_OK) return st;
+  if (next_n < 1 || next_n > 64)
+    return report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64",
+                        fn, next_n);
+  if (num_requests * next_n > (int64_t)INT32_MAX / num_heads)
+    return report_error(DS_ERR_UNSUPPORTED,
+                        "%s: num_requests=%lld is too large with next_n=%d and num_heads=%d "
+                        "(below 2^31 rows)", fn, (long long)num_requests, next_n, num_heads);
+  if (num_requests == 0) return report_ok();
+  st = check_ptrs(fn, {{q, "q", 16},
+                       {masks, "masks", 8, !tree},
+                       {kv_pages, "kv_pages", 16},
+                       {kv_scales, "kv_scales", 4},
+                       {block_table, "block_table", 4},
+                       {lens, "lens", 4},
+                       {out, "out", 16},
+                       {lse, "lse", 4},
+                       {workspace, "workspace", 256},
+                       {err_flag, "err_flag", 4, true}});
+  if (st != DS_OK) return st;
+  const size_t need = dsmla::kv8_decode_workspace_bytes(num_requests, next_n, num_heads,
+                                                        num_kv_heads, head_dim, bt_stride);
+  if (workspace_bytes < need)
+    return report_error(DS_ERR_WORKSPACE,
+                        "%s: workspace_bytes=%zu is smaller than the %zu bytes needed", fn,
+                        workspace_bytes, need);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.tokens = num_requests * next_n;
+  a.next_n = next_n;
+  a.masks = masks;
+  a.heads = num_heads;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  return launched(fn, dsmla::launch_kv8_decode(a, as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -185,48 +237,20 @@ int ds_kv8_decode(const void* q, int64_t q_stride, const void* kv_pages, const f
                   const int32_t* lens, int64_t num_requests, int next_n, int num_heads,
                   int num_kv_heads, int head_dim, float scale, void* out, float* lse,
                   void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
-  const char* fn = "ds_kv8_decode";
-  dsmla::Kv8AttnArgs a{};
-  a.c = {const_cast<uint8_t*>(static_cast<const uint8_t*>(kv_pages)),
-         const_cast<float*>(kv_scales), num_pages, block_table, bt_stride, lens, num_requests,
-         num_kv_heads, head_dim, err_flag};
-  int st = check_cache(fn, a.c);
-  if (st == DS_OK) st = check_heads(fn, num_heads, num_kv_heads, q_stride, head_dim, scale);
-  if (st != DS_OK) return st;
-  if (next_n < 1 || next_n > 64)
-    return report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64",
-                        fn, next_n);
-  if (num_requests * next_n > (int64_t)INT32_MAX / num_heads)
-    return report_error(DS_ERR_UNSUPPORTED,
-                        "%s: num_requests=%lld is too large with next_n=%d and num_heads=%d "
-                        "(below 2^31 rows)", fn, (long long)num_requests, next_n, num_heads);
-  if (num_requests == 0) return report_ok();
-  st = check_ptrs(fn, {{q, "q", 16},
-                       {kv_pages, "kv_pages", 16},
-                       {kv_scales, "kv_scales", 4},
-                       {block_table, "block_table", 4},
-                       {lens, "lens", 4},
-                       {out, "out", 16},
-                       {lse, "lse", 4},
-                       {workspace, "workspace", 256},
-                       {err_flag, "err_flag", 4, true}});
-  if (st != DS_OK) return st;
-  const size_t need = dsmla::kv8_decode_workspace_bytes(num_requests, next_n, num_heads,
-                                                        num_kv_heads, head_dim, bt_stride);
-  if (workspace_bytes < need)
-    return report_error(DS_ERR_WORKSPACE,
-                        "%s: workspace_bytes=%zu is smaller than the %zu bytes needed", fn,
-                        workspace_bytes, need);
-  a.q = q;
-  a.q_stride = q_stride;
-  a.tokens = num_requests * next_n;
-  a.next_n = next_n;
-  a.heads = num_heads;
-  a.scale = scale;
-  a.out = out;
-  a.lse = lse;
-  a.workspace = workspace;
-  return launched(fn, dsmla::launch_kv8_decode(a, as_stream(stream)));
+  return decode("ds_kv8_decode", q, q_stride, false, nullptr, kv_pages, kv_scales, num_pages,
+                block_table, bt_stride, lens, num_requests, next_n, num_heads, num_kv_heads,
+                head_dim, scale, out, lse, workspace, workspace_bytes, err_flag, stream);
+}
+
+int ds_kv8_tree_decode(const void* q, int64_t q_stride, const uint64_t* masks,
+                       const void* kv_pages, const float* kv_scales, int64_t num_pages,
+                       const int32_t* block_table, int64_t bt_stride, const int32_t* lens,
+                       int64_t num_requests, int next_n, int num_heads, int num_kv_heads,
+                       int head_dim, float scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  return decode("ds_kv8_tree_decode", q, q_stride, true, masks, kv_pages, kv_scales, num_pages,
+                block_table, bt_stride, lens, num_requests, next_n, num_heads, num_kv_heads,
+                head_dim, scale, out, lse, workspace, workspace_bytes, err_flag, stream);
 }
 
 size_t ds_kv8_prefill_workspace_size(int64_t num_tokens, int64_t num_requests, int num_heads,

@@ -103,7 +103,7 @@ Shape shape_of(int next_n, int group) {
   return s;
 }
 
-template <int R8, int DIM>
+template <int R8, int DIM, bool TREE>
 struct Layout {
   static constexpr int kNP = (R8 + 15) / 16 * 16;           // columns of P and O
   static constexpr int kUnit = kTile * DIM;                 // K or V codes of one tile
@@ -136,7 +136,8 @@ struct Layout {
   static constexpr int kBy = kVis + R8 * 4;                 // by how much a reference moved
   static constexpr int kSet = kBy + R8 * 4;                 // 1: row has one; 2: only low scores
   static constexpr int kLost = kSet + R8 * 4;               // what a score may lose at key scale 1
-  static constexpr int kMisc = kLost + R8 * 4;              // tmem slot, abort, start of work
+  static constexpr int kMask = kLost + R8 * 4;              // TREE: the drafts each row sees
+  static constexpr int kMisc = kMask + (TREE ? R8 * 8 : 0);   // tmem slot, abort, start of work
   static constexpr int kEnd = kMisc + 64;
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= kBudget, "shared memory of an SM");
@@ -169,6 +170,7 @@ struct Params {
   float* part_o;
   float2* part_ml;
   int64_t spans;         // slots per (request, kv head, row group)
+  const uint64_t* masks; // TREE: [requests, next_n]
   Kv8Cache c;
 };
 
@@ -419,10 +421,13 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
     return make_sw64_desc(addr, 16, 512);
 }
 
-template <int R8, int DIM>
-__global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_kernel(
+// TREE: the next_n tokens are the nodes of a tree of drafts. All see the positions
+// before them, and draft i at position len - next_n + i where bit i of their mask
+// is set; only the tiles that hold drafts differ from those of a causal suffix.
+template <int R8, int DIM, bool TREE>
+__global__ void __launch_bounds__(kThreads, Layout<R8, DIM, TREE>::kCtas) kv8_decode_kernel(
     const __grid_constant__ CUtensorMap map, const Params p) {
-  using LY = Layout<R8, DIM>;
+  using LY = Layout<R8, DIM, TREE>;
   constexpr int NP = LY::kNP, NK = LY::kNK, NV = LY::kNV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -437,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
   float* by_s = reinterpret_cast<float*>(smem + LY::kBy);
   int* set_s = reinterpret_cast<int*>(smem + LY::kSet);
   float* lost_s = reinterpret_cast<float*>(smem + LY::kLost);
+  uint64_t* mask_s = reinterpret_cast<uint64_t*>(smem + LY::kMask);   // TREE
   volatile int* lossy_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 48);   // a Q's number
   volatile int* move_s = reinterpret_cast<volatile int*>(smem + LY::kMisc + 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
@@ -725,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
     auto give_up = [&] { abort_s[(g + 1) & 1] = (int)(g + 2); };
     int64_t last_q = -1;       // (request, hg) whose Q is in shared memory
     int token = 0;             // of row tid
+    uint64_t mask = 0;         // TREE: of row tid
     int queries = 0;           // Qs so far
     // Requests without positions are no items: their outputs here.
     for (int64_t r = blockIdx.x; r < p.c.requests; r += gridDim.x) {
@@ -749,6 +756,11 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
       if (qid != last_q) {
         last_q = qid;
         token = (row0 + tid) / p.group;
+        if constexpr (TREE) {
+          mask = 0;
+          if (tid < R8 && token < p.next_n) mask = p.masks[(int64_t)w.r * p.next_n + token];
+          if (p.next_n < 64) mask &= (1ull << p.next_n) - 1;
+        }
         ++queries;
         constexpr int E = DIM / 32, NR = R8 / 8;
         float x[NR][E];
@@ -804,11 +816,25 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
         mbar_arrive(&bars[kQReady]);   // (f_s is read behind the barrier below)
       }
       // Row r's token j sees len - next_n + 1 + j positions (clamped).
+      // (A tree's row: up to its last draft.)
+      auto clamped = [&](int64_t v) { return (int)(v < 0 ? 0 : (v > w.len ? w.len : v)); };
+      const int64_t base = (int64_t)w.raw - p.next_n;   // TREE: the first draft's position
       if (tid < R8) {
-        const int64_t v = (int64_t)w.raw - p.next_n + 1 + token;
         m_s[tid] = 0.0f;
-        vis_s[tid] = (int)(v < 0 ? 0 : (v > w.len ? w.len : v));
+        if constexpr (TREE) {
+          mask_s[tid] = mask;
+          vis_s[tid] = clamped(base + 64 - __clzll((long long)mask));
+        } else {
+          vis_s[tid] = clamped(base + 1 + token);
+        }
       }
+      // Whether row i (of this warp's) sees position ps of the request.
+      auto sees = [&](int i, int ps) {
+        if constexpr (TREE)
+          return ps < base || ((mask_s[rh + i] >> ((ps - base) & 63)) & 1u) != 0u;
+        else
+          return ps < vis_s[rh + i];
+      };
 #pragma unroll
       for (int i = 0; i < RH; ++i) l[i] = 0.0f;
       uint32_t nan_rows = 0;    // rows that see a NaN value in this lane's dim
@@ -816,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
       float lost_top = 0.0f;    // most that a row of this warp may lose at key scale 1
       if (*lossy_s == queries)
         for (int i = 0; i < RH; ++i) lost_top = fmaxf(lost_top, lost_s[rh + i]);
-      const int min_vis = vis_s[0];
+      const int min_vis = TREE ? clamped(base) : vis_s[0];   // all rows see what is before
       bool unset = true;        // some row has no reference yet
 
       for (int t = 0; t < nt; ++t, ++g) {
@@ -880,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
           const bool here = mt.w != 0.0f && pos < w.len;
 #pragma unroll
           for (int i = 0; i < RH; ++i)
-            if (!here || pos >= vis_s[rh + i]) s[i] = -INFINITY;
+            if (!here || !sees(i, pos)) s[i] = -INFINITY;
         }
         bool above = unset;
 #pragma unroll
@@ -947,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM>::kCtas) kv8_decode_k
                   if ((*at & 0x7FFFu) <= 0x7C00u) continue;
                   if (pass == 1) *at = 0;
                   for (int r = 0; r < RH; ++r)
-                    if (ps < vis_s[rh + r]) nan_rows |= 1u << r;
+                    if (sees(r, ps)) nan_rows |= 1u << r;
                 }
               }
               named_bar_sync(1, kSoftmax);
@@ -1178,12 +1204,12 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
   if (lane == 0) p.lse[w] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <int R8, int DIM>
+template <int R8, int DIM, bool TREE>
 cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, int64_t items,
                         cudaStream_t stream) {
-  using LY = Layout<R8, DIM>;
+  using LY = Layout<R8, DIM, TREE>;
   static PerDeviceOnce once;
-  auto kern = kv8_decode_kernel<R8, DIM>;
+  auto kern = kv8_decode_kernel<R8, DIM, TREE>;
   const cudaError_t e = set_max_dynamic_smem(once, dev, kern, LY::kSmem);
   if (e != cudaSuccess) return e;
   // At most one CTA per item.
@@ -1192,16 +1218,16 @@ cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, int64_
                     stream, 1u, map, p);
 }
 
-template <int DIM>
+template <int DIM, bool TREE>
 cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStream_t stream) {
   const int64_t items = p.c.requests * p.c.kv_heads * p.row_groups * p.spans;
   cudaError_t e;
   switch ((p.rows + 7) / 8) {
-    case 1: e = launch_main<8, DIM>(map, p, dev, items, stream); break;
-    case 2: e = launch_main<16, DIM>(map, p, dev, items, stream); break;
-    case 3: e = launch_main<24, DIM>(map, p, dev, items, stream); break;
-    case 4: e = launch_main<32, DIM>(map, p, dev, items, stream); break;
-    default: e = launch_main<40, DIM>(map, p, dev, items, stream); break;
+    case 1: e = launch_main<8, DIM, TREE>(map, p, dev, items, stream); break;
+    case 2: e = launch_main<16, DIM, TREE>(map, p, dev, items, stream); break;
+    case 3: e = launch_main<24, DIM, TREE>(map, p, dev, items, stream); break;
+    case 4: e = launch_main<32, DIM, TREE>(map, p, dev, items, stream); break;
+    default: e = launch_main<40, DIM, TREE>(map, p, dev, items, stream); break;
   }
   if (e != cudaSuccess || p.spans == 1) return e;   // no table holds a row of two spans
   const int64_t rows = p.c.requests * p.next_n * p.heads;
@@ -1270,7 +1296,12 @@ cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream) {
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) +
                                         pad256((size_t)slots * dim * 4));
   p.c = a.c;
-  return dim == 128 ? launch_dim<128>(map, p, dev, stream) : launch_dim<64>(map, p, dev, stream);
+  p.masks = a.masks;
+  if (a.masks != nullptr)
+    return dim == 128 ? launch_dim<128, true>(map, p, dev, stream)
+                      : launch_dim<64, true>(map, p, dev, stream);
+  return dim == 128 ? launch_dim<128, false>(map, p, dev, stream)
+                    : launch_dim<64, false>(map, p, dev, stream);
 }
 
 }  // namespace dsmla

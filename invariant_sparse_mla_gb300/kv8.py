@@ -197,6 +197,25 @@ def kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=N
         with torch.cuda.stream(stream):
             return kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out, lse,
                               workspace, err_flag)
+    return _decode(None, q, kv_pages, kv_scales, block_table, lens, scale, out, lse, workspace,
+                   err_flag)
+
+
+def kv8_tree_decode(q, masks, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=None,
+                    workspace=None, err_flag=None, stream=None):
+    """Attention of a tree of ``next_n`` drafts per request, its last positions:
+    as kv8_decode, but node j sees draft i where bit i of ``masks[r, j]`` (int64
+    [R, next_n]) is set, and all positions before the drafts."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_tree_decode(q, masks, kv_pages, kv_scales, block_table, lens, scale, out,
+                                   lse, workspace, err_flag)
+    return _decode(masks, q, kv_pages, kv_scales, block_table, lens, scale, out, lse, workspace,
+                   err_flag, tree=True)
+
+
+def _decode(masks, q, kv_pages, kv_scales, block_table, lens, scale, out, lse, workspace, err_flag,
+            tree=False):
     dev = _device(kv_pages, "kv_pages", torch.uint8)
     pages, hk, d = _cache(kv_pages, kv_scales, dev)
     qs = _tokens(q, "q", torch.bfloat16, dev, 2)
@@ -204,6 +223,10 @@ def kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=N
     r, nn, h, _ = q.shape
     if r != n:
         raise ValueError("q must have one row per block_table row")
+    if tree:
+        _arg(masks, "masks", torch.int64, dev, 2)
+        if masks.shape != (r, nn):
+            raise ValueError(f"masks must be [{r}, {nn}], got {tuple(masks.shape)}")
     out, lse = _outputs(q, d, dev, out, lse)
     L = lib()
     if workspace is None:
@@ -211,9 +234,13 @@ def kv8_decode(q, kv_pages, kv_scales, block_table, lens, scale, out=None, lse=N
         workspace = _scratch(need or 256, dev, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         _arg(workspace, "workspace", torch.uint8, dev)
-    _run(dev, L.ds_kv8_decode, q.data_ptr(), qs, kv_pages.data_ptr(), kv_scales.data_ptr(), pages,
-         block_table.data_ptr(), width, lens.data_ptr(), r, nn, h, hk, d, float(scale),
-         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), flag)
+    rest = (kv_pages.data_ptr(), kv_scales.data_ptr(), pages, block_table.data_ptr(), width,
+            lens.data_ptr(), r, nn, h, hk, d, float(scale), out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), flag)
+    if tree:
+        _run(dev, L.ds_kv8_tree_decode, q.data_ptr(), qs, masks.data_ptr(), *rest)
+    else:
+        _run(dev, L.ds_kv8_decode, q.data_ptr(), qs, *rest)
     return out, lse
 
 
