@@ -96,7 +96,8 @@ struct Params {
   const int32_t* starts;
   int64_t tokens;
   int heads, group;
-  int step_heads, step_tokens;     // 8 rows further: heads, and tokens
+  int step_heads, step_tokens;     // the rows of a pass of copies: heads, and tokens
+  int all_heads, all_tokens;       // the rows of a step
   float scale_log2;
   float* mass;
   int64_t mass_stride;
@@ -106,7 +107,7 @@ struct Params {
 // One request, and the CTA's place in it.
 struct Walk {
   int64_t at, end;       // cost before the present item; end of the CTA's share
-  int r;
+  int r, item_r;         // request; of the item before
   int raw, len, n;       // lens[r], clamped, new tokens
   int64_t t0;            // first token
   int tiles, cost;       // cost of an item
@@ -114,6 +115,7 @@ struct Walk {
   int kvh, tile;         // of the present item
   int row_lo;            // first row that sees the tile
   int steps;
+  bool same;             // one step, of the rows that the item before it had in its one step
 };
 
 __device__ __forceinline__ int64_t start_of(const Params& p, int64_t r) {
@@ -141,11 +143,15 @@ __device__ __forceinline__ void tile_of(const Walk& w, int i, int* kvh, int* til
 }
 
 __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
+  const int kvh = w.kvh, row_lo = w.row_lo, r = w.item_r;
+  const bool one = w.steps == 1;
   tile_of(w, w.i, &w.kvh, &w.tile);
   // Token i sees position p if p <= base + i.
   const int64_t first = (int64_t)w.tile * kTile - ((int64_t)w.raw - w.n);
   w.row_lo = first > 0 ? (int)first * p.group : 0;
   w.steps = (w.n * p.group - w.row_lo + kStep - 1) / kStep;
+  w.same = one && w.steps == 1 && r == w.r && kvh == w.kvh && row_lo == w.row_lo;
+  w.item_r = w.r;
 }
 
 // The next item from w.i on, in later requests where need be.
@@ -269,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // The first item that begins in the share.
     w.r = (int)start_s[0];
     load_request(p, w.r, w);
+    w.steps = 0;           // no item before the first
     w.i = (int)((lo - start_s[1] + w.cost - 1) / w.cost);
     w.at = start_s[1] + (int64_t)w.i * w.cost;
     some = walk_settle(p, w);
@@ -350,13 +357,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // ---------------------------------------------------------- MMA issuer
     const uint64_t q_desc = make_sw128_desc(sbase + LY::kQ, 16, 1024);
     const bool leader = elect_one();
-    uint32_t item = 0, g = 0;
+    // Steps (of S buffers) and loads of Q so far: an item of one step may use the
+    // load of the one before it, which is let go when the next comes.
+    uint32_t item = 0, g = 0, ql = 0;
+    bool held = false;
     while (some && !failed) {
       const int rows = w.n * p.group - w.row_lo;
       bool ok = mbar_wait_long(&bars[kAFull + (item & 1)], (item >> 1) & 1u);
+      if (held && !w.same) {
+        if (leader) mma_commit(&bars[kQEmpty + (ql - 1) % NQ]);
+        __syncwarp();
+        held = false;
+      }
       for (int s = 0; s < w.steps; ++s, ++g) {
-        const uint32_t st = g % NQ, buf = g & 1;
-        ok = ok && mbar_wait_long(&bars[kQFull + st], (g / NQ) & 1u) &&
+        const uint32_t buf = g & 1;
+        if (!w.same) ++ql;
+        const uint32_t st = (ql - 1) % NQ;
+        ok = ok && (w.same || mbar_wait_long(&bars[kQFull + st], ((ql - 1) / NQ) & 1u)) &&
              (g < 2 || mbar_wait_long(&bars[kSFree + buf], ((g >> 1) - 1) & 1u));
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
@@ -373,11 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           for (int k = 0; k < DIM / 16; ++k)
             mma_f16_ts(tmem + buf * kStep, tmem + LY::kA + (item & 1) * LY::kACols + 8 * k,
                        b + (((k >> 2) * (kStep * 128) + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
-          mma_commit(&bars[kQEmpty + st]);
+          if (w.steps > 1) mma_commit(&bars[kQEmpty + st]);
           mma_commit(&bars[kSFull + buf]);
         }
         __syncwarp();
       }
+      held = w.steps == 1;
       ++item;
       if (!failed) some = walk_next(p, w);
     }
@@ -392,33 +410,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const int t = tid - 32 * kQWarp, col = t % L;
     uint32_t g = 0;
     while (some && !failed) {
-      const int end = w.n * p.group;
-      const int base = w.raw - w.n;
+      if (w.same) {
+        some = walk_next(p, w);
+        continue;
+      }
+      const int rows = w.n * p.group - w.row_lo;      // of the item
+      const int seen = w.raw - w.n + 1;               // by token 0
       const __nv_bfloat16* q0 = p.q + w.t0 * p.q_stride + (int64_t)w.kvh * p.group * DIM + col * 8;
       const float* lse0 = p.lse + w.t0 * p.heads + w.kvh * p.group;
+      // (token, head) of this thread's next row to copy, and of its row of lse,
+      // which is read a step ahead.
+      int token = (w.row_lo + t / L) / p.group, h = (w.row_lo + t / L) % p.group;
+      int l_token = (w.row_lo + t) / p.group, l_h = (w.row_lo + t) % p.group;
+      float l_next = t < rows ? lse0[(int64_t)l_token * p.heads + l_h] : INFINITY;
       for (int s = 0; s < w.steps; ++s, ++g) {
         const uint32_t st = g % NQ;
-        const int row0 = w.row_lo + s * kStep;
-        const int rows = end - row0 < kStep ? end - row0 : kStep;
-        // This thread's row of lse and length seen.
-        float l = INFINITY;
-        int vis = 0;
-        if (t < rows) {
-          const int token = (row0 + t) / p.group, h = (row0 + t) % p.group;
-          l = lse0[(int64_t)token * p.heads + h];
-          l = l == -INFINITY ? INFINITY : l * kLog2e;   // (sees nothing: adds nothing)
-          vis = base + 1 + token;
-        }
+        const int left = rows - s * kStep;
         if (!__all_sync(0xffffffffu, g < NQ || mbar_wait_long(&bars[kQEmpty + st],
                                                               (g / NQ - 1) & 1u))) {
           failed = true;
           break;
         }
         const uint32_t dst = sbase + LY::kQ + st * LY::kQBytes;
-        int64_t token = (row0 + t / L) / p.group;
-        int h = (row0 + t / L) % p.group;
-        for (int r = t / L; r < ((rows + 15) & ~15); r += ROWS) {
-          const bool in = r < rows;
+        const int upto = left < kStep ? (left + 15) & ~15 : kStep;
+#pragma unroll 4
+        for (int r = t / L; r < upto; r += ROWS) {
+          const bool in = r < left;
           const __nv_bfloat16* src = in ? q0 + token * p.q_stride + h * DIM : p.q;
           cp_async_16(dst + (col >> 3) * (kStep * 128) + r * 128 + (((col & 7) ^ (r & 7)) << 4), src,
                       in ? 16u : 0u);
@@ -430,8 +447,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           }
         }
         cp_async_mbar_arrive_noinc(&bars[kQFull + st]);
+        // A row that sees nothing adds nothing, nor does one behind the last.
+        const float l = l_next;
+        const int vis = t < left ? seen + l_token : 0;
+        l_token += p.all_tokens;
+        l_h += p.all_heads;
+        if (l_h >= p.group) {
+          l_h -= p.group;
+          ++l_token;
+        }
+        l_next = t < left - kStep ? lse0[(int64_t)l_token * p.heads + l_h] : INFINITY;
         float* ls = reinterpret_cast<float*>(smem + LY::kLse + st * (kStep * 8));
-        ls[t] = l;
+        ls[t] = t >= left || l == -INFINITY ? -INFINITY : -l * kLog2e;
         reinterpret_cast<int*>(ls)[kStep + t] = vis;
         mbar_arrive(&bars[kLFull + st]);
       }
@@ -443,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const int quad = warp & 3, half = warp >> 2;
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    uint32_t item = 0, g = 0;
+    uint32_t item = 0, g = 0, ql = 0;
+    bool held = false;
     // K of the item-th item to bf16, this thread's half of the dims; returns
     // (scale, page there, a NaN among them).
     auto convert = [&](uint32_t it, float* ks, bool* there, bool* nan) {
@@ -489,6 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const int pos0 = w.tile * kTile, pos = pos0 + tok;
       const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
       const int steps = w.steps;
+      const bool same = w.same;
+      if (held && !same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
+      held = steps == 1;
       float* at = p.mass + ((int64_t)w.r * p.c.kv_heads + w.kvh) * p.mass_stride + pos;
       const bool in = pos < w.len;
       float old = 0.0f;
@@ -502,72 +533,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const float2 k2 = make_float2(ks, ks);
       float total = 0.0f;
       for (int s = 0; s < steps; ++s, ++g) {
-        const uint32_t st = g % NQ, buf = g & 1;
+        if (!same) ++ql;
+        const uint32_t st = (ql - 1) % NQ, buf = g & 1;
         const int left = rows_all - s * kStep;
         const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 8));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
-        const bool ok = mbar_wait_long(&bars[kLFull + st], (g / NQ) & 1u) &&
+        const bool ok = (same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
                         mbar_wait_long(&bars[kSFull + buf], (g >> 1) & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
         }
         tc_fence_after();
-        const uint32_t t_s = tmem + lane_base + buf * kStep;
+        const uint32_t t_s = tmem + lane_base + buf * kStep + half * 8;
+        const float* lh = ls + half * 8;
+        const int* vh = vs + half * 8;
+        // Columns of 8, warps w and w + 4 in turn. ls holds minus the lse.
         float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
+        const bool masked = edge && vs[0] < pos0 + kTile;
+        auto add8 = [&](const float* x, int c) {
+          const float4 l0 = *reinterpret_cast<const float4*>(lh + c);
+          const float4 l1 = *reinterpret_cast<const float4*>(lh + c + 4);
+          float2 a = fma2(make_float2(x[0], x[1]), k2, make_float2(l0.x, l0.y));
+          float2 b = fma2(make_float2(x[2], x[3]), k2, make_float2(l0.z, l0.w));
+          float2 d = fma2(make_float2(x[4], x[5]), k2, make_float2(l1.x, l1.y));
+          float2 e = fma2(make_float2(x[6], x[7]), k2, make_float2(l1.z, l1.w));
+          if (masked) {
+            const int4 v0 = *reinterpret_cast<const int4*>(vh + c);
+            const int4 v1 = *reinterpret_cast<const int4*>(vh + c + 4);
+            if (pos >= v0.x) a.x = -INFINITY;
+            if (pos >= v0.y) a.y = -INFINITY;
+            if (pos >= v0.z) b.x = -INFINITY;
+            if (pos >= v0.w) b.y = -INFINITY;
+            if (pos >= v1.x) d.x = -INFINITY;
+            if (pos >= v1.y) d.y = -INFINITY;
+            if (pos >= v1.z) e.x = -INFINITY;
+            if (pos >= v1.w) e.y = -INFINITY;
+          }
+          acc0 = add2(acc0, make_float2(ex2(a.x), ex2(a.y)));
+          acc1 = add2(acc1, make_float2(ex2(b.x), ex2(b.y)));
+          acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
+          acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
+        };
         if (left >= kStep) {
           float x[64];
-          tmem_ld64_sync(t_s + half * 64, x);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) tmem_ld<8>(t_s + 16 * c, x + 8 * c);
+          tmem_fence<64>(x);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
-          const int c0 = half * 64;
-          const bool masked = edge && vs[0] < pos0 + kTile;
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(ls + c0 + c);
-            float2 a = fma2(make_float2(x[c], x[c + 1]), k2, make_float2(-l.x, -l.y));
-            float2 b = fma2(make_float2(x[c + 2], x[c + 3]), k2, make_float2(-l.z, -l.w));
-            if (masked) {
-              const int4 v = *reinterpret_cast<const int4*>(vs + c0 + c);
-              if (pos >= v.x) a.x = -INFINITY;
-              if (pos >= v.y) a.y = -INFINITY;
-              if (pos >= v.z) b.x = -INFINITY;
-              if (pos >= v.w) b.y = -INFINITY;
-            }
-            acc0 = add2(acc0, make_float2(ex2(a.x), ex2(a.y)));
-            acc1 = add2(acc1, make_float2(ex2(b.x), ex2(b.y)));
-          }
+          for (int c = 0; c < 8; ++c) add8(x + 8 * c, 16 * c);
         } else {
-          // The last step: columns of 8, half of them each.
-          const int n = (left + 7) & ~7, mid = ((n >> 3) + 1) / 2 * 8;
-          for (int c = half ? mid : 0; c < (half ? n : mid); c += 8) {
+          for (int c = 0; c + half * 8 < left; c += 16) {
             float x[8];
             tmem_ld<8>(t_s + c, x);
             tmem_fence<8>(x);
-            const float4 l0 = *reinterpret_cast<const float4*>(ls + c);
-            const float4 l1 = *reinterpret_cast<const float4*>(ls + c + 4);
-            const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              float2 a = fma2(make_float2(x[e], x[e + 1]), k2, make_float2(-l[e], -l[e + 1]));
-              if (edge) {
-                if (pos >= vs[c + e]) a.x = -INFINITY;
-                if (pos >= vs[c + e + 1]) a.y = -INFINITY;
-              }
-              const float2 z = make_float2(ex2(a.x), ex2(a.y));
-              if (e & 2)
-                acc1 = add2(acc1, z);
-              else
-                acc0 = add2(acc0, z);
-            }
+            add8(x, c);
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kQEmpty + st]);
+        if (steps > 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kQEmpty + st]);
+        }
         total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
       }
       if (failed) break;
@@ -649,6 +681,8 @@ cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream) {
   const int rows = 32 * kQWarps / (dim / 8);
   p.step_tokens = rows / p.group;
   p.step_heads = rows % p.group;
+  p.all_tokens = kStep / p.group;
+  p.all_heads = kStep % p.group;
   p.scale_log2 = a.scale * kLog2e;
   p.mass = a.mass;
   p.mass_stride = a.mass_stride;
