@@ -10,30 +10,39 @@
 // rows), nothing is reduced across threads, and the order of the additions
 // follows from the request alone.
 //
-// Both operands are bf16: an E4M3 code has 4 significant bits and an exponent
-// that bf16 holds, so K and q enter the product exactly, whatever their
-// magnitudes; sums are fp32. A code becomes bf16 by placing its exponent and
-// mantissa bits under bf16's (subnormals included) and multiplying by 2^120.
+// An item is (request, kv head, 128 positions), its codes brought by TMA. Two
+// forms, by the request's number of rows R = tokens * heads of the group:
 //
-// K stays, Q streams: an item is (request, kv head, 128 positions). Its codes
-// arrive by TMA, are converted once and written to TMEM as the A operand (64
-// columns of bf16 pairs for dim 128, two buffers); the query rows that see the
-// tile come in steps of 128 through a ring in shared memory, and S has two
-// buffers of 128 columns, so that the product of one step runs under the
-// exponentials of the last. With one token a request an item is one step, and the
-// bound is HBM, dim bytes a position and head; with prompts it is the tensor
-// core (2 dim flops a position and row) and the exponentials next to it.
+// - Few rows (R <= 40): K is multiplied as it lies, on the 8-bit tensor cores,
+//   with q as three E4M3 pieces, each a column of its own under the row's power of
+//   two: q = 2^-k (q0 + q1 / 32 + q2 / 1024). A bf16 number has 8 significant
+//   bits, so this is exact down to 2^-19 of the row's largest |q| and off by up to
+//   2^-27 of that below. The pieces are made once per (request, kv head) and
+//   serve all its tiles; an item is then a product of 3 R columns and 128 R
+//   exponentials. The bound is HBM, dim bytes a position and head.
 //
-// Work split: a persistent grid, each CTA a run of items of equal cost (steps,
-// and a constant for the conversion). A request's tiles are taken from both ends
-// in turn, since the last ones are seen by fewer rows.
+// - More: K becomes bf16 once per item (an E4M3 code has 4 significant bits and an
+//   exponent that bf16 holds: exponent and mantissa bits are placed under bf16's,
+//   subnormals included, and multiplied by 2^120) and lies in TMEM as the A
+//   operand, two buffers; the query rows stream past it in steps of up to 128, by
+//   TMA as they lie, and both operands are exact. S has two buffers of 128
+//   columns, so the product of one step runs under the exponentials of the last.
+//   The bound is the tensor core (2 dim flops a position and row) and the
+//   exponentials beside it.
+//
+// Sums are fp32: of a step first, then over the steps.
+//
+// Work split: a persistent grid, each CTA a run of items of equal cost. A
+// request's tiles are taken from both ends in turn, since the last ones are seen
+// by fewer rows.
 //
 // Per CTA: warps 0-7 convert and sum (warps w and w + 4 take half of the dims and
-// half of the columns each), warp 8 brings K, warp 9 issues the products, warps
-// 10-13 bring Q and lse.
+// half of the columns each), warp 8 brings K, warp 9 issues the products, warp 10
+// brings Q, warps 11-14 lse and the pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "kv8_common.cuh"
@@ -45,22 +54,22 @@ namespace {
 constexpr int kTile = 128;                 // positions of an item
 constexpr int kStep = 128;                 // query rows of a step
 constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 4;
-constexpr int kThreads = 32 * (kQWarp + kQWarps);
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11, kLWarps = 4;
+constexpr int kThreads = 32 * (kLWarp + kLWarps);
 constexpr int kMetaSlots = 8;
-constexpr int kItemCost = 3;               // of the conversion, in steps
+constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 
 template <int DIM>
 struct Layout {
   static constexpr int kKBytes = kTile * DIM;
   static constexpr int kQBytes = kStep * DIM * 2;
-  static constexpr int kNK = DIM == 128 ? 4 : 6;    // stages (at most kMetaSlots - 2)
+  static constexpr int kNK = 6;                     // stages (at most kMetaSlots - 2)
   static constexpr int kNQ = DIM == 128 ? 3 : 4;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kNK * kKBytes;
-  static constexpr int kLse = kQ + kNQ * kQBytes;             // per stage: 128 lse, 128 visible
-  static constexpr int kBars = kLse + kNQ * kStep * 8;
+  static constexpr int kLse = kQ + kNQ * kQBytes;   // per stage: 128 lse, visible, factors
+  static constexpr int kBars = kLse + kNQ * kStep * 12;
   static constexpr int kMeta = kBars + 64 * 8;                // kMetaSlots x float4
   static constexpr int kOther = kMeta + kMetaSlots * 16;      // sums of warps 4-7, two slots
   static constexpr int kMisc = kOther + 2 * kTile * 4;        // tmem slot, start of work, scan
@@ -96,8 +105,9 @@ struct Params {
   const int32_t* starts;
   int64_t tokens;
   int heads, group;
-  int step_heads, step_tokens;     // the rows of a pass of copies: heads, and tokens
-  int all_heads, all_tokens;       // the rows of a step
+  // A step: `tokens` tokens of `heads` heads each; of `chunks` steps of a token
+  // where its heads do not fit one.
+  int step_tokens, step_heads, chunks;
   float scale_log2;
   float* mass;
   int64_t mass_stride;
@@ -111,9 +121,10 @@ struct Walk {
   int raw, len, n;       // lens[r], clamped, new tokens
   int64_t t0;            // first token
   int tiles, cost;       // cost of an item
+  bool few;              // multiplied in pieces
   int i, items;          // present item, items of the request
   int kvh, tile;         // of the present item
-  int row_lo;            // first row that sees the tile
+  int first;             // first token that sees the tile (few: 0)
   int steps;
   bool same;             // one step, of the rows that the item before it had in its one step
 };
@@ -133,7 +144,10 @@ __device__ __forceinline__ void load_request(const Params& p, int64_t r, Walk& w
   w.n = n < 0 || w.len == 0 ? 0 : (int)n;
   w.tiles = w.n > 0 ? (w.len + kTile - 1) / kTile : 0;
   w.items = w.tiles * p.c.kv_heads;
-  w.cost = kItemCost + (w.n * p.group + kStep - 1) / kStep;   // (rows are below 2^31 - 256)
+  const int rows = w.n * p.group;   // (below 2^31 - 256)
+  // (The pieces stay clear of the rows of a stage that no step writes.)
+  w.few = rows <= kFewRows && 3 * ((rows + 7) & ~7) <= p.step_tokens * p.step_heads;
+  w.cost = w.few ? 1 : 1 + (w.n + p.step_tokens - 1) / p.step_tokens * p.chunks;
 }
 
 __device__ __forceinline__ void tile_of(const Walk& w, int i, int* kvh, int* tile) {
@@ -143,15 +157,35 @@ __device__ __forceinline__ void tile_of(const Walk& w, int i, int* kvh, int* til
 }
 
 __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
-  const int kvh = w.kvh, row_lo = w.row_lo, r = w.item_r;
+  const int kvh = w.kvh, before = w.first, r = w.item_r;
   const bool one = w.steps == 1;
   tile_of(w, w.i, &w.kvh, &w.tile);
   // Token i sees position p if p <= base + i.
   const int64_t first = (int64_t)w.tile * kTile - ((int64_t)w.raw - w.n);
-  w.row_lo = first > 0 ? (int)first * p.group : 0;
-  w.steps = (w.n * p.group - w.row_lo + kStep - 1) / kStep;
-  w.same = one && w.steps == 1 && r == w.r && kvh == w.kvh && row_lo == w.row_lo;
+  w.first = first > 0 && !w.few ? (int)first : 0;
+  w.steps = w.few ? 1 : (w.n - w.first + p.step_tokens - 1) / p.step_tokens * p.chunks;
+  w.same = one && w.steps == 1 && r == w.r && kvh == w.kvh && before == w.first;
   w.item_r = w.r;
+}
+
+// Step s of an item: its first token, its chunk of heads and its rows.
+struct Step {
+  int token, head, rows;
+};
+__device__ __forceinline__ Step step_of(const Params& p, const Walk& w, int s) {
+  Step x;
+  if (p.chunks == 1) {
+    x.token = w.first + s * p.step_tokens;
+    x.head = 0;
+    const int left = w.n - x.token;
+    x.rows = (left < p.step_tokens ? left : p.step_tokens) * p.step_heads;
+  } else {
+    x.token = w.first + s / p.chunks;
+    x.head = s % p.chunks * kStep;
+    const int left = p.group - x.head;
+    x.rows = left < kStep ? left : kStep;
+  }
+  return x;
 }
 
 // The next item from w.i on, in later requests where need be.
@@ -189,9 +223,38 @@ __device__ __forceinline__ uint32_t nan_bits(uint32_t w) {
   return (w & 0x7F7F7F7Fu) + 0x01010101u;
 }
 
+// The power of two that brings a row's largest |q|, a, to [128, 256); it stays a
+// normal float.
+__device__ __forceinline__ int q_exponent(float a) {
+  const int k = a > 0.0f ? 7 - ((int)(__float_as_uint(a) >> 23) - 127) : 0;
+  return k > 120 ? 120 : (k < -120 ? -120 : k);
+}
+__device__ __forceinline__ float pow2f(int k) {
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+// Two values as E4M3, and 32 times what that leaves of them.
+__device__ __forceinline__ uint16_t piece(float& u0, float& u1) {
+  const __nv_fp8x2_storage_t b =
+      __nv_cvt_float2_to_fp8x2(make_float2(u0, u1), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  u0 = (u0 - f.x) * 32.0f;
+  u1 = (u1 - f.y) * 32.0f;
+  return b;
+}
+
+template <int DIM>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+  if constexpr (DIM == 128)
+    return make_sw128_desc(addr, 16, 1024);
+  else
+    return make_sw64_desc(addr, 16, 512);
+}
+
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
-    const __grid_constant__ CUtensorMap map, const Params p) {
+    const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map,
+    const Params p) {
   using LY = Layout<DIM>;
   constexpr int NK = LY::kNK, NQ = LY::kNQ;
   extern __shared__ uint8_t smem_raw[];
@@ -208,8 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((i >= kKEmpty && i < kKEmpty + NK) || (i >= kAFull && i < kAFull + 2)) n = kSum;
-      if (i >= kQFull && i < kLFull + NQ) n = 32 * kQWarps;
+      if (i >= kKEmpty && i < kKEmpty + NK) n = kSumWarps;
+      if (i >= kAFull && i < kAFull + 2) n = kSum;
+      if (i >= kLFull && i < kLFull + NQ) n = 32 * kLWarps;
       if (i >= kQEmpty && i < kQEmpty + NQ) n = 1 + kSumWarps;
       if (i >= kSFree && i < kSFree + 2) n = kSumWarps;
       if (i >= kXFull && i < kXFree + 2) n = kSum / 2;
@@ -222,6 +286,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     tmem_alloc(tmem_slot, LY::kCols);
     tmem_relinquish();
   }
+  // Rows that no step writes stay 0, so that their scores are.
+  const int capacity = p.step_tokens * p.step_heads;
+  for (int i = tid; i < NQ * (DIM / 64) * (kStep - capacity) * 8; i += kThreads) {
+    const int block = i / ((kStep - capacity) * 8), at = i % ((kStep - capacity) * 8);
+    *reinterpret_cast<uint4*>(smem + LY::kQ + (block * kStep + capacity) * 128 + at * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   pdl_wait();
   pdl_trigger();
 
@@ -356,42 +428,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
     const uint64_t q_desc = make_sw128_desc(sbase + LY::kQ, 16, 1024);
+    const uint64_t q8_desc = tile_desc<DIM>(sbase + LY::kQ);
+    const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
     const bool leader = elect_one();
-    // Steps (of S buffers) and loads of Q so far: an item of one step may use the
-    // load of the one before it, which is let go when the next comes.
-    uint32_t item = 0, g = 0, ql = 0;
+    // Items, converted ones, steps (of S buffers) and loads of Q so far: an item of
+    // one step may use the load of the one before it, which is let go when the
+    // next comes.
+    uint32_t item = 0, conv = 0, g = 0, ql = 0;
     bool held = false;
     while (some && !failed) {
-      const int rows = w.n * p.group - w.row_lo;
-      bool ok = mbar_wait_long(&bars[kAFull + (item & 1)], (item >> 1) & 1u);
+      bool ok;
+      if (w.few) {
+        ok = mbar_wait_long(&bars[kKFull + item % NK], (item / NK) & 1u);
+      } else {
+        ok = mbar_wait_long(&bars[kAFull + (conv & 1)], (conv >> 1) & 1u);
+        ++conv;
+      }
       if (held && !w.same) {
         if (leader) mma_commit(&bars[kQEmpty + (ql - 1) % NQ]);
         __syncwarp();
-        held = false;
       }
       for (int s = 0; s < w.steps; ++s, ++g) {
         const uint32_t buf = g & 1;
         if (!w.same) ++ql;
-        const uint32_t st = (ql - 1) % NQ;
-        ok = ok && (w.same || mbar_wait_long(&bars[kQFull + st], ((ql - 1) / NQ) & 1u)) &&
+        const uint32_t st = (ql - 1) % NQ, ph = ((ql - 1) / NQ) & 1u;
+        ok = ok && (w.same || (mbar_wait_long(&bars[kQFull + st], ph) &&
+                               (!w.few || mbar_wait_long(&bars[kLFull + st], ph)))) &&
              (g < 2 || mbar_wait_long(&bars[kSFree + buf], ((g >> 1) - 1) & 1u));
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
         }
-        fence_proxy_async_smem();   // Q landed through cp.async
         tc_fence_after();
-        const int left = rows - s * kStep;
-        const int n = left >= kStep ? kStep : (left + 15) & ~15;
-        if (leader) {
-          const uint32_t idesc = make_idesc_bf16(kTile, n, 0, 0);
-          const uint64_t b = q_desc + (uint64_t)((st * LY::kQBytes) >> 4);
+        if (w.few) {
+          if (leader) {
+            const int n = (3 * ((w.n * p.group + 7) & ~7) + 15) & ~15;
+            const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
+            const uint64_t a = k_desc + (uint64_t)((item % NK * LY::kKBytes) >> 4);
+            const uint64_t b = q8_desc + (uint64_t)((st * LY::kQBytes) >> 4);
 #pragma unroll
-          for (int k = 0; k < DIM / 16; ++k)
-            mma_f16_ts(tmem + buf * kStep, tmem + LY::kA + (item & 1) * LY::kACols + 8 * k,
-                       b + (((k >> 2) * (kStep * 128) + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
-          if (w.steps > 1) mma_commit(&bars[kQEmpty + st]);
-          mma_commit(&bars[kSFull + buf]);
+            for (int k = 0; k < DIM / 32; ++k)
+              mma_f8_ss(tmem + buf * kStep, a + ((k * 32) >> 4), b + ((k * 32) >> 4), idesc,
+                        k > 0 ? 1u : 0u);
+            mma_commit(&bars[kSFull + buf]);
+          }
+        } else {
+          const int n = (step_of(p, w, s).rows + 15) & ~15;
+          if (leader) {
+            const uint32_t idesc = make_idesc_bf16(kTile, n, 0, 0);
+            const uint64_t b = q_desc + (uint64_t)((st * LY::kQBytes) >> 4);
+            const uint32_t a = tmem + LY::kA + ((conv - 1) & 1) * LY::kACols;
+#pragma unroll
+            for (int k = 0; k < DIM / 16; ++k)
+              mma_f16_ts(tmem + buf * kStep, a + 8 * k,
+                         b + (((k >> 2) * (kStep * 128) + (k & 3) * 32) >> 4), idesc,
+                         k > 0 ? 1u : 0u);
+            if (w.steps > 1) mma_commit(&bars[kQEmpty + st]);
+            mma_commit(&bars[kSFull + buf]);
+          }
         }
         __syncwarp();
       }
@@ -403,86 +497,155 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     __syncwarp();
     if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
     __syncwarp();
-  } else if (warp >= kQWarp) {
-    // -------------------------------------------------------- Q and lse
-    constexpr int L = DIM / 8;                 // lanes of a row (16 bytes each)
-    constexpr int ROWS = 32 * kQWarps / L;     // rows of a pass
-    const int t = tid - 32 * kQWarp, col = t % L;
-    uint32_t g = 0;
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------------------ Q
+    uint32_t ql = 0, issued = 0;
+    const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
+    while (some && !failed) {
+      if (!w.same) {
+        for (int s = 0; s < w.steps; ++s, ++ql) {
+          const uint32_t st = ql % NQ;
+          if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
+                                                                 (ql / NQ - 1) & 1u))) {
+            failed = true;
+            break;
+          }
+          if (lane == 0) {
+            if (w.few) {
+              mbar_arrive(&bars[kQFull + st]);   // (the pieces come from the next warps)
+            } else {
+              const Step x = step_of(p, w, s);
+              mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
+#pragma unroll
+              for (int b = 0; b < DIM / 64; ++b)
+                tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
+                              w.kvh * p.group + x.head, (int)w.t0 + x.token, &bars[kQFull + st]);
+            }
+            issued = ql + 1;
+          }
+          __syncwarp();
+        }
+      }
+      if (!failed) some = walk_next(p, w);
+    }
+    if (lane == 0)   // every copy has landed before the CTA can exit
+      for (uint32_t i = issued > NQ ? issued - NQ : 0; i < issued; ++i)
+        if (!mbar_wait_long(&bars[kQFull + i % NQ], (i / NQ) & 1u)) failed = true;
+    __syncwarp();
+  } else if (warp >= kLWarp) {
+    // --------------------------------------------- lse, and pieces of few rows
+    const int t = tid - 32 * kLWarp;
+    const int t_token = t / p.step_heads, t_head = t % p.step_heads;   // of a step's row t
+    uint32_t ql = 0;
     while (some && !failed) {
       if (w.same) {
         some = walk_next(p, w);
         continue;
       }
-      const int rows = w.n * p.group - w.row_lo;      // of the item
       const int seen = w.raw - w.n + 1;               // by token 0
-      const __nv_bfloat16* q0 = p.q + w.t0 * p.q_stride + (int64_t)w.kvh * p.group * DIM + col * 8;
       const float* lse0 = p.lse + w.t0 * p.heads + w.kvh * p.group;
-      // (token, head) of this thread's next row to copy, and of its row of lse,
-      // which is read a step ahead.
-      int token = (w.row_lo + t / L) / p.group, h = (w.row_lo + t / L) % p.group;
-      int l_token = (w.row_lo + t) / p.group, l_h = (w.row_lo + t) % p.group;
-      float l_next = t < rows ? lse0[(int64_t)l_token * p.heads + l_h] : INFINITY;
-      for (int s = 0; s < w.steps; ++s, ++g) {
-        const uint32_t st = g % NQ;
-        const int left = rows - s * kStep;
-        if (!__all_sync(0xffffffffu, g < NQ || mbar_wait_long(&bars[kQEmpty + st],
-                                                              (g / NQ - 1) & 1u))) {
+      // Row t's lse and length seen, read a step ahead.
+      auto look = [&](int s, float* l, int* vis) {
+        *l = -INFINITY;
+        *vis = INT_MIN;
+        if (s >= w.steps) return;
+        int token, head;
+        bool in;
+        if (w.few) {
+          token = t / p.group;
+          head = t % p.group;
+          in = t < w.n * p.group;
+        } else {
+          const Step x = step_of(p, w, s);
+          token = x.token + t_token;
+          head = x.head + t_head;
+          in = t < x.rows;
+        }
+        if (!in) return;
+        *l = lse0[(int64_t)token * p.heads + head];
+        *vis = seen + token;
+      };
+      float l;
+      int vis;
+      look(0, &l, &vis);
+      for (int s = 0; s < w.steps; ++s, ++ql) {
+        const uint32_t st = ql % NQ;
+        if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
+                                                               (ql / NQ - 1) & 1u))) {
           failed = true;
           break;
         }
-        const uint32_t dst = sbase + LY::kQ + st * LY::kQBytes;
-        const int upto = left < kStep ? (left + 15) & ~15 : kStep;
-#pragma unroll 4
-        for (int r = t / L; r < upto; r += ROWS) {
-          const bool in = r < left;
-          const __nv_bfloat16* src = in ? q0 + token * p.q_stride + h * DIM : p.q;
-          cp_async_16(dst + (col >> 3) * (kStep * 128) + r * 128 + (((col & 7) ^ (r & 7)) << 4), src,
-                      in ? 16u : 0u);
-          token += p.step_tokens;
-          h += p.step_heads;
-          if (h >= p.group) {
-            h -= p.group;
-            ++token;
-          }
-        }
-        cp_async_mbar_arrive_noinc(&bars[kQFull + st]);
-        // A row that sees nothing adds nothing, nor does one behind the last.
-        const float l = l_next;
-        const int vis = t < left ? seen + l_token : 0;
-        l_token += p.all_tokens;
-        l_h += p.all_heads;
-        if (l_h >= p.group) {
-          l_h -= p.group;
-          ++l_token;
-        }
-        l_next = t < left - kStep ? lse0[(int64_t)l_token * p.heads + l_h] : INFINITY;
-        float* ls = reinterpret_cast<float*>(smem + LY::kLse + st * (kStep * 8));
-        ls[t] = t >= left || l == -INFINITY ? -INFINITY : -l * kLog2e;
+        float* ls = reinterpret_cast<float*>(smem + LY::kLse + st * (kStep * 12));
+        ls[t] = l == -INFINITY ? -INFINITY : -l * kLog2e;   // (a row of -inf adds nothing)
         reinterpret_cast<int*>(ls)[kStep + t] = vis;
+        if (w.few) {
+          // A warp a row, in turn. (What lies behind the rows is anything: columns
+          // of the product that nobody reads.)
+          constexpr int E = DIM / 32;
+          const int rows = w.n * p.group, r8 = (rows + 7) & ~7;
+          uint8_t* q8 = smem + LY::kQ + st * LY::kQBytes;
+          for (int r = warp - kLWarp; r < rows; r += kLWarps) {
+            const __nv_bfloat16* src = p.q + (w.t0 + r / p.group) * p.q_stride +
+                                       ((int64_t)w.kvh * p.group + r % p.group) * DIM + lane * E;
+            float x[E], a = 0.0f;
+            bool nan = false;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const uint32_t v = reinterpret_cast<const uint32_t*>(src)[e / 2];
+              x[e] = __uint_as_float(v << 16);
+              x[e + 1] = __uint_as_float(v & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              a = fmaxf(a, fabsf(x[e]));
+              nan |= x[e] != x[e];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            nan = __any_sync(0xffffffffu, nan) || a == INFINITY;
+            const int k = q_exponent(a);
+            const float up = pow2f(k);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              float u0 = x[e] * up, u1 = x[e + 1] * up;
+#pragma unroll
+              for (int z = 0; z < 3; ++z)
+                *reinterpret_cast<uint16_t*>(q8 + swz<DIM>(z * r8 + r, lane * E + e)) =
+                    piece(u0, u1);
+            }
+            if (lane == 0) ls[2 * kStep + r] = nan ? NAN : pow2f(-k);
+          }
+          fence_proxy_async_smem();
+        }
         mbar_arrive(&bars[kLFull + st]);
+        look(s + 1, &l, &vis);
       }
       if (!failed) some = walk_next(p, w);
     }
-    cp_async_wait_all();
   } else {
     // --------------------------------------------------- convert and sum
     const int quad = warp & 3, half = warp >> 2;
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    uint32_t item = 0, g = 0, ql = 0;
+    // Items, converted ones, steps and loads of Q so far (as the issuer counts).
+    uint32_t item = 0, conv = 0, g = 0, ql = 0;
     bool held = false;
-    // K of the item-th item to bf16, this thread's half of the dims; returns
-    // (scale, page there, a NaN among them).
-    auto convert = [&](uint32_t it, float* ks, bool* there, bool* nan) {
+    struct Keys {
+      float scale;
+      bool there, nan;     // the page is; a NaN among this thread's codes
+    };
+    auto read_meta = [&](uint32_t it) {
+      const float4 m = meta[it & (kMetaSlots - 1)];
+      return Keys{tok < kPage ? m.x : m.z, (tok < kPage ? m.y : m.w) != 0.0f, false};
+    };
+    // K of item `it` to bf16, this thread's half of the dims.
+    auto convert = [&](uint32_t it, Keys* keys) {
       const int st = (int)(it % NK);
       if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kKFull + st], (it / NK) & 1u))) return false;
-      const float4 m = meta[it & (kMetaSlots - 1)];
-      *ks = tok < kPage ? m.x : m.z;
-      *there = (tok < kPage ? m.y : m.w) != 0.0f;
+      *keys = read_meta(it);
       const uint8_t* src = smem + LY::kK + st * LY::kKBytes;
       uint32_t bad = 0;
-      const uint32_t t_a = tmem + lane_base + LY::kA + (it & 1) * LY::kACols + half * (DIM / 4);
+      const uint32_t t_a = tmem + lane_base + LY::kA + (conv & 1) * LY::kACols + half * (DIM / 4);
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < DIM / 64; ++c) {
@@ -501,42 +664,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         }
         tmem_st16u(t_a + 16 * c, v);
       }
-      *nan = (bad & 0x80808080u) != 0u;
+      keys->nan = (bad & 0x80808080u) != 0u;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars[kKEmpty + st]);
-      mbar_arrive(&bars[kAFull + (it & 1)]);
+      mbar_arrive(&bars[kAFull + (conv & 1)]);
+      ++conv;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kKEmpty + st]);
       return true;
     };
-    float ks = 0.0f, ks_next = 0.0f;
-    bool there = false, there_next = false, nan = false, nan_next = false;
-    if (some && !convert(0, &ks, &there, &nan)) failed = true;
+    Keys keys{0.0f, false, false}, next{0.0f, false, false};
+    if (some && !w.few && !convert(0, &next)) failed = true;
     while (some && !failed) {
-      const int rows_all = w.n * p.group - w.row_lo;
-      const int base = w.raw - w.n;
+      keys = next;
+      const bool few = w.few, same = w.same;
+      const int steps = w.steps, base = w.raw - w.n;
       const int pos0 = w.tile * kTile, pos = pos0 + tok;
       const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
-      const int steps = w.steps;
-      const bool same = w.same;
-      if (held && !same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
-      held = steps == 1;
+      const Walk now = w;
       float* at = p.mass + ((int64_t)w.r * p.c.kv_heads + w.kvh) * p.mass_stride + pos;
       const bool in = pos < w.len;
       float old = 0.0f;
       if (half == 0 && in && pos < base) old = *at;
+      if (held && !same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
+      held = steps == 1;
       // The next item's K, while the products of this one run.
       some = walk_next(p, w);
-      if (some && !convert(item + 1, &ks_next, &there_next, &nan_next)) {
+      if (some && !w.few && !convert(item + 1, &next)) {
         failed = true;
         break;
       }
-      const float2 k2 = make_float2(ks, ks);
       float total = 0.0f;
       for (int s = 0; s < steps; ++s, ++g) {
         if (!same) ++ql;
         const uint32_t st = (ql - 1) % NQ, buf = g & 1;
-        const int left = rows_all - s * kStep;
-        const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 8));
+        const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 12));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
         const bool ok = (same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
                         mbar_wait_long(&bars[kSFull + buf], (g >> 1) & 1u);
@@ -545,56 +707,99 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           break;
         }
         tc_fence_after();
-        const uint32_t t_s = tmem + lane_base + buf * kStep + half * 8;
-        const float* lh = ls + half * 8;
-        const int* vh = vs + half * 8;
-        // Columns of 8, warps w and w + 4 in turn. ls holds minus the lse.
         float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-        const bool masked = edge && vs[0] < pos0 + kTile;
-        auto add8 = [&](const float* x, int c) {
-          const float4 l0 = *reinterpret_cast<const float4*>(lh + c);
-          const float4 l1 = *reinterpret_cast<const float4*>(lh + c + 4);
-          float2 a = fma2(make_float2(x[0], x[1]), k2, make_float2(l0.x, l0.y));
-          float2 b = fma2(make_float2(x[2], x[3]), k2, make_float2(l0.z, l0.w));
-          float2 d = fma2(make_float2(x[4], x[5]), k2, make_float2(l1.x, l1.y));
-          float2 e = fma2(make_float2(x[6], x[7]), k2, make_float2(l1.z, l1.w));
-          if (masked) {
-            const int4 v0 = *reinterpret_cast<const int4*>(vh + c);
-            const int4 v1 = *reinterpret_cast<const int4*>(vh + c + 4);
-            if (pos >= v0.x) a.x = -INFINITY;
-            if (pos >= v0.y) a.y = -INFINITY;
-            if (pos >= v0.z) b.x = -INFINITY;
-            if (pos >= v0.w) b.y = -INFINITY;
-            if (pos >= v1.x) d.x = -INFINITY;
-            if (pos >= v1.y) d.y = -INFINITY;
-            if (pos >= v1.z) e.x = -INFINITY;
-            if (pos >= v1.w) e.y = -INFINITY;
+        if (few) {
+          // The product is done, so K is read: its stage is free.
+          keys = read_meta(item);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kKEmpty + item % NK]);
+          const int rows = now.n * p.group, r8 = (rows + 7) & ~7;
+          const uint32_t t_s = tmem + lane_base + buf * kStep;
+          const float2 ks = make_float2(keys.scale, keys.scale);
+          for (int c = half * 4; c < rows; c += 8) {
+            float x[4], y[4], z[4];
+            tmem_ld<4>(t_s + c, x);
+            tmem_ld<4>(t_s + r8 + c, y);
+            tmem_ld<4>(t_s + 2 * r8 + c, z);
+            const float4 l = *reinterpret_cast<const float4*>(ls + c);
+            const float4 f = *reinterpret_cast<const float4*>(ls + 2 * kStep + c);
+            tmem_fence<4>(x);
+            tmem_fence<4>(y);
+            tmem_fence<4>(z);
+            const float2 w5 = make_float2(0x1p-5f, 0x1p-5f);
+            float2 a = fma2(make_float2(z[0], z[1]), w5, make_float2(y[0], y[1]));
+            float2 b = fma2(make_float2(z[2], z[3]), w5, make_float2(y[2], y[3]));
+            a = fma2(a, w5, make_float2(x[0], x[1]));
+            b = fma2(b, w5, make_float2(x[2], x[3]));
+            a = fma2(a, mul2(make_float2(f.x, f.y), ks), make_float2(l.x, l.y));
+            b = fma2(b, mul2(make_float2(f.z, f.w), ks), make_float2(l.z, l.w));
+            if (edge || c + 4 > rows) {
+              // (Columns behind the rows hold anything.)
+              const int4 v = *reinterpret_cast<const int4*>(vs + c);
+              if (pos >= v.x) a.x = -INFINITY;
+              if (pos >= v.y) a.y = -INFINITY;
+              if (pos >= v.z) b.x = -INFINITY;
+              if (pos >= v.w) b.y = -INFINITY;
+            }
+            acc0 = add2(acc0, make_float2(ex2(a.x), ex2(a.y)));
+            acc1 = add2(acc1, make_float2(ex2(b.x), ex2(b.y)));
           }
-          acc0 = add2(acc0, make_float2(ex2(a.x), ex2(a.y)));
-          acc1 = add2(acc1, make_float2(ex2(b.x), ex2(b.y)));
-          acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
-          acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
-        };
-        if (left >= kStep) {
-          float x[64];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) tmem_ld<8>(t_s + 16 * c, x + 8 * c);
-          tmem_fence<64>(x);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) add8(x + 8 * c, 16 * c);
         } else {
-          for (int c = 0; c + half * 8 < left; c += 16) {
-            float x[8];
-            tmem_ld<8>(t_s + c, x);
-            tmem_fence<8>(x);
-            add8(x, c);
+          // Columns of 8, warps w and w + 4 in turn. ls holds minus the lse.
+          const uint32_t t_s = tmem + lane_base + buf * kStep + half * 8;
+          const float* lh = ls + half * 8;
+          const int* vh = vs + half * 8;
+          const float2 ks = make_float2(keys.scale, keys.scale);
+          auto add8 = [&](const float* x, int c, bool masked) {
+            const float4 l0 = *reinterpret_cast<const float4*>(lh + c);
+            const float4 l1 = *reinterpret_cast<const float4*>(lh + c + 4);
+            float2 a = fma2(make_float2(x[0], x[1]), ks, make_float2(l0.x, l0.y));
+            float2 b = fma2(make_float2(x[2], x[3]), ks, make_float2(l0.z, l0.w));
+            float2 d = fma2(make_float2(x[4], x[5]), ks, make_float2(l1.x, l1.y));
+            float2 e = fma2(make_float2(x[6], x[7]), ks, make_float2(l1.z, l1.w));
+            if (masked) {
+              const int4 v0 = *reinterpret_cast<const int4*>(vh + c);
+              const int4 v1 = *reinterpret_cast<const int4*>(vh + c + 4);
+              if (pos >= v0.x) a.x = -INFINITY;
+              if (pos >= v0.y) a.y = -INFINITY;
+              if (pos >= v0.z) b.x = -INFINITY;
+              if (pos >= v0.w) b.y = -INFINITY;
+              if (pos >= v1.x) d.x = -INFINITY;
+              if (pos >= v1.y) d.y = -INFINITY;
+              if (pos >= v1.z) e.x = -INFINITY;
+              if (pos >= v1.w) e.y = -INFINITY;
+            }
+            acc0 = add2(acc0, make_float2(ex2(a.x), ex2(a.y)));
+            acc1 = add2(acc1, make_float2(ex2(b.x), ex2(b.y)));
+            acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
+            acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
+          };
+          const int rows = step_of(p, now, s).rows;
+          const bool masked = edge && vs[0] < pos0 + kTile;
+          if (rows == capacity && capacity > kStep - 16 && !masked) {
+            float x[64];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) tmem_ld<8>(t_s + 16 * c, x + 8 * c);
+            tmem_fence<64>(x);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) add8(x + 8 * c, 16 * c, false);
+          } else {
+            for (int c = 0; c + half * 8 < rows; c += 16) {
+              float x[8];
+              tmem_ld<8>(t_s + c, x);
+              tmem_fence<8>(x);
+              add8(x, c, true);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
         }
         if (steps > 1) {
           __syncwarp();
@@ -605,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (failed) break;
       // Both halves together; a page outside the pool adds nothing, and a NaN key
       // makes its position NaN.
-      if (nan) total = NAN;
+      if (keys.nan) total = NAN;
       const uint32_t slot = item & 1;
       if (half == 1) {
         if (!__all_sync(0xffffffffu, item < 2 || mbar_wait_long(&bars[kXFree + slot],
@@ -622,12 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         }
         total += other[slot * kTile + tok];
         mbar_arrive(&bars[kXFree + slot]);
-        if (in && (there || pos >= base)) *at = old + (there ? total : 0.0f);
+        if (in && (keys.there || pos >= base)) *at = old + (keys.there ? total : 0.0f);
       }
       ++item;
-      ks = ks_next;
-      there = there_next;
-      nan = nan_next;
     }
   }
   if (failed && p.c.err != nullptr) atomicOr(p.c.err, kErrTimeout);
@@ -638,7 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
 }
 
 template <int DIM>
-cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStream_t stream) {
+cudaError_t launch_dim(const CUtensorMap& map, const CUtensorMap& q_map, const Params& p, int dev,
+                       cudaStream_t stream) {
   static PerDeviceOnce once;
   auto kern = kv8_mass_kernel<DIM>;
   const cudaError_t e = set_max_dynamic_smem(once, dev, kern, Layout<DIM>::kSmem);
@@ -647,7 +850,7 @@ cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStr
   const int64_t items = p.c.requests * p.c.kv_heads * ((p.c.bt_stride + 1) / 2);
   const int64_t sms = kv8_sm_count(dev);
   return launch_pdl(kern, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads),
-                    Layout<DIM>::kSmem, stream, 1u, map, p);
+                    Layout<DIM>::kSmem, stream, 1u, map, q_map, p);
 }
 
 }  // namespace
@@ -678,16 +881,25 @@ cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream) {
   p.tokens = a.tokens;
   p.heads = a.heads;
   p.group = a.heads / a.c.kv_heads;
-  const int rows = 32 * kQWarps / (dim / 8);
-  p.step_tokens = rows / p.group;
-  p.step_heads = rows % p.group;
-  p.all_tokens = kStep / p.group;
-  p.all_heads = kStep % p.group;
+  p.step_heads = p.group < kStep ? p.group : kStep;
+  p.step_tokens = kStep / p.step_heads;
+  p.chunks = (p.group + kStep - 1) / kStep;
+  // q as [tokens][heads][dim], in boxes of a step's rows by 64 dims.
+  CUtensorMap q_map;
+  const cuuint64_t qdim[3] = {(cuuint64_t)dim, (cuuint64_t)a.heads, (cuuint64_t)a.tokens};
+  const cuuint64_t qstride[2] = {(cuuint64_t)dim * 2, (cuuint64_t)a.q_stride * 2};
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)p.step_heads, (cuuint32_t)p.step_tokens};
+  const cuuint32_t qestride[3] = {1, 1, 1};
+  if (enc(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), qdim, qstride, qbox,
+          qestride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   p.scale_log2 = a.scale * kLog2e;
   p.mass = a.mass;
   p.mass_stride = a.mass_stride;
   p.c = a.c;
-  return dim == 128 ? launch_dim<128>(map, p, dev, stream) : launch_dim<64>(map, p, dev, stream);
+  return dim == 128 ? launch_dim<128>(map, q_map, p, dev, stream)
+                    : launch_dim<64>(map, q_map, p, dev, stream);
 }
 
 }  // namespace dsmla

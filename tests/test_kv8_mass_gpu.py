@@ -127,11 +127,13 @@ def test_every_code_and_magnitude(ds):
     _case(ds, [64, 200], [3, 9], 2, 1, 128, seed=6, gain=40.0)
 
 
-def test_non_finite_inputs(ds):
+@pytest.mark.parametrize("counts", [[3, 2], [60, 30]])
+def test_non_finite_inputs(ds, counts):
+    """Few rows and many: a request's rows are multiplied in pieces or as they are."""
     c = Cache([200, 150], 2, 64, 7)
-    scale = 0.125
-    q = c.q(5, 4)
-    starts = _starts([3, 2])
+    scale, n0, n1 = 0.125, counts[0], counts[1]
+    q = c.q(n0 + n1, 4)
+    starts = _starts(counts)
     lse = _lse_of(q, starts, c, scale)
     codes, scales, table, lens = c.device()
 
@@ -151,18 +153,51 @@ def test_non_finite_inputs(ds):
     assert torch.equal(got, want)
     # a row whose lse is -inf adds nothing, one of +inf neither; NaN shows where it sees
     l2 = lse.copy()
-    l2[0, 0], l2[4, 3] = -np.inf, np.nan
+    l2[0, 0], l2[-1, 3] = -np.inf, np.nan
     got = run(q, l2)
-    # (token 0 sees 198 positions and its weights sum to 1; one below 2^-25 is lost beside 1)
-    assert not got[0].isnan().any() and (got[0, 0] <= want[0, 0]).all()
+    # (token 0's weights sum to 1; one far below the sum it is added to is lost)
+    assert not got[0].isnan().any() and (got[0, 0] <= want[0, 0] * (1 + 2.0 ** -20)).all()
     less = (want[0, 0].double() - got[0, 0].double()).sum().item()
-    assert abs(less - 1.0) <= 200 * 2.0 ** -22 and torch.equal(got[0, 1], want[0, 1])
+    assert abs(less - 1.0) <= want[0, 0].sum().item() * 2.0 ** -20
+    assert torch.equal(got[0, 1], want[0, 1])
     assert got[1, 1, :150].isnan().all() and not got[1, 0].isnan().any()
     q2 = q.clone()
-    q2[1, 2, 3] = float("nan")     # token 1 of request 0 sees 199 positions
+    q2[1, 2, 3] = float("nan")     # token 1 of request 0 sees 200 - n0 + 2 positions
     got = run(q2, lse)
-    assert got[0, 1, :199].isnan().all() and not got[0, 1, 199:].isnan().any()
+    sees = 200 - n0 + 2
+    assert got[0, 1, :sees].isnan().all() and not got[0, 1, sees:].isnan().any()
     assert not got[0, 0].isnan().any() and torch.equal(got[1], want[1])
+    # the next request's q and what lies behind the last token reach nobody else
+    q2 = torch.cat([q, torch.full((9, 4, 64), float("nan"), dtype=torch.bfloat16)])
+    q2[n0:n0 + n1] = float("inf")
+    l2 = np.concatenate([lse, np.zeros((9, 4), np.float32)])
+    got = run(q2, l2)
+    assert torch.equal(got[0], want[0]) and got[1, :, :150].isnan().all()
+
+
+@pytest.mark.parametrize("heads,hk", [(7, 1), (46, 2), (39, 1), (40, 1), (41, 1), (100, 1), (113, 1),
+                                      (128, 1), (200, 1), (300, 1)])
+def test_groups_that_fill_a_step_and_do_not(ds, heads, hk):
+    """Steps of whole tokens with rows to spare, of one token, of parts of one."""
+    _case(ds, [300, 129, 64], [1, 40, 23], heads, hk, 64, seed=heads, tail=1)
+    _case(ds, [200, 66], [5, 2], heads, hk, 128, seed=heads)
+
+
+def test_few_rows_and_many_in_one_call(ds):
+    rng = np.random.default_rng(14)
+    _case(ds, rng.integers(70, 900, 30), rng.choice([0, 1, 2, 5, 11, 60], 30), 8, 2, 128, seed=14)
+
+
+def test_small_elements_of_q(ds):
+    """Elements down to 2^-19 of a row's largest count exactly, smaller ones within
+    2^-27 of it."""
+    def edit(q, c):
+        c.codes[:, 0, :, :, 0] = 0                    # the large element's keys
+        q[:] = (q.float() * 2.0 ** -17).to(torch.bfloat16)
+        q[:, :, 0] = 8.0
+    c_scale = 64 ** -0.5
+    assert c_scale == 0.125
+    _case(ds, [150, 80], [2, 1], 4, 1, 64, seed=15, edit=edit)
 
 
 def test_bits_do_not_depend_on_the_batch(ds):
