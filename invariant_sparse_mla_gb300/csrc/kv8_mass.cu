@@ -6,9 +6,9 @@
 //   mass[p] += sum over rows (token, head of the group) that see p of
 //              2^(scale * log2e * a * (q . K_p) - lse * log2e).
 // S^T = K Q^T, positions on the rows of the product: a TMEM lane is a position,
-// so its sum over the query rows stays in one thread (two, each with half of the
-// rows), nothing is reduced across threads, and the order of the additions
-// follows from the request alone.
+// so its sum over the query rows stays in one thread (or two, with every other
+// step), nothing is reduced across threads, and the order of the additions follows
+// from the request alone.
 //
 // An item is (request, kv head, 128 positions), its codes brought by TMA. Two
 // forms, by the request's number of rows R = tokens * heads of the group:
@@ -25,8 +25,8 @@
 //   exponent that bf16 holds: exponent and mantissa bits are placed under bf16's,
 //   subnormals included, and multiplied by 2^120) and lies in TMEM as the A
 //   operand, two buffers; the query rows stream past it in steps of up to 128, by
-//   TMA as they lie, and both operands are exact. S has two buffers of 128
-//   columns, so the product of one step runs under the exponentials of the last.
+//   TMA as they lie, and both operands are exact. S has three buffers of 128
+//   columns, so the product of a step runs under the exponentials of the two before.
 //   The bound is the tensor core (2 dim flops a position and row) and the
 //   exponentials beside it.
 //
@@ -36,8 +36,9 @@
 // request's tiles are taken from both ends in turn, since the last ones are seen
 // by fewer rows.
 //
-// Per CTA: warps 0-7 convert and sum (warps w and w + 4 take half of the dims and
-// half of the columns each), warp 8 brings K, warp 9 issues the products, warp 10
+// Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: each
+// converts half of the dims, and they take the steps, or with few rows the items,
+// in turn, so that one's exponentials run while the other waits), warp 8 brings K, warp 9 issues the products, warp 10
 // brings Q, warps 11-14 lse and the pieces of q.
 
 #include <cuda.h>
@@ -57,6 +58,7 @@ constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11, kLWarps = 4;
 constexpr int kThreads = 32 * (kLWarp + kLWarps);
 constexpr int kMetaSlots = 8;
+constexpr int kNS = 3;                     // S buffers
 constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 
@@ -76,8 +78,8 @@ struct Layout {
   static constexpr int kEnd = kMisc + 32 + 8 * (kThreads / 32);
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  // TMEM columns: S0, S1, then A0, A1.
-  static constexpr int kA = 2 * kStep;
+  // TMEM columns: the S buffers, then A0, A1.
+  static constexpr int kA = kNS * kStep;
   static constexpr int kACols = DIM / 2;
   static constexpr uint32_t kCols = 512;
   static_assert(kA + 2 * kACols <= 512, "TMEM columns");
@@ -90,12 +92,12 @@ enum Bar {
   kLFull = 20,      // lse written
   kQEmpty = 24,     // product done and lse read
   kAFull = 28,      // 2: A written
-  kSFull = 30,      // 2: S ready
-  kSFree = 32,      // 2: S read
-  kXFull = 34,      // 2: the other half's sums written
-  kXFree = 36,      // 2: read
-  kDrain = 38,
-  kNumBars = 39
+  kSFull = 30,      // kNS: S ready
+  kSFree = 33,      // kNS: S read
+  kXFull = 36,      // 2: the other set's sums written
+  kXFree = 38,      // 2: read
+  kDrain = 40,
+  kNumBars = 41
 };
 
 struct Params {
@@ -117,12 +119,14 @@ struct Params {
 // One request, and the CTA's place in it.
 struct Walk {
   int64_t at, end;       // cost before the present item; end of the CTA's share
-  int r, item_r;         // request; of the item before
+  int r;                 // request
+  int item_r, item_kvh;  // of the last item loaded
   int raw, len, n;       // lens[r], clamped, new tokens
   int64_t t0;            // first token
   int tiles, cost;       // cost of an item
   bool few;              // multiplied in pieces
   int i, items;          // present item, items of the request
+  int j;                 // its number among its head's tiles
   int kvh, tile;         // of the present item
   int first;             // first token that sees the tile (few: 0)
   int steps;
@@ -150,22 +154,22 @@ __device__ __forceinline__ void load_request(const Params& p, int64_t r, Walk& w
   w.cost = w.few ? 1 : 1 + (w.n + p.step_tokens - 1) / p.step_tokens * p.chunks;
 }
 
-__device__ __forceinline__ void tile_of(const Walk& w, int i, int* kvh, int* tile) {
-  *kvh = i / w.tiles;
-  const int j = i % w.tiles;
-  *tile = j & 1 ? w.tiles - 1 - (j >> 1) : j >> 1;
+// A head's tiles from both ends in turn.
+__device__ __forceinline__ int tile_of(const Walk& w, int j) {
+  return j & 1 ? w.tiles - 1 - (j >> 1) : j >> 1;
 }
 
 __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
-  const int kvh = w.kvh, before = w.first, r = w.item_r;
+  const int kvh = w.item_kvh, before = w.first, r = w.item_r;
   const bool one = w.steps == 1;
-  tile_of(w, w.i, &w.kvh, &w.tile);
+  w.tile = tile_of(w, w.j);
   // Token i sees position p if p <= base + i.
   const int64_t first = (int64_t)w.tile * kTile - ((int64_t)w.raw - w.n);
   w.first = first > 0 && !w.few ? (int)first : 0;
   w.steps = w.few ? 1 : (w.n - w.first + p.step_tokens - 1) / p.step_tokens * p.chunks;
   w.same = one && w.steps == 1 && r == w.r && kvh == w.kvh && before == w.first;
   w.item_r = w.r;
+  w.item_kvh = w.kvh;
 }
 
 // Step s of an item: its first token, its chunk of heads and its rows.
@@ -193,7 +197,7 @@ __device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
   while (w.i >= w.items) {
     if (++w.r >= p.c.requests) return false;
     load_request(p, w.r, w);
-    w.i = 0;
+    w.i = w.j = w.kvh = 0;
   }
   if (w.at >= w.end) return false;
   load_item(p, w);
@@ -202,6 +206,11 @@ __device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
 __device__ __forceinline__ bool walk_next(const Params& p, Walk& w, int items = 1) {
   w.at += (int64_t)items * w.cost;
   w.i += items;
+  w.j += items;
+  while (w.j >= w.tiles && w.i < w.items) {
+    w.j -= w.tiles;
+    ++w.kvh;
+  }
   if (w.at >= w.end) return false;
   return walk_settle(p, w);
 }
@@ -243,6 +252,14 @@ __device__ __forceinline__ uint16_t piece(float& u0, float& u1) {
   return b;
 }
 
+// Two arrivals (of a set, where both are counted and the other does not come by).
+__device__ __forceinline__ void mbar_arrive_twice(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.shared::cta.b64 st, [%0], 2;\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int DIM>
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
   if constexpr (DIM == 128)
@@ -275,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (i >= kAFull && i < kAFull + 2) n = kSum;
       if (i >= kLFull && i < kLFull + NQ) n = 32 * kLWarps;
       if (i >= kQEmpty && i < kQEmpty + NQ) n = 1 + kSumWarps;
-      if (i >= kSFree && i < kSFree + 2) n = kSumWarps;
+      if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
       if (i >= kXFull && i < kXFree + 2) n = kSum / 2;
       mbar_init(&bars[i], n);
     }
@@ -350,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     w.steps = 0;           // no item before the first
     w.i = (int)((lo - start_s[1] + w.cost - 1) / w.cost);
     w.at = start_s[1] + (int64_t)w.i * w.cost;
+    w.kvh = w.i / w.tiles;
+    w.j = w.i % w.tiles;
     some = walk_settle(p, w);
   }
 
@@ -373,9 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       k.y = none;
       k.ks = 0.0f;
       if (lane / 2 < k.count) {
-        int kvh, tile;
-        tile_of(v, v.i + lane / 2, &kvh, &tile);
-        const int b = 2 * tile + (lane & 1);
+        const int i = v.i + lane / 2, kvh = i / v.tiles;
+        const int b = 2 * tile_of(v, i - kvh * v.tiles) + (lane & 1);
         if ((int64_t)b * kPage < v.len) {
           const int64_t page = p.c.block_table[(int64_t)v.r * p.c.bt_stride + b];
           if (page >= 0 && page < p.c.num_pages) {
@@ -434,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // Items, converted ones, steps (of S buffers) and loads of Q so far: an item of
     // one step may use the load of the one before it, which is let go when the
     // next comes.
-    uint32_t item = 0, conv = 0, g = 0, ql = 0;
+    uint32_t item = 0, conv = 0, g = 0, buf = 0, ql = 0;
     bool held = false;
     while (some && !failed) {
       bool ok;
@@ -448,13 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         if (leader) mma_commit(&bars[kQEmpty + (ql - 1) % NQ]);
         __syncwarp();
       }
-      for (int s = 0; s < w.steps; ++s, ++g) {
-        const uint32_t buf = g & 1;
+      for (int s = 0; s < w.steps; ++s, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
         if (!w.same) ++ql;
         const uint32_t st = (ql - 1) % NQ, ph = ((ql - 1) / NQ) & 1u;
         ok = ok && (w.same || (mbar_wait_long(&bars[kQFull + st], ph) &&
                                (!w.few || mbar_wait_long(&bars[kLFull + st], ph)))) &&
-             (g < 2 || mbar_wait_long(&bars[kSFree + buf], ((g >> 1) - 1) & 1u));
+             (g < kNS || mbar_wait_long(&bars[kSFree + buf], (g / kNS - 1) & 1u));
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
@@ -624,11 +641,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     }
   } else {
     // --------------------------------------------------- convert and sum
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, set = warp >> 2;
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     // Items, converted ones, steps and loads of Q so far (as the issuer counts).
-    uint32_t item = 0, conv = 0, g = 0, ql = 0;
+    uint32_t item = 0, conv = 0, summed = 0, g = 0, buf = 0, ql = 0;
     bool held = false;
     struct Keys {
       float scale;
@@ -645,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       *keys = read_meta(it);
       const uint8_t* src = smem + LY::kK + st * LY::kKBytes;
       uint32_t bad = 0;
-      const uint32_t t_a = tmem + lane_base + LY::kA + (conv & 1) * LY::kACols + half * (DIM / 4);
+      const uint32_t t_a = tmem + lane_base + LY::kA + (conv & 1) * LY::kACols + set * (DIM / 4);
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < DIM / 64; ++c) {
@@ -653,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint4 x = *reinterpret_cast<const uint4*>(
-              src + swz<DIM>(tok, half * (DIM / 2) + c * 32 + e * 16));
+              src + swz<DIM>(tok, set * (DIM / 2) + c * 32 + e * 16));
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -673,50 +690,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (lane == 0) mbar_arrive(&bars[kKEmpty + st]);
       return true;
     };
+    // What the mass held before, read an item ahead by the set that adds to it: of
+    // few rows' items set 0 has the even ones, of the others it has all.
+    auto mass_at = [&](const Walk& v) {
+      return p.mass + ((int64_t)v.r * p.c.kv_heads + v.kvh) * p.mass_stride + v.tile * kTile + tok;
+    };
+    auto mine = [&](const Walk& v, uint32_t it) { return v.few ? (int)(it & 1) == set : set == 0; };
+    auto held_mass = [&](const Walk& v, uint32_t it) {
+      const int pos = v.tile * kTile + tok;
+      return mine(v, it) && pos < v.len && pos < v.raw - v.n ? *mass_at(v) : 0.0f;
+    };
     Keys keys{0.0f, false, false}, next{0.0f, false, false};
+    float old = 0.0f, old_next = 0.0f;
+    if (some) old_next = held_mass(w, 0);
     if (some && !w.few && !convert(0, &next)) failed = true;
     while (some && !failed) {
-      keys = next;
-      const bool few = w.few, same = w.same;
-      const int steps = w.steps, base = w.raw - w.n;
-      const int pos0 = w.tile * kTile, pos = pos0 + tok;
-      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
       const Walk now = w;
-      float* at = p.mass + ((int64_t)w.r * p.c.kv_heads + w.kvh) * p.mass_stride + pos;
-      const bool in = pos < w.len;
-      float old = 0.0f;
-      if (half == 0 && in && pos < base) old = *at;
-      if (held && !same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
-      held = steps == 1;
+      keys = next;
+      old = old_next;
+      const int rows = now.n * p.group, base = now.raw - now.n;
+      const int pos0 = now.tile * kTile, pos = pos0 + tok;
+      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
+      if (held && !now.same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
+      held = now.steps == 1;
       // The next item's K, while the products of this one run.
       some = walk_next(p, w);
+      if (some) old_next = held_mass(w, item + 1);
       if (some && !w.few && !convert(item + 1, &next)) {
         failed = true;
         break;
       }
       float total = 0.0f;
-      for (int s = 0; s < steps; ++s, ++g) {
-        if (!same) ++ql;
-        const uint32_t st = (ql - 1) % NQ, buf = g & 1;
+      // Few rows: the sets take items in turn, else steps in turn. Both wait for
+      // every product and both let its buffer (and Q) go, the one that has nothing to
+      // do there at once: a set that is behind would otherwise miss a phase.
+      for (int s = 0; s < now.steps; ++s, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
+        if (!now.same) ++ql;
+        const uint32_t st = (ql - 1) % NQ;
         const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 12));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
-        const bool ok = (same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
-                        mbar_wait_long(&bars[kSFull + buf], (g >> 1) & 1u);
+        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
+                        mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
         }
+        if ((int)((now.few ? item : (uint32_t)s) & 1) != set) {
+          if (lane == 0) {
+            mbar_arrive(&bars[kSFree + buf]);
+            if (now.steps > 1) mbar_arrive(&bars[kQEmpty + st]);
+          }
+          continue;
+        }
         tc_fence_after();
         float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-        if (few) {
+        const uint32_t t_s = tmem + lane_base + buf * kStep;
+        if (now.few) {
           // The product is done, so K is read: its stage is free.
           keys = read_meta(item);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kKEmpty + item % NK]);
-          const int rows = now.n * p.group, r8 = (rows + 7) & ~7;
-          const uint32_t t_s = tmem + lane_base + buf * kStep;
+          if (lane == 0) mbar_arrive_twice(&bars[kKEmpty + item % NK]);
+          const int r8 = (rows + 7) & ~7;
           const float2 ks = make_float2(keys.scale, keys.scale);
-          for (int c = half * 4; c < rows; c += 8) {
+          for (int c = 0; c < rows; c += 4) {
             float x[4], y[4], z[4];
             tmem_ld<4>(t_s + c, x);
             tmem_ld<4>(t_s + r8 + c, y);
@@ -748,21 +784,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
         } else {
-          // Columns of 8, warps w and w + 4 in turn. ls holds minus the lse.
-          const uint32_t t_s = tmem + lane_base + buf * kStep + half * 8;
-          const float* lh = ls + half * 8;
-          const int* vh = vs + half * 8;
+          // Columns of 8. ls holds minus the lse.
           const float2 ks = make_float2(keys.scale, keys.scale);
           auto add8 = [&](const float* x, int c, bool masked) {
-            const float4 l0 = *reinterpret_cast<const float4*>(lh + c);
-            const float4 l1 = *reinterpret_cast<const float4*>(lh + c + 4);
+            const float4 l0 = *reinterpret_cast<const float4*>(ls + c);
+            const float4 l1 = *reinterpret_cast<const float4*>(ls + c + 4);
             float2 a = fma2(make_float2(x[0], x[1]), ks, make_float2(l0.x, l0.y));
             float2 b = fma2(make_float2(x[2], x[3]), ks, make_float2(l0.z, l0.w));
             float2 d = fma2(make_float2(x[4], x[5]), ks, make_float2(l1.x, l1.y));
             float2 e = fma2(make_float2(x[6], x[7]), ks, make_float2(l1.z, l1.w));
             if (masked) {
-              const int4 v0 = *reinterpret_cast<const int4*>(vh + c);
-              const int4 v1 = *reinterpret_cast<const int4*>(vh + c + 4);
+              const int4 v0 = *reinterpret_cast<const int4*>(vs + c);
+              const int4 v1 = *reinterpret_cast<const int4*>(vs + c + 4);
               if (pos >= v0.x) a.x = -INFINITY;
               if (pos >= v0.y) a.y = -INFINITY;
               if (pos >= v0.z) b.x = -INFINITY;
@@ -777,20 +810,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
             acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
           };
-          const int rows = step_of(p, now, s).rows;
+          const int here = step_of(p, now, s).rows;
           const bool masked = edge && vs[0] < pos0 + kTile;
-          if (rows == capacity && capacity > kStep - 16 && !masked) {
-            float x[64];
+          if (here == capacity && capacity > kStep - 16 && !masked) {
+            // 32 columns at a time, the next ones on their way meanwhile.
+            float x[2][32];
+            tmem_ld32(t_s, x[0]);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) tmem_ld<8>(t_s + 16 * c, x + 8 * c);
-            tmem_fence<64>(x);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
+            for (int c = 0; c < 4; ++c) {
+              tmem_fence<32>(x[c & 1]);
+              if (c < 3) tmem_ld32(t_s + 32 * (c + 1), x[(c + 1) & 1]);
+              if (c == 3) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
+              }
 #pragma unroll
-            for (int c = 0; c < 8; ++c) add8(x + 8 * c, 16 * c, false);
+              for (int e = 0; e < 4; ++e) add8(x[c & 1] + 8 * e, 32 * c + 8 * e, false);
+            }
           } else {
-            for (int c = 0; c + half * 8 < rows; c += 16) {
+            for (int c = 0; c < here; c += 8) {
               float x[8];
               tmem_ld<8>(t_s + c, x);
               tmem_fence<8>(x);
@@ -800,35 +839,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
           }
-        }
-        if (steps > 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kQEmpty + st]);
+          if (now.steps > 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kQEmpty + st]);
+          }
         }
         total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
       }
       if (failed) break;
-      // Both halves together; a page outside the pool adds nothing, and a NaN key
-      // makes its position NaN.
-      if (keys.nan) total = NAN;
-      const uint32_t slot = item & 1;
-      if (half == 1) {
-        if (!__all_sync(0xffffffffu, item < 2 || mbar_wait_long(&bars[kXFree + slot],
-                                                                ((item >> 1) - 1) & 1u))) {
+      if (!now.few) {
+        // Both sets together; a NaN key makes its position NaN.
+        if (keys.nan) total = NAN;
+        const uint32_t slot = summed & 1;
+        bool ok;
+        if (set == 1) {
+          ok = summed < 2 || mbar_wait_long(&bars[kXFree + slot], ((summed >> 1) - 1) & 1u);
+          if (ok) {
+            other[slot * kTile + tok] = total;
+            mbar_arrive(&bars[kXFull + slot]);
+          }
+        } else {
+          ok = mbar_wait_long(&bars[kXFull + slot], (summed >> 1) & 1u);
+          if (ok) {
+            total += other[slot * kTile + tok];
+            mbar_arrive(&bars[kXFree + slot]);
+          }
+        }
+        ++summed;
+        if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
         }
-        other[slot * kTile + tok] = total;
-        mbar_arrive(&bars[kXFull + slot]);
-      } else {
-        if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kXFull + slot], (item >> 1) & 1u))) {
-          failed = true;
-          break;
-        }
-        total += other[slot * kTile + tok];
-        mbar_arrive(&bars[kXFree + slot]);
-        if (in && (keys.there || pos >= base)) *at = old + (keys.there ? total : 0.0f);
       }
+      // (A page outside the pool adds nothing.)
+      if (mine(now, item) && pos < now.len && (keys.there || pos >= base))
+        *mass_at(now) = old + (keys.there ? total : 0.0f);
       ++item;
     }
   }
