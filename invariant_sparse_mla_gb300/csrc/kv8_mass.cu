@@ -160,14 +160,20 @@ __device__ __forceinline__ int tile_of(const Walk& w, int j) {
 }
 
 __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
-  const int kvh = w.item_kvh, before = w.first, r = w.item_r;
-  const bool one = w.steps == 1;
   w.tile = tile_of(w, w.j);
-  // Token i sees position p if p <= base + i.
-  const int64_t first = (int64_t)w.tile * kTile - ((int64_t)w.raw - w.n);
-  w.first = first > 0 && !w.few ? (int)first : 0;
-  w.steps = w.few ? 1 : (w.n - w.first + p.step_tokens - 1) / p.step_tokens * p.chunks;
-  w.same = one && w.steps == 1 && r == w.r && kvh == w.kvh && before == w.first;
+  const bool one = w.steps == 1 && w.item_r == w.r && w.item_kvh == w.kvh;
+  if (w.few) {
+    w.same = one;
+    w.first = 0;
+    w.steps = 1;
+  } else {
+    // Token i sees position p if p <= base + i.
+    const int before = w.first;
+    const int64_t first = (int64_t)w.tile * kTile - ((int64_t)w.raw - w.n);
+    w.first = first > 0 ? (int)first : 0;
+    w.steps = (w.n - w.first + p.step_tokens - 1) / p.step_tokens * p.chunks;
+    w.same = one && w.steps == 1 && before == w.first;
+  }
   w.item_r = w.r;
   w.item_kvh = w.kvh;
 }
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           __syncwarp();
         }
       }
-      if (!failed) some = walk_next(p, w);
+      if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
     }
     if (lane == 0)   // every copy has landed before the CTA can exit
       for (uint32_t i = issued > NQ ? issued - NQ : 0; i < issued; ++i)
@@ -637,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         mbar_arrive(&bars[kLFull + st]);
         look(s + 1, &l, &vis);
       }
-      if (!failed) some = walk_next(p, w);
+      // (Few rows serve all tiles of their head.)
+      if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
     }
   } else {
     // --------------------------------------------------- convert and sum
@@ -692,13 +699,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     };
     // What the mass held before, read an item ahead by the set that adds to it: of
     // few rows' items set 0 has the even ones, of the others it has all.
-    auto mass_at = [&](const Walk& v) {
-      return p.mass + ((int64_t)v.r * p.c.kv_heads + v.kvh) * p.mass_stride + v.tile * kTile + tok;
-    };
-    auto mine = [&](const Walk& v, uint32_t it) { return v.few ? (int)(it & 1) == set : set == 0; };
+    float* row = nullptr;      // this thread's position of the next item's head's tile 0
+    auto mine = [&](const Walk& v, uint32_t it) { return (v.few ? (int)(it & 1) : 0) == set; };
     auto held_mass = [&](const Walk& v, uint32_t it) {
+      if (!v.same)
+        row = p.mass + ((int64_t)v.r * p.c.kv_heads + v.kvh) * p.mass_stride + tok;
       const int pos = v.tile * kTile + tok;
-      return mine(v, it) && pos < v.len && pos < v.raw - v.n ? *mass_at(v) : 0.0f;
+      return mine(v, it) && pos < v.len && pos < v.raw - v.n ? row[v.tile * kTile] : 0.0f;
     };
     Keys keys{0.0f, false, false}, next{0.0f, false, false};
     float old = 0.0f, old_next = 0.0f;
@@ -713,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
       if (held && !now.same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
       held = now.steps == 1;
+      float* const at = row + pos0;
       // The next item's K, while the products of this one run.
       some = walk_next(p, w);
       if (some) old_next = held_mass(w, item + 1);
@@ -873,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       }
       // (A page outside the pool adds nothing.)
       if (mine(now, item) && pos < now.len && (keys.there || pos >= base))
-        *mass_at(now) = old + (keys.there ? total : 0.0f);
+        *at = old + (keys.there ? total : 0.0f);
       ++item;
     }
   }

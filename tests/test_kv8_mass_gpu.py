@@ -239,6 +239,31 @@ def test_weights_of_a_row_sum_to_one(ds):
         assert (rest - 8).abs().max() <= 8 * 2.0 ** -13
 
 
+@pytest.mark.parametrize("counts", [[1, 2], [5, 1], [3, 70], [90, 1]])
+def test_long_runs_of_items(ds, counts):
+    """Dozens of items for every CTA, few rows and many: the weights of a row sum to
+    one (what lies behind the rows' own positions was 0)."""
+    lens, hk, heads, d = [90000, 60000], 8, 32, 64
+    c = Cache([64, 64], hk, d, 12)
+    rng = np.random.default_rng(12)
+    pages = 1400
+    codes = torch.randint(0, 0x70, (pages, 2, hk, 64, d), dtype=torch.uint8, device=DEV)
+    scales = torch.full((pages, 2, hk), 2.0 ** -7, device=DEV)
+    table = torch.as_tensor(rng.integers(0, pages, (2, 1408)), dtype=torch.int32).to(DEV)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    starts = torch.as_tensor(_starts(counts)).to(DEV)
+    q = c.q(sum(counts), heads, gain=0.05).to(DEV)
+    _, lse = ds.kv8_prefill(q, starts, codes, scales, table, ln, 0.125)
+    mass = torch.zeros((2, hk, 64 * 1408), device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ds.kv8_mass(q, lse, starts, codes, scales, table, ln, 0.125, mass, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    want = torch.tensor(counts, dtype=torch.float64)[:, None] * (heads // hk)
+    assert ((mass.double().sum(-1).cpu() / want - 1).abs() <= 2.0 ** -13).all()
+    assert all((mass[r, :, n:] == 0).all() and (mass[r, :, :n] > 0).all() for r, n in enumerate(lens))
+
+
 def test_capture_streams_and_two_at_once(ds):
     c = Cache([1500, 800], 2, 64, 10)
     codes, scales, table, ln = c.device()
