@@ -18,8 +18,10 @@
 //   two: q = 2^-k (q0 + q1 / 32 + q2 / 1024). A bf16 number has 8 significant
 //   bits, so this is exact down to 2^-19 of the row's largest |q| and off by up to
 //   2^-27 of that below. The pieces are made once per (request, kv head) and
-//   serve all its tiles; an item is then a product of 3 R columns and 128 R
-//   exponentials. The bound is HBM, dim bytes a position and head.
+//   serve all its tiles; a tile is then a product of 3 R columns and 128 R
+//   exponentials, and up to four of them are an item, so that the walk and the waits
+//   are paid once and a thread has two positions to work on. The bound is HBM, dim
+//   bytes a position and head.
 //
 // - More: K becomes bf16 once per item (an E4M3 code has 4 significant bits and an
 //   exponent that bf16 holds: exponent and mantissa bits are placed under bf16's,
@@ -38,8 +40,8 @@
 //
 // Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: each
 // converts half of the dims, and they take the steps, or with few rows the items,
-// in turn, so that one's exponentials run while the other waits), warp 8 brings K, warp 9 issues the products, warp 10
-// brings Q, warps 11-14 lse and the pieces of q.
+// in turn, so that one's exponentials run while the other waits), warp 8 brings K, warp 9 issues the products,
+// warps 10 and 11 bring Q, lse and the pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -55,9 +57,9 @@ namespace {
 constexpr int kTile = 128;                 // positions of an item
 constexpr int kStep = 128;                 // query rows of a step
 constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11, kLWarps = 4;
-constexpr int kThreads = 32 * (kLWarp + kLWarps);
-constexpr int kMetaSlots = 8;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
+constexpr int kThreads = 32 * (kQWarp + kQWarps);   // (12 warps: 168 registers a thread)
+constexpr int kMetaSlots = 32;
 constexpr int kNS = 3;                     // S buffers
 constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
@@ -66,7 +68,7 @@ template <int DIM>
 struct Layout {
   static constexpr int kKBytes = kTile * DIM;
   static constexpr int kQBytes = kStep * DIM * 2;
-  static constexpr int kNK = 6;                     // stages (at most kMetaSlots - 2)
+  static constexpr int kNK = 6;                     // stages
   static constexpr int kNQ = DIM == 128 ? 3 : 4;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kNK * kKBytes;
@@ -87,7 +89,7 @@ struct Layout {
 
 enum Bar {
   kKFull = 0,       // K landed (<= 6)
-  kKEmpty = 8,      // K converted
+  kKEmpty = 8,      // K converted, or its product done
   kQFull = 16,      // Q landed (<= 4)
   kLFull = 20,      // lse written
   kQEmpty = 24,     // product done and lse read
@@ -125,6 +127,7 @@ struct Walk {
   int64_t t0;            // first token
   int tiles, cost;       // cost of an item
   bool few;              // multiplied in pieces
+  int batch, nb;         // most tiles of an item, and those of the present one
   int i, items;          // present item, items of the request
   int j;                 // its number among its head's tiles
   int kvh, tile;         // of the present item
@@ -151,6 +154,9 @@ __device__ __forceinline__ void load_request(const Params& p, int64_t r, Walk& w
   const int rows = w.n * p.group;   // (below 2^31 - 256)
   // (The pieces stay clear of the rows of a stage that no step writes.)
   w.few = rows <= kFewRows && 3 * ((rows + 7) & ~7) <= p.step_tokens * p.step_heads;
+  // As many tiles as S columns of one buffer: products of 32 columns with up to 8
+  // rows, 48 with 16.
+  w.batch = !w.few || rows > 16 ? 1 : (rows > 8 ? 2 : 4);
   w.cost = w.few ? 1 : 1 + (w.n + p.step_tokens - 1) / p.step_tokens * p.chunks;
 }
 
@@ -160,12 +166,14 @@ __device__ __forceinline__ int tile_of(const Walk& w, int j) {
 }
 
 __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
-  w.tile = tile_of(w, w.j);
+  w.tile = tile_of(w, w.j);   // (the first of a batch)
   const bool one = w.steps == 1 && w.item_r == w.r && w.item_kvh == w.kvh;
   if (w.few) {
     w.same = one;
     w.first = 0;
     w.steps = 1;
+    const int left = w.tiles - w.j < w.batch ? w.tiles - w.j : w.batch;
+    w.nb = w.end - w.at < left ? (int)(w.end - w.at) : left;   // (cost 1 each)
   } else {
     // Token i sees position p if p <= base + i.
     const int before = w.first;
@@ -173,6 +181,7 @@ __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
     w.first = first > 0 ? (int)first : 0;
     w.steps = (w.n - w.first + p.step_tokens - 1) / p.step_tokens * p.chunks;
     w.same = one && w.steps == 1 && before == w.first;
+    w.nb = 1;
   }
   w.item_r = w.r;
   w.item_kvh = w.kvh;
@@ -209,7 +218,8 @@ __device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
   load_item(p, w);
   return true;
 }
-__device__ __forceinline__ bool walk_next(const Params& p, Walk& w, int items = 1) {
+// `items` in tiles: those of the present item, or more.
+__device__ __forceinline__ bool walk_next(const Params& p, Walk& w, int items) {
   w.at += (int64_t)items * w.cost;
   w.i += items;
   w.j += items;
@@ -258,14 +268,6 @@ __device__ __forceinline__ uint16_t piece(float& u0, float& u1) {
   return b;
 }
 
-// Two arrivals (of a set, where both are counted and the other does not come by).
-__device__ __forceinline__ void mbar_arrive_twice(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b64 st;\n\t"
-      "mbarrier.arrive.shared::cta.b64 st, [%0], 2;\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-
 template <int DIM>
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
   if constexpr (DIM == 128)
@@ -294,9 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if (i >= kKEmpty && i < kKEmpty + NK) n = kSumWarps;
       if (i >= kAFull && i < kAFull + 2) n = kSum;
-      if (i >= kLFull && i < kLFull + NQ) n = 32 * kLWarps;
+      if (i >= kLFull && i < kLFull + NQ) n = 32 * kQWarps;
       if (i >= kQEmpty && i < kQEmpty + NQ) n = 1 + kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
       if (i >= kXFull && i < kXFree + 2) n = kSum / 2;
@@ -455,18 +456,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const uint64_t q8_desc = tile_desc<DIM>(sbase + LY::kQ);
     const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
     const bool leader = elect_one();
-    // Items, converted ones, steps (of S buffers) and loads of Q so far: an item of
+    // Tiles, converted ones, steps (of S buffers) and loads of Q so far: an item of
     // one step may use the load of the one before it, which is let go when the
     // next comes.
-    uint32_t item = 0, conv = 0, g = 0, buf = 0, ql = 0;
+    uint32_t tile = 0, conv = 0, g = 0, buf = 0, ql = 0;
     bool held = false;
     while (some && !failed) {
-      bool ok;
-      if (w.few) {
-        ok = mbar_wait_long(&bars[kKFull + item % NK], (item / NK) & 1u);
-      } else {
+      bool ok = true;
+      if (!w.few) {
         ok = mbar_wait_long(&bars[kAFull + (conv & 1)], (conv >> 1) & 1u);
         ++conv;
+        if (lane == 0) mbar_arrive(&bars[kKEmpty + tile % NK]);   // K is read
+        ++tile;
       }
       if (held && !w.same) {
         if (leader) mma_commit(&bars[kQEmpty + (ql - 1) % NQ]);
@@ -484,17 +485,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         }
         tc_fence_after();
         if (w.few) {
-          if (leader) {
-            const int n = (3 * ((w.n * p.group + 7) & ~7) + 15) & ~15;
-            const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
-            const uint64_t a = k_desc + (uint64_t)((item % NK * LY::kKBytes) >> 4);
-            const uint64_t b = q8_desc + (uint64_t)((st * LY::kQBytes) >> 4);
+          const int n = (3 * ((w.n * p.group + 7) & ~7) + 15) & ~15;
+          const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
+          const uint64_t b = q8_desc + (uint64_t)((st * LY::kQBytes) >> 4);
+          for (int u = 0; u < w.nb; ++u, ++tile) {
+            const uint32_t kst = tile % NK;
+            if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kKFull + kst], (tile / NK) & 1u))) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            if (leader) {
+              const uint64_t a = k_desc + (uint64_t)((kst * LY::kKBytes) >> 4);
 #pragma unroll
-            for (int k = 0; k < DIM / 32; ++k)
-              mma_f8_ss(tmem + buf * kStep, a + ((k * 32) >> 4), b + ((k * 32) >> 4), idesc,
-                        k > 0 ? 1u : 0u);
-            mma_commit(&bars[kSFull + buf]);
+              for (int k = 0; k < DIM / 32; ++k)
+                mma_f8_ss(tmem + buf * kStep + u * n, a + ((k * 32) >> 4), b + ((k * 32) >> 4),
+                          idesc, k > 0 ? 1u : 0u);
+              mma_commit(&bars[kKEmpty + kst]);
+            }
+            __syncwarp();
           }
+          if (failed) break;
+          if (leader) mma_commit(&bars[kSFull + buf]);
         } else {
           const int n = (step_of(p, w, s).rows + 15) & ~15;
           if (leader) {
@@ -513,84 +525,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         __syncwarp();
       }
       held = w.steps == 1;
-      ++item;
-      if (!failed) some = walk_next(p, w);
+      if (!failed) some = walk_next(p, w, w.nb);
     }
     if (leader) mma_commit(&bars[kDrain]);
     __syncwarp();
     if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
     __syncwarp();
-  } else if (warp == kQWarp) {
-    // ------------------------------------------------------------------ Q
-    uint32_t ql = 0, issued = 0;
-    const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
-    while (some && !failed) {
-      if (!w.same) {
-        for (int s = 0; s < w.steps; ++s, ++ql) {
-          const uint32_t st = ql % NQ;
-          if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
-                                                                 (ql / NQ - 1) & 1u))) {
-            failed = true;
-            break;
-          }
-          if (lane == 0) {
-            if (w.few) {
-              mbar_arrive(&bars[kQFull + st]);   // (the pieces come from the next warps)
-            } else {
-              const Step x = step_of(p, w, s);
-              mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
+  } else if (warp >= kQWarp) {
+    // --------------------------------------- Q, lse, and pieces of few rows
+    constexpr int T = 32 * kQWarps, N = kStep / T;     // a thread's rows of a step: t, t + T
+    const int t = tid - 32 * kQWarp;
+    int t_token[N], t_head[N];
 #pragma unroll
-              for (int b = 0; b < DIM / 64; ++b)
-                tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
-                              w.kvh * p.group + x.head, (int)w.t0 + x.token, &bars[kQFull + st]);
-            }
-            issued = ql + 1;
-          }
-          __syncwarp();
-        }
-      }
-      if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
+    for (int i = 0; i < N; ++i) {
+      t_token[i] = (t + i * T) / p.step_heads;
+      t_head[i] = (t + i * T) % p.step_heads;
     }
-    if (lane == 0)   // every copy has landed before the CTA can exit
-      for (uint32_t i = issued > NQ ? issued - NQ : 0; i < issued; ++i)
-        if (!mbar_wait_long(&bars[kQFull + i % NQ], (i / NQ) & 1u)) failed = true;
-    __syncwarp();
-  } else if (warp >= kLWarp) {
-    // --------------------------------------------- lse, and pieces of few rows
-    const int t = tid - 32 * kLWarp;
-    const int t_token = t / p.step_heads, t_head = t % p.step_heads;   // of a step's row t
+    const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
     uint32_t ql = 0;
     while (some && !failed) {
       if (w.same) {
-        some = walk_next(p, w);
+        some = walk_next(p, w, w.nb);
         continue;
       }
       const int seen = w.raw - w.n + 1;               // by token 0
       const float* lse0 = p.lse + w.t0 * p.heads + w.kvh * p.group;
-      // Row t's lse and length seen, read a step ahead.
-      auto look = [&](int s, float* l, int* vis) {
-        *l = -INFINITY;
-        *vis = INT_MIN;
-        if (s >= w.steps) return;
-        int token, head;
-        bool in;
-        if (w.few) {
-          token = t / p.group;
-          head = t % p.group;
-          in = t < w.n * p.group;
-        } else {
-          const Step x = step_of(p, w, s);
-          token = x.token + t_token;
-          head = x.head + t_head;
-          in = t < x.rows;
+      // The lse and the length seen of this thread's rows, read a step ahead.
+      float l[N];
+      int vis[N];
+      auto look = [&](int s) {
+        const Step x = step_of(p, w, s);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int row = t + i * T;
+          const int token = w.few ? row / p.group : x.token + t_token[i];
+          const int head = w.few ? row % p.group : x.head + t_head[i];
+          l[i] = -INFINITY;
+          vis[i] = INT_MIN;
+          if (row < (w.few ? w.n * p.group : x.rows)) {
+            l[i] = lse0[(int64_t)token * p.heads + head];
+            vis[i] = seen + token;
+          }
         }
-        if (!in) return;
-        *l = lse0[(int64_t)token * p.heads + head];
-        *vis = seen + token;
       };
-      float l;
-      int vis;
-      look(0, &l, &vis);
+      look(0);
       for (int s = 0; s < w.steps; ++s, ++ql) {
         const uint32_t st = ql % NQ;
         if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
@@ -598,16 +576,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           failed = true;
           break;
         }
+        if (t == 0) {
+          if (w.few) {
+            mbar_arrive(&bars[kQFull + st]);   // (the pieces come with the lse)
+          } else {
+            const Step x = step_of(p, w, s);
+            mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
+#pragma unroll
+            for (int b = 0; b < DIM / 64; ++b)
+              tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
+                            w.kvh * p.group + x.head, (int)w.t0 + x.token, &bars[kQFull + st]);
+          }
+        }
         float* ls = reinterpret_cast<float*>(smem + LY::kLse + st * (kStep * 12));
-        ls[t] = l == -INFINITY ? -INFINITY : -l * kLog2e;   // (a row of -inf adds nothing)
-        reinterpret_cast<int*>(ls)[kStep + t] = vis;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          // (A row of -inf adds nothing.)
+          ls[t + i * T] = l[i] == -INFINITY ? -INFINITY : -l[i] * kLog2e;
+          reinterpret_cast<int*>(ls)[kStep + t + i * T] = vis[i];
+        }
         if (w.few) {
           // A warp a row, in turn. (What lies behind the rows is anything: columns
           // of the product that nobody reads.)
           constexpr int E = DIM / 32;
           const int rows = w.n * p.group, r8 = (rows + 7) & ~7;
           uint8_t* q8 = smem + LY::kQ + st * LY::kQBytes;
-          for (int r = warp - kLWarp; r < rows; r += kLWarps) {
+#pragma unroll 4
+          for (int r = warp - kQWarp; r < rows; r += kQWarps) {
             const __nv_bfloat16* src = p.q + (w.t0 + r / p.group) * p.q_stride +
                                        ((int64_t)w.kvh * p.group + r % p.group) * DIM + lane * E;
             float x[E], a = 0.0f;
@@ -641,18 +636,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           fence_proxy_async_smem();
         }
         mbar_arrive(&bars[kLFull + st]);
-        look(s + 1, &l, &vis);
+        if (s + 1 < w.steps) look(s + 1);
       }
       // (Few rows serve all tiles of their head.)
       if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
     }
+    if (t == 0)   // every copy has landed before the CTA can exit
+      for (uint32_t i = ql > NQ ? ql - NQ : 0; i < ql; ++i)
+        if (!mbar_wait_long(&bars[kQFull + i % NQ], (i / NQ) & 1u)) failed = true;
+    __syncwarp();
   } else {
     // --------------------------------------------------- convert and sum
     const int quad = warp & 3, set = warp >> 2;
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    // Items, converted ones, steps and loads of Q so far (as the issuer counts).
-    uint32_t item = 0, conv = 0, summed = 0, g = 0, buf = 0, ql = 0;
+    // Items, tiles, converted ones, steps and loads of Q so far (as the issuer counts).
+    uint32_t item = 0, tile = 0, conv = 0, summed = 0, g = 0, buf = 0, ql = 0;
     bool held = false;
     struct Keys {
       float scale;
@@ -662,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const float4 m = meta[it & (kMetaSlots - 1)];
       return Keys{tok < kPage ? m.x : m.z, (tok < kPage ? m.y : m.w) != 0.0f, false};
     };
-    // K of item `it` to bf16, this thread's half of the dims.
+    // K of tile number `it` to bf16, this thread's half of the dims.
     auto convert = [&](uint32_t it, Keys* keys) {
       const int st = (int)(it % NK);
       if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kKFull + st], (it / NK) & 1u))) return false;
@@ -693,22 +692,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       tc_fence_before();
       mbar_arrive(&bars[kAFull + (conv & 1)]);
       ++conv;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kKEmpty + st]);
       return true;
     };
-    // What the mass held before, read an item ahead by the set that adds to it: of
-    // few rows' items set 0 has the even ones, of the others it has all.
+    // What the mass held before, read an item ahead by the set that adds to it. Of
+    // few rows' items the sets take the tiles in turn (or the items, where they
+    // have one tile), up to two a set; of the others set 0 has all.
     float* row = nullptr;      // this thread's position of the next item's head's tile 0
-    auto mine = [&](const Walk& v, uint32_t it) { return (v.few ? (int)(it & 1) : 0) == set; };
+    auto first_mine = [&](const Walk& v, uint32_t it) {
+      return v.few && v.batch == 1 ? (int)(it + set) & 1 : set;
+    };
+    auto tile_at = [&](const Walk& v, int u) { return v.nb == 1 ? v.tile : tile_of(v, v.j + u); };
+    struct Two {
+      float a, b;
+    };
     auto held_mass = [&](const Walk& v, uint32_t it) {
       if (!v.same)
         row = p.mass + ((int64_t)v.r * p.c.kv_heads + v.kvh) * p.mass_stride + tok;
-      const int pos = v.tile * kTile + tok;
-      return mine(v, it) && pos < v.len && pos < v.raw - v.n ? row[v.tile * kTile] : 0.0f;
+      auto get = [&](int u) {
+        if (u >= v.nb) return 0.0f;
+        const int t0 = tile_at(v, u) * kTile;
+        return t0 + tok < v.len && t0 + tok < v.raw - v.n ? row[t0] : 0.0f;
+      };
+      const int u = first_mine(v, it);
+      return Two{get(u), get(u + 2)};
     };
     Keys keys{0.0f, false, false}, next{0.0f, false, false};
-    float old = 0.0f, old_next = 0.0f;
+    Two old{0.0f, 0.0f}, old_next{0.0f, 0.0f};
     if (some) old_next = held_mass(w, 0);
     if (some && !w.few && !convert(0, &next)) failed = true;
     while (some && !failed) {
@@ -716,22 +725,106 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       keys = next;
       old = old_next;
       const int rows = now.n * p.group, base = now.raw - now.n;
-      const int pos0 = now.tile * kTile, pos = pos0 + tok;
-      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
       if (held && !now.same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
       held = now.steps == 1;
-      float* const at = row + pos0;
+      float* const at = row;
       // The next item's K, while the products of this one run.
-      some = walk_next(p, w);
+      some = walk_next(p, w, w.nb);
       if (some) old_next = held_mass(w, item + 1);
-      if (some && !w.few && !convert(item + 1, &next)) {
+      if (some && !w.few && !convert(tile + now.nb, &next)) {
         failed = true;
         break;
       }
+      // (A page outside the pool adds nothing.)
+      auto put = [&](int pos0, float before, bool there, float total) {
+        const int pos = pos0 + tok;
+        if (pos < now.len && (there || pos >= base)) at[pos0] = before + (there ? total : 0.0f);
+      };
+      if (now.few) {
+        if (!now.same) ++ql;
+        const uint32_t st = (ql - 1) % NQ;
+        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
+                        mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const int u0 = first_mine(now, item), mine = u0 >= now.nb ? 0 : (u0 + 2 >= now.nb ? 1 : 2);
+        if (mine > 0) {
+          const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 12));
+          const int* vs = reinterpret_cast<const int*>(ls) + kStep;
+          const int r8 = (rows + 7) & ~7, cols = (3 * r8 + 15) & ~15;
+          const uint32_t t_s = tmem + lane_base + buf * kStep + u0 * cols;
+          const Keys k0 = read_meta(tile + u0), k1 = mine > 1 ? read_meta(tile + u0 + 2) : k0;
+          const int p0 = tile_at(now, u0) * kTile, p1 = mine > 1 ? tile_at(now, u0 + 2) * kTile : p0;
+          float2 acc[2][2] = {};
+          // Eight rows of both tiles.
+          for (int c = 0; c < rows; c += 8) {
+            float x[2][3][8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (u < mine)
+#pragma unroll
+                for (int z = 0; z < 3; ++z) tmem_ld<8>(t_s + 2 * u * cols + z * r8 + c, x[u][z]);
+            const float4 l0 = *reinterpret_cast<const float4*>(ls + c);
+            const float4 l1 = *reinterpret_cast<const float4*>(ls + c + 4);
+            const float4 f0 = *reinterpret_cast<const float4*>(ls + 2 * kStep + c);
+            const float4 f1 = *reinterpret_cast<const float4*>(ls + 2 * kStep + c + 4);
+            const float2 l[4] = {make_float2(l0.x, l0.y), make_float2(l0.z, l0.w),
+                                 make_float2(l1.x, l1.y), make_float2(l1.z, l1.w)};
+            const float2 f[4] = {make_float2(f0.x, f0.y), make_float2(f0.z, f0.w),
+                                 make_float2(f1.x, f1.y), make_float2(f1.z, f1.w)};
+            const float2 w5 = make_float2(0x1p-5f, 0x1p-5f);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (u >= mine) continue;
+#pragma unroll
+              for (int z = 0; z < 3; ++z) tmem_fence<8>(x[u][z]);
+              const float scale = u ? k1.scale : k0.scale;
+              const int pos0 = u ? p1 : p0, pos = pos0 + tok;
+              const float2 ks = make_float2(scale, scale);
+              float2 y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[e] = fma2(make_float2(x[u][2][2 * e], x[u][2][2 * e + 1]), w5,
+                            make_float2(x[u][1][2 * e], x[u][1][2 * e + 1]));
+                y[e] = fma2(y[e], w5, make_float2(x[u][0][2 * e], x[u][0][2 * e + 1]));
+                y[e] = fma2(y[e], mul2(f[e], ks), l[e]);
+              }
+              // Rows that do not see the position; columns behind the rows hold anything.
+              if (pos0 + kTile - 1 > base || c + 8 > rows) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int2 v = *reinterpret_cast<const int2*>(vs + c + 2 * e);
+                  if (pos >= v.x) y[e].x = -INFINITY;
+                  if (pos >= v.y) y[e].y = -INFINITY;
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[u][e & 1] = add2(acc[u][e & 1], make_float2(ex2(y[e].x), ex2(y[e].y)));
+            }
+          }
+          tc_fence_before();
+          auto sum = [&](const float2* a) { return (a[0].x + a[1].x) + (a[0].y + a[1].y); };
+          put(p0, old.a, k0.there, sum(acc[0]));
+          if (mine > 1) put(p1, old.b, k1.there, sum(acc[1]));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
+        ++g;
+        buf = buf + 1 == kNS ? 0 : buf + 1;
+        tile += now.nb;
+        ++item;
+        continue;
+      }
+      const int pos0 = now.tile * kTile, pos = pos0 + tok;
+      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
       float total = 0.0f;
-      // Few rows: the sets take items in turn, else steps in turn. Both wait for
-      // every product and both let its buffer (and Q) go, the one that has nothing to
-      // do there at once: a set that is behind would otherwise miss a phase.
+      // The sets take the steps in turn. Both wait for every product and both let
+      // its buffer and Q go, the one that has nothing to do there at once: a set that
+      // is behind would otherwise miss a phase.
       for (int s = 0; s < now.steps; ++s, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
         if (!now.same) ++ql;
         const uint32_t st = (ql - 1) % NQ;
@@ -743,55 +836,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           failed = true;
           break;
         }
-        if ((int)((now.few ? item : (uint32_t)s) & 1) != set) {
+        float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
+        if ((s & 1) != set) {
           if (lane == 0) {
             mbar_arrive(&bars[kSFree + buf]);
             if (now.steps > 1) mbar_arrive(&bars[kQEmpty + st]);
           }
-          continue;
-        }
-        tc_fence_after();
-        float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-        const uint32_t t_s = tmem + lane_base + buf * kStep;
-        if (now.few) {
-          // The product is done, so K is read: its stage is free.
-          keys = read_meta(item);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_twice(&bars[kKEmpty + item % NK]);
-          const int r8 = (rows + 7) & ~7;
-          const float2 ks = make_float2(keys.scale, keys.scale);
-          for (int c = 0; c < rows; c += 4) {
-            float x[4], y[4], z[4];
-            tmem_ld<4>(t_s + c, x);
-            tmem_ld<4>(t_s + r8 + c, y);
-            tmem_ld<4>(t_s + 2 * r8 + c, z);
-            const float4 l = *reinterpret_cast<const float4*>(ls + c);
-            const float4 f = *reinterpret_cast<const float4*>(ls + 2 * kStep + c);
-            tmem_fence<4>(x);
-            tmem_fence<4>(y);
-            tmem_fence<4>(z);
-            const float2 w5 = make_float2(0x1p-5f, 0x1p-5f);
-            float2 a = fma2(make_float2(z[0], z[1]), w5, make_float2(y[0], y[1]));
-            float2 b = fma2(make_float2(z[2], z[3]), w5, make_float2(y[2], y[3]));
-            a = fma2(a, w5, make_float2(x[0], x[1]));
-            b = fma2(b, w5, make_float2(x[2], x[3]));
-            a = fma2(a, mul2(make_float2(f.x, f.y), ks), make_float2(l.x, l.y));
-            b = fma2(b, mul2(make_float2(f.z, f.w), ks), make_float2(l.z, l.w));
-            if (edge || c + 4 > rows) {
-              // (Columns behind the rows hold anything.)
-              const int4 v = *reinterpret_cast<const int4*>(vs + c);
-              if (pos >= v.x) a.x = -INFINITY;
-              if (pos >= v.y) a.y = -INFINITY;
-              if (pos >= v.z) b.x = -INFINITY;
-              if (pos >= v.w) b.y = -INFINITY;
-            }
-            acc0 = add2(acc0, make_float2(ex2(a.x), ex2(a.y)));
-            acc1 = add2(acc1, make_float2(ex2(b.x), ex2(b.y)));
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
         } else {
+          tc_fence_after();
+          const uint32_t t_s = tmem + lane_base + buf * kStep;
           // Columns of 8. ls holds minus the lse.
           const float2 ks = make_float2(keys.scale, keys.scale);
           auto add8 = [&](const float* x, int c, bool masked) {
@@ -855,33 +908,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
       }
       if (failed) break;
-      if (!now.few) {
-        // Both sets together; a NaN key makes its position NaN.
-        if (keys.nan) total = NAN;
-        const uint32_t slot = summed & 1;
-        bool ok;
-        if (set == 1) {
-          ok = summed < 2 || mbar_wait_long(&bars[kXFree + slot], ((summed >> 1) - 1) & 1u);
-          if (ok) {
-            other[slot * kTile + tok] = total;
-            mbar_arrive(&bars[kXFull + slot]);
-          }
-        } else {
-          ok = mbar_wait_long(&bars[kXFull + slot], (summed >> 1) & 1u);
-          if (ok) {
-            total += other[slot * kTile + tok];
-            mbar_arrive(&bars[kXFree + slot]);
-          }
+      // Both sets together; a NaN key makes its position NaN.
+      if (keys.nan) total = NAN;
+      const uint32_t slot = summed & 1;
+      bool ok;
+      if (set == 1) {
+        ok = summed < 2 || mbar_wait_long(&bars[kXFree + slot], ((summed >> 1) - 1) & 1u);
+        if (ok) {
+          other[slot * kTile + tok] = total;
+          mbar_arrive(&bars[kXFull + slot]);
         }
-        ++summed;
-        if (!__all_sync(0xffffffffu, ok)) {
-          failed = true;
-          break;
+      } else {
+        ok = mbar_wait_long(&bars[kXFull + slot], (summed >> 1) & 1u);
+        if (ok) {
+          total += other[slot * kTile + tok];
+          mbar_arrive(&bars[kXFree + slot]);
+          put(pos0, old.a, keys.there, total);
         }
       }
-      // (A page outside the pool adds nothing.)
-      if (mine(now, item) && pos < now.len && (keys.there || pos >= base))
-        *at = old + (keys.there ? total : 0.0f);
+      ++summed;
+      if (!__all_sync(0xffffffffu, ok)) {
+        failed = true;
+        break;
+      }
+      ++tile;
       ++item;
     }
   }
