@@ -39,9 +39,9 @@
 // by fewer rows.
 //
 // Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: each
-// converts half of the dims, and they take the steps, or with few rows the items,
-// in turn, so that one's exponentials run while the other waits), warp 8 brings K, warp 9 issues the products,
-// warps 10 and 11 bring Q, lse and the pieces of q.
+// converts half of the dims, and they take the steps, or with few rows the tiles, in
+// turn, so that one's exponentials run while the other waits), warp 8 brings K, warp
+// 9 issues the products, warp 10 brings Q, warp 11 lse and the pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -57,10 +57,12 @@ namespace {
 constexpr int kTile = 128;                 // positions of an item
 constexpr int kStep = 128;                 // query rows of a step
 constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
-constexpr int kThreads = 32 * (kQWarp + kQWarps);   // (12 warps: 168 registers a thread)
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11;
+constexpr int kThreads = 32 * (kLWarp + 1);   // (12 warps: 168 registers a thread)
 constexpr int kMetaSlots = 32;
 constexpr int kNS = 3;                     // S buffers
+constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
+                                           // when a step is summed, Q once its product is done)
 constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 
@@ -68,12 +70,12 @@ template <int DIM>
 struct Layout {
   static constexpr int kKBytes = kTile * DIM;
   static constexpr int kQBytes = kStep * DIM * 2;
-  static constexpr int kNK = 6;                     // stages
-  static constexpr int kNQ = DIM == 128 ? 3 : 4;
+  static constexpr int kNK = DIM == 128 ? 5 : 8;    // stages
+  static constexpr int kNQ = DIM == 128 ? 4 : 6;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kNK * kKBytes;
-  static constexpr int kLse = kQ + kNQ * kQBytes;   // per stage: 128 lse, visible, factors
-  static constexpr int kBars = kLse + kNQ * kStep * 12;
+  static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
+  static constexpr int kBars = kLse + kNL * kStep * 12;
   static constexpr int kMeta = kBars + 64 * 8;                // kMetaSlots x float4
   static constexpr int kOther = kMeta + kMetaSlots * 16;      // sums of warps 4-7, two slots
   static constexpr int kMisc = kOther + 2 * kTile * 4;        // tmem slot, start of work, scan
@@ -88,18 +90,19 @@ struct Layout {
 };
 
 enum Bar {
-  kKFull = 0,       // K landed (<= 6)
+  kKFull = 0,       // <= 8: K landed
   kKEmpty = 8,      // K converted, or its product done
-  kQFull = 16,      // Q landed (<= 4)
-  kLFull = 20,      // lse written
-  kQEmpty = 24,     // product done and lse read
-  kAFull = 28,      // 2: A written
-  kSFull = 30,      // kNS: S ready
-  kSFree = 33,      // kNS: S read
-  kXFull = 36,      // 2: the other set's sums written
-  kXFree = 38,      // 2: read
-  kDrain = 40,
-  kNumBars = 41
+  kQFull = 16,      // <= 8: Q landed
+  kQEmpty = 24,     // product done
+  kLFull = 32,      // kNL: lse written
+  kLEmpty = 40,     // lse read
+  kAFull = 48,      // 2: A written
+  kSFull = 50,      // kNS: S ready
+  kSFree = 53,      // kNS: S read
+  kXFull = 56,      // 2: the other set's sums written
+  kXFree = 58,      // 2: read
+  kDrain = 60,
+  kNumBars = 61
 };
 
 struct Params {
@@ -297,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if (i >= kAFull && i < kAFull + 2) n = kSum;
-      if (i >= kLFull && i < kLFull + NQ) n = 32 * kQWarps;
-      if (i >= kQEmpty && i < kQEmpty + NQ) n = 1 + kSumWarps;
+      if (i >= kLFull && i < kLFull + kNL) n = 32;
+      if (i >= kLEmpty && i < kLEmpty + kNL) n = kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
       if (i >= kXFull && i < kXFree + 2) n = kSum / 2;
       mbar_init(&bars[i], n);
@@ -477,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         if (!w.same) ++ql;
         const uint32_t st = (ql - 1) % NQ, ph = ((ql - 1) / NQ) & 1u;
         ok = ok && (w.same || (mbar_wait_long(&bars[kQFull + st], ph) &&
-                               (!w.few || mbar_wait_long(&bars[kLFull + st], ph)))) &&
+                               (!w.few || mbar_wait_long(&bars[kLFull + (ql - 1) % kNL],
+                                                         ((ql - 1) / kNL) & 1u)))) &&
              (g < kNS || mbar_wait_long(&bars[kSFree + buf], (g / kNS - 1) & 1u));
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
@@ -531,120 +535,166 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     __syncwarp();
     if (!mbar_wait_long(&bars[kDrain], 0)) failed = true;
     __syncwarp();
-  } else if (warp >= kQWarp) {
-    // --------------------------------------- Q, lse, and pieces of few rows
-    constexpr int T = 32 * kQWarps, N = kStep / T;     // a thread's rows of a step: t, t + T
-    const int t = tid - 32 * kQWarp;
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------------------ Q
+    const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
+    uint32_t ql = 0;
+    while (some && !failed) {
+      if (!w.same) {
+        for (int s = 0; s < w.steps; ++s, ++ql) {
+          const uint32_t st = ql % NQ;
+          if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
+                                                                 (ql / NQ - 1) & 1u))) {
+            failed = true;
+            break;
+          }
+          if (lane == 0) {
+            if (w.few) {
+              mbar_arrive(&bars[kQFull + st]);   // (the pieces come with the lse)
+            } else {
+              const Step x = step_of(p, w, s);
+              mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
+#pragma unroll
+              for (int b = 0; b < DIM / 64; ++b)
+                tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
+                              w.kvh * p.group + x.head, (int)w.t0 + x.token, &bars[kQFull + st]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // (Few rows serve all tiles of their head.)
+      if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
+    }
+    if (lane == 0)   // every copy has landed before the CTA can exit
+      for (uint32_t i = ql > NQ ? ql - NQ : 0; i < ql; ++i)
+        if (!mbar_wait_long(&bars[kQFull + i % NQ], (i / NQ) & 1u)) failed = true;
+    __syncwarp();
+  } else if (warp == kLWarp) {
+    // --------------------------------------------- lse, and pieces of few rows
+    constexpr int N = kStep / 32;              // rows of a lane: lane, lane + 32, ...
+    constexpr int D = 4;                       // steps whose lse is read at once
     int t_token[N], t_head[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      t_token[i] = (t + i * T) / p.step_heads;
-      t_head[i] = (t + i * T) % p.step_heads;
+      t_token[i] = (lane + 32 * i) / p.step_heads;
+      t_head[i] = (lane + 32 * i) % p.step_heads;
     }
-    const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
     uint32_t ql = 0;
     while (some && !failed) {
       if (w.same) {
         some = walk_next(p, w, w.nb);
         continue;
       }
-      const int seen = w.raw - w.n + 1;               // by token 0
+      const int seen = w.raw - w.n + 1;        // by token 0
       const float* lse0 = p.lse + w.t0 * p.heads + w.kvh * p.group;
-      // The lse and the length seen of this thread's rows, read a step ahead.
-      float l[N];
-      int vis[N];
-      auto look = [&](int s) {
-        const Step x = step_of(p, w, s);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int row = t + i * T;
-          const int token = w.few ? row / p.group : x.token + t_token[i];
-          const int head = w.few ? row % p.group : x.head + t_head[i];
-          l[i] = -INFINITY;
-          vis[i] = INT_MIN;
-          if (row < (w.few ? w.n * p.group : x.rows)) {
-            l[i] = lse0[(int64_t)token * p.heads + head];
-            vis[i] = seen + token;
-          }
-        }
+      // A row that there is not sees nothing, and one of -inf adds nothing.
+      auto put = [&](uint32_t slot, int i, bool in, int token, float l) {
+        float* ls = reinterpret_cast<float*>(smem + LY::kLse + slot * (kStep * 12)) + lane + 32 * i;
+        ls[0] = in && l != -INFINITY ? -l * kLog2e : -INFINITY;
+        reinterpret_cast<int*>(ls)[kStep] = in ? seen + token : INT_MIN;
       };
-      look(0);
-      for (int s = 0; s < w.steps; ++s, ++ql) {
-        const uint32_t st = ql % NQ;
+      auto wait_slot = [&] {
+        return __all_sync(0xffffffffu, ql < kNL || mbar_wait_long(&bars[kLEmpty + ql % kNL],
+                                                                  (ql / kNL - 1) & 1u));
+      };
+      if (w.few) {
+        const uint32_t st = ql % NQ, sl = ql % kNL;
+        const int rows = w.n * p.group, r8 = (rows + 7) & ~7;
         if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
-                                                               (ql / NQ - 1) & 1u))) {
+                                                               (ql / NQ - 1) & 1u)) ||
+            !wait_slot()) {
           failed = true;
           break;
         }
-        if (t == 0) {
-          if (w.few) {
-            mbar_arrive(&bars[kQFull + st]);   // (the pieces come with the lse)
-          } else {
-            const Step x = step_of(p, w, s);
-            mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
-#pragma unroll
-            for (int b = 0; b < DIM / 64; ++b)
-              tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
-                            w.kvh * p.group + x.head, (int)w.t0 + x.token, &bars[kQFull + st]);
-          }
-        }
-        float* ls = reinterpret_cast<float*>(smem + LY::kLse + st * (kStep * 12));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          // (A row of -inf adds nothing.)
-          ls[t + i * T] = l[i] == -INFINITY ? -INFINITY : -l[i] * kLog2e;
-          reinterpret_cast<int*>(ls)[kStep + t + i * T] = vis[i];
+          const int row = lane + 32 * i, token = row / p.group;
+          const bool in = row < rows;
+          put(sl, i, in, token, in ? lse0[(int64_t)token * p.heads + row % p.group] : 0.0f);
         }
-        if (w.few) {
-          // A warp a row, in turn. (What lies behind the rows is anything: columns
-          // of the product that nobody reads.)
-          constexpr int E = DIM / 32;
-          const int rows = w.n * p.group, r8 = (rows + 7) & ~7;
-          uint8_t* q8 = smem + LY::kQ + st * LY::kQBytes;
-#pragma unroll 4
-          for (int r = warp - kQWarp; r < rows; r += kQWarps) {
-            const __nv_bfloat16* src = p.q + (w.t0 + r / p.group) * p.q_stride +
-                                       ((int64_t)w.kvh * p.group + r % p.group) * DIM + lane * E;
-            float x[E], a = 0.0f;
-            bool nan = false;
+        // (What lies behind the rows is anything: columns of the product that nobody
+        // reads.)
+        constexpr int E = DIM / 32;
+        uint8_t* q8 = smem + LY::kQ + st * LY::kQBytes;
+        float* factor = reinterpret_cast<float*>(smem + LY::kLse + sl * (kStep * 12)) + 2 * kStep;
+        const __nv_bfloat16* q0 = p.q + w.t0 * p.q_stride + (int64_t)w.kvh * p.group * DIM + lane * E;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          float x[8][E];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int r = r0 + u < rows ? r0 + u : rows - 1;
+            const __nv_bfloat16* src = q0 + (r / p.group) * p.q_stride + (r % p.group) * DIM;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
               const uint32_t v = reinterpret_cast<const uint32_t*>(src)[e / 2];
-              x[e] = __uint_as_float(v << 16);
-              x[e + 1] = __uint_as_float(v & 0xFFFF0000u);
+              x[u][e] = __uint_as_float(v << 16);
+              x[u][e + 1] = __uint_as_float(v & 0xFFFF0000u);
             }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int r = r0 + u;
+            float a = 0.0f;
+            bool nan = false;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-              a = fmaxf(a, fabsf(x[e]));
-              nan |= x[e] != x[e];
+              a = fmaxf(a, fabsf(x[u][e]));
+              nan |= x[u][e] != x[u][e];
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
             nan = __any_sync(0xffffffffu, nan) || a == INFINITY;
+            if (r >= rows) continue;
             const int k = q_exponent(a);
             const float up = pow2f(k);
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-              float u0 = x[e] * up, u1 = x[e + 1] * up;
+              float u0 = x[u][e] * up, u1 = x[u][e + 1] * up;
 #pragma unroll
               for (int z = 0; z < 3; ++z)
                 *reinterpret_cast<uint16_t*>(q8 + swz<DIM>(z * r8 + r, lane * E + e)) =
                     piece(u0, u1);
             }
-            if (lane == 0) ls[2 * kStep + r] = nan ? NAN : pow2f(-k);
+            if (lane == 0) factor[r] = nan ? NAN : pow2f(-k);
           }
-          fence_proxy_async_smem();
         }
-        mbar_arrive(&bars[kLFull + st]);
-        if (s + 1 < w.steps) look(s + 1);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kLFull + sl]);
+        ++ql;
+        some = walk_next(p, w, w.tiles - w.j);   // (they serve all tiles of their head)
+        continue;
       }
-      // (Few rows serve all tiles of their head.)
-      if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
+      for (int s0 = 0; s0 < w.steps && !failed; s0 += D) {
+        float l[D][N];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const Step x = step_of(p, w, s0 + d);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            l[d][i] = s0 + d < w.steps && lane + 32 * i < x.rows
+                          ? lse0[(int64_t)(x.token + t_token[i]) * p.heads + x.head + t_head[i]]
+                          : 0.0f;
+        }
+        for (int d = 0; d < D && s0 + d < w.steps; ++d, ++ql) {
+          if (!wait_slot()) {
+            failed = true;
+            break;
+          }
+          const Step x = step_of(p, w, s0 + d);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            float v = l[0][i];
+#pragma unroll
+            for (int e = 1; e < D; ++e)
+              if (d == e) v = l[e][i];
+            put(ql % kNL, i, lane + 32 * i < x.rows, x.token + t_token[i], v);
+          }
+          mbar_arrive(&bars[kLFull + ql % kNL]);
+        }
+      }
+      if (!failed) some = walk_next(p, w, 1);
     }
-    if (t == 0)   // every copy has landed before the CTA can exit
-      for (uint32_t i = ql > NQ ? ql - NQ : 0; i < ql; ++i)
-        if (!mbar_wait_long(&bars[kQFull + i % NQ], (i / NQ) & 1u)) failed = true;
-    __syncwarp();
   } else {
     // --------------------------------------------------- convert and sum
     const int quad = warp & 3, set = warp >> 2;
@@ -725,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       keys = next;
       old = old_next;
       const int rows = now.n * p.group, base = now.raw - now.n;
-      if (held && !now.same && lane == 0) mbar_arrive(&bars[kQEmpty + (ql - 1) % NQ]);
+      if (held && !now.same && lane == 0) mbar_arrive(&bars[kLEmpty + (ql - 1) % kNL]);
       held = now.steps == 1;
       float* const at = row;
       // The next item's K, while the products of this one run.
@@ -742,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       };
       if (now.few) {
         if (!now.same) ++ql;
-        const uint32_t st = (ql - 1) % NQ;
-        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
+        const uint32_t sl = (ql - 1) % kNL;
+        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u)) &&
                         mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
@@ -752,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         tc_fence_after();
         const int u0 = first_mine(now, item), mine = u0 >= now.nb ? 0 : (u0 + 2 >= now.nb ? 1 : 2);
         if (mine > 0) {
-          const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 12));
+          const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
           const int* vs = reinterpret_cast<const int*>(ls) + kStep;
           const int r8 = (rows + 7) & ~7, cols = (3 * r8 + 15) & ~15;
           const uint32_t t_s = tmem + lane_base + buf * kStep + u0 * cols;
@@ -823,14 +873,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
       float total = 0.0f;
       // The sets take the steps in turn. Both wait for every product and both let
-      // its buffer and Q go, the one that has nothing to do there at once: a set that
+      // its buffer and lse go, the one that has nothing to do there at once: a set that
       // is behind would otherwise miss a phase.
       for (int s = 0; s < now.steps; ++s, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
         if (!now.same) ++ql;
-        const uint32_t st = (ql - 1) % NQ;
-        const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + st * (kStep * 12));
+        const uint32_t sl = (ql - 1) % kNL;
+        const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
-        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + st], ((ql - 1) / NQ) & 1u)) &&
+        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u)) &&
                         mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
@@ -840,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         if ((s & 1) != set) {
           if (lane == 0) {
             mbar_arrive(&bars[kSFree + buf]);
-            if (now.steps > 1) mbar_arrive(&bars[kQEmpty + st]);
+            if (now.steps > 1) mbar_arrive(&bars[kLEmpty + sl]);
           }
         } else {
           tc_fence_after();
@@ -902,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           }
           if (now.steps > 1) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kQEmpty + st]);
+            if (lane == 0) mbar_arrive(&bars[kLEmpty + sl]);
           }
         }
         total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
