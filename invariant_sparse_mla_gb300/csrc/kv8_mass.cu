@@ -10,8 +10,9 @@
 // step), nothing is reduced across threads, and the order of the additions follows
 // from the request alone.
 //
-// An item is (request, kv head, 128 positions), its codes brought by TMA. Two
-// forms, by the request's number of rows R = tokens * heads of the group:
+// Work goes by tiles of 128 positions of a (request, kv head), their codes brought
+// by TMA. Two forms, by the request's number of rows R = tokens * heads of the
+// group:
 //
 // - Few rows (R <= 40): K is multiplied as it lies, on the 8-bit tensor cores,
 //   with q as three E4M3 pieces, each a column of its own under the row's power of
@@ -23,14 +24,14 @@
 //   are paid once and a thread has two positions to work on. The bound is HBM, dim
 //   bytes a position and head.
 //
-// - More: K becomes bf16 once per item (an E4M3 code has 4 significant bits and an
-//   exponent that bf16 holds: exponent and mantissa bits are placed under bf16's,
-//   subnormals included, and multiplied by 2^120) and lies in TMEM as the A
-//   operand, two buffers; the query rows stream past it in steps of up to 128, by
-//   TMA as they lie, and both operands are exact. S has three buffers of 128
-//   columns, so the product of a step runs under the exponentials of the two before.
-//   The bound is the tensor core (2 dim flops a position and row) and the
-//   exponentials beside it.
+// - More: K becomes bf16 (an E4M3 code has 4 significant bits and an exponent that
+//   bf16 holds: exponent and mantissa bits are placed under bf16's, subnormals
+//   included, and multiplied by 2^120) and lies in TMEM as the A operand, two tiles
+//   for an item; the query rows stream past both in steps of up to 128, by TMA as
+//   they lie, and both operands are exact. S has three buffers of 128 columns, so
+//   the products run under the exponentials of those before. (With one tile an item
+//   the rows' 32 KB a step were the bound: 9.6 TB/s from L2.) The bound is the tensor
+//   core (2 dim flops a position and row) and the exponentials beside it.
 //
 // Sums are fp32: of a step first, then over the steps.
 //
@@ -38,10 +39,10 @@
 // request's tiles are taken from both ends in turn, since the last ones are seen
 // by fewer rows.
 //
-// Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: each
-// converts half of the dims, and they take the steps, or with few rows the tiles, in
-// turn, so that one's exponentials run while the other waits), warp 8 brings K, warp
-// 9 issues the products, warp 10 brings Q, warp 11 lse and the pieces of q.
+// Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: of
+// two tiles each has one, so that one's exponentials run while the other waits),
+// warp 8 brings K, warp 9 issues the products, warp 10 brings Q, warp 11 lse and the
+// pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -77,12 +78,11 @@ struct Layout {
   static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
   static constexpr int kBars = kLse + kNL * kStep * 12;
   static constexpr int kMeta = kBars + 64 * 8;                // kMetaSlots x float4
-  static constexpr int kOther = kMeta + kMetaSlots * 16;      // sums of warps 4-7, two slots
-  static constexpr int kMisc = kOther + 2 * kTile * 4;        // tmem slot, start of work, scan
+  static constexpr int kMisc = kMeta + kMetaSlots * 16;       // tmem slot, start of work, scan
   static constexpr int kEnd = kMisc + 32 + 8 * (kThreads / 32);
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  // TMEM columns: the S buffers, then A0, A1.
+  // TMEM columns: the S buffers, then K of two tiles.
   static constexpr int kA = kNS * kStep;
   static constexpr int kACols = DIM / 2;
   static constexpr uint32_t kCols = 512;
@@ -96,13 +96,11 @@ enum Bar {
   kQEmpty = 24,     // product done
   kLFull = 32,      // kNL: lse written
   kLEmpty = 40,     // lse read
-  kAFull = 48,      // 2: A written
+  kAFull = 48,      // 2: A of a tile written
   kSFull = 50,      // kNS: S ready
   kSFree = 53,      // kNS: S read
-  kXFull = 56,      // 2: the other set's sums written
-  kXFree = 58,      // 2: read
-  kDrain = 60,
-  kNumBars = 61
+  kDrain = 56,
+  kNumBars = 57
 };
 
 struct Params {
@@ -128,13 +126,17 @@ struct Walk {
   int item_r, item_kvh;  // of the last item loaded
   int raw, len, n;       // lens[r], clamped, new tokens
   int64_t t0;            // first token
-  int tiles, cost;       // cost of an item
+  int tiles;
   bool few;              // multiplied in pieces
-  int batch, nb;         // most tiles of an item, and those of the present one
-  int i, items;          // present item, items of the request
-  int j;                 // its number among its head's tiles
-  int kvh, tile;         // of the present item
-  int first;             // first token that sees the tile (few: 0)
+  // Units: a tile with few rows, else two (the last may be one). An item is a unit,
+  // or with few rows up to `batch` of them.
+  int units, cost;       // of a head; cost of one
+  int batch;
+  int i, items;          // first unit of the present item; units of the request
+  int j;                 // its number among its head's
+  int kvh, tile;         // of the present item: its first tile
+  int nb;                // its tiles
+  int first;             // first token that sees them (few: 0)
   int steps;
   bool same;             // one step, of the rows that the item before it had in its one step
 };
@@ -153,19 +155,21 @@ __device__ __forceinline__ void load_request(const Params& p, int64_t r, Walk& w
   const int64_t n = start_of(p, r + 1) - w.t0;
   w.n = n < 0 || w.len == 0 ? 0 : (int)n;
   w.tiles = w.n > 0 ? (w.len + kTile - 1) / kTile : 0;
-  w.items = w.tiles * p.c.kv_heads;
   const int rows = w.n * p.group;   // (below 2^31 - 256)
   // (The pieces stay clear of the rows of a stage that no step writes.)
   w.few = rows <= kFewRows && 3 * ((rows + 7) & ~7) <= p.step_tokens * p.step_heads;
   // As many tiles as S columns of one buffer: products of 32 columns with up to 8
   // rows, 48 with 16.
   w.batch = !w.few || rows > 16 ? 1 : (rows > 8 ? 2 : 4);
-  w.cost = w.few ? 1 : 1 + (w.n + p.step_tokens - 1) / p.step_tokens * p.chunks;
+  w.units = w.few ? w.tiles : (w.tiles + 1) / 2;
+  w.items = w.units * p.c.kv_heads;
+  w.cost = w.few ? 1 : 2 + 2 * ((w.n + p.step_tokens - 1) / p.step_tokens) * p.chunks;
 }
 
-// A head's tiles from both ends in turn.
+// A head's units from both ends in turn: the first tile of the j-th.
 __device__ __forceinline__ int tile_of(const Walk& w, int j) {
-  return j & 1 ? w.tiles - 1 - (j >> 1) : j >> 1;
+  const int u = j & 1 ? w.units - 1 - (j >> 1) : j >> 1;
+  return w.few ? u : 2 * u;
 }
 
 __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
@@ -175,7 +179,7 @@ __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
     w.same = one;
     w.first = 0;
     w.steps = 1;
-    const int left = w.tiles - w.j < w.batch ? w.tiles - w.j : w.batch;
+    const int left = w.units - w.j < w.batch ? w.units - w.j : w.batch;
     w.nb = w.end - w.at < left ? (int)(w.end - w.at) : left;   // (cost 1 each)
   } else {
     // Token i sees position p if p <= base + i.
@@ -184,7 +188,7 @@ __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
     w.first = first > 0 ? (int)first : 0;
     w.steps = (w.n - w.first + p.step_tokens - 1) / p.step_tokens * p.chunks;
     w.same = one && w.steps == 1 && before == w.first;
-    w.nb = 1;
+    w.nb = w.tiles - w.tile < 2 ? w.tiles - w.tile : 2;
   }
   w.item_r = w.r;
   w.item_kvh = w.kvh;
@@ -221,13 +225,14 @@ __device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
   load_item(p, w);
   return true;
 }
-// `items` in tiles: those of the present item, or more.
-__device__ __forceinline__ bool walk_next(const Params& p, Walk& w, int items) {
-  w.at += (int64_t)items * w.cost;
-  w.i += items;
-  w.j += items;
-  while (w.j >= w.tiles && w.i < w.items) {
-    w.j -= w.tiles;
+// Moves on by a number of units: those of the present item, or more.
+__device__ __forceinline__ int item_units(const Walk& w) { return w.few ? w.nb : 1; }
+__device__ __forceinline__ bool walk_next(const Params& p, Walk& w, int units) {
+  w.at += (int64_t)units * w.cost;
+  w.i += units;
+  w.j += units;
+  while (w.j >= w.units && w.i < w.items) {
+    w.j -= w.units;
     ++w.kvh;
   }
   if (w.at >= w.end) return false;
@@ -290,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LY::kBars);
   float4* meta = reinterpret_cast<float4*>(smem + LY::kMeta);
-  float* other = reinterpret_cast<float*>(smem + LY::kOther);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
   int64_t* start_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 8);   // request, cost before it
   int64_t* scan_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 32);
@@ -299,11 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if (i >= kAFull && i < kAFull + 2) n = kSum;
+      if (i >= kAFull && i < kAFull + 2) n = kSum / 2;
       if (i >= kLFull && i < kLFull + kNL) n = 32;
       if (i >= kLEmpty && i < kLEmpty + kNL) n = kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
-      if (i >= kXFull && i < kXFree + 2) n = kSum / 2;
       mbar_init(&bars[i], n);
     }
     mbar_fence_init();
@@ -377,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     w.steps = 0;           // no item before the first
     w.i = (int)((lo - start_s[1] + w.cost - 1) / w.cost);
     w.at = start_s[1] + (int64_t)w.i * w.cost;
-    w.kvh = w.i / w.tiles;
-    w.j = w.i % w.tiles;
+    w.kvh = w.i / w.units;
+    w.j = w.i % w.units;
     some = walk_settle(p, w);
   }
 
@@ -388,22 +391,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const int none = (int)(p.c.num_pages * 2 * p.c.kv_heads * kPage);   // a row past the pool: zeros
     int err_bits = 0;
     uint32_t g = 0, issued = 0;
-    // Lanes 2 e and 2 e + 1 look up the pages of the e-th item from w.i on, 16
-    // items of a request at once, and the next 16 while these are issued.
+    // The pages of up to 16 units of a request (8 of two tiles) are looked up at
+    // once, a page a lane, and the next ones while these are brought.
     struct Lookup {
-      int count, y;
+      int count, pages;      // units, and page places of each
+      int y;
       float ks;
+      bool there;            // a place of a tile that there is
     };
     auto look = [&](const Walk& v) {
       Lookup k;
+      k.pages = v.few ? 2 : 4;
+      const int most = 32 / k.pages;
       const int64_t left = (v.end - v.at + v.cost - 1) / v.cost;
-      k.count = v.items - v.i < 16 ? v.items - v.i : 16;
+      k.count = v.items - v.i < most ? v.items - v.i : most;
       if (left < k.count) k.count = (int)left;
       k.y = none;
       k.ks = 0.0f;
-      if (lane / 2 < k.count) {
-        const int i = v.i + lane / 2, kvh = i / v.tiles;
-        const int b = 2 * tile_of(v, i - kvh * v.tiles) + (lane & 1);
+      k.there = false;
+      const int e = v.few ? lane >> 1 : lane >> 2, at = v.few ? lane & 1 : lane & 3;
+      if (e < k.count) {
+        const int i = v.i + e, kvh = i / v.units;
+        const int tile = tile_of(v, i - kvh * v.units) + (at >> 1);
+        const int b = 2 * tile + (at & 1);
+        k.there = tile < v.tiles;
         if ((int64_t)b * kPage < v.len) {
           const int64_t page = p.c.block_table[(int64_t)v.r * p.c.bt_stride + b];
           if (page >= 0 && page < p.c.num_pages) {
@@ -423,11 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const Lookup now = next;
       some = walk_next(p, w, now.count);
       if (some) next = look(w);
-      for (int e = 0; e < now.count; ++e, ++g) {
-        const int y0 = __shfl_sync(0xffffffffu, now.y, 2 * e);
-        const int y1 = __shfl_sync(0xffffffffu, now.y, 2 * e + 1);
-        const float k0 = __shfl_sync(0xffffffffu, now.ks, 2 * e);
-        const float k1 = __shfl_sync(0xffffffffu, now.ks, 2 * e + 1);
+      for (int e = 0; e < now.count * now.pages; e += 2) {
+        if (!__shfl_sync(0xffffffffu, (int)now.there, e)) continue;
+        const int y0 = __shfl_sync(0xffffffffu, now.y, e);
+        const int y1 = __shfl_sync(0xffffffffu, now.y, e + 1);
+        const float k0 = __shfl_sync(0xffffffffu, now.ks, e);
+        const float k1 = __shfl_sync(0xffffffffu, now.ks, e + 1);
         bool ok = true;
         if (lane == 0) {
           const int st = (int)(g % NK);
@@ -442,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             issued = g + 1;
           }
         }
+        ++g;
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
@@ -459,77 +472,117 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const uint64_t q8_desc = tile_desc<DIM>(sbase + LY::kQ);
     const uint64_t k_desc = tile_desc<DIM>(sbase + LY::kK);
     const bool leader = elect_one();
-    // Tiles, converted ones, steps (of S buffers) and loads of Q so far: an item of
-    // one step may use the load of the one before it, which is let go when the
-    // next comes.
-    uint32_t tile = 0, conv = 0, g = 0, buf = 0, ql = 0;
-    bool held = false;
-    while (some && !failed) {
-      bool ok = true;
-      if (!w.few) {
-        ok = mbar_wait_long(&bars[kAFull + (conv & 1)], (conv >> 1) & 1u);
-        ++conv;
-        if (lane == 0) mbar_arrive(&bars[kKEmpty + tile % NK]);   // K is read
-        ++tile;
+    // The loop runs on values from one lane (a shuffle): the compiler sees that they
+    // are uniform then, keeps them and the descriptors in uniform registers, and
+    // the warp gets to the next product in a third of a product's time instead of two
+    // of them, which was the bound.
+    auto uni = [](auto x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t t_d = uni(tmem), bar0 = uni(smem_u32(bars));
+    // A ring's place and phase.
+    struct Ring {
+      uint32_t at = 0, phase = 0;
+    };
+    auto next = [](Ring& r, uint32_t n) {
+      if (++r.at == n) {
+        r.at = 0;
+        r.phase ^= 1u;
       }
-      if (held && !w.same) {
-        if (leader) mma_commit(&bars[kQEmpty + (ql - 1) % NQ]);
+    };
+    auto wait = [&](int bar, uint32_t at, uint32_t phase) {
+      return mbar_wait_at(bar0 + (uint32_t)(bar + at) * 8u, phase);
+    };
+    auto commit = [&](int bar, uint32_t at) { mma_commit_at(bar0 + (uint32_t)(bar + at) * 8u); };
+    // An item of one step may use the load of Q of the one before it (`held`), which
+    // is let go when the next comes. `phases`: bit u is that of place u's tiles.
+    // (A buffer's first use waits for nothing: the phase before the first is over.)
+    Ring tile, s_free, load, lse;
+    uint32_t phases = 0, held_at = 0;
+    s_free.phase = 1u;
+    bool held = false, on = uni((int)some) != 0;
+    while (on) {
+      const int steps = uni(w.steps), nb = uni(w.nb), few = uni((int)w.few), same = uni((int)w.same);
+      const int rows = uni(w.n * p.group);
+      bool ok = true;
+      if (held && !same) {
+        if (leader) commit(kQEmpty, held_at);
         __syncwarp();
       }
-      for (int s = 0; s < w.steps; ++s, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
-        if (!w.same) ++ql;
-        const uint32_t st = (ql - 1) % NQ, ph = ((ql - 1) / NQ) & 1u;
-        ok = ok && (w.same || (mbar_wait_long(&bars[kQFull + st], ph) &&
-                               (!w.few || mbar_wait_long(&bars[kLFull + (ql - 1) % kNL],
-                                                         ((ql - 1) / kNL) & 1u)))) &&
-             (g < kNS || mbar_wait_long(&bars[kSFree + buf], (g / kNS - 1) & 1u));
-        if (!__all_sync(0xffffffffu, ok)) {
-          failed = true;
-          break;
+      if (few) {
+        // One buffer of S for all tiles of the item.
+        const int n = (3 * ((rows + 7) & ~7) + 15) & ~15;
+        const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
+        if (!same) {
+          ok = wait(kQFull, load.at, load.phase) && wait(kLFull, lse.at, lse.phase);
+          held_at = load.at;
+          next(load, NQ);
+          next(lse, kNL);
         }
-        tc_fence_after();
-        if (w.few) {
-          const int n = (3 * ((w.n * p.group + 7) & ~7) + 15) & ~15;
-          const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
-          const uint64_t b = q8_desc + (uint64_t)((st * LY::kQBytes) >> 4);
-          for (int u = 0; u < w.nb; ++u, ++tile) {
-            const uint32_t kst = tile % NK;
-            if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kKFull + kst], (tile / NK) & 1u))) {
-              failed = true;
-              break;
+        ok = wait(kSFree, s_free.at, s_free.phase) && ok;
+        const uint64_t b = q8_desc + (uint64_t)(held_at * (LY::kQBytes >> 4));
+        for (int u = 0; u < nb; ++u) {
+          ok = wait(kKFull, tile.at, tile.phase) && ok;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t a = k_desc + (uint64_t)(tile.at * (LY::kKBytes >> 4));
+#pragma unroll
+            for (int k = 0; k < DIM / 32; ++k)
+              mma_f8_ss(t_d + s_free.at * kStep + u * n, a + ((k * 32) >> 4), b + ((k * 32) >> 4),
+                        idesc, k > 0 ? 1u : 0u);
+            commit(kKEmpty, tile.at);
+          }
+          __syncwarp();
+          next(tile, NK);
+        }
+        if (leader) commit(kSFull, s_free.at);
+        __syncwarp();
+        next(s_free, kNS);
+      } else {
+        for (int s = 0; s < steps; ++s) {
+          if (!same) {
+            ok = wait(kQFull, load.at, load.phase) && ok;
+            held_at = load.at;
+            next(load, NQ);
+            next(lse, kNL);
+          }
+          const int n = s + 1 < steps && p.chunks == 1 ? (capacity + 15) & ~15
+                                                       : uni((step_of(p, w, s).rows + 15) & ~15);
+          const uint32_t idesc = make_idesc_bf16(kTile, n, 0, 0);
+          const uint64_t b = q_desc + (uint64_t)(held_at * (LY::kQBytes >> 4));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (u >= nb) break;
+            ok = wait(kSFree, s_free.at, s_free.phase) && ok;
+            if (s == 0) {
+              // K of the tile is in TMEM: its stage is free.
+              ok = wait(kAFull, u, (phases >> u) & 1u) && ok;
+              if (lane == 0) mbar_arrive(&bars[kKEmpty + tile.at]);
+              phases ^= 1u << u;
+              next(tile, NK);
             }
             tc_fence_after();
             if (leader) {
-              const uint64_t a = k_desc + (uint64_t)((kst * LY::kKBytes) >> 4);
 #pragma unroll
-              for (int k = 0; k < DIM / 32; ++k)
-                mma_f8_ss(tmem + buf * kStep + u * n, a + ((k * 32) >> 4), b + ((k * 32) >> 4),
-                          idesc, k > 0 ? 1u : 0u);
-              mma_commit(&bars[kKEmpty + kst]);
+              for (int k = 0; k < DIM / 16; ++k)
+                mma_f16_ts(t_d + s_free.at * kStep, t_d + LY::kA + u * LY::kACols + 8 * k,
+                           b + (((k >> 2) * (kStep * 128) + (k & 3) * 32) >> 4), idesc,
+                           k > 0 ? 1u : 0u);
+              commit(kSFull, s_free.at);
             }
             __syncwarp();
+            next(s_free, kNS);
           }
-          if (failed) break;
-          if (leader) mma_commit(&bars[kSFull + buf]);
-        } else {
-          const int n = (step_of(p, w, s).rows + 15) & ~15;
-          if (leader) {
-            const uint32_t idesc = make_idesc_bf16(kTile, n, 0, 0);
-            const uint64_t b = q_desc + (uint64_t)((st * LY::kQBytes) >> 4);
-            const uint32_t a = tmem + LY::kA + ((conv - 1) & 1) * LY::kACols;
-#pragma unroll
-            for (int k = 0; k < DIM / 16; ++k)
-              mma_f16_ts(tmem + buf * kStep, a + 8 * k,
-                         b + (((k >> 2) * (kStep * 128) + (k & 3) * 32) >> 4), idesc,
-                         k > 0 ? 1u : 0u);
-            if (w.steps > 1) mma_commit(&bars[kQEmpty + st]);
-            mma_commit(&bars[kSFull + buf]);
-          }
+          if (leader && steps > 1) commit(kQEmpty, held_at);
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, ok)) break;
         }
-        __syncwarp();
       }
-      held = w.steps == 1;
-      if (!failed) some = walk_next(p, w, w.nb);
+      if (!__all_sync(0xffffffffu, ok)) {
+        failed = true;
+        break;
+      }
+      held = steps == 1;
+      some = walk_next(p, w, item_units(w));
+      on = uni((int)some) != 0;
     }
     if (leader) mma_commit(&bars[kDrain]);
     __syncwarp();
@@ -564,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         }
       }
       // (Few rows serve all tiles of their head.)
-      if (!failed) some = walk_next(p, w, w.few ? w.tiles - w.j : 1);
+      if (!failed) some = walk_next(p, w, w.few ? w.units - w.j : 1);
     }
     if (lane == 0)   // every copy has landed before the CTA can exit
       for (uint32_t i = ql > NQ ? ql - NQ : 0; i < ql; ++i)
@@ -583,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     uint32_t ql = 0;
     while (some && !failed) {
       if (w.same) {
-        some = walk_next(p, w, w.nb);
+        some = walk_next(p, w, item_units(w));
         continue;
       }
       const int seen = w.raw - w.n + 1;        // by token 0
@@ -662,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         fence_proxy_async_smem();
         mbar_arrive(&bars[kLFull + sl]);
         ++ql;
-        some = walk_next(p, w, w.tiles - w.j);   // (they serve all tiles of their head)
+        some = walk_next(p, w, w.units - w.j);   // (they serve all tiles of their head)
         continue;
       }
       for (int s0 = 0; s0 < w.steps && !failed; s0 += D) {
@@ -700,33 +753,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const int quad = warp & 3, set = warp >> 2;
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    // Items, tiles, converted ones, steps and loads of Q so far (as the issuer counts).
-    uint32_t item = 0, tile = 0, conv = 0, summed = 0, g = 0, buf = 0, ql = 0;
+    // Items, tiles, S buffers and loads of Q so far (as the issuer counts).
+    uint32_t item = 0, tile = 0, g = 0, buf = 0, ql = 0;
     bool held = false;
     struct Keys {
       float scale;
-      bool there, nan;     // the page is; a NaN among this thread's codes
+      bool there, nan;     // the page is; a NaN among the position's codes
     };
     auto read_meta = [&](uint32_t it) {
       const float4 m = meta[it & (kMetaSlots - 1)];
       return Keys{tok < kPage ? m.x : m.z, (tok < kPage ? m.y : m.w) != 0.0f, false};
     };
-    // K of tile number `it` to bf16, this thread's half of the dims.
+    // K of tile number `it` to bf16, into this set's place.
     auto convert = [&](uint32_t it, Keys* keys) {
       const int st = (int)(it % NK);
       if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kKFull + st], (it / NK) & 1u))) return false;
       *keys = read_meta(it);
       const uint8_t* src = smem + LY::kK + st * LY::kKBytes;
       uint32_t bad = 0;
-      const uint32_t t_a = tmem + lane_base + LY::kA + (conv & 1) * LY::kACols + set * (DIM / 4);
+      const uint32_t t_a = tmem + lane_base + LY::kA + set * LY::kACols;
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < DIM / 64; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < DIM / 32; ++c) {
         uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint4 x = *reinterpret_cast<const uint4*>(
-              src + swz<DIM>(tok, set * (DIM / 2) + c * 32 + e * 16));
+          const uint4 x = *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, c * 32 + e * 16));
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -740,18 +792,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       keys->nan = (bad & 0x80808080u) != 0u;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars[kAFull + (conv & 1)]);
-      ++conv;
+      mbar_arrive(&bars[kAFull + set]);
       return true;
     };
-    // What the mass held before, read an item ahead by the set that adds to it. Of
-    // few rows' items the sets take the tiles in turn (or the items, where they
-    // have one tile), up to two a set; of the others set 0 has all.
+    // What the mass held before, read an item ahead by the set that adds to it: the
+    // sets take an item's tiles in turn (or, where few rows have one tile an item,
+    // the items), up to two a set.
     float* row = nullptr;      // this thread's position of the next item's head's tile 0
     auto first_mine = [&](const Walk& v, uint32_t it) {
       return v.few && v.batch == 1 ? (int)(it + set) & 1 : set;
     };
-    auto tile_at = [&](const Walk& v, int u) { return v.nb == 1 ? v.tile : tile_of(v, v.j + u); };
+    auto tile_at = [&](const Walk& v, int u) {
+      return u == 0 ? v.tile : (v.few ? tile_of(v, v.j + u) : v.tile + u);
+    };
     struct Two {
       float a, b;
     };
@@ -769,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     Keys keys{0.0f, false, false}, next{0.0f, false, false};
     Two old{0.0f, 0.0f}, old_next{0.0f, 0.0f};
     if (some) old_next = held_mass(w, 0);
-    if (some && !w.few && !convert(0, &next)) failed = true;
+    if (some && !w.few && set < w.nb && !convert(set, &next)) failed = true;
     while (some && !failed) {
       const Walk now = w;
       keys = next;
@@ -778,10 +831,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (held && !now.same && lane == 0) mbar_arrive(&bars[kLEmpty + (ql - 1) % kNL]);
       held = now.steps == 1;
       float* const at = row;
-      // The next item's K, while the products of this one run.
-      some = walk_next(p, w, w.nb);
+      some = walk_next(p, w, item_units(w));
       if (some) old_next = held_mass(w, item + 1);
-      if (some && !w.few && !convert(tile + now.nb, &next)) {
+      // The next item's K, as soon as the last product of this one's is done.
+      const bool ahead = some && !w.few && set < w.nb;
+      if (ahead && now.few && !convert(tile + now.nb + set, &next)) {
         failed = true;
         break;
       }
@@ -869,31 +923,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         ++item;
         continue;
       }
-      const int pos0 = now.tile * kTile, pos = pos0 + tok;
-      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
+      const int pos0 = (now.tile + set) * kTile, pos = pos0 + tok;   // this set's tile
+      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of it
       float total = 0.0f;
-      // The sets take the steps in turn. Both wait for every product and both let
-      // its buffer and lse go, the one that has nothing to do there at once: a set that
-      // is behind would otherwise miss a phase.
-      for (int s = 0; s < now.steps; ++s, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
+      for (int s = 0; s < now.steps && !failed; ++s) {
         if (!now.same) ++ql;
         const uint32_t sl = (ql - 1) % kNL;
         const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
-        const bool ok = (now.same || mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u)) &&
-                        mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) {
-          failed = true;
-          break;
-        }
-        float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-        if ((s & 1) != set) {
-          if (lane == 0) {
-            mbar_arrive(&bars[kSFree + buf]);
-            if (now.steps > 1) mbar_arrive(&bars[kLEmpty + sl]);
+        bool ok = now.same || mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u);
+        // Both sets wait for every product and both let its buffer go, the one that
+        // has nothing to do there at once: a set that is behind would otherwise miss
+        // a phase.
+#pragma unroll 1
+        for (int u = 0; u < now.nb; ++u, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
+          ok = ok && mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
+          if (!__all_sync(0xffffffffu, ok)) {
+            failed = true;
+            break;
           }
-        } else {
+          if (ahead && s + 1 == now.steps && u == min(set, now.nb - 1) &&
+              !convert(tile + now.nb + set, &next)) {
+            failed = true;
+            break;
+          }
+          if (u != set) {
+            if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
+            continue;
+          }
           tc_fence_after();
+          float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
           const uint32_t t_s = tmem + lane_base + buf * kStep;
           // Columns of 8. ls holds minus the lse.
           const float2 ks = make_float2(keys.scale, keys.scale);
@@ -950,38 +1009,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
           }
-          if (now.steps > 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kLEmpty + sl]);
-          }
+          total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
         }
-        total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
+        if (now.steps > 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kLEmpty + sl]);
+        }
       }
       if (failed) break;
-      // Both sets together; a NaN key makes its position NaN.
-      if (keys.nan) total = NAN;
-      const uint32_t slot = summed & 1;
-      bool ok;
-      if (set == 1) {
-        ok = summed < 2 || mbar_wait_long(&bars[kXFree + slot], ((summed >> 1) - 1) & 1u);
-        if (ok) {
-          other[slot * kTile + tok] = total;
-          mbar_arrive(&bars[kXFull + slot]);
-        }
-      } else {
-        ok = mbar_wait_long(&bars[kXFull + slot], (summed >> 1) & 1u);
-        if (ok) {
-          total += other[slot * kTile + tok];
-          mbar_arrive(&bars[kXFree + slot]);
-          put(pos0, old.a, keys.there, total);
-        }
-      }
-      ++summed;
-      if (!__all_sync(0xffffffffu, ok)) {
-        failed = true;
-        break;
-      }
-      ++tile;
+      // (A NaN key makes its position NaN.)
+      if (set < now.nb) put(pos0, old.a, keys.there, keys.nan ? NAN : total);
+      tile += now.nb;
       ++item;
     }
   }

@@ -92,6 +92,27 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The same for a barrier given by its shared-memory address.
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity,
+                                             uint64_t limit_cycles = 1ull << 32) {
+  auto attempt = [&](uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+  };
+  if (attempt(20000u)) return true;
+  const uint64_t t0 = clock64();
+  while (!attempt(20000u))
+    if ((uint64_t)(clock64() - t0) > limit_cycles) return false;
+  return true;
+}
+
 // Arrives once on `bar` and adds `tx` bytes to the transfer count its
 // current phase waits for (the bytes asynchronous copies will deliver).
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t tx) {
@@ -224,6 +245,12 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_at(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
 
