@@ -28,10 +28,10 @@
 //   bf16 holds: exponent and mantissa bits are placed under bf16's, subnormals
 //   included, and multiplied by 2^120) and lies in TMEM as the A operand, two tiles
 //   for an item; the query rows stream past both in steps of up to 128, by TMA as
-//   they lie, and both operands are exact. S has three buffers of 128 columns, so
-//   the products run under the exponentials of those before. (With one tile an item
-//   the rows' 32 KB a step were the bound: 9.6 TB/s from L2.) The bound is the tensor
-//   core (2 dim flops a position and row) and the exponentials beside it.
+//   they lie, and both operands are exact. Each tile has its set of warps and its
+//   buffer of S: most of it goes to registers at once, so that the next product runs
+//   under the exponentials. The bound is the tensor core (2 dim flops a position and
+//   row) and the exponentials beside it.
 //
 // Sums are fp32: of a step first, then over the steps.
 //
@@ -61,7 +61,7 @@ constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11;
 constexpr int kThreads = 32 * (kLWarp + 1);   // (12 warps: 168 registers a thread)
 constexpr int kMetaSlots = 32;
-constexpr int kNS = 3;                     // S buffers
+constexpr int kNS = 3;                     // S buffers (more rows: one for each set)
 constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
                                            // when a step is summed, Q once its product is done)
 constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
@@ -97,10 +97,12 @@ enum Bar {
   kLFull = 32,      // kNL: lse written
   kLEmpty = 40,     // lse read
   kAFull = 48,      // 2: A of a tile written
-  kSFull = 50,      // kNS: S ready
+  kSFull = 50,      // kNS: few rows: S of an item ready
   kSFree = 53,      // kNS: S read
-  kDrain = 56,
-  kNumBars = 57
+  kCFull = 56,      // 2: more rows: S of a set ready
+  kCFree = 58,      // 2: read
+  kDrain = 60,
+  kNumBars = 61
 };
 
 struct Params {
@@ -307,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (i >= kLFull && i < kLFull + kNL) n = 32;
       if (i >= kLEmpty && i < kLEmpty + kNL) n = kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
+      if (i >= kCFree && i < kCFree + 2) n = kSumWarps / 2;
       mbar_init(&bars[i], n);
     }
     mbar_fence_init();
@@ -385,6 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     some = walk_settle(p, w);
   }
 
+  // 12 warps of 168 registers: 384 * 168 = 128 * 96 + 256 * 204.
+  if (warp >= kSumWarps)
+    regs_dec<96>();
+  else
+    regs_inc<200>();
   bool failed = false;
   if (warp == kProducerWarp) {
     // ---------------------------------------------------------- K producer
@@ -496,9 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // is let go when the next comes. `phases`: bit u is that of place u's tiles.
     // (A buffer's first use waits for nothing: the phase before the first is over.)
     Ring tile, s_free, load, lse;
-    uint32_t phases = 0, held_at = 0;
+    uint32_t phases = 0, held_at = 0, c_free[2] = {1u, 1u};
     s_free.phase = 1u;
-    bool held = false, on = uni((int)some) != 0;
+    bool held = false, was_few = false, on = uni((int)some) != 0;
     while (on) {
       const int steps = uni(w.steps), nb = uni(w.nb), few = uni((int)w.few), same = uni((int)w.same);
       const int rows = uni(w.n * p.group);
@@ -507,12 +515,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         if (leader) commit(kQEmpty, held_at);
         __syncwarp();
       }
+      if (few != (int)was_few) {
+        // The two forms share the buffers: all of the other one are read first.
+        was_few = few;
+        if (few)
+          ok = wait(kCFree, 0, c_free[0]) && wait(kCFree, 1, c_free[1]);
+        else
+          for (uint32_t i = 0; i < kNS; ++i)
+            ok = wait(kSFree, i, i < s_free.at ? s_free.phase ^ 1u : s_free.phase) && ok;
+      }
       if (few) {
         // One buffer of S for all tiles of the item.
         const int n = (3 * ((rows + 7) & ~7) + 15) & ~15;
         const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
         if (!same) {
-          ok = wait(kQFull, load.at, load.phase) && wait(kLFull, lse.at, lse.phase);
+          ok = wait(kQFull, load.at, load.phase) && wait(kLFull, lse.at, lse.phase) && ok;
           held_at = load.at;
           next(load, NQ);
           next(lse, kNL);
@@ -539,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       } else {
         for (int s = 0; s < steps; ++s) {
           if (!same) {
-            ok = wait(kQFull, load.at, load.phase) && ok;
+            // (And the lse, so that who waits for the product needs not.)
+            ok = wait(kQFull, load.at, load.phase) && wait(kLFull, lse.at, lse.phase) && ok;
             held_at = load.at;
             next(load, NQ);
             next(lse, kNL);
@@ -551,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             if (u >= nb) break;
-            ok = wait(kSFree, s_free.at, s_free.phase) && ok;
+            ok = wait(kCFree, u, c_free[u]) && ok;
+            c_free[u] ^= 1u;
             if (s == 0) {
               // K of the tile is in TMEM: its stage is free.
               ok = wait(kAFull, u, (phases >> u) & 1u) && ok;
@@ -563,13 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             if (leader) {
 #pragma unroll
               for (int k = 0; k < DIM / 16; ++k)
-                mma_f16_ts(t_d + s_free.at * kStep, t_d + LY::kA + u * LY::kACols + 8 * k,
+                mma_f16_ts(t_d + u * kStep, t_d + LY::kA + u * LY::kACols + 8 * k,
                            b + (((k >> 2) * (kStep * 128) + (k & 3) * 32) >> 4), idesc,
                            k > 0 ? 1u : 0u);
-              commit(kSFull, s_free.at);
+              commit(kCFull, u);
             }
             __syncwarp();
-            next(s_free, kNS);
           }
           if (leader && steps > 1) commit(kQEmpty, held_at);
           __syncwarp();
@@ -754,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     // Items, tiles, S buffers and loads of Q so far (as the issuer counts).
-    uint32_t item = 0, tile = 0, g = 0, buf = 0, ql = 0;
+    uint32_t item = 0, tile = 0, g = 0, buf = 0, ql = 0, c_phase = 0;
+    const uint32_t c_full = smem_u32(&bars[kCFull + set]);
     bool held = false;
     struct Keys {
       float scale;
@@ -926,34 +945,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       const int pos0 = (now.tile + set) * kTile, pos = pos0 + tok;   // this set's tile
       const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of it
       float total = 0.0f;
-      for (int s = 0; s < now.steps && !failed; ++s) {
+      for (int s = 0; s < now.steps; ++s) {
         if (!now.same) ++ql;
         const uint32_t sl = (ql - 1) % kNL;
         const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
-        bool ok = now.same || mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u);
-        // Both sets wait for every product and both let its buffer go, the one that
-        // has nothing to do there at once: a set that is behind would otherwise miss
-        // a phase.
-#pragma unroll 1
-        for (int u = 0; u < now.nb; ++u, ++g, buf = buf + 1 == kNS ? 0 : buf + 1) {
-          ok = ok && mbar_wait_long(&bars[kSFull + buf], (g / kNS) & 1u);
-          if (!__all_sync(0xffffffffu, ok)) {
-            failed = true;
-            break;
-          }
-          if (ahead && s + 1 == now.steps && u == min(set, now.nb - 1) &&
-              !convert(tile + now.nb + set, &next)) {
-            failed = true;
-            break;
-          }
-          if (u != set) {
-            if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
-            continue;
-          }
+        // (The product was issued when its lse was there. A set without a tile only
+        // goes along.)
+        const bool work = set < now.nb;
+        const bool ok = work ? mbar_wait_at(c_full, c_phase)
+                             : mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+        if (ahead && s + 1 == now.steps && !convert(tile + now.nb + set, &next)) {
+          failed = true;
+          break;
+        }
+        if (work) {
+          c_phase ^= 1u;
           tc_fence_after();
           float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-          const uint32_t t_s = tmem + lane_base + buf * kStep;
+          const uint32_t t_s = tmem + lane_base + set * kStep;
           // Columns of 8. ls holds minus the lse.
           const float2 ks = make_float2(keys.scale, keys.scale);
           auto add8 = [&](const float* x, int c, bool masked) {
@@ -980,24 +994,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
             acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
           };
-          const int here = step_of(p, now, s).rows;
-          const bool masked = edge && vs[0] < pos0 + kTile;
-          if (here == capacity && capacity > kStep - 16 && !masked) {
-            // 32 columns at a time, the next ones on their way meanwhile.
-            float x[2][32];
-            tmem_ld32(t_s, x[0]);
+          const int here = s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now, s).rows;
+          if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile)) {
+            // 32 columns at a time; the last ones come once the first are done.
+            float x[3][32];
+            auto add32 = [&](const float* v, int c) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_fence<32>(x[c & 1]);
-              if (c < 3) tmem_ld32(t_s + 32 * (c + 1), x[(c + 1) & 1]);
-              if (c == 3) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
-              }
+              for (int e = 0; e < 4; ++e) add8(v + 8 * e, c + 8 * e, false);
+            };
 #pragma unroll
-              for (int e = 0; e < 4; ++e) add8(x[c & 1] + 8 * e, 32 * c + 8 * e, false);
-            }
+            for (int c = 0; c < 3; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+#pragma unroll
+            for (int c = 0; c < 3; ++c) tmem_fence<32>(x[c]);
+            add32(x[0], 0);
+            tmem_ld32(t_s + 96, x[0]);
+            add32(x[1], 32);
+            tmem_fence<32>(x[0]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kCFree + set]);
+            add32(x[2], 64);
+            add32(x[0], 96);
           } else {
             for (int c = 0; c < here; c += 8) {
               float x[8];
@@ -1007,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
+            if (lane == 0) mbar_arrive(&bars[kCFree + set]);
           }
           total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
         }
