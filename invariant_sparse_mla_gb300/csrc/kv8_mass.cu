@@ -41,8 +41,8 @@
 //
 // Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: of
 // two tiles each has one, so that one's exponentials run while the other waits),
-// warp 8 brings K, warp 9 issues the products, warp 10 brings Q, warp 11 lse and the
-// pieces of q.
+// warp 8 walks the items, lists them for the others and brings K, warp 9 issues the
+// products, warp 10 brings Q, warp 11 lse and the pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -61,6 +61,9 @@ constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11;
 constexpr int kThreads = 32 * (kLWarp + 1);   // (12 warps: 168 registers a thread)
 constexpr int kMetaSlots = 32;
+constexpr int kItems = 16;                 // slots of the list of items
+constexpr int kAhead = 4;                  // items that are looked up at once
+constexpr int kReaders = kSumWarps + 3;    // warps that read the list
 constexpr int kNS = 3;                     // S buffers (more rows: one for each set)
 constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
                                            // when a step is summed, Q once its product is done)
@@ -77,8 +80,9 @@ struct Layout {
   static constexpr int kQ = kK + kNK * kKBytes;
   static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
   static constexpr int kBars = kLse + kNL * kStep * 12;
-  static constexpr int kMeta = kBars + 64 * 8;                // kMetaSlots x float4
-  static constexpr int kMisc = kMeta + kMetaSlots * 16;       // tmem slot, start of work, scan
+  static constexpr int kMeta = kBars + 96 * 8;                // kMetaSlots x float4
+  static constexpr int kList = kMeta + kMetaSlots * 16;       // kItems x Item
+  static constexpr int kMisc = kList + kItems * 64;           // tmem slot, start of work, scan
   static constexpr int kEnd = kMisc + 32 + 8 * (kThreads / 32);
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -102,7 +106,9 @@ enum Bar {
   kCFull = 56,      // 2: more rows: S of a set ready
   kCFree = 58,      // 2: read
   kDrain = 60,
-  kNumBars = 61
+  kIFull = 61,      // kItems: an item is in the list
+  kIEmpty = 77,     // every reader is done with it
+  kNumBars = 93
 };
 
 struct Params {
@@ -196,19 +202,32 @@ __device__ __forceinline__ void load_item(const Params& p, Walk& w) {
   w.item_kvh = w.kvh;
 }
 
+// What the warps are told of an item.
+struct __align__(16) Item {
+  int nb;                // tiles; 0 ends the list
+  int steps;
+  int n, first;          // new tokens; the first that sees the tiles
+  int tile[4];
+  int raw, len;          // lens[r], and clamped
+  int r, kvh;
+  int t0;                // the request's first token
+  int few, same, single; // in pieces; Q as it is; in pieces and one tile an item
+};
+static_assert(sizeof(Item) == 64, "an item's slot");
+
 // Step s of an item: its first token, its chunk of heads and its rows.
 struct Step {
   int token, head, rows;
 };
-__device__ __forceinline__ Step step_of(const Params& p, const Walk& w, int s) {
+__device__ __forceinline__ Step step_of(const Params& p, int n, int first, int s) {
   Step x;
   if (p.chunks == 1) {
-    x.token = w.first + s * p.step_tokens;
+    x.token = first + s * p.step_tokens;
     x.head = 0;
-    const int left = w.n - x.token;
+    const int left = n - x.token;
     x.rows = (left < p.step_tokens ? left : p.step_tokens) * p.step_heads;
   } else {
-    x.token = w.first + s / p.chunks;
+    x.token = first + s / p.chunks;
     x.head = s % p.chunks * kStep;
     const int left = p.group - x.head;
     x.rows = left < kStep ? left : kStep;
@@ -297,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LY::kBars);
   float4* meta = reinterpret_cast<float4*>(smem + LY::kMeta);
+  Item* list = reinterpret_cast<Item*>(smem + LY::kList);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
   int64_t* start_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 8);   // request, cost before it
   int64_t* scan_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 32);
@@ -306,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if (i >= kAFull && i < kAFull + 2) n = kSum / 2;
+      if (i >= kIEmpty && i < kIEmpty + kItems) n = kReaders;
       if (i >= kLFull && i < kLFull + kNL) n = 32;
       if (i >= kLEmpty && i < kLEmpty + kNL) n = kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
@@ -388,67 +409,98 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     some = walk_settle(p, w);
   }
 
-  // 12 warps of 168 registers: 384 * 168 = 128 * 96 + 256 * 204.
-  if (warp >= kSumWarps)
-    regs_dec<96>();
-  else
-    regs_inc<200>();
   bool failed = false;
+  // The number-th item of the list, for a reading warp as a whole; nb is 0 behind
+  // the last (and if a wait gave up).
+  auto take = [&](uint32_t number) {
+    const uint32_t slot = number % kItems;
+    Item x;
+    x.nb = 0;
+    if (__all_sync(0xffffffffu, mbar_wait_long(&bars[kIFull + slot], (number / kItems) & 1u))) {
+      x = list[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kIEmpty + slot]);
+    } else {
+      failed = true;
+    }
+    return x;
+  };
   if (warp == kProducerWarp) {
     // ---------------------------------------------------------- K producer
     const int none = (int)(p.c.num_pages * 2 * p.c.kv_heads * kPage);   // a row past the pool: zeros
     int err_bits = 0;
-    uint32_t g = 0, issued = 0;
-    // The pages of up to 16 units of a request (8 of two tiles) are looked up at
-    // once, a page a lane, and the next ones while these are brought.
-    struct Lookup {
-      int count, pages;      // units, and page places of each
+    uint32_t g = 0, issued = 0, listed = 0;
+    // kAhead items go to the list at once, and lane 8 e + i looks up the i-th page of
+    // the e-th of them; the next ones' while these are brought.
+    struct Batch {
       int y;
       float ks;
-      bool there;            // a place of a tile that there is
+      int places;            // page places of the lane's item
     };
-    auto look = [&](const Walk& v) {
-      Lookup k;
-      k.pages = v.few ? 2 : 4;
-      const int most = 32 / k.pages;
-      const int64_t left = (v.end - v.at + v.cost - 1) / v.cost;
-      k.count = v.items - v.i < most ? v.items - v.i : most;
-      if (left < k.count) k.count = (int)left;
-      k.y = none;
-      k.ks = 0.0f;
-      k.there = false;
-      const int e = v.few ? lane >> 1 : lane >> 2, at = v.few ? lane & 1 : lane & 3;
-      if (e < k.count) {
-        const int i = v.i + e, kvh = i / v.units;
-        const int tile = tile_of(v, i - kvh * v.units) + (at >> 1);
-        const int b = 2 * tile + (at & 1);
-        k.there = tile < v.tiles;
-        if ((int64_t)b * kPage < v.len) {
-          const int64_t page = p.c.block_table[(int64_t)v.r * p.c.bt_stride + b];
-          if (page >= 0 && page < p.c.num_pages) {
-            const int64_t part = page * 2 * p.c.kv_heads + kvh;
-            k.y = (int)(part * kPage);
-            k.ks = p.c.scales[part] * p.scale_log2;
-          } else {
-            err_bits |= kErrPage;
+    auto list_items = [&](bool* ok) {
+      Batch b;
+      b.y = none;
+      b.ks = 0.0f;
+      b.places = 0;
+      int tile = 0, r = 0, kvh = 0, len = 0;
+#pragma unroll 1
+      for (int e = 0; e < kAhead; ++e) {
+        Item x;
+        x.nb = 0;
+        if (some) {
+          x = {w.nb, w.steps, w.n, w.first, {w.tile, 0, 0, 0}, w.raw, w.len, w.r, w.kvh, (int)w.t0,
+               (int)w.few, (int)w.same, (int)(w.few && w.batch == 1)};
+#pragma unroll
+          for (int u = 1; u < 4; ++u)
+            x.tile[u] = u < w.nb ? (w.few ? tile_of(w, w.j + u) : w.tile + u) : 0;
+          if (lane >> 3 == e) {
+            const int u = (lane >> 1) & 3;
+            b.places = 2 * w.nb;
+            tile = u == 0 ? x.tile[0] : (u == 1 ? x.tile[1] : (u == 2 ? x.tile[2] : x.tile[3]));
+            r = w.r;
+            kvh = w.kvh;
+            len = w.len;
           }
         }
+        const uint32_t slot = listed % kItems;
+        *ok = *ok && (listed < kItems ||
+                      mbar_wait_long(&bars[kIEmpty + slot], (listed / kItems - 1) & 1u));
+        if (!__all_sync(0xffffffffu, *ok)) break;
+        if (lane == 0) {
+          list[slot] = x;
+          mbar_arrive(&bars[kIFull + slot]);
+        }
+        __syncwarp();
+        ++listed;
+        if (!some) break;
+        some = walk_next(p, w, item_units(w));
       }
-      return k;
+      const int block = 2 * tile + (lane & 1);
+      if ((lane & 7) < b.places && (int64_t)block * kPage < len) {
+        const int64_t page = p.c.block_table[(int64_t)r * p.c.bt_stride + block];
+        if (page >= 0 && page < p.c.num_pages) {
+          const int64_t part = page * 2 * p.c.kv_heads + kvh;
+          b.y = (int)(part * kPage);
+          b.ks = p.c.scales[part] * p.scale_log2;
+        } else {
+          err_bits |= kErrPage;
+        }
+      }
+      return b;
     };
-    Lookup next;
-    if (some) next = look(w);
-    while (some && !failed) {
-      const Lookup now = next;
-      some = walk_next(p, w, now.count);
-      if (some) next = look(w);
-      for (int e = 0; e < now.count * now.pages; e += 2) {
-        if (!__shfl_sync(0xffffffffu, (int)now.there, e)) continue;
+    bool ok = true;
+    Batch next = list_items(&ok);
+    while (ok && __any_sync(0xffffffffu, next.places > 0)) {
+      const Batch now = next;
+      // (Behind the list's end there is nothing more to say.)
+      next.places = 0;
+      if (some || __all_sync(0xffffffffu, now.places > 0)) next = list_items(&ok);
+      for (int e = 0; e < 32 && ok; e += 2) {
+        if ((e & 7) >= __shfl_sync(0xffffffffu, now.places, e)) continue;
         const int y0 = __shfl_sync(0xffffffffu, now.y, e);
         const int y1 = __shfl_sync(0xffffffffu, now.y, e + 1);
         const float k0 = __shfl_sync(0xffffffffu, now.ks, e);
         const float k1 = __shfl_sync(0xffffffffu, now.ks, e + 1);
-        bool ok = true;
         if (lane == 0) {
           const int st = (int)(g % NK);
           if (g >= NK) ok = mbar_wait_long(&bars[kKEmpty + st], (uint32_t)((g / NK - 1) & 1));
@@ -463,12 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           }
         }
         ++g;
-        if (!__all_sync(0xffffffffu, ok)) {
-          failed = true;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, ok);
       }
     }
+    failed = !ok;
     if (lane == 0)   // every copy has landed before the CTA can exit
       for (uint32_t i = issued > NK ? issued - NK : 0; i < issued; ++i)
         if (!mbar_wait_long(&bars[kKFull + i % NK], (uint32_t)((i / NK) & 1))) failed = true;
@@ -506,10 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     Ring tile, s_free, load, lse;
     uint32_t phases = 0, held_at = 0, c_free[2] = {1u, 1u};
     s_free.phase = 1u;
-    bool held = false, was_few = false, on = uni((int)some) != 0;
-    while (on) {
-      const int steps = uni(w.steps), nb = uni(w.nb), few = uni((int)w.few), same = uni((int)w.same);
-      const int rows = uni(w.n * p.group);
+    bool held = false, was_few = false;
+    for (uint32_t item = 0;; ++item) {
+      const Item x = take(item);
+      const int nb = uni(x.nb);
+      if (nb == 0) break;
+      const int steps = uni(x.steps), few = uni(x.few), same = uni(x.same);
+      const int rows = uni(x.n * p.group);
       bool ok = true;
       if (held && !same) {
         if (leader) commit(kQEmpty, held_at);
@@ -563,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             next(lse, kNL);
           }
           const int n = s + 1 < steps && p.chunks == 1 ? (capacity + 15) & ~15
-                                                       : uni((step_of(p, w, s).rows + 15) & ~15);
+                                                       : uni((step_of(p, x.n, x.first, s).rows + 15) & ~15);
           const uint32_t idesc = make_idesc_bf16(kTile, n, 0, 0);
           const uint64_t b = q_desc + (uint64_t)(held_at * (LY::kQBytes >> 4));
 #pragma unroll
@@ -599,8 +652,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         break;
       }
       held = steps == 1;
-      some = walk_next(p, w, item_units(w));
-      on = uni((int)some) != 0;
     }
     if (leader) mma_commit(&bars[kDrain]);
     __syncwarp();
@@ -610,32 +661,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // ------------------------------------------------------------------ Q
     const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
     uint32_t ql = 0;
-    while (some && !failed) {
-      if (!w.same) {
-        for (int s = 0; s < w.steps; ++s, ++ql) {
-          const uint32_t st = ql % NQ;
-          if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
-                                                                 (ql / NQ - 1) & 1u))) {
-            failed = true;
-            break;
-          }
-          if (lane == 0) {
-            if (w.few) {
-              mbar_arrive(&bars[kQFull + st]);   // (the pieces come with the lse)
-            } else {
-              const Step x = step_of(p, w, s);
-              mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
-#pragma unroll
-              for (int b = 0; b < DIM / 64; ++b)
-                tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
-                              w.kvh * p.group + x.head, (int)w.t0 + x.token, &bars[kQFull + st]);
-            }
-          }
-          __syncwarp();
+    for (uint32_t item = 0; !failed; ++item) {
+      const Item x = take(item);
+      if (x.nb == 0) break;
+      if (x.same) continue;
+      for (int s = 0; s < x.steps; ++s, ++ql) {
+        const uint32_t st = ql % NQ;
+        if (!__all_sync(0xffffffffu,
+                        ql < NQ || mbar_wait_long(&bars[kQEmpty + st], (ql / NQ - 1) & 1u))) {
+          failed = true;
+          break;
         }
+        if (lane == 0) {
+          if (x.few) {
+            mbar_arrive(&bars[kQFull + st]);   // (the pieces come with the lse)
+          } else {
+            const Step y = step_of(p, x.n, x.first, s);
+            mbar_arrive_expect_tx(&bars[kQFull + st], bytes);
+#pragma unroll
+            for (int b = 0; b < DIM / 64; ++b)
+              tma_load_box3(sbase + LY::kQ + st * LY::kQBytes + b * (kStep * 128), &q_map, 64 * b,
+                            x.kvh * p.group + y.head, x.t0 + y.token, &bars[kQFull + st]);
+          }
+        }
+        __syncwarp();
       }
-      // (Few rows serve all tiles of their head.)
-      if (!failed) some = walk_next(p, w, w.few ? w.units - w.j : 1);
     }
     if (lane == 0)   // every copy has landed before the CTA can exit
       for (uint32_t i = ql > NQ ? ql - NQ : 0; i < ql; ++i)
@@ -652,13 +702,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       t_head[i] = (lane + 32 * i) % p.step_heads;
     }
     uint32_t ql = 0;
-    while (some && !failed) {
-      if (w.same) {
-        some = walk_next(p, w, item_units(w));
-        continue;
-      }
+    for (uint32_t item = 0; !failed; ++item) {
+      const Item w = take(item);
+      if (w.nb == 0) break;
+      if (w.same) continue;
       const int seen = w.raw - w.n + 1;        // by token 0
-      const float* lse0 = p.lse + w.t0 * p.heads + w.kvh * p.group;
+      const float* lse0 = p.lse + (int64_t)w.t0 * p.heads + w.kvh * p.group;
       // A row that there is not sees nothing, and one of -inf adds nothing.
       auto put = [&](uint32_t slot, int i, bool in, int token, float l) {
         float* ls = reinterpret_cast<float*>(smem + LY::kLse + slot * (kStep * 12)) + lane + 32 * i;
@@ -689,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         constexpr int E = DIM / 32;
         uint8_t* q8 = smem + LY::kQ + st * LY::kQBytes;
         float* factor = reinterpret_cast<float*>(smem + LY::kLse + sl * (kStep * 12)) + 2 * kStep;
-        const __nv_bfloat16* q0 = p.q + w.t0 * p.q_stride + (int64_t)w.kvh * p.group * DIM + lane * E;
+        const __nv_bfloat16* q0 = p.q + (int64_t)w.t0 * p.q_stride + (int64_t)w.kvh * p.group * DIM + lane * E;
         for (int r0 = 0; r0 < rows; r0 += 8) {
           float x[8][E];
 #pragma unroll
@@ -733,14 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         fence_proxy_async_smem();
         mbar_arrive(&bars[kLFull + sl]);
         ++ql;
-        some = walk_next(p, w, w.units - w.j);   // (they serve all tiles of their head)
         continue;
       }
       for (int s0 = 0; s0 < w.steps && !failed; s0 += D) {
         float l[D][N];
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-          const Step x = step_of(p, w, s0 + d);
+          const Step x = step_of(p, w.n, w.first, s0 + d);
 #pragma unroll
           for (int i = 0; i < N; ++i)
             l[d][i] = s0 + d < w.steps && lane + 32 * i < x.rows
@@ -752,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             failed = true;
             break;
           }
-          const Step x = step_of(p, w, s0 + d);
+          const Step x = step_of(p, w.n, w.first, s0 + d);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             float v = l[0][i];
@@ -764,7 +812,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           mbar_arrive(&bars[kLFull + ql % kNL]);
         }
       }
-      if (!failed) some = walk_next(p, w, 1);
     }
   } else {
     // --------------------------------------------------- convert and sum
@@ -817,43 +864,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // What the mass held before, read an item ahead by the set that adds to it: the
     // sets take an item's tiles in turn (or, where few rows have one tile an item,
     // the items), up to two a set.
-    float* row = nullptr;      // this thread's position of the next item's head's tile 0
-    auto first_mine = [&](const Walk& v, uint32_t it) {
-      return v.few && v.batch == 1 ? (int)(it + set) & 1 : set;
-    };
-    auto tile_at = [&](const Walk& v, int u) {
-      return u == 0 ? v.tile : (v.few ? tile_of(v, v.j + u) : v.tile + u);
+    auto first_mine = [&](const Item& v, uint32_t it) {
+      return v.single ? (int)(it + set) & 1 : set;
     };
     struct Two {
       float a, b;
     };
-    auto held_mass = [&](const Walk& v, uint32_t it) {
+    float* row = nullptr;      // this thread's position of the next item's head's tile 0
+    auto held_mass = [&](const Item& v, uint32_t it) {
       if (!v.same)
         row = p.mass + ((int64_t)v.r * p.c.kv_heads + v.kvh) * p.mass_stride + tok;
       auto get = [&](int u) {
         if (u >= v.nb) return 0.0f;
-        const int t0 = tile_at(v, u) * kTile;
+        const int t0 = (u < 2 ? (u ? v.tile[1] : v.tile[0]) : (u == 2 ? v.tile[2] : v.tile[3])) * kTile;
         return t0 + tok < v.len && t0 + tok < v.raw - v.n ? row[t0] : 0.0f;
       };
       const int u = first_mine(v, it);
       return Two{get(u), get(u + 2)};
     };
+    // The item after the present one is looked at early (and read again when it is
+    // its turn: kept in registers it would push others out).
     Keys keys{0.0f, false, false}, next{0.0f, false, false};
     Two old{0.0f, 0.0f}, old_next{0.0f, 0.0f};
-    if (some) old_next = held_mass(w, 0);
-    if (some && !w.few && set < w.nb && !convert(set, &next)) failed = true;
-    while (some && !failed) {
-      const Walk now = w;
+    bool more = false, ahead = false;
+    auto look_ahead = [&](uint32_t it) {
+      const uint32_t slot = it % kItems;
+      if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kIFull + slot], (it / kItems) & 1u))) {
+        failed = true;
+        return;
+      }
+      const Item& v = list[slot];
+      more = v.nb > 0;
+      ahead = !v.few && set < v.nb;
+      if (more) old_next = held_mass(v, it);
+    };
+    look_ahead(0);
+    if (ahead && !failed && !convert(set, &next)) failed = true;
+    while (more && !failed) {
+      const Item now = take(item);
       keys = next;
       old = old_next;
       const int rows = now.n * p.group, base = now.raw - now.n;
       if (held && !now.same && lane == 0) mbar_arrive(&bars[kLEmpty + (ql - 1) % kNL]);
       held = now.steps == 1;
       float* const at = row;
-      some = walk_next(p, w, item_units(w));
-      if (some) old_next = held_mass(w, item + 1);
+      look_ahead(item + 1);
+      if (failed) break;
       // The next item's K, as soon as the last product of this one's is done.
-      const bool ahead = some && !w.few && set < w.nb;
       if (ahead && now.few && !convert(tile + now.nb + set, &next)) {
         failed = true;
         break;
@@ -880,7 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           const int r8 = (rows + 7) & ~7, cols = (3 * r8 + 15) & ~15;
           const uint32_t t_s = tmem + lane_base + buf * kStep + u0 * cols;
           const Keys k0 = read_meta(tile + u0), k1 = mine > 1 ? read_meta(tile + u0 + 2) : k0;
-          const int p0 = tile_at(now, u0) * kTile, p1 = mine > 1 ? tile_at(now, u0 + 2) * kTile : p0;
+          const int p0 = (u0 ? now.tile[1] : now.tile[0]) * kTile;
+          const int p1 = mine > 1 ? (u0 ? now.tile[3] : now.tile[2]) * kTile : p0;
           float2 acc[2][2] = {};
           // Eight rows of both tiles.
           for (int c = 0; c < rows; c += 8) {
@@ -942,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         ++item;
         continue;
       }
-      const int pos0 = (now.tile + set) * kTile, pos = pos0 + tok;   // this set's tile
+      const int pos0 = (set ? now.tile[1] : now.tile[0]) * kTile, pos = pos0 + tok;   // this set's tile
       const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of it
       float total = 0.0f;
       for (int s = 0; s < now.steps; ++s) {
@@ -994,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
             acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
           };
-          const int here = s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now, s).rows;
+          const int here = s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now.n, now.first, s).rows;
           if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile)) {
             // 32 columns at a time; the last ones come once the first are done.
             float x[3][32];
