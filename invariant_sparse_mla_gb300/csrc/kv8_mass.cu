@@ -41,8 +41,8 @@
 //
 // Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: of
 // two tiles each has one, so that one's exponentials run while the other waits),
-// warp 8 walks the items, lists them for the others and brings K, warp 9 issues the
-// products, warp 10 brings Q, warp 11 lse and the pieces of q.
+// warp 8 brings K, warp 9 issues the products, warp 10 walks the items, lists them for
+// the others and brings Q, warp 11 lse and the pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -61,8 +61,11 @@ constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11;
 constexpr int kThreads = 32 * (kLWarp + 1);   // (12 warps: 168 registers a thread)
 constexpr int kMetaSlots = 32;
-constexpr int kItems = 16;                 // slots of the list of items
-constexpr int kAhead = 4;                  // items that are looked up at once
+constexpr int kItems = 32;                 // slots of the list of items
+constexpr int kLook = 4;                   // items whose pages are looked up at once
+// Items listed ahead of the one whose Q is being brought: K is looked up to 2 kLook
+// ahead of the one in work, and waits for the list.
+constexpr int kAhead = 3 * kLook;
 constexpr int kReaders = kSumWarps + 3;    // warps that read the list
 constexpr int kNS = 3;                     // S buffers (more rows: one for each set)
 constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
@@ -80,7 +83,7 @@ struct Layout {
   static constexpr int kQ = kK + kNK * kKBytes;
   static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
   static constexpr int kBars = kLse + kNL * kStep * 12;
-  static constexpr int kMeta = kBars + 96 * 8;                // kMetaSlots x float4
+  static constexpr int kMeta = kBars + 128 * 8;               // kMetaSlots x float4
   static constexpr int kList = kMeta + kMetaSlots * 16;       // kItems x Item
   static constexpr int kMisc = kList + kItems * 64;           // tmem slot, start of work, scan
   static constexpr int kEnd = kMisc + 32 + 8 * (kThreads / 32);
@@ -107,8 +110,8 @@ enum Bar {
   kCFree = 58,      // 2: read
   kDrain = 60,
   kIFull = 61,      // kItems: an item is in the list
-  kIEmpty = 77,     // every reader is done with it
-  kNumBars = 93
+  kIEmpty = 93,     // every reader is done with it
+  kNumBars = 125
 };
 
 struct Params {
@@ -429,51 +432,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // ---------------------------------------------------------- K producer
     const int none = (int)(p.c.num_pages * 2 * p.c.kv_heads * kPage);   // a row past the pool: zeros
     int err_bits = 0;
-    uint32_t g = 0, issued = 0, listed = 0;
-    // kAhead items go to the list at once, and lane 8 e + i looks up the i-th page of
-    // the e-th of them; the next ones' while these are brought.
+    uint32_t g = 0, issued = 0, looked = 0;
+    // Lane 8 e + i looks up the i-th page of the e-th of kLook items; the next ones'
+    // while these are brought.
     struct Batch {
       int y;
       float ks;
-      int places;            // page places of the lane's item
+      int places;            // page places of the lane's item; 0 behind the last
     };
-    auto list_items = [&](bool* ok) {
+    bool ok = true, more = true;
+    auto look = [&] {
       Batch b;
       b.y = none;
       b.ks = 0.0f;
       b.places = 0;
       int tile = 0, r = 0, kvh = 0, len = 0;
 #pragma unroll 1
-      for (int e = 0; e < kAhead; ++e) {
-        Item x;
-        x.nb = 0;
-        if (some) {
-          x = {w.nb, w.steps, w.n, w.first, {w.tile, 0, 0, 0}, w.raw, w.len, w.r, w.kvh, (int)w.t0,
-               (int)w.few, (int)w.same, (int)(w.few && w.batch == 1)};
-#pragma unroll
-          for (int u = 1; u < 4; ++u)
-            x.tile[u] = u < w.nb ? (w.few ? tile_of(w, w.j + u) : w.tile + u) : 0;
-          if (lane >> 3 == e) {
-            const int u = (lane >> 1) & 3;
-            b.places = 2 * w.nb;
-            tile = u == 0 ? x.tile[0] : (u == 1 ? x.tile[1] : (u == 2 ? x.tile[2] : x.tile[3]));
-            r = w.r;
-            kvh = w.kvh;
-            len = w.len;
-          }
-        }
-        const uint32_t slot = listed % kItems;
-        *ok = *ok && (listed < kItems ||
-                      mbar_wait_long(&bars[kIEmpty + slot], (listed / kItems - 1) & 1u));
-        if (!__all_sync(0xffffffffu, *ok)) break;
-        if (lane == 0) {
-          list[slot] = x;
-          mbar_arrive(&bars[kIFull + slot]);
+      for (int e = 0; e < kLook && more && ok; ++e, ++looked) {
+        const uint32_t slot = looked % kItems;
+        ok = __all_sync(0xffffffffu, mbar_wait_long(&bars[kIFull + slot], (looked / kItems) & 1u));
+        if (!ok) break;
+        const Item& x = list[slot];
+        more = x.nb > 0;
+        if (lane >> 3 == e) {
+          b.places = 2 * x.nb;
+          tile = x.tile[(lane >> 1) & 3];
+          r = x.r;
+          kvh = x.kvh;
+          len = x.len;
         }
         __syncwarp();
-        ++listed;
-        if (!some) break;
-        some = walk_next(p, w, item_units(w));
+        if (lane == 0) mbar_arrive(&bars[kIEmpty + slot]);
       }
       const int block = 2 * tile + (lane & 1);
       if ((lane & 7) < b.places && (int64_t)block * kPage < len) {
@@ -488,13 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       }
       return b;
     };
-    bool ok = true;
-    Batch next = list_items(&ok);
+    Batch next = look();
     while (ok && __any_sync(0xffffffffu, next.places > 0)) {
       const Batch now = next;
-      // (Behind the list's end there is nothing more to say.)
-      next.places = 0;
-      if (some || __all_sync(0xffffffffu, now.places > 0)) next = list_items(&ok);
+      next = look();
       for (int e = 0; e < 32 && ok; e += 2) {
         if ((e & 7) >= __shfl_sync(0xffffffffu, now.places, e)) continue;
         const int y0 = __shfl_sync(0xffffffffu, now.y, e);
@@ -660,9 +646,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   } else if (warp == kQWarp) {
     // ------------------------------------------------------------------ Q
     const uint32_t bytes = (uint32_t)(capacity * DIM * 2);
-    uint32_t ql = 0;
+    uint32_t ql = 0, listed = 0;
+    bool ended = false;
+    // Adds an item to the list, or its end.
+    auto list_one = [&] {
+      const uint32_t slot = listed % kItems;
+      if (!__all_sync(0xffffffffu, listed < kItems ||
+                                       mbar_wait_long(&bars[kIEmpty + slot],
+                                                      (listed / kItems - 1) & 1u))) {
+        failed = true;
+        return;
+      }
+      if (lane == 0) {
+        Item& x = list[slot];
+        x.nb = some ? w.nb : 0;
+        if (some) {
+          x.steps = w.steps;
+          x.n = w.n;
+          x.first = w.first;
+          x.raw = w.raw;
+          x.len = w.len;
+          x.r = w.r;
+          x.kvh = w.kvh;
+          x.t0 = (int)w.t0;
+          x.few = w.few;
+          x.same = w.same;
+          x.single = w.few && w.batch == 1;
+          x.tile[0] = w.tile;
+          for (int u = 1; u < w.nb; ++u) x.tile[u] = w.few ? tile_of(w, w.j + u) : w.tile + u;
+        } else {
+          x.few = x.same = x.single = 0;
+        }
+        mbar_arrive(&bars[kIFull + slot]);
+      }
+      __syncwarp();
+      ++listed;
+      ended = !some;
+      if (some) some = walk_next(p, w, item_units(w));
+    };
     for (uint32_t item = 0; !failed; ++item) {
-      const Item x = take(item);
+      while (!ended && !failed && listed <= item + kAhead) list_one();
+      if (failed) break;
+      const Item x = list[item % kItems];   // (its own: nobody else writes)
       if (x.nb == 0) break;
       if (x.same) continue;
       for (int s = 0; s < x.steps; ++s, ++ql) {
