@@ -28,9 +28,8 @@
 //   bf16 holds: exponent and mantissa bits are placed under bf16's, subnormals
 //   included, and multiplied by 2^120) and lies in TMEM as the A operand, two tiles
 //   for an item; the query rows stream past both in steps of up to 128, by TMA as
-//   they lie, and both operands are exact. Each tile has its set of warps and its
-//   buffer of S: most of it goes to registers at once, so that the next product runs
-//   under the exponentials. The bound is the tensor core (2 dim flops a position and
+//   they lie, and both operands are exact. Each of the two tiles has its eight warps
+//   and its buffer of S. The bound is the tensor core (2 dim flops a position and
 //   row) and the exponentials beside it.
 //
 // Sums are fp32: of a step first, then over the steps.
@@ -39,10 +38,10 @@
 // request's tiles are taken from both ends in turn, since the last ones are seen
 // by fewer rows.
 //
-// Per CTA: warps 0-7 convert and sum (two sets of a warp for each 32 positions: of
-// two tiles each has one, so that one's exponentials run while the other waits),
-// warp 8 brings K, warp 9 issues the products, warp 10 walks the items, lists them for
-// the others and brings Q, warp 11 lse and the pieces of q.
+// Per CTA: warps 0-15 convert and sum (enough of them that the exponentials of some
+// run while others wait for their product), warp 16 brings K, warp 17 issues the
+// products, warp 18 walks the items, lists them for the others and brings Q, warp 19
+// lse and the pieces of q.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -57,9 +56,9 @@ namespace {
 
 constexpr int kTile = 128;                 // positions of an item
 constexpr int kStep = 128;                 // query rows of a step
-constexpr int kSumWarps = 8, kSum = 32 * kSumWarps;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kLWarp = 11;
-constexpr int kThreads = 32 * (kLWarp + 1);   // (12 warps: 168 registers a thread)
+constexpr int kSumWarps = 16;
+constexpr int kProducerWarp = 16, kMmaWarp = 17, kQWarp = 18, kLWarp = 19;
+constexpr int kThreads = 32 * (kLWarp + 1);   // (96 registers a thread)
 constexpr int kMetaSlots = 32;
 constexpr int kItems = 32;                 // slots of the list of items
 constexpr int kLook = 4;                   // items whose pages are looked up at once
@@ -83,9 +82,10 @@ struct Layout {
   static constexpr int kQ = kK + kNK * kKBytes;
   static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
   static constexpr int kBars = kLse + kNL * kStep * 12;
-  static constexpr int kMeta = kBars + 128 * 8;               // kMetaSlots x float4
+  static constexpr int kMeta = kBars + 136 * 8;               // kMetaSlots x float4
   static constexpr int kList = kMeta + kMetaSlots * 16;       // kItems x Item
-  static constexpr int kMisc = kList + kItems * 64;           // tmem slot, start of work, scan
+  static constexpr int kOther = kList + kItems * 64;          // 4 x kTile sums
+  static constexpr int kMisc = kOther + 4 * kTile * 4;        // tmem slot, start of work, scan
   static constexpr int kEnd = kMisc + 32 + 8 * (kThreads / 32);
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -108,10 +108,12 @@ enum Bar {
   kSFree = 53,      // kNS: S read
   kCFull = 56,      // 2: more rows: S of a set ready
   kCFree = 58,      // 2: read
-  kDrain = 60,
-  kIFull = 61,      // kItems: an item is in the list
-  kIEmpty = 93,     // every reader is done with it
-  kNumBars = 125
+  kXFull = 60,      // 4: the other half's sums of a tile written, two slots each
+  kXFree = 64,      // 4: read
+  kDrain = 68,
+  kIFull = 69,      // kItems: an item is in the list
+  kIEmpty = 101,    // every reader is done with it
+  kNumBars = 133
 };
 
 struct Params {
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LY::kBars);
   float4* meta = reinterpret_cast<float4*>(smem + LY::kMeta);
   Item* list = reinterpret_cast<Item*>(smem + LY::kList);
+  float* other = reinterpret_cast<float*>(smem + LY::kOther);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::kMisc);
   int64_t* start_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 8);   // request, cost before it
   int64_t* scan_s = reinterpret_cast<int64_t*>(smem + LY::kMisc + 32);
@@ -328,12 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if (i >= kAFull && i < kAFull + 2) n = kSum / 2;
+      if (i >= kAFull && i < kAFull + 2) n = 2 * kTile;
+      if (i >= kXFull && i < kXFree + 4) n = kTile;
       if (i >= kIEmpty && i < kIEmpty + kItems) n = kReaders;
       if (i >= kLFull && i < kLFull + kNL) n = 32;
       if (i >= kLEmpty && i < kLEmpty + kNL) n = kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
-      if (i >= kCFree && i < kCFree + 2) n = kSumWarps / 2;
+      if (i >= kCFree && i < kCFree + 2) n = kSumWarps / 2;   // of one place
       mbar_init(&bars[i], n);
     }
     mbar_fence_init();
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
   } else if (warp == kLWarp) {
     // --------------------------------------------- lse, and pieces of few rows
     constexpr int N = kStep / 32;              // rows of a lane: lane, lane + 32, ...
-    constexpr int D = 4;                       // steps whose lse is read at once
+    constexpr int D = 2;                       // steps whose lse is read at once
     int t_token[N], t_head[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -764,10 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         uint8_t* q8 = smem + LY::kQ + st * LY::kQBytes;
         float* factor = reinterpret_cast<float*>(smem + LY::kLse + sl * (kStep * 12)) + 2 * kStep;
         const __nv_bfloat16* q0 = p.q + (int64_t)w.t0 * p.q_stride + (int64_t)w.kvh * p.group * DIM + lane * E;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-          float x[8][E];
+        for (int r0 = 0; r0 < rows; r0 += 4) {
+          float x[4][E];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
+          for (int u = 0; u < 4; ++u) {
             const int r = r0 + u < rows ? r0 + u : rows - 1;
             const __nv_bfloat16* src = q0 + (r / p.group) * p.q_stride + (r % p.group) * DIM;
 #pragma unroll
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             }
           }
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
+          for (int u = 0; u < 4; ++u) {
             const int r = r0 + u;
             float a = 0.0f;
             bool nan = false;
@@ -840,36 +844,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     }
   } else {
     // --------------------------------------------------- convert and sum
-    const int quad = warp & 3, set = warp >> 2;
+    // Four sets of a warp for each 32 positions. Few rows: a set has a tile of the
+    // item. More: sets 0 and 2 have the first tile, 1 and 3 the second, each half of
+    // the dims to convert and half of a step's columns to sum.
+    const int quad = warp & 3, set = warp >> 2, place = set & 1, half = set >> 1;
     const int tok = quad * 32 + lane;          // position of the tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    // Items, tiles, S buffers and loads of Q so far (as the issuer counts).
-    uint32_t item = 0, tile = 0, g = 0, buf = 0, ql = 0, c_phase = 0;
-    const uint32_t c_full = smem_u32(&bars[kCFull + set]);
+    // Items, tiles, S buffers and loads of Q so far (as the issuer counts), and items
+    // of more rows that had a tile for this place.
+    uint32_t item = 0, tile = 0, g = 0, buf = 0, ql = 0, c_phase = 0, summed = 0;
+    const uint32_t c_full = smem_u32(&bars[kCFull + place]);
     bool held = false;
     struct Keys {
       float scale;
-      bool there, nan;     // the page is; a NaN among the position's codes
+      bool there, nan;     // the page is; a NaN among this thread's codes
     };
     auto read_meta = [&](uint32_t it) {
       const float4 m = meta[it & (kMetaSlots - 1)];
       return Keys{tok < kPage ? m.x : m.z, (tok < kPage ? m.y : m.w) != 0.0f, false};
     };
-    // K of tile number `it` to bf16, into this set's place.
+    // K of tile number `it` to bf16, this thread's half of the dims, into its place.
     auto convert = [&](uint32_t it, Keys* keys) {
       const int st = (int)(it % NK);
       if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kKFull + st], (it / NK) & 1u))) return false;
       *keys = read_meta(it);
       const uint8_t* src = smem + LY::kK + st * LY::kKBytes;
       uint32_t bad = 0;
-      const uint32_t t_a = tmem + lane_base + LY::kA + set * LY::kACols;
+      const uint32_t t_a = tmem + lane_base + LY::kA + place * LY::kACols + half * (DIM / 4);
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < DIM / 32; ++c) {
+      for (int c = 0; c < DIM / 64; ++c) {
         uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + swz<DIM>(tok, c * 32 + e * 16));
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              src + swz<DIM>(tok, half * (DIM / 2) + c * 32 + e * 16));
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -883,34 +892,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       keys->nan = (bad & 0x80808080u) != 0u;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars[kAFull + set]);
+      mbar_arrive(&bars[kAFull + place]);
       return true;
     };
-    // What the mass held before, read an item ahead by the set that adds to it: the
-    // sets take an item's tiles in turn (or, where few rows have one tile an item,
-    // the items), up to two a set.
-    auto first_mine = [&](const Item& v, uint32_t it) {
-      return v.single ? (int)(it + set) & 1 : set;
+    // The tile of an item whose mass this thread adds to, or -1. (Where few rows have
+    // one tile an item, the sets take the items in turn.)
+    auto mine = [&](const Item& v, uint32_t it) {
+      if (v.single) return (int)(it & 3) == set ? 0 : -1;
+      return set < v.nb && (v.few || half == 0) ? set : -1;
     };
-    struct Two {
-      float a, b;
-    };
+    // What the mass held before is read an item ahead.
     float* row = nullptr;      // this thread's position of the next item's head's tile 0
     auto held_mass = [&](const Item& v, uint32_t it) {
       if (!v.same)
         row = p.mass + ((int64_t)v.r * p.c.kv_heads + v.kvh) * p.mass_stride + tok;
-      auto get = [&](int u) {
-        if (u >= v.nb) return 0.0f;
-        const int t0 = (u < 2 ? (u ? v.tile[1] : v.tile[0]) : (u == 2 ? v.tile[2] : v.tile[3])) * kTile;
-        return t0 + tok < v.len && t0 + tok < v.raw - v.n ? row[t0] : 0.0f;
-      };
-      const int u = first_mine(v, it);
-      return Two{get(u), get(u + 2)};
+      const int u = mine(v, it);
+      if (u < 0) return 0.0f;
+      const int t0 = v.tile[u] * kTile;
+      return t0 + tok < v.len && t0 + tok < v.raw - v.n ? row[t0] : 0.0f;
     };
     // The item after the present one is looked at early (and read again when it is
     // its turn: kept in registers it would push others out).
     Keys keys{0.0f, false, false}, next{0.0f, false, false};
-    Two old{0.0f, 0.0f}, old_next{0.0f, 0.0f};
+    float old = 0.0f, old_next = 0.0f;
     bool more = false, ahead = false;
     auto look_ahead = [&](uint32_t it) {
       const uint32_t slot = it % kItems;
@@ -920,11 +924,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       }
       const Item& v = list[slot];
       more = v.nb > 0;
-      ahead = !v.few && set < v.nb;
+      ahead = !v.few && place < v.nb;
       if (more) old_next = held_mass(v, it);
     };
     look_ahead(0);
-    if (ahead && !failed && !convert(set, &next)) failed = true;
+    if (ahead && !failed && !convert(place, &next)) failed = true;
     while (more && !failed) {
       const Item now = take(item);
       keys = next;
@@ -936,14 +940,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       look_ahead(item + 1);
       if (failed) break;
       // The next item's K, as soon as the last product of this one's is done.
-      if (ahead && now.few && !convert(tile + now.nb + set, &next)) {
+      if (ahead && now.few && !convert(tile + now.nb + place, &next)) {
         failed = true;
         break;
       }
       // (A page outside the pool adds nothing.)
-      auto put = [&](int pos0, float before, bool there, float total) {
+      auto put = [&](int pos0, bool there, float total) {
         const int pos = pos0 + tok;
-        if (pos < now.len && (there || pos >= base)) at[pos0] = before + (there ? total : 0.0f);
+        if (pos < now.len && (there || pos >= base)) at[pos0] = old + (there ? total : 0.0f);
       };
       if (now.few) {
         if (!now.same) ++ql;
@@ -955,24 +959,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           break;
         }
         tc_fence_after();
-        const int u0 = first_mine(now, item), mine = u0 >= now.nb ? 0 : (u0 + 2 >= now.nb ? 1 : 2);
-        if (mine > 0) {
+        const int u = mine(now, item);
+        if (u >= 0) {
           const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
           const int* vs = reinterpret_cast<const int*>(ls) + kStep;
           const int r8 = (rows + 7) & ~7, cols = (3 * r8 + 15) & ~15;
-          const uint32_t t_s = tmem + lane_base + buf * kStep + u0 * cols;
-          const Keys k0 = read_meta(tile + u0), k1 = mine > 1 ? read_meta(tile + u0 + 2) : k0;
-          const int p0 = (u0 ? now.tile[1] : now.tile[0]) * kTile;
-          const int p1 = mine > 1 ? (u0 ? now.tile[3] : now.tile[2]) * kTile : p0;
-          float2 acc[2][2] = {};
-          // Eight rows of both tiles.
+          const uint32_t t_s = tmem + lane_base + buf * kStep + u * cols;
+          const Keys k0 = read_meta(tile + u);
+          const int tile_u = u == 0 ? now.tile[0] : (u == 1 ? now.tile[1] : (u == 2 ? now.tile[2]
+                                                                                 : now.tile[3]));
+          const int pos0 = tile_u * kTile, pos = pos0 + tok;
+          const float2 ks = make_float2(k0.scale, k0.scale), w5 = make_float2(0x1p-5f, 0x1p-5f);
+          float2 acc[2] = {};
           for (int c = 0; c < rows; c += 8) {
-            float x[2][3][8];
+            float x[3][8];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-              if (u < mine)
-#pragma unroll
-                for (int z = 0; z < 3; ++z) tmem_ld<8>(t_s + 2 * u * cols + z * r8 + c, x[u][z]);
+            for (int z = 0; z < 3; ++z) tmem_ld<8>(t_s + z * r8 + c, x[z]);
             const float4 l0 = *reinterpret_cast<const float4*>(ls + c);
             const float4 l1 = *reinterpret_cast<const float4*>(ls + c + 4);
             const float4 f0 = *reinterpret_cast<const float4*>(ls + 2 * kStep + c);
@@ -981,41 +983,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
                                  make_float2(l1.x, l1.y), make_float2(l1.z, l1.w)};
             const float2 f[4] = {make_float2(f0.x, f0.y), make_float2(f0.z, f0.w),
                                  make_float2(f1.x, f1.y), make_float2(f1.z, f1.w)};
-            const float2 w5 = make_float2(0x1p-5f, 0x1p-5f);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (u >= mine) continue;
+            for (int z = 0; z < 3; ++z) tmem_fence<8>(x[z]);
+            float2 y[4];
 #pragma unroll
-              for (int z = 0; z < 3; ++z) tmem_fence<8>(x[u][z]);
-              const float scale = u ? k1.scale : k0.scale;
-              const int pos0 = u ? p1 : p0, pos = pos0 + tok;
-              const float2 ks = make_float2(scale, scale);
-              float2 y[4];
+            for (int e = 0; e < 4; ++e) {
+              y[e] = fma2(make_float2(x[2][2 * e], x[2][2 * e + 1]), w5,
+                          make_float2(x[1][2 * e], x[1][2 * e + 1]));
+              y[e] = fma2(y[e], w5, make_float2(x[0][2 * e], x[0][2 * e + 1]));
+              y[e] = fma2(y[e], mul2(f[e], ks), l[e]);
+            }
+            // Rows that do not see the position; columns behind the rows hold anything.
+            if (pos0 + kTile - 1 > base || c + 8 > rows) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                y[e] = fma2(make_float2(x[u][2][2 * e], x[u][2][2 * e + 1]), w5,
-                            make_float2(x[u][1][2 * e], x[u][1][2 * e + 1]));
-                y[e] = fma2(y[e], w5, make_float2(x[u][0][2 * e], x[u][0][2 * e + 1]));
-                y[e] = fma2(y[e], mul2(f[e], ks), l[e]);
+                const int2 v = *reinterpret_cast<const int2*>(vs + c + 2 * e);
+                if (pos >= v.x) y[e].x = -INFINITY;
+                if (pos >= v.y) y[e].y = -INFINITY;
               }
-              // Rows that do not see the position; columns behind the rows hold anything.
-              if (pos0 + kTile - 1 > base || c + 8 > rows) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int2 v = *reinterpret_cast<const int2*>(vs + c + 2 * e);
-                  if (pos >= v.x) y[e].x = -INFINITY;
-                  if (pos >= v.y) y[e].y = -INFINITY;
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[u][e & 1] = add2(acc[u][e & 1], make_float2(ex2(y[e].x), ex2(y[e].y)));
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[e & 1] = add2(acc[e & 1], make_float2(ex2(y[e].x), ex2(y[e].y)));
           }
           tc_fence_before();
-          auto sum = [&](const float2* a) { return (a[0].x + a[1].x) + (a[0].y + a[1].y); };
-          put(p0, old.a, k0.there, sum(acc[0]));
-          if (mine > 1) put(p1, old.b, k1.there, sum(acc[1]));
+          put(pos0, k0.there, (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kSFree + buf]);
@@ -1025,8 +1017,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         ++item;
         continue;
       }
-      const int pos0 = (set ? now.tile[1] : now.tile[0]) * kTile, pos = pos0 + tok;   // this set's tile
-      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of it
+      const int pos0 = (place ? now.tile[1] : now.tile[0]) * kTile, pos = pos0 + tok;
+      const bool edge = pos0 + kTile - 1 > base;   // some row does not see all of the tile
+      const bool work = place < now.nb;
+      const float2 ks = make_float2(keys.scale, keys.scale);
       float total = 0.0f;
       for (int s = 0; s < now.steps; ++s) {
         if (!now.same) ++ql;
@@ -1035,14 +1029,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
         // (The product was issued when its lse was there. A set without a tile only
         // goes along.)
-        const bool work = set < now.nb;
         const bool ok = work ? mbar_wait_at(c_full, c_phase)
                              : mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
         }
-        if (ahead && s + 1 == now.steps && !convert(tile + now.nb + set, &next)) {
+        if (ahead && s + 1 == now.steps && !convert(tile + now.nb + place, &next)) {
           failed = true;
           break;
         }
@@ -1050,9 +1043,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           c_phase ^= 1u;
           tc_fence_after();
           float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-          const uint32_t t_s = tmem + lane_base + set * kStep;
+          const uint32_t t_s = tmem + lane_base + place * kStep;
           // Columns of 8. ls holds minus the lse.
-          const float2 ks = make_float2(keys.scale, keys.scale);
           auto add8 = [&](const float* x, int c, bool masked) {
             const float4 l0 = *reinterpret_cast<const float4*>(ls + c);
             const float4 l1 = *reinterpret_cast<const float4*>(ls + c + 4);
@@ -1077,37 +1069,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             acc0 = add2(acc0, make_float2(ex2(d.x), ex2(d.y)));
             acc1 = add2(acc1, make_float2(ex2(e.x), ex2(e.y)));
           };
-          const int here = s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now.n, now.first, s).rows;
-          if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile)) {
-            // 32 columns at a time; the last ones come once the first are done.
-            float x[3][32];
-            auto add32 = [&](const float* v, int c) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) add8(v + 8 * e, c + 8 * e, false);
-            };
-#pragma unroll
-            for (int c = 0; c < 3; ++c) tmem_ld32(t_s + 32 * c, x[c]);
-#pragma unroll
-            for (int c = 0; c < 3; ++c) tmem_fence<32>(x[c]);
-            add32(x[0], 0);
-            tmem_ld32(t_s + 96, x[0]);
-            add32(x[1], 32);
-            tmem_fence<32>(x[0]);
+          auto let_go = [&] {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kCFree + set]);
-            add32(x[2], 64);
-            add32(x[0], 96);
+            if (lane == 0) mbar_arrive(&bars[kCFree + place]);
+          };
+          const int here =
+              s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now.n, now.first, s).rows;
+          const int c0 = half * 64;
+          if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile)) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              float x[32];
+              tmem_ld32(t_s + c0 + c, x);
+              tmem_fence<32>(x);
+              if (c == 32) let_go();
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) add8(x + e, c0 + c + e, false);
+            }
           } else {
-            for (int c = 0; c < here; c += 8) {
+            for (int c = c0; c < here && c < c0 + 64; c += 8) {
               float x[8];
               tmem_ld<8>(t_s + c, x);
               tmem_fence<8>(x);
               add8(x, c, true);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kCFree + set]);
+            let_go();
           }
           total += (acc0.x + acc1.x) + (acc0.y + acc1.y);
         }
@@ -1117,8 +1104,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         }
       }
       if (failed) break;
-      // (A NaN key makes its position NaN.)
-      if (set < now.nb) put(pos0, old.a, keys.there, keys.nan ? NAN : total);
+      if (work) {
+        // Both halves together; a NaN key makes its position NaN.
+        if (keys.nan) total = NAN;
+        const uint32_t slot = place * 2 + (summed & 1);
+        bool ok;
+        if (half == 1) {
+          ok = summed < 2 || mbar_wait_long(&bars[kXFree + slot], ((summed >> 1) - 1) & 1u);
+          if (ok) {
+            other[slot * kTile + tok] = total;
+            mbar_arrive(&bars[kXFull + slot]);
+          }
+        } else {
+          ok = mbar_wait_long(&bars[kXFull + slot], (summed >> 1) & 1u);
+          if (ok) {
+            total += other[slot * kTile + tok];
+            mbar_arrive(&bars[kXFree + slot]);
+            put(pos0, keys.there, total);
+          }
+        }
+        ++summed;
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+      }
       tile += now.nb;
       ++item;
     }
