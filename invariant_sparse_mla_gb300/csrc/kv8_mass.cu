@@ -99,7 +99,7 @@ struct Layout {
 enum Bar {
   kKFull = 0,       // <= 8: K landed
   kKEmpty = 8,      // K converted, or its product done
-  kQFull = 16,      // <= 8: Q landed
+  kQFull = 16,      // <= 8: Q landed, and its lse is written
   kQEmpty = 24,     // product done
   kLFull = 32,      // kNL: lse written
   kLEmpty = 40,     // lse read
@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (i >= kXFull && i < kXFree + 4) n = kTile;
       if (i >= kIEmpty && i < kIEmpty + kItems) n = kReaders;
       if (i >= kLFull && i < kLFull + kNL) n = 32;
+      if (i >= kQFull && i < kQFull + NQ) n = 2;
       if (i >= kLEmpty && i < kLEmpty + kNL) n = kSumWarps;
       if (i >= kSFree && i < kSFree + kNS) n = kSumWarps;
       if (i >= kCFree && i < kCFree + 2) n = kSumWarps / 2;   // of one place
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
     // An item of one step may use the load of Q of the one before it (`held`), which
     // is let go when the next comes. `phases`: bit u is that of place u's tiles.
     // (A buffer's first use waits for nothing: the phase before the first is over.)
-    Ring tile, s_free, load, lse;
+    Ring tile, s_free, load;
     uint32_t phases = 0, held_at = 0, c_free[2] = {1u, 1u};
     s_free.phase = 1u;
     bool held = false, was_few = false;
@@ -572,10 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         const int n = (3 * ((rows + 7) & ~7) + 15) & ~15;
         const uint32_t idesc = make_idesc_e4m3(kTile, n, 0, 0);
         if (!same) {
-          ok = wait(kQFull, load.at, load.phase) && wait(kLFull, lse.at, lse.phase) && ok;
+          ok = wait(kQFull, load.at, load.phase) && ok;
           held_at = load.at;
           next(load, NQ);
-          next(lse, kNL);
         }
         ok = wait(kSFree, s_free.at, s_free.phase) && ok;
         const uint64_t b = q8_desc + (uint64_t)(held_at * (LY::kQBytes >> 4));
@@ -599,11 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       } else {
         for (int s = 0; s < steps; ++s) {
           if (!same) {
-            // (And the lse, so that who waits for the product needs not.)
-            ok = wait(kQFull, load.at, load.phase) && wait(kLFull, lse.at, lse.phase) && ok;
+            ok = wait(kQFull, load.at, load.phase) && ok;
             held_at = load.at;
             next(load, NQ);
-            next(lse, kNL);
           }
           const int n = s + 1 < steps && p.chunks == 1 ? (capacity + 15) & ~15
                                                        : uni((step_of(p, x.n, x.first, s).rows + 15) & ~15);
@@ -743,16 +741,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         ls[0] = in && l != -INFINITY ? -l * kLog2e : -INFINITY;
         reinterpret_cast<int*>(ls)[kStep] = in ? seen + token : INT_MIN;
       };
+      // (Its arrival counts for Q's stage too, which has to be free for that.)
       auto wait_slot = [&] {
-        return __all_sync(0xffffffffu, ql < kNL || mbar_wait_long(&bars[kLEmpty + ql % kNL],
-                                                                  (ql / kNL - 1) & 1u));
+        const bool ok = (ql < NQ || mbar_wait_long(&bars[kQEmpty + ql % NQ], (ql / NQ - 1) & 1u)) &&
+                        (ql < kNL || mbar_wait_long(&bars[kLEmpty + ql % kNL], (ql / kNL - 1) & 1u));
+        return __all_sync(0xffffffffu, ok);
+      };
+      auto arrive = [&] {
+        mbar_arrive(&bars[kLFull + ql % kNL]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kQFull + ql % NQ]);
+        ++ql;
       };
       if (w.few) {
         const uint32_t st = ql % NQ, sl = ql % kNL;
         const int rows = w.n * p.group, r8 = (rows + 7) & ~7;
-        if (!__all_sync(0xffffffffu, ql < NQ || mbar_wait_long(&bars[kQEmpty + st],
-                                                               (ql / NQ - 1) & 1u)) ||
-            !wait_slot()) {
+        if (!wait_slot()) {
           failed = true;
           break;
         }
@@ -809,8 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bars[kLFull + sl]);
-        ++ql;
+        arrive();
         continue;
       }
       for (int s0 = 0; s0 < w.steps && !failed; s0 += D) {
@@ -824,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
                           ? lse0[(int64_t)(x.token + t_token[i]) * p.heads + x.head + t_head[i]]
                           : 0.0f;
         }
-        for (int d = 0; d < D && s0 + d < w.steps; ++d, ++ql) {
+        for (int d = 0; d < D && s0 + d < w.steps; ++d) {
           if (!wait_slot()) {
             failed = true;
             break;
@@ -838,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
               if (d == e) v = l[e][i];
             put(ql % kNL, i, lane + 32 * i < x.rows, x.token + t_token[i], v);
           }
-          mbar_arrive(&bars[kLFull + ql % kNL]);
+          arrive();
         }
       }
     }
