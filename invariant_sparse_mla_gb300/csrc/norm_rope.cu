@@ -12,8 +12,10 @@
 // Layout. A row is cut into units of two 16-byte chunks so that a unit holds
 // both halves of the pairs it rotates (dims i and i + rot / 2 are 8 chunks apart
 // with rot 128): no exchange between lanes but the sum of squares. LANES lanes
-// hold a row (8 for D = 128), UNITS units each. A CTA takes TOK tokens and works
-// out their sines and cosines once, in shared memory, for all heads of both sides.
+// hold a row (8 for D = 128), UNITS units each. A warp takes a token (or, of few
+// tokens, some of a token's heads): what all heads share, the weights and the sines
+// and cosines, it has in registers (or, with several units a lane, in shared memory)
+// and works out once. A row is then about 100 instructions for 32 / LANES of them.
 //
 // The bound is HBM, 4 bytes an element.
 
@@ -21,6 +23,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kv8_common.cuh"
 #include "norm_rope.h"
 
 namespace dsmla {
@@ -28,7 +31,7 @@ namespace dsmla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxAngles = 1024;   // of one CTA
+constexpr int kWarps = kThreads / 32;
 
 struct Side {
   const __nv_bfloat16* x;
@@ -42,8 +45,7 @@ struct Side {
 struct Params {
   Side q, k;
   int64_t tokens;
-  int per_cta;                 // tokens of a CTA
-  int row_step;                // rows of a CTA's tokens that the CTAs of grid.y share: stride
+  int splits, part;            // warps of a token, and the heads of each
   int units;                   // of a row
   int norm_dim, rot_chunk, rot_chunks;   // first rotated chunk, number of them
   const int32_t* positions;
@@ -69,185 +71,216 @@ __device__ __forceinline__ float2 rotation(int pos, float freq) {
   return cs;
 }
 
-__device__ __forceinline__ void unpack(uint4 v, float* x) {
+__device__ __forceinline__ void unpack(uint4 v, float2* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack(const float* x) {
+__device__ __forceinline__ uint4 pack(const float2* x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[i].x, x[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// What turns a float2 of values. Halves: two pairs (u from one chunk, v from the
+// other); u' = u c + v ns, v' = v c + u s. Neighbours: one pair (u, v); with c twice
+// and (-s, s), the pair times c plus the swapped pair times that.
+struct Turn {
+  float2 c, s, ns;
+};
+
 template <int LANES, int UNITS, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
-  constexpr int kRows = kThreads / LANES;      // rows at a time
-  __shared__ float2 cs[kMaxAngles];
-  const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
-  const int heads = p.q.heads + p.k.heads;
-  const int64_t token0 = (int64_t)blockIdx.x * p.per_cta;
-  const int here = p.tokens - token0 < p.per_cta ? (int)(p.tokens - token0) : p.per_cta;
-  const int rows = here * heads;
-  const int half = p.rot_chunks * 4;           // angles of a token
+__global__ void __launch_bounds__(kThreads, UNITS == 1 ? 3 : (UNITS < 4 ? 2 : 1)) norm_rope_kernel(const Params p) {
+  constexpr int kRows = 32 / LANES;            // rows of a warp at a time
+  extern __shared__ float2 tables[];
+  const int lane32 = threadIdx.x & 31, lane = lane32 % LANES, group = lane32 / LANES;
+  const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t token = job / p.splits;
+  const int head0 = (int)(job % p.splits) * p.part;
   pdl_wait();
   pdl_trigger();
+  if (token >= p.tokens) return;
 
-  // The two chunks of unit u. Rotated by halves: chunk i of the first half and of
-  // the second; all others two neighbours in what is left.
-  auto chunks = [&](int u, int* c0, int* c1, bool* turn0, bool* turn1) {
+  // The token's angles.
+  const int half = p.rot_chunks * 4;
+  float2* cs = tables + (threadIdx.x >> 5) * half;
+  if (half > 0) {
+    const int pos = p.positions[token];
+    for (int i = lane32; i < half; i += 32) cs[i] = rotation(pos, p.inv_freq[i]);
+    __syncwarp();
+  }
+
+  // The two chunks of unit i of this lane, and whether they are turned. Rotated by
+  // halves: chunk u of the first half and of the second; all others two neighbours in
+  // what is left.
+  struct Place {
+    int c0, c1;
+    bool in, turn0, turn1;
+  };
+  auto place = [&](int i) {
+    const int u = lane + i * LANES;
+    Place x;
+    x.in = u < p.units;
     if constexpr (PAIRS) {
-      *c0 = 2 * u;
-      *c1 = 2 * u + 1;
-      *turn0 = (unsigned)(*c0 - p.rot_chunk) < (unsigned)p.rot_chunks;
-      *turn1 = (unsigned)(*c1 - p.rot_chunk) < (unsigned)p.rot_chunks;
+      x.c0 = 2 * u;
+      x.c1 = 2 * u + 1;
+      x.turn0 = x.in && (unsigned)(x.c0 - p.rot_chunk) < (unsigned)p.rot_chunks;
+      x.turn1 = x.in && (unsigned)(x.c1 - p.rot_chunk) < (unsigned)p.rot_chunks;
     } else {
       const int hc = p.rot_chunks / 2;
-      *turn0 = *turn1 = u < hc;
+      x.turn0 = x.turn1 = u < hc;
       if (u < hc) {
-        *c0 = p.rot_chunk + u;
-        *c1 = p.rot_chunk + hc + u;
+        x.c0 = p.rot_chunk + u;
+        x.c1 = p.rot_chunk + hc + u;
       } else {
         const int v = 2 * (u - hc);
-        *c0 = v < p.rot_chunk ? v : v + p.rot_chunks;
-        *c1 = v + 1 < p.rot_chunk ? v + 1 : v + 1 + p.rot_chunks;
+        x.c0 = v < p.rot_chunk ? v : v + p.rot_chunks;
+        x.c1 = v + 1 < p.rot_chunk ? v + 1 : v + 1 + p.rot_chunks;
       }
     }
+    return x;
   };
-  auto row_at = [&](int row, const Side** side, int64_t* token, int* head) {
-    *token = token0 + row / heads;
-    const int h = row % heads;
-    *side = h < p.q.heads ? &p.q : &p.k;
-    *head = h < p.q.heads ? h : h - p.q.heads;
+  // The turns of a unit: [0..3] for the first chunk's float2s, [4..7] the second's
+  // (halves: the same four for both).
+  auto turn_of = [&](const Place& x, int e) {
+    Turn t;
+    if constexpr (PAIRS) {
+      const float2 a = cs[((e < 4 ? x.c0 : x.c1) - p.rot_chunk) * 4 + (e & 3)];
+      t.c = make_float2(a.x, a.x);
+      t.s = t.ns = make_float2(-a.y, a.y);
+    } else {
+      const float4 a =
+          *reinterpret_cast<const float4*>(cs + (x.c0 - p.rot_chunk) * 8 + 2 * (e & 3));
+      t.c = make_float2(a.x, a.z);
+      t.s = make_float2(a.y, a.w);
+      t.ns = make_float2(-a.y, -a.w);
+    }
+    return t;
   };
+  constexpr int kTurns = PAIRS ? 8 : 4;
+  constexpr bool kKeep = UNITS == 1;           // weights and turns in registers
+  const Place only = place(0);
+  Turn turns[kKeep ? kTurns : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int e = 0; e < kTurns; ++e)
+      if (e < 4 ? only.turn0 : only.turn1) turns[e] = turn_of(only, e);
+  }
 
-  uint4 raw[UNITS][2];
-  auto load = [&](int row) {
-    if (row >= rows) return;
-    const Side* side;
-    int64_t token;
-    int head;
-    row_at(row, &side, &token, &head);
-    const uint4* x = reinterpret_cast<const uint4*>(side->x + token * side->x_stride) +
-                     (int64_t)head * (2 * p.units);
+  // Some heads of one side.
+  auto side = [&](const Side& sd, int lo, int hi) {
+    if (lo >= hi) return;
+    const bool norm = sd.weight != nullptr;
+    const uint4* w4 = reinterpret_cast<const uint4*>(sd.weight);
+    float2 weight[kKeep ? 8 : 1];
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-      const int u = lane + i * LANES;
-      if (u < p.units) {
-        int c0, c1;
-        bool t0, t1;
-        chunks(u, &c0, &c1, &t0, &t1);
-        raw[i][0] = x[c0];
-        raw[i][1] = x[c1];
-      }
+      for (int e = 0; e < 8; ++e) weight[e] = make_float2(1.0f, 1.0f);
+      if (norm && only.in && 8 * only.c0 < p.norm_dim) unpack(w4[only.c0], weight);
+      if (norm && only.in && 8 * only.c1 < p.norm_dim) unpack(w4[only.c1], weight + 4);
     }
-  };
-  int row = blockIdx.y * kRows + group;
-  load(row);
-  for (int i = tid; i < here * half; i += kThreads)
-    cs[i] = rotation(p.positions[token0 + i / half], p.inv_freq[i % half]);
-  __syncthreads();
-
-  // Every lane of a row's group runs the same turns, and whole warps stay
-  // together: rows past the end are skipped inside.
-  for (int base = blockIdx.y * kRows; base < rows; base += p.row_step, row += p.row_step) {
-    const bool on = row < rows;
-    float x[UNITS][16];
-    const Side* side = &p.q;
-    int64_t token = token0;
-    int head = 0;
-    if (on) row_at(row, &side, &token, &head);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-      const int u = lane + i * LANES;
-      if (on && u < p.units) {
-        unpack(raw[i][0], x[i]);
-        unpack(raw[i][1], x[i] + 8);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[i][e] = 0.0f;
-      }
-    }
-    load(row + p.row_step);   // the next row's, while this one is worked on
-    if (p.norm_dim > 0) {
+    const uint4* from = reinterpret_cast<const uint4*>(sd.x + token * sd.x_stride);
+    uint4* to = reinterpret_cast<uint4*>(sd.out + token * sd.out_stride);
+    const int row_chunks = 2 * p.units;
+    uint4 raw[UNITS][2];
+    auto load = [&](int h) {
+      if (h >= hi) return;
 #pragma unroll
       for (int i = 0; i < UNITS; ++i) {
-        int c0, c1;
-        bool t0, t1;
-        chunks(lane + i * LANES, &c0, &c1, &t0, &t1);
-        if (8 * c0 < p.norm_dim) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum = __fmaf_rn(x[i][e], x[i][e], sum);
+        const Place x = UNITS == 1 ? only : place(i);
+        if (x.in) {
+          raw[i][0] = from[(int64_t)h * row_chunks + x.c0];
+          raw[i][1] = from[(int64_t)h * row_chunks + x.c1];
         }
-        if (8 * c1 < p.norm_dim) {
+      }
+    };
+    load(lo + group);
+    // (Whole warps stay together: a group behind the last head works on nothing.)
+    for (int base = lo; base < hi; base += kRows) {
+      const int h = base + group;
+      const bool on = h < hi;
+      float2 x[UNITS][8];
 #pragma unroll
-          for (int e = 8; e < 16; ++e) sum = __fmaf_rn(x[i][e], x[i][e], sum);
+      for (int i = 0; i < UNITS; ++i) {
+        const Place c = UNITS == 1 ? only : place(i);
+        if (on && c.in) {
+          unpack(raw[i][0], x[i]);
+          unpack(raw[i][1], x[i] + 4);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] = make_float2(0.0f, 0.0f);
+        }
+      }
+      load(h + kRows);   // the next row's, while this one is worked on
+      if (norm) {
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+          const Place c = UNITS == 1 ? only : place(i);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (8 * (e < 4 ? c.c0 : c.c1) < p.norm_dim) sum = fma2(x[i][e], x[i][e], sum);
+        }
+        float total = sum.x + sum.y;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const float r = rsqrtf(__fmaf_rn(total, p.inv_norm, p.eps));
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+          const Place c = UNITS == 1 ? only : place(i);
+          float2 g[8];
+          if constexpr (!kKeep) {
+            if (c.in && 8 * c.c0 < p.norm_dim) unpack(w4[c.c0], g);
+            if (c.in && 8 * c.c1 < p.norm_dim) unpack(w4[c.c1], g + 4);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (8 * (e < 4 ? c.c0 : c.c1) < p.norm_dim)
+              x[i][e] = mul2(mul2(x[i][e], r2), kKeep ? weight[e] : g[e]);
         }
       }
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if (!on) continue;
-    const __nv_bfloat16* w = side->weight;
-    const float r = w != nullptr ? rsqrtf(__fmaf_rn(sum, p.inv_norm, p.eps)) : 1.0f;
-    const float2* turn = cs + (row / heads) * half;
-    uint4* out = reinterpret_cast<uint4*>(side->out + token * side->out_stride) +
-                 (int64_t)head * (2 * p.units);
+      for (int i = 0; i < UNITS; ++i) {
+        const Place c = UNITS == 1 ? only : place(i);
+        if constexpr (PAIRS) {
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-      const int u = lane + i * LANES;
-      if (u >= p.units) continue;
-      int c[2];
-      bool t[2];
-      chunks(u, &c[0], &c[1], &t[0], &t[1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (w != nullptr && 8 * c[h] < p.norm_dim) {
-          float g[8];
-          unpack(reinterpret_cast<const uint4*>(w)[c[h]], g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][8 * h + e] *= r * g[e];
-        }
-      }
-      if constexpr (PAIRS) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!t[h]) continue;
-          const float2* a = turn + (c[h] - p.rot_chunk) * 4;
+          for (int e = 0; e < 8; ++e) {
+            if (!(e < 4 ? c.turn0 : c.turn1)) continue;
+            const Turn t = kKeep ? turns[e] : turn_of(c, e);
+            const float2 v = x[i][e];
+            x[i][e] = fma2(v, t.c, mul2(make_float2(v.y, v.x), t.s));
+          }
+        } else if (c.turn0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float* y = x[i] + 8 * h + 2 * e;
-            const float y0 = y[0], y1 = y[1];
-            y[0] = y0 * a[e].x - y1 * a[e].y;
-            y[1] = y1 * a[e].x + y0 * a[e].y;
+            const Turn t = kKeep ? turns[e] : turn_of(c, e);
+            const float2 u = x[i][e], v = x[i][4 + e];
+            x[i][e] = fma2(u, t.c, mul2(v, t.ns));
+            x[i][4 + e] = fma2(v, t.c, mul2(u, t.s));
           }
         }
-      } else if (t[0]) {
-        const float2* a = turn + u * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y0 = x[i][e], y1 = x[i][8 + e];
-          x[i][e] = y0 * a[e].x - y1 * a[e].y;
-          x[i][8 + e] = y1 * a[e].x + y0 * a[e].y;
+        if (on && c.in) {
+          to[(int64_t)h * row_chunks + c.c0] = pack(x[i]);
+          to[(int64_t)h * row_chunks + c.c1] = pack(x[i] + 4);
         }
       }
-      out[c[0]] = pack(x[i]);
-      out[c[1]] = pack(x[i] + 8);
     }
-  }
+  };
+  const int end = head0 + p.part;
+  side(p.q, head0, end < p.q.heads ? end : p.q.heads);
+  const int k0 = head0 - p.q.heads, k1 = end - p.q.heads;
+  side(p.k, k0 > 0 ? k0 : 0, k1 < p.k.heads ? k1 : p.k.heads);
 }
 
 template <int LANES, int UNITS>
 cudaError_t launch_shape(const NormRopeArgs& a, cudaStream_t stream) {
-  constexpr int kRows = kThreads / LANES;
+  constexpr int kRows = 32 / LANES;
   Params p;
   auto side = [](const NormRopeSide& s) {
     return Side{static_cast<const __nv_bfloat16*>(s.x), s.x_stride,
@@ -258,32 +291,28 @@ cudaError_t launch_shape(const NormRopeArgs& a, cudaStream_t stream) {
   p.k = side(a.k);
   p.tokens = a.tokens;
   p.units = a.dim / 16;
-  p.norm_dim = a.q.weight != nullptr || a.k.weight != nullptr ? a.norm_dim : 0;
+  p.norm_dim = a.norm_dim;
   p.rot_chunk = a.rot_start / 8;
   p.rot_chunks = a.rot_dim / 8;
   p.positions = a.positions;
   p.inv_freq = a.inv_freq;
   p.eps = a.eps;
   p.inv_norm = a.norm_dim > 0 ? 1.0f / (float)a.norm_dim : 0.0f;
-  const int heads = a.q.heads + a.k.heads, half = a.rot_dim / 2;
-  // Few heads: several tokens a CTA, so that it has about four turns.
-  int per = 4 * kRows / heads;
-  if (half > 0 && per > kMaxAngles / half) per = kMaxAngles / half;
-  if (per < 1) per = 1;
-  // Fewer where that leaves SMs without work.
-  while (per > 1 && (a.tokens + per - 1) / per < 608) per /= 2;
-  p.per_cta = per;
-  const int64_t blocks = (a.tokens + per - 1) / per;
-  // A small call's rows are shared by several CTAs, one turn each.
-  int split = (per * heads + kRows - 1) / kRows;
-  if (blocks >= 152) split = 1;
-  if (split > 64) split = 64;
-  p.row_step = split * kRows;
-  const dim3 grid((unsigned)blocks, (unsigned)split);
-  return a.interleaved
-             ? launch_pdl(norm_rope_kernel<LANES, UNITS, true>, grid, dim3(kThreads), 0, stream, 1u, p)
-             : launch_pdl(norm_rope_kernel<LANES, UNITS, false>, grid, dim3(kThreads), 0, stream, 1u,
-                          p);
+  // A warp a token where that fills the GPU (32 warps an SM), else as many as it has
+  // turns of kRows heads.
+  const int heads = a.q.heads + a.k.heads, most = (heads + kRows - 1) / kRows;
+  const int64_t want = (152 * 32 + a.tokens - 1) / a.tokens;
+  p.splits = want < most ? (int)want : most;
+  const int turns = (most + p.splits - 1) / p.splits;
+  p.part = turns * kRows;
+  p.splits = (most + turns - 1) / turns;
+  const int64_t jobs = a.tokens * p.splits;
+  const dim3 grid((unsigned)((jobs + kWarps - 1) / kWarps));
+  const size_t smem = (size_t)kWarps * p.rot_chunks * 4 * sizeof(float2);
+  return a.interleaved ? launch_pdl(norm_rope_kernel<LANES, UNITS, true>, grid, dim3(kThreads),
+                                    smem, stream, 1u, p)
+                       : launch_pdl(norm_rope_kernel<LANES, UNITS, false>, grid, dim3(kThreads),
+                                    smem, stream, 1u, p);
 }
 
 }  // namespace
