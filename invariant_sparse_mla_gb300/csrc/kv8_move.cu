@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) kv8_accept_kernel(
 constexpr int kPlanThreads = 256;
 constexpr int kMoveThreads = 256;
 constexpr int kCluster = 8;            // CTAs of one (request, head, side)
-constexpr int kPagesPerCta = 2;        // a round
+constexpr int kRound = 4;              // pages that a CTA reads before it writes any
+constexpr int kBlock = 8;              // pages that it looks up at once
 
 // Which requests are cut, their new lengths, and the range that is ranked.
 __global__ void __launch_bounds__(kPlanThreads) kv8_evict_plan_kernel(const Kv8EvictArgs a) {
@@ -221,17 +222,23 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// A cluster per (request, head, side) walks the pages of the budget in rounds of
-// kCluster * kPagesPerCta: it reads what goes to them, waits for all its CTAs,
-// and writes.
+// A cluster per (request, head, side) takes the pages of the budget in turn, a block
+// of kCluster * kBlock at a time: where the positions come from, their scales and
+// masses are looked up first (three dependent loads, once for the block), then
+// the codes follow in rounds: all CTAs read what goes to their pages of the round, wait
+// for one another, and write. 32 requests of 8 heads x 128 held to 4096 positions:
+// 550 MB moved.
 template <int DIM>
 __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Kv8EvictArgs a) {
   constexpr int L = DIM / 16;                     // lanes of a row
   constexpr int ROWS = kMoveThreads / L;          // rows of a pass
   constexpr int PASSES = kPage / ROWS;            // of a page
-  constexpr int P = kPagesPerCta;
-  __shared__ float warp_top[2][P][kMoveThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int E = kBlock * kPage / kMoveThreads;   // places a thread looks up
+  __shared__ int from[kBlock * kPage];            // row of the pool's codes, or -1
+  __shared__ float scale[kBlock * kPage];
+  __shared__ float weight[kBlock * kPage];        // side 0: mass
+  __shared__ float warp_top[kBlock * 2];          // largest scale of half a page
+  const int tid = threadIdx.x, lane = tid & 31;
   const int rank = blockIdx.x % kCluster;
   const int64_t unit = blockIdx.x / kCluster;
   const int side = (int)(unit & 1);
@@ -256,56 +263,61 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Kv8E
   };
   auto part = [&](int64_t page) { return (page * 2 + side) * a.c.kv_heads + g; };
   const int col = tid % L, row0 = tid / L;
-  int turn = 0;
-  for (int b0 = 0; b0 < blocks; b0 += kCluster * P, turn ^= 1) {
-    uint4 v[P][PASSES];
-    float s[P][PASSES], m[P][PASSES];
-    bool moved[P][PASSES];
+  for (int b0 = 0; b0 < blocks; b0 += kCluster * kBlock) {
+    // Page i of the block that this CTA writes is b0 + i * kCluster + rank.
+    __syncthreads();               // the block before is written
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int b = b0 + i * kCluster + rank;
-      float top = 0.0f;
-#pragma unroll
-      for (int q = 0; q < PASSES; ++q) {
-        const int j = b * kPage + q * ROWS + row0;
-        moved[i][q] = false;
-        s[i][q] = 0.0f;
-        if (b < blocks && j < a.budget) {
-          const int p = source(j);
-          const int64_t t = part(table[p >> 6]);
-          s[i][q] = a.c.scales[t];
-          v[i][q] = reinterpret_cast<const uint4*>(a.c.pages + (t * kPage + (p & 63)) * DIM)[col];
-          if (side == 0 && col == 0) m[i][q] = mass[p];
-          moved[i][q] = p != j;
-          top = fmaxf(top, s[i][q]);
-        }
+    for (int e = 0; e < E; ++e) {
+      const int at = tid + e * kMoveThreads;
+      const int j = (b0 + at / kPage * kCluster + rank) * kPage + at % kPage;
+      int row = -1;
+      float s = 0.0f;
+      if (j < a.budget) {
+        const int p = source(j);
+        const int64_t t = part(table[p >> 6]);
+        row = (int)t * kPage + (p & 63);   // (below 2^31: the pool's rows are)
+        s = a.c.scales[t];
+        if (side == 0) weight[at] = mass[p];
       }
+      from[at] = row;
+      scale[at] = s;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) warp_top[turn][i][warp] = top;
+      for (int o = 16; o > 0; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+      if (lane == 0) warp_top[at / 32] = s;
     }
     __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+#pragma unroll 1
+    for (int i0 = 0; i0 < kBlock; i0 += kRound) {
+      // (The same for all CTAs of the cluster.)
+      if (b0 + i0 * kCluster >= blocks) break;
+      uint4 v[kRound][PASSES];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int b = b0 + i * kCluster + rank;
-      if (b >= blocks) continue;
-      float top = warp_top[turn][i][0];
+      for (int i = 0; i < kRound; ++i)
 #pragma unroll
-      for (int w = 1; w < kMoveThreads / 32; ++w) top = fmaxf(top, warp_top[turn][i][w]);
-      const int64_t t = part(table[b]);
+        for (int q = 0; q < PASSES; ++q) {
+          const int row = from[(i0 + i) * kPage + q * ROWS + row0];
+          if (row >= 0) v[i][q] = reinterpret_cast<const uint4*>(a.c.pages + (int64_t)row * DIM)[col];
+        }
+      cluster_arrive();
+      cluster_wait();
 #pragma unroll
-      for (int q = 0; q < PASSES; ++q) {
-        const int j = b * kPage + q * ROWS + row0;
-        if (j >= a.budget) continue;
-        const float ratio = __fdiv_rn(s[i][q], top);
-        if (moved[i][q] || ratio != 1.0f)
-          reinterpret_cast<uint4*>(a.c.pages + (t * kPage + (j & 63)) * DIM)[col] =
-              requantise(v[i][q], ratio);
-        if (side == 0 && col == 0 && moved[i][q]) mass[j] = m[i][q];
+      for (int i = 0; i < kRound; ++i) {
+        const int b = b0 + (i0 + i) * kCluster + rank;
+        if (b >= blocks) continue;
+        const float top = fmaxf(warp_top[2 * (i0 + i)], warp_top[2 * (i0 + i) + 1]);
+        const int64_t t = part(table[b]);
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) {
+          const int slot = q * ROWS + row0, at = (i0 + i) * kPage + slot;
+          const int to = (int)t * kPage + slot;
+          if (from[at] < 0) continue;
+          const float ratio = __fdiv_rn(scale[at], top);
+          if (from[at] != to || ratio != 1.0f)
+            reinterpret_cast<uint4*>(a.c.pages + (int64_t)to * DIM)[col] = requantise(v[i][q], ratio);
+          if (side == 0 && col == 0 && from[at] != to) mass[b * kPage + slot] = weight[at];
+        }
+        if (tid == 0) a.c.scales[t] = top;
       }
-      if (tid == 0) a.c.scales[t] = top;
     }
   }
 }
