@@ -499,8 +499,12 @@ size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_he
  *
  *  masks        uint64 [num_requests, next_n], 8-byte aligned.
  *
- * All else as for ds_kv8_decode, its workspace size included. With masks of a
- * chain (bit i set for i <= j) the results are those of ds_kv8_decode, bit for bit.
+ * All else as for ds_kv8_decode, but bt_stride is at most 2^20, and the workspace
+ * has ds_kv8_tree_decode_workspace_size() bytes. Trees of up to 40 rows (next_n *
+ * num_heads / num_kv_heads) are computed as by ds_kv8_decode, and with masks of a
+ * chain (bit i set for i <= j) the results are then the same, bit for bit; larger
+ * ones by tiles of 256 rows as in ds_kv8_prefill (q as precise as there), over spans
+ * of the context that follow from the request's length alone.
  */
 int ds_kv8_tree_decode(const void* q, int64_t q_stride, const uint64_t* masks,
                        const void* kv_pages, const float* kv_scales, int64_t num_pages,
@@ -508,6 +512,11 @@ int ds_kv8_tree_decode(const void* q, int64_t q_stride, const uint64_t* masks,
                        int64_t num_requests, int next_n, int num_heads, int num_kv_heads,
                        int head_dim, float scale, void* out, float* lse, void* workspace,
                        size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* Workspace bytes of ds_kv8_tree_decode (0 for an unsupported shape): up to 8
+ * spans for each row of q, or as for ds_kv8_decode. */
+size_t ds_kv8_tree_decode_workspace_size(int64_t num_requests, int next_n, int num_heads,
+                                         int num_kv_heads, int head_dim, int64_t bt_stride);
 
 /*
  * ds_kv8_prefill: the same attention for ragged prompts (or prompt chunks):

@@ -40,6 +40,7 @@ from .kv8 import (  # noqa: F401
     kv8_prefill,
     kv8_prefill_workspace_size,
     kv8_tree_decode,
+    kv8_tree_decode_workspace_size,
 )
 from .norm_rope import qk_norm_rope  # noqa: F401
 from .pages import (  # noqa: F401

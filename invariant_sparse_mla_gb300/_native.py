@@ -114,6 +114,8 @@ def lib():
         L.ds_kv8_tree_decode.restype = i32
         L.ds_kv8_tree_decode.argtypes = [vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, i32, i32, i32,
                                          i32, f32, vp, vp, vp, sz, vp, vp]
+        L.ds_kv8_tree_decode_workspace_size.restype = sz
+        L.ds_kv8_tree_decode_workspace_size.argtypes = [i64, i32, i32, i32, i32, i64]
         L.ds_kv8_mass.restype = i32
         L.ds_kv8_mass.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i32, i32,
                                   i32, f32, vp, i64, vp, vp]
@@ -136,7 +138,8 @@ EXPORTED = ("ds_last_error", "ds_supported_config", "ds_topk_workspace_size",
             "ds_kv8_append", "ds_kv8_decode", "ds_kv8_decode_workspace_size", "ds_kv8_prefill",
             "ds_kv8_prefill_workspace_size", "ds_pages_workspace_size", "ds_pages_copy",
             "ds_pages_free", "ds_pages_fork", "ds_pages_extend", "ds_pages_compact",
-            "ds_pages_shrink", "ds_qk_norm_rope", "ds_kv8_tree_decode", "ds_kv8_mass", "ds_kv8_accept",
+            "ds_pages_shrink", "ds_qk_norm_rope", "ds_kv8_tree_decode",
+            "ds_kv8_tree_decode_workspace_size", "ds_kv8_mass", "ds_kv8_accept",
             "ds_kv8_evict", "ds_kv8_evict_workspace_size")
 
 

@@ -85,6 +85,12 @@ struct Kv8MassArgs {
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream);
+// A tree of drafts (masks) by tiles of 256 rows instead of 40.
+cudaError_t launch_kv8_tree(const Kv8AttnArgs& a, cudaStream_t stream);
+size_t kv8_tree_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
+                                int64_t bt_stride);
+// Whether a tree takes that form, by its rows (nodes * heads of a kv head).
+inline bool kv8_tree_tiles(int next_n, int group) { return next_n * group > 40; }
 cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int num_layers, const Kv8AcceptArgs& a,
                               cudaStream_t stream);

@@ -120,6 +120,26 @@ int launched(const char* fn, cudaError_t e) {
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
+bool check_decode_shape(const char* fn, int64_t num_requests, int next_n, int num_heads,
+                        int num_kv_heads, int head_dim, int64_t bt_stride) {
+  dsmla::Kv8Cache c{};
+  c.num_pages = 1;
+  c.bt_stride = bt_stride;
+  c.requests = num_requests;
+  c.kv_heads = num_kv_heads;
+  c.dim = head_dim;
+  if (check_cache(fn, c) != DS_OK ||
+      check_heads(fn, num_heads, num_kv_heads, (int64_t)num_heads * head_dim, head_dim, 1.0f) !=
+          DS_OK)
+    return false;
+  if (next_n < 1 || next_n > 64) {
+    report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64", fn,
+                 next_n);
+    return false;
+  }
+  return true;
+}
+
 // Decode attention, causal or (tree) by masks.
 int decode(const char* fn, const void* q, int64_t q_stride, bool tree, const uint64_t* masks,
            const void* kv_pages, const float* kv_scales, int64_t num_pages,
@@ -137,6 +157,9 @@ int decode(const char* fn, const void* q, int64_t q_stride, bool tree, const uin
   if (next_n < 1 || next_n > 64)
     return report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64",
                         fn, next_n);
+  if (tree && bt_stride > (1 << 20))
+    return report_error(DS_ERR_UNSUPPORTED, "%s: bt_stride=%lld exceeds 2^20", fn,
+                        (long long)bt_stride);
   if (num_requests * next_n > (int64_t)INT32_MAX / num_heads)
     return report_error(DS_ERR_UNSUPPORTED,
                         "%s: num_requests=%lld is too large with next_n=%d and num_heads=%d "
@@ -153,8 +176,9 @@ int decode(const char* fn, const void* q, int64_t q_stride, bool tree, const uin
                        {workspace, "workspace", 256},
                        {err_flag, "err_flag", 4, true}});
   if (st != DS_OK) return st;
-  const size_t need = dsmla::kv8_decode_workspace_bytes(num_requests, next_n, num_heads,
-                                                        num_kv_heads, head_dim, bt_stride);
+  const bool tiles = tree && dsmla::kv8_tree_tiles(next_n, num_heads / num_kv_heads);
+  const size_t need = (tiles ? dsmla::kv8_tree_workspace_bytes : dsmla::kv8_decode_workspace_bytes)(
+      num_requests, next_n, num_heads, num_kv_heads, head_dim, bt_stride);
   if (workspace_bytes < need)
     return report_error(DS_ERR_WORKSPACE,
                         "%s: workspace_bytes=%zu is smaller than the %zu bytes needed", fn,
@@ -169,7 +193,8 @@ int decode(const char* fn, const void* q, int64_t q_stride, bool tree, const uin
   a.out = out;
   a.lse = lse;
   a.workspace = workspace;
-  return launched(fn, dsmla::launch_kv8_decode(a, as_stream(stream)));
+  return launched(fn, tiles ? dsmla::launch_kv8_tree(a, as_stream(stream))
+                            : dsmla::launch_kv8_decode(a, as_stream(stream)));
 }
 
 }  // namespace
@@ -212,24 +237,21 @@ int ds_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stri
 
 size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_heads,
                                     int num_kv_heads, int head_dim, int64_t bt_stride) {
-  const char* fn = "ds_kv8_decode_workspace_size";
-  dsmla::Kv8Cache c{};
-  c.num_pages = 1;
-  c.bt_stride = bt_stride;
-  c.requests = num_requests;
-  c.kv_heads = num_kv_heads;
-  c.dim = head_dim;
-  if (check_cache(fn, c) != DS_OK ||
-      check_heads(fn, num_heads, num_kv_heads, (int64_t)num_heads * head_dim, head_dim, 1.0f) !=
-          DS_OK)
+  if (!check_decode_shape("ds_kv8_decode_workspace_size", num_requests, next_n, num_heads,
+                          num_kv_heads, head_dim, bt_stride))
     return 0;
-  if (next_n < 1 || next_n > 64) {
-    report_error(DS_ERR_UNSUPPORTED, "%s: next_n=%d is not supported; available: 1 .. 64", fn,
-                 next_n);
-    return 0;
-  }
   return dsmla::kv8_decode_workspace_bytes(num_requests, next_n, num_heads, num_kv_heads, head_dim,
                                            bt_stride);
+}
+
+size_t ds_kv8_tree_decode_workspace_size(int64_t num_requests, int next_n, int num_heads,
+                                         int num_kv_heads, int head_dim, int64_t bt_stride) {
+  if (!check_decode_shape("ds_kv8_tree_decode_workspace_size", num_requests, next_n, num_heads,
+                          num_kv_heads, head_dim, bt_stride))
+    return 0;
+  const bool tiles = dsmla::kv8_tree_tiles(next_n, num_heads / num_kv_heads);
+  return (tiles ? dsmla::kv8_tree_workspace_bytes : dsmla::kv8_decode_workspace_bytes)(
+      num_requests, next_n, num_heads, num_kv_heads, head_dim, bt_stride);
 }
 
 int ds_kv8_decode(const void* q, int64_t q_stride, const void* kv_pages, const float* kv_scales,

@@ -58,6 +58,7 @@
 #include <atomic>
 
 #include "kv8_common.cuh"
+#include "kv8_join.cuh"
 
 namespace dsmla {
 
@@ -74,21 +75,9 @@ constexpr float kTau = 12.0f;              // log2: p b may reach 2^kTau
 constexpr float kPScale = 8.0f;            // 2^(15 - kTau): stored weights stay <= 2^15
 constexpr float kLog2PScale = 3.0f;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
-constexpr int kMinSpan = 1024, kMaxSpan = 4096;
-constexpr float kOnlyLow = -0x1p30f;        // reference of a span's row that only has lower scores
+// Spans of at most 4096 positions, 32 of them up to 131072.
+using Spans = SpanRule<1024, 4096, 32>;
 constexpr float kLostMax = 0x1p-14f;       // log2: what two pieces of q may lose of a score
-
-__host__ __device__ inline int span_of(int64_t len) {
-  int s = kMinSpan;
-  while (s < kMaxSpan && (int64_t)s * 32 < len) s *= 2;
-  return s;
-}
-
-// Most spans a row of at most `len` positions can have.
-int64_t max_spans(int64_t len) {
-  const int64_t a = (len + kMinSpan - 1) / kMinSpan, b = (len + kMaxSpan - 1) / kMaxSpan;
-  return a < 32 ? a : (b > 32 ? b : 32);
-}
 
 struct Shape {
   int rows;     // per row group
@@ -197,7 +186,7 @@ __device__ __forceinline__ void walk_load(const Params& p, Walk& w) {
   w.raw = p.c.lens[w.r];
   w.len = clamp_len(p, w.raw);
   w.tiles = (int)((w.len + kTile - 1) / kTile);
-  const int span = span_of(w.len);
+  const int span = Spans::of(w.len);
   w.span_tiles = span / kTile;
   w.spans = (int)((w.len + span - 1) / span);
 }
@@ -1140,70 +1129,6 @@ __global__ void __launch_bounds__(kThreads, Layout<R8, DIM, TREE>::kCtas) kv8_de
   if (warp == kMmaWarp) tmem_dealloc(tmem, LY::kCols);
 }
 
-// Joins the spans of a row, in order: one warp per (request, token, head).
-// Requests with one span (or none) are complete already.
-template <int DIM>
-__global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Params p) {
-  constexpr int E = DIM / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  pdl_wait();
-  pdl_trigger();
-  if (w >= p.c.requests * p.next_n * p.heads) return;
-  const int64_t token = w / p.heads;
-  const int h = (int)(w % p.heads);
-  const int64_t r = token / p.next_n;
-  const int len = row_len(p, r);
-  const int span = span_of(len);
-  const int spans = (len + span - 1) / span;
-  if (spans <= 1) return;
-  const int kvh = h / p.group;
-  const int row = (int)(token % p.next_n) * p.group + h % p.group;
-  const int rg = row / p.rows, rr = row % p.rows;
-  const int64_t slot0 =
-      ((r * p.c.kv_heads + kvh) * p.row_groups + rg) * p.spans * p.rows + rr;
-  float M = -INFINITY;
-  for (int s = lane; s < spans; s += 32) M = fmaxf(M, p.part_ml[slot0 + s * p.rows].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float m0 = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, acc[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < spans; ++s) {
-    const float2 ml = p.part_ml[slot0 + s * p.rows];
-    const float wt = ex2(ml.x - m0);
-    L = __fmaf_rn(wt, ml.y, L);
-    const float* o = p.part_o + (slot0 + s * p.rows) * DIM + lane * E;
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(o);
-      acc[0] = __fmaf_rn(wt, v.x, acc[0]);
-      acc[1] = __fmaf_rn(wt, v.y, acc[1]);
-      acc[2] = __fmaf_rn(wt, v.z, acc[2]);
-      acc[3] = __fmaf_rn(wt, v.w, acc[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(o);
-      acc[0] = __fmaf_rn(wt, v.x, acc[0]);
-      acc[1] = __fmaf_rn(wt, v.y, acc[1]);
-    }
-  }
-  if (M == kOnlyLow) L = NAN;
-  const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-  uint32_t b[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    b[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  __nv_bfloat16* out = p.out + w * DIM + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(b[0], b[1]);
-  else
-    *reinterpret_cast<uint32_t*>(out) = b[0];
-  if (lane == 0) p.lse[w] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-}
-
 template <int R8, int DIM, bool TREE>
 cudaError_t launch_main(const CUtensorMap& map, const Params& p, int dev, int64_t items,
                         cudaStream_t stream) {
@@ -1231,8 +1156,10 @@ cudaError_t launch_dim(const CUtensorMap& map, const Params& p, int dev, cudaStr
   }
   if (e != cudaSuccess || p.spans == 1) return e;   // no table holds a row of two spans
   const int64_t rows = p.c.requests * p.next_n * p.heads;
-  return launch_pdl(kv8_decode_join_kernel<DIM>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0,
-                    stream, 1u, p);
+  const JoinArgs a{p.part_o,  p.part_ml, p.out,   p.lse,  p.c,          p.next_n,
+                   p.heads,   p.group,   p.rows,  p.row_groups, p.spans};
+  return launch_pdl(kv8_join_kernel<DIM, Spans>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0,
+                    stream, 1u, a);
 }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1256,7 +1183,7 @@ int kv8_sm_count(int dev) {
 size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
                                   int64_t bt_stride) {
   const Shape s = shape_of(next_n, heads / kv_heads);
-  const int64_t rows = requests * kv_heads * s.groups * max_spans(bt_stride * kPage) * s.rows;
+  const int64_t rows = requests * kv_heads * s.groups * Spans::most(bt_stride * kPage) * s.rows;
   return 256 + pad256((size_t)rows * dim * 4) + (size_t)rows * 8;
 }
 
@@ -1290,7 +1217,7 @@ cudaError_t launch_kv8_decode(const Kv8AttnArgs& a, cudaStream_t stream) {
   p.scale_log2 = a.scale * kLog2e;
   p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
-  p.spans = max_spans(a.c.bt_stride * kPage);
+  p.spans = Spans::most(a.c.bt_stride * kPage);
   const int64_t slots = a.c.requests * a.c.kv_heads * s.groups * p.spans * s.rows;
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) +

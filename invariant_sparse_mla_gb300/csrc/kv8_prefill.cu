@@ -62,6 +62,7 @@
 #include <stdint.h>
 
 #include "kv8_common.cuh"
+#include "kv8_join.cuh"
 
 namespace dsmla {
 
@@ -71,6 +72,8 @@ constexpr int kTile = 128;               // positions per K/V tile (two pages)
 constexpr int kRows = 256;               // query rows per CTA
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMaxCtas = 192;
+// Trees of drafts: contexts are cut so that few requests fill the GPU too.
+using TreeSpans = SpanRule<1024, 1 << 28, 8>;
 
 // What the first kernel writes: item (unit u of one kv head) has weight
 // first[u + 1] - first[u]: its tiles and kItemCost for its queries and outputs
@@ -81,6 +84,7 @@ struct alignas(32) UnitInfo {
   int32_t r, t0, n;      // request, its first token, its tokens
   int32_t row0;          // first row of the request's rows; < 0: none
   int32_t raw_len;
+  int32_t jb, span;      // first tile, and number of the span (trees; else 0)
 };
 struct Plan {
   int64_t* first;        // [units + 1]
@@ -156,6 +160,7 @@ struct alignas(64) Piece {
   int32_t r, t0, n, row0, raw_len;
   int32_t kvh, nt, j0, j1;
   int32_t take, give;    // state slots to continue from / to hand over to, or -1
+  int32_t jb, span;      // tile j of the piece is tile jb + j of the request
 };
 
 struct Params {
@@ -170,6 +175,13 @@ struct Params {
   float* lse;
   Plan plan;
   Kv8Cache c;
+  // Trees of drafts: every request has next_n tokens, its context is cut into spans,
+  // and a unit is (request, span, 256 rows).
+  int next_n, row_units, rows;   // units of a span; rows of a unit's slot
+  const uint64_t* masks;         // [requests, next_n]
+  int64_t spans;                 // slots of a request
+  float* part_o;
+  float2* part_ml;
 };
 
 __device__ __forceinline__ int clamp_pos(const Params& p, int64_t v) {
@@ -189,9 +201,32 @@ __device__ __forceinline__ int item_tiles(const Params& p, int raw_len, int n, i
   return (visible(p, raw_len, n, last_row_of(p, row0, n)) + kTile - 1) / kTile;
 }
 
+// Trees: unit (request, span, 256 rows).
+__device__ __forceinline__ UnitInfo tree_unit(const Params& p, int64_t u, int* weight) {
+  UnitInfo i;
+  const int64_t rs = u / p.row_units;
+  i.r = (int)(rs / p.spans);
+  i.span = (int)(rs % p.spans);
+  i.t0 = i.r * p.next_n;
+  i.n = p.next_n;
+  i.raw_len = p.c.lens[i.r];
+  const int len = clamp_pos(p, i.raw_len), span = TreeSpans::of(len);
+  const int tiles = (len + kTile - 1) / kTile;
+  i.jb = i.span * (span / kTile);
+  const int left = tiles - i.jb;
+  i.row0 = -1;
+  *weight = 0;
+  if (i.span == 0 || left > 0) {     // (an empty request has one unit, for its outputs)
+    i.row0 = (int)(u % p.row_units) * kRows;
+    *weight = (left < span / kTile ? left : span / kTile) + kItemCost;
+  }
+  return i;
+}
+
 // Units of request r are numbered from floor(starts[r] * group / 256) + r (at
 // least as many as it has); one CTA finds each unit's request and numbers the
 // tiles.
+template <bool TREE>
 __global__ void __launch_bounds__(1024) kv8_prefill_plan_kernel(const Params p) {
   __shared__ int64_t part[32];
   pdl_wait();
@@ -205,7 +240,14 @@ __global__ void __launch_bounds__(1024) kv8_prefill_plan_kernel(const Params p) 
   const int64_t per = (p.units + 1023) / 1024;
   const int64_t u0 = tid * per, u1 = u0 + per < p.units ? u0 + per : p.units;
   int64_t sum = 0;
-  if (u0 < u1) {
+  if constexpr (TREE) {
+    for (int64_t u = u0; u < u1; ++u) {
+      int w;
+      p.plan.info[u] = tree_unit(p, u, &w);
+      p.plan.first[u] = sum;     // within the thread's run; completed below
+      sum += w;
+    }
+  } else if (u0 < u1) {
     // The request of the first unit; the others follow.
     int64_t lo = 0, hi = p.c.requests - 1;
     while (lo < hi) {
@@ -229,6 +271,7 @@ __global__ void __launch_bounds__(1024) kv8_prefill_plan_kernel(const Params p) 
       i.t0 = (int)t0;
       i.n = (int)(t1 > t0 ? t1 - t0 : 0);
       i.raw_len = raw;
+      i.jb = i.span = 0;
       const int64_t row0 = (u - (t0 * p.group / kRows + r)) * kRows;
       i.row0 = -1;
       int w = 0;
@@ -324,6 +367,8 @@ struct Scheduler {
     x.t0 = info.t0;
     x.n = info.n;
     x.raw_len = info.raw_len;
+    x.jb = info.jb;
+    x.span = info.span;
     x.kvh = (int)(i / p.units);
     x.take = x.j0 > 0 ? (int)blockIdx.x - 1 : -1;
     x.give = x.j1 < nt ? (int)blockIdx.x : -1;
@@ -361,7 +406,10 @@ struct Scheduler {
   }
 };
 
-template <int DIM>
+// TREE: the rows are nodes of a tree of drafts: all see the positions before the
+// drafts, and draft i where bit i of their mask is set; items are spans, and a span
+// of several gives its part to the join.
+template <int DIM, bool TREE>
 __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(const Params p) {
   using LY = Layout<DIM>;
   constexpr int kMmaWarp = LY::kMmaWarp, kLoaderWarp = LY::kLoaderWarp, H = LY::kShare;
@@ -444,8 +492,30 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       const int first = x.row0 + m * kTile;            // rows of the row tile
       const int rows = x.n * p.group - first;          // at most 128 of them exist
       const bool any = rows > 0;
-      const int vis = row < rows ? visible(p, x.raw_len, x.n, first + row) : 0;
-      const int min_vis = visible(p, x.raw_len, x.n, x.row0);
+      // TREE: the first draft's position and the row's drafts; a row sees something
+      // up to `vis`.
+      const int64_t base = (int64_t)x.raw_len - x.n;
+      uint64_t drafts = 0;
+      int vis, min_vis;
+      if constexpr (TREE) {
+        if (row < rows) {
+          drafts = p.masks[(int64_t)x.r * p.next_n + (first + row) / p.group];
+          if (p.next_n < 64) drafts &= (1ull << p.next_n) - 1;
+        }
+        vis = row < rows ? clamp_pos(p, base + 64 - __clzll((long long)drafts)) : 0;
+        min_vis = clamp_pos(p, base);
+      } else {
+        vis = row < rows ? visible(p, x.raw_len, x.n, first + row) : 0;
+        min_vis = visible(p, x.raw_len, x.n, x.row0);
+      }
+      // TREE: what the row sees of the 64 positions from `from` on, a bit each.
+      auto sees = [&](int from) {
+        if (row >= rows) return (uint64_t)0;
+        const int64_t e = base - from;
+        if (e >= 64) return ~(uint64_t)0;
+        if (e > 0) return ((uint64_t)1 << e) - 1 | drafts << e;
+        return e > -64 ? drafts >> -e : (uint64_t)0;
+      };
       // Element offset of a row of this warp in q (stride q_stride) or out.
       auto offset = [&](int i, int64_t stride) {
         const int rr = first + (warp & 3) * 32 + i;
@@ -585,7 +655,7 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       };
       uint32_t g = kv;         // tile of the CTA
       for (int j = any ? x.j0 : x.j1; j < x.j1; ++j, ++g) {
-        const int pos0 = j * kTile;
+        const int pos0 = (TREE ? x.jb + j : j) * kTile;
         if constexpr (H == 2) {
           wait(kSFull + m, tiles);
         } else if (!__all_sync(0xffffffffu, mbar_wait_long(&bars[kSFull + m], tiles & 1))) {
@@ -599,6 +669,7 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
           // weights: 64 values do not fit in the registers of 24 warps.
           const float4 mt = meta[(g & 3) * 2 + half];
           const int end = mt.w != 0.0f ? vis - pos0 - half * kPage : 0;
+          const uint64_t bits = TREE && mt.w != 0.0f ? sees(pos0 + half * kPage) : 0;
           const float gg = f * mt.x;
           float s[32];
           // 32 columns of S, what the row does not see at -infinity.
@@ -607,7 +678,13 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
             tmem_fence<32>(s);
           };
           auto mask = [&](int q) {
-            if (end < kPage) {
+            if constexpr (TREE) {
+              const uint32_t b = (uint32_t)(bits >> (32 * q));
+              if (b != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = (b >> i) & 1u ? s[i] : -INFINITY;
+              }
+            } else if (end < kPage) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[i] = 32 * q + i < end ? s[i] : -INFINITY;
             }
@@ -675,6 +752,8 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
           const float4 mt0 = meta[(g & 3) * 2], mt1 = meta[(g & 3) * 2 + 1];
           // (key scale, log2 of 8 times the value scale, its reciprocal, valid)
           const int end0 = mt0.w != 0.0f ? vis - pos0 : 0, end1 = mt1.w != 0.0f ? vis - pos0 - 64 : 0;
+          const uint64_t bits0 = TREE && mt0.w != 0.0f ? sees(pos0) : 0;
+          const uint64_t bits1 = TREE && mt1.w != 0.0f ? sees(pos0 + kPage) : 0;
           const float g0 = f * mt0.x, g1 = f * mt1.x;
           // s = exponents relative to the reference; returns the largest.
           auto exponents = [&](int page) {
@@ -686,7 +765,13 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
             tmem_fence<64>(s1);
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[i] = fma2(s[i], g2, c2);
-            if (end < 64) {
+            if constexpr (TREE) {
+              const uint64_t b = page ? bits1 : bits0;
+              if (b != ~(uint64_t)0) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s1[i] = (b >> i) & 1u ? s1[i] : -INFINITY;
+              }
+            } else if (end < 64) {
 #pragma unroll
               for (int i = 0; i < 64; ++i) s1[i] = i < end ? s1[i] : -INFINITY;
             }
@@ -760,8 +845,10 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
             if (!row_nan)
               for (int c = 0; c < NB; ++c) row_bits[c] = 0;
             row_nan = true;
-            for (int i = 0; i < kTile && pos0 + i < vis; ++i)
+            for (int i = 0; i < kTile && pos0 + i < vis; ++i) {
+              if (TREE && !((sees(pos0 + i / 64 * 64) >> (i & 63)) & 1u)) continue;
               for (int c = 0; c < NB; ++c) row_bits[c] |= map[i * (DIM / 16) + c];
+            }
           }
         }
         tmem_wait_st();
@@ -804,11 +891,44 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         piece_done();
         continue;
       }
-      if (unset && low) l = NAN;
+      bool part = false;         // TREE: one of several spans
+      if constexpr (TREE) part = clamp_pos(p, x.raw_len) > TreeSpans::of(clamp_pos(p, x.raw_len));
+      if (unset && low && !part) l = NAN;
       if constexpr (H == 2) {
         swap[half] = l;
         named_bar_sync(pair, 64);
         l = swap[0] + swap[1];
+      }
+      if (part) {
+        // The row's part of the join: outputs relative to its reference, and (reference,
+        // sum). (The loads are the warp's, also where only some of its rows exist.)
+        const int64_t group = ((int64_t)x.r * p.c.kv_heads + x.kvh) * p.row_units + x.row0 / kRows;
+        const int64_t slot = (group * p.spans + x.span) * p.rows + m * kTile + row;
+        float* to = p.part_o + slot * DIM + half * (DIM / H);
+#pragma unroll 1
+        for (int c = 0; c < DIM / H; c += 16) {
+          float o[16];
+          tmem_ld<16>(t_o + c, o);
+          tmem_fence<16>(o);
+          const uint32_t bits = row_nan ? row_bits[c >> 4] : 0u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = (bits >> i) & 1 ? NAN : o[i] * 0.125f;
+          if (row < rows) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(to + c + i) =
+                  make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+          __syncwarp();
+        }
+        if (half == 0 && row < rows)
+          p.part_ml[slot] = make_float2(unset ? (low ? kOnlyLow : -INFINITY) : ref, l);
+        if constexpr (H == 2)
+          named_bar_sync(pair, 64);
+        else
+          __syncwarp();
+        piece_done();
+        continue;
       }
       // Outputs by way of the row tile's Q buffer (its last S is long done), so
       // that rows are written in long pieces. A warp does its half of the dims.
@@ -883,13 +1003,15 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       const int j0 = x.j0, j1 = x.j1, kvh = x.kvh;
       const int32_t* table = p.c.block_table + x.r * p.c.bt_stride;
       const int len = clamp_pos(p, x.raw_len);
-      const int min_vis = visible(p, x.raw_len, x.n, x.row0);
+      const int min_vis = TREE ? clamp_pos(p, (int64_t)x.raw_len - x.n)
+                               : visible(p, x.raw_len, x.n, x.row0);
+      const int jb = TREE ? x.jb : 0;
       // The pages of tile j (-1: none, or outside the pool).
       auto pages_of = [&](int j, int* pg) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           pg[h] = -1;
-          const int b = j * 2 + h;
+          const int b = (jb + j) * 2 + h;
           if (j < j1 && b * kPage < len) {
             const int v = table[b];
             if (v >= 0 && v < p.c.num_pages)
@@ -969,10 +1091,10 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         // Positions behind the context hold anything: zeros in their place (a
         // weight of 0 times NaN is NaN). Where the item's rows see different
         // lengths, NaN codes become 0 too, and are listed.
-        if ((j + 1) * kTile > min_vis) {
+        if ((jb + j + 1) * kTile > min_vis) {
 #pragma unroll
           for (int e = 0; e < NC; ++e) {
-            const int row = lt / RC + e * (128 / RC), pos = j * kTile + row;
+            const int row = lt / RC + e * (128 / RC), pos = (jb + j) * kTile + row;
             uint32_t bits = 0u;
             if (pos >= len) {
               vx[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -1136,13 +1258,13 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
   if (warp == kMmaWarp) tmem_dealloc(tmem, LY::kCols);
 }
 
-template <int DIM>
+template <int DIM, bool TREE>
 cudaError_t launch(const Params& p, int dev, cudaStream_t stream) {
   static PerDeviceOnce once;
-  auto kern = kv8_prefill_kernel<DIM>;
+  auto kern = kv8_prefill_kernel<DIM, TREE>;
   cudaError_t e = set_max_dynamic_smem(once, dev, kern, Layout<DIM>::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kv8_prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, 1u, p);
+  e = launch_pdl(kv8_prefill_plan_kernel<TREE>, dim3(1), dim3(1024), 0, stream, 1u, p);
   if (e != cudaSuccess) return e;
   const int64_t items = p.units * p.c.kv_heads;
   int64_t ctas = kv8_sm_count(dev);
@@ -1197,7 +1319,7 @@ cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream) {
   int dev = 0;
   const cudaError_t e = stream_device(stream, &dev);
   if (e != cudaSuccess) return e;
-  Params p;
+  Params p{};
   p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
   p.q_stride = a.q_stride;
   p.tokens = a.tokens;
@@ -1210,7 +1332,72 @@ cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   p.c = a.c;
   carve(&p.plan, a.workspace, p.units, a.c.dim);
-  return a.c.dim == 128 ? launch<128>(p, dev, stream) : launch<64>(p, dev, stream);
+  return a.c.dim == 128 ? launch<128, false>(p, dev, stream) : launch<64, false>(p, dev, stream);
+}
+
+namespace {
+
+// Shape of a tree call: spans of a request, units of a span, rows of a unit.
+struct TreeShape {
+  int64_t spans, units, slots;
+  int row_units, rows;
+};
+TreeShape tree_shape(int64_t requests, int next_n, int heads, int kv_heads, int64_t bt_stride) {
+  const int total = next_n * (heads / kv_heads);
+  TreeShape s;
+  s.row_units = (total + kRows - 1) / kRows;
+  s.rows = total < kRows ? total : kRows;
+  s.spans = TreeSpans::most(bt_stride * kPage);
+  s.units = requests * s.spans * s.row_units;
+  s.slots = requests * kv_heads * s.row_units * s.spans * s.rows;
+  return s;
+}
+
+}  // namespace
+
+size_t kv8_tree_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
+                                int64_t bt_stride) {
+  const TreeShape s = tree_shape(requests, next_n, heads, kv_heads, bt_stride);
+  return carve(nullptr, nullptr, s.units, dim) + pad256((size_t)s.slots * dim * 4) +
+         pad256((size_t)s.slots * 8) + 256;
+}
+
+template <int DIM>
+cudaError_t launch_tree(const Params& p, int dev, cudaStream_t stream) {
+  const cudaError_t e = launch<DIM, true>(p, dev, stream);
+  if (e != cudaSuccess || p.spans == 1) return e;   // no table holds a row of two spans
+  const int64_t rows = p.c.requests * p.next_n * p.heads;
+  const JoinArgs a{p.part_o, p.part_ml, p.out,  p.lse,       p.c,    p.next_n,
+                   p.heads,  p.group,   p.rows, p.row_units, p.spans};
+  return launch_pdl(kv8_join_kernel<DIM, TreeSpans>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0,
+                    stream, 1u, a);
+}
+
+cudaError_t launch_kv8_tree(const Kv8AttnArgs& a, cudaStream_t stream) {
+  int dev = 0;
+  const cudaError_t e = stream_device(stream, &dev);
+  if (e != cudaSuccess) return e;
+  const TreeShape s = tree_shape(a.c.requests, a.next_n, a.heads, a.c.kv_heads, a.c.bt_stride);
+  Params p{};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  p.q_stride = a.q_stride;
+  p.tokens = a.tokens;
+  p.heads = a.heads;
+  p.group = a.heads / a.c.kv_heads;
+  p.units = s.units;
+  p.scale_log2 = a.scale * kLog2e;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.c = a.c;
+  p.next_n = a.next_n;
+  p.row_units = s.row_units;
+  p.rows = s.rows;
+  p.masks = a.masks;
+  p.spans = s.spans;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace) + carve(&p.plan, a.workspace, p.units, a.c.dim);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + pad256((size_t)s.slots * a.c.dim * 4));
+  return a.c.dim == 128 ? launch_tree<128>(p, dev, stream) : launch_tree<64>(p, dev, stream);
 }
 
 }  // namespace dsmla

@@ -165,6 +165,12 @@ def kv8_decode_workspace_size(num_requests, next_n, num_heads, num_kv_heads, hea
                                                   head_dim, bt_stride))
 
 
+def kv8_tree_decode_workspace_size(num_requests, next_n, num_heads, num_kv_heads, head_dim,
+                                   bt_stride):
+    return int(lib().ds_kv8_tree_decode_workspace_size(num_requests, next_n, num_heads,
+                                                       num_kv_heads, head_dim, bt_stride))
+
+
 def kv8_prefill_workspace_size(num_tokens, num_requests, num_heads, num_kv_heads, head_dim):
     return int(lib().ds_kv8_prefill_workspace_size(num_tokens, num_requests, num_heads,
                                                    num_kv_heads, head_dim))
@@ -230,7 +236,8 @@ def _decode(masks, q, kv_pages, kv_scales, block_table, lens, scale, out, lse, w
     out, lse = _outputs(q, d, dev, out, lse)
     L = lib()
     if workspace is None:
-        need = r and L.ds_kv8_decode_workspace_size(r, nn, h, hk, d, width)
+        size = L.ds_kv8_tree_decode_workspace_size if tree else L.ds_kv8_decode_workspace_size
+        need = r and size(r, nn, h, hk, d, width)
         workspace = _scratch(need or 256, dev, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         _arg(workspace, "workspace", torch.uint8, dev)

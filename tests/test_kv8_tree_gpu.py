@@ -51,7 +51,8 @@ def _run(ds, c, masks, heads, scale=None, gain=2.5, q=None, bound_scale=None, **
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("n,kv_heads,group", [(1, 1, 1), (2, 2, 8), (5, 3, 7), (8, 2, 3), (13, 1, 16),
-                                              (33, 2, 4), (64, 1, 2)])
+                                              (33, 2, 4), (64, 1, 2), (16, 2, 8), (43, 1, 6),
+                                              (64, 2, 8), (64, 1, 12)])
 def test_trees(ds, n, kv_heads, group, dim):
     c = Cache([n, n + 1, n + 63, n + 64, 200 + n, 0, 129 + n, n - 1, n + 100, -4], kv_heads, dim,
               seed=n + group)
@@ -59,7 +60,8 @@ def test_trees(ds, n, kv_heads, group, dim):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-def test_masks_of_any_kind(ds, dim):
+@pytest.mark.parametrize("heads", [6, 16])
+def test_masks_of_any_kind(ds, heads, dim):
     """No bit at all (the prefix alone, or nothing), bits of later nodes, bits that
     no node has, all of them."""
     n = 9
@@ -69,21 +71,23 @@ def test_masks_of_any_kind(ds, dim):
     masks[:, 3] = 0x100
     masks[:, 4] = np.uint64(0xFFFFFFFFFFFFFFFF)
     masks[:, 5] = np.uint64(0xFFFFFFFFFFFFFE00)
-    out, lse = _run(ds, c, masks, 6)
+    out, lse = _run(ds, c, masks, heads)
     assert (out[0, 0] == 0).all() and torch.isneginf(lse[0, 0]).all()
     assert (out[0, 5] == 0).all() and torch.isneginf(lse[0, 5]).all()
 
 
-@pytest.mark.parametrize("n,lens", [(8, [5000, 1030, 1024, 2049 + 6]), (64, [2100, 1024 + 63, 1100]),
-                                    (16, [40000])])
-def test_long_contexts(ds, n, lens):
+@pytest.mark.parametrize("n,lens,dim", [
+    (8, [5000, 1030, 1024, 2049 + 6], 128), (64, [2100, 1024 + 63, 1100], 128), (16, [40000], 128),
+    (20, [9000, 1030, 1024, 1044, 2048 + 19, 8192 + 7], 128), (33, [3000, 1056, 64], 64)])
+def test_long_contexts(ds, n, lens, dim):
     """Trees that begin, end and straddle where spans are cut."""
-    c = Cache(lens, 1, 128, seed=n)
+    c = Cache(lens, 1, dim, seed=n)
     _run(ds, c, _tree(c.rng, len(lens), n), 4)
 
 
-@pytest.mark.parametrize("n,group", [(1, 8), (5, 8), (12, 3), (64, 1)])
+@pytest.mark.parametrize("n,group", [(1, 8), (5, 8), (12, 3), (40, 1)])
 def test_a_chain_is_decode(ds, n, group):
+    """Up to 40 rows, bit for bit."""
     c = Cache([700, n, 64 + n, 1500, 3, 0], 2, 128, seed=n)
     masks = np.array([(1 << (j + 1)) - 1 for j in range(n)], np.uint64)
     masks = np.broadcast_to(masks, (6, n)).copy()
@@ -94,13 +98,14 @@ def test_a_chain_is_decode(ds, n, group):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_nan_drafts_reach_only_who_sees_them(ds):
+@pytest.mark.parametrize("n,heads,d", [(6, 8, 128), (30, 8, 128), (30, 8, 64), (64, 12, 128)])
+def test_nan_drafts_reach_only_who_sees_them(ds, n, heads, d):
     """A NaN key or value of draft 3: nodes that do not see it stay as they are."""
-    n, hk, d = 6, 2, 128
-    c = Cache([64 + n - 2, 300], hk, d, seed=5)
+    hk, half = 2, heads // 2
+    c = Cache([64 + n - 2, 1100], hk, d, seed=5)
     masks = _tree(c.rng, 2, n)
     codes, scales, table, lens = c.device()
-    q = c.q(2 * n, 8).to(DEV).view(2, n, 8, d)
+    q = c.q(2 * n, heads).to(DEV).view(2, n, heads, d)
     want = ds.kv8_tree_decode(q, _dev(masks), codes, scales, table, lens, 0.1)
     for side in (0, 1):
         bad = codes.clone()
@@ -112,16 +117,16 @@ def test_nan_drafts_reach_only_who_sees_them(ds):
         for r in range(2):
             for j in range(n):
                 sees = bool(int(masks[r, j]) >> 3 & 1)
-                assert torch.equal(out[r, j, :4], want[0][r, j, :4])     # kv head 0
+                assert torch.equal(out[r, j, :half], want[0][r, j, :half])     # kv head 0
                 if sees:
-                    assert out[r, j, 4:, 17].isnan().all()
+                    assert out[r, j, half:, 17].isnan().all()
                 else:
-                    assert torch.equal(out[r, j, 4:], want[0][r, j, 4:])
+                    assert torch.equal(out[r, j, half:], want[0][r, j, half:])
                     assert torch.equal(lse[r, j], want[1][r, j])
 
 
-def test_pages_outside_the_pool(ds):
-    n = 10
+@pytest.mark.parametrize("n", [10, 31])
+def test_pages_outside_the_pool(ds, n):
     c = Cache([300, 100], 2, 64, seed=6)
     c.table[0, 2], c.table[0, 4], c.table[1, 0] = -1, 10 ** 6, -5
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
@@ -129,22 +134,23 @@ def test_pages_outside_the_pool(ds):
     assert int(err) == ds.DEVERR_PAGE
 
 
-def test_large_elements_of_q(ds):
+@pytest.mark.parametrize("n", [7, 20])
+def test_large_elements_of_q(ds, n):
     """Elements hundreds of times the others: what the 8-bit pieces lose is added."""
     c = Cache([500, 90], 1, 128, seed=7)
-    q = c.q(2 * 7, 4, gain=1.0)
+    q = c.q(2 * n, 4, gain=1.0)
     q[:, 1, 5] = 900.0
     codes = c.codes[:, 0]
     codes[..., 5] = 0
-    _run(ds, c, _tree(c.rng, 2, 7), 4, q=q)
+    _run(ds, c, _tree(c.rng, 2, n), 4, q=q)
 
 
-def test_bits_do_not_depend_on_the_batch(ds):
-    n = 12
-    c = Cache([2500, 64, 900, 1300, 40], 2, 128, seed=8)
+@pytest.mark.parametrize("n,dim", [(5, 128), (12, 128), (12, 64), (40, 128)])
+def test_bits_do_not_depend_on_the_batch(ds, n, dim):
+    c = Cache([2500, 64, 900, 1300, 40], 2, dim, seed=8)
     masks = _tree(c.rng, 5, n)
     codes, scales, table, lens = c.device()
-    q = c.q(5 * n, 16).to(DEV).view(5, n, 16, 128)
+    q = c.q(5 * n, 16).to(DEV).view(5, n, 16, dim)
     whole = ds.kv8_tree_decode(q, _dev(masks), codes, scales, table, lens, 0.1)
     for r in range(5):
         one = ds.kv8_tree_decode(q[r:r + 1], _dev(masks[r:r + 1]), codes, scales,
@@ -259,3 +265,28 @@ def test_a_speculative_step_then_eviction(ds, capture):
     want = oracle.kv8_attention(qb, rows_seen, e[1], e[2], table.cpu().numpy(), 0.125)
     err = np.abs(outs["after"][:, 0].float().cpu().numpy() - want[0])
     assert (err <= 2.0 ** -7 * want[2] + 1e-6).all()
+
+
+def test_many_large_trees(ds):
+    """Runs of tiles that end inside an item, empty requests among them; two streams."""
+    rng = np.random.default_rng(11)
+    lens = rng.integers(40, 3000, 40)
+    lens[[3, 17, 18]] = 0
+    c = Cache(lens, 2, 128, seed=11)
+    masks = _tree(c.rng, 40, 32)
+    codes, scales, table, ln = c.device()
+    q = c.q(40 * 32, 16).to(DEV).view(40, 32, 16, 128)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = ds.kv8_tree_decode(q, _dev(masks), codes, scales, table, ln, 0.1, err_flag=err)
+    md = _dev(masks)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [ds.kv8_tree_decode(q, md, codes, scales, table, ln, 0.1, stream=s) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    for out, lse in got:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for r in (0, 3, 7, 39):
+        one = ds.kv8_tree_decode(q[r:r + 1], md[r:r + 1].contiguous(), codes, scales,
+                                 table[r:r + 1].contiguous(), ln[r:r + 1], 0.1)
+        assert torch.equal(one[0][0], want[0][r]) and torch.equal(one[1][0], want[1][r])
