@@ -500,7 +500,7 @@ size_t ds_kv8_decode_workspace_size(int64_t num_requests, int next_n, int num_he
  *  masks        uint64 [num_requests, next_n], 8-byte aligned.
  *
  * All else as for ds_kv8_decode, but bt_stride is at most 2^20, and the workspace
- * has ds_kv8_tree_decode_workspace_size() bytes. Trees of up to 40 rows (next_n *
+ * has ds_kv8_tree_decode_workspace_size() bytes. Trees of up to 80 rows (next_n *
  * num_heads / num_kv_heads) are computed as by ds_kv8_decode, and with masks of a
  * chain (bit i set for i <= j) the results are then the same, bit for bit; larger
  * ones by tiles of 256 rows as in ds_kv8_prefill (q as precise as there), over spans

@@ -89,8 +89,11 @@ cudaError_t launch_kv8_prefill(const Kv8AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_tree(const Kv8AttnArgs& a, cudaStream_t stream);
 size_t kv8_tree_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
                                 int64_t bt_stride);
-// Whether a tree takes that form, by its rows (nodes * heads of a kv head).
-inline bool kv8_tree_tiles(int next_n, int group) { return next_n * group > 40; }
+// Whether a tree takes that form, by its rows (nodes * heads of a kv head): from
+// three row groups of decode on. 16 requests on 4096 to 32768 positions, 8 kv heads x
+// 128, took 322 us by decode and 412 by tiles with 64 rows, 507 and 357 with 128, 802
+// and 459 with 192; one request on 32768 positions with 192 rows 121 and 118.
+inline bool kv8_tree_tiles(int next_n, int group) { return next_n * group > 80; }
 cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int num_layers, const Kv8AcceptArgs& a,
                               cudaStream_t stream);

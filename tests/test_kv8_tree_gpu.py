@@ -78,16 +78,17 @@ def test_masks_of_any_kind(ds, heads, dim):
 
 @pytest.mark.parametrize("n,lens,dim", [
     (8, [5000, 1030, 1024, 2049 + 6], 128), (64, [2100, 1024 + 63, 1100], 128), (16, [40000], 128),
-    (20, [9000, 1030, 1024, 1044, 2048 + 19, 8192 + 7], 128), (33, [3000, 1056, 64], 64)])
+    (20, [9000, 1030, 1024, 1044, 2048 + 19, 8192 + 7], 128), (33, [3000, 1056, 64], 64),
+    (41, [9000, 1030, 1024, 1065, 2048 + 19, 8192 + 7], 64)])
 def test_long_contexts(ds, n, lens, dim):
     """Trees that begin, end and straddle where spans are cut."""
     c = Cache(lens, 1, dim, seed=n)
     _run(ds, c, _tree(c.rng, len(lens), n), 4)
 
 
-@pytest.mark.parametrize("n,group", [(1, 8), (5, 8), (12, 3), (40, 1)])
+@pytest.mark.parametrize("n,group", [(1, 8), (5, 8), (12, 3), (64, 1), (10, 8)])
 def test_a_chain_is_decode(ds, n, group):
-    """Up to 40 rows, bit for bit."""
+    """Up to 80 rows, bit for bit."""
     c = Cache([700, n, 64 + n, 1500, 3, 0], 2, 128, seed=n)
     masks = np.array([(1 << (j + 1)) - 1 for j in range(n)], np.uint64)
     masks = np.broadcast_to(masks, (6, n)).copy()
