@@ -98,7 +98,7 @@ cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int num_layers, const Kv8AcceptArgs& a,
                               cudaStream_t stream);
 cudaError_t launch_kv8_evict(Kv8EvictArgs a, void* workspace, cudaStream_t stream);
-size_t kv8_evict_workspace_bytes(int64_t requests, int kv_heads, int ranked, int64_t mass_stride);
+size_t kv8_evict_workspace_bytes(int64_t requests, int kv_heads, int ranked);
 size_t kv8_decode_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
                                   int64_t bt_stride);
 size_t kv8_prefill_workspace_bytes(int64_t tokens, int64_t requests, int heads, int kv_heads,

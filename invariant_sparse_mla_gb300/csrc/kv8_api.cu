@@ -404,8 +404,7 @@ size_t ds_kv8_evict_workspace_size(int64_t num_requests, int num_kv_heads, int64
   c.dim = 64;
   if (check_cache(fn, c) != DS_OK || check_budget(fn, budget, first, recent, mass_stride) != DS_OK)
     return 0;
-  return dsmla::kv8_evict_workspace_bytes(num_requests, num_kv_heads, budget - first - recent,
-                                          mass_stride);
+  return dsmla::kv8_evict_workspace_bytes(num_requests, num_kv_heads, budget - first - recent);
 }
 
 int ds_kv8_evict(float* mass, int64_t mass_stride, int budget, int first, int recent,
@@ -437,8 +436,8 @@ int ds_kv8_evict(float* mass, int64_t mass_stride, int budget, int first, int re
   if (st != DS_OK) return st;
   if (new_lens == lens)
     return report_error(DS_ERR_SHAPE, "%s: new_lens must not be lens", fn);
-  const size_t need = dsmla::kv8_evict_workspace_bytes(num_requests, num_kv_heads,
-                                                       budget - first - recent, mass_stride);
+  const size_t need =
+      dsmla::kv8_evict_workspace_bytes(num_requests, num_kv_heads, budget - first - recent);
   if (workspace_bytes < need)
     return report_error(DS_ERR_WORKSPACE,
                         "%s: workspace_bytes=%zu is smaller than the %zu bytes needed", fn,

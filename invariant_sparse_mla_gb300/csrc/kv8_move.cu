@@ -253,13 +253,11 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Kv8E
   const int32_t* table = a.c.block_table + r * a.c.bt_stride;
   float* mass = a.mass + rg * a.mass_stride;
   const int blocks = (a.budget + kPage - 1) / kPage;
-  // The position that comes to place j. (The ranking's indices lie in the row
-  // as they are; if one of its bounded waits gave up they could be anything.)
+  // The position that comes to place j.
   auto source = [&](int j) {
     if (j < a.first) return j;
     if (j >= a.first + k) return len - a.budget + j;
-    const int p = a.first + top_idx[j - a.first];
-    return p < j ? j : (p < len ? p : len - 1);
+    return a.first + top_idx[j - a.first];
   };
   auto part = [&](int64_t page) { return (page * 2 + side) * a.c.kv_heads + g; };
   const int col = tid % L, row0 = tid / L;
@@ -343,11 +341,10 @@ cudaError_t run_accept(const ds_kv8_layer* layers, int n, const Kv8AcceptArgs& a
 
 struct EvictWorkspace {
   int32_t *starts, *ends, *top;
-  void* topk;
-  size_t topk_bytes, bytes;
+  size_t bytes;
 };
 
-EvictWorkspace carve(void* base, int64_t rows, int k, int64_t mass_stride) {
+EvictWorkspace carve(void* base, int64_t rows, int k) {
   EvictWorkspace w;
   uint8_t* p = static_cast<uint8_t*>(base);
   size_t at = 0;
@@ -359,8 +356,6 @@ EvictWorkspace carve(void* base, int64_t rows, int k, int64_t mass_stride) {
   w.starts = reinterpret_cast<int32_t*>(take((size_t)rows * 4));
   w.ends = reinterpret_cast<int32_t*>(take((size_t)rows * 4));
   w.top = reinterpret_cast<int32_t*>(take((size_t)rows * k * 4));
-  w.topk_bytes = k > 0 ? topk_workspace_bytes(rows, mass_stride) : 0;
-  w.topk = take(w.topk_bytes);
   w.bytes = at + 256;
   return w;
 }
@@ -373,14 +368,14 @@ cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int n, const Kv8Accept
                          : run_accept<DS_MAX_KV8_LAYERS>(layers, n, a, stream);
 }
 
-size_t kv8_evict_workspace_bytes(int64_t requests, int kv_heads, int k, int64_t mass_stride) {
-  return carve(nullptr, requests * kv_heads, k, mass_stride).bytes;
+size_t kv8_evict_workspace_bytes(int64_t requests, int kv_heads, int k) {
+  return carve(nullptr, requests * kv_heads, k).bytes;
 }
 
 cudaError_t launch_kv8_evict(Kv8EvictArgs a, void* workspace, cudaStream_t stream) {
   const int64_t rows = a.c.requests * a.c.kv_heads;
   const int k = a.budget - a.first - a.recent;
-  const EvictWorkspace w = carve(workspace, rows, k, a.mass_stride);
+  const EvictWorkspace w = carve(workspace, rows, k);
   a.starts = w.starts;
   a.ends = w.ends;
   a.top = w.top;
@@ -388,8 +383,10 @@ cudaError_t launch_kv8_evict(Kv8EvictArgs a, void* workspace, cudaStream_t strea
                              dim3(kPlanThreads), 0, stream, 1u, a);
   if (e != cudaSuccess) return e;
   if (k > 0) {
-    e = launch_topk(a.mass, a.mass_stride, rows, w.starts, w.ends, k, w.top, w.topk, w.topk_bytes,
-                    stream);
+    // Without the grid kernel's workspace: over rows of mass it took 19 us where the
+    // cluster kernel takes 7 (8 rows of 2048), 41 and 15 (8 of 131072), 60 and 45 (64 of
+    // 131072), and 70 and 80 with 128 rows, for 143 MB of it.
+    e = launch_topk(a.mass, a.mass_stride, rows, w.starts, w.ends, k, w.top, nullptr, 0, stream);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((unsigned)(rows * 2 * kCluster));
