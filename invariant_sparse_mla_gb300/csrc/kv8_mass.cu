@@ -27,7 +27,7 @@
 // - More: K becomes bf16 (an E4M3 code has 4 significant bits and an exponent that
 //   bf16 holds: exponent and mantissa bits are placed under bf16's, subnormals
 //   included, and multiplied by 2^120) and lies in TMEM as the A operand, two tiles
-//   for an item; the query rows stream past both in steps of up to 128, by TMA as
+//   for an item; the query rows stream past both in steps of up to 192, by TMA as
 //   they lie, and both operands are exact. Each of the two tiles has its eight warps
 //   and its buffer of S. The bound is the tensor core (2 dim flops a position and
 //   row) and the exponentials beside it.
@@ -55,7 +55,8 @@ namespace dsmla {
 namespace {
 
 constexpr int kTile = 128;                 // positions of an item
-constexpr int kStep = 128;                 // query rows of a step
+constexpr int kStep = 192;                 // query rows of a step
+constexpr int kFewCols = 128;              // columns of an S buffer with few rows
 constexpr int kSumWarps = 16;
 constexpr int kProducerWarp = 16, kMmaWarp = 17, kQWarp = 18, kLWarp = 19;
 constexpr int kThreads = 32 * (kLWarp + 1);   // (96 registers a thread)
@@ -66,7 +67,7 @@ constexpr int kLook = 4;                   // items whose pages are looked up at
 // ahead of the one in work, and waits for the list.
 constexpr int kAhead = 3 * kLook;
 constexpr int kReaders = kSumWarps + 3;    // warps that read the list
-constexpr int kNS = 3;                     // S buffers (more rows: one for each set)
+constexpr int kNS = 3;                     // S buffers of few rows (more: one for each place)
 constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
                                            // when a step is summed, Q once its product is done)
 constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
@@ -76,8 +77,8 @@ template <int DIM>
 struct Layout {
   static constexpr int kKBytes = kTile * DIM;
   static constexpr int kQBytes = kStep * DIM * 2;
-  static constexpr int kNK = DIM == 128 ? 5 : 8;    // stages
-  static constexpr int kNQ = DIM == 128 ? 4 : 6;
+  static constexpr int kNK = DIM == 128 ? 6 : 8;    // stages
+  static constexpr int kNQ = DIM == 128 ? 2 : 4;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kNK * kKBytes;
   static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
@@ -90,7 +91,8 @@ struct Layout {
   static constexpr int kSmem = kEnd + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   // TMEM columns: the S buffers, then K of two tiles.
-  static constexpr int kA = kNS * kStep;
+  static constexpr int kA = 2 * kStep;
+  static_assert(kNS * kFewCols <= kA, "the buffers of few rows");
   static constexpr int kACols = DIM / 2;
   static constexpr uint32_t kCols = 512;
   static_assert(kA + 2 * kACols <= 512, "TMEM columns");
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
             const uint64_t a = k_desc + (uint64_t)(tile.at * (LY::kKBytes >> 4));
 #pragma unroll
             for (int k = 0; k < DIM / 32; ++k)
-              mma_f8_ss(t_d + s_free.at * kStep + u * n, a + ((k * 32) >> 4), b + ((k * 32) >> 4),
+              mma_f8_ss(t_d + s_free.at * kFewCols + u * n, a + ((k * 32) >> 4), b + ((k * 32) >> 4),
                         idesc, k > 0 ? 1u : 0u);
             commit(kKEmpty, tile.at);
           }
@@ -967,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
           const int* vs = reinterpret_cast<const int*>(ls) + kStep;
           const int r8 = (rows + 7) & ~7, cols = (3 * r8 + 15) & ~15;
-          const uint32_t t_s = tmem + lane_base + buf * kStep + u * cols;
+          const uint32_t t_s = tmem + lane_base + buf * kFewCols + u * cols;
           const Keys k0 = read_meta(tile + u);
           const int tile_u = u == 0 ? now.tile[0] : (u == 1 ? now.tile[1] : (u == 2 ? now.tile[2]
                                                                                  : now.tile[3]));
@@ -1079,19 +1081,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           };
           const int here =
               s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now.n, now.first, s).rows;
-          const int c0 = half * 64;
+          const int c0 = half * (kStep / 2);
           if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile)) {
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
+            for (int c = 0; c < kStep / 2; c += 32) {
               float x[32];
               tmem_ld32(t_s + c0 + c, x);
               tmem_fence<32>(x);
-              if (c == 32) let_go();
+              if (c + 32 == kStep / 2) let_go();
 #pragma unroll
               for (int e = 0; e < 32; e += 8) add8(x + e, c0 + c + e, false);
             }
           } else {
-            for (int c = c0; c < here && c < c0 + 64; c += 8) {
+            for (int c = c0; c < here && c < c0 + kStep / 2; c += 8) {
               float x[8];
               tmem_ld<8>(t_s + c, x);
               tmem_fence<8>(x);
