@@ -1093,11 +1093,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
               for (int e = 0; e < 32; e += 8) add8(x + e, c0 + c + e, false);
             }
           } else {
-            for (int c = c0; c < here && c < c0 + kStep / 2; c += 8) {
-              float x[8];
-              tmem_ld<8>(t_s + c, x);
-              tmem_fence<8>(x);
+            // (Columns behind the rows hold anything; no row of theirs sees a position.)
+#pragma unroll 1
+            for (int c = c0; c < here && c < c0 + kStep / 2; c += 16) {
+              float x[16];
+              tmem_ld<16>(t_s + c, x);
+              tmem_fence<16>(x);
               add8(x, c, true);
+              add8(x + 8, c + 8, true);
             }
             let_go();
           }
