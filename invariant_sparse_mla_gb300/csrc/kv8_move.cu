@@ -47,6 +47,12 @@ __device__ __forceinline__ uint4 requantise(uint4 v, float ratio) {
                     requantise4(v.w, ratio));
 }
 
+// What codes under scale s are times under `top`. (Equal scales change nothing,
+// whatever they are: 0 or an infinity has no quotient.)
+__device__ __forceinline__ float ratio_of(float s, float top) {
+  return s == top ? 1.0f : __fdiv_rn(s, top);
+}
+
 // ------------------------------------------------------------------ accept
 constexpr int kAcceptWarps = 8;
 constexpr int kFewLayers = 16;
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) kv8_accept_kernel(
                                                  (lane + 32 < count && cross(lane + 32, n1)));
   float top = off > 0 || from0 ? s0 : s1;
   if (from1) top = fmaxf(top, s1);
-  const float ratio0 = __fdiv_rn(s0, top), ratio1 = __fdiv_rn(s1, top);
+  const float ratio0 = ratio_of(s0, top), ratio1 = ratio_of(s1, top);
   const int col = lane % L;
   for (int j0 = 0; j0 < count; j0 += CHUNK) {
     uint4 v[CHUNK / ROWS];
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Kv8E
           const int slot = q * ROWS + row0, at = (i0 + i) * kPage + slot;
           const int to = (int)t * kPage + slot;
           if (from[at] < 0) continue;
-          const float ratio = __fdiv_rn(scale[at], top);
+          const float ratio = ratio_of(scale[at], top);
           if (from[at] != to || ratio != 1.0f)
             reinterpret_cast<uint4*>(a.c.pages + (int64_t)to * DIM)[col] = requantise(v[i][q], ratio);
           if (side == 0 && col == 0 && from[at] != to) mass[b * kPage + slot] = weight[at];

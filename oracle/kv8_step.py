@@ -52,7 +52,7 @@ def _place(codes, scales, pages, head_list, src):
                 top = s.max()
                 for j in range(lo, hi):
                     row = old_codes[pages[src[j] // PAGE], side, g, src[j] % PAGE]
-                    ratio = np.float32(s[j - lo] / top)
+                    ratio = np.float32(1 if s[j - lo] == top else s[j - lo] / top)
                     if ratio != 1:
                         row = e4m3_encode((e4m3_to_float64(row) * float(ratio)).astype(np.float32))
                     codes[pages[b], side, g, j % PAGE] = row

@@ -36,8 +36,10 @@ def _paths(rng, reqs, next_n, width):
 
 # ------------------------------------------------------------------ accept
 def _accept(ds, lens, next_n, accepted, hk, dim, seed, layers=1, spread=3, odd_scales=False,
-            bad=()):
+            bad=(), edit=None):
     c = Cache(lens, hk, dim, seed, spread=spread)
+    if edit is not None:
+        edit(c)
     for r, b, p in bad:
         c.table[r, b] = p
     host = []
@@ -107,8 +109,10 @@ def test_accept_leaves_and_flags(ds):
 
 # ------------------------------------------------------------------- evict
 def _evict(ds, lens, budget, first, recent, hk, dim, seed, spread=3, odd_scales=False, mass=None,
-           refs=None, bad=(), extra=0, capture=False):
+           refs=None, bad=(), extra=0, capture=False, edit=None):
     c = Cache(lens, hk, dim, seed, spread=spread)
+    if edit is not None:
+        edit(c)
     for r, b, p in bad:
         c.table[r, b] = p
     if odd_scales:
@@ -201,6 +205,21 @@ def test_evict_leaves_and_flags(ds):
 def test_evict_wider_mass_and_capture(ds):
     assert not _evict(ds, [900, 150, 66], 60, 3, 9, 2, 128, seed=9, extra=4, capture=True)
     assert not _evict(ds, [3000], 1500, 3, 9, 2, 64, seed=10, extra=36, capture=True)
+
+
+@pytest.mark.parametrize("value", [0.0, np.inf])
+def test_codes_under_equal_scales_are_copied(ds, value):
+    """Also where the scales have no quotient: pages that were never scaled, or lost."""
+    def all_pages(c):
+        c.scales[...] = value
+
+    def some_pages(c):
+        c.scales[c.rng.random(c.scales.shape) < 0.5] = 0.0
+    rng = np.random.default_rng(14)
+    for edit in (all_pages, some_pages):
+        lens = [90, 120, 64, 300]
+        assert not _accept(ds, lens, 40, _paths(rng, 4, 40, 20), 2, 64, seed=5, edit=edit)
+        assert not _evict(ds, lens, 80, 2, 20, 2, 128, seed=6, edit=edit)
 
 
 # ------------------------------------------------------------------ shrink
