@@ -242,12 +242,19 @@ __device__ __forceinline__ Step step_of(const Params& p, int n, int first, int s
   return x;
 }
 
-// The next item from w.i on, in later requests where need be.
+// The next item from w.i on, in later requests where need be. (Whole warps call it
+// with one state: behind a request without tokens the lanes look at 32 at a time,
+// since the other warps wait for the list, and a batch may be empty but for a few.)
 __device__ __forceinline__ bool walk_settle(const Params& p, Walk& w) {
   while (w.i >= w.items) {
     if (++w.r >= p.c.requests) return false;
     load_request(p, w.r, w);
     w.i = w.j = w.kvh = 0;
+    if (w.items > 0) break;
+    const int64_t r = (int64_t)w.r + 1 + (threadIdx.x & 31);
+    const uint32_t in = __ballot_sync(
+        0xffffffffu, r < p.c.requests && p.c.lens[r] > 0 && start_of(p, r + 1) > start_of(p, r));
+    w.r += in ? __ffs((int)in) - 1 : 32;
   }
   if (w.at >= w.end) return false;
   load_item(p, w);
@@ -1032,10 +1039,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         const uint32_t sl = (ql - 1) % kNL;
         const float* ls = reinterpret_cast<const float*>(smem + LY::kLse + sl * (kStep * 12));
         const int* vs = reinterpret_cast<const int*>(ls) + kStep;
-        // (The product was issued when its lse was there. A set without a tile only
-        // goes along.)
-        const bool ok = work ? mbar_wait_at(c_full, c_phase)
-                             : mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u);
+        // (A set without a tile only goes along.)
+        const bool ok = (!work || mbar_wait_at(c_full, c_phase)) &&
+                              mbar_wait_long(&bars[kLFull + sl], ((ql - 1) / kNL) & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
@@ -1196,7 +1202,9 @@ cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream) {
   // q as [tokens][heads][dim], in boxes of a step's rows by 64 dims.
   CUtensorMap q_map;
   const cuuint64_t qdim[3] = {(cuuint64_t)dim, (cuuint64_t)a.heads, (cuuint64_t)a.tokens};
-  const cuuint64_t qstride[2] = {(cuuint64_t)dim * 2, (cuuint64_t)a.q_stride * 2};
+  // (One token's stride is never used, and might be none that a map takes.)
+  const cuuint64_t qstride[2] = {(cuuint64_t)dim * 2,
+                                 (cuuint64_t)(a.tokens > 1 ? a.q_stride : (int64_t)a.heads * dim) * 2};
   const cuuint32_t qbox[3] = {64, (cuuint32_t)p.step_heads, (cuuint32_t)p.step_tokens};
   const cuuint32_t qestride[3] = {1, 1, 1};
   if (enc(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), qdim, qstride, qbox,

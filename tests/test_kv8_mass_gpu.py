@@ -264,6 +264,49 @@ def test_long_runs_of_items(ds, counts):
     assert all((mass[r, :, n:] == 0).all() and (mass[r, :, :n] > 0).all() for r, n in enumerate(lens))
 
 
+def test_a_batch_of_mostly_empty_requests(ds):
+    """2^20 requests, tokens in few of them, at the ends of the list above all."""
+    reqs, n = 1 << 20, 50
+    rng = np.random.default_rng(13)
+    full = np.array([0, 1, 3, 40, 500_000, reqs - 1] + list(range(100, 700)))
+    codes = torch.as_tensor(rng.integers(0, 0x70, (4, 2, 1, 64, 64)), dtype=torch.uint8).to(DEV)
+    scales = torch.full((4, 2, 1), 2.0 ** -7, device=DEV)
+    table = torch.as_tensor(rng.integers(0, 4, (reqs, 1)), dtype=torch.int32).to(DEV)
+    lens = torch.full((reqs,), n, dtype=torch.int32, device=DEV)
+    counts = np.zeros(reqs, np.int64)
+    counts[full] = 1
+    starts = torch.as_tensor(_starts(counts)).to(DEV)
+    q = torch.as_tensor(rng.standard_normal((len(full), 2, 64))).to(torch.bfloat16).to(DEV)
+    _, lse = ds.kv8_decode(q[:, None], codes, scales, table[np.sort(full)], lens[:len(full)], 0.125)
+    mass = torch.full((reqs, 1, 64), 3.0, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ds.kv8_mass(q, lse[:, 0], starts, codes, scales, table, lens, 0.125, mass, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    got = mass[np.sort(full), 0].double().cpu()
+    assert (got[:, n:] == 3).all() and (got[:, :n - 1] > 3).all()
+    # Sums of the two heads' weights, on 3 but for the token's own position.
+    assert ((got[:, :n].sum(-1) - 3 * (n - 1)) / 2 - 1).abs().max() <= n * 2.0 ** -23 + 2.0 ** -13
+    mass[np.sort(full)] = 3.0
+    assert (mass == 3).all()
+
+
+def test_one_token_has_no_stride(ds):
+    c = Cache([100], 2, 64, 14)
+    codes, scales, table, ln = c.device()
+    starts = torch.as_tensor(_starts([1])).to(DEV)
+    q, lse = c.q(1, 4).to(DEV), torch.full((1, 4), 5.0, device=DEV)
+    mass = torch.zeros((2, 1, 2, 64 * table.shape[1]), device=DEV)
+    for stride, m in ((256, mass[0]), (1 << 60, mass[1])):
+        status = ds.lib().ds_kv8_mass(
+            q.data_ptr(), stride, lse.data_ptr(), 1, starts.data_ptr(), 1, codes.data_ptr(),
+            scales.data_ptr(), codes.shape[0], table.data_ptr(), table.shape[1], ln.data_ptr(), 4, 2,
+            64, 0.125, m.data_ptr(), m.shape[2], None, torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+    torch.cuda.synchronize()
+    assert mass[0].any() and torch.equal(mass[0], mass[1])
+
+
 def test_capture_streams_and_two_at_once(ds):
     c = Cache([1500, 800], 2, 64, 10)
     codes, scales, table, ln = c.device()
