@@ -1,5 +1,6 @@
-// Contexts cut into spans, and the kernel that joins what the spans of a row gave:
-// shared by the decode and the tree attention over the block-scaled 8-bit cache.
+// Contexts cut into spans, and the kernel that joins what the spans of a row gave.
+// (The trees by tiles of 256 rows have spans of their own length and keep their
+// partial outputs in another order, which their own kernel joins.)
 #pragma once
 
 #include "kv8_common.cuh"

@@ -900,11 +900,15 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         l = swap[0] + swap[1];
       }
       if (part) {
-        // The row's part of the join: outputs relative to its reference, and (reference,
-        // sum). (The loads are the warp's, also where only some of its rows exist.)
+        // The row's part of the join: outputs relative to its reference, dims [dim / 4][rows]
+        // so that a warp writes 512 bytes in a piece (rows of their own, 16 bytes each,
+        // cost an item 4 us more), and (reference, sum). (The loads are the warp's, also
+        // where only some of its rows exist.)
         const int64_t group = ((int64_t)x.r * p.c.kv_heads + x.kvh) * p.row_units + x.row0 / kRows;
-        const int64_t slot = (group * p.spans + x.span) * p.rows + m * kTile + row;
-        float* to = p.part_o + slot * DIM + half * (DIM / H);
+        const int64_t slot0 = (group * p.spans + x.span) * p.rows;
+        const int rr = m * kTile + row;
+        float4* to = reinterpret_cast<float4*>(p.part_o + slot0 * DIM) +
+                     half * (DIM / 4 / H) * p.rows + rr;
 #pragma unroll 1
         for (int c = 0; c < DIM / H; c += 16) {
           float o[16];
@@ -916,13 +920,12 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
           if (row < rows) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(to + c + i) =
-                  make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              to[(c + i) / 4 * p.rows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
           __syncwarp();
         }
         if (half == 0 && row < rows)
-          p.part_ml[slot] = make_float2(unset ? (low ? kOnlyLow : -INFINITY) : ref, l);
+          p.part_ml[slot0 + rr] = make_float2(unset ? (low ? kOnlyLow : -INFINITY) : ref, l);
         if constexpr (H == 2)
           named_bar_sync(pair, 64);
         else
@@ -1362,16 +1365,78 @@ size_t kv8_tree_workspace_bytes(int64_t requests, int next_n, int heads, int kv_
          pad256((size_t)s.slots * 8) + 256;
 }
 
+namespace {
+
+// Joins the spans of a tree's rows, in order. A block has 32 rows of a unit, one a
+// lane, and each warp an eighth of the dims. Requests with one span (or none) are
+// complete already.
+template <int DIM>
+__global__ void __launch_bounds__(256) kv8_tree_join_kernel(const JoinArgs p) {
+  constexpr int V = DIM / 4 / 8;        // float4s of a thread
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int blocks = (p.rows + 31) / 32;
+  const int64_t group = blockIdx.x / blocks;                  // (request, kv head, unit)
+  const int rr = blockIdx.x % blocks * 32 + lane;
+  const int row = (int)(group % p.row_groups) * kRows + rr;   // of the kv head's
+  const int64_t rk = group / p.row_groups, r = rk / p.c.kv_heads;
+  const int kvh = (int)(rk % p.c.kv_heads);
+  pdl_wait();
+  pdl_trigger();
+  const int64_t most = p.c.bt_stride * kPage, raw = p.c.lens[r];
+  const int len = (int)(raw < 0 ? 0 : (raw > most ? most : raw));
+  const int span = TreeSpans::of(len);
+  const int spans = (len + span - 1) / span;
+  if (spans <= 1 || rr >= p.rows || row >= p.next_n * p.group) return;
+  const int64_t slot0 = group * p.spans * p.rows;
+  const float2* ml = p.part_ml + slot0 + rr;
+  const float4* o = reinterpret_cast<const float4*>(p.part_o + slot0 * DIM) +
+                    (int64_t)warp * V * p.rows + rr;
+  float M = -INFINITY;
+  for (int s = 0; s < spans; ++s) M = fmaxf(M, ml[s * p.rows].x);
+  const float m0 = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  float4 acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < spans; ++s) {
+    const float2 x = ml[s * p.rows];
+    const float wt = ex2(x.x - m0);
+    L = __fmaf_rn(wt, x.y, L);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float4 v = o[((int64_t)s * (DIM / 4) + i) * p.rows];
+      acc[i] = make_float4(__fmaf_rn(wt, v.x, acc[i].x), __fmaf_rn(wt, v.y, acc[i].y),
+                           __fmaf_rn(wt, v.z, acc[i].z), __fmaf_rn(wt, v.w, acc[i].w));
+    }
+  }
+  if (M == kOnlyLow) L = NAN;
+  const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
+  const int64_t w =
+      (r * p.next_n + row / p.group) * p.heads + kvh * p.group + row % p.group;
+  uint4* out = reinterpret_cast<uint4*>(p.out + w * DIM + warp * V * 4);
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    const __nv_bfloat162 b[4] = {__floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv),
+                                 __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv),
+                                 __floats2bfloat162_rn(acc[i + 1].x * inv, acc[i + 1].y * inv),
+                                 __floats2bfloat162_rn(acc[i + 1].z * inv, acc[i + 1].w * inv)};
+    out[i / 2] = *reinterpret_cast<const uint4*>(b);
+  }
+  if (warp == 0) p.lse[w] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
 template <int DIM>
 cudaError_t launch_tree(const Params& p, int dev, cudaStream_t stream) {
   const cudaError_t e = launch<DIM, true>(p, dev, stream);
   if (e != cudaSuccess || p.spans == 1) return e;   // no table holds a row of two spans
-  const int64_t rows = p.c.requests * p.next_n * p.heads;
   const JoinArgs a{p.part_o, p.part_ml, p.out,  p.lse,       p.c,    p.next_n,
                    p.heads,  p.group,   p.rows, p.row_units, p.spans};
-  return launch_pdl(kv8_join_kernel<DIM, TreeSpans>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0,
-                    stream, 1u, a);
+  const int64_t blocks = p.c.requests * p.c.kv_heads * p.row_units * ((p.rows + 31) / 32);
+  return launch_pdl(kv8_tree_join_kernel<DIM>, dim3((unsigned)blocks), dim3(256), 0, stream, 1u, a);
 }
+
+}  // namespace
 
 cudaError_t launch_kv8_tree(const Kv8AttnArgs& a, cudaStream_t stream) {
   int dev = 0;
