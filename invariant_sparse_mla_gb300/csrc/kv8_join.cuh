@@ -11,6 +11,7 @@ namespace dsmla {
 // where MAX allows it: a function of the request's length alone.
 template <int MIN, int MAX, int MOST>
 struct SpanRule {
+  static constexpr int kMost = MOST;
   __host__ __device__ static int of(int64_t len) {
     int s = MIN;
     while (s < MAX && (int64_t)s * MOST < len) s *= 2;

@@ -527,46 +527,78 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         // The rows' q, each times a power of two of its own, in f16. A warp does
         // its 32 rows, or 16 of them, RI at a time.
         constexpr int RL = DIM / 8, RI = 32 / RL;      // lanes of a row; rows of a step
+        constexpr int NR = RL / H;                     // steps
         const int sub = lane / RL, ch = lane % RL;     // row of the step, 16-byte chunk
-        uint4 v[RL / H];
+        uint4 v[NR];
+        {
+          // From a row to the one RI behind it without a division each (half of this
+          // stretch's instructions, which took 8000 cycles of an item).
+          const int r0 = first + (warp & 3) * 32 + half * 16 + sub;
+          const int tokens = RI / p.group, heads = RI % p.group;
+          const int64_t step = tokens * p.q_stride + heads * DIM;
+          const int64_t wrap = p.q_stride - (int64_t)p.group * DIM;
+          int head = r0 % p.group;
+          const __nv_bfloat16* at = p.q + offset(half * 16 + sub, p.q_stride) + ch * 8;
 #pragma unroll
-        for (int i = 0; i < RL / H; ++i) {
-          const int rr = half * 16 + i * RI + sub;
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < left)
-            v[i] = *reinterpret_cast<const uint4*>(p.q + offset(rr, p.q_stride) + ch * 8);
+          for (int i = 0; i < NR; ++i) {
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (half * 16 + i * RI + sub < left) v[i] = *reinterpret_cast<const uint4*>(at);
+            head += heads;
+            at += step;
+            if (head >= p.group) {
+              head -= p.group;
+              at += wrap;
+            }
+          }
+        }
+        // Largest magnitude bits of the rows (NaN above infinity), two values a word:
+        // reduced over a row's lanes so that lane ch ends with step ch / H's alone, and
+        // works its factors out for all.
+        uint32_t t[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+          t[i] = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                          __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+#pragma unroll
+        for (int o = RL / 2, n = NR; o > 0; o >>= 1) {
+          if (n > 1) {
+            n /= 2;
+            const bool upper = (ch & o) != 0;
+#pragma unroll
+            for (int i = 0; i < NR / 2; ++i)
+              if (i < n) {
+                const uint32_t keep = upper ? t[i + n] : t[i], give = upper ? t[i] : t[i + n];
+                t[i] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, o));
+              }
+          } else {
+            t[0] = __vmaxu2(t[0], __shfl_xor_sync(0xffffffffu, t[0], o));
+          }
+        }
+        const uint32_t top = max(t[0] << 16, t[0] & 0xFFFF0000u);
+        // Largest |q| 2^k in [2^14, 2^15); 2^k stays a normal float.
+        int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
+        k = k > 120 ? 120 : (k < -120 ? -120 : k);
+        const float up = copysignf(__uint_as_float((uint32_t)(k + 127) << 23), p.scale_log2);
+        const float mine =
+            top >= 0x7F800000u
+                ? NAN
+                : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
+        if constexpr (H == 2) {
+          if (ch % H == 0) factor[(warp & 3) * 32 + half * 16 + ch / H * RI + sub] = mine;
+        } else {
+          f = __shfl_sync(0xffffffffu, mine, (lane % RI) * RL + lane / RI);
         }
         uint8_t* dst = smem + LY::kQ + m * LY::kTileBytes + (ch >> 3) * LY::kBlock;
 #pragma unroll
-        for (int i = 0; i < RL / H; ++i) {
+        for (int i = 0; i < NR; ++i) {
           const int rr = (warp & 3) * 32 + half * 16 + i * RI + sub;
+          const float by = __shfl_sync(0xffffffffu, up, sub * RL + i * H);
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t top = 0u;   // largest magnitude bits (NaN above infinity)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            top = max(top, max((w[u] << 16) & 0x7FFFFFFFu, w[u] & 0x7FFF0000u));
-#pragma unroll
-          for (int o = RL / 2; o > 0; o >>= 1)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // Largest |q| 2^k in [2^14, 2^15); 2^k stays a normal float.
-          int k = top > 0u ? 14 - ((int)(top >> 23) - 127) : 0;
-          k = k > 120 ? 120 : (k < -120 ? -120 : k);
-          const float up = copysignf(__uint_as_float((uint32_t)(k + 127) << 23), p.scale_log2);
-          const float mine =
-              top >= 0x7F800000u
-                  ? NAN
-                  : __uint_as_float((uint32_t)(127 - k) << 23) * fabsf(p.scale_log2);
-          if constexpr (H == 2) {
-            if (ch == 0) factor[rr] = mine;
-          } else {
-            const float its = __shfl_sync(0xffffffffu, mine, (lane % RI) * RL);
-            if (lane / RI == i) f = its;
-          }
           uint32_t h[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const __half2 y = __floats2half2_rn(__uint_as_float(w[u] << 16) * up,
-                                                __uint_as_float(w[u] & 0xFFFF0000u) * up);
+            const __half2 y = __floats2half2_rn(__uint_as_float(w[u] << 16) * by,
+                                                __uint_as_float(w[u] & 0xFFFF0000u) * by);
             h[u] = *reinterpret_cast<const uint32_t*>(&y);
           }
           *reinterpret_cast<uint4*>(dst + swz<128>(rr, (ch & 7) * 16)) =
@@ -910,16 +942,21 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
         float4* to = reinterpret_cast<float4*>(p.part_o + slot0 * DIM) +
                      half * (DIM / 4 / H) * p.rows + rr;
 #pragma unroll 1
-        for (int c = 0; c < DIM / H; c += 16) {
-          float o[16];
-          tmem_ld<16>(t_o + c, o);
-          tmem_fence<16>(o);
-          const uint32_t bits = row_nan ? row_bits[c >> 4] : 0u;
+        for (int c = 0; c < DIM / H; c += 32) {
+          float o[32];
+          tmem_ld32(t_o + c, o);
+          tmem_fence<32>(o);
+          if (row_nan) {
+            const uint32_t bits = row_bits[c >> 4] | (uint32_t)row_bits[(c >> 4) + 1] << 16;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = (bits >> i) & 1 ? NAN : o[i] * 0.125f;
+            for (int i = 0; i < 32; ++i)
+              if ((bits >> i) & 1) o[i] = NAN;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= 0.125f;
           if (row < rows) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
+            for (int i = 0; i < 32; i += 4)
               to[(c + i) / 4 * p.rows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
           __syncwarp();
@@ -1391,21 +1428,28 @@ __global__ void __launch_bounds__(256) kv8_tree_join_kernel(const JoinArgs p) {
   const float2* ml = p.part_ml + slot0 + rr;
   const float4* o = reinterpret_cast<const float4*>(p.part_o + slot0 * DIM) +
                     (int64_t)warp * V * p.rows + rr;
+  constexpr int S = TreeSpans::kMost;
+  float2 x[S];
   float M = -INFINITY;
-  for (int s = 0; s < spans; ++s) M = fmaxf(M, ml[s * p.rows].x);
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < spans) x[s] = ml[s * p.rows];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < spans) M = fmaxf(M, x[s].x);
   const float m0 = M == -INFINITY ? 0.0f : M;
   float L = 0.0f;
   float4 acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int s = 0; s < spans; ++s) {
-    const float2 x = ml[s * p.rows];
-    const float wt = ex2(x.x - m0);
-    L = __fmaf_rn(wt, x.y, L);
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (s >= spans) break;
+    const float wt = ex2(x[s].x - m0);
+    L = __fmaf_rn(wt, x[s].y, L);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float4 v = o[((int64_t)s * (DIM / 4) + i) * p.rows];
+      const float4 v = o[(s * (DIM / 4) + i) * p.rows];
       acc[i] = make_float4(__fmaf_rn(wt, v.x, acc[i].x), __fmaf_rn(wt, v.y, acc[i].y),
                            __fmaf_rn(wt, v.z, acc[i].z), __fmaf_rn(wt, v.w, acc[i].w));
     }
