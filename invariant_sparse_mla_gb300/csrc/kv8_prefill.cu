@@ -72,7 +72,12 @@ constexpr int kTile = 128;               // positions per K/V tile (two pages)
 constexpr int kRows = 256;               // query rows per CTA
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMaxCtas = 192;
-// Trees of drafts: contexts are cut so that few requests fill the GPU too.
+// Trees of drafts: contexts are cut so that few requests fill the GPU too, into at most
+// 8 spans. An item costs about 8 us beside its tiles (q, the first S, partial outputs):
+// 16 requests x 24 nodes on 4096 to 32768 positions, 64 / 8 heads x 128, take 433 us, of
+// which the join is about 25. At most 4 spans, or 1, took 417 or 613 us where 8 took 463
+// (few items are badly spread), and one request on 32768 positions 185 or 601 where 8
+// took 118.
 using TreeSpans = SpanRule<1024, 1 << 28, 8>;
 
 // What the first kernel writes: item (unit u of one kv head) has weight
