@@ -191,3 +191,21 @@ def test_bindings_reject_cpu_tensors(ds):
         ds.kv8_evict(z(1, 1, 64), 32, 0, 0, pages, scales, i.view(1, 1), i)
     with pytest.raises(ValueError):
         ds.pages_shrink(i, i.view(1, 1), i, i, i)
+
+
+@host_only
+def test_tree_workspace(L):
+    """Its size changes with the form (rows of a kv head), and the call asks for it."""
+    size = L.ds_kv8_tree_decode_workspace_size
+    few, many = (2, 20, 8, 2, 128, 64), (2, 21, 8, 2, 128, 64)
+    assert size(*few) == L.ds_kv8_decode_workspace_size(*few)
+    # 4 spans at most (4096 positions) of 84 rows, for 2 requests x 2 kv heads
+    assert size(*many) >= 2 * 2 * 4 * 84 * (128 * 4 + 8)
+    for nn, need in ((20, size(*few)), (21, size(*many))):
+        _bad(L, "ds_kv8_tree_decode", TREE)(DS_ERR_WORKSPACE, f"the {need} bytes needed", nn=nn, bts=64,
+                                            wsb=need - 1)
+    for i, (value, word) in enumerate([(-1, "num_requests"), (65, "next_n"), (9, "num_heads"),
+                                       (0, "num_kv_heads"), (96, "head_dim"), (0, "bt_stride")]):
+        args = list(many)
+        args[i] = value
+        assert size(*args) == 0 and word in _msg(L), (args, _msg(L))
