@@ -222,6 +222,35 @@ def test_codes_under_equal_scales_are_copied(ds, value):
         assert not _evict(ds, lens, 80, 2, 20, 2, 128, seed=6, edit=edit)
 
 
+def test_accept_captured_and_two_evictions_at_once(ds):
+    c = Cache([700, 900], 2, 64, 16)
+    codes, scales, table, lens = c.device()
+    acc = _i32([[0, 3, 7, -1], [2, -1, -1, -1]])
+    want = (codes.clone(), scales.clone())
+    new = ds.kv8_accept([want], table, lens, 8, acc)
+    got = (codes.clone(), scales.clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lens2 = ds.kv8_accept([got], table, lens, 8, acc)
+    g.replay()
+    torch.cuda.synchronize()
+    # (As bits: the scales of unused pages are NaN.)
+    assert torch.equal(new, lens2) and torch.equal(got[0], want[0])
+    assert torch.equal(got[1].view(torch.int32), want[1].view(torch.int32))
+    mass = torch.rand((2, 2, 64 * table.shape[1]), device=DEV)
+
+    def evict(kw):
+        m, k, s = mass.clone(), codes.clone(), scales.clone()
+        torch.cuda.synchronize()
+        new = ds.kv8_evict(m, 300, 4, 50, k, s, table, lens, **kw)
+        return m, k, s.view(torch.int32), new
+    one = evict({})
+    for _ in range(3):
+        both = [evict(dict(stream=torch.cuda.Stream())) for _ in range(2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for b in both for x, y in zip(b, one))
+
+
 # ------------------------------------------------------------------ shrink
 @pytest.mark.parametrize("rows,new_lens", [
     ([0], [64]), ([0, 1, 2, 4], [0, 64, 0, 129]), ([4, -1, 0], [1, 7, 700]), ([3, 2], [0, 1]),

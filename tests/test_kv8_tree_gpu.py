@@ -159,6 +159,34 @@ def test_bits_do_not_depend_on_the_batch(ds, n, dim):
         assert torch.equal(one[0][0], whole[0][r]) and torch.equal(one[1][0], whole[1][r])
 
 
+@pytest.mark.parametrize("n", [5, 24])
+def test_captured_and_on_two_streams(ds, n):
+    """Both forms, replayed twice, and two calls at once."""
+    c = Cache([2500, 64, 9000, 0], 2, 128, seed=15)
+    masks = _dev(_tree(c.rng, 4, n))
+    codes, scales, table, lens = c.device()
+    q = c.q(4 * n, 16).to(DEV).view(4, n, 16, 128)
+
+    def run(x, **kw):
+        return ds.kv8_tree_decode(x, masks, codes, scales, table, lens, 0.1, **kw)
+    want, other = run(q), run(-q)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        a, b = run(q, stream=streams[0]), run(-q, stream=streams[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((*a, *b), (*want, *other)))
+    x = q.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(x)
+    for y, ref in ((-q, other), (q, want)):
+        x.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, ref))
+
+
 def test_refusals(ds):
     c = Cache([100], 2, 64, seed=9)
     codes, scales, table, lens = c.device()
