@@ -81,6 +81,9 @@ constexpr int kNS = 3;                     // S buffers of few rows (more: one f
 constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
                                            // when a step is summed, Q once its product is done)
 constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
+// Word of an lse slot (behind the factors, of which few rows need kFewRows) that tells
+// whether a row of the step is left out: the paths without masks are not for it then.
+constexpr int kLeftOut = 3 * kStep - 1;
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 
 template <int DIM>
@@ -91,7 +94,7 @@ struct Layout {
   static constexpr int kNQ = DIM == 128 ? 2 : 4;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kNK * kKBytes;
-  static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: 128 lse, visible, factors
+  static constexpr int kLse = kQ + kNQ * kQBytes;   // per slot: lse, visible, factors; kStep each
   static constexpr int kBars = kLse + kNL * kStep * 12;
   static constexpr int kMeta = kBars + 136 * 8;               // kMetaSlots x float4
   static constexpr int kList = kMeta + kMetaSlots * 16;       // kItems x Item
@@ -327,6 +330,15 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
     return make_sw128_desc(addr, 16, 1024);
   else
     return make_sw64_desc(addr, 16, 512);
+}
+
+// Whether one of tokens from .. n - 1 has a head that is not left out; lse is the group's
+// of token 0. (The last token first: it sees all of the others' positions.)
+__device__ __noinline__ bool weighs(const float* lse, int heads, int group, int from, int n) {
+  for (int i = n - 1; i >= 0 && i >= from; --i)
+    for (int h = 0; h < group; ++h)
+      if (lse[(int64_t)i * heads + h] != -INFINITY) return true;
+  return false;
 }
 
 template <int DIM>
@@ -754,10 +766,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
       if (w.same) continue;
       const int seen = w.raw - w.n + 1;        // by token 0
       const float* lse0 = p.lse + (int64_t)w.t0 * p.heads + w.kvh * p.group;
-      // A row that there is not sees nothing, and one of -inf adds nothing.
+      // A row that there is not sees nothing, nor does one of lse -inf: its q may hold
+      // anything, and infinity or NaN less infinity is NaN.
+      bool out = false;      // some row of this lane's is left out
       auto put = [&](uint32_t slot, int i, bool in, int token, float l) {
         float* ls = reinterpret_cast<float*>(smem + LY::kLse + slot * (kStep * 12)) + lane + 32 * i;
-        ls[0] = in && l != -INFINITY ? -l * kLog2e : -INFINITY;
+        out |= in && l == -INFINITY;
+        in &= l != -INFINITY;
+        ls[0] = in ? -l * kLog2e : -INFINITY;
         reinterpret_cast<int*>(ls)[kStep] = in ? seen + token : INT_MIN;
       };
       // (Its arrival counts for Q's stage too, which has to be free for that.)
@@ -767,6 +783,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
         return __all_sync(0xffffffffu, ok);
       };
       auto arrive = [&] {
+        out = __any_sync(0xffffffffu, out);
+        if (lane == 0)
+          reinterpret_cast<int*>(smem + LY::kLse + ql % kNL * (kStep * 12))[kLeftOut] = out;
+        out = false;
         mbar_arrive(&bars[kLFull + ql % kNL]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kQFull + ql % NQ]);
@@ -993,6 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           const int pos0 = tile_u * kTile, pos = pos0 + tok;
           const float2 ks = make_float2(k0.scale, k0.scale), w5 = make_float2(0x1p-5f, 0x1p-5f);
           float2 acc[2] = {};
+          const bool all = pos0 + kTile - 1 <= base && vs[kLeftOut - kStep] == 0;
           for (int c = 0; c < rows; c += 8) {
             float x[3][8];
 #pragma unroll
@@ -1016,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
               y[e] = fma2(y[e], mul2(f[e], ks), l[e]);
             }
             // Rows that do not see the position; columns behind the rows hold anything.
-            if (pos0 + kTile - 1 > base || c + 8 > rows) {
+            if (!all || c + 8 > rows) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int2 v = *reinterpret_cast<const int2*>(vs + c + 2 * e);
@@ -1098,7 +1119,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           const int here =
               s + 1 < now.steps && p.chunks == 1 ? capacity : step_of(p, now.n, now.first, s).rows;
           const int c0 = half * (kStep / 2);
-          if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile)) {
+          if (here == capacity && capacity > kStep - 16 && !(edge && vs[0] < pos0 + kTile) &&
+              vs[kLeftOut - kStep] == 0) {
 #pragma unroll
             for (int c = 0; c < kStep / 2; c += 32) {
               float x[32];
@@ -1144,6 +1166,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_mass_kernel(
           if (ok) {
             total += other[slot * kTile + tok];
             mbar_arrive(&bars[kXFree + slot]);
+            // (Rarely: unless only rows that are left out see the position.)
+            if (total != total && !weighs(p.lse + (int64_t)now.t0 * p.heads + now.kvh * p.group,
+                                          p.heads, p.group, pos - base, now.n))
+              total = 0.0f;
             put(pos0, keys.there, total);
           }
         }

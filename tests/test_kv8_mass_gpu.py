@@ -359,3 +359,94 @@ def test_refusals(ds):
                     0.1, mass)
     ds.kv8_mass(q[:0], lse[:0], starts * 0, codes, scales, table, ln, 0.1, mass)
     assert (mass == 0).all()
+
+
+def _mass(ds, c, q, lse, starts, scale, codes=None):
+    """The kernel's mass on top of ones, as a host tensor."""
+    dev_codes, scales, table, lens = c.device()
+    mass = torch.ones((len(c.lens), c.kv_heads, 64 * table.shape[1]), device=DEV)
+    ds.kv8_mass(q.to(DEV), torch.as_tensor(lse).to(DEV), torch.as_tensor(starts).to(DEV),
+                dev_codes if codes is None else codes.to(DEV), scales, table, lens, scale, mass)
+    torch.cuda.synchronize()
+    return mass.cpu()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,counts,heads,hk", [
+    ([200, 150], [3, 2], 4, 2), ([300, 64], [1, 1], 16, 2), ([700, 500], [200, 250], 4, 2),
+    ([600, 129], [40, 1], 14, 2), ([400, 300], [130, 128], 300, 1)])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), 3e38])
+def test_a_row_of_lse_minus_infinity_is_left_out_whatever_its_q(ds, lens, counts, heads, hk, dim, fill):
+    """Padding: q that holds anything, or scores that overflow, under an lse of -inf."""
+    if heads > 100:
+        counts = [x // 40 for x in counts]
+    c = Cache(lens, hk, dim, 21)
+    starts, scale = _starts(counts), dim ** -0.5
+    q = c.q(int(starts[-1]), heads)
+    lse = _lse_of(q, starts, c, scale)
+    dead = c.rng.random(lse.shape) < 0.1
+    for a, b in zip(starts, starts[1:]):
+        dead[(a + b) // 2] = True              # a whole token, in the middle
+        dead[b - 1, heads // 2] = True         # a head of the one that sees everything
+        dead[a, 0] = True                      # a step's first row
+    lse[dead] = -np.inf
+    junk = q.clone()
+    q[torch.as_tensor(dead)] = 0.0
+    junk[torch.as_tensor(dead)] = fill
+    want, got = _mass(ds, c, q, lse, starts, scale), _mass(ds, c, junk, lse, starts, scale)
+    assert torch.isfinite(want).all() and torch.equal(got, want)
+    # and those are the sums without these rows
+    old = np.ones(tuple(want.shape), np.float32)
+    ref, reach = oracle.kv8_mass(bits(q), lse, starts, c.codes, c.scales, c.table, c.lens, scale, old)
+    _check(got.numpy(), ref, old, reach, dim, max(counts) * heads // hk // 128 + 1, starts, c.lens,
+           c.table.shape[1])
+    # no row at all: what lies before the call's tokens stays, their own positions are 0
+    none = _mass(ds, c, torch.full_like(q, fill), np.full_like(lse, -np.inf), starts, scale)
+    for r, (n, length) in enumerate(zip(counts, lens)):
+        assert (none[r, :, :length - n] == 1).all() and (none[r, :, length - n:length] == 0).all()
+
+
+@pytest.mark.parametrize("counts", [[3, 2], [60, 90]])
+def test_lse_of_plus_infinity_adds_nothing(ds, counts):
+    c = Cache([200, 300], 2, 64, 22)
+    starts = _starts(counts)
+    q = c.q(sum(counts), 4)
+    lse = _lse_of(q, starts, c, 0.125)
+    minus, plus = lse.copy(), lse.copy()
+    minus[1, 0] = minus[-1, 3] = -np.inf
+    plus[1, 0] = plus[-1, 3] = np.inf
+    want = _mass(ds, c, q, minus, starts, 0.125)
+    assert torch.equal(_mass(ds, c, q, plus, starts, 0.125), want) and torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("lens,counts", [([200], [3]), ([400], [1]), ([300], [60]), ([700], [250])])
+@pytest.mark.parametrize("at", [3, 60])
+def test_a_nan_key_shows_where_a_row_of_weight_sees_it(ds, lens, counts, at):
+    """Its dim in either half of the head; a position that only rows of lse -inf see
+    gets nothing."""
+    c = Cache(lens, 2, 64, 23)
+    n, starts = counts[0], _starts(counts)
+    q = c.q(n, 4)
+    lse = _lse_of(q, starts, c, 0.125)
+    codes, _, table, _ = c.device()
+
+    def poisoned(pos):
+        bad = codes.clone()
+        bad[table[0, pos // 64].item(), 0, 1, pos % 64, at] = 0xFF
+        return bad
+    last = lens[0] - 1
+    for pos in (0, lens[0] - n, last):
+        want = _mass(ds, c, q, lse, starts, 0.125)
+        got = _mass(ds, c, q, lse, starts, 0.125, poisoned(pos))
+        assert got[0, 1, pos].isnan() and got.isnan().sum() == 1
+        got[0, 1, pos] = want[0, 1, pos]
+        assert torch.equal(got, want)
+    # the last token's rows of kv head 1 have no weight: nobody else sees its position
+    lse[-1, 2:] = -np.inf
+    want = _mass(ds, c, q, lse, starts, 0.125)
+    got = _mass(ds, c, q, lse, starts, 0.125, poisoned(last))
+    assert got[0, 1, last] == 0 and torch.equal(got, want)
+    # one of its two heads has: the position is NaN
+    lse[-1, 3] = 5.0
+    got = _mass(ds, c, q, lse, starts, 0.125, poisoned(last))
+    assert got[0, 1, last].isnan() and got.isnan().sum() == 1
