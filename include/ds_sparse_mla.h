@@ -556,7 +556,8 @@ size_t ds_kv8_prefill_workspace_size(int64_t num_tokens, int64_t num_requests, i
  * a_i = position * inv_freq_i: (u cos a_i - v sin a_i, v cos a_i + u sin a_i).
  * Pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved != 0. All
  * in float32 (squares of values above 2^63 overflow there), rounded to bfloat16
- * once; the angle is exact to about 2^-22 turns at any position.
+ * once; the angle is exact to 2^-22 turns at any position, for frequencies up to
+ * 1024 in magnitude.
  *
  *  q, k         bfloat16, row t at q + t * q_stride (k + t * k_stride)
  *               elements, [heads, head_dim] contiguous; 16-byte aligned, strides

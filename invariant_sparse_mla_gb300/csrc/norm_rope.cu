@@ -5,9 +5,10 @@
 //   y_d = x_d behind,
 // and with angles a_i = position * inv_freq_i the pairs (u, v) of the rotated dims
 //   (u cos a_i - v sin a_i, v cos a_i + u sin a_i),
-// all in fp32 and rounded to bf16 once. The angle is taken in turns: position and
-// frequency are multiplied in two floats each, whole turns are dropped from the
-// high part exactly, so that a position of 10^6 loses no more than one of 10.
+// all in fp32 and rounded to bf16 once. The angle is taken in turns: the position in two
+// floats times the frequency in three, whole turns dropped from each product exactly, so
+// that a position of 2^31 loses no more than one of 10 (with frequencies up to 1024 the
+// angle is off by 2^-23 turns; with the frequency in two floats it was 2^-18.5).
 //
 // Layout. A row is cut into units of two 16-byte chunks so that a unit holds
 // both halves of the pairs it rotates (dims i and i + rot / 2 are 8 chunks apart
@@ -58,17 +59,24 @@ struct Params {
 
 // cos and sin of pos * freq.
 __device__ __forceinline__ float2 rotation(int pos, float freq) {
-  // 1 / (2 pi) in two floats; the frequency in turns, in two floats.
-  constexpr double kInv2Pi = 0.15915494309189533576888;
-  constexpr float kHi = (float)kInv2Pi, kLo = (float)(kInv2Pi - (double)kHi);
-  const float fh = freq * kHi;
-  const float fl = __fmaf_rn(freq, kLo, __fmaf_rn(freq, kHi, -fh));
-  // The position as a multiple of 4096 and a rest, both exact in a float.
+  // 1 / (2 pi) in three floats.
+  constexpr float kHi = 0x1.45f306p-3f, kLo = 0x1.b93910p-28f, kRest = 0x1.529fc2p-54f;
+  // The frequency in turns, fh + fl + fr: fl is (what fh leaves) + freq * kLo, fr what the
+  // rounding of that sum leaves (Knuth's sum) and the last term. (No product below is
+  // contracted with a sum: its own rounding error is what the next term holds.)
+  const float fh = __fmul_rn(freq, kHi), r = __fmaf_rn(freq, kHi, -fh);
+  const float p = __fmul_rn(freq, kLo), pl = __fmaf_rn(freq, kLo, -p);
+  const float fl = __fadd_rn(r, p), y = __fsub_rn(fl, r);
+  const float left = __fadd_rn(__fsub_rn(r, __fsub_rn(fl, y)), __fsub_rn(p, y));
+  const float fr = __fadd_rn(left, __fmaf_rn(freq, kRest, pl));
+  // The position as a multiple of 4096 and a rest, both exact in a float. Near 2^31
+  // the products of a have whole turns down to that with fl.
   const float a = (float)(pos & ~4095), b = (float)(pos & 4095);
-  const float ah = a * fh, al = __fmaf_rn(a, fh, -ah);
-  const float bh = b * fh, bl = __fmaf_rn(b, fh, -bh);
+  const float ah = __fmul_rn(a, fh), al = __fmaf_rn(a, fh, -ah);
+  const float am = __fmul_rn(a, fl), ar = __fmaf_rn(a, fl, -am);
+  const float bh = __fmul_rn(b, fh), bl = __fmaf_rn(b, fh, -bh);
   float t = (ah - rintf(ah)) + (bh - rintf(bh));
-  t += (al - rintf(al)) + (bl + __fmaf_rn(a, fl, b * fl));
+  t += ((al - rintf(al)) + (am - rintf(am))) + (__fmaf_rn(a, fr, ar) + __fmaf_rn(b, fl, bl));
   float2 cs;
   sincospif(2.0f * t, &cs.y, &cs.x);
   return cs;

@@ -1,5 +1,7 @@
 """GPU tests of the norm of queries and keys with rotation against float64."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -199,3 +201,63 @@ def test_refusals(ds):
         ds.qk_norm_rope(q, k, pos, f.cpu())
     e, _ = ds.qk_norm_rope(q[:0], None, pos[:0], f)
     assert e.shape == (0, 2, 128)
+
+
+# 1 / (2 pi) to 60 digits, as a fraction.
+_INV_2PI = Fraction("0.159154943091895335768883763372514362034459645740456448747667")
+
+
+def _angle(pos, freq):
+    """pos * freq without its whole turns, exact to a float64's rounding."""
+    turns = Fraction(int(pos)) * Fraction(float(freq)) * _INV_2PI
+    return 2 * np.pi * float(turns - round(turns))
+
+
+def _nearly_cancelling(angle):
+    """(u, v) of 8 significant bits each whose u cos a - v sin a is near 0, so that
+    no rounding of it hides the angle: the best of all pairs."""
+    c, s = np.cos(angle), np.sin(angle)
+    m = np.arange(128.0, 256.0)
+    best = None
+    for e in (-1, 0, 1):                       # |u / v| near |tan a|
+        shift = 2.0 ** (np.floor(np.log2(abs(s / c))) + e)
+        u, v = m[:, None] * shift, m[None, :]
+        r = np.abs(u * abs(c) - v * abs(s)) / np.hypot(u, v)
+        i, j = np.unravel_index(np.argmin(r), r.shape)
+        if best is None or r[i, j] < best[0]:
+            best = r[i, j], u[i, 0], v[0, j]
+    _, u, v = best
+    scale = 2.0 ** -np.floor(np.log2(max(u, v)))
+    return u * scale, v * scale * np.sign(s * c)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("near,freqs", [
+    (1 << 12, [1.0, 0.3, 1e-3]), (10 ** 6, [1.0, 0.73, 0.01]), (1 << 27, [1.0, 0.71, 0.049]),
+    (1 << 30, [1.0, 0.649, 0.11]), ((1 << 31) - 50, [1.0, 0.649, 0.25, 0.0131]),
+    ((1 << 31) - 50, [16.0, 11.3, 2.5])])
+def test_angles_of_far_positions(ds, near, freqs, inter):
+    """Pairs that the turn brings near 0: the angle is off by 2^-22 turns at most
+    (2^-19.3 of the pair's length), sine and cosine, the products and their sum by four
+    half steps of float32 (each 2^-24 of at most 1.5 lengths, and twice that for the
+    functions), the result by one of bf16."""
+    rng = np.random.default_rng(near & 0xFFFF)
+    f = np.array(freqs * (8 // len(freqs) + 1), np.float32)[:8]
+    pos = np.concatenate([near - rng.integers(0, 40, 32), -near + rng.integers(0, 40, 32)]).astype(np.int32)
+    a = np.array([[_angle(p, x) for x in f] for p in pos])
+    uv = np.array([[_nearly_cancelling(y) for y in row] for row in a])
+    u, v = uv[..., 0], uv[..., 1]
+    x = np.zeros((len(pos), 1, 16))
+    iu, iv = (np.arange(0, 16, 2), np.arange(1, 16, 2)) if inter else (np.arange(8), np.arange(8, 16))
+    x[:, 0, iu], x[:, 0, iv] = u, v
+    q = torch.as_tensor(x).to(torch.bfloat16)
+    assert (q.double().numpy() == x).all()
+    got, _ = ds.qk_norm_rope(q.to(DEV), None, torch.as_tensor(pos).to(DEV), torch.as_tensor(f).to(DEV),
+                             interleaved=inter)
+    got = got.double().cpu().numpy()[:, 0]
+    size = np.hypot(u, v)
+    e = size * (2 * np.pi * 2.0 ** -22 + 2.0 ** -21)
+    for at, y in ((iu, u * np.cos(a) - v * np.sin(a)), (iv, v * np.cos(a) + u * np.sin(a))):
+        err = np.abs(got[:, at] - y)
+        assert (err <= e + 2.0 ** -8 * (np.abs(y) + e)).all(), (err / size).max() / (2 * np.pi)
+    assert np.median(np.abs(u * np.cos(a) - v * np.sin(a)) / size) <= 2.0 ** -16
