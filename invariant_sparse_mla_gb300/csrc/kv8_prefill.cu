@@ -932,6 +932,8 @@ __global__ void __launch_bounds__(Layout<DIM>::kThreads, 1) kv8_prefill_kernel(c
       if constexpr (TREE) part = clamp_pos(p, x.raw_len) > TreeSpans::of(clamp_pos(p, x.raw_len));
       if (unset && low && !part) l = NAN;
       if constexpr (H == 2) {
+        // (Each thread has seen one page of a tile; a span reports for both.)
+        if (part) low = named_bar_or(pair, 64, low);
         swap[half] = l;
         named_bar_sync(pair, 64);
         l = swap[0] + swap[1];

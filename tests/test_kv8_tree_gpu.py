@@ -319,3 +319,22 @@ def test_many_large_trees(ds):
         one = ds.kv8_tree_decode(q[r:r + 1], md[r:r + 1].contiguous(), codes, scales,
                                  table[r:r + 1].contiguous(), ln[r:r + 1], 0.1)
         assert torch.equal(one[0][0], want[0][r]) and torch.equal(one[1][0], want[1][r])
+
+
+@pytest.mark.parametrize("dim,n,group", [(64, 24, 4), (64, 41, 8), (128, 24, 4), (64, 5, 4)])
+@pytest.mark.parametrize("length", [600, 3000])
+@pytest.mark.parametrize("gone", [0, 1, None])
+def test_scores_too_low_for_a_reference_give_nan(ds, dim, n, group, length, gone):
+    """Scores near -2^26 in every span, and the even or the odd pages outside the pool: the
+    outputs are NaN as where all pages are there, never 0 with an lse of -inf."""
+    c = Cache([length], 1, dim, seed=25)
+    c.codes[c.table[0, :-(-length // 64)]] = 0x7E          # 448 everywhere
+    c.scales[:] = 1.0
+    if gone is not None:
+        c.table[0, gone::2] = -1
+    q = torch.full((1, n, group, dim), -8.0, dtype=torch.bfloat16, device=DEV)
+    codes, scales, table, lens = c.device()
+    masks = _dev(_tree(c.rng, 1, n))
+    out, lse = ds.kv8_tree_decode(q, masks, codes, scales, table, lens, 2.0 ** 26 / (448 * 8 * dim))
+    torch.cuda.synchronize()
+    assert out.isnan().all() and lse.isnan().all()
