@@ -284,3 +284,71 @@ def test_shrink_then_extend_gives_the_lowest_pages_again(ds):
     b = oracle.pages_extend(a[0], a[1], a[2], [1, 0], [256, 300])
     torch.cuda.synchronize()
     assert (refs.tolist(), table.tolist(), lens.tolist()) == (b[0], b[1], b[2])
+
+
+def test_evictions_again_and_again(ds):
+    """A cache at its budget that grows by a few tokens and is cut again, many times: each
+    cut as the oracle's, and values no further off than one rounding in the normal
+    range and half a step of the page's present scale, and of each smaller one, below it."""
+    rng = np.random.default_rng(31)
+    reqs, hk, heads, d, budget, first, recent, width = 2, 2, 4, 64, 150, 3, 30, 5
+    pages = reqs * width
+    table = _i32(rng.permutation(pages).reshape(reqs, width))
+    codes = torch.zeros((pages, 2, hk, 64, d), dtype=torch.uint8, device=DEV)
+    scales = torch.ones((pages, 2, hk), device=DEV)
+    mass = torch.zeros((reqs, hk, 64 * width), device=DEV)
+    lens = np.zeros(reqs, np.int64)
+    exact = [[np.zeros((0, 2, d)) for _ in range(hk)] for _ in range(reqs)]
+    need = np.zeros((2, hk))                  # largest scale that any token asked for
+    cuts = 0
+    for step in range(24):
+        counts = [int(rng.integers(1, 9)) for _ in range(reqs)] if step else [150, 40]
+        lens += counts
+        n = sum(counts)
+        # (Tokens of very different sizes: pages' scales differ, and grow.)
+        x = rng.standard_normal((n, 2, hk, d)) * np.exp2(rng.uniform(-6, 6, (n, 2, hk, 1)))
+        x = torch.as_tensor(x).to(torch.bfloat16)
+        starts = _i32(np.concatenate([[0], np.cumsum(counts)]))
+        dev_lens, dev_x = _i32(lens), x.to(DEV)
+        ds.kv8_append(dev_x[:, 0], dev_x[:, 1], starts, table, dev_lens, codes, scales)
+        q = torch.as_tensor(rng.standard_normal((n, heads, d))).to(torch.bfloat16).to(DEV)
+        _, lse = ds.kv8_prefill(q, starts, codes, scales, table, dev_lens, 0.02)
+        ds.kv8_mass(q, lse, starts, codes, scales, table, dev_lens, 0.02, mass)
+        torch.cuda.synchronize()
+        before = [t.cpu().numpy() for t in (mass, codes, scales, table)]
+        got = ds.kv8_evict(mass, budget, first, recent, codes, scales, table, dev_lens)
+        torch.cuda.synchronize()
+        want = oracle.kv8_evict(before[0], budget, first, recent, before[1], before[2], before[3],
+                                dev_lens.cpu().numpy())
+        assert got.tolist() == want[3]
+        assert np.array_equal(mass.cpu().numpy(), want[0]) and not np.isnan(want[0]).any()
+        _same(codes, scales, want[1], want[2])
+        host = x.double().numpy()
+        top = np.maximum.reduce(np.abs(host).max(-1), axis=0) / 448
+        need = np.maximum(need, np.exp2(np.ceil(np.log2(top))))
+        at = 0
+        for r in range(reqs):
+            for g in range(hk):
+                e = np.concatenate([exact[r][g], host[at:at + counts[r], :, g]])
+                if lens[r] > budget:
+                    k = budget - first - recent
+                    best = oracle.topk_per_row(before[0][r, g][None], np.array([first], np.int32),
+                                               np.array([lens[r] - recent], np.int32), k)[0]
+                    e = e[[*range(first), *(first + int(b) for b in best),
+                           *range(lens[r] - recent, lens[r])]]
+                    cuts += 1
+                exact[r][g] = e
+            at += counts[r]
+        lens = np.minimum(lens, budget)
+    assert cuts >= 40
+    held_codes, held_scales = codes.cpu().numpy(), scales.cpu().numpy()
+    for r in range(reqs):
+        for g in range(hk):
+            for side in range(2):
+                p = table[r].cpu().numpy()[:-(-int(lens[r]) // 64)]
+                s = held_scales[p, side, g]
+                assert (s <= need[side, g]).all()
+                v = oracle.e4m3_to_float64(held_codes[p, side, g]) * s[:, None, None]
+                v, s = v.reshape(-1, d)[:lens[r]], np.repeat(s, 64)[:lens[r], None]
+                x = exact[r][g][:, side]
+                assert (np.abs(v - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -9 * s).all()
