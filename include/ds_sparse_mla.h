@@ -643,7 +643,7 @@ int ds_kv8_accept(const ds_kv8_layer* layers, int num_layers, int64_t num_pages,
  *               positions get nothing (0 where they are the call's own).
  *
  * Scores are products of bfloat16 q and the codes with fp32 sums (about 2^-20 of
- * the largest partial sum), exponentials and sums are fp32. Up to 40 rows a kv head
+ * the largest partial sum), exponentials and sums are fp32. Up to 24 rows a kv head
  * (tokens times heads of the group) take q as three E4M3 pieces: exact down to 2^-19
  * of the row's largest |q|, and below that off by at most 2^-27 of it. A NaN key makes its
  * own position NaN, a non-finite q or a NaN lse the positions that the row sees.

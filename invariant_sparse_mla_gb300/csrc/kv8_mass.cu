@@ -14,7 +14,7 @@
 // by TMA. Two forms, by the request's number of rows R = tokens * heads of the
 // group:
 //
-// - Few rows (R <= 40): K is multiplied as it lies, on the 8-bit tensor cores,
+// - Few rows (R <= 24): K is multiplied as it lies, on the 8-bit tensor cores,
 //   with q as three E4M3 pieces, each a column of its own under the row's power of
 //   two: q = 2^-k (q0 + q1 / 32 + q2 / 1024). A bf16 number has 8 significant
 //   bits, so this is exact down to 2^-19 of the row's largest |q| and off by up to
@@ -80,7 +80,15 @@ constexpr int kReaders = kSumWarps + 3;    // warps that read the list
 constexpr int kNS = 3;                     // S buffers of few rows (more: one for each place)
 constexpr int kNL = 8;                     // slots of lse (more than stages of Q: they are let go
                                            // when a step is summed, Q once its product is done)
-constexpr int kFewRows = 40;               // most rows that are multiplied in pieces
+// Most rows that are multiplied in pieces. us by pieces / as bf16, 64 / 8 heads x 128, inputs
+// not in L2:
+//   rows                                       8      16      24      32      40
+//   32 requests on 4096 to 32768 positions  148/298 192/300 277/301 294/310 314/337
+//   one on 32768                             29/40   34/40   39/40   42/40   46/42
+//   32 on 300 to 1000                        36/36   46/33   56/36   68/36   76/36
+// (Dim 64 is much the same: 120/275 and 31/33 with 8 rows, 282/300 and 54/36 with 24.) Beyond
+// 24 a long batch has 2 to 7 % of it, and a short one pays twice.
+constexpr int kFewRows = 24;
 // Word of an lse slot (behind the factors, of which few rows need kFewRows) that tells
 // whether a row of the step is left out: the paths without masks are not for it then.
 constexpr int kLeftOut = 3 * kStep - 1;
