@@ -292,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, UNITS == 1 ? 3 : (UNITS < 4 ? 2 : 1)
 template <int LANES, int UNITS>
 cudaError_t launch_shape(const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int kRows = 32 / LANES;
+  int dev = 0;
+  const cudaError_t e = stream_device(stream, &dev);
+  if (e != cudaSuccess) return e;
   Params p;
   auto side = [](const NormRopeSide& s) {
     return Side{static_cast<const __nv_bfloat16*>(s.x), s.x_stride,
@@ -312,7 +315,7 @@ cudaError_t launch_shape(const NormRopeArgs& a, cudaStream_t stream) {
   // A warp a token where that fills the GPU (32 warps an SM), else as many as it has
   // turns of kRows heads.
   const int heads = a.q.heads + a.k.heads, most = (heads + kRows - 1) / kRows;
-  const int64_t want = (152 * 32 + a.tokens - 1) / a.tokens;
+  const int64_t want = (kv8_sm_count(dev) * 32 + a.tokens - 1) / a.tokens;
   p.splits = want < most ? (int)want : most;
   const int turns = (most + p.splits - 1) / p.splits;
   p.part = turns * kRows;
