@@ -450,3 +450,8 @@ def test_a_nan_key_shows_where_a_row_of_weight_sees_it(ds, lens, counts, at):
     lse[-1, 3] = 5.0
     got = _mass(ds, c, q, lse, starts, 0.125, poisoned(last))
     assert got[0, 1, last].isnan() and got.isnan().sum() == 1
+
+
+@pytest.mark.parametrize("counts,heads,hk", [([1, 3], 1024, 1024), ([40, 2], 512, 256), ([2, 1], 1024, 1)])
+def test_many_heads(ds, counts, heads, hk):
+    _case(ds, [130, 70], counts, heads, hk, 64, seed=31)

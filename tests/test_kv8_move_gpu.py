@@ -352,3 +352,9 @@ def test_evictions_again_and_again(ds):
                 v, s = v.reshape(-1, d)[:lens[r]], np.repeat(s, 64)[:lens[r], None]
                 x = exact[r][g][:, side]
                 assert (np.abs(v - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -9 * s).all()
+
+
+def test_evict_and_accept_with_many_heads(ds):
+    assert not _evict(ds, [200, 130, 60], 70, 2, 10, 300, 64, seed=17)
+    rng = np.random.default_rng(17)
+    assert not _accept(ds, [90, 64 + 5, 64], 20, _paths(rng, 3, 20, 20), 300, 64, seed=18)

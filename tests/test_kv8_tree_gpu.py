@@ -338,3 +338,35 @@ def test_scores_too_low_for_a_reference_give_nan(ds, dim, n, group, length, gone
     out, lse = ds.kv8_tree_decode(q, masks, codes, scales, table, lens, 2.0 ** 26 / (448 * 8 * dim))
     torch.cuda.synchronize()
     assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_thousands_of_requests(ds, dim):
+    """More units than the kernel that numbers them has threads; most requests are short,
+    many empty. A request's outputs are those of a call of its own."""
+    rng = np.random.default_rng(26)
+    reqs, n, heads, pages = 3000, 12, 8, 40
+    lens = rng.integers(-3, 200, reqs)
+    lens[rng.integers(0, reqs, 40)] = rng.integers(1000, 2500, 40)
+    codes = torch.as_tensor(rng.integers(0, 0x70, (pages, 2, 1, 64, dim)), dtype=torch.uint8).to(DEV)
+    scales = torch.full((pages, 2, 1), 2.0 ** -7, device=DEV)
+    table = torch.as_tensor(rng.integers(0, pages, (reqs, 40)), dtype=torch.int32).to(DEV)
+    ln = torch.as_tensor(lens, dtype=torch.int32).to(DEV)
+    masks = _dev(_tree(rng, reqs, n))
+    q = torch.as_tensor(rng.standard_normal((reqs, n, heads, dim))).to(torch.bfloat16).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = ds.kv8_tree_decode(q, masks, codes, scales, table, ln, 0.1, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    for r in [0, 1, reqs - 1, *rng.integers(0, reqs, 40), *np.argsort(lens)[-5:], *np.argsort(lens)[:3]]:
+        a, b = ds.kv8_tree_decode(q[r:r + 1], masks[r:r + 1], codes, scales, table[r:r + 1].contiguous(),
+                                  ln[r:r + 1], 0.1)
+        assert torch.equal(a[0], out[r]) and torch.equal(b[0], lse[r])
+        if lens[r] <= 0:
+            assert (out[r] == 0).all() and torch.isneginf(lse[r]).all()
+
+
+@pytest.mark.parametrize("n,kv_heads,group", [(2, 1024, 1), (64, 200, 2), (3, 40, 25), (1, 1, 1024)])
+def test_many_heads(ds, n, kv_heads, group):
+    c = Cache([n + 70, n], kv_heads, 64, seed=27)
+    _run(ds, c, _tree(c.rng, 2, n), kv_heads * group)
