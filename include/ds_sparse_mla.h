@@ -634,7 +634,8 @@ int ds_kv8_accept(const ds_kv8_layer* layers, int num_layers, int64_t num_pages,
  *
  *  q, token_starts, kv_pages, kv_scales, block_table, lens, scale   as for
  *               ds_kv8_prefill (decode: one token a request).
- *  lse          float32 [num_tokens, num_heads]; -inf: the row adds nothing.
+ *  lse          float32 [num_tokens, num_heads]; -inf: the row adds nothing, whatever
+ *               its q holds (a padding token).
  *  mass         float32 [num_requests, num_kv_heads, mass_stride], mass_stride at
  *               least 64 * bt_stride. Rows of requests without tokens and
  *               entries at and past lens[r] keep their values. A fork's row is a
@@ -646,7 +647,8 @@ int ds_kv8_accept(const ds_kv8_layer* layers, int num_layers, int64_t num_pages,
  * the largest partial sum), exponentials and sums are fp32. Up to 24 rows a kv head
  * (tokens times heads of the group) take q as three E4M3 pieces: exact down to 2^-19
  * of the row's largest |q|, and below that off by at most 2^-27 of it. A NaN key makes its
- * own position NaN, a non-finite q or a NaN lse the positions that the row sees.
+ * own position NaN where a row sees it, a non-finite q or a NaN lse the positions that the
+ * row sees (rows of lse -inf aside).
  * num_tokens * num_heads / num_kv_heads is below 2^31 - 256 and bt_stride at most
  * 2^20. A request's mass depends on that request alone, bit for bit; it does
  * depend, in the last bits, on how its tokens are spread over calls. Needs no
@@ -686,8 +688,12 @@ int ds_kv8_mass(const void* q, int64_t q_stride, const float* lse, int64_t num_t
  *               mass_stride, DS_DEVERR_PAGE for a page outside the pool; such a
  *               request stays as it is.
  *
- * Scales as for ds_kv8_accept. num_requests * num_kv_heads is at most 2^26. A
- * request's result depends on that request alone, bit for bit.
+ * Scales as for ds_kv8_accept: over many calls a page's scale tends to the largest that
+ * its head had, and a value is off by one rounding and, in E4M3's subnormal range, half a
+ * step of each scale it went through (with powers of two together less than 2^-9 of the
+ * present scale). All positions behind the first dropped one move, also where few are
+ * dropped. num_requests * num_kv_heads is at most 2^26. A request's result depends on that
+ * request alone, bit for bit.
  */
 int ds_kv8_evict(float* mass, int64_t mass_stride, int budget, int first, int recent,
                  void* kv_pages, float* kv_scales, int64_t num_pages, const int32_t* refcounts,

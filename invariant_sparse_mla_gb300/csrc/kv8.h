@@ -90,9 +90,17 @@ cudaError_t launch_kv8_tree(const Kv8AttnArgs& a, cudaStream_t stream);
 size_t kv8_tree_workspace_bytes(int64_t requests, int next_n, int heads, int kv_heads, int dim,
                                 int64_t bt_stride);
 // Whether a tree takes that form, by its rows (nodes * heads of a kv head): from
-// three row groups of decode on. 16 requests on 4096 to 32768 positions, 8 kv heads x
-// 128, took 322 us by decode and 412 by tiles with 64 rows, 507 and 357 with 128, 802
-// and 459 with 192; one request on 32768 positions with 192 rows 121 and 118.
+// three row groups of decode on. us by decode / by tiles, 8 kv heads, one build, inputs not
+// in L2:
+//   rows                                  64      80      88      96     128     192     256
+//   x 128, 16 requests on 4k to 32k    326/390 408/452 470/416 417/363 522/344 816/438 889/369
+//          one on 32768                 61/103  68/109  81/111  81/104  97/104 123/116 151/118
+//          16 on 512 to 1024            53/51   62/51   62/59   59/54   72/45   99/54  119/56
+//          one on 1000                  30/43   35/44   32/45   34/45   33/43   37/47   38/48
+//   x 64,  16 requests on 4k to 32k    249/280 326/329 321/290 342/276 452/248 675/325 971/308
+//          one on 32768                 52/78   63/88   65/91   66/81   77/75  110/93  128/88
+// The limit is that of batches, which have most to lose; a lone request would like 128 to
+// 192 rows (up to 30 us), but what a request gets may not depend on the batch.
 inline bool kv8_tree_tiles(int next_n, int group) { return next_n * group > 80; }
 cudaError_t launch_kv8_mass(const Kv8MassArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_accept(const ds_kv8_layer* layers, int num_layers, const Kv8AcceptArgs& a,

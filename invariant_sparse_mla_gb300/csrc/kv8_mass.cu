@@ -39,14 +39,17 @@
 // by fewer rows.
 //
 // Measured: one token of 32 requests with 4096 to 32768 positions, 64 / 8 heads x 128:
-// 133 us (684 MB, 5.1 TB/s: 76 % of a plain copy; bf16 products of the same took 319,
-// one tile an item 153). The last 2048 of 32768 positions: 811 us, 1314 TFLOP/s, 68 %
-// (the tensor pipe 58 % busy, issue slots 54 %: exponentials, and the products of the
-// two tiles take turns with them). 12 ragged prompts of dim 64, 28 / 4 heads: 225 us,
-// where exponentials alone take 87: a product of dim 64 is half as long, so that issuing
-// and waiting count twice, and a quarter of the steps is masked. Not kept: S in three
-// buffers that both tiles share (chunk 938 us where it was 883), eight warps that sum
-// (919), lse read four steps ahead (1560: registers), steps of 128 rows (863).
+// 132 us (684 MB, 5.2 TB/s: 76 % of a plain copy; bf16 products of the same took 319,
+// one tile an item 153); 6 tokens of each 322, 24 tokens 372. The last 2048 of 32768
+// positions: 838 us, 1270 TFLOP/s, 66 % (the tensor pipe 57 % busy, issue slots 55 %:
+// exponentials, and the products of the two tiles take turns with them; of it 20 us since
+// rows of lse -inf are looked for behind the wait for S. Looked for before it the chunk
+// takes 806 and 48 to 192 rows 5 to 8 % more, dim 64 the other way round: registers
+// spill). 12 ragged prompts of dim 64, 28 / 4 heads: 226 us, where exponentials alone
+// take 87: a product of dim 64 is half as long, so that issuing and waiting count twice,
+// and a quarter of the steps is masked. Not kept, each against the build of its time: S
+// in three buffers that both tiles share (chunk 938 us, 883 without), eight warps that sum
+// (919, 883), lse read four steps ahead (1560: registers), steps of 128 rows (863, 821).
 //
 // Per CTA: warps 0-15 convert and sum (enough of them that the exponentials of some
 // run while others wait for their product), warp 16 brings K, warp 17 issues the
@@ -64,7 +67,7 @@ namespace dsmla {
 
 namespace {
 
-constexpr int kTile = 128;                 // positions of an item
+constexpr int kTile = 128;                 // positions of a tile
 constexpr int kStep = 192;                 // query rows of a step
 constexpr int kFewCols = 128;              // columns of an S buffer with few rows
 constexpr int kSumWarps = 16;

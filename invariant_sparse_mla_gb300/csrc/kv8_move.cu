@@ -238,7 +238,9 @@ __device__ __forceinline__ void cluster_wait() {
 // held to 4096: 135 us in all (561 MB; 83 at the rate of a plain copy), of which the
 // moves take about 100, the ranking 27 and the plan 6.5. With one page a round and its
 // lookups each time it was 196: rows of 128 bytes scattered over the pool come at
-// about 5 TB/s, and a round waits for the slowest CTA of eight.
+// about 5 TB/s, and a round waits for the slowest CTA of eight. The same requests with
+// 1, 64 or 512 positions past the budget take 118, 128 or 132 us: all that lies behind the
+// first dropped position moves up (20 us where nothing is past it).
 template <int DIM>
 __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Kv8EvictArgs a) {
   constexpr int L = DIM / 16;                     // lanes of a row

@@ -73,11 +73,13 @@ constexpr int kRows = 256;               // query rows per CTA
 constexpr int kErrPage = DS_DEVERR_PAGE, kErrTimeout = DS_DEVERR_TIMEOUT;
 constexpr int kMaxCtas = 192;
 // Trees of drafts: contexts are cut so that few requests fill the GPU too, into at most
-// 8 spans. An item costs about 8 us beside its tiles (q, the first S, partial outputs):
-// 16 requests x 24 nodes on 4096 to 32768 positions, 64 / 8 heads x 128, take 433 us, of
-// which the join is about 25. At most 4 spans, or 1, took 417 or 613 us where 8 took 463
-// (few items are badly spread), and one request on 32768 positions 185 or 601 where 8
-// took 118.
+// 8 spans. An item costs about 8 us beside its tiles (q, the first S, partial outputs), the
+// join about 20. us with at most 1 / 4 / 8 / 16 spans, 64 / 8 heads x 128, one build, inputs
+// not in L2:
+//   16 requests on 4096 to 32768 positions   24 nodes 614 / 399 / 440 / 507   12: 576 / 330 / 363 / 413
+//   one on 32768                             24 nodes 607 / 189 / 116 / 80    12: 564 / 174 / 105 / 75
+//   4 on 3000 to 8000                        24 nodes 165 /  86 /  79 / 78    12: 165 /  76 /  76 / 72
+// 8 lie between: 4 are 10 % faster for the batch and 60 % slower for one request.
 using TreeSpans = SpanRule<1024, 1 << 28, 8>;
 
 // What the first kernel writes: item (unit u of one kv head) has weight

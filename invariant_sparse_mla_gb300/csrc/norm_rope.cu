@@ -19,9 +19,9 @@
 // and works out once. A row is then about 100 instructions for 32 / LANES of them.
 //
 // The bound is HBM, 4 bytes an element: 16384 tokens of 72 heads x 128, all normed
-// and turned, 108 us (5.5 TB/s, 82 % of a plain copy; a CTA for some rows with the
+// and turned, 110 us (5.5 TB/s, 81 % of a plain copy; a CTA for some rows with the
 // angles worked out per CTA and a barrier took 144), 4095 tokens of 129 latent rows of
-// 576 dims 205 us (5.9 TB/s; 217). Two tokens: 5 us, the launch and two dependent reads.
+// 576 dims 206 us (5.9 TB/s; 217). Two tokens: 5 us, the launch and two dependent reads.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
